@@ -378,6 +378,172 @@ fa_status fa_decode_paged_noalloc(const void* q, const void* k_pages, const void
                                   fa_stream_t stream);
 
 /*
+ * ---------------------------------------------------------------------------------------
+ * Packed tokens, grouped K/V heads, rotary positions.
+ *
+ * Layout of the calls below. Tokens of all sequences are packed without padding, [T, heads, d],
+ * the way a projection leaves them: the heads of a token lie next to each other (d elements
+ * apart) and consecutive tokens are `*_token` elements apart, so q, k and v may be slices of
+ * one fused projection. cu_seqlens holds B + 1 non-decreasing int32 row numbers on the device:
+ * sequence b owns rows cu[b] .. cu[b+1]-1 (none when they are equal); rows behind cu[B] belong
+ * to nobody and no output row of theirs is written. H query heads share Hkv K/V heads, H a
+ * multiple of Hkv: query head h reads K/V head h / (H / Hkv). H / Hkv is at most 128.
+ * Everything about lengths is read on the device, so a captured graph may be replayed after
+ * they change. A start outside [0, total], a decreasing one, or a length beyond a cache's
+ * capacity is reported as FA_ERR_BAD_PAGE by fa_get_device_status; such a sequence counts as
+ * empty (starts) or is cut to the capacity (lengths).
+ */
+
+/* Layout of the rotated pairs: (i, i + R/2), or (2i, 2i + 1). */
+enum { FA_ROPE_HALF = 0, FA_ROPE_PAIRS = 1 };
+/* Frequency rules of fa_rope_freqs. */
+enum { FA_ROPE_PLAIN = 0, FA_ROPE_LINEAR = 1, FA_ROPE_BASE = 2, FA_ROPE_BY_PARTS = 3 };
+
+/*
+ * fa_rope_freqs - frequencies of a rotary embedding, on the HOST (no GPU is involved):
+ * freqs[i], i < rot_dim / 2, in radians per position, and the amplitude that the rotation is
+ * multiplied by.
+ *   FA_ROPE_PLAIN     w_i = base^(-2i / rot_dim), amplitude 1
+ *   FA_ROPE_LINEAR    w_i / factor (positions interpolated), amplitude 1
+ *   FA_ROPE_BASE      w_i with base * factor^(rot_dim / (rot_dim - 2)), amplitude 1
+ *                     (rot_dim >= 4)
+ *   FA_ROPE_BY_PARTS  with r = trained_len w_i / (2 pi), the turns a pair makes over the
+ *                     trained length, and g = clamp((r - slow) / (fast - slow), 0, 1):
+ *                     g w_i + (1 - g) w_i / factor, amplitude 0.1 ln(factor) + 1
+ *                     (fast > slow; 32 and 1 are usual)
+ * rot_dim even in [2, 512], base > 0, factor >= 1; arguments that a rule does not use are
+ * ignored.
+ */
+fa_status fa_rope_freqs(double* freqs, float* amplitude, int rot_dim, double base, int scaling,
+                        double factor, int trained_len, double fast, double slow);
+
+/*
+ * fa_rope - rotate the first rot_dim elements of every head of every token by its position:
+ * with t = positions[token] * freqs[i], A = amplitude and (a, b) pair i of the layout,
+ *     y_a = A (x_a cos t - x_b sin t),   y_b = A (x_b cos t + x_a sin t);
+ * elements rot_dim .. d-1 are copied. inverse != 0 turns by -t: the gradient with respect to
+ * x of the forward call, given the gradient with respect to y.
+ *   x, y       element e of head h of token t at t * x_token + h * x_head + e (y likewise);
+ *              y may be x with the same steps (in place), else it must not overlap x
+ *   positions  int32 [T], device; any values (angles are formed modulo one turn in 64-bit
+ *              fixed point, so far positions lose nothing)
+ *   freqs      float64 [rot_dim / 2], device
+ *   T >= 0, H >= 1, d in [2, 512], rot_dim even in [2, d]; style FA_ROPE_HALF or
+ *   FA_ROPE_PAIRS; dtype FA_F16, FA_BF16 or FA_F32. x and y aligned to their element; with
+ *   16-byte aligned pointers, steps of a multiple of 16 bytes and rot_dim and d likewise, heads
+ *   move in 16-byte accesses, else element by element.
+ */
+fa_status fa_rope(const void* x, void* y, const int32_t* positions, const double* freqs, int64_t T,
+                  int H, int d, int rot_dim, int64_t x_token, int64_t x_head, int64_t y_token,
+                  int64_t y_head, int style, float amplitude, int inverse, int dtype,
+                  fa_stream_t stream);
+
+/*
+ * fa_rope_append - the step between the projections and fa_fwd_paged_varlen: rotate q and k of
+ * a packed chunk of new tokens as fa_rope does, write q to q_out, and write k and v into the
+ * paged cache. Token t of sequence b sits at position ctx_lens[b] + t - cu_seqlens[b] (ctx_lens:
+ * tokens cached BEFORE the chunk, as for fa_kv_append; the caller adds the chunk's lengths
+ * afterwards) and is stored in page block_table[b, position / page_size] at offset
+ * position % page_size. Only the new tokens' slots are written (fa_kv_append also zeroes the
+ * rest of the last page, which fa_fwd_paged needs and fa_fwd_paged_varlen does not).
+ *   q, q_out [T, H, d]; k, v [T, Hkv, d]; pools [num_pages, Hkv, page_size, d]: dtype FA_F16 or
+ *   FA_BF16, 16-byte aligned, steps a multiple of 8 elements; q_out may be q. d 64 or 128;
+ *   page_size a multiple of 16 in [16, 4096].
+ * A token whose table entry is outside [0, num_pages), or whose position is beyond
+ * page_size * max_pages_per_seq, is not cached (its q is rotated) and reported as
+ * FA_ERR_BAD_PAGE.
+ */
+typedef struct fa_rope_append_params {
+  const void* q;
+  const void* k;
+  const void* v;
+  void* q_out;
+  void* k_pages;
+  void* v_pages;
+  const int32_t* block_table; /* [B, max_pages_per_seq] */
+  const int32_t* ctx_lens;    /* [B] */
+  const int32_t* cu_seqlens;  /* [B + 1] */
+  const double* freqs;        /* [rot_dim / 2] */
+  int64_t q_token, k_token, v_token, q_out_token;
+  int T, B, H, Hkv, d, rot_dim, page_size, max_pages_per_seq, num_pages;
+  int style;
+  float amplitude;
+  int dtype;
+} fa_rope_append_params;
+
+fa_status fa_rope_append(const fa_rope_append_params* params, fa_stream_t stream);
+
+/*
+ * fa_fwd_varlen - attention over packed sequences of different lengths with grouped K/V heads:
+ * for every sequence what fa_fwd computes (o and lse under the same masks, queries aligned to
+ * the last keys of their own sequence).
+ *   q, o [total_q, H, d]; k, v [total_k, Hkv, d]; lse [total_q, H] float32 or NULL
+ *   cu_seqlens_q, cu_seqlens_k [B + 1] (the same array for self-attention)
+ *   d 64 or 128; dtype FA_F16 or FA_BF16; token steps a multiple of 8 elements; mask_mode every
+ *   mask but FA_MASK_BLOCK_SPARSE, with window and n_global per sequence.
+ *   workspace  device scratch of fa_varlen_workspace_size(...) bytes, 16-byte aligned, owned by
+ *              the caller; its contents on entry do not matter. Calls that may overlap on the
+ *              GPU, two captured graphs among them, need workspaces of their own.
+ * Results do not depend on how the work is spread over the GPU, and are the same on every
+ * run. An infinity or NaN in V reaches the queries of its own sequence only.
+ */
+typedef struct fa_varlen_params {
+  const void* q;
+  const void* k;
+  const void* v;
+  void* o;
+  float* lse;
+  int64_t q_token, k_token, v_token, o_token;
+  const int32_t* cu_seqlens_q;
+  const int32_t* cu_seqlens_k;
+  int B, H, Hkv, d, total_q, total_k;
+  float scale;
+  int mask_mode, window, n_global, dtype;
+  void* workspace;
+  size_t workspace_bytes;
+  uint32_t timeout_us; /* per-wait time limit: 0 = 1 s */
+} fa_varlen_params;
+
+fa_status fa_fwd_varlen(const fa_varlen_params* params, fa_stream_t stream);
+size_t fa_varlen_workspace_size(int B, int H, int Hkv, int total_q, int total_k, int d);
+
+/*
+ * fa_fwd_paged_varlen - attention of packed chunks of new tokens over a paged cache with grouped
+ * heads: the tokens cu_seqlens_q[b] .. cu_seqlens_q[b+1]-1 are the last tokens of sequence b,
+ * whose ctx_lens[b] keys (the chunk's own included) are in the cache, e.g. by fa_rope_append.
+ * Chunks of one token (a decode step) and of hundreds may be mixed in one call.
+ *   q, o [total_q, H, d]; lse [total_q, H] float32 or NULL
+ *   pools [num_pages, Hkv, page_size, d]; block_table int32 [B, max_pages_per_seq];
+ *   ctx_lens int32 [B]; page_size a multiple of 16 in [16, 4096]
+ *   max_q      at least the longest chunk (chunks are cut to it, which is reported as
+ *              FA_ERR_BAD_PAGE); up to 64 / (H / Hkv) the call runs kernels for few rows
+ *   everything else as for fa_fwd_varlen; workspace fa_paged_varlen_workspace_size(...) bytes.
+ * Slots behind a sequence's last key may hold anything. A table entry outside [0, num_pages) is
+ * read as page 0 and reported as FA_ERR_BAD_PAGE.
+ */
+typedef struct fa_paged_varlen_params {
+  const void* q;
+  const void* k_pages;
+  const void* v_pages;
+  const int32_t* block_table;
+  const int32_t* ctx_lens;
+  const int32_t* cu_seqlens_q;
+  void* o;
+  float* lse;
+  int64_t q_token, o_token;
+  int B, H, Hkv, d, total_q, max_q, page_size, max_pages_per_seq, num_pages;
+  float scale;
+  int mask_mode, window, n_global, dtype;
+  void* workspace;
+  size_t workspace_bytes;
+  uint32_t timeout_us; /* per-wait time limit: 0 = 1 s */
+} fa_paged_varlen_params;
+
+fa_status fa_fwd_paged_varlen(const fa_paged_varlen_params* params, fa_stream_t stream);
+size_t fa_paged_varlen_workspace_size(int B, int H, int Hkv, int total_q, int max_q,
+                                      int max_pages_per_seq, int page_size, int d);
+
+/*
  * fa_get_device_status - synchronise `stream`, then read and clear the device
  * status word. Returns FA_OK, FA_ERR_BAD_PAGE or FA_ERR_TIMEOUT (FA_ERR_CUDA if the
  * stream itself failed). FA_ERR_UNSUPPORTED means that a backward kernel found its dynamic

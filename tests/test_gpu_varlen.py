@@ -1,0 +1,261 @@
+"""Packed grouped-head attention through the C ABI against a plain implementation in 64 bits
+(tolerances: _packed.py)."""
+import math
+
+import pytest
+import torch
+
+import tiled_attention_06_gb300 as fa
+
+from _packed import attention, check_forward, starts
+
+pytestmark = pytest.mark.gpu
+
+DT = {"f16": torch.float16, "bf16": torch.bfloat16}
+MASKS = {"none": (fa.FA_MASK_NONE, 0, 0), "causal": (fa.FA_MASK_CAUSAL, 0, 0),
+         "window": (fa.FA_MASK_CAUSAL_WINDOW, 50, 5), "band": (fa.FA_MASK_BAND, 40, 0),
+         "prefix": (fa.FA_MASK_PREFIX_LM, 0, 70)}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from tiled_attention_06_gb300 import build
+    build.build()
+    fa.lib()
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def forward(q, k, v, cu_q, cu_k, scale, mask=(fa.FA_MASK_CAUSAL, 0, 0), want_lse=True):
+    """q, k, v on the GPU; o and lse poisoned first."""
+    T, H, d = q.shape
+    o = torch.full((T, H, d), float("nan"), dtype=q.dtype, device="cuda")
+    lse = torch.full((T, H), float("nan"), device="cuda") if want_lse else None
+    ws = torch.empty(max(fa.fa_varlen_workspace_size(len(cu_q) - 1, H, k.shape[1], T, k.shape[0],
+                                                     d), 16), dtype=torch.uint8, device="cuda")
+    fa.fa_fwd_varlen(q, k, v, o, lse, i32(cu_q), i32(cu_k), scale, ws, *mask)
+    assert fa.fa_get_device_status() == fa.FA_OK
+    return o, lse
+
+
+def case(lens_q, lens_k, H, Hkv, d, dtype, seed, pad=0):
+    g = torch.Generator().manual_seed(seed)
+    q = torch.randn(sum(lens_q) + pad, H, d, generator=g).to(dtype)
+    k = torch.randn(sum(lens_k) + pad, Hkv, d, generator=g).to(dtype)
+    v = torch.randn(sum(lens_k) + pad, Hkv, d, generator=g).to(dtype)
+    return q, k, v, starts(lens_q), starts(lens_k)
+
+
+LENS = [[1], [1, 1, 1], [0, 5, 0], [128], [129, 1, 127], [17, 300, 64, 2], [640]]
+
+
+@pytest.mark.parametrize("lens", LENS, ids=str)
+@pytest.mark.parametrize("H,Hkv,d,dt", [(4, 4, 64, "f16"), (8, 2, 128, "bf16"),
+                                        (7, 1, 128, "f16"), (6, 2, 64, "bf16")])
+@pytest.mark.parametrize("mask", list(MASKS))
+def test_self_attention(lens, H, Hkv, d, dt, mask):
+    q, k, v, cu, _ = case(lens, lens, H, Hkv, d, DT[dt], seed=sum(lens) + H, pad=2)
+    scale = 1 / math.sqrt(d)
+    o, lse = forward(q.cuda(), k.cuda(), v.cuda(), cu, cu, scale, MASKS[mask])
+    T = sum(lens)
+    check_forward(o, lse, attention(q, k, v, cu, cu, scale, *MASKS[mask]), DT[dt], T,
+                  f"{lens} {mask}")
+    assert o[T:].isnan().all() and lse[T:].isnan().all()  # rows behind the last sequence
+
+
+@pytest.mark.parametrize("lens_q,lens_k", [([3, 200, 1], [200, 3, 0]), ([1, 1], [1000, 129]),
+                                           ([5], [4099]), ([130, 0, 2], [0, 7, 260])], ids=str)
+@pytest.mark.parametrize("G", [1, 5])
+@pytest.mark.parametrize("mask", list(MASKS))
+def test_other_keys_than_queries(lens_q, lens_k, G, mask):
+    """Cross attention, long contexts (split over the SMs), queries without any key."""
+    H, Hkv, d = 2 * G, 2, 128
+    q, k, v, cu_q, cu_k = case(lens_q, lens_k, H, Hkv, d, torch.bfloat16, seed=G)
+    scale = 1 / math.sqrt(d)
+    o, lse = forward(q.cuda(), k.cuda(), v.cuda(), cu_q, cu_k, scale, MASKS[mask])
+    check_forward(o, lse, attention(q, k, v, cu_q, cu_k, scale, *MASKS[mask]), torch.bfloat16,
+                  sum(lens_q), f"{lens_q} {lens_k} {mask}")
+
+
+@pytest.mark.parametrize("G", [1, 2, 3, 8, 12, 33, 64, 100, 128])
+def test_group_sizes(G):
+    lens = [70, 3, 150]
+    q, k, v, cu, _ = case(lens, lens, G, 1, 64, torch.float16, seed=G)
+    o, lse = forward(q.cuda(), k.cuda(), v.cuda(), cu, cu, 0.125)
+    check_forward(o, lse, attention(q, k, v, cu, cu, 0.125, fa.FA_MASK_CAUSAL), torch.float16,
+                  sum(lens), f"G={G}")
+
+
+def test_slices_of_a_fused_projection_and_wider_outputs():
+    H, Hkv, d, lens = 6, 2, 64, [40, 129]
+    g = torch.Generator().manual_seed(1)
+    qkv = torch.randn(sum(lens), H + 2 * Hkv, d, generator=g).to(torch.bfloat16)
+    x = qkv.cuda()
+    q, k, v = x[:, :H], x[:, H:H + Hkv], x[:, H + Hkv:]
+    cu = starts(lens)
+    wide = torch.full((sum(lens), H + 1, d), 5.0, dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(fa.fa_varlen_workspace_size(2, H, Hkv, sum(lens), sum(lens), d),
+                     dtype=torch.uint8, device="cuda")
+    fa.fa_fwd_varlen(q, k, v, wide[:, 1:], None, i32(cu), i32(cu), 0.125, ws)
+    ref = attention(qkv[:, :H], qkv[:, H:H + Hkv], qkv[:, H + Hkv:], cu, cu, 0.125,
+                    fa.FA_MASK_CAUSAL)
+    check_forward(wide[:, 1:], None, ref, torch.bfloat16, sum(lens))
+    assert (wide[:, 0] == 5.0).all()
+
+
+def test_infinities_of_one_sequence_stay_there():
+    """NaN and infinities in another sequence's q, k, v, and in rows of nobody."""
+    lens, H, Hkv, d = [100, 30, 200], 4, 2, 64
+    q, k, v, cu, _ = case(lens, lens, H, Hkv, d, torch.float16, seed=3, pad=40)
+    ref = attention(q, k, v, cu, cu, 0.125, fa.FA_MASK_CAUSAL)
+    for t in (q, k, v):
+        t[100:130] = float("nan")
+        t[110] = float("inf")
+        t[330:] = float("nan")
+    o, lse = forward(q.cuda(), k.cuda(), v.cuda(), cu, cu, 0.125)
+    for rows in (slice(0, 100), slice(130, 330)):
+        check_forward(o[rows], lse[rows], tuple(r[rows] for r in ref), torch.float16, 10 ** 9)
+
+
+def test_same_bits_on_every_run_and_for_any_neighbours():
+    """A sequence's result does not depend on what it is packed with."""
+    H, Hkv, d = 8, 2, 128
+    q, k, v, cu, _ = case([500, 77], [500, 77], H, Hkv, d, torch.bfloat16, seed=4)
+    qg, kg, vg = q.cuda(), k.cuda(), v.cuda()
+    o1, l1 = forward(qg, kg, vg, cu, cu, 0.09)
+    o2, l2 = forward(qg, kg, vg, cu, cu, 0.09)
+    assert torch.equal(o1, o2) and torch.equal(l1, l2)
+
+
+def test_captured_call_follows_new_lengths():
+    H, Hkv, d, T = 4, 1, 64, 300
+    q, k, v, _, _ = case([T], [T], H, Hkv, d, torch.float16, seed=5)
+    qg, kg, vg = q.cuda(), k.cuda(), v.cuda()
+    cu = i32([0, 100, 300])
+    o = torch.zeros(T, H, d, dtype=torch.float16, device="cuda")
+    lse = torch.zeros(T, H, device="cuda")
+    ws = torch.empty(fa.fa_varlen_workspace_size(2, H, Hkv, T, T, d), dtype=torch.uint8,
+                     device="cuda")
+    fa.fa_fwd_varlen(qg, kg, vg, o, lse, cu, cu, 0.125, ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        fa.fa_fwd_varlen(qg, kg, vg, o, lse, cu, cu, 0.125, ws)
+    for split in (100, 1, 0, 299):
+        cu.copy_(i32([0, split, 300]))
+        o.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        c = [0, split, 300]
+        check_forward(o, lse, attention(q, k, v, c, c, 0.125, fa.FA_MASK_CAUSAL), torch.float16,
+                      T, f"split {split}")
+
+
+def test_bad_starts_are_reported_and_read_nothing():
+    H, Hkv, d, T = 2, 1, 64, 64
+    q, k, v, _, _ = case([T], [T], H, Hkv, d, torch.float16, seed=6)
+    qg, kg, vg = q.cuda(), k.cuda(), v.cuda()
+    for cu in ([0, 40, 65], [0, 40, 20], [-1, 20, 64]):
+        o = torch.full((T, H, d), float("nan"), dtype=torch.float16, device="cuda")
+        ws = torch.empty(fa.fa_varlen_workspace_size(2, H, Hkv, T, T, d), dtype=torch.uint8,
+                         device="cuda")
+        fa.fa_fwd_varlen(qg, kg, vg, o, None, i32(cu), i32(cu), 0.125, ws)
+        assert fa.fa_get_device_status() == fa.FA_ERR_BAD_PAGE
+        good = [(a, b) for a, b in zip(cu, cu[1:]) if 0 <= a <= b <= T]
+        for a, b in good:
+            ref = attention(q, k, v, [a, b], [a, b], 0.125, fa.FA_MASK_CAUSAL)
+            check_forward(o[a:b], None, tuple(r[a:b] for r in ref), torch.float16, 10 ** 9)
+        rows = torch.ones(T, dtype=torch.bool)
+        for a, b in good:
+            rows[a:b] = False
+        assert o[rows.cuda()].isnan().all()
+
+
+# ------------------------------------------------------------------ over a paged cache
+
+def paged_case(new, before, H, Hkv, d, page, dtype, seed, pad=2):
+    """Chunks of new tokens over caches of before[b] + new[b] keys; unused slots are NaN."""
+    g = torch.Generator().manual_seed(seed)
+    total = [n + c for n, c in zip(new, before)]
+    need = [-(-t // page) for t in total]
+    width, pages = max(need + [1]) + 1, sum(need) + 4
+    perm = torch.randperm(pages, generator=g).tolist()
+    table = torch.full((len(new), width), -1, dtype=torch.int32)
+    kp = torch.full((pages, Hkv, page, d), float("nan"), dtype=dtype)
+    vp = kp.clone()
+    q = torch.randn(sum(new) + pad, H, d, generator=g).to(dtype)
+    k = torch.randn(sum(total), Hkv, d, generator=g).to(dtype)
+    v = torch.randn(sum(total), Hkv, d, generator=g).to(dtype)
+    cu_k, at = starts(total), 0
+    for b, n in enumerate(need):
+        table[b, :n] = torch.tensor(perm[at:at + n], dtype=torch.int32)
+        at += n
+        pos = torch.arange(total[b])
+        phys, slot = table[b, pos // page].long(), pos % page
+        kp[phys, :, slot] = k[cu_k[b]:cu_k[b + 1]]
+        vp[phys, :, slot] = v[cu_k[b]:cu_k[b + 1]]
+    return q, k, v, kp, vp, table, total, starts(new), cu_k
+
+
+def run_paged(q, kp, vp, table, total, cu, max_q, scale, mask=(fa.FA_MASK_CAUSAL, 0, 0)):
+    T, H, d = q.shape
+    o = torch.full((T, H, d), float("nan"), dtype=q.dtype, device="cuda")
+    lse = torch.full((T, H), float("nan"), device="cuda")
+    B, width = table.shape
+    ws = torch.empty(fa.fa_paged_varlen_workspace_size(B, H, kp.shape[1], T, max_q, width,
+                                                       kp.shape[2], d),
+                     dtype=torch.uint8, device="cuda")
+    fa.fa_fwd_paged_varlen(q.cuda(), kp.cuda(), vp.cuda(), table.cuda(), i32(total), i32(cu),
+                           max_q, o, lse, scale, ws, *mask)
+    return o, lse
+
+
+PAGED = [([1, 1, 1], [0, 17, 300]), ([1], [4000]), ([3, 1, 0, 4], [60, 0, 9, 127]),
+         ([16, 2, 9], [1000, 1, 0]), ([130, 1, 64], [70, 2000, 0]), ([300], [5])]
+
+
+@pytest.mark.parametrize("new,before", PAGED, ids=str)
+@pytest.mark.parametrize("H,Hkv,d,page,dt", [(4, 4, 64, 16, "f16"), (8, 2, 128, 256, "bf16"),
+                                             (7, 1, 128, 64, "f16"), (10, 2, 64, 48, "bf16"),
+                                             (16, 1, 128, 128, "bf16")])
+@pytest.mark.parametrize("mask", ["none", "causal", "window"])
+def test_paged_chunks(new, before, H, Hkv, d, page, dt, mask):
+    q, k, v, kp, vp, table, total, cu, cu_k = paged_case(new, before, H, Hkv, d, page, DT[dt],
+                                                         seed=sum(new) + page)
+    scale = 1 / math.sqrt(d)
+    o, lse = run_paged(q, kp, vp, table, total, cu, max(new), scale, MASKS[mask])
+    assert fa.fa_get_device_status() == fa.FA_OK
+    T = sum(new)
+    check_forward(o, lse, attention(q, k, v, cu, cu_k, scale, *MASKS[mask]), DT[dt], T,
+                  f"{new} {before} {mask}")
+    assert o[T:].isnan().all() and lse[T:].isnan().all()
+
+
+@pytest.mark.parametrize("new", [1, 40])
+def test_paged_lengths_and_pages_out_of_range(new):
+    """A length beyond the table is cut to it, a page outside the pool is read as page 0, and
+    both are reported; a chunk longer than the keys leaves its first rows empty."""
+    H, Hkv, d, page = 4, 2, 64, 16
+    q, k, v, kp, vp, table, total, cu, cu_k = paged_case([new], [60], H, Hkv, d, page,
+                                                         torch.float16, seed=1)
+    kp, vp = kp.nan_to_num(0.5), vp.nan_to_num(0.5)
+    full = table.clone()
+    full[full < 0] = 0
+    o, _ = run_paged(q, kp, vp, full, [10 ** 6], cu, new, 0.125)
+    assert fa.fa_get_device_status() == fa.FA_ERR_BAD_PAGE
+    want, _ = run_paged(q, kp, vp, full, [full.shape[1] * page], cu, new, 0.125)
+    assert fa.fa_get_device_status() == fa.FA_OK
+    assert torch.equal(o[:new], want[:new])
+    bad, zero = table.clone(), table.clone()
+    bad[0, 1], zero[0, 1] = kp.shape[0], 0
+    o, _ = run_paged(q, kp, vp, bad, total, cu, new, 0.125)
+    assert fa.fa_get_device_status() == fa.FA_ERR_BAD_PAGE
+    want, _ = run_paged(q, kp, vp, zero, total, cu, new, 0.125)
+    assert torch.equal(o[:new], want[:new])
+    few = max(0, new - 5)  # queries sit at the last positions: the first 5 before the first key
+    o, lse = run_paged(q, kp, vp, full, [few], cu, new, 0.125)
+    assert fa.fa_get_device_status() == fa.FA_OK
+    assert (o[:new - few] == 0).all() and lse[:new - few].isneginf().all()
+    assert torch.isfinite(lse[new - few:new]).all()

@@ -19,6 +19,10 @@ __all__ = [
     "fa_get_device_status",
     "fa_selftest_timeout", "fa_last_error_string", "fa_version", "fa_fwd_block_m",
     "fa_fwd_default_block_m", "fa_bwd", "fa_bwd_block_sparse", "fa_bwd_workspace_size", "fa_fwd_workspace_size",
+    "fa_rope_freqs", "fa_rope", "fa_rope_append", "fa_fwd_varlen",
+    "fa_fwd_paged_varlen", "fa_varlen_workspace_size",
+    "fa_paged_varlen_workspace_size", "FA_ROPE_HALF", "FA_ROPE_PAIRS", "FA_ROPE_PLAIN",
+    "FA_ROPE_LINEAR", "FA_ROPE_BASE", "FA_ROPE_BY_PARTS",
     "FA_OK", "FA_ERR_INVALID_ARG", "FA_ERR_UNSUPPORTED", "FA_ERR_CUDA", "FA_ERR_TIMEOUT",
     "FA_ERR_BAD_PAGE", "FA_F16", "FA_BF16", "FA_F32", "FA_MASK_NONE", "FA_MASK_CAUSAL",
     "FA_MASK_CAUSAL_WINDOW", "FA_MASK_BAND", "FA_MASK_PREFIX_LM", "FA_MASK_BLOCK_SPARSE",
@@ -30,6 +34,8 @@ FA_F16, FA_BF16, FA_F32 = 0, 1, 2
 FA_MASK_NONE, FA_MASK_CAUSAL, FA_MASK_CAUSAL_WINDOW, FA_MASK_BAND, FA_MASK_PREFIX_LM = 0, 1, 2, 3, 4
 FA_MASK_BLOCK_SPARSE = 5
 FA_LAYOUT_BLOCK = 128
+FA_ROPE_HALF, FA_ROPE_PAIRS = 0, 1
+FA_ROPE_PLAIN, FA_ROPE_LINEAR, FA_ROPE_BASE, FA_ROPE_BY_PARTS = 0, 1, 2, 3
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libfa.so")
 
@@ -38,6 +44,7 @@ _i = ctypes.c_int
 _f = ctypes.c_float
 _u32 = ctypes.c_uint32
 _sz = ctypes.c_size_t
+_i64 = ctypes.c_int64
 
 
 class FaError(RuntimeError):
@@ -62,6 +69,34 @@ class DecodeParams(ctypes.Structure):
                 ("page_size", _i), ("max_pages_per_seq", _i), ("num_pages", _i), ("scale", _f),
                 ("dtype", _i), ("workspace", _vp), ("workspace_bytes", _sz),
                 ("pages_per_split", _i), ("trace_pages", _vp), ("trace_splits", _vp)]
+
+
+class RopeAppendParams(ctypes.Structure):
+    _fields_ = [("q", _vp), ("k", _vp), ("v", _vp), ("q_out", _vp), ("k_pages", _vp),
+                ("v_pages", _vp), ("block_table", _vp), ("ctx_lens", _vp), ("cu_seqlens", _vp),
+                ("freqs", _vp), ("q_token", _i64), ("k_token", _i64), ("v_token", _i64),
+                ("q_out_token", _i64), ("T", _i), ("B", _i), ("H", _i), ("Hkv", _i), ("d", _i),
+                ("rot_dim", _i), ("page_size", _i), ("max_pages_per_seq", _i), ("num_pages", _i),
+                ("style", _i), ("amplitude", _f), ("dtype", _i)]
+
+
+class VarlenParams(ctypes.Structure):
+    _fields_ = [("q", _vp), ("k", _vp), ("v", _vp), ("o", _vp), ("lse", _vp),
+                ("q_token", _i64), ("k_token", _i64), ("v_token", _i64), ("o_token", _i64),
+                ("cu_seqlens_q", _vp), ("cu_seqlens_k", _vp), ("B", _i), ("H", _i), ("Hkv", _i),
+                ("d", _i), ("total_q", _i), ("total_k", _i), ("scale", _f), ("mask_mode", _i),
+                ("window", _i), ("n_global", _i), ("dtype", _i), ("workspace", _vp),
+                ("workspace_bytes", _sz), ("timeout_us", _u32)]
+
+
+class PagedVarlenParams(ctypes.Structure):
+    _fields_ = [("q", _vp), ("k_pages", _vp), ("v_pages", _vp), ("block_table", _vp),
+                ("ctx_lens", _vp), ("cu_seqlens_q", _vp), ("o", _vp), ("lse", _vp),
+                ("q_token", _i64), ("o_token", _i64), ("B", _i), ("H", _i), ("Hkv", _i),
+                ("d", _i), ("total_q", _i), ("max_q", _i), ("page_size", _i),
+                ("max_pages_per_seq", _i), ("num_pages", _i), ("scale", _f), ("mask_mode", _i),
+                ("window", _i), ("n_global", _i), ("dtype", _i), ("workspace", _vp),
+                ("workspace_bytes", _sz), ("timeout_us", _u32)]
 
 
 _lib = None
@@ -121,6 +156,21 @@ def lib():
         L.fa_last_error_string.argtypes = []
         L.fa_version.restype = _i
         L.fa_version.argtypes = []
+        L.fa_rope_freqs.restype = _i
+        L.fa_rope_freqs.argtypes = [ctypes.POINTER(ctypes.c_double), ctypes.POINTER(_f), _i,
+                                    ctypes.c_double, _i, ctypes.c_double, _i, ctypes.c_double,
+                                    ctypes.c_double]
+        L.fa_rope.restype = _i
+        L.fa_rope.argtypes = [_vp] * 4 + [_i64, _i, _i, _i] + [_i64] * 4 + [_i, _f, _i, _i, _vp]
+        for name, args in (("fa_rope_append", [ctypes.POINTER(RopeAppendParams)]),
+                           ("fa_fwd_varlen", [ctypes.POINTER(VarlenParams)]),
+                           ("fa_fwd_paged_varlen", [ctypes.POINTER(PagedVarlenParams)])):
+            getattr(L, name).restype = _i
+            getattr(L, name).argtypes = args + [_vp]
+        for name, n in (("fa_varlen_workspace_size", 6),
+                        ("fa_paged_varlen_workspace_size", 8)):
+            getattr(L, name).restype = _sz
+            getattr(L, name).argtypes = [_i] * n
         _lib = L
     return _lib
 
@@ -392,3 +442,194 @@ def fa_get_device_status(stream=None):
 
 def fa_selftest_timeout(timeout_us, stream=None):
     _check(lib().fa_selftest_timeout(timeout_us, _stream(stream)))
+
+
+# ----------------------------------------------------------- packed tokens, grouped heads
+
+def _refuse(msg):
+    raise FaError(FA_ERR_INVALID_ARG, msg)
+
+
+def _rows(name, t, heads, d, dtype, device):
+    """Elements between the tokens of packed rows [tokens, heads, d] (a view of a wider row
+    is fine: the last two dimensions have to be dense)."""
+    if t.dim() != 3 or t.dtype != dtype or t.device != device:
+        _refuse(f"{name} must be [tokens, heads, d] of {dtype} on {device}")
+    n, h, e = t.shape
+    if h != heads or e != d:
+        _refuse(f"{name} has {h} heads of {e}, not {heads} of {d}")
+    st = t.stride()
+    if n == 0:
+        return heads * d
+    if (d > 1 and st[2] != 1) or (heads > 1 and st[1] != d):
+        _refuse(f"{name}: the heads of a token must lie next to each other")
+    return st[0] if n > 1 else heads * d
+
+
+def _ints(name, t, shape, device):
+    if t.dtype != torch.int32 or t.device != device or not t.is_contiguous() \
+            or tuple(t.shape) != shape:
+        _refuse(f"{name} must be a contiguous int32 tensor {shape} on {device}")
+    return t.data_ptr()
+
+
+def _packed_device(t):
+    """The device of t, which must be the current one: the library launches there."""
+    if not t.is_cuda:
+        _refuse("tensors must be CUDA tensors")
+    if t.device.index != torch.cuda.current_device():
+        _refuse(f"tensors are on {t.device}, the current device is "
+                f"cuda:{torch.cuda.current_device()}")
+    return t.device
+
+
+def _lse_ptr(lse, n, heads, device):
+    if lse is None:
+        return None
+    if lse.dtype != torch.float32 or lse.device != device or not lse.is_contiguous() \
+            or tuple(lse.shape) != (n, heads):
+        _refuse(f"lse must be a contiguous float32 tensor ({n}, {heads}) on {device}")
+    return lse.data_ptr()
+
+
+def _bytes_of(workspace, device):
+    if workspace.device != device or not workspace.is_contiguous():
+        _refuse(f"workspace must be a contiguous tensor on {device}")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def fa_rope_freqs(rot_dim, base=10000.0, scaling=FA_ROPE_PLAIN, factor=1.0, trained_len=0,
+                  fast=32.0, slow=1.0, device=None):
+    """(frequencies float64 [rot_dim/2] in radians per position, amplitude) of a rotary
+    embedding; the rules are those of fa_rope_freqs in fa.h. On `device` (CPU when None)."""
+    host = torch.empty(max(rot_dim // 2, 1), dtype=torch.float64)
+    amp = _f()
+    _check(lib().fa_rope_freqs(ctypes.cast(host.data_ptr(), ctypes.POINTER(ctypes.c_double)),
+                               ctypes.byref(amp), rot_dim, float(base), scaling, float(factor),
+                               trained_len, float(fast), float(slow)))
+    return (host if device is None else host.to(device)), amp.value
+
+
+def _freqs_ptr(freqs, device):
+    if freqs.dtype != torch.float64 or freqs.device != device or freqs.dim() != 1 \
+            or not freqs.is_contiguous():
+        _refuse(f"freqs must be a contiguous float64 vector on {device}")
+    return freqs.data_ptr()
+
+
+def fa_rope(x, y, positions, freqs, style=FA_ROPE_HALF, amplitude=1.0, inverse=False,
+            stream=None):
+    """y = x [T, H, d] with the first 2 * len(freqs) elements of every head rotated by
+    positions (int32 [T]) * freqs; y may be x. inverse=True turns back: the gradient of x
+    from the gradient of y. float16, bfloat16 or float32; any token and head steps."""
+    device = _packed_device(x)
+    if x.dim() != 3 or y.shape != x.shape or y.dtype != x.dtype or y.device != device:
+        _refuse("x and y must be [tokens, heads, d] of one dtype on one device")
+    T, H, d = x.shape
+    if T == 0 or H == 0:
+        return
+    xs, ys = x.stride(), y.stride()
+    if d > 1 and (xs[2] != 1 or ys[2] != 1):
+        _refuse("the elements of a head must be contiguous")
+    dense = H * d
+    _check(lib().fa_rope(x.data_ptr(), y.data_ptr(), _ints("positions", positions, (T,), device),
+                         _freqs_ptr(freqs, device), T, H, d, 2 * freqs.numel(),
+                         xs[0] if T > 1 else dense, xs[1] if H > 1 else d,
+                         ys[0] if T > 1 else dense, ys[1] if H > 1 else d,
+                         style, float(amplitude), 1 if inverse else 0, _dtype_code(x),
+                         _stream(stream)))
+
+
+def fa_rope_append(q, k, v, q_out, k_pages, v_pages, block_table, ctx_lens, cu_seqlens, freqs,
+                   style=FA_ROPE_HALF, amplitude=1.0, stream=None):
+    """Rotate q and k of a packed chunk (q, q_out [T, H, d]; k, v [T, Hkv, d]) by the tokens'
+    positions ctx_lens[b] + t - cu_seqlens[b] (ctx_lens: tokens cached before the chunk), write
+    q to q_out and k and v into the pools [num_pages, Hkv, page_size, d]."""
+    device = _packed_device(q)
+    T, H, d = q.shape
+    P, Hkv, page, _ = k_pages.shape
+    B, width = block_table.shape
+    if k.shape[0] != T or v.shape[0] != T or q_out.shape[0] != T:
+        _refuse("q, k, v and q_out must have the same tokens")
+    _pools(k_pages, v_pages, d, q.dtype, device)
+    p = RopeAppendParams(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(), k_pages.data_ptr(),
+        v_pages.data_ptr(), _ints("block_table", block_table, (B, width), device),
+        _ints("ctx_lens", ctx_lens, (B,), device),
+        _ints("cu_seqlens", cu_seqlens, (B + 1,), device), _freqs_ptr(freqs, device),
+        _rows("q", q, H, d, q.dtype, device), _rows("k", k, Hkv, d, q.dtype, device),
+        _rows("v", v, Hkv, d, q.dtype, device), _rows("q_out", q_out, H, d, q.dtype, device),
+        T, B, H, Hkv, d, 2 * freqs.numel(), page, width, P, style, float(amplitude),
+        _dtype_code(q))
+    _check(lib().fa_rope_append(ctypes.byref(p), _stream(stream)))
+
+
+def _pools(k_pages, v_pages, d, dtype, device):
+    for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
+        if t.dtype != dtype or t.device != device or not t.is_contiguous() \
+                or t.shape != k_pages.shape or t.shape[3] != d:
+            _refuse(f"{name} must be contiguous [num_pages, Hkv, page_size, {d}] of {dtype} on "
+                    f"{device}")
+
+
+def fa_varlen_workspace_size(B, H, Hkv, total_q, total_k, d):
+    return lib().fa_varlen_workspace_size(B, H, Hkv, total_q, total_k, d)
+
+
+def fa_paged_varlen_workspace_size(B, H, Hkv, total_q, max_q, max_pages_per_seq, page_size, d):
+    return lib().fa_paged_varlen_workspace_size(B, H, Hkv, total_q, max_q, max_pages_per_seq,
+                                                page_size, d)
+
+
+def _varlen(q, k, v, o, lse, cu_seqlens_q, cu_seqlens_k, scale, workspace, mask_mode, window,
+            n_global):
+    device = _packed_device(q)
+    Tq, H, d = q.shape
+    Tk, Hkv, _ = k.shape
+    B = cu_seqlens_q.numel() - 1
+    if o.shape[0] != Tq or v.shape[0] != Tk:
+        _refuse("o must have q's tokens, v k's")
+    ws, ws_bytes = _bytes_of(workspace, device)
+    return VarlenParams(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), _lse_ptr(lse, Tq, H, device),
+        _rows("q", q, H, d, q.dtype, device), _rows("k", k, Hkv, d, q.dtype, device),
+        _rows("v", v, Hkv, d, q.dtype, device), _rows("o", o, H, d, q.dtype, device),
+        _ints("cu_seqlens_q", cu_seqlens_q, (B + 1,), device),
+        _ints("cu_seqlens_k", cu_seqlens_k, (B + 1,), device), B, H, Hkv, d, Tq, Tk,
+        float(scale), mask_mode, window, n_global, _dtype_code(q), ws, ws_bytes, 0)
+
+
+def fa_fwd_varlen(q, k, v, o, lse, cu_seqlens_q, cu_seqlens_k, scale, workspace,
+                  mask_mode=FA_MASK_CAUSAL, window=0, n_global=0, stream=None):
+    """Attention over packed sequences: q, o [Tq, H, d], k, v [Tk, Hkv, d] (slices of wider rows
+    are fine), cu_seqlens_* int32 [B + 1], lse float32 [Tq, H] or None; query head h reads K/V
+    head h // (H // Hkv). workspace: a CUDA byte tensor of fa_varlen_workspace_size(...)."""
+    p = _varlen(q, k, v, o, lse, cu_seqlens_q, cu_seqlens_k, scale, workspace, mask_mode, window,
+                n_global)
+    _check(lib().fa_fwd_varlen(ctypes.byref(p), _stream(stream)))
+
+
+def fa_fwd_paged_varlen(q, k_pages, v_pages, block_table, ctx_lens, cu_seqlens_q, max_q, o, lse,
+                        scale, workspace, mask_mode=FA_MASK_CAUSAL, window=0, n_global=0,
+                        stream=None):
+    """Attention of packed chunks of new tokens (the last tokens of their sequences) over a
+    paged cache: q, o [Tq, H, d]; pools [num_pages, Hkv, page_size, d]; block_table int32
+    [B, max_pages]; ctx_lens int32 [B] (cached keys, the chunk's included); max_q at least the
+    longest chunk. workspace: a CUDA byte tensor of fa_paged_varlen_workspace_size(...)."""
+    device = _packed_device(q)
+    Tq, H, d = q.shape
+    P, Hkv, page, _ = k_pages.shape
+    B, width = block_table.shape
+    if o.shape[0] != Tq:
+        _refuse("o must have q's tokens")
+    _pools(k_pages, v_pages, d, q.dtype, device)
+    ws, ws_bytes = _bytes_of(workspace, device)
+    p = PagedVarlenParams(
+        q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
+        _ints("block_table", block_table, (B, width), device),
+        _ints("ctx_lens", ctx_lens, (B,), device),
+        _ints("cu_seqlens_q", cu_seqlens_q, (B + 1,), device), o.data_ptr(),
+        _lse_ptr(lse, Tq, H, device), _rows("q", q, H, d, q.dtype, device),
+        _rows("o", o, H, d, q.dtype, device), B, H, Hkv, d, Tq, max_q, page, width, P,
+        float(scale), mask_mode, window, n_global, _dtype_code(q), ws, ws_bytes, 0)
+    _check(lib().fa_fwd_paged_varlen(ctypes.byref(p), _stream(stream)))

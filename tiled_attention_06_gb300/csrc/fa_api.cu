@@ -21,6 +21,7 @@
 
 #include "fa.h"
 #include "fa_bwd_tiles.h"
+#include "fa_host.h"
 #include "fa_internal.h"
 #include "fa_plan.h"
 
@@ -29,6 +30,15 @@ namespace {
 __device__ uint32_t g_status_word;
 
 thread_local std::string t_last_error = "no error";
+
+constexpr int kMaxDevices = 64;
+std::mutex g_mu;
+fa::host::DeviceInfo g_dev[kMaxDevices];
+
+}  // namespace
+
+namespace fa {
+namespace host {
 
 fa_status fail(fa_status s, const char* fmt, ...) {
   char buf[512];
@@ -43,19 +53,6 @@ fa_status fail(fa_status s, const char* fmt, ...) {
 fa_status cuda_fail(cudaError_t e, const char* what) {
   return fail(FA_ERR_CUDA, "%s: %s (%s)", what, cudaGetErrorName(e), cudaGetErrorString(e));
 }
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
-
-constexpr int kMaxDevices = 64;
-
-struct DeviceInfo {
-  bool ready = false;
-  int sms = 0;
-  uint32_t* status = nullptr;
-};
-std::mutex g_mu;
-DeviceInfo g_dev[kMaxDevices];
 
 // Per-device facts, looked up once per device with that device current.
 fa_status device_info(DeviceInfo* out) {
@@ -91,6 +88,19 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   });
   return fn;
 }
+
+}  // namespace host
+}  // namespace fa
+
+namespace {
+
+using fa::host::aligned16;
+using fa::host::aligned4;
+using fa::host::cuda_fail;
+using fa::host::device_info;
+using fa::host::DeviceInfo;
+using fa::host::encode_fn;
+using fa::host::fail;
 
 // A [BH, S, D] tensor of 16-bit elements as a 3-D TMA map with 128-byte swizzle;
 // one box is 64 elements of d by `rows` rows of one (batch, head).

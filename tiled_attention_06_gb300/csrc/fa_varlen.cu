@@ -1,0 +1,829 @@
+// Attention over packed sequences of different lengths with grouped K/V heads, for sm_103a:
+// whole prompts (K and V packed like Q) and chunks of new tokens over a paged cache.
+//
+// Per sequence, query head h and K/V head h / G: O = softmax(scale Q K^T + mask) V, computed
+// block by block with the running maximum and sum of the tiled forward (fa_prefill.cu).
+//
+// Tiles. The G heads of a group read the same K/V, so they share its tile loads: a tensor-core
+// tile of 128 rows holds TPT = 128 / G tokens times the G heads, which one TMA box of
+// (64 elements of d, G heads, TPT tokens) brings in that order. Besides the G-fold smaller K/V
+// traffic, a tile of few tokens wastes little of the key block that crosses the causal
+// diagonal, and a single token still fills G rows.
+//
+// Three kernels:
+//   var_plan_kernel   one CTA: reads the lengths on the device, lists the work items (two
+//                     tiles over the key blocks they see) from most key blocks to fewest, and
+//                     splits their key blocks when there are too few items for the SMs.
+//   var_fwd_kernel    persistent, one CTA per SM, which takes the list's items in a snake
+//                     order. Warps 0-3 and 4-7 are the softmax of tiles A and B (TMEM lane =
+//                     row, a whole row per thread), warp 8 loads by TMA, warp 9 issues the
+//                     MMAs. Tensor-pipe order S_A S_B | PV_A S_A' | PV_B S_B' | ..., so that
+//                     one tile's softmax runs while the tensor core works for the other.
+//   var_merge_kernel  joins the partial results of split items.
+//
+// Rows of V behind a sequence's last key belong to the next sequence, or are a page's unused
+// slots: their probability is 0, but 0 times an infinity or NaN is not. The MMA warp zeroes
+// them in shared memory before the block's P V; the scores of such keys are replaced by -inf.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <climits>
+#include <cstdint>
+
+#include "fa_mma.cuh"
+#include "fa_plan.h"
+#include "fa_ptx.cuh"
+#include "fa_varlen.h"
+
+namespace fa {
+namespace {
+
+constexpr int kTile = 128;     // rows of a tile (= TMEM lanes)
+constexpr int BN = kVarBN;
+constexpr float kTau = 8.0f;   // lazy-rescale threshold, log2 units
+constexpr uint32_t kSmemLimit = 232448;
+constexpr int kThreads = 384;
+constexpr int kTmaWarp = 8;
+constexpr int kMmaWarp = 9;
+// launched at 168 registers per thread: 128 x (200 + 200 + 104) = 384 x 168
+constexpr uint32_t kRegsSoftmax = 200;
+constexpr uint32_t kRegsProducer = 104;
+
+// Wait that ignores the abort flag (used while winding down).
+__device__ __forceinline__ void mbar_wait_quiet(uint32_t bar, uint32_t parity, const WaitCtx& wc) {
+  volatile uint32_t zero = 0;
+  WaitCtx w2 = wc;
+  w2.abort = &zero;
+  mbar_wait(bar, parity, w2);
+}
+
+// ------------------------------------------------------------------ masks by key position
+
+// Key blocks seen by queries at key positions [lo, hi) of a sequence with sk keys.
+__device__ __forceinline__ Range blocks_seen(int lo, int hi, int sk, const PrefillParams& m) {
+  PrefillParams f;
+  f.mask_mode = m.mask_mode;
+  f.window = m.window;
+  f.n_global = m.n_global;
+  f.Sq = sk;  // positions instead of query indices
+  return key_range(lo, hi, BN, sk, f, 0);
+}
+
+// The j-th visited block.
+__device__ __forceinline__ int block_at(const Range& r, int j) {
+  return j < r.a_end ? j : r.b_start + (j - r.a_end);
+}
+
+// Every query at positions [lo, hi] sees every key of the block at n0 (and all are in range).
+__device__ __forceinline__ bool block_full(int lo, int hi, int n0, int sk,
+                                           const PrefillParams& m) {
+  const int n1 = n0 + BN;
+  if (n1 > sk) return false;
+  switch (m.mask_mode) {
+    case FA_MASK_NONE:
+      return true;
+    case FA_MASK_BAND:
+      return static_cast<long long>(hi) - n0 <= m.window &&
+             static_cast<long long>(n1 - 1) - lo <= m.window;
+    case FA_MASK_PREFIX_LM:
+      return n1 <= m.n_global || n1 - 1 <= lo;
+    case FA_MASK_CAUSAL:
+      return n1 - 1 <= lo;
+    default:
+      return n1 - 1 <= lo && (n1 <= m.n_global || hi - max(n0, m.n_global) < m.window);
+  }
+}
+
+// Scores of the hidden keys of one row to -inf: per 32 columns a bit mask of the visible
+// ones, c <= lim and (c >= lo or c < gl).
+__device__ __forceinline__ void mask_row(uint32_t* s, int n0, int pos, int sk,
+                                         const PrefillParams& m) {
+  int lim = min(pos, sk - 1) - n0, lo = INT_MIN, gl = INT_MIN;
+  if (m.mask_mode == FA_MASK_NONE) {
+    lim = sk - 1 - n0;
+  } else if (m.mask_mode == FA_MASK_CAUSAL_WINDOW) {
+    const long long l0 = static_cast<long long>(pos) - m.window + 1 - n0;
+    lo = l0 < INT_MIN ? INT_MIN : static_cast<int>(l0);
+    gl = m.n_global - n0;
+  } else if (m.mask_mode == FA_MASK_BAND) {
+    const long long hi = static_cast<long long>(pos) + m.window;
+    lim = static_cast<int>((hi < sk - 1 ? hi : sk - 1) - n0);
+    const long long l0 = static_cast<long long>(pos) - m.window - n0;
+    lo = l0 < INT_MIN ? INT_MIN : static_cast<int>(l0);
+  } else if (m.mask_mode == FA_MASK_PREFIX_LM) {
+    lim = min(max(pos, m.n_global - 1), sk - 1) - n0;
+  }
+  lim = max(lim, -1);
+  lo = max(lo, -1);
+  gl = max(gl, 0);
+#pragma unroll
+  for (int k = 0; k < BN / 32; ++k) {
+    const int b = lim - 32 * k, a = lo - 32 * k, g = gl - 32 * k;
+    const uint32_t upto = b < 0 ? 0u : (b >= 31 ? 0xffffffffu : (2u << b) - 1u);
+    const uint32_t from = a <= 0 ? 0xffffffffu : (a >= 32 ? 0u : ~((1u << a) - 1u));
+    const uint32_t below = g <= 0 ? 0u : (g >= 32 ? 0xffffffffu : (1u << g) - 1u);
+    const uint32_t mk = upto & (from | below);
+#pragma unroll
+    for (int c = 0; c < 32; ++c)
+      if (!((mk >> c) & 1u)) s[32 * k + c] = __float_as_uint(-INFINITY);
+  }
+}
+
+// ------------------------------------------------------------------ plan
+
+constexpr int kPlanThreads = 1024;
+constexpr int kBins = 1024;
+constexpr int kCandidates = 16;
+
+struct PlanSmem {
+  int off[kPlanThreads + 1];  // token blocks before each sequence of the batch
+  int q0[kPlanThreads], sq[kPlanThreads], k0[kPlanThreads], sk[kPlanThreads];
+  int warp_sum[32];
+  int bins[kBins + 1];
+  int pairs, n_max, slots, groups, split;
+  unsigned long long cost;
+  int units[kCandidates];
+};
+
+// Calls f(token block of a sequence ...) for every token block of every sequence, sequences
+// in batches of one per thread. Every thread of the CTA takes part.
+template <typename F>
+__device__ __forceinline__ void for_each_block(const VarParams& p, PlanSmem& s, bool report,
+                                               F f) {
+  const int tpi = 2 * p.TPT;
+  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+  for (int base = 0; base < p.B; base += kPlanThreads) {
+    const int b = base + tid;
+    int nblk = 0;
+    if (b < p.B) {
+      const int a = p.cu_q[b], e = p.cu_q[b + 1];
+      bool bad = a < 0 || e < a || e > p.total_q;
+      int sq = bad ? 0 : e - a, sk, k0 = 0;
+      if (p.block_table) {
+        const int cap = p.page_size * p.max_pages;
+        sk = p.ctx[b];
+        bad = bad || sk < 0 || sk > cap;
+        sk = sk < 0 ? 0 : min(sk, cap);
+      } else {
+        k0 = p.cu_k[b];
+        const int ke = p.cu_k[b + 1];
+        const bool kbad = k0 < 0 || ke < k0 || ke > p.total_k;
+        sk = kbad ? 0 : ke - k0;
+        bad = bad || kbad;
+      }
+      if (bad && report) atomicOr(p.m.status, FA_DEV_BAD_PAGE);
+      s.q0[tid] = a;
+      s.sq[tid] = sq;
+      s.k0[tid] = k0;
+      s.sk[tid] = sk;
+      nblk = (sq + tpi - 1) / tpi;
+    }
+    int x = nblk;  // inclusive scan over the CTA
+    for (int o = 1; o < 32; o *= 2) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) s.warp_sum[warp] = x;
+    __syncthreads();
+    if (warp == 0) {
+      int w = s.warp_sum[lane];
+      for (int o = 1; o < 32; o *= 2) {
+        const int y = __shfl_up_sync(0xffffffffu, w, o);
+        if (lane >= o) w += y;
+      }
+      s.warp_sum[lane] = w;
+    }
+    __syncthreads();
+    s.off[tid + 1] = x + (warp ? s.warp_sum[warp - 1] : 0);
+    if (tid == 0) s.off[0] = 0;
+    __syncthreads();
+    const int nseq = min(kPlanThreads, p.B - base), total = s.off[nseq];
+    for (int i = tid; i < total; i += kPlanThreads) {
+      int lo = 0, hi = nseq;  // last sequence with off <= i
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (s.off[mid] <= i) lo = mid; else hi = mid;
+      }
+      const int first = (i - s.off[lo]) * tpi;
+      VarUnit u;
+      u.q0 = s.q0[lo] + first;
+      u.nq = min(tpi, s.sq[lo] - first);
+      u.sk = s.sk[lo];
+      u.k0 = s.k0[lo];
+      u.qpos = first + s.sk[lo] - s.sq[lo];
+      u.seq = base + lo;
+      u.j0 = 0;
+      u.j1 = range_count(blocks_seen(u.qpos, u.qpos + u.nq, u.sk, p.m));
+      u.slot = -1;
+      f(u);
+    }
+    __syncthreads();
+  }
+}
+
+__device__ __forceinline__ int bin_of(int n, const VarParams& p) {
+  return kBins - 1 - min(kBins - 1, n >> p.cost_shift);  // most key blocks first
+}
+
+// The work list. Splitting: an item of n key blocks takes about n + 4 block times (the 4:
+// first loads, last P V, epilogue); with splits of at most S blocks the launch takes about
+// max(S + 4, ceil(items / SMs) (mean + 4)), and 8 more to join them (a 512-token chunk over
+// 8192 cached tokens with 8 K/V heads has 64 items for 152 SMs). The least of a few S wins.
+__global__ void __launch_bounds__(kPlanThreads) var_plan_kernel(const VarParams p, int sms) {
+  __shared__ PlanSmem s;
+  const int tid = threadIdx.x;
+  for (int i = tid; i <= kBins; i += kPlanThreads) s.bins[i] = 0;
+  if (tid < kCandidates) s.units[tid] = 0;
+  if (tid == 0) {
+    s.pairs = s.n_max = s.slots = s.groups = 0;
+    s.cost = 0;
+    s.split = INT_MAX;
+  }
+  __syncthreads();
+  for_each_block(p, s, true, [&](const VarUnit& u) {
+    atomicAdd(&s.bins[bin_of(u.j1, p) + 1], 1);
+    if (p.part) {
+      atomicAdd(&s.pairs, 1);
+      atomicMax(&s.n_max, u.j1);
+      atomicAdd(&s.cost, static_cast<unsigned long long>(u.j1));
+    }
+  });
+  if (p.part && s.pairs * p.Hkv < 2 * sms && s.n_max >= 8) {
+    for_each_block(p, s, false, [&](const VarUnit& u) {
+      for (int c = 0; c < kCandidates; ++c) {
+        const int S = (s.n_max + c) / (c + 1);
+        atomicAdd(&s.units[c], max(1, (u.j1 + S - 1) / S));
+      }
+    });
+    if (tid == 0) {
+      float best = 0.f;
+      for (int c = 0; c < kCandidates; ++c) {
+        const int S = (s.n_max + c) / (c + 1), items = s.units[c] * p.Hkv;
+        if (c > 0 && (S < 4 || items > kVarMaxSplit || s.units[c] > p.max_units)) break;
+        const float mean = static_cast<float>(s.cost) / s.units[c];
+        float est = fmaxf(S + 4.f, ((items + sms - 1) / sms) * (mean + 4.f));
+        if (c > 0) est += 8.f;
+        if (c == 0 || est < best) {
+          best = est;
+          s.split = c == 0 ? INT_MAX : S;
+        }
+      }
+    }
+    __syncthreads();
+    if (s.split != INT_MAX) {  // bins of the split items
+      for (int i = tid; i <= kBins; i += kPlanThreads) s.bins[i] = 0;
+      __syncthreads();
+      for_each_block(p, s, false, [&](const VarUnit& u) {
+        const int ns = max(1, (u.j1 + s.split - 1) / s.split);
+        for (int k = 0; k < ns; ++k)
+          atomicAdd(&s.bins[bin_of(u.j1 * (k + 1) / ns - u.j1 * k / ns, p) + 1], 1);
+      });
+    }
+  }
+  // exclusive scan of the bins (one bin per thread)
+  static_assert(kBins == kPlanThreads, "one bin per thread");
+  {
+    const int lane = tid % 32, warp = tid / 32;
+    const int v = s.bins[tid + 1];
+    int x = v;
+    for (int o = 1; o < 32; o *= 2) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) s.warp_sum[warp] = x;
+    __syncthreads();
+    if (warp == 0) {
+      int w = s.warp_sum[lane];
+      for (int o = 1; o < 32; o *= 2) {
+        const int y = __shfl_up_sync(0xffffffffu, w, o);
+        if (lane >= o) w += y;
+      }
+      s.warp_sum[lane] = w;
+    }
+    __syncthreads();
+    const int incl = x + (warp ? s.warp_sum[warp - 1] : 0);
+    s.bins[tid] = incl - v;
+    if (tid == kBins - 1) {  // more only when starts overlap, which no sequence of rows has
+      p.hdr->units = min(incl, p.max_units);
+      if (incl > p.max_units) atomicOr(p.m.status, FA_DEV_BAD_PAGE);
+    }
+    __syncthreads();
+  }
+  const int split = s.split;
+  for_each_block(p, s, false, [&](VarUnit u) {
+    const int n = u.j1, ns = split == INT_MAX ? 1 : max(1, (n + split - 1) / split);
+    if (ns > 1) {
+      u.slot = atomicAdd(&s.slots, ns);
+      p.groups[atomicAdd(&s.groups, 1)] = VarGroup{u.q0, u.nq, u.slot, ns};
+    }
+    for (int k = 0; k < ns; ++k) {
+      u.j0 = n * k / ns;
+      u.j1 = n * (k + 1) / ns;
+      const int at = atomicAdd(&s.bins[bin_of(u.j1 - u.j0, p)], 1);
+      if (at < p.max_units) p.units[at] = u;
+      if (ns > 1) ++u.slot;
+    }
+  });
+  if (tid == 0) p.hdr->groups = s.groups;
+}
+
+// ------------------------------------------------------------------ forward
+
+template <int D>
+struct Cfg {
+  static constexpr int KCH = D / 64;
+  static constexpr int Q_BYTES = kTile * D * 2;  // one tile
+  static constexpr int TILE_BYTES = BN * D * 2;
+  static constexpr int BAR_BYTES = 1024;
+  static constexpr int FIT = (int)((kSmemLimit - 1024 - BAR_BYTES - 2 * Q_BYTES) / TILE_BYTES);
+  static constexpr int NSLOT = FIT > 8 ? 8 : FIT;
+  static constexpr int SMEM = 1024 + 2 * Q_BYTES + NSLOT * TILE_BYTES + BAR_BYTES;
+  static constexpr int TMEM_COLS = 512;  // S_A S_B [0, 256), O_A O_B [256, 256 + 2 D)
+  static_assert(2 * BN + 2 * D <= 512, "TMEM over budget");
+};
+
+struct Bars {
+  uint64_t full[8], empty[8];
+  uint64_t q_full[2], q_empty[2];
+  uint64_t s_full[2], p_full[2], pv_done[2], o_empty[2];
+  uint64_t final_mma;
+  uint32_t tmem_base;
+  uint32_t abort;
+};
+
+// Item t of the launch: its unit and K/V head.
+struct Item {
+  VarUnit u;
+  int kvh;
+  Range rg;
+  int tiles;  // 2, or 1 when the second tile has no token
+};
+
+// The k-th item of this CTA (false when there is none left). Snake order over a list sorted
+// by cost: round r covers items r G .. r G + G - 1, backwards on odd rounds.
+__device__ __forceinline__ bool next_item(const VarParams& p, int total, int& k, Item& it) {
+  const int G = gridDim.x;
+  while (k * G < total) {
+    const int t = item_of_round(k, G, blockIdx.x);
+    ++k;
+    if (t >= total) continue;
+    const int4* src = reinterpret_cast<const int4*>(p.units + t / p.Hkv);
+    const int4 a = src[0], b = src[1], c = src[2];
+    it.u.q0 = a.x, it.u.nq = a.y, it.u.sk = a.z, it.u.k0 = a.w;
+    it.u.qpos = b.x, it.u.seq = b.y, it.u.j0 = b.z, it.u.j1 = b.w;
+    it.u.slot = c.x;
+    it.kvh = t - (t / p.Hkv) * p.Hkv;
+    it.rg = blocks_seen(it.u.qpos, it.u.qpos + it.u.nq, it.u.sk, p.m);
+    it.tiles = it.u.nq > p.TPT ? 2 : 1;
+    return true;
+  }
+  return false;
+}
+
+// One row of one S tile by one thread: mask, running maximum, lazy rescale of O and l (only
+// when the maximum rose by more than kTau; decided per warp), P = 2^(S sl2 - m) rounded to 16
+// bits over S, l += the unrounded sum. P of at most 2^8 and l in FP32 keep the rounding of P
+// the only one on the way.
+template <int D, bool BF16>
+__device__ __forceinline__ void softmax_row(uint32_t t_lane, uint32_t s_col, uint32_t o_col,
+                                            bool full, int n0, int pos, int sk,
+                                            const PrefillParams& m, float& m_ref, float& l) {
+  uint32_t s[BN];
+  tmem_ld64(t_lane + s_col, s);
+  tmem_ld64(t_lane + s_col + 64, s + 64);
+  tmem_ld_wait<BN>(s);
+  if (!full) mask_row(s, n0, pos, sk, m);
+  float mx[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    mx[i] = fmaxf(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1]));
+#pragma unroll
+  for (int c = 8; c < BN; c += 8)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      mx[i] = max3f(mx[i], __uint_as_float(s[c + 2 * i]), __uint_as_float(s[c + 2 * i + 1]));
+  const float m_new = fmaxf(m_ref, max3f(mx[0], mx[1], fmaxf(mx[2], mx[3])) * m.sl2);
+  const bool need = m_ref != -INFINITY && m_new > m_ref + kTau;
+  if (m_ref == -INFINITY) m_ref = m_new;
+  if (__any_sync(0xffffffffu, need)) {
+    const float alpha = need ? ex2_approx(m_ref - m_new) : 1.f;
+    if (need) {
+      l *= alpha;
+      m_ref = m_new;
+    }
+#pragma unroll 1
+    for (int c = 0; c < D / 32; ++c) {
+      uint32_t ov[32];
+      tmem_ld32(t_lane + o_col + c * 32, ov);
+      tmem_ld_wait<32>(ov);
+#pragma unroll
+      for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
+      tmem_st32(t_lane + o_col + c * 32, ov);
+    }
+  }
+  const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
+  const uint64_t scale2 = f2(m.sl2, m.sl2), neg_m2 = f2(-m_use, -m_use);
+  uint64_t acc[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int c = 0; c < BN; c += 2) {
+    const uint64_t x =
+        f2_fma(f2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), scale2, neg_m2);
+    float x0, x1;
+    f2_split(x, x0, x1);
+    const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+    acc[(c / 2) & 3] = f2_add(acc[(c / 2) & 3], f2(p0, p1));
+    s[c / 2] = BF16 ? cvt_pack_bf16(p0, p1) : cvt_pack_f16(p0, p1);
+  }
+  float a0, a1;
+  f2_split(f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3])), a0, a1);
+  l += a0 + a1;
+  tmem_st32(t_lane + s_col, s);
+  tmem_st32(t_lane + s_col + 32, s + 32);
+  tmem_st_wait();
+}
+
+template <int D, bool BF16, bool PAGED>
+__global__ void __launch_bounds__(kThreads, 1)
+    var_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                   const __grid_constant__ CUtensorMap tmV, const __grid_constant__ VarParams p) {
+  using C = Cfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* smem = smem_raw + (base - raw);
+  const uint32_t sQ = base, sRing = base + 2 * C::Q_BYTES;
+  Bars* bars = reinterpret_cast<Bars*>(smem + 2 * C::Q_BYTES + C::NSLOT * C::TILE_BYTES);
+  auto B = [&](uint64_t& b) { return smem_u32(&b); };
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::NSLOT; ++i) {
+      mbar_init(B(bars->full[i]), 1);
+      mbar_init(B(bars->empty[i]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(B(bars->q_full[i]), 1);
+      mbar_init(B(bars->q_empty[i]), 1);
+      mbar_init(B(bars->s_full[i]), 1);
+      mbar_init(B(bars->p_full[i]), 128);
+      mbar_init(B(bars->pv_done[i]), 1);
+      mbar_init(B(bars->o_empty[i]), 128);
+    }
+    mbar_init(B(bars->final_mma), 1);
+    bars->abort = 0;
+    mbar_fence_init();
+  }
+  if (warp == 0) {
+    tmem_alloc(smem_u32(&bars->tmem_base), C::TMEM_COLS);
+    tmem_relinquish();
+  }
+  if (warp == kTmaWarp && lane == 0) {
+    tma_prefetch_desc(&tmQ);
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem_base;
+  const WaitCtx wc{&bars->abort, p.m.status, p.m.timeout_ns};
+  const int total = p.hdr->units * p.Hkv;
+  // The role branches never rejoin: each ends with the CTA-wide teardown barrier, so no code
+  // runs under two register budgets.
+  if (warp >= 8) {
+    regs_decrease<kRegsProducer>();
+    if (warp == kTmaWarp) {
+      // -------------------------------------------------------------- TMA producer
+      const bool leader = elect_one();
+      uint32_t pos = 0, iq[2] = {0, 0};
+      uint32_t fills[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+      bool ok = true;
+      Item it;
+      const uint32_t q_bytes = static_cast<uint32_t>(p.TPT * p.G) * D * 2;
+      for (int k = 0; ok && next_item(p, total, k, it);) {
+        if (it.u.j1 == it.u.j0) continue;
+        for (int q = 0; q < it.tiles && ok; ++q) {
+          if (iq[q] > 0 && !(ok = mbar_wait(B(bars->q_empty[q]), (iq[q] - 1) & 1, wc))) break;
+          if (leader) {
+            mbar_arrive_expect_tx(B(bars->q_full[q]), q_bytes);
+            for (int c = 0; c < C::KCH; ++c)
+              tma_load_3d(sQ + q * C::Q_BYTES + c * (kTile * 128), &tmQ, B(bars->q_full[q]),
+                          c * 64, it.kvh * p.G, it.u.q0 + q * p.TPT);
+          }
+          ++iq[q];
+        }
+        for (int j = it.u.j0; j < it.u.j1 && ok; ++j) {
+          const int n0 = block_at(it.rg, j) * BN;
+          // paged: lane i loads box i of the block, rows of one page; boxes behind the last
+          // key are left out
+          int y = 0, z = 0, boxes = 1;
+          if constexpr (PAGED) {
+            boxes = (min(BN, it.u.sk - n0) + p.box - 1) / p.box;
+            if (lane < boxes) {
+              const int row = n0 + lane * p.box, lp = row / p.page_size;
+              int phys = p.block_table[static_cast<size_t>(it.u.seq) * p.max_pages + lp];
+              if (phys < 0 || phys >= p.num_pages) {
+                atomicOr(p.m.status, FA_DEV_BAD_PAGE);
+                phys = 0;
+              }
+              y = row - lp * p.page_size;
+              z = phys * p.Hkv + it.kvh;
+            }
+          }
+          for (int kv = 0; kv < 2; ++kv) {  // K, then V
+            const int slot = pos % C::NSLOT;
+            const uint32_t use = pos / C::NSLOT;
+            if (!(ok = mbar_wait(B(bars->empty[slot]), (use & 1) ^ 1, wc))) break;
+            const uint32_t dst = sRing + slot * C::TILE_BYTES;
+            const void* map = kv ? (const void*)&tmV : (const void*)&tmK;
+            if constexpr (PAGED) {
+              if (leader)
+                mbar_arrive_expect_tx(B(bars->full[slot]), boxes * p.box * (C::KCH * 128));
+              __syncwarp();
+              if (lane < boxes)
+                for (int c = 0; c < C::KCH; ++c)
+                  tma_load_3d(dst + c * (BN * 128) + lane * p.box * 128, map, B(bars->full[slot]),
+                              c * 64, y, z);
+              __syncwarp();
+            } else if (leader) {
+              mbar_arrive_expect_tx(B(bars->full[slot]), C::TILE_BYTES);
+              for (int c = 0; c < C::KCH; ++c)
+                tma_load_3d(dst + c * (BN * 128), map, B(bars->full[slot]), c * 64, it.kvh,
+                            it.u.k0 + n0);
+            }
+            fills[slot] = use + 1;
+            ++pos;
+          }
+        }
+      }
+      if (!ok) {  // wind down: every load issued lands before the CTA exits
+        for (int s = 0; s < C::NSLOT; ++s)
+          if (fills[s] > 0) mbar_wait_quiet(B(bars->full[s]), (fills[s] - 1) & 1, wc);
+        for (int q = 0; q < 2; ++q)
+          if (iq[q] > 0) mbar_wait_quiet(B(bars->q_full[q]), (iq[q] - 1) & 1, wc);
+      }
+      __syncwarp();
+    } else if (warp == kMmaWarp) {
+      // -------------------------------------------------------------- MMA issuer
+      const bool leader = elect_one();
+      const uint32_t tS[2] = {tmem, tmem + BN};
+      const uint32_t tO[2] = {tmem + 2 * BN, tmem + 2 * BN + D};
+      uint32_t pos = 0, iq[2] = {0, 0}, tc[2] = {0, 0};
+      bool ok = true;
+      Item it;
+      auto qk = [&](int q, int slot) {
+        issue_qk<D, BN, BF16>(tS[q], sQ + q * C::Q_BYTES, sRing + slot * C::TILE_BYTES);
+        umma_commit(B(bars->s_full[q]));
+      };
+      for (int k = 0; ok && next_item(p, total, k, it);) {
+        const int n = it.u.j1 - it.u.j0, last = it.tiles - 1;
+        if (n == 0) continue;
+        {
+          const int slot = pos % C::NSLOT;
+          if (!(ok = mbar_wait(B(bars->full[slot]), (pos / C::NSLOT) & 1, wc))) break;
+          for (int q = 0; q < it.tiles && ok; ++q) {
+            if (!(ok = mbar_wait(B(bars->q_full[q]), iq[q] & 1, wc))) break;
+            tc_fence_after();
+            if (leader) {
+              qk(q, slot);
+              if (n == 1) umma_commit(B(bars->q_empty[q]));
+            }
+          }
+          if (!ok) break;
+          if (leader) umma_commit(B(bars->empty[slot]));
+          ++pos;
+        }
+        for (int j = 0; j < n && ok; ++j) {
+          const int vslot = pos % C::NSLOT, kslot = (pos + 1) % C::NSLOT;
+          if (!(ok = mbar_wait(B(bars->full[vslot]), (pos / C::NSLOT) & 1, wc))) break;
+          const int live = it.u.sk - block_at(it.rg, it.u.j0 + j) * BN;  // rows below sk
+          if (live < BN) {  // zero the rows of V behind the last key
+            uint8_t* v = smem + 2 * C::Q_BYTES + vslot * C::TILE_BYTES;
+            for (int c = 0; c < C::KCH; ++c) {
+              uint4* r = reinterpret_cast<uint4*>(v + c * (BN * 128));
+              for (int i = live * 8 + lane; i < BN * 8; i += 32) r[i] = make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
+          tc_fence_after();
+          for (int q = 0; q < it.tiles && ok; ++q) {
+            if (!(ok = mbar_wait(B(bars->p_full[q]), tc[q] & 1, wc))) break;
+            ++tc[q];
+            tc_fence_after();
+            if (j == 0 && iq[q] > 0) {  // the epilogue of the tile's previous item has read O
+              if (!(ok = mbar_wait(B(bars->o_empty[q]), (iq[q] - 1) & 1, wc))) break;
+              tc_fence_after();
+            }
+            if (leader) {
+              issue_pv<D, BN, BF16>(tO[q], tS[q], sRing + vslot * C::TILE_BYTES, j > 0);
+              if (j == n - 1) umma_commit(B(bars->pv_done[q]));
+              if (q == last) umma_commit(B(bars->empty[vslot]));
+            }
+            if (j + 1 < n) {  // S(j+1) overwrites P(j) only after PV(j) in the pipe
+              if (q == 0) {
+                if (!(ok = mbar_wait(B(bars->full[kslot]), ((pos + 1) / C::NSLOT) & 1, wc))) break;
+                tc_fence_after();
+              }
+              if (leader) {
+                qk(q, kslot);
+                if (j + 2 == n) umma_commit(B(bars->q_empty[q]));
+                if (q == last) umma_commit(B(bars->empty[kslot]));
+              }
+            }
+          }
+          pos += (j + 1 < n) ? 2 : 1;
+        }
+        for (int q = 0; q < it.tiles; ++q) ++iq[q];
+      }
+      if (leader) umma_commit(B(bars->final_mma));  // all MMAs done before TMEM is released
+      mbar_wait_quiet(B(bars->final_mma), 0, wc);
+      __syncwarp();
+    }
+    tc_fence_before();
+    __syncthreads();  // teardown: every role is done with TMEM and shared memory
+    return;
+  }
+  regs_increase<kRegsSoftmax>();
+  // ---------------------------------------------------------------- softmax, tiles A / B
+  const int q = warp / 4;
+  const int row = (warp % 4) * 32 + lane;
+  const uint32_t t_lane = tmem + (static_cast<uint32_t>((warp % 4) * 32) << 16);
+  const uint32_t s_col = q * BN, o_col = 2 * BN + q * D;
+  const int tok = row / p.G, head = row - (row / p.G) * p.G;  // of the tile, of the group
+  uint32_t ii = 0, tc = 0;
+  bool ok = true;
+  Item it;
+  for (int k = 0; ok && next_item(p, total, k, it);) {
+    if (q >= it.tiles) continue;
+    const int n = it.u.j1 - it.u.j0;
+    const int left = it.u.nq - q * p.TPT;  // tokens of this tile and behind it
+    const int toks = min(p.TPT, left);
+    const bool valid = tok < toks;
+    const bool work = (warp % 4) * 32 < toks * p.G;  // a warp without rows only keeps step
+    const size_t orow = static_cast<size_t>(it.u.q0 + q * p.TPT + tok) * p.H + it.kvh * p.G + head;
+    uint16_t* out = static_cast<uint16_t*>(p.o) +
+                    static_cast<int64_t>(it.u.q0 + q * p.TPT + tok) * p.o_token +
+                    (it.kvh * p.G + head) * D;
+    if (n == 0) {  // nothing visible for any row of the item
+      if (valid) {
+        for (int c = 0; c < D / 8; ++c) reinterpret_cast<uint4*>(out)[c] = make_uint4(0, 0, 0, 0);
+        if (p.lse) p.lse[orow] = -INFINITY;
+      }
+      continue;
+    }
+    const int p_lo = it.u.qpos + q * p.TPT, p_hi = p_lo + toks - 1, pos_q = p_lo + tok;
+    float m_ref = -INFINITY, l = 0.f;
+    for (int j = it.u.j0; j < it.u.j1; ++j) {
+      const int n0 = block_at(it.rg, j) * BN;
+      ok = mbar_wait(B(bars->s_full[q]), tc & 1, wc);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      tc_fence_after();
+      // S(j) was issued after PV(j-1), so O needs no wait before a rescale
+      if (work)
+        softmax_row<D, BF16>(t_lane, s_col, o_col, block_full(p_lo, p_hi, n0, it.u.sk, p.m), n0,
+                             pos_q, it.u.sk, p.m, m_ref, l);
+      tc_fence_before();
+      mbar_arrive(B(bars->p_full[q]));
+      ++tc;
+    }
+    if (!ok) break;
+    ok = mbar_wait(B(bars->pv_done[q]), ii & 1, wc);
+    ok = __all_sync(0xffffffffu, ok);
+    if (!ok) break;
+    tc_fence_after();
+    if (it.u.slot < 0) {
+      const float inv_l = l > 0.f ? 1.f / l : 0.f;
+      const bool wide = ((reinterpret_cast<uintptr_t>(p.o) | (p.o_token * 2)) & 31u) == 0;
+#pragma unroll 1
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t ov[32], pk[16];
+        tmem_ld32(t_lane + o_col + c * 32, ov);
+        tmem_ld_wait<32>(ov);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const float a = __uint_as_float(ov[2 * e]) * inv_l, b = __uint_as_float(ov[2 * e + 1]) * inv_l;
+          pk[e] = BF16 ? cvt_pack_bf16(a, b) : cvt_pack_f16(a, b);
+        }
+        if (valid) {
+          if (wide) {
+            st_global_v8(out + c * 32, pk);
+            st_global_v8(out + c * 32 + 16, pk + 8);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              reinterpret_cast<uint4*>(out + c * 32)[e] =
+                  make_uint4(pk[4 * e], pk[4 * e + 1], pk[4 * e + 2], pk[4 * e + 3]);
+          }
+        }
+      }
+      if (valid && p.lse)
+        p.lse[orow] = l > 0.f ? (m_ref + lg2_approx(l)) * 0.69314718055994531f : -INFINITY;
+    } else {  // partial result: O unnormalised, m in log2 units, l
+      float* slot = p.part + (static_cast<size_t>(it.u.slot) * p.Hkv + it.kvh) *
+                                 (static_cast<size_t>(kVarSplitRows) * (D + 2));
+      const int r = q * kTile + row;
+#pragma unroll 1
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t ov[32];
+        tmem_ld32(t_lane + o_col + c * 32, ov);
+        tmem_ld_wait<32>(ov);
+        if (valid) {
+          uint4* dst = reinterpret_cast<uint4*>(slot + static_cast<size_t>(r) * D + c * 32);
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            dst[e] = make_uint4(ov[4 * e], ov[4 * e + 1], ov[4 * e + 2], ov[4 * e + 3]);
+        }
+      }
+      if (valid) {
+        slot[kVarSplitRows * D + r] = m_ref;
+        slot[kVarSplitRows * (D + 1) + r] = l;
+      }
+    }
+    tc_fence_before();
+    mbar_arrive(B(bars->o_empty[q]));
+    ++ii;
+  }
+  tc_fence_before();
+  __syncthreads();  // teardown
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::TMEM_COLS);
+  }
+}
+
+// ------------------------------------------------------------------ joining split items
+
+// One warp per row: M = max m_s, O = sum 2^(m_s - M) O_s / sum 2^(m_s - M) l_s over the
+// group's slots in order.
+template <int D, bool BF16>
+__global__ void __launch_bounds__(256) var_merge_kernel(const VarParams p) {
+  constexpr int E = D / 32;  // elements per lane
+  const int lane = threadIdx.x % 32;
+  const int warps = gridDim.x * 8, per = p.Hkv * kVarSplitRows;
+  const int total = p.hdr->groups * per;
+  const size_t step = static_cast<size_t>(p.Hkv) * kVarSplitRows * (D + 2);
+  for (int w = blockIdx.x * 8 + threadIdx.x / 32; w < total; w += warps) {
+    const VarGroup g = p.groups[w / per];
+    const int kvh = (w % per) / kVarSplitRows, r = w % kVarSplitRows;
+    const int tok = (r / kTile) * p.TPT + (r % kTile) / p.G;
+    if ((r % kTile) / p.G >= p.TPT || tok >= g.nq) continue;
+    const float* s0 = p.part + (static_cast<size_t>(g.slot) * p.Hkv + kvh) *
+                                   (static_cast<size_t>(kVarSplitRows) * (D + 2));
+    float M = -INFINITY, L = 0.f, acc[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+    for (int s = 0; s < g.n; ++s) {
+      const float* sl = s0 + s * step;
+      const float m = sl[kVarSplitRows * D + r], l = sl[kVarSplitRows * (D + 1) + r];
+      if (!(l > 0.f)) continue;  // saw no key
+      const float mn = fmaxf(M, m), c = ex2_approx(M - mn), wt = ex2_approx(m - mn);
+      L = L * c + l * wt;
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+        acc[e] = acc[e] * c + wt * sl[static_cast<size_t>(r) * D + lane * E + e];
+      M = mn;
+    }
+    const float inv = L > 0.f ? 1.f / L : 0.f;
+    const int h = kvh * p.G + (r % kTile) % p.G;
+    uint32_t* out = reinterpret_cast<uint32_t*>(
+        static_cast<uint16_t*>(p.o) + static_cast<int64_t>(g.q0 + tok) * p.o_token + h * D);
+#pragma unroll
+    for (int e = 0; e < E; e += 2)
+      out[(lane * E + e) / 2] = BF16 ? cvt_pack_bf16(acc[e] * inv, acc[e + 1] * inv)
+                                     : cvt_pack_f16(acc[e] * inv, acc[e + 1] * inv);
+    if (lane == 0 && p.lse)
+      p.lse[static_cast<size_t>(g.q0 + tok) * p.H + h] =
+          L > 0.f ? (M + lg2_approx(L)) * 0.69314718055994531f : -INFINITY;
+  }
+}
+
+template <int D, bool BF16>
+cudaError_t launch_t(const VarLaunch& L, cudaStream_t stream) {
+  var_plan_kernel<<<1, kPlanThreads, 0, stream>>>(L.p, L.sms);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  auto* k = L.p.block_table ? var_fwd_kernel<D, BF16, true> : var_fwd_kernel<D, BF16, false>;
+  constexpr int smem = Cfg<D>::SMEM;
+  e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  const int64_t items = static_cast<int64_t>(L.p.max_units) * L.p.Hkv;
+  const int grid = static_cast<int>(items < L.sms ? items : L.sms);
+  k<<<grid, kThreads, smem, stream>>>(L.tmQ, L.tmK, L.tmV, L.p);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if (L.p.part) {
+    var_merge_kernel<D, BF16><<<L.sms * 8, 256, 0, stream>>>(L.p);
+    e = cudaGetLastError();
+  }
+  return e;
+}
+
+}  // namespace
+
+cudaError_t launch_varlen(const VarLaunch& L, int D, bool bf16, cudaStream_t stream) {
+  if (D == 128) return bf16 ? launch_t<128, true>(L, stream) : launch_t<128, false>(L, stream);
+  return bf16 ? launch_t<64, true>(L, stream) : launch_t<64, false>(L, stream);
+}
+
+}  // namespace fa

@@ -1,0 +1,105 @@
+// Internal interface between the C-ABI layer (fa_api_varlen.cu) and the kernels over packed
+// tokens: rotary positions, packed grouped-head attention, its gradient, and attention of new
+// tokens over a paged cache.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cstddef>
+#include <cstdint>
+
+#include "fa.h"
+#include "fa_internal.h"
+
+namespace fa {
+
+// Rotary positions (fa_rope.cu). Token and head steps are in elements. fa_rope: x -> y, H
+// heads, pos[T]. fa_rope_append: x = q and y = q_out with heads d apart, k and v beside it,
+// positions from ctx and cu, k and v into the pools.
+struct RopeParams {
+  const void* x;
+  void* y;
+  const double* freqs;  // [rot/2] radians per position
+  const int32_t* pos;
+  int64_t T, x_token, x_head, y_token, y_head;
+  int H, d, rot;
+  float amplitude;
+  int inverse, copy_rest;  // copy_rest: elements rot .. d-1 are copied (not when y is x)
+  const void* k;
+  const void* v;
+  void* k_pages;
+  void* v_pages;
+  int64_t k_token, v_token;
+  const int32_t* cu;           // [B+1]
+  const int32_t* ctx;          // [B] tokens cached before the chunk
+  const int32_t* block_table;  // [B, max_pages]
+  int B, Hkv, page_size, max_pages, num_pages;
+  uint32_t* status;
+};
+cudaError_t launch_rope(const RopeParams& p, int dtype, bool half_style, bool vec, int sms,
+                        cudaStream_t stream);
+cudaError_t launch_rope_append(const RopeParams& p, int dtype, bool half_style, bool vec, int sms,
+                               cudaStream_t stream);
+
+
+// ------------------------------------------------ packed grouped-head attention (fa_varlen.cu)
+//
+// Query heads come in groups of G = H / Hkv that read the same K/V head. A tensor-core tile of
+// 128 rows holds TPT = 128 / G consecutive tokens with the G heads of one group (row r: token
+// r / G, head r % G of the group); a work item is two such tiles, 2 TPT tokens, over a run of
+// the key blocks that they see.
+
+constexpr int kVarBN = 128;  // keys per block
+
+// One work item of every K/V head, written by the plan kernel (48 bytes).
+struct VarUnit {
+  int32_t q0, nq;  // first row of q, tokens (<= 2 TPT)
+  int32_t sk, k0;  // keys of the sequence; its first row of k and v
+  int32_t qpos;    // key position of the first token (queries are the last of the keys)
+  int32_t seq;
+  int32_t j0, j1;  // which of the visited key blocks
+  int32_t slot;    // -1: writes o and lse; else a partial result, slot * Hkv + kv head
+  int32_t pad[3];
+};
+// A token block whose key blocks were split: its partial results, slot .. slot + n - 1.
+struct VarGroup {
+  int32_t q0, nq, slot, n;
+};
+struct VarHeader {
+  int32_t units, groups, pad[14];
+};
+
+constexpr int kVarMaxSplit = 456;  // work items (all K/V heads) of a split plan: 3 per SM
+constexpr int kVarSplitRows = 256;
+inline size_t var_slot_floats(int d) { return static_cast<size_t>(kVarSplitRows) * (d + 2); }
+
+struct VarParams {
+  PrefillParams m;  // mask_mode, window, n_global, sl2, status, timeout_ns alone are read
+  void* o;          // [total_q, H, D], o_token elements from one token to the next
+  float* lse;       // [total_q, H] or nullptr
+  int64_t o_token;
+  int B, H, Hkv, G, TPT, total_q, total_k;
+  const int32_t* cu_q;  // [B+1]
+  const int32_t* cu_k;  // [B+1] (contiguous K/V)
+  // paged K/V: lengths and table; a key block is loaded as boxes of `box` rows of one page
+  const int32_t* ctx;
+  const int32_t* block_table;
+  int page_size, max_pages, num_pages, box;
+  // workspace
+  VarHeader* hdr;
+  VarUnit* units;
+  VarGroup* groups;
+  float* part;    // slots, or nullptr: no splitting
+  int max_units;  // entries of `units`
+  int cost_shift; // key blocks >> cost_shift is a sort key below 1024
+};
+
+struct VarLaunch {
+  CUtensorMap tmQ, tmK, tmV;
+  VarParams p;
+  int sms;
+};
+cudaError_t launch_varlen(const VarLaunch& L, int D, bool bf16, cudaStream_t stream);
+
+}  // namespace fa
