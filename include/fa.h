@@ -508,6 +508,27 @@ fa_status fa_fwd_varlen(const fa_varlen_params* params, fa_stream_t stream);
 size_t fa_varlen_workspace_size(int B, int H, int Hkv, int total_q, int total_k, int d);
 
 /*
+ * fa_bwd_varlen - gradients of fa_fwd_varlen: params holds the forward call's arguments, with o
+ * and lse as it wrote them (lse is required) and a workspace of
+ * fa_bwd_varlen_workspace_size(...) bytes; grads the upstream gradient dout [total_q, H, d] and
+ * the outputs dq [total_q, H, d], dk and dv [total_k, Hkv, d] (sums over the heads of a group).
+ * A key no query sees gets dk = dv = 0, a query that sees no key dq = 0. dq adds the key blocks'
+ * contributions with FP32 atomics, so its last bit can differ between runs; dk and dv are the
+ * same on every run.
+ */
+typedef struct fa_varlen_grads {
+  const void* dout;
+  void* dq;
+  void* dk;
+  void* dv;
+  int64_t dout_token, dq_token, dk_token, dv_token;
+} fa_varlen_grads;
+
+fa_status fa_bwd_varlen(const fa_varlen_params* params, const fa_varlen_grads* grads,
+                        fa_stream_t stream);
+size_t fa_bwd_varlen_workspace_size(int B, int H, int Hkv, int total_q, int total_k, int d);
+
+/*
  * fa_fwd_paged_varlen - attention of packed chunks of new tokens over a paged cache with grouped
  * heads: the tokens cu_seqlens_q[b] .. cu_seqlens_q[b+1]-1 are the last tokens of sequence b,
  * whose ctx_lens[b] keys (the chunk's own included) are in the cache, e.g. by fa_rope_append.

@@ -10,13 +10,14 @@ LSE: scores are FP32 sums of d exact products (error below d 2^-24 sum |q k| sca
 logarithm's and exponentials' approximations stay below 2^-20 absolute each: 1e-4 for the
 inputs here (|scores| < 100, d <= 128).
 
-Gradients. The kernels round P (u), dS (u), o (u, through D = dout . o) and the result (u), and
-the sums behind a result add these errors: |dv| error <= u sum |P dout| + u |dv|, |dk| error <=
-scale (u sum |dS q| + ...): see grad_bounds, which evaluates these sums in 64 bits.
+Gradients. P and dS are rounded to 16 bits, o is rounded (which moves D = dout . o), and so are
+the results. With |dS|_ij = P_ij (|dP_ij| + |D_i|), to first order in u:
+    |dv - ref| <= u (P^T |dout|) + u |dv|
+    |dk - ref| <= scale (u (|dS|^T |q|) + u (E^T |q|)) + u |dk|,  E_ij = P_ij (|dout| . |o|)_i
+    |dq - ref| <= scale (u |dS| |k| + u E |k|) + u |dq|
+where E is what the rounding of o moves dS by. FP32 accumulation and the LSE's own rounding
+(P off by 2^-18 of itself) add about 2^-16 of the same sums. gradients() evaluates them.
 """
-import math
-
-import numpy as np
 import torch
 
 import tiled_attention_06_gb300 as fa
@@ -111,3 +112,39 @@ def rotate(x, pos, freqs, rot, half, amplitude=1.0, inverse=False):
     y[..., ia] = a * c - b * s
     y[..., ib] = b * c + a * s
     return y
+
+
+def gradients(q, k, v, dout, cu_q, cu_k, scale, dtype, mask, window=0, n_global=0):
+    """[(dq, bound), (dk, bound), (dv, bound)] in 64 bits, CPU tensors."""
+    u, slack = half_step(dtype), 2.0 ** -16
+    G = q.shape[1] // k.shape[1]
+    out = [[torch.zeros(x.shape, dtype=torch.float64) for _ in range(2)] for x in (q, k, v)]
+    for b in range(len(cu_q) - 1):
+        rq, rk = slice(cu_q[b], cu_q[b + 1]), slice(cu_k[b], cu_k[b + 1])
+        vis = seen(cu_q[b + 1] - cu_q[b], cu_k[b + 1] - cu_k[b], mask, window, n_global)
+        for h in range(q.shape[1]):
+            hk = h // G
+            qh, kh, vh, do = (x.double() for x in (q[rq, h], k[rk, hk], v[rk, hk], dout[rq, h]))
+            p, o, _ = head(qh, kh, vh, vis, scale)
+            if p.shape[1] == 0:
+                continue
+            dp, dsum = do @ vh.T, (do * o).sum(-1, keepdim=True)
+            ds = p * (dp - dsum)
+            big = p * (dp.abs() + dsum.abs())
+            e = p * (do.abs() * o.abs()).sum(-1, keepdim=True)
+            w = (u + slack) * big + u * e
+            out[0][0][rq, h] = scale * ds @ kh
+            out[0][1][rq, h] = scale * w @ kh.abs()
+            out[1][0][rk, hk] += scale * ds.T @ qh
+            out[1][1][rk, hk] += scale * w.T @ qh.abs()
+            out[2][0][rk, hk] += p.T @ do
+            out[2][1][rk, hk] += (u + slack) * (p.T @ do.abs())
+    return [(ref, bound + u * (ref.abs() + bound) + 2.0 ** -24) for ref, bound in out]
+
+
+def check_gradients(got, ref, rows_q, rows_k, what=""):
+    for name, x, (r, bound), rows in zip(("dq", "dk", "dv"), got, ref, (rows_q, rows_k, rows_k)):
+        x = x[:rows].double().cpu()
+        assert torch.isfinite(x).all(), f"{what} {name}: non-finite"
+        over = (x - r[:rows]).abs() - bound[:rows]
+        assert (over <= 0).all(), f"{what} {name}: {float(over.max()):.3e} over its bound"

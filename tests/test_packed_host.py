@@ -151,6 +151,20 @@ def test_paged_varlen_refusals(L, kw, want):
     assert L.fa_fwd_paged_varlen(ctypes.byref(p), None) == want
 
 
+GRADS = dict(dout=A, dq=A, dk=A, dv=A, dout_token=256, dq_token=256, dk_token=128, dv_token=128)
+
+
+@pytest.mark.parametrize("kw,gkw,want", [(kw, {}, w) for kw, w in SHARED] + [
+    ({}, dict(dout=None), INVALID), ({}, dict(dq=A + 8), INVALID), ({}, dict(dk=None), INVALID),
+    ({}, dict(dv_token=100), INVALID), ({}, dict(dq_token=252), INVALID),
+    (dict(lse=None), {}, INVALID),
+    (dict(total_q=0, total_k=0, q=None, k=None, workspace=None), {}, OK)], ids=str)
+def test_bwd_varlen_refusals(L, kw, gkw, want):
+    p, g = fill(fa.VarlenParams, VARLEN, kw), fill(fa.VarlenGrads, GRADS, gkw)
+    assert L.fa_bwd_varlen(ctypes.byref(p), ctypes.byref(g), None) == want
+    assert L.fa_bwd_varlen(ctypes.byref(p), None, None) == INVALID
+
+
 def test_null_params(L):
     for name in ("fa_rope_append", "fa_fwd_varlen", "fa_fwd_paged_varlen"):
         assert getattr(L, name)(None, None) == INVALID
@@ -168,6 +182,7 @@ def test_struct_layouts_match_header(tmp_path):
     import subprocess
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     structs = {"fa_rope_append_params": fa.RopeAppendParams, "fa_varlen_params": fa.VarlenParams,
+               "fa_varlen_grads": fa.VarlenGrads,
                "fa_paged_varlen_params": fa.PagedVarlenParams}
     lines = ["#include <stdio.h>", "#include <stddef.h>", '#include "fa.h"', "int main(void){"]
     for st, cls in structs.items():

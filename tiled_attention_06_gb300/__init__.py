@@ -19,8 +19,8 @@ __all__ = [
     "fa_get_device_status",
     "fa_selftest_timeout", "fa_last_error_string", "fa_version", "fa_fwd_block_m",
     "fa_fwd_default_block_m", "fa_bwd", "fa_bwd_block_sparse", "fa_bwd_workspace_size", "fa_fwd_workspace_size",
-    "fa_rope_freqs", "fa_rope", "fa_rope_append", "fa_fwd_varlen",
-    "fa_fwd_paged_varlen", "fa_varlen_workspace_size",
+    "fa_rope_freqs", "fa_rope", "fa_rope_append", "fa_fwd_varlen", "fa_bwd_varlen",
+    "fa_fwd_paged_varlen", "fa_varlen_workspace_size", "fa_bwd_varlen_workspace_size",
     "fa_paged_varlen_workspace_size", "FA_ROPE_HALF", "FA_ROPE_PAIRS", "FA_ROPE_PLAIN",
     "FA_ROPE_LINEAR", "FA_ROPE_BASE", "FA_ROPE_BY_PARTS",
     "FA_OK", "FA_ERR_INVALID_ARG", "FA_ERR_UNSUPPORTED", "FA_ERR_CUDA", "FA_ERR_TIMEOUT",
@@ -87,6 +87,11 @@ class VarlenParams(ctypes.Structure):
                 ("d", _i), ("total_q", _i), ("total_k", _i), ("scale", _f), ("mask_mode", _i),
                 ("window", _i), ("n_global", _i), ("dtype", _i), ("workspace", _vp),
                 ("workspace_bytes", _sz), ("timeout_us", _u32)]
+
+
+class VarlenGrads(ctypes.Structure):
+    _fields_ = [("dout", _vp), ("dq", _vp), ("dk", _vp), ("dv", _vp), ("dout_token", _i64),
+                ("dq_token", _i64), ("dk_token", _i64), ("dv_token", _i64)]
 
 
 class PagedVarlenParams(ctypes.Structure):
@@ -164,10 +169,12 @@ def lib():
         L.fa_rope.argtypes = [_vp] * 4 + [_i64, _i, _i, _i] + [_i64] * 4 + [_i, _f, _i, _i, _vp]
         for name, args in (("fa_rope_append", [ctypes.POINTER(RopeAppendParams)]),
                            ("fa_fwd_varlen", [ctypes.POINTER(VarlenParams)]),
+                           ("fa_bwd_varlen", [ctypes.POINTER(VarlenParams),
+                                              ctypes.POINTER(VarlenGrads)]),
                            ("fa_fwd_paged_varlen", [ctypes.POINTER(PagedVarlenParams)])):
             getattr(L, name).restype = _i
             getattr(L, name).argtypes = args + [_vp]
-        for name, n in (("fa_varlen_workspace_size", 6),
+        for name, n in (("fa_varlen_workspace_size", 6), ("fa_bwd_varlen_workspace_size", 6),
                         ("fa_paged_varlen_workspace_size", 8)):
             getattr(L, name).restype = _sz
             getattr(L, name).argtypes = [_i] * n
@@ -576,6 +583,10 @@ def fa_varlen_workspace_size(B, H, Hkv, total_q, total_k, d):
     return lib().fa_varlen_workspace_size(B, H, Hkv, total_q, total_k, d)
 
 
+def fa_bwd_varlen_workspace_size(B, H, Hkv, total_q, total_k, d):
+    return lib().fa_bwd_varlen_workspace_size(B, H, Hkv, total_q, total_k, d)
+
+
 def fa_paged_varlen_workspace_size(B, H, Hkv, total_q, max_q, max_pages_per_seq, page_size, d):
     return lib().fa_paged_varlen_workspace_size(B, H, Hkv, total_q, max_q, max_pages_per_seq,
                                                 page_size, d)
@@ -607,6 +618,26 @@ def fa_fwd_varlen(q, k, v, o, lse, cu_seqlens_q, cu_seqlens_k, scale, workspace,
     p = _varlen(q, k, v, o, lse, cu_seqlens_q, cu_seqlens_k, scale, workspace, mask_mode, window,
                 n_global)
     _check(lib().fa_fwd_varlen(ctypes.byref(p), _stream(stream)))
+
+
+def fa_bwd_varlen(q, k, v, o, dout, lse, dq, dk, dv, cu_seqlens_q, cu_seqlens_k, scale,
+                  workspace, mask_mode=FA_MASK_CAUSAL, window=0, n_global=0, stream=None):
+    """Gradients dq [Tq, H, d], dk, dv [Tk, Hkv, d] of fa_fwd_varlen for the upstream gradient
+    dout; o and lse as the forward call wrote them. workspace: a CUDA byte tensor of
+    fa_bwd_varlen_workspace_size(...)."""
+    if lse is None:
+        _refuse("the backward needs the forward's lse")
+    p = _varlen(q, k, v, o, lse, cu_seqlens_q, cu_seqlens_k, scale, workspace, mask_mode, window,
+                n_global)
+    if dout.shape[0] != p.total_q or dq.shape[0] != p.total_q or dk.shape[0] != p.total_k \
+            or dv.shape[0] != p.total_k:
+        _refuse("dout and dq must have q's tokens, dk and dv k's")
+    g = VarlenGrads(dout.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
+                    _rows("dout", dout, p.H, p.d, q.dtype, q.device),
+                    _rows("dq", dq, p.H, p.d, q.dtype, q.device),
+                    _rows("dk", dk, p.Hkv, p.d, q.dtype, q.device),
+                    _rows("dv", dv, p.Hkv, p.d, q.dtype, q.device))
+    _check(lib().fa_bwd_varlen(ctypes.byref(p), ctypes.byref(g), _stream(stream)))
 
 
 def fa_fwd_paged_varlen(q, k_pages, v_pages, block_table, ctx_lens, cu_seqlens_q, max_q, o, lse,

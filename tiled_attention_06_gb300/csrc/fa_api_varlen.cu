@@ -124,6 +124,34 @@ VarLayout var_layout(int B, int H, int Hkv, int total_q, int d) {
   return L;
 }
 
+// How the backward deals a group's heads and lays its workspace out (fa_varlen.h).
+struct BwdLayout {
+  int HS, GS, TPH, slots, max_units;
+  size_t units, stats, dqacc, part, total;
+};
+BwdLayout bwd_layout(int B, int H, int Hkv, int total_q, int total_k, int d) {
+  BwdLayout L;
+  const int G = H / Hkv;
+  const long long blocks = static_cast<long long>(ceil_div(std::max(total_k, 1), 128)) * Hkv;
+  L.HS = 1;  // the least divisor of G that gives enough items of at most 64 heads
+  while (G % L.HS || G / L.HS > fa::kBwdHalf ||
+         (blocks * L.HS < fa::kBwdMinItems && L.HS < G))
+    ++L.HS;
+  L.GS = G / L.HS;
+  L.TPH = fa::kBwdHalf / L.GS;
+  L.slots = total_q / L.TPH + B + 1;
+  L.max_units = static_cast<int>(
+      std::min<long long>(static_cast<long long>(total_k) / 128 + B, std::max(total_k, 1)));
+  const size_t planes = static_cast<size_t>(Hkv) * L.HS * L.slots;
+  L.units = 64;
+  L.stats = L.units + round16(sizeof(fa::VarBwdUnit) * static_cast<size_t>(L.max_units));
+  L.dqacc = L.stats + planes * 2 * fa::kBwdHalf * sizeof(float);
+  L.part = L.dqacc + planes * fa::kBwdHalf * d * sizeof(float);
+  L.total = L.part + (L.HS > 1 ? static_cast<size_t>(L.HS) * 2 * total_k * Hkv * d * sizeof(float)
+                               : 0);
+  return L;
+}
+
 fa_status check_workspace(const void* ws, size_t bytes, size_t need) {
   if (!ws || !aligned16(ws))
     return fail(FA_ERR_INVALID_ARG, "a 16-byte aligned workspace is needed");
@@ -470,6 +498,94 @@ fa_status fa_fwd_paged_varlen(const fa_paged_varlen_params* params, fa_stream_t 
     return st;
   const cudaError_t e = fa::launch_varlen(L, a.d, bf16, reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "paged packed attention launch");
+  return FA_OK;
+}
+
+size_t fa_bwd_varlen_workspace_size(int B, int H, int Hkv, int total_q, int total_k, int d) {
+  if (B < 1 || Hkv < 1 || H < Hkv || H % Hkv || H / Hkv > 128 || total_q < 0 || total_k < 0 ||
+      d < 1)
+    return 0;
+  return bwd_layout(B, H, Hkv, total_q, total_k, d).total;
+}
+
+fa_status fa_bwd_varlen(const fa_varlen_params* params, const fa_varlen_grads* grads,
+                        fa_stream_t stream) {
+  if (!params || !grads) return fail(FA_ERR_INVALID_ARG, "params or grads is null");
+  const fa_varlen_params& a = *params;
+  const fa_varlen_grads& g = *grads;
+  fa_status st = check_varlen(a);
+  if (st != FA_OK) return st;
+  if (a.total_q > 0) {
+    if (!a.lse) return fail(FA_ERR_INVALID_ARG, "lse must be non-null");
+    if ((st = check_rows("dout", g.dout, g.dout_token, a.H, a.d)) != FA_OK) return st;
+    if ((st = check_rows("dq", g.dq, g.dq_token, a.H, a.d)) != FA_OK) return st;
+  }
+  if (a.total_k > 0) {
+    if ((st = check_rows("dk", g.dk, g.dk_token, a.Hkv, a.d)) != FA_OK) return st;
+    if ((st = check_rows("dv", g.dv, g.dv_token, a.Hkv, a.d)) != FA_OK) return st;
+  }
+  if (a.total_q == 0 && a.total_k == 0) return FA_OK;
+  const BwdLayout B = bwd_layout(a.B, a.H, a.Hkv, a.total_q, a.total_k, a.d);
+  if ((st = check_workspace(a.workspace, a.workspace_bytes, B.total)) != FA_OK) return st;
+  if (static_cast<long long>(B.max_units) * a.Hkv * B.HS > (1LL << 31) - 1 ||
+      static_cast<long long>(a.Hkv) * B.HS > 65535)
+    return fail(FA_ERR_INVALID_ARG, "problem too large");
+  DeviceInfo dev;
+  if ((st = device_info(&dev)) != FA_OK) return st;
+  fa::VarBwdLaunch L;
+  std::memset(&L, 0, sizeof L);
+  fa::VarBwdParams& p = L.p;
+  fill_mask(&p.m, common_of(a), a.timeout_us, dev.status);
+  p.o = a.o;
+  p.dout = g.dout;
+  p.lse = a.lse;
+  p.dq = g.dq;
+  p.dk = g.dk;
+  p.dv = g.dv;
+  p.o_token = a.o_token;
+  p.dout_token = g.dout_token;
+  p.dq_token = g.dq_token;
+  p.dk_token = g.dk_token;
+  p.dv_token = g.dv_token;
+  p.cu_q = a.cu_seqlens_q;
+  p.cu_k = a.cu_seqlens_k;
+  p.scale = a.scale;
+  p.B = a.B;
+  p.H = a.H;
+  p.Hkv = a.Hkv;
+  p.G = a.H / a.Hkv;
+  p.GS = B.GS;
+  p.HS = B.HS;
+  p.TPH = B.TPH;
+  p.total_q = a.total_q;
+  p.total_k = a.total_k;
+  p.slots = B.slots;
+  p.max_units = B.max_units;
+  while (((a.total_q / B.TPH + 1) >> p.cost_shift) >= 1024) ++p.cost_shift;
+  uint8_t* ws = static_cast<uint8_t*>(a.workspace);
+  p.n_units = reinterpret_cast<int32_t*>(ws);
+  p.units = reinterpret_cast<fa::VarBwdUnit*>(ws + B.units);
+  p.stats = reinterpret_cast<float*>(ws + B.stats);
+  p.dqacc = reinterpret_cast<float*>(ws + B.dqacc);
+  p.part = reinterpret_cast<float*>(ws + B.part);
+  const bool bf16 = a.dtype == FA_BF16;
+  // a side without rows is never loaded; its maps only need a valid address
+  const bool nq = a.total_q > 0, nk = a.total_k > 0;
+  const void* q = nq ? a.q : a.k;
+  const void* dout = nq ? g.dout : a.k;
+  const int qh = nq ? a.H : a.Hkv, kh = nk ? a.Hkv : a.H;
+  const int gs = std::min(B.GS, qh);
+  const long long qn = nq ? a.total_q : 1, kn = nk ? a.total_k : 1;
+  const long long qt = nq ? a.q_token : a.k_token, ot = nq ? g.dout_token : a.k_token;
+  const long long kt = nk ? a.k_token : a.q_token, vt = nk ? a.v_token : a.q_token;
+  if ((st = make_map3(&L.tmQ, q, bf16, a.d, qh, a.d, qn, qt, gs, B.TPH)) != FA_OK) return st;
+  if ((st = make_map3(&L.tmdO, dout, bf16, a.d, qh, a.d, qn, ot, gs, B.TPH)) != FA_OK) return st;
+  if ((st = make_map3(&L.tmK, nk ? a.k : a.q, bf16, a.d, kh, a.d, kn, kt, 1, 64)) != FA_OK)
+    return st;
+  if ((st = make_map3(&L.tmV, nk ? a.v : a.q, bf16, a.d, kh, a.d, kn, vt, 1, 64)) != FA_OK)
+    return st;
+  const cudaError_t e = fa::launch_bwd_varlen(L, a.d, bf16, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "packed backward launch");
   return FA_OK;
 }
 

@@ -34,6 +34,7 @@
 #include "fa_plan.h"
 #include "fa_ptx.cuh"
 #include "fa_varlen.h"
+#include "fa_varlen_plan.cuh"
 
 namespace fa {
 namespace {
@@ -131,98 +132,58 @@ __device__ __forceinline__ void mask_row(uint32_t* s, int n0, int pos, int sk,
 
 // ------------------------------------------------------------------ plan
 
-constexpr int kPlanThreads = 1024;
-constexpr int kBins = 1024;
 constexpr int kCandidates = 16;
 
 struct PlanSmem {
-  int off[kPlanThreads + 1];  // token blocks before each sequence of the batch
-  int q0[kPlanThreads], sq[kPlanThreads], k0[kPlanThreads], sk[kPlanThreads];
-  int warp_sum[32];
+  SeqScan scan;
   int bins[kBins + 1];
   int pairs, n_max, slots, groups, split;
   unsigned long long cost;
   int units[kCandidates];
 };
 
-// Calls f(token block of a sequence ...) for every token block of every sequence, sequences
-// in batches of one per thread. Every thread of the CTA takes part.
+// Calls f(unit) for every token block of every sequence (one unit of all its key blocks).
 template <typename F>
 __device__ __forceinline__ void for_each_block(const VarParams& p, PlanSmem& s, bool report,
                                                F f) {
   const int tpi = 2 * p.TPT;
-  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
-  for (int base = 0; base < p.B; base += kPlanThreads) {
-    const int b = base + tid;
-    int nblk = 0;
-    if (b < p.B) {
-      const int a = p.cu_q[b], e = p.cu_q[b + 1];
-      bool bad = a < 0 || e < a || e > p.total_q;
-      int sq = bad ? 0 : e - a, sk, k0 = 0;
-      if (p.block_table) {
-        const int cap = p.page_size * p.max_pages;
-        sk = p.ctx[b];
-        bad = bad || sk < 0 || sk > cap;
-        sk = sk < 0 ? 0 : min(sk, cap);
-      } else {
-        k0 = p.cu_k[b];
-        const int ke = p.cu_k[b + 1];
-        const bool kbad = k0 < 0 || ke < k0 || ke > p.total_k;
-        sk = kbad ? 0 : ke - k0;
-        bad = bad || kbad;
-      }
-      if (bad && report) atomicOr(p.m.status, FA_DEV_BAD_PAGE);
-      s.q0[tid] = a;
-      s.sq[tid] = sq;
-      s.k0[tid] = k0;
-      s.sk[tid] = sk;
-      nblk = (sq + tpi - 1) / tpi;
-    }
-    int x = nblk;  // inclusive scan over the CTA
-    for (int o = 1; o < 32; o *= 2) {
-      const int y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
-    }
-    if (lane == 31) s.warp_sum[warp] = x;
-    __syncthreads();
-    if (warp == 0) {
-      int w = s.warp_sum[lane];
-      for (int o = 1; o < 32; o *= 2) {
-        const int y = __shfl_up_sync(0xffffffffu, w, o);
-        if (lane >= o) w += y;
-      }
-      s.warp_sum[lane] = w;
-    }
-    __syncthreads();
-    s.off[tid + 1] = x + (warp ? s.warp_sum[warp - 1] : 0);
-    if (tid == 0) s.off[0] = 0;
-    __syncthreads();
-    const int nseq = min(kPlanThreads, p.B - base), total = s.off[nseq];
-    for (int i = tid; i < total; i += kPlanThreads) {
-      int lo = 0, hi = nseq;  // last sequence with off <= i
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) / 2;
-        if (s.off[mid] <= i) lo = mid; else hi = mid;
-      }
-      const int first = (i - s.off[lo]) * tpi;
-      VarUnit u;
-      u.q0 = s.q0[lo] + first;
-      u.nq = min(tpi, s.sq[lo] - first);
-      u.sk = s.sk[lo];
-      u.k0 = s.k0[lo];
-      u.qpos = first + s.sk[lo] - s.sq[lo];
-      u.seq = base + lo;
-      u.j0 = 0;
-      u.j1 = range_count(blocks_seen(u.qpos, u.qpos + u.nq, u.sk, p.m));
-      u.slot = -1;
-      f(u);
-    }
-    __syncthreads();
-  }
+  for_each_part(
+      s.scan, p.B,
+      [&](int b) {
+        SeqRows r = rows_of(p.cu_q, b, p.total_q);
+        Seq q{r.first, r.n, 0, 0, 0};
+        bool bad = r.bad;
+        if (p.block_table) {
+          const int cap = p.page_size * p.max_pages, sk = p.ctx[b];
+          bad = bad || sk < 0 || sk > cap;
+          q.sk = sk < 0 ? 0 : min(sk, cap);
+        } else {
+          r = rows_of(p.cu_k, b, p.total_k);
+          bad = bad || r.bad;
+          q.k0 = r.first;
+          q.sk = r.n;
+        }
+        if (bad && report) atomicOr(p.m.status, FA_DEV_BAD_PAGE);
+        q.parts = (q.sq + tpi - 1) / tpi;
+        return q;
+      },
+      [&](int b, const Seq& q, int i) {
+        VarUnit u;
+        u.q0 = q.q0 + i * tpi;
+        u.nq = min(tpi, q.sq - i * tpi);
+        u.sk = q.sk;
+        u.k0 = q.k0;
+        u.qpos = i * tpi + q.sk - q.sq;
+        u.seq = b;
+        u.j0 = 0;
+        u.j1 = range_count(blocks_seen(u.qpos, u.qpos + u.nq, u.sk, p.m));
+        u.slot = -1;
+        f(u);
+      });
 }
 
 __device__ __forceinline__ int bin_of(int n, const VarParams& p) {
-  return kBins - 1 - min(kBins - 1, n >> p.cost_shift);  // most key blocks first
+  return cost_bin(n, p.cost_shift);
 }
 
 // The work list. Splitting: an item of n key blocks takes about n + 4 block times (the 4:
@@ -280,34 +241,10 @@ __global__ void __launch_bounds__(kPlanThreads) var_plan_kernel(const VarParams 
       });
     }
   }
-  // exclusive scan of the bins (one bin per thread)
-  static_assert(kBins == kPlanThreads, "one bin per thread");
-  {
-    const int lane = tid % 32, warp = tid / 32;
-    const int v = s.bins[tid + 1];
-    int x = v;
-    for (int o = 1; o < 32; o *= 2) {
-      const int y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
-    }
-    if (lane == 31) s.warp_sum[warp] = x;
-    __syncthreads();
-    if (warp == 0) {
-      int w = s.warp_sum[lane];
-      for (int o = 1; o < 32; o *= 2) {
-        const int y = __shfl_up_sync(0xffffffffu, w, o);
-        if (lane >= o) w += y;
-      }
-      s.warp_sum[lane] = w;
-    }
-    __syncthreads();
-    const int incl = x + (warp ? s.warp_sum[warp - 1] : 0);
-    s.bins[tid] = incl - v;
-    if (tid == kBins - 1) {  // more only when starts overlap, which no sequence of rows has
-      p.hdr->units = min(incl, p.max_units);
-      if (incl > p.max_units) atomicOr(p.m.status, FA_DEV_BAD_PAGE);
-    }
-    __syncthreads();
+  const int units = scan_bins(s.scan, s.bins);
+  if (tid == 0) {  // more than fit only when starts overlap, which no packed rows have
+    p.hdr->units = min(units, p.max_units);
+    if (units > p.max_units) atomicOr(p.m.status, FA_DEV_BAD_PAGE);
   }
   const int split = s.split;
   for_each_block(p, s, false, [&](VarUnit u) {

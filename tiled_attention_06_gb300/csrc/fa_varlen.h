@@ -102,4 +102,51 @@ struct VarLaunch {
 };
 cudaError_t launch_varlen(const VarLaunch& L, int D, bool bf16, cudaStream_t stream);
 
+// ------------------------------------------------ gradient (fa_varlen_bwd.cu)
+//
+// The query side moves in halves of 64 rows: TPH = 64 / GS consecutive tokens of a sequence with
+// GS heads of one group (row r: token r / GS, head r % GS). A group's G heads are dealt to HS
+// subsets of GS = G / HS when there are too few key blocks for the SMs; each subset then has
+// its own partial dk and dv. A half's slot: sequence b's halves start at cu[b] / TPH + b, which
+// leaves room for every sequence's rounding without a scan.
+constexpr int kBwdHalf = 64;
+constexpr int kBwdMinItems = 304;  // key blocks x K/V heads x HS aimed at: 2 per SM
+
+struct VarBwdUnit {  // one block of 128 keys (48 bytes), written by the plan kernel
+  int32_t k0, nk, j0;     // first row of k, keys in the block, first key's position
+  int32_t q0, sq, delta;  // first row of q, queries, sk - sq
+  int32_t h0, n;          // halves that see a key of the block: h0 .. h0 + n - 1
+  int32_t slot0, pad[3];  // slot of the sequence's first half
+};
+
+struct VarBwdParams {
+  PrefillParams m;  // mask_mode, window, n_global, sl2, status, timeout_ns alone are read
+  const void* o;
+  const void* dout;
+  const float* lse;
+  void* dq;
+  void* dk;
+  void* dv;
+  int64_t o_token, dout_token, dq_token, dk_token, dv_token;
+  const int32_t* cu_q;
+  const int32_t* cu_k;
+  float scale;
+  int B, H, Hkv, G, GS, HS, TPH, total_q, total_k;
+  int slots;      // half slots: total_q / TPH + B + 1
+  int max_units;  // entries of `units`
+  int cost_shift;
+  // workspace
+  int32_t* n_units;   // [16]
+  VarBwdUnit* units;
+  float* stats;       // [Hkv HS][slots][2][64]: -lse log2(e), -D
+  float* dqacc;       // [Hkv HS][slots][16 groups of 4 rows][D][4]
+  float* part;        // HS > 1: [HS][2 (dk, dv)][total_k][Hkv][D]
+};
+
+struct VarBwdLaunch {
+  CUtensorMap tmQ, tmK, tmV, tmdO;
+  VarBwdParams p;
+};
+cudaError_t launch_bwd_varlen(const VarBwdLaunch& L, int D, bool bf16, cudaStream_t stream);
+
 }  // namespace fa
