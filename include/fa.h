@@ -536,9 +536,11 @@ size_t fa_bwd_varlen_workspace_size(int B, int H, int Hkv, int total_q, int tota
  *   q, o [total_q, H, d]; lse [total_q, H] float32 or NULL
  *   pools [num_pages, Hkv, page_size, d]; block_table int32 [B, max_pages_per_seq];
  *   ctx_lens int32 [B]; page_size a multiple of 16 in [16, 4096]
- *   max_q      at least the longest chunk (chunks are cut to it, which is reported as
- *              FA_ERR_BAD_PAGE); up to 64 / (H / Hkv) the call runs kernels for few rows
- *   everything else as for fa_fwd_varlen; workspace fa_paged_varlen_workspace_size(...) bytes.
+ *   max_q      at least the longest chunk; up to 64 / (H / Hkv) tokens the call runs a kernel
+ *              for few rows. Rows of a chunk from max_q on may be left as they were, which is
+ *              reported as FA_ERR_BAD_PAGE
+ *   B at most 65535, everything else as for fa_fwd_varlen; the workspace has
+ *   fa_paged_varlen_workspace_size(...) bytes.
  * Slots behind a sequence's last key may hold anything. A table entry outside [0, num_pages) is
  * read as page 0 and reported as FA_ERR_BAD_PAGE.
  */

@@ -152,6 +152,13 @@ BwdLayout bwd_layout(int B, int H, int Hkv, int total_q, int total_k, int d) {
   return L;
 }
 
+// Rows (a multiple of 16) that the kernel for few rows is built with for chunks of up to max_q
+// tokens, 0 when they are too many for it.
+int few_rows(int max_q, int G) {
+  const long long rows = static_cast<long long>(std::max(max_q, 1)) * G;
+  return rows > fa::kFewRows ? 0 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+}
+
 fa_status check_workspace(const void* ws, size_t bytes, size_t need) {
   if (!ws || !aligned16(ws))
     return fail(FA_ERR_INVALID_ARG, "a 16-byte aligned workspace is needed");
@@ -439,9 +446,11 @@ size_t fa_paged_varlen_workspace_size(int B, int H, int Hkv, int total_q, int ma
                                       int max_pages_per_seq, int page_size, int d) {
   (void)max_pages_per_seq;
   (void)page_size;
-  (void)max_q;
-  if (B < 1 || Hkv < 1 || H < Hkv || H % Hkv || H / Hkv > 128 || total_q < 0 || d < 1) return 0;
-  return var_layout(B, H, Hkv, total_q, d).total;
+  if (B < 1 || Hkv < 1 || H < Hkv || H % Hkv || H / Hkv > 128 || total_q < 0 || max_q < 0 || d < 1)
+    return 0;
+  const int rows = few_rows(max_q, H / Hkv);
+  return rows ? fa::few_part_floats(rows, d) * sizeof(float)
+              : var_layout(B, H, Hkv, total_q, d).total;
 }
 
 fa_status fa_fwd_paged_varlen(const fa_paged_varlen_params* params, fa_stream_t stream) {
@@ -451,8 +460,9 @@ fa_status fa_fwd_paged_varlen(const fa_paged_varlen_params* params, fa_stream_t 
                  a.mask_mode, a.window, a.n_global, a.dtype};
   fa_status st = check_common(c);
   if (st != FA_OK) return st;
-  if (a.max_pages_per_seq < 1 || a.num_pages < 1 || a.max_q < 0)
-    return fail(FA_ERR_INVALID_ARG, "need max_pages_per_seq, num_pages >= 1 and max_q >= 0");
+  if (a.max_pages_per_seq < 1 || a.num_pages < 1 || a.max_q < 0 || a.B > 65535)
+    return fail(FA_ERR_INVALID_ARG,
+                "need max_pages_per_seq, num_pages >= 1, max_q >= 0 and B <= 65535");
   if (a.page_size < 16 || a.page_size > 4096 || a.page_size % 16 != 0)
     return fail(FA_ERR_UNSUPPORTED, "page_size %d (a multiple of 16 in [16, 4096])", a.page_size);
   const long long cap = static_cast<long long>(a.page_size) * a.max_pages_per_seq;
@@ -473,6 +483,47 @@ fa_status fa_fwd_paged_varlen(const fa_paged_varlen_params* params, fa_stream_t 
   if ((st = check_workspace(a.workspace, a.workspace_bytes, need)) != FA_OK) return st;
   DeviceInfo dev;
   if ((st = device_info(&dev)) != FA_OK) return st;
+  const bool bf16 = a.dtype == FA_BF16;
+  const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  // pools as (d, page, num_pages * Hkv); a box is rows of one page, a power of two of them
+  const long long planes = static_cast<long long>(a.num_pages) * a.Hkv;
+  const long long plane = static_cast<long long>(a.page_size) * a.d;
+  const int pow2 = a.page_size & -a.page_size;
+  if (const int rows = few_rows(a.max_q, a.H / a.Hkv)) {
+    fa::FewLaunch F;
+    std::memset(&F, 0, sizeof F);
+    fa::FewParams& p = F.p;
+    fill_mask(&p.m, c, a.timeout_us, dev.status);
+    p.q = a.q;
+    p.o = a.o;
+    p.lse = a.lse;
+    p.q_token = a.q_token;
+    p.o_token = a.o_token;
+    p.cu_q = a.cu_seqlens_q;
+    p.ctx = a.ctx_lens;
+    p.block_table = a.block_table;
+    p.B = a.B;
+    p.H = a.H;
+    p.Hkv = a.Hkv;
+    p.G = a.H / a.Hkv;
+    p.total_q = a.total_q;
+    p.max_q = a.max_q;
+    p.page_size = a.page_size;
+    p.max_pages = a.max_pages_per_seq;
+    p.num_pages = a.num_pages;
+    p.box = std::min(64, pow2);
+    p.part = static_cast<float*>(a.workspace);
+    F.sms = dev.sms;
+    if ((st = make_map3(&F.tmK, a.k_pages, bf16, a.d, a.page_size, a.d, planes, plane, p.box,
+                        1)) != FA_OK)
+      return st;
+    if ((st = make_map3(&F.tmV, a.v_pages, bf16, a.d, a.page_size, a.d, planes, plane, p.box,
+                        1)) != FA_OK)
+      return st;
+    const cudaError_t e = fa::launch_few(F, a.d, bf16, rows, cs);
+    if (e != cudaSuccess) return cuda_fail(e, "paged packed attention launch");
+    return FA_OK;
+  }
   fa::VarLaunch L;
   std::memset(&L, 0, sizeof L);
   fill_var(&L.p, c, a.o, a.lse, a.o_token, a.cu_seqlens_q, a.workspace, cap, a.timeout_us,
@@ -482,21 +533,18 @@ fa_status fa_fwd_paged_varlen(const fa_paged_varlen_params* params, fa_stream_t 
   L.p.page_size = a.page_size;
   L.p.max_pages = a.max_pages_per_seq;
   L.p.num_pages = a.num_pages;
-  L.p.box = std::min(fa::kVarBN, a.page_size & -a.page_size);  // rows of one page, a power of two
+  L.p.box = std::min(fa::kVarBN, pow2);
   L.sms = dev.sms;
-  const bool bf16 = a.dtype == FA_BF16;
   if ((st = make_map3(&L.tmQ, a.q, bf16, a.d, a.H, a.d, a.total_q, a.q_token, L.p.G, L.p.TPT)) !=
       FA_OK)
     return st;
-  const long long planes = static_cast<long long>(a.num_pages) * a.Hkv;
-  const long long plane = static_cast<long long>(a.page_size) * a.d;
   if ((st = make_map3(&L.tmK, a.k_pages, bf16, a.d, a.page_size, a.d, planes, plane, L.p.box,
                       1)) != FA_OK)
     return st;
   if ((st = make_map3(&L.tmV, a.v_pages, bf16, a.d, a.page_size, a.d, planes, plane, L.p.box,
                       1)) != FA_OK)
     return st;
-  const cudaError_t e = fa::launch_varlen(L, a.d, bf16, reinterpret_cast<cudaStream_t>(stream));
+  const cudaError_t e = fa::launch_varlen(L, a.d, bf16, cs);
   if (e != cudaSuccess) return cuda_fail(e, "paged packed attention launch");
   return FA_OK;
 }

@@ -1,0 +1,656 @@
+// Attention of a few new rows over a paged cache with grouped heads, for sm_103a: a decode
+// step, or a handful of drafted tokens. The rows of a sequence and K/V head are its tokens times
+// the G query heads that share the head (row r: token r / G, head r % G); at most 64.
+//
+// Bound by reading K and V once: 4 d bytes per key and K/V head against 4 d G multiply-adds per
+// token, which the FP32 pipes cannot keep up with from G = 4 or so, hence warp-level tensor-core
+// MMAs (m16n8k16: 16 rows are its natural tile; a tcgen05 tile would be 128 rows, 4 to 32 times
+// more than there are, and its softmax would serialise on one warp).
+//
+// few_kernel, two CTAs per SM, each four compute warps and a TMA warp. The 64-key tiles of all
+// (sequence, K/V head) pairs are numbered end to end and CTA x takes an equal run of them, so
+// ragged lengths cost no balance. A run's piece of one pair is a segment: a whole pair is
+// written to o, a piece to the workspace. The four warps are MT row groups of 16 rows times
+// 4 / MT key groups of the tile; each keeps its own running maximum, sum and output in
+// registers, joined through shared memory at the end of a segment.
+// few_merge_kernel joins the pieces, one CTA per sequence, K/V head and row, in the order of
+// the keys; it is launched with programmatic dependence, so its own set-up overlaps.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <climits>
+#include <cstdint>
+
+#include "fa_plan.h"
+#include "fa_ptx.cuh"
+#include "fa_varlen.h"
+
+namespace fa {
+namespace {
+
+constexpr int BK = 64;              // keys per tile
+constexpr int kCompute = 128;       // compute threads
+constexpr int kThreads = kCompute + 32;
+constexpr float kTau = 8.0f;        // lazy-rescale threshold, log2 units
+
+template <int D>
+struct Cfg {
+  static constexpr int KCH = D / 64;
+  static constexpr int TILE = BK * D * 2;    // K or V of one tile
+  static constexpr int COMB = 2 * 16 * D * 4;  // two warps' outputs
+  static constexpr int STATES = 4 * 16 * 2 * 4;  // (m, l) of four warps
+  static constexpr int BARS = 256;
+  // two CTAs share an SM's 228 KB, 1 KB of it taken per CTA
+  static constexpr int BUDGET = 233472 / 2 - 1024;
+  static constexpr int FIT = (BUDGET - COMB - STATES - BARS) / (2 * TILE);
+  static constexpr int NST = FIT > 8 ? 8 : FIT;
+  static constexpr int SMEM = NST * 2 * TILE + COMB + STATES + BARS;
+  static_assert(NST >= 3, "too few stages");
+};
+
+struct Bars {
+  uint64_t full[8], empty[8];
+  int64_t sum[4];   // scratch of tile_totals
+  int first[2];     // sequence of the CTA's first tile, tile within it (all K/V heads)
+  uint32_t abort;
+};
+static_assert(sizeof(Bars) <= 256, "barrier block over its reserve");
+
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t* r) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t* r) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+// c (16 x 8, FP32) += a (16 x 16) b (16 x 8)
+template <bool BF16>
+__device__ __forceinline__ void mma(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  if constexpr (BF16)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void compute_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+
+// One sequence: its rows, keys and the tiles that the mask lets its queries see.
+struct FewSeq {
+  int q0, n, sk, qpos, tiles;
+  Range rg;
+};
+__device__ __forceinline__ FewSeq few_seq(const FewParams& p, int b, bool report) {
+  FewSeq s;
+  const int a = p.cu_q[b], e = p.cu_q[b + 1], cap = p.page_size * p.max_pages;
+  int sk = p.ctx[b];
+  bool bad = a < 0 || e < a || e > p.total_q;
+  s.q0 = bad ? 0 : a;
+  const int n = bad ? 0 : e - a;
+  bad = bad || sk < 0 || sk > cap || n > p.max_q;
+  sk = sk < 0 ? 0 : min(sk, cap);
+  if (bad && report) atomicOr(p.m.status, FA_DEV_BAD_PAGE);
+  s.n = min(n, p.max_q);
+  s.sk = sk;
+  s.qpos = sk - n;
+  PrefillParams f;  // ranges by key position: as many queries as keys
+  f.mask_mode = p.m.mask_mode;
+  f.window = p.m.window;
+  f.n_global = p.m.n_global;
+  f.Sq = sk;
+  s.rg = key_range(s.qpos, s.qpos + s.n, BK, sk, f, 0);
+  s.tiles = range_count(s.rg);
+  return s;
+}
+__device__ __forceinline__ int tile_at(const Range& r, int j) {
+  return j < r.a_end ? j : r.b_start + (j - r.a_end);
+}
+
+// Sums over the CTA's first 128 threads of each thread's contiguous share of the sequences.
+struct Totals {
+  int64_t before, mine, all;  // tiles before this thread's share, in it, of every sequence
+  int b0, b1;                 // the share
+};
+__device__ __forceinline__ Totals tile_totals(const FewParams& p, int64_t* scratch) {
+  Totals t{0, 0, 0, 0, 0};
+  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+  int64_t x = 0;
+  if (tid < kCompute) {
+    const int per = (p.B + kCompute - 1) / kCompute;
+    t.b0 = min(p.B, tid * per);
+    t.b1 = min(p.B, t.b0 + per);
+    for (int b = t.b0; b < t.b1; ++b) x += few_seq(p, b, blockIdx.x == 0).tiles;
+    t.mine = x;
+    for (int o = 1; o < 32; o *= 2) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) scratch[warp] = x;
+  }
+  __syncthreads();
+  for (int w = 0; w < kCompute / 32; ++w) {
+    if (w < warp) t.before += scratch[w];
+    t.all += scratch[w];
+  }
+  t.before += x - t.mine;
+  return t;
+}
+
+// CTAs that share the tiles: two at least for each (a tile is about 1.3 us of one CTA's share
+// of the bandwidth, a merge of many short pieces costs more than it spreads).
+__device__ __forceinline__ int ctas_used(int64_t tiles, int grid) {
+  const int64_t want = (tiles + 1) / 2;
+  return static_cast<int>(want < grid ? (want < 1 ? 1 : want) : grid);
+}
+
+// A walk over the tiles [t, end) of this CTA: one segment after the other.
+struct Walk {
+  int b, kvh, j;
+  int64_t left;
+  FewSeq s;
+};
+
+template <int D, bool BF16, int MT>
+__global__ void __launch_bounds__(kThreads, 2)
+    few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+               const __grid_constant__ FewParams p) {
+  using C = Cfg<D>;
+  constexpr int KW = 4 / MT;      // key groups
+  constexpr int KPW = BK / KW;    // keys of a warp per tile
+  constexpr int NT = KPW / 8;     // 8-key columns of S
+  constexpr int NO = D / 8;       // 8-element columns of O
+  constexpr int ROWS = 16 * MT;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t base = smem_u32(smem);
+  float* comb = reinterpret_cast<float*>(smem + C::NST * 2 * C::TILE);
+  float* states = reinterpret_cast<float*>(smem + C::NST * 2 * C::TILE + C::COMB);
+  Bars* bars =
+      reinterpret_cast<Bars*>(smem + C::NST * 2 * C::TILE + C::COMB + C::STATES);
+  auto B = [&](uint64_t& x) { return smem_u32(&x); };
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  if (base & 1023u) {  // the swizzle needs the stages on 1024-byte boundaries
+    if (threadIdx.x == 0) atomicOr(p.m.status, FA_DEV_SMEM_BASE);
+    return;
+  }
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::NST; ++i) {
+      mbar_init(B(bars->full[i]), 1);
+      mbar_init(B(bars->empty[i]), 4);
+    }
+    bars->abort = 0;
+    mbar_fence_init();
+  }
+  if (warp == 4 && lane == 0) {
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+  }
+  const Totals tot = tile_totals(p, bars->sum);
+  const int64_t all = tot.all * p.Hkv;
+  const int used = ctas_used(all, gridDim.x);
+  const bool idle = static_cast<int>(blockIdx.x) >= used || all == 0;
+  const int64_t begin = idle ? 0 : all * blockIdx.x / used;
+  const int64_t end = idle ? 0 : all * (blockIdx.x + 1) / used;
+  // the thread whose share holds the first tile finds its sequence
+  if (!idle && threadIdx.x < kCompute && begin >= tot.before * p.Hkv &&
+      begin < (tot.before + tot.mine) * p.Hkv) {
+    int64_t at = tot.before * p.Hkv;
+    for (int b = tot.b0; b < tot.b1; ++b) {
+      const int64_t n = static_cast<int64_t>(few_seq(p, b, false).tiles) * p.Hkv;
+      if (begin < at + n) {
+        bars->first[0] = b;
+        bars->first[1] = static_cast<int>(begin - at);
+        break;
+      }
+      at += n;
+    }
+  }
+  __syncthreads();
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (begin >= end) return;  // uniform: no barrier is used from here
+  Walk w;
+  w.b = bars->first[0];
+  w.s = few_seq(p, w.b, false);
+  w.kvh = bars->first[1] / w.s.tiles;
+  w.j = bars->first[1] - w.kvh * w.s.tiles;
+  w.left = end - begin;
+  // step to the segment after one of `done` tiles
+  auto advance = [&](int done) {
+    w.left -= done;
+    w.j = 0;
+    if (++w.kvh < p.Hkv || w.left <= 0) return;
+    w.kvh = 0;
+    do {
+      w.s = few_seq(p, ++w.b, false);
+    } while (w.s.tiles == 0);  // ends: `left` tiles lie ahead
+  };
+  const WaitCtx wc{&bars->abort, p.m.status, p.m.timeout_ns};
+
+  if (warp == 4) {
+    // -------------------------------------------------------------- TMA
+    // lane = (K or V, 64-element region of d, box of the tile)
+    const bool leader = elect_one();
+    const int per_tile = BK / p.box;
+    const int kv = lane / (C::KCH * per_tile), c = (lane / per_tile) % C::KCH, bx = lane % per_tile;
+    uint32_t pos = 0, fills[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    bool ok = true;
+    while (w.left > 0 && ok) {
+      const int cnt = static_cast<int>(min(w.left, static_cast<int64_t>(w.s.tiles - w.j)));
+      for (int j = w.j; j < w.j + cnt && ok; ++j, ++pos) {
+        const int n0 = tile_at(w.s.rg, j) * BK;
+        const int boxes = (min(BK, w.s.sk - n0) + p.box - 1) / p.box;
+        int y = 0, z = 0;
+        if (kv < 2 && bx < boxes) {
+          const int row = n0 + bx * p.box, lp = row / p.page_size;
+          int phys = p.block_table[static_cast<size_t>(w.b) * p.max_pages + lp];
+          if (phys < 0 || phys >= p.num_pages) {
+            atomicOr(p.m.status, FA_DEV_BAD_PAGE);
+            phys = 0;
+          }
+          y = row - lp * p.page_size;
+          z = phys * p.Hkv + w.kvh;
+        }
+        const int st = pos % C::NST;
+        const uint32_t use = pos / C::NST;
+        if (!(ok = mbar_wait(B(bars->empty[st]), (use & 1) ^ 1, wc))) break;
+        if (leader) mbar_arrive_expect_tx(B(bars->full[st]), boxes * p.box * C::KCH * 256);
+        __syncwarp();
+        if (kv < 2 && bx < boxes)
+          tma_load_3d(base + (2 * st + kv) * C::TILE + c * (BK * 128) + bx * p.box * 128,
+                      kv ? (const void*)&tmV : (const void*)&tmK, B(bars->full[st]), c * 64, y, z);
+        __syncwarp();
+        fills[st] = use + 1;
+      }
+      advance(cnt);
+    }
+    if (!ok) {  // every load issued lands before the CTA exits
+      volatile uint32_t zero = 0;
+      WaitCtx quiet = wc;
+      quiet.abort = &zero;
+      for (int i = 0; i < C::NST; ++i)
+        if (fills[i] > 0) mbar_wait(B(bars->full[i]), (fills[i] - 1) & 1, quiet);
+    }
+    return;
+  }
+  // ---------------------------------------------------------------- compute
+  const int rw = warp % MT, kw = warp / MT;  // row group, key group
+  const int r0 = rw * 16 + lane / 4;         // this thread's rows: r0 and r0 + 8
+  const int cq = lane % 4;
+  uint32_t pos = 0;
+  while (w.left > 0) {
+    const int cnt = static_cast<int>(min(w.left, static_cast<int64_t>(w.s.tiles - w.j)));
+    const int rows = w.s.n * p.G;
+    // Q fragments straight from global memory (rows past the chunk are zero)
+    uint32_t qf[D / 16][4];
+    int tok[2], head[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = r0 + 8 * i;
+      tok[i] = r / p.G;
+      head[i] = w.kvh * p.G + r - tok[i] * p.G;
+      const uint16_t* src = static_cast<const uint16_t*>(p.q) +
+                            static_cast<int64_t>(w.s.q0 + tok[i]) * p.q_token + head[i] * D + 2 * cq;
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        qf[kk][i] = r < rows ? *reinterpret_cast<const uint32_t*>(src + 16 * kk) : 0u;
+        qf[kk][2 + i] = r < rows ? *reinterpret_cast<const uint32_t*>(src + 16 * kk + 8) : 0u;
+      }
+    }
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, o[NO][4];
+#pragma unroll
+    for (int i = 0; i < NO; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
+    for (int j = w.j; j < w.j + cnt; ++j, ++pos) {
+      const int n0 = tile_at(w.s.rg, j) * BK;
+      const int st = pos % C::NST;
+      if (!mbar_wait(B(bars->full[st]), (pos / C::NST) & 1, wc)) return;
+      const uint32_t sK = base + 2 * st * C::TILE, sV = sK + C::TILE;
+      const int live = w.s.sk - n0;
+      float s[NT][4];
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[t][e] = 0.f;
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+#pragma unroll
+        for (int t = 0; t < NT; t += 2) {
+          const int key = kw * KPW + 8 * t + (lane / 16) * 8 + lane % 8;
+          const int ch = 2 * kk + (lane / 8) % 2;
+          uint32_t kf[4];
+          ldsm4(sK + (ch / 8) * (BK * 128) + key * 128 + (((ch % 8) ^ (key & 7)) << 4), kf);
+          mma<BF16>(s[t], qf[kk], kf[0], kf[1]);
+          mma<BF16>(s[t + 1], qf[kk], kf[2], kf[3]);
+        }
+      }
+      // hidden keys to -inf where some row does not see the whole tile
+      const int lo_pos = w.s.qpos, hi_pos = w.s.qpos + w.s.n - 1;
+      bool full = n0 + BK <= w.s.sk;
+      if (p.m.mask_mode != FA_MASK_NONE) {
+        if (p.m.mask_mode == FA_MASK_CAUSAL || p.m.mask_mode == FA_MASK_CAUSAL_WINDOW)
+          full = full && n0 + BK - 1 <= lo_pos;
+        if (p.m.mask_mode == FA_MASK_CAUSAL_WINDOW)
+          full = full && (n0 + BK <= p.m.n_global || hi_pos - max(n0, p.m.n_global) < p.m.window);
+        if (p.m.mask_mode == FA_MASK_BAND)
+          full = full && static_cast<long long>(hi_pos) - n0 <= p.m.window &&
+                 static_cast<long long>(n0 + BK - 1) - lo_pos <= p.m.window;
+        if (p.m.mask_mode == FA_MASK_PREFIX_LM)
+          full = full && (n0 + BK <= p.m.n_global || n0 + BK - 1 <= lo_pos);
+      }
+      if (!full) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const long long at = static_cast<long long>(w.s.qpos) + tok[i];
+          long long lim = min(at, static_cast<long long>(w.s.sk - 1)), lo = LLONG_MIN;
+          int gl = INT_MIN;
+          if (p.m.mask_mode == FA_MASK_NONE) lim = w.s.sk - 1;
+          if (p.m.mask_mode == FA_MASK_CAUSAL_WINDOW) {
+            lo = at - p.m.window + 1;
+            gl = p.m.n_global;
+          }
+          if (p.m.mask_mode == FA_MASK_BAND) {
+            lim = min(at + p.m.window, static_cast<long long>(w.s.sk - 1));
+            lo = at - p.m.window;
+          }
+          if (p.m.mask_mode == FA_MASK_PREFIX_LM)
+            lim = min(max(at, static_cast<long long>(p.m.n_global) - 1),
+                      static_cast<long long>(w.s.sk - 1));
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int key = n0 + kw * KPW + 8 * t + 2 * cq + e;
+              if (!(key <= lim && (key >= lo || key < gl))) s[t][2 * i + e] = -INFINITY;
+            }
+        }
+      }
+      // running maximum (a row is shared by four lanes), lazy rescale, P
+      bool need = false;
+      float mn[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float mx = -INFINITY;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) mx = max3f(mx, s[t][2 * i], s[t][2 * i + 1]);
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        mn[i] = fmaxf(m[i], mx * p.m.sl2);
+        need = need || (m[i] != -INFINITY && mn[i] > m[i] + kTau);
+        if (m[i] == -INFINITY) m[i] = mn[i];
+      }
+      if (__any_sync(0xffffffffu, need)) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const bool move = mn[i] > m[i] + kTau;
+          const float a = move ? ex2_approx(m[i] - mn[i]) : 1.f;
+          if (move) m[i] = mn[i];
+          l[i] *= a;
+#pragma unroll
+          for (int t = 0; t < NO; ++t) {
+            o[t][2 * i] *= a;
+            o[t][2 * i + 1] *= a;
+          }
+        }
+      }
+      uint32_t pf[NT][2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float mu = m[i] == -INFINITY ? 0.f : m[i];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          const float a = ex2_approx(fmaf(s[t][2 * i], p.m.sl2, -mu));
+          const float b = ex2_approx(fmaf(s[t][2 * i + 1], p.m.sl2, -mu));
+          l[i] += a + b;
+          pf[t][i] = BF16 ? cvt_pack_bf16(a, b) : cvt_pack_f16(a, b);
+        }
+      }
+      if (live < BK) {  // rows of V behind the last key: 0 times what they hold may not be 0
+        for (int i = lane; i < KPW * 8 * C::KCH; i += 32) {
+          const int key = kw * KPW + (i / 8) % KPW;
+          if (key >= live)
+            st_shared_v4(sV + (i / (8 * KPW)) * (BK * 128) + key * 128 + (i % 8) * 16, 0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();  // before the slot's next load
+        __syncwarp();
+      }
+#pragma unroll
+      for (int kk = 0; kk < NT / 2; ++kk) {  // 16 keys
+        const uint32_t pa[4] = {pf[2 * kk][0], pf[2 * kk][1], pf[2 * kk + 1][0], pf[2 * kk + 1][1]};
+        const int key = kw * KPW + 16 * kk + ((lane / 8) % 2) * 8 + lane % 8;
+#pragma unroll
+        for (int t = 0; t < NO; t += 2) {
+          const int ch = t + lane / 16;
+          uint32_t vf[4];
+          ldsm4_t(sV + (ch / 8) * (BK * 128) + key * 128 + (((ch % 8) ^ (key & 7)) << 4), vf);
+          mma<BF16>(o[t], pa, vf[0], vf[1]);
+          mma<BF16>(o[t + 1], pa, vf[2], vf[3]);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(B(bars->empty[st]));
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+    }
+    // join the key groups: the upper half hands its state to the lower, until one is left
+#pragma unroll
+    for (int half = KW / 2; half >= 1; half /= 2) {
+      if (kw >= half && kw < 2 * half) {
+        float* dst = comb + ((kw - half) * MT + rw) * 16 * D;
+        float* sd = states + ((kw - half) * MT + rw) * 32;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int r = lane / 4 + 8 * i;
+#pragma unroll
+          for (int t = 0; t < NO; ++t)
+            *reinterpret_cast<float2*>(dst + r * D + 8 * t + 2 * cq) =
+                make_float2(o[t][2 * i], o[t][2 * i + 1]);
+          if (cq == 0) {
+            sd[r] = m[i];
+            sd[16 + r] = l[i];
+          }
+        }
+      }
+      compute_sync();
+      if (kw < half) {
+        const float* src = comb + (kw * MT + rw) * 16 * D;
+        const float* sd = states + (kw * MT + rw) * 32;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int r = lane / 4 + 8 * i;
+          const float m2 = sd[r], l2 = sd[16 + r];
+          const float M = fmaxf(m[i], m2), mu = M == -INFINITY ? 0.f : M;
+          const float a = ex2_approx(m[i] - mu), b = ex2_approx(m2 - mu);
+          l[i] = l[i] * a + l2 * b;
+          m[i] = M;
+#pragma unroll
+          for (int t = 0; t < NO; ++t) {
+            const float2 v = *reinterpret_cast<const float2*>(src + r * D + 8 * t + 2 * cq);
+            o[t][2 * i] = o[t][2 * i] * a + v.x * b;
+            o[t][2 * i + 1] = o[t][2 * i + 1] * a + v.y * b;
+          }
+        }
+      }
+      compute_sync();
+    }
+    if (kw == 0) {
+      const bool whole = w.j == 0 && cnt == w.s.tiles;
+      // a piece that starts its pair goes to slot 2x + 1, one that continues it to slot 2x
+      const int slot = 2 * blockIdx.x + (w.j == 0 ? 1 : 0);
+      const int nslots = 2 * gridDim.x;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int r = r0 + 8 * i;
+        if (r >= rows) continue;
+        if (whole) {
+          const float inv = l[i] > 0.f ? 1.f / l[i] : 0.f;
+          uint16_t* dst = static_cast<uint16_t*>(p.o) +
+                          static_cast<int64_t>(w.s.q0 + tok[i]) * p.o_token + head[i] * D + 2 * cq;
+#pragma unroll
+          for (int t = 0; t < NO; ++t) {
+            const float a = o[t][2 * i] * inv, b = o[t][2 * i + 1] * inv;
+            *reinterpret_cast<uint32_t*>(dst + 8 * t) = BF16 ? cvt_pack_bf16(a, b) : cvt_pack_f16(a, b);
+          }
+          if (cq == 0 && p.lse)
+            p.lse[static_cast<size_t>(w.s.q0 + tok[i]) * p.H + head[i]] =
+                l[i] > 0.f ? (m[i] + lg2_approx(l[i])) * 0.69314718055994531f : -INFINITY;
+        } else {
+          float* dst = p.part + (static_cast<size_t>(slot) * ROWS + r) * D + 2 * cq;
+#pragma unroll
+          for (int t = 0; t < NO; ++t)
+            *reinterpret_cast<float2*>(dst + 8 * t) = make_float2(o[t][2 * i], o[t][2 * i + 1]);
+          if (cq == 0) {
+            float* ml = p.part + static_cast<size_t>(nslots) * ROWS * D;
+            ml[slot * ROWS + r] = m[i];
+            ml[(nslots + slot) * ROWS + r] = l[i];
+          }
+        }
+      }
+    }
+    advance(cnt);
+  }
+}
+
+// One CTA per (K/V head, sequence): the pieces of the pair in key order, four warps taking
+// every fourth piece of a row. A pair that one CTA held whole is already written.
+template <int D, bool BF16, int MT>
+__global__ void __launch_bounds__(kCompute) few_merge_kernel(const FewParams p, int grid) {
+  constexpr int E = D / 32, ROWS = 16 * MT;
+  __shared__ int64_t s_sum[4];
+  __shared__ int64_t s_at;
+  __shared__ float s_ml[4][2], s_acc[4][D];
+  const int kvh = blockIdx.x, b = blockIdx.y;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const Totals tot = tile_totals(p, s_sum);
+  if (b >= tot.b0 && b < tot.b1) {
+    int64_t at = tot.before;
+    for (int i = tot.b0; i < b; ++i) at += few_seq(p, i, false).tiles;
+    s_at = at;
+  }
+  __syncthreads();
+  const FewSeq s = few_seq(p, b, false);
+  const int rows = s.n * p.G;
+  // the pieces are there once the kernel before has ended; every CTA waits, so that what follows
+  // this launch in its stream follows that kernel too
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (rows == 0) return;
+  const int64_t all = tot.all * p.Hkv;
+  const int64_t t0 = s_at * p.Hkv + static_cast<int64_t>(kvh) * s.tiles, t1 = t0 + s.tiles;
+  const int used = ctas_used(all, grid);
+  // CTA x holds the tiles [all x / used, all (x + 1) / used)
+  auto cta_of = [&](int64_t t) {
+    int x = static_cast<int>(t * used / all);
+    while (all * (x + 1) / used <= t) ++x;
+    while (all * x / used > t) --x;
+    return x;
+  };
+  const int x0 = s.tiles ? cta_of(t0) : 0, x1 = s.tiles ? cta_of(t1 - 1) : -1;
+  if (x0 == x1) return;
+  const int nslots = 2 * grid;
+  const float* ml = p.part + static_cast<size_t>(nslots) * ROWS * D;
+  for (int r = blockIdx.z; r < rows; r += gridDim.z) {
+    float M = -INFINITY, L = 0.f, acc[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+#pragma unroll 4
+    for (int x = x0 + warp; x <= x1; x += 4) {
+      const int slot = 2 * x + (x == x0 ? 1 : 0);
+      const float m = ml[slot * ROWS + r], l = ml[(nslots + slot) * ROWS + r];
+      const float* src = p.part + (static_cast<size_t>(slot) * ROWS + r) * D + lane * E;
+      float v[E];
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[e] = src[e];
+      const float mn = fmaxf(M, m), mu = mn == -INFINITY ? 0.f : mn;
+      const float c = ex2_approx(M - mu), wt = ex2_approx(m - mu);
+      L = L * c + l * wt;
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] = acc[e] * c + v[e] * wt;
+      M = mn;
+    }
+    if (lane == 0) {
+      s_ml[warp][0] = M;
+      s_ml[warp][1] = L;
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) s_acc[warp][lane * E + e] = acc[e];
+    __syncthreads();
+    float Ma = -INFINITY;
+    for (int i = 0; i < 4; ++i) Ma = fmaxf(Ma, s_ml[i][0]);
+    const float mu = Ma == -INFINITY ? 0.f : Ma;
+    float La = 0.f, wts[4];
+    for (int i = 0; i < 4; ++i) {
+      wts[i] = ex2_approx(s_ml[i][0] - mu);
+      La += s_ml[i][1] * wts[i];
+    }
+    const int tok = r / p.G, h = kvh * p.G + r - tok * p.G;
+    const float inv = La > 0.f ? 1.f / La : 0.f;
+    uint16_t* out = static_cast<uint16_t*>(p.o) + static_cast<int64_t>(s.q0 + tok) * p.o_token + h * D;
+    for (int e = 2 * threadIdx.x; e < D; e += 2 * kCompute) {
+      float a = 0.f, c = 0.f;
+      for (int i = 0; i < 4; ++i) {
+        a += s_acc[i][e] * wts[i];
+        c += s_acc[i][e + 1] * wts[i];
+      }
+      *reinterpret_cast<uint32_t*>(out + e) =
+          BF16 ? cvt_pack_bf16(a * inv, c * inv) : cvt_pack_f16(a * inv, c * inv);
+    }
+    if (threadIdx.x == 0 && p.lse)
+      p.lse[static_cast<size_t>(s.q0 + tok) * p.H + h] =
+          La > 0.f ? (Ma + lg2_approx(La)) * 0.69314718055994531f : -INFINITY;
+    __syncthreads();
+  }
+}
+
+template <int D, bool BF16, int MT>
+cudaError_t launch_mt(const FewLaunch& L, cudaStream_t stream) {
+  const int grid = 2 * L.sms < kFewMaxCtas ? 2 * L.sms : kFewMaxCtas;
+  auto* k = few_kernel<D, BF16, MT>;
+  constexpr int smem = Cfg<D>::SMEM;
+  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  k<<<grid, kThreads, smem, stream>>>(L.tmK, L.tmV, L.p);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  const int rows = L.p.max_q * L.p.G;
+  cudaLaunchConfig_t cfg = {};
+  // few pairs: a CTA per row as well, else the rows of a pair one after the other
+  const int64_t pairs = static_cast<int64_t>(L.p.B) * L.p.Hkv;
+  const int z = static_cast<int>(pairs * rows <= 8LL * L.sms ? rows : (rows + 3) / 4);
+  cfg.gridDim = dim3(L.p.Hkv, L.p.B, z < 1 ? 1 : z);
+  cfg.blockDim = dim3(kCompute);
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, few_merge_kernel<D, BF16, MT>, L.p, grid);
+}
+
+template <int D, bool BF16>
+cudaError_t launch_t(const FewLaunch& L, int rows, cudaStream_t stream) {
+  if (rows <= 16) return launch_mt<D, BF16, 1>(L, stream);
+  if (rows <= 32) return launch_mt<D, BF16, 2>(L, stream);
+  return launch_mt<D, BF16, 4>(L, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_few(const FewLaunch& L, int D, bool bf16, int rows, cudaStream_t stream) {
+  if (D == 128) return bf16 ? launch_t<128, true>(L, rows, stream) : launch_t<128, false>(L, rows, stream);
+  return bf16 ? launch_t<64, true>(L, rows, stream) : launch_t<64, false>(L, rows, stream);
+}
+
+}  // namespace fa

@@ -149,4 +149,36 @@ struct VarBwdLaunch {
 };
 cudaError_t launch_bwd_varlen(const VarBwdLaunch& L, int D, bool bf16, cudaStream_t stream);
 
+// ------------------------------------------------ few rows over a paged cache (fa_few.cu)
+//
+// Chunks whose rows (tokens x heads of a group) are at most 64, a decode step above all: bound
+// by reading the cache, so the key tiles of all sequences and K/V heads are laid end to end and
+// dealt to the CTAs in equal runs, whatever the lengths.
+constexpr int kFewRows = 64;
+constexpr int kFewMaxCtas = 320;
+inline size_t few_part_floats(int rows, int d) {  // a CTA leaves at most two partial results
+  return static_cast<size_t>(2) * kFewMaxCtas * rows * (d + 2);
+}
+
+struct FewParams {
+  PrefillParams m;  // mask_mode, window, n_global, sl2, status, timeout_ns alone are read
+  const void* q;
+  void* o;
+  float* lse;
+  int64_t q_token, o_token;
+  const int32_t* cu_q;
+  const int32_t* ctx;
+  const int32_t* block_table;
+  int B, H, Hkv, G, total_q, max_q;
+  int page_size, max_pages, num_pages, box;  // box: rows of one TMA box (<= 64)
+  float* part;  // [2 CTAs][rows][D], then m [2 CTAs][rows], l [2 CTAs][rows]
+};
+
+struct FewLaunch {
+  CUtensorMap tmK, tmV;
+  FewParams p;
+  int sms;
+};
+cudaError_t launch_few(const FewLaunch& L, int D, bool bf16, int rows, cudaStream_t stream);
+
 }  // namespace fa
