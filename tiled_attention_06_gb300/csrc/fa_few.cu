@@ -14,7 +14,7 @@
 // 4 / MT key groups of the tile; each keeps its own running maximum, sum and output in
 // registers, joined through shared memory at the end of a segment.
 // few_merge_kernel joins the pieces, one CTA per sequence, K/V head and row, in the order of
-// the keys; it is launched with programmatic dependence, so its own set-up overlaps.
+// the keys.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -216,7 +216,6 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
   }
   __syncthreads();
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (begin >= end) return;  // uniform: no barrier is used from here
   Walk w;
   w.b = bars->first[0];
@@ -543,9 +542,6 @@ __global__ void __launch_bounds__(kCompute) few_merge_kernel(const FewParams p, 
   __syncthreads();
   const FewSeq s = few_seq(p, b, false);
   const int rows = s.n * p.G;
-  // the pieces are there once the kernel before has ended; every CTA waits, so that what follows
-  // this launch in its stream follows that kernel too
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (rows == 0) return;
   const int64_t all = tot.all * p.Hkv;
   const int64_t t0 = s_at * p.Hkv + static_cast<int64_t>(kvh) * s.tiles, t1 = t0 + s.tiles;
@@ -624,19 +620,12 @@ cudaError_t launch_mt(const FewLaunch& L, cudaStream_t stream) {
   k<<<grid, kThreads, smem, stream>>>(L.tmK, L.tmV, L.p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   const int rows = L.p.max_q * L.p.G;
-  cudaLaunchConfig_t cfg = {};
   // few pairs: a CTA per row as well, else the rows of a pair one after the other
   const int64_t pairs = static_cast<int64_t>(L.p.B) * L.p.Hkv;
   const int z = static_cast<int>(pairs * rows <= 8LL * L.sms ? rows : (rows + 3) / 4);
-  cfg.gridDim = dim3(L.p.Hkv, L.p.B, z < 1 ? 1 : z);
-  cfg.blockDim = dim3(kCompute);
-  cfg.stream = stream;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, few_merge_kernel<D, BF16, MT>, L.p, grid);
+  few_merge_kernel<D, BF16, MT>
+      <<<dim3(L.p.Hkv, L.p.B, z < 1 ? 1 : z), kCompute, 0, stream>>>(L.p, grid);
+  return cudaGetLastError();
 }
 
 template <int D, bool BF16>

@@ -77,12 +77,12 @@ __device__ __forceinline__ int sequence_of(const int32_t* cu, int B, int64_t t) 
   return n;
 }
 
-// One CTA per `tok` tokens. A job is one unit of one row (head) of one token. VEC > 1: a unit
-// of a rotated row in the half layout is the two 16-byte chunks (u, u + R/2) or a chunk of
-// the unrotated rest; in the pair layout it is one chunk. VEC = 1: one pair, or one element
-// of the rest. APPEND: rows 0 .. H-1 are q's, then Hkv of k's and Hkv of v's (copied).
+// One CTA per `tok` tokens. A row (head) is cut into units. VEC > 1: in the half layout a unit
+// is the two 16-byte chunks u and u + R/2, or one chunk of the unrotated rest; in the pair
+// layout one chunk. VEC = 1: one pair, or one element of the rest. APPEND: rows 0 .. H-1 are
+// q's, then Hkv of k's; v's rows are copied.
 template <int DT, int VEC, bool HALF, bool APPEND>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p, int tok) {
+__global__ void __launch_bounds__(kRopeThreads, 3) rope_kernel(const RopeParams p, int tok) {
   using E = Elem<DT>;
   using T = typename E::T;
   using C = Chunk<T, VEC>;
@@ -133,78 +133,97 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p, 
   }
   __syncthreads();
 
-  const int ru = half / kAngles;                          // rotated units of a row
+  // A thread keeps one unit, its angles in registers, and takes every `step`-th row of one token
+  // (or of several, when a row has so many units that the CTA covers fewer tokens at once).
+  const int ru = half / kAngles;                           // rotated units of a row
   const int rest = (p.copy_rest ? p.d - p.rot : 0) / VEC;  // units of the unrotated rest
   const int vu = kTwo && VEC > 1 ? p.d / (2 * VEC) : p.d / VEC;  // units of a copied row
   const int U = APPEND ? max(ru + rest, vu) : ru + rest;
-  const int rows = APPEND ? p.H + 2 * p.Hkv : p.H;
-  const int per_tok = rows * U, total = nt * per_tok;
-#pragma unroll 4
-  for (int j = threadIdx.x; j < total; j += kRopeThreads) {
-    const int tk = j / per_tok, w = j - tk * per_tok;
-    const int r = w / U, u = w - r * U;
+  const int lu = min(U, kRopeThreads), groups = kRopeThreads / lu;
+  const int g = threadIdx.x / lu, gt = min(tok, groups), step = groups / gt;
+  if (g >= gt * step) return;
+  const int turned = APPEND ? p.H + p.Hkv : p.H;
+  for (int tk = g / step; tk < nt; tk += gt) {  // lanes next to each other: rows of one token
     const int64_t t = t0 + tk;
-    const T* src;
-    T* dst;
-    bool turn = true;
-    if constexpr (APPEND) {
-      if (s_dst[tk] == -2) continue;
-      if (r < p.H) {
-        src = static_cast<const T*>(p.x) + t * p.x_token + static_cast<int64_t>(r) * p.d;
-        dst = static_cast<T*>(p.y) + t * p.y_token + static_cast<int64_t>(r) * p.d;
+    const int64_t slot = APPEND ? s_dst[tk] : 0;
+    if (APPEND && slot == -2) continue;
+    for (int u = threadIdx.x - g * lu; u < U; u += lu) {
+      // first elements of the unit's chunks
+      const bool rot = u < ru;
+      int oa, ob = 0;
+      if (!rot) {
+        oa = p.rot + (u - ru) * VEC;
+      } else if (VEC == 1) {
+        oa = HALF ? u : 2 * u;
+        ob = HALF ? half + u : 2 * u + 1;
       } else {
-        if (s_dst[tk] < 0) continue;
-        turn = r < p.H + p.Hkv;
-        const int h = r - p.H - (turn ? 0 : p.Hkv);
-        src = static_cast<const T*>(turn ? p.k : p.v) + t * (turn ? p.k_token : p.v_token) +
-              static_cast<int64_t>(h) * p.d;
-        dst = static_cast<T*>(turn ? p.k_pages : p.v_pages) + s_dst[tk] +
-              static_cast<int64_t>(h) * p.page_size * p.d;
+        oa = u * VEC;
+        ob = half + u * VEC;
       }
-      if (u >= (turn ? ru + rest : vu)) continue;
-    } else {
-      src = static_cast<const T*>(p.x) + t * p.x_token + r * p.x_head;
-      dst = static_cast<T*>(p.y) + t * p.y_token + r * p.y_head;
-    }
-    if (!turn) {
-      if constexpr (kTwo && VEC > 1) {
-        const C a = *reinterpret_cast<const C*>(src + u * VEC);
-        const C b = *reinterpret_cast<const C*>(src + p.d / 2 + u * VEC);
-        *reinterpret_cast<C*>(dst + u * VEC) = a;
-        *reinterpret_cast<C*>(dst + p.d / 2 + u * VEC) = b;
-      } else {
-        *reinterpret_cast<C*>(dst + u * VEC) = *reinterpret_cast<const C*>(src + u * VEC);
+      float2 cs[kAngles];
+      if (rot) {
+#pragma unroll
+        for (int e = 0; e < kAngles; ++e) cs[e] = s_cs[tk * half + u * kAngles + e];
       }
-    } else if (u >= ru) {
-      const int o = p.rot + (u - ru) * VEC;
-      *reinterpret_cast<C*>(dst + o) = *reinterpret_cast<const C*>(src + o);
-    } else {
-      const float2* cs = s_cs + tk * half + u * kAngles;
-      if constexpr (kTwo) {
-        const int oa = HALF ? u * VEC : 2 * u, ob = HALF ? half + u * VEC : 2 * u + 1;
-        const C a = *reinterpret_cast<const C*>(src + oa);
-        const C b = *reinterpret_cast<const C*>(src + ob);
-        C ya, yb;
+      auto src_of = [&](int r) -> const T* {
+        if (APPEND && r >= p.H)
+          return static_cast<const T*>(p.k) + t * p.k_token + static_cast<int64_t>(r - p.H) * p.d;
+        return static_cast<const T*>(p.x) + t * p.x_token + r * p.x_head;
+      };
+      auto dst_of = [&](int r) -> T* {
+        if (APPEND && r >= p.H)
+          return static_cast<T*>(p.k_pages) + slot +
+                 static_cast<int64_t>(r - p.H) * p.page_size * p.d;
+        return static_cast<T*>(p.y) + t * p.y_token + r * p.y_head;
+      };
+      const int rows = APPEND && slot < 0 ? p.H : turned;  // no slot: q alone
+      constexpr int N = 2;                                 // rows in flight
+      for (int r0 = g % step; r0 < rows && u < ru + rest; r0 += N * step) {
+        C a[N], b[N];
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          const float2 k = cs[e];
-          const float xa = E::get(a.e[e]), xb = E::get(b.e[e]);
-          ya.e[e] = E::put(xa * k.x - xb * k.y);
-          yb.e[e] = E::put(xb * k.x + xa * k.y);
+        for (int i = 0; i < N; ++i) {
+          const int r = r0 + i * step;
+          if (r < rows) {
+            a[i] = *reinterpret_cast<const C*>(src_of(r) + oa);
+            if (kTwo && rot) b[i] = *reinterpret_cast<const C*>(src_of(r) + ob);
+          }
         }
-        *reinterpret_cast<C*>(dst + oa) = ya;
-        *reinterpret_cast<C*>(dst + ob) = yb;
-      } else {
-        const C a = *reinterpret_cast<const C*>(src + u * VEC);
-        C y;
 #pragma unroll
-        for (int e = 0; e < kAngles; ++e) {
-          const float2 k = cs[e];
-          const float xa = E::get(a.e[2 * e]), xb = E::get(a.e[2 * e + 1]);
-          y.e[2 * e] = E::put(xa * k.x - xb * k.y);
-          y.e[2 * e + 1] = E::put(xb * k.x + xa * k.y);
+        for (int i = 0; i < N; ++i) {
+          const int r = r0 + i * step;
+          if (r >= rows) break;
+          if (rot) {
+            if constexpr (kTwo) {
+#pragma unroll
+              for (int e = 0; e < VEC; ++e) {
+                const float xa = E::get(a[i].e[e]), xb = E::get(b[i].e[e]);
+                a[i].e[e] = E::put(xa * cs[e].x - xb * cs[e].y);
+                b[i].e[e] = E::put(xb * cs[e].x + xa * cs[e].y);
+              }
+              *reinterpret_cast<C*>(dst_of(r) + ob) = b[i];
+            } else {
+#pragma unroll
+              for (int e = 0; e < kAngles; ++e) {
+                const float xa = E::get(a[i].e[2 * e]), xb = E::get(a[i].e[2 * e + 1]);
+                a[i].e[2 * e] = E::put(xa * cs[e].x - xb * cs[e].y);
+                a[i].e[2 * e + 1] = E::put(xb * cs[e].x + xa * cs[e].y);
+              }
+            }
+          }
+          *reinterpret_cast<C*>(dst_of(r) + oa) = a[i];
         }
-        *reinterpret_cast<C*>(dst + u * VEC) = y;
+      }
+      if constexpr (APPEND) {
+        for (int r = g % step; r < p.Hkv && u < vu && slot >= 0; r += step) {
+          const T* src = static_cast<const T*>(p.v) + t * p.v_token + static_cast<int64_t>(r) * p.d;
+          T* dst = static_cast<T*>(p.v_pages) + slot + static_cast<int64_t>(r) * p.page_size * p.d;
+          const C a = *reinterpret_cast<const C*>(src + u * VEC);
+          if constexpr (kTwo && VEC > 1) {
+            const C b = *reinterpret_cast<const C*>(src + p.d / 2 + u * VEC);
+            *reinterpret_cast<C*>(dst + p.d / 2 + u * VEC) = b;
+          }
+          *reinterpret_cast<C*>(dst + u * VEC) = a;
+        }
       }
     }
   }

@@ -201,7 +201,12 @@ __global__ void __launch_bounds__(kPlanThreads) var_plan_kernel(const VarParams 
     s.split = INT_MAX;
   }
   __syncthreads();
+  // the last unit a thread has seen; all of them when there are no more units than threads
+  VarUnit mine;
+  bool has = false;
   for_each_block(p, s, true, [&](const VarUnit& u) {
+    mine = u;
+    has = true;
     atomicAdd(&s.bins[bin_of(u.j1, p) + 1], 1);
     if (p.part) {
       atomicAdd(&s.pairs, 1);
@@ -209,8 +214,17 @@ __global__ void __launch_bounds__(kPlanThreads) var_plan_kernel(const VarParams 
       atomicAdd(&s.cost, static_cast<unsigned long long>(u.j1));
     }
   });
+  const bool one_pass = p.B <= kPlanThreads && s.scan.off[p.B] <= kPlanThreads;
+  auto every_unit = [&](auto f) {
+    if (one_pass) {
+      if (has) f(mine);
+      __syncthreads();
+    } else {
+      for_each_block(p, s, false, f);
+    }
+  };
   if (p.part && s.pairs * p.Hkv < 2 * sms && s.n_max >= 8) {
-    for_each_block(p, s, false, [&](const VarUnit& u) {
+    every_unit([&](const VarUnit& u) {
       for (int c = 0; c < kCandidates; ++c) {
         const int S = (s.n_max + c) / (c + 1);
         atomicAdd(&s.units[c], max(1, (u.j1 + S - 1) / S));
@@ -234,7 +248,7 @@ __global__ void __launch_bounds__(kPlanThreads) var_plan_kernel(const VarParams 
     if (s.split != INT_MAX) {  // bins of the split items
       for (int i = tid; i <= kBins; i += kPlanThreads) s.bins[i] = 0;
       __syncthreads();
-      for_each_block(p, s, false, [&](const VarUnit& u) {
+      every_unit([&](const VarUnit& u) {
         const int ns = max(1, (u.j1 + s.split - 1) / s.split);
         for (int k = 0; k < ns; ++k)
           atomicAdd(&s.bins[bin_of(u.j1 * (k + 1) / ns - u.j1 * k / ns, p) + 1], 1);
@@ -247,7 +261,7 @@ __global__ void __launch_bounds__(kPlanThreads) var_plan_kernel(const VarParams 
     if (units > p.max_units) atomicOr(p.m.status, FA_DEV_BAD_PAGE);
   }
   const int split = s.split;
-  for_each_block(p, s, false, [&](VarUnit u) {
+  every_unit([&](VarUnit u) {
     const int n = u.j1, ns = split == INT_MAX ? 1 : max(1, (n + split - 1) / split);
     if (ns > 1) {
       u.slot = atomicAdd(&s.slots, ns);
@@ -748,12 +762,9 @@ cudaError_t launch_t(const VarLaunch& L, cudaStream_t stream) {
   const int64_t items = static_cast<int64_t>(L.p.max_units) * L.p.Hkv;
   const int grid = static_cast<int>(items < L.sms ? items : L.sms);
   k<<<grid, kThreads, smem, stream>>>(L.tmQ, L.tmK, L.tmV, L.p);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  if (L.p.part) {
-    var_merge_kernel<D, BF16><<<L.sms * 8, 256, 0, stream>>>(L.p);
-    e = cudaGetLastError();
-  }
-  return e;
+  if ((e = cudaGetLastError()) != cudaSuccess || !L.p.part) return e;
+  var_merge_kernel<D, BF16><<<L.sms * 8, 256, 0, stream>>>(L.p);
+  return cudaGetLastError();
 }
 
 }  // namespace

@@ -148,14 +148,24 @@ __global__ void __launch_bounds__(kPlanThreads) bwd_plan_kernel(const VarBwdPara
   __shared__ BwdPlanSmem s;
   for (int i = threadIdx.x; i <= kBins; i += kPlanThreads) s.bins[i] = 0;
   __syncthreads();
+  // the last unit a thread has seen; all of them when there are no more units than threads
+  VarBwdUnit mine;
+  bool has = false;
   for_each_key_block(p, s, true, [&](const VarBwdUnit& u) {
+    mine = u;
+    has = true;
     atomicAdd(&s.bins[cost_bin(u.n, p.cost_shift) + 1], 1);
   });
+  const bool one_pass = p.B <= kPlanThreads && s.scan.off[p.B] <= kPlanThreads;
   const int units = scan_bins(s.scan, s.bins);
-  for_each_key_block(p, s, false, [&](const VarBwdUnit& u) {
+  auto put = [&](const VarBwdUnit& u) {
     const int at = atomicAdd(&s.bins[cost_bin(u.n, p.cost_shift)], 1);
     if (at < p.max_units) p.units[at] = u;
-  });
+  };
+  if (!one_pass)
+    for_each_key_block(p, s, false, put);
+  else if (has)
+    put(mine);
   if (threadIdx.x == 0) {  // more than fit only when starts overlap, which no packed rows have
     p.n_units[0] = min(units, p.max_units);
     if (units > p.max_units) atomicOr(p.m.status, FA_DEV_BAD_PAGE);
@@ -168,14 +178,17 @@ __global__ void __launch_bounds__(kPlanThreads) bwd_plan_kernel(const VarBwdPara
 struct HalfRows {
   int t0, n;
 };
+// Found by one warp: 32 sequences probed at a time narrow the range 32-fold per load.
 __device__ __forceinline__ HalfRows half_rows(const VarBwdParams& p, int s) {
-  int lo = 0, hi = p.B;  // the last sequence whose slots start at or before s
-  while (hi - lo > 1) {
-    const int mid = lo + (hi - lo) / 2;
-    if (p.cu_q[mid] / p.TPH + mid <= s)
-      lo = mid;
-    else
-      hi = mid;
+  const int lane = threadIdx.x % 32;
+  int lo = 0, n = p.B;  // the last sequence whose slots start at or before s is in [lo, lo + n)
+  while (n > 1) {
+    const int step = (n + 31) / 32, at = lo + lane * step;
+    const bool in = lane * step < n && p.cu_q[at] / p.TPH + at <= s;
+    const uint32_t hit = __ballot_sync(0xffffffffu, in);
+    const int last = hit ? 31 - __clz(hit) : 0;
+    n = min(step, n - last * step);
+    lo += last * step;
   }
   const SeqRows r = rows_of(p.cu_q, lo, p.total_q);
   const int at = (s - (r.first / p.TPH + lo)) * p.TPH;
@@ -210,7 +223,10 @@ __global__ void __launch_bounds__(256) bwd_prep_kernel(const VarBwdParams p) {
   __shared__ HalfRows sh;
   const int hh = blockIdx.y;          // K/V head x head subset
   const int kvh = hh / p.HS, h0 = kvh * p.G + (hh % p.HS) * p.GS;
-  if (threadIdx.x == 0) sh = half_rows(p, blockIdx.x);
+  if (threadIdx.x < 32) {
+    const HalfRows f = half_rows(p, blockIdx.x);
+    if (threadIdx.x == 0) sh = f;
+  }
   __syncthreads();
   const HalfRows r = sh;
   if (r.n == 0) return;
@@ -247,7 +263,10 @@ __global__ void __launch_bounds__(256) bwd_dq_kernel(const VarBwdParams p) {
   __shared__ HalfRows sh;
   const int hh = blockIdx.y;
   const int kvh = hh / p.HS, h0 = kvh * p.G + (hh % p.HS) * p.GS;
-  if (threadIdx.x == 0) sh = half_rows(p, blockIdx.x);
+  if (threadIdx.x < 32) {
+    const HalfRows f = half_rows(p, blockIdx.x);
+    if (threadIdx.x == 0) sh = f;
+  }
   __syncthreads();
   const HalfRows r = sh;
   if (r.n == 0) return;
@@ -278,21 +297,25 @@ __global__ void __launch_bounds__(256) bwd_dq_kernel(const VarBwdParams p) {
   }
 }
 
-// dk and dv of the keys of one unit and K/V head: the head subsets' partials summed in order.
+// dk and dv of a quarter of the keys of one unit and K/V head: the head subsets' partials summed
+// in order.
 template <int D, bool BF16>
 __global__ void __launch_bounds__(256) bwd_sum_kernel(const VarBwdParams p) {
-  if (static_cast<int>(blockIdx.x) >= p.n_units[0]) return;
-  const VarBwdUnit u = p.units[blockIdx.x];
+  const int unit = blockIdx.x / 4, r0 = (blockIdx.x % 4) * (kBT / 4);
+  if (unit >= p.n_units[0]) return;
+  const int k0 = p.units[unit].k0, nk = p.units[unit].nk;
   const int kvh = blockIdx.y;
   const size_t plane = static_cast<size_t>(p.total_k) * p.Hkv * D;
-  for (int i = threadIdx.x; i < 2 * u.nk * (D / 4); i += 256) {
-    const int which = i / (u.nk * (D / 4)), w = i - which * u.nk * (D / 4);
-    const int row = w / (D / 4), c = w % (D / 4);
-    const float* src = p.part + which * plane +
-                       (static_cast<size_t>(u.k0 + row) * p.Hkv + kvh) * D + 4 * c;
+  constexpr int CH = D / 4;  // 16-byte chunks of a row
+#pragma unroll
+  for (int i = threadIdx.x; i < 2 * (kBT / 4) * CH; i += 256) {
+    const int which = i / ((kBT / 4) * CH), row = r0 + (i / CH) % (kBT / 4), c = i % CH;
+    if (row >= nk) continue;
+    const float* src = p.part + which * plane + (static_cast<size_t>(k0 + row) * p.Hkv + kvh) * D + 4 * c;
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
     for (int s = 0; s < p.HS; ++s) {
-      const float4 v = *reinterpret_cast<const float4*>(src + 2 * plane * s);
+      const float4 v = __ldcs(reinterpret_cast<const float4*>(src + 2 * plane * s));
       a.x += v.x, a.y += v.y, a.z += v.z, a.w += v.w;
     }
     const float mul = which ? 1.f : p.scale;
@@ -300,7 +323,7 @@ __global__ void __launch_bounds__(256) bwd_sum_kernel(const VarBwdParams p) {
     o.x = BF16 ? cvt_pack_bf16(a.x * mul, a.y * mul) : cvt_pack_f16(a.x * mul, a.y * mul);
     o.y = BF16 ? cvt_pack_bf16(a.z * mul, a.w * mul) : cvt_pack_f16(a.z * mul, a.w * mul);
     uint16_t* out = static_cast<uint16_t*>(which ? p.dv : p.dk) +
-                    static_cast<int64_t>(u.k0 + row) * (which ? p.dv_token : p.dk_token) + kvh * D;
+                    static_cast<int64_t>(k0 + row) * (which ? p.dv_token : p.dk_token) + kvh * D;
     reinterpret_cast<uint2*>(out)[c] = o;
   }
 }
@@ -779,14 +802,14 @@ cudaError_t launch_t(const VarBwdLaunch& L, cudaStream_t stream) {
   }
   if (p.total_k > 0) {
     constexpr int smem = Cfg<D>::SMEM;
-    auto k = bwd_main_kernel<D, BF16>;
+    auto* k = bwd_main_kernel<D, BF16>;
     e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     k<<<static_cast<unsigned>(p.max_units) * per, kThreads, smem, stream>>>(L.tmQ, L.tmK, L.tmV,
                                                                             L.tmdO, p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     if (p.HS > 1) {
-      bwd_sum_kernel<D, BF16><<<dim3(p.max_units, p.Hkv), 256, 0, stream>>>(p);
+      bwd_sum_kernel<D, BF16><<<dim3(4 * p.max_units, p.Hkv), 256, 0, stream>>>(p);
       if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
   }
