@@ -428,10 +428,10 @@ fa_status fa_rope_freqs(double* freqs, float* amplitude, int rot_dim, double bas
  *   positions  int32 [T], device; any values (angles are formed modulo one turn in 64-bit
  *              fixed point, so far positions lose nothing)
  *   freqs      float64 [rot_dim / 2], device
- *   T >= 0, H >= 1, d in [2, 512], rot_dim even in [2, d]; style FA_ROPE_HALF or
+ *   T >= 0, H >= 1, d even in [2, 512], rot_dim even in [2, d]; style FA_ROPE_HALF or
  *   FA_ROPE_PAIRS; dtype FA_F16, FA_BF16 or FA_F32. x and y aligned to their element; with
- *   16-byte aligned pointers, steps of a multiple of 16 bytes and rot_dim and d likewise, heads
- *   move in 16-byte accesses, else element by element.
+ *   16-byte aligned pointers, steps of a multiple of 16 bytes and rot_dim and d a multiple of
+ *   32 bytes, heads move in 16-byte accesses, else element by element.
  */
 fa_status fa_rope(const void* x, void* y, const int32_t* positions, const double* freqs, int64_t T,
                   int H, int d, int rot_dim, int64_t x_token, int64_t x_head, int64_t y_token,
@@ -539,8 +539,8 @@ size_t fa_bwd_varlen_workspace_size(int B, int H, int Hkv, int total_q, int tota
  *   max_q      at least the longest chunk; up to 64 / (H / Hkv) tokens the call runs a kernel
  *              for few rows. Rows of a chunk from max_q on may be left as they were, which is
  *              reported as FA_ERR_BAD_PAGE
- *   B at most 65535, everything else as for fa_fwd_varlen; the workspace has
- *   fa_paged_varlen_workspace_size(...) bytes.
+ *   everything else as for fa_fwd_varlen; the workspace has fa_paged_varlen_workspace_size(...)
+ *   bytes.
  * Slots behind a sequence's last key may hold anything. A table entry outside [0, num_pages) is
  * read as page 0 and reported as FA_ERR_BAD_PAGE.
  */

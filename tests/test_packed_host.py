@@ -69,7 +69,7 @@ def rope(L, **kw):
 
 @pytest.mark.parametrize("kw,want", [
     (dict(T=0, x=None), OK), (dict(T=-1), INVALID), (dict(H=0), INVALID), (dict(d=1), INVALID),
-    (dict(d=514, xh=514, yh=514), INVALID), (dict(rot=0), INVALID), (dict(rot=63), INVALID),
+    (dict(d=514, xh=514, yh=514), INVALID), (dict(d=63, rot=62), UNSUPPORTED), (dict(rot=0), INVALID), (dict(rot=63), INVALID),
     (dict(rot=66), INVALID), (dict(style=2), INVALID), (dict(amp=math.inf), INVALID),
     (dict(dtype=3), UNSUPPORTED), (dict(x=None), INVALID), (dict(pos=None), INVALID),
     (dict(fr=None), INVALID), (dict(x=A + 1), INVALID), (dict(dtype=2, y=A + 2), INVALID),

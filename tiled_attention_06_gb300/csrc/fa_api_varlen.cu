@@ -253,6 +253,7 @@ fa_status fa_rope(const void* x, void* y, const int32_t* positions, const double
     return fail(FA_ERR_INVALID_ARG, "need T >= 0, H >= 1 and d in [2, 512]");
   if (rot_dim < 2 || rot_dim > d || rot_dim % 2)
     return fail(FA_ERR_INVALID_ARG, "rot_dim %d (even, in [2, d])", rot_dim);
+  if (d % 2) return fail(FA_ERR_UNSUPPORTED, "head dim %d (even)", d);
   if (style != FA_ROPE_HALF && style != FA_ROPE_PAIRS)
     return fail(FA_ERR_INVALID_ARG, "style %d", style);
   if (!std::isfinite(amplitude)) return fail(FA_ERR_INVALID_ARG, "amplitude must be finite");
@@ -294,8 +295,8 @@ fa_status fa_rope(const void* x, void* y, const int32_t* positions, const double
   p.copy_rest = x != y;
   p.status = dev.status;
   const int v = static_cast<int>(16 / es);
-  const bool vec = both % 16 == 0 && (x_token | x_head | y_token | y_head) % v == 0 && d % v == 0 &&
-                   (style == FA_ROPE_HALF ? rot_dim / 2 : rot_dim) % v == 0;
+  const bool vec = both % 16 == 0 && (x_token | x_head | y_token | y_head) % v == 0 &&
+                   d % (2 * v) == 0 && rot_dim % (2 * v) == 0;
   const cudaError_t e = fa::launch_rope(p, dtype, style == FA_ROPE_HALF, vec, dev.sms,
                                         reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "rope launch");
@@ -368,7 +369,7 @@ fa_status fa_rope_append(const fa_rope_append_params* params, fa_stream_t stream
   p.max_pages = a.max_pages_per_seq;
   p.num_pages = a.num_pages;
   p.status = dev.status;
-  const bool vec = (a.style == FA_ROPE_HALF ? a.rot_dim / 2 : a.rot_dim) % 8 == 0;
+  const bool vec = a.rot_dim % 16 == 0;
   const cudaError_t e = fa::launch_rope_append(p, a.dtype, a.style == FA_ROPE_HALF, vec, dev.sms,
                                                reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "rope append launch");
@@ -449,7 +450,7 @@ size_t fa_paged_varlen_workspace_size(int B, int H, int Hkv, int total_q, int ma
   if (B < 1 || Hkv < 1 || H < Hkv || H % Hkv || H / Hkv > 128 || total_q < 0 || max_q < 0 || d < 1)
     return 0;
   const int rows = few_rows(max_q, H / Hkv);
-  return rows ? fa::few_part_floats(rows, d) * sizeof(float)
+  return rows ? fa::kFewHeadBytes + fa::few_part_floats(rows, d) * sizeof(float)
               : var_layout(B, H, Hkv, total_q, d).total;
 }
 
@@ -460,9 +461,8 @@ fa_status fa_fwd_paged_varlen(const fa_paged_varlen_params* params, fa_stream_t 
                  a.mask_mode, a.window, a.n_global, a.dtype};
   fa_status st = check_common(c);
   if (st != FA_OK) return st;
-  if (a.max_pages_per_seq < 1 || a.num_pages < 1 || a.max_q < 0 || a.B > 65535)
-    return fail(FA_ERR_INVALID_ARG,
-                "need max_pages_per_seq, num_pages >= 1, max_q >= 0 and B <= 65535");
+  if (a.max_pages_per_seq < 1 || a.num_pages < 1 || a.max_q < 0)
+    return fail(FA_ERR_INVALID_ARG, "need max_pages_per_seq, num_pages >= 1 and max_q >= 0");
   if (a.page_size < 16 || a.page_size > 4096 || a.page_size % 16 != 0)
     return fail(FA_ERR_UNSUPPORTED, "page_size %d (a multiple of 16 in [16, 4096])", a.page_size);
   const long long cap = static_cast<long long>(a.page_size) * a.max_pages_per_seq;
@@ -512,7 +512,8 @@ fa_status fa_fwd_paged_varlen(const fa_paged_varlen_params* params, fa_stream_t 
     p.max_pages = a.max_pages_per_seq;
     p.num_pages = a.num_pages;
     p.box = std::min(64, pow2);
-    p.part = static_cast<float*>(a.workspace);
+    p.heads = static_cast<fa::FewHead*>(a.workspace);
+    p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + fa::kFewHeadBytes);
     F.sms = dev.sms;
     if ((st = make_map3(&F.tmK, a.k_pages, bf16, a.d, a.page_size, a.d, planes, plane, p.box,
                         1)) != FA_OK)

@@ -13,8 +13,8 @@
 // written to o, a piece to the workspace. The four warps are MT row groups of 16 rows times
 // 4 / MT key groups of the tile; each keeps its own running maximum, sum and output in
 // registers, joined through shared memory at the end of a segment.
-// few_merge_kernel joins the pieces, one CTA per sequence, K/V head and row, in the order of
-// the keys.
+// few_merge_kernel joins the pieces of each pair in the order of the keys; the CTA that holds a
+// pair's first piece leaves word of where the others are.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -72,13 +72,13 @@ __device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t* r) {
 template <bool BF16>
 __device__ __forceinline__ void mma(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
   if constexpr (BF16)
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
         "{%8, %9}, {%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
   else
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
         "{%8, %9}, {%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -215,6 +215,18 @@ __global__ void __launch_bounds__(kThreads, 2)
       at += n;
     }
   }
+  if (threadIdx.x == 0) p.heads[blockIdx.x] = FewHead{0, 0, 0, 0};
+  if (blockIdx.x == 0 && threadIdx.x < kCompute) {  // chunks that see no key at all
+    for (int b = tot.b0; b < tot.b1; ++b) {
+      const FewSeq s = few_seq(p, b, false);
+      if (s.tiles > 0) continue;
+      for (int t = s.q0; t < s.q0 + s.n; ++t) {
+        uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + t * p.o_token);
+        for (int i = 0; i < p.H * D / 8; ++i) dst[i] = make_uint4(0, 0, 0, 0);
+        for (int h = 0; h < p.H && p.lse; ++h) p.lse[static_cast<size_t>(t) * p.H + h] = -INFINITY;
+      }
+    }
+  }
   __syncthreads();
   if (begin >= end) return;  // uniform: no barrier is used from here
   Walk w;
@@ -314,6 +326,10 @@ __global__ void __launch_bounds__(kThreads, 2)
       const int n0 = tile_at(w.s.rg, j) * BK;
       const int st = pos % C::NST;
       if (!mbar_wait(B(bars->full[st]), (pos / C::NST) & 1, wc)) return;
+      if (16 * rw >= rows) {  // no row of this group: only keep step
+        if (lane == 0) mbar_arrive(B(bars->empty[st]));
+        continue;
+      }
       const uint32_t sK = base + 2 * st * C::TILE, sV = sK + C::TILE;
       const int live = w.s.sk - n0;
       float s[NT][4];
@@ -490,6 +506,13 @@ __global__ void __launch_bounds__(kThreads, 2)
       // a piece that starts its pair goes to slot 2x + 1, one that continues it to slot 2x
       const int slot = 2 * blockIdx.x + (w.j == 0 ? 1 : 0);
       const int nslots = 2 * gridDim.x;
+      if (!whole && w.j == 0 && threadIdx.x == 0) {
+        // the piece that starts a pair says where the rest is: CTAs on to that of its last tile
+        const int64_t last = end - w.left + w.s.tiles - 1;  // end - left: the segment's first tile
+        int x = blockIdx.x + 1;
+        while (all * (x + 1) / used <= last) ++x;
+        p.heads[blockIdx.x] = FewHead{w.s.q0, rows, w.kvh, x};
+      }
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int r = r0 + 8 * i;
@@ -523,46 +546,22 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
 }
 
-// One CTA per (K/V head, sequence): the pieces of the pair in key order, four warps taking
-// every fourth piece of a row. A pair that one CTA held whole is already written.
+// CTA (x, z): the pair whose first piece CTA x of few_kernel holds, every gridDim.y-th row. Four
+// warps take every fourth piece of a row.
 template <int D, bool BF16, int MT>
-__global__ void __launch_bounds__(kCompute) few_merge_kernel(const FewParams p, int grid) {
+__global__ void __launch_bounds__(kCompute) few_merge_kernel(const FewParams p) {
   constexpr int E = D / 32, ROWS = 16 * MT;
-  __shared__ int64_t s_sum[4];
-  __shared__ int64_t s_at;
   __shared__ float s_ml[4][2], s_acc[4][D];
-  const int kvh = blockIdx.x, b = blockIdx.y;
+  const int x0 = blockIdx.x, nslots = 2 * gridDim.x;
+  const FewHead hd = p.heads[x0];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const Totals tot = tile_totals(p, s_sum);
-  if (b >= tot.b0 && b < tot.b1) {
-    int64_t at = tot.before;
-    for (int i = tot.b0; i < b; ++i) at += few_seq(p, i, false).tiles;
-    s_at = at;
-  }
-  __syncthreads();
-  const FewSeq s = few_seq(p, b, false);
-  const int rows = s.n * p.G;
-  if (rows == 0) return;
-  const int64_t all = tot.all * p.Hkv;
-  const int64_t t0 = s_at * p.Hkv + static_cast<int64_t>(kvh) * s.tiles, t1 = t0 + s.tiles;
-  const int used = ctas_used(all, grid);
-  // CTA x holds the tiles [all x / used, all (x + 1) / used)
-  auto cta_of = [&](int64_t t) {
-    int x = static_cast<int>(t * used / all);
-    while (all * (x + 1) / used <= t) ++x;
-    while (all * x / used > t) --x;
-    return x;
-  };
-  const int x0 = s.tiles ? cta_of(t0) : 0, x1 = s.tiles ? cta_of(t1 - 1) : -1;
-  if (x0 == x1) return;
-  const int nslots = 2 * grid;
   const float* ml = p.part + static_cast<size_t>(nslots) * ROWS * D;
-  for (int r = blockIdx.z; r < rows; r += gridDim.z) {
+  for (int r = blockIdx.y; r < hd.rows; r += gridDim.y) {
     float M = -INFINITY, L = 0.f, acc[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = 0.f;
 #pragma unroll 4
-    for (int x = x0 + warp; x <= x1; x += 4) {
+    for (int x = x0 + warp; x <= hd.last; x += 4) {
       const int slot = 2 * x + (x == x0 ? 1 : 0);
       const float m = ml[slot * ROWS + r], l = ml[(nslots + slot) * ROWS + r];
       const float* src = p.part + (static_cast<size_t>(slot) * ROWS + r) * D + lane * E;
@@ -591,9 +590,10 @@ __global__ void __launch_bounds__(kCompute) few_merge_kernel(const FewParams p, 
       wts[i] = ex2_approx(s_ml[i][0] - mu);
       La += s_ml[i][1] * wts[i];
     }
-    const int tok = r / p.G, h = kvh * p.G + r - tok * p.G;
+    const int tok = r / p.G, h = hd.kvh * p.G + r - tok * p.G;
     const float inv = La > 0.f ? 1.f / La : 0.f;
-    uint16_t* out = static_cast<uint16_t*>(p.o) + static_cast<int64_t>(s.q0 + tok) * p.o_token + h * D;
+    uint16_t* out =
+        static_cast<uint16_t*>(p.o) + static_cast<int64_t>(hd.q0 + tok) * p.o_token + h * D;
     for (int e = 2 * threadIdx.x; e < D; e += 2 * kCompute) {
       float a = 0.f, c = 0.f;
       for (int i = 0; i < 4; ++i) {
@@ -604,7 +604,7 @@ __global__ void __launch_bounds__(kCompute) few_merge_kernel(const FewParams p, 
           BF16 ? cvt_pack_bf16(a * inv, c * inv) : cvt_pack_f16(a * inv, c * inv);
     }
     if (threadIdx.x == 0 && p.lse)
-      p.lse[static_cast<size_t>(s.q0 + tok) * p.H + h] =
+      p.lse[static_cast<size_t>(hd.q0 + tok) * p.H + h] =
           La > 0.f ? (Ma + lg2_approx(La)) * 0.69314718055994531f : -INFINITY;
     __syncthreads();
   }
@@ -620,11 +620,8 @@ cudaError_t launch_mt(const FewLaunch& L, cudaStream_t stream) {
   k<<<grid, kThreads, smem, stream>>>(L.tmK, L.tmV, L.p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   const int rows = L.p.max_q * L.p.G;
-  // few pairs: a CTA per row as well, else the rows of a pair one after the other
-  const int64_t pairs = static_cast<int64_t>(L.p.B) * L.p.Hkv;
-  const int z = static_cast<int>(pairs * rows <= 8LL * L.sms ? rows : (rows + 3) / 4);
-  few_merge_kernel<D, BF16, MT>
-      <<<dim3(L.p.Hkv, L.p.B, z < 1 ? 1 : z), kCompute, 0, stream>>>(L.p, grid);
+  const int y = rows < 1 ? 1 : (rows < 8 ? rows : 8);
+  few_merge_kernel<D, BF16, MT><<<dim3(grid, y), kCompute, 0, stream>>>(L.p);
   return cudaGetLastError();
 }
 

@@ -137,8 +137,8 @@ constexpr int kCandidates = 16;
 struct PlanSmem {
   SeqScan scan;
   int bins[kBins + 1];
-  int pairs, n_max, slots, groups, split;
-  unsigned long long cost;
+  // units, largest and sum of their key blocks (used for few units alone), split choice
+  int pairs, n_max, cost, slots, groups, split;
   int units[kCandidates];
 };
 
@@ -182,99 +182,99 @@ __device__ __forceinline__ void for_each_block(const VarParams& p, PlanSmem& s, 
       });
 }
 
-__device__ __forceinline__ int bin_of(int n, const VarParams& p) {
-  return cost_bin(n, p.cost_shift);
-}
-
 // The work list. Splitting: an item of n key blocks takes about n + 4 block times (the 4:
 // first loads, last P V, epilogue); with splits of at most S blocks the launch takes about
 // max(S + 4, ceil(items / SMs) (mean + 4)), and 8 more to join them (a 512-token chunk over
 // 8192 cached tokens with 8 K/V heads has 64 items for 152 SMs). The least of a few S wins.
+//
+// One CTA for a few microseconds, most of them spent fetching its instructions: the passes over
+// the units share one copy of the code, and units stay in registers when there are no more of
+// them than threads.
+enum { kCount, kTry, kRecount, kWrite, kPasses };
 __global__ void __launch_bounds__(kPlanThreads) var_plan_kernel(const VarParams p, int sms) {
   __shared__ PlanSmem s;
   const int tid = threadIdx.x;
   for (int i = tid; i <= kBins; i += kPlanThreads) s.bins[i] = 0;
   if (tid < kCandidates) s.units[tid] = 0;
   if (tid == 0) {
-    s.pairs = s.n_max = s.slots = s.groups = 0;
-    s.cost = 0;
+    s.pairs = s.n_max = s.cost = s.slots = s.groups = 0;
     s.split = INT_MAX;
   }
   __syncthreads();
-  // the last unit a thread has seen; all of them when there are no more units than threads
-  VarUnit mine;
-  bool has = false;
-  for_each_block(p, s, true, [&](const VarUnit& u) {
-    mine = u;
-    has = true;
-    atomicAdd(&s.bins[bin_of(u.j1, p) + 1], 1);
-    if (p.part) {
-      atomicAdd(&s.pairs, 1);
-      atomicMax(&s.n_max, u.j1);
-      atomicAdd(&s.cost, static_cast<unsigned long long>(u.j1));
-    }
-  });
-  const bool one_pass = p.B <= kPlanThreads && s.scan.off[p.B] <= kPlanThreads;
-  auto every_unit = [&](auto f) {
-    if (one_pass) {
-      if (has) f(mine);
-      __syncthreads();
-    } else {
-      for_each_block(p, s, false, f);
-    }
-  };
-  if (p.part && s.pairs * p.Hkv < 2 * sms && s.n_max >= 8) {
-    every_unit([&](const VarUnit& u) {
-      for (int c = 0; c < kCandidates; ++c) {
-        const int S = (s.n_max + c) / (c + 1);
-        atomicAdd(&s.units[c], max(1, (u.j1 + S - 1) / S));
-      }
-    });
-    if (tid == 0) {
-      float best = 0.f;
-      for (int c = 0; c < kCandidates; ++c) {
-        const int S = (s.n_max + c) / (c + 1), items = s.units[c] * p.Hkv;
-        if (c > 0 && (S < 4 || items > kVarMaxSplit || s.units[c] > p.max_units)) break;
-        const float mean = static_cast<float>(s.cost) / s.units[c];
-        float est = fmaxf(S + 4.f, ((items + sms - 1) / sms) * (mean + 4.f));
-        if (c > 0) est += 8.f;
-        if (c == 0 || est < best) {
-          best = est;
-          s.split = c == 0 ? INT_MAX : S;
-        }
-      }
-    }
-    __syncthreads();
-    if (s.split != INT_MAX) {  // bins of the split items
+  VarUnit mine;       // the last unit this thread has seen
+  bool has = false, one_pass = false;
+#pragma unroll 1
+  for (int pass = kCount; pass < kPasses; ++pass) {
+    const int split = s.split, n_max = s.n_max;
+    if (pass == kTry && !(p.part && s.pairs * p.Hkv < 2 * sms && n_max >= 8)) continue;
+    if (pass == kRecount) {
+      if (split == INT_MAX) continue;
       for (int i = tid; i <= kBins; i += kPlanThreads) s.bins[i] = 0;
       __syncthreads();
-      every_unit([&](const VarUnit& u) {
-        const int ns = max(1, (u.j1 + s.split - 1) / s.split);
-        for (int k = 0; k < ns; ++k)
-          atomicAdd(&s.bins[bin_of(u.j1 * (k + 1) / ns - u.j1 * k / ns, p) + 1], 1);
+    }
+    if (pass == kWrite) {
+      const int units = scan_bins(s.scan, s.bins);
+      if (tid == 0) {  // more than fit only when starts overlap, which no packed rows have
+        p.hdr->units = min(units, p.max_units);
+        if (units > p.max_units) atomicOr(p.m.status, FA_DEV_BAD_PAGE);
+      }
+    }
+    auto visit = [&](VarUnit u) {
+      const int n = u.j1, ns = split == INT_MAX ? 1 : max(1, (n + split - 1) / split);
+      if (pass == kCount && p.part) {
+        atomicAdd(&s.pairs, 1);
+        atomicMax(&s.n_max, n);
+        atomicAdd(&s.cost, n);
+      }
+      if (pass == kTry) {
+        for (int c = 0; c < kCandidates; ++c) {
+          const int S = (n_max + c) / (c + 1);
+          atomicAdd(&s.units[c], max(1, (n + S - 1) / S));
+        }
+        return;
+      }
+      if (pass == kWrite && ns > 1) {
+        u.slot = atomicAdd(&s.slots, ns);
+        p.groups[atomicAdd(&s.groups, 1)] = VarGroup{u.q0, u.nq, u.slot, ns};
+      }
+      for (int k = 0; k < ns; ++k) {
+        u.j0 = n * k / ns;
+        u.j1 = n * (k + 1) / ns;
+        const int bin = cost_bin(u.j1 - u.j0, p.cost_shift);
+        const int at = atomicAdd(&s.bins[pass == kWrite ? bin : bin + 1], 1);
+        if (pass == kWrite && at < p.max_units) p.units[at] = u;
+        if (ns > 1) ++u.slot;
+      }
+    };
+    if (one_pass) {
+      if (has) visit(mine);
+      __syncthreads();
+    } else {
+      for_each_block(p, s, pass == kCount, [&](const VarUnit& u) {
+        mine = u;
+        has = true;
+        visit(u);
       });
+      one_pass = p.B <= kPlanThreads && s.scan.off[p.B] <= kPlanThreads;
+    }
+    if (pass == kTry) {
+      if (tid == 0) {
+        float best = 0.f;
+        for (int c = 0; c < kCandidates; ++c) {
+          const int S = (n_max + c) / (c + 1), items = s.units[c] * p.Hkv;
+          if (c > 0 && (S < 4 || items > kVarMaxSplit || s.units[c] > p.max_units)) break;
+          const float mean = static_cast<float>(s.cost) / s.units[c];
+          float est = fmaxf(S + 4.f, ((items + sms - 1) / sms) * (mean + 4.f));
+          if (c > 0) est += 8.f;
+          if (c == 0 || est < best) {
+            best = est;
+            s.split = c == 0 ? INT_MAX : S;
+          }
+        }
+      }
+      __syncthreads();
     }
   }
-  const int units = scan_bins(s.scan, s.bins);
-  if (tid == 0) {  // more than fit only when starts overlap, which no packed rows have
-    p.hdr->units = min(units, p.max_units);
-    if (units > p.max_units) atomicOr(p.m.status, FA_DEV_BAD_PAGE);
-  }
-  const int split = s.split;
-  every_unit([&](VarUnit u) {
-    const int n = u.j1, ns = split == INT_MAX ? 1 : max(1, (n + split - 1) / split);
-    if (ns > 1) {
-      u.slot = atomicAdd(&s.slots, ns);
-      p.groups[atomicAdd(&s.groups, 1)] = VarGroup{u.q0, u.nq, u.slot, ns};
-    }
-    for (int k = 0; k < ns; ++k) {
-      u.j0 = n * k / ns;
-      u.j1 = n * (k + 1) / ns;
-      const int at = atomicAdd(&s.bins[bin_of(u.j1 - u.j0, p)], 1);
-      if (at < p.max_units) p.units[at] = u;
-      if (ns > 1) ++u.slot;
-    }
-  });
   if (tid == 0) p.hdr->groups = s.groups;
 }
 
@@ -302,34 +302,53 @@ struct Bars {
   uint32_t abort;
 };
 
-// Item t of the launch: its unit and K/V head.
+// A work item: its unit, K/V head, visited key blocks, and tiles (1 when the second has no token).
 struct Item {
   VarUnit u;
   int kvh;
   Range rg;
-  int tiles;  // 2, or 1 when the second tile has no token
+  int tiles;
 };
 
-// The k-th item of this CTA (false when there is none left). Snake order over a list sorted
-// by cost: round r covers items r G .. r G + G - 1, backwards on odd rounds.
-__device__ __forceinline__ bool next_item(const VarParams& p, int total, int& k, Item& it) {
-  const int G = gridDim.x;
-  while (k * G < total) {
-    const int t = item_of_round(k, G, blockIdx.x);
-    ++k;
-    if (t >= total) continue;
-    const int4* src = reinterpret_cast<const int4*>(p.units + t / p.Hkv);
-    const int4 a = src[0], b = src[1], c = src[2];
+// The items of this CTA one after the other, in snake order over a list sorted by cost: round r
+// covers items r G .. r G + G - 1, backwards on odd rounds. The words of the item to come are
+// loaded while the present one is worked on.
+struct Items {
+  int total, round, t;  // t: the item whose words are in a, b, slot; total when there is none
+  int4 a, b;
+  int slot;
+  __device__ __forceinline__ void fetch(const VarParams& p) {
+    const int G = gridDim.x;
+    t = total;
+    while (round * G < total) {
+      const int x = item_of_round(round++, G, blockIdx.x);
+      if (x < total) {
+        t = x;
+        break;
+      }
+    }
+    if (t < total) {
+      const int4* src = reinterpret_cast<const int4*>(p.units + t / p.Hkv);
+      a = src[0];
+      b = src[1];
+      slot = src[2].x;
+    }
+  }
+  __device__ __forceinline__ Items(const VarParams& p, int total) : total(total), round(0) {
+    fetch(p);
+  }
+  __device__ __forceinline__ bool next(const VarParams& p, Item& it) {
+    if (t >= total) return false;
     it.u.q0 = a.x, it.u.nq = a.y, it.u.sk = a.z, it.u.k0 = a.w;
     it.u.qpos = b.x, it.u.seq = b.y, it.u.j0 = b.z, it.u.j1 = b.w;
-    it.u.slot = c.x;
+    it.u.slot = slot;
     it.kvh = t - (t / p.Hkv) * p.Hkv;
     it.rg = blocks_seen(it.u.qpos, it.u.qpos + it.u.nq, it.u.sk, p.m);
     it.tiles = it.u.nq > p.TPT ? 2 : 1;
+    fetch(p);
     return true;
   }
-  return false;
-}
+};
 
 // One row of one S tile by one thread: mask, running maximum, lazy rescale of O and l (only
 // when the maximum rose by more than kTau; decided per warp), P = 2^(S sl2 - m) rounded to 16
@@ -451,9 +470,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       Item it;
       const uint32_t q_bytes = static_cast<uint32_t>(p.TPT * p.G) * D * 2;
-      for (int k = 0; ok && next_item(p, total, k, it);) {
+      for (Items items(p, total); ok && items.next(p, it);) {
         if (it.u.j1 == it.u.j0) continue;
-        for (int q = 0; q < it.tiles && ok; ++q) {
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          if (q >= it.tiles) break;
           if (iq[q] > 0 && !(ok = mbar_wait(B(bars->q_empty[q]), (iq[q] - 1) & 1, wc))) break;
           if (leader) {
             mbar_arrive_expect_tx(B(bars->q_full[q]), q_bytes);
@@ -526,13 +547,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         issue_qk<D, BN, BF16>(tS[q], sQ + q * C::Q_BYTES, sRing + slot * C::TILE_BYTES);
         umma_commit(B(bars->s_full[q]));
       };
-      for (int k = 0; ok && next_item(p, total, k, it);) {
+      for (Items items(p, total); ok && items.next(p, it);) {
         const int n = it.u.j1 - it.u.j0, last = it.tiles - 1;
         if (n == 0) continue;
         {
           const int slot = pos % C::NSLOT;
           if (!(ok = mbar_wait(B(bars->full[slot]), (pos / C::NSLOT) & 1, wc))) break;
-          for (int q = 0; q < it.tiles && ok; ++q) {
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            if (q >= it.tiles) break;
             if (!(ok = mbar_wait(B(bars->q_full[q]), iq[q] & 1, wc))) break;
             tc_fence_after();
             if (leader) {
@@ -558,7 +581,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
           }
           tc_fence_after();
-          for (int q = 0; q < it.tiles && ok; ++q) {
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            if (q >= it.tiles) break;
             if (!(ok = mbar_wait(B(bars->p_full[q]), tc[q] & 1, wc))) break;
             ++tc[q];
             tc_fence_after();
@@ -585,7 +610,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           pos += (j + 1 < n) ? 2 : 1;
         }
-        for (int q = 0; q < it.tiles; ++q) ++iq[q];
+        ++iq[0];
+        if (it.tiles > 1) ++iq[1];
       }
       if (leader) umma_commit(B(bars->final_mma));  // all MMAs done before TMEM is released
       mbar_wait_quiet(B(bars->final_mma), 0, wc);
@@ -605,7 +631,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t ii = 0, tc = 0;
   bool ok = true;
   Item it;
-  for (int k = 0; ok && next_item(p, total, k, it);) {
+  for (Items items(p, total); ok && items.next(p, it);) {
     if (q >= it.tiles) continue;
     const int n = it.u.j1 - it.u.j0;
     const int left = it.u.nq - q * p.TPT;  // tokens of this tile and behind it
@@ -708,14 +734,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // One warp per row: M = max m_s, O = sum 2^(m_s - M) O_s / sum 2^(m_s - M) l_s over the
 // group's slots in order.
+constexpr int kMergeThreads = 512;
 template <int D, bool BF16>
-__global__ void __launch_bounds__(256) var_merge_kernel(const VarParams p) {
+__global__ void __launch_bounds__(kMergeThreads) var_merge_kernel(const VarParams p) {
   constexpr int E = D / 32;  // elements per lane
   const int lane = threadIdx.x % 32;
-  const int warps = gridDim.x * 8, per = p.Hkv * kVarSplitRows;
+  const int warps = gridDim.x * (kMergeThreads / 32), per = p.Hkv * kVarSplitRows;
   const int total = p.hdr->groups * per;
   const size_t step = static_cast<size_t>(p.Hkv) * kVarSplitRows * (D + 2);
-  for (int w = blockIdx.x * 8 + threadIdx.x / 32; w < total; w += warps) {
+  for (int w = blockIdx.x * (kMergeThreads / 32) + threadIdx.x / 32; w < total; w += warps) {
     const VarGroup g = p.groups[w / per];
     const int kvh = (w % per) / kVarSplitRows, r = w % kVarSplitRows;
     const int tok = (r / kTile) * p.TPT + (r % kTile) / p.G;
@@ -763,7 +790,7 @@ cudaError_t launch_t(const VarLaunch& L, cudaStream_t stream) {
   const int grid = static_cast<int>(items < L.sms ? items : L.sms);
   k<<<grid, kThreads, smem, stream>>>(L.tmQ, L.tmK, L.tmV, L.p);
   if ((e = cudaGetLastError()) != cudaSuccess || !L.p.part) return e;
-  var_merge_kernel<D, BF16><<<L.sms * 8, 256, 0, stream>>>(L.p);
+  var_merge_kernel<D, BF16><<<L.sms * 2, kMergeThreads, 0, stream>>>(L.p);
   return cudaGetLastError();
 }
 

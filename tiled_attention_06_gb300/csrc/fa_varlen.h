@@ -156,6 +156,12 @@ cudaError_t launch_bwd_varlen(const VarBwdLaunch& L, int D, bool bf16, cudaStrea
 // dealt to the CTAs in equal runs, whatever the lengths.
 constexpr int kFewRows = 64;
 constexpr int kFewMaxCtas = 320;
+// A pair (sequence, K/V head) whose first piece CTA x holds: its first row of q, rows, K/V head,
+// and the CTA of its last piece; rows = 0: none.
+struct FewHead {
+  int32_t q0, rows, kvh, last;
+};
+constexpr size_t kFewHeadBytes = kFewMaxCtas * sizeof(FewHead);
 inline size_t few_part_floats(int rows, int d) {  // a CTA leaves at most two partial results
   return static_cast<size_t>(2) * kFewMaxCtas * rows * (d + 2);
 }
@@ -171,6 +177,7 @@ struct FewParams {
   const int32_t* block_table;
   int B, H, Hkv, G, total_q, max_q;
   int page_size, max_pages, num_pages, box;  // box: rows of one TMA box (<= 64)
+  FewHead* heads;  // [CTAs]
   float* part;  // [2 CTAs][rows][D], then m [2 CTAs][rows], l [2 CTAs][rows]
 };
 

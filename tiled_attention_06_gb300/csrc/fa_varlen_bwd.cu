@@ -148,27 +148,34 @@ __global__ void __launch_bounds__(kPlanThreads) bwd_plan_kernel(const VarBwdPara
   __shared__ BwdPlanSmem s;
   for (int i = threadIdx.x; i <= kBins; i += kPlanThreads) s.bins[i] = 0;
   __syncthreads();
-  // the last unit a thread has seen; all of them when there are no more units than threads
+  // two passes, counting and writing, that share one copy of the code; units stay in registers
+  // when there are no more of them than threads
   VarBwdUnit mine;
-  bool has = false;
-  for_each_key_block(p, s, true, [&](const VarBwdUnit& u) {
-    mine = u;
-    has = true;
-    atomicAdd(&s.bins[cost_bin(u.n, p.cost_shift) + 1], 1);
-  });
-  const bool one_pass = p.B <= kPlanThreads && s.scan.off[p.B] <= kPlanThreads;
-  const int units = scan_bins(s.scan, s.bins);
-  auto put = [&](const VarBwdUnit& u) {
-    const int at = atomicAdd(&s.bins[cost_bin(u.n, p.cost_shift)], 1);
-    if (at < p.max_units) p.units[at] = u;
-  };
-  if (!one_pass)
-    for_each_key_block(p, s, false, put);
-  else if (has)
-    put(mine);
-  if (threadIdx.x == 0) {  // more than fit only when starts overlap, which no packed rows have
-    p.n_units[0] = min(units, p.max_units);
-    if (units > p.max_units) atomicOr(p.m.status, FA_DEV_BAD_PAGE);
+  bool has = false, one_pass = false;
+#pragma unroll 1
+  for (int pass = 0; pass < 2; ++pass) {
+    if (pass == 1) {
+      const int units = scan_bins(s.scan, s.bins);
+      if (threadIdx.x == 0) {  // more than fit only when starts overlap, which no packed rows have
+        p.n_units[0] = min(units, p.max_units);
+        if (units > p.max_units) atomicOr(p.m.status, FA_DEV_BAD_PAGE);
+      }
+    }
+    auto visit = [&](const VarBwdUnit& u) {
+      const int bin = cost_bin(u.n, p.cost_shift);
+      const int at = atomicAdd(&s.bins[pass ? bin : bin + 1], 1);
+      if (pass && at < p.max_units) p.units[at] = u;
+    };
+    if (one_pass) {
+      if (has) visit(mine);
+    } else {
+      for_each_key_block(p, s, pass == 0, [&](const VarBwdUnit& u) {
+        mine = u;
+        has = true;
+        visit(u);
+      });
+      one_pass = p.B <= kPlanThreads && s.scan.off[p.B] <= kPlanThreads;
+    }
   }
 }
 
