@@ -536,7 +536,7 @@ size_t fa_bwd_varlen_workspace_size(int B, int H, int Hkv, int total_q, int tota
  *   q, o [total_q, H, d]; lse [total_q, H] float32 or NULL
  *   pools [num_pages, Hkv, page_size, d]; block_table int32 [B, max_pages_per_seq];
  *   ctx_lens int32 [B]; page_size a multiple of 16 in [16, 4096]
- *   max_q      at least the longest chunk; up to 64 / (H / Hkv) tokens the call runs a kernel
+ *   max_q      at least the longest chunk; up to 16 / (H / Hkv) tokens the call runs a kernel
  *              for few rows. Rows of a chunk from max_q on may be left as they were, which is
  *              reported as FA_ERR_BAD_PAGE
  *   everything else as for fa_fwd_varlen; the workspace has fa_paged_varlen_workspace_size(...)

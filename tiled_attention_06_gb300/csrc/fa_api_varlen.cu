@@ -152,11 +152,9 @@ BwdLayout bwd_layout(int B, int H, int Hkv, int total_q, int total_k, int d) {
   return L;
 }
 
-// Rows (a multiple of 16) that the kernel for few rows is built with for chunks of up to max_q
-// tokens, 0 when they are too many for it.
-int few_rows(int max_q, int G) {
-  const long long rows = static_cast<long long>(std::max(max_q, 1)) * G;
-  return rows > fa::kFewRows ? 0 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+// Chunks of up to max_q tokens are few rows (fa_few.cu).
+bool few_rows(int max_q, int G) {
+  return static_cast<long long>(std::max(max_q, 1)) * G <= fa::kFewRows;
 }
 
 fa_status check_workspace(const void* ws, size_t bytes, size_t need) {
@@ -449,9 +447,8 @@ size_t fa_paged_varlen_workspace_size(int B, int H, int Hkv, int total_q, int ma
   (void)page_size;
   if (B < 1 || Hkv < 1 || H < Hkv || H % Hkv || H / Hkv > 128 || total_q < 0 || max_q < 0 || d < 1)
     return 0;
-  const int rows = few_rows(max_q, H / Hkv);
-  return rows ? fa::kFewHeadBytes + fa::few_part_floats(rows, d) * sizeof(float)
-              : var_layout(B, H, Hkv, total_q, d).total;
+  return few_rows(max_q, H / Hkv) ? fa::kFewHeadBytes + fa::few_part_floats(d) * sizeof(float)
+                                  : var_layout(B, H, Hkv, total_q, d).total;
 }
 
 fa_status fa_fwd_paged_varlen(const fa_paged_varlen_params* params, fa_stream_t stream) {
@@ -489,7 +486,7 @@ fa_status fa_fwd_paged_varlen(const fa_paged_varlen_params* params, fa_stream_t 
   const long long planes = static_cast<long long>(a.num_pages) * a.Hkv;
   const long long plane = static_cast<long long>(a.page_size) * a.d;
   const int pow2 = a.page_size & -a.page_size;
-  if (const int rows = few_rows(a.max_q, a.H / a.Hkv)) {
+  if (few_rows(a.max_q, a.H / a.Hkv)) {
     fa::FewLaunch F;
     std::memset(&F, 0, sizeof F);
     fa::FewParams& p = F.p;
@@ -521,7 +518,7 @@ fa_status fa_fwd_paged_varlen(const fa_paged_varlen_params* params, fa_stream_t 
     if ((st = make_map3(&F.tmV, a.v_pages, bf16, a.d, a.page_size, a.d, planes, plane, p.box,
                         1)) != FA_OK)
       return st;
-    const cudaError_t e = fa::launch_few(F, a.d, bf16, rows, cs);
+    const cudaError_t e = fa::launch_few(F, a.d, bf16, cs);
     if (e != cudaSuccess) return cuda_fail(e, "paged packed attention launch");
     return FA_OK;
   }

@@ -1,18 +1,19 @@
 // Attention of a few new rows over a paged cache with grouped heads, for sm_103a: a decode
-// step, or a handful of drafted tokens. The rows of a sequence and K/V head are its tokens times
-// the G query heads that share the head (row r: token r / G, head r % G); at most 64.
+// step, or a couple of drafted tokens. The rows of a sequence and K/V head are its tokens times
+// the G query heads that share the head (row r: token r / G, head r % G); at most 16.
 //
 // Bound by reading K and V once: 4 d bytes per key and K/V head against 4 d G multiply-adds per
 // token, which the FP32 pipes cannot keep up with from G = 4 or so, hence warp-level tensor-core
-// MMAs (m16n8k16: 16 rows are its natural tile; a tcgen05 tile would be 128 rows, 4 to 32 times
-// more than there are, and its softmax would serialise on one warp).
+// MMAs (m16n8k16, whose 16 rows fit; at 6.2 TB/s their pipe is 16 % busy). With 32 or 64 rows
+// this form was bound by the latency of its MMAs (40 rows over 84,000 keys x 4 heads: 49 us
+// where the memory needs 26), and the 128-row tiles of fa_varlen.cu take over.
 //
 // few_kernel, two CTAs per SM, each four compute warps and a TMA warp. The 64-key tiles of all
 // (sequence, K/V head) pairs are numbered end to end and CTA x takes an equal run of them, so
-// ragged lengths cost no balance. A run's piece of one pair is a segment: a whole pair is
-// written to o, a piece to the workspace. The four warps are MT row groups of 16 rows times
-// 4 / MT key groups of the tile; each keeps its own running maximum, sum and output in
-// registers, joined through shared memory at the end of a segment.
+// ragged lengths cost no balance. A run's piece of one pair is a segment: a whole pair is written
+// to o, a piece to the workspace. A warp takes 16 keys of every tile and keeps its own running
+// maximum, sum and output in registers; the four are joined through shared memory at the end of
+// a segment.
 // few_merge_kernel joins the pieces of each pair in the order of the keys; the CTA that holds a
 // pair's first piece leaves word of where the others are.
 #include <cuda_bf16.h>
@@ -29,7 +30,9 @@ namespace fa {
 namespace {
 
 constexpr int BK = 64;              // keys per tile
-constexpr int kCompute = 128;       // compute threads
+constexpr int ROWS = kFewRows;      // rows of a warp's tile
+constexpr int NW = 4;               // compute warps; the next one loads
+constexpr int kCompute = 32 * NW;
 constexpr int kThreads = kCompute + 32;
 constexpr float kTau = 8.0f;        // lazy-rescale threshold, log2 units
 
@@ -51,6 +54,8 @@ struct Cfg {
 struct Bars {
   uint64_t full[8], empty[8];
   int64_t sum[4];   // scratch of tile_totals
+  int64_t all;      // tiles of the call, and the CTAs that share them
+  int used;
   int first[2];     // sequence of the CTA's first tile, tile within it (all K/V heads)
   uint32_t abort;
 };
@@ -84,7 +89,9 @@ __device__ __forceinline__ void mma(float* c, const uint32_t* a, uint32_t b0, ui
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ void compute_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ void compute_sync() {
+  asm volatile("bar.sync 1, %0;" ::"n"(kCompute) : "memory");
+}
 
 // One sequence: its rows, keys and the tiles that the mask lets its queries see.
 struct FewSeq {
@@ -156,21 +163,18 @@ __device__ __forceinline__ int ctas_used(int64_t tiles, int grid) {
 
 // A walk over the tiles [t, end) of this CTA: one segment after the other.
 struct Walk {
-  int b, kvh, j;
-  int64_t left;
+  int b, kvh, j, left;
   FewSeq s;
 };
 
-template <int D, bool BF16, int MT>
+template <int D, bool BF16>
 __global__ void __launch_bounds__(kThreads, 2)
     few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                const __grid_constant__ FewParams p) {
   using C = Cfg<D>;
-  constexpr int KW = 4 / MT;      // key groups
-  constexpr int KPW = BK / KW;    // keys of a warp per tile
+  constexpr int KPW = BK / NW;    // keys of a warp per tile
   constexpr int NT = KPW / 8;     // 8-key columns of S
   constexpr int NO = D / 8;       // 8-element columns of O
-  constexpr int ROWS = 16 * MT;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t base = smem_u32(smem);
   float* comb = reinterpret_cast<float*>(smem + C::NST * 2 * C::TILE);
@@ -186,12 +190,12 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::NST; ++i) {
       mbar_init(B(bars->full[i]), 1);
-      mbar_init(B(bars->empty[i]), 4);
+      mbar_init(B(bars->empty[i]), NW);
     }
     bars->abort = 0;
     mbar_fence_init();
   }
-  if (warp == 4 && lane == 0) {
+  if (warp == NW && lane == 0) {
     tma_prefetch_desc(&tmK);
     tma_prefetch_desc(&tmV);
   }
@@ -199,6 +203,10 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int64_t all = tot.all * p.Hkv;
   const int used = ctas_used(all, gridDim.x);
   const bool idle = static_cast<int>(blockIdx.x) >= used || all == 0;
+  if (threadIdx.x == 0) {
+    bars->all = all;
+    bars->used = used;
+  }
   const int64_t begin = idle ? 0 : all * blockIdx.x / used;
   const int64_t end = idle ? 0 : all * (blockIdx.x + 1) / used;
   // the thread whose share holds the first tile finds its sequence
@@ -234,7 +242,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   w.s = few_seq(p, w.b, false);
   w.kvh = bars->first[1] / w.s.tiles;
   w.j = bars->first[1] - w.kvh * w.s.tiles;
-  w.left = end - begin;
+  w.left = static_cast<int>(end - begin);
   // step to the segment after one of `done` tiles
   auto advance = [&](int done) {
     w.left -= done;
@@ -247,7 +255,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   };
   const WaitCtx wc{&bars->abort, p.m.status, p.m.timeout_ns};
 
-  if (warp == 4) {
+  if (warp == NW) {
     // -------------------------------------------------------------- TMA
     // lane = (K or V, 64-element region of d, box of the tile)
     const bool leader = elect_one();
@@ -256,7 +264,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     uint32_t pos = 0, fills[8] = {0, 0, 0, 0, 0, 0, 0, 0};
     bool ok = true;
     while (w.left > 0 && ok) {
-      const int cnt = static_cast<int>(min(w.left, static_cast<int64_t>(w.s.tiles - w.j)));
+      const int cnt = min(w.left, w.s.tiles - w.j);
       for (int j = w.j; j < w.j + cnt && ok; ++j, ++pos) {
         const int n0 = tile_at(w.s.rg, j) * BK;
         const int boxes = (min(BK, w.s.sk - n0) + p.box - 1) / p.box;
@@ -294,23 +302,22 @@ __global__ void __launch_bounds__(kThreads, 2)
     return;
   }
   // ---------------------------------------------------------------- compute
-  const int rw = warp % MT, kw = warp / MT;  // row group, key group
-  const int r0 = rw * 16 + lane / 4;         // this thread's rows: r0 and r0 + 8
+  const int kw = warp, r0 = lane / 4;  // key group; this thread's rows are r0 and r0 + 8
   const int cq = lane % 4;
   uint32_t pos = 0;
   while (w.left > 0) {
-    const int cnt = static_cast<int>(min(w.left, static_cast<int64_t>(w.s.tiles - w.j)));
+    const int cnt = min(w.left, w.s.tiles - w.j);
     const int rows = w.s.n * p.G;
     // Q fragments straight from global memory (rows past the chunk are zero)
     uint32_t qf[D / 16][4];
-    int tok[2], head[2];
+    int tok[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int r = r0 + 8 * i;
       tok[i] = r / p.G;
-      head[i] = w.kvh * p.G + r - tok[i] * p.G;
       const uint16_t* src = static_cast<const uint16_t*>(p.q) +
-                            static_cast<int64_t>(w.s.q0 + tok[i]) * p.q_token + head[i] * D + 2 * cq;
+                            static_cast<int64_t>(w.s.q0 + tok[i]) * p.q_token +
+                            (w.kvh * p.G + r - tok[i] * p.G) * D + 2 * cq;
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
         qf[kk][i] = r < rows ? *reinterpret_cast<const uint32_t*>(src + 16 * kk) : 0u;
@@ -326,10 +333,6 @@ __global__ void __launch_bounds__(kThreads, 2)
       const int n0 = tile_at(w.s.rg, j) * BK;
       const int st = pos % C::NST;
       if (!mbar_wait(B(bars->full[st]), (pos / C::NST) & 1, wc)) return;
-      if (16 * rw >= rows) {  // no row of this group: only keep step
-        if (lane == 0) mbar_arrive(B(bars->empty[st]));
-        continue;
-      }
       const uint32_t sK = base + 2 * st * C::TILE, sV = sK + C::TILE;
       const int live = w.s.sk - n0;
       float s[NT][4];
@@ -366,26 +369,29 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (!full) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const long long at = static_cast<long long>(w.s.qpos) + tok[i];
-          long long lim = min(at, static_cast<long long>(w.s.sk - 1)), lo = LLONG_MIN;
-          int gl = INT_MIN;
-          if (p.m.mask_mode == FA_MASK_NONE) lim = w.s.sk - 1;
+          // keys of the tile that the row sees: up to lim, and from lo on or below gl
+          const long long at = static_cast<long long>(w.s.qpos) + tok[i] - n0;
+          const int last = w.s.sk - 1 - n0, wide = p.m.window;
+          long long hi = at, from = -1;
+          int gl = 0;
+          if (p.m.mask_mode == FA_MASK_NONE) hi = BK;
           if (p.m.mask_mode == FA_MASK_CAUSAL_WINDOW) {
-            lo = at - p.m.window + 1;
-            gl = p.m.n_global;
+            from = at - wide + 1;
+            gl = p.m.n_global - n0;
           }
           if (p.m.mask_mode == FA_MASK_BAND) {
-            lim = min(at + p.m.window, static_cast<long long>(w.s.sk - 1));
-            lo = at - p.m.window;
+            hi = at + wide;
+            from = at - wide;
           }
           if (p.m.mask_mode == FA_MASK_PREFIX_LM)
-            lim = min(max(at, static_cast<long long>(p.m.n_global) - 1),
-                      static_cast<long long>(w.s.sk - 1));
+            hi = max(at, static_cast<long long>(p.m.n_global) - 1 - n0);
+          const int lim = min(static_cast<int>(max(-1ll, min(hi, static_cast<long long>(BK)))), last);
+          const int lo = static_cast<int>(max(-1ll, min(from, static_cast<long long>(BK))));
 #pragma unroll
           for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const int key = n0 + kw * KPW + 8 * t + 2 * cq + e;
+              const int key = kw * KPW + 8 * t + 2 * cq + e;
               if (!(key <= lim && (key >= lo || key < gl))) s[t][2 * i + e] = -INFINITY;
             }
         }
@@ -462,13 +468,13 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     // join the key groups: the upper half hands its state to the lower, until one is left
 #pragma unroll
-    for (int half = KW / 2; half >= 1; half /= 2) {
+    for (int half = NW / 2; half >= 1; half /= 2) {
       if (kw >= half && kw < 2 * half) {
-        float* dst = comb + ((kw - half) * MT + rw) * 16 * D;
-        float* sd = states + ((kw - half) * MT + rw) * 32;
+        float* dst = comb + (kw - half) * 16 * D;
+        float* sd = states + (kw - half) * 32;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const int r = lane / 4 + 8 * i;
+          const int r = r0 + 8 * i;
 #pragma unroll
           for (int t = 0; t < NO; ++t)
             *reinterpret_cast<float2*>(dst + r * D + 8 * t + 2 * cq) =
@@ -481,15 +487,14 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
       compute_sync();
       if (kw < half) {
-        const float* src = comb + (kw * MT + rw) * 16 * D;
-        const float* sd = states + (kw * MT + rw) * 32;
+        const float* src = comb + kw * 16 * D;
+        const float* sd = states + kw * 32;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const int r = lane / 4 + 8 * i;
-          const float m2 = sd[r], l2 = sd[16 + r];
-          const float M = fmaxf(m[i], m2), mu = M == -INFINITY ? 0.f : M;
+          const int r = r0 + 8 * i;
+          const float m2 = sd[r], M = fmaxf(m[i], m2), mu = M == -INFINITY ? 0.f : M;
           const float a = ex2_approx(m[i] - mu), b = ex2_approx(m2 - mu);
-          l[i] = l[i] * a + l2 * b;
+          l[i] = l[i] * a + sd[16 + r] * b;
           m[i] = M;
 #pragma unroll
           for (int t = 0; t < NO; ++t) {
@@ -508,26 +513,28 @@ __global__ void __launch_bounds__(kThreads, 2)
       const int nslots = 2 * gridDim.x;
       if (!whole && w.j == 0 && threadIdx.x == 0) {
         // the piece that starts a pair says where the rest is: CTAs on to that of its last tile
-        const int64_t last = end - w.left + w.s.tiles - 1;  // end - left: the segment's first tile
+        const int64_t n = bars->all, own_end = n * (blockIdx.x + 1) / bars->used;
+        const int64_t last = own_end - w.left + w.s.tiles - 1;
         int x = blockIdx.x + 1;
-        while (all * (x + 1) / used <= last) ++x;
+        while (n * (x + 1) / bars->used <= last) ++x;
         p.heads[blockIdx.x] = FewHead{w.s.q0, rows, w.kvh, x};
       }
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int r = r0 + 8 * i;
         if (r >= rows) continue;
+        const int head = w.kvh * p.G + r - tok[i] * p.G;
         if (whole) {
           const float inv = l[i] > 0.f ? 1.f / l[i] : 0.f;
           uint16_t* dst = static_cast<uint16_t*>(p.o) +
-                          static_cast<int64_t>(w.s.q0 + tok[i]) * p.o_token + head[i] * D + 2 * cq;
+                          static_cast<int64_t>(w.s.q0 + tok[i]) * p.o_token + head * D + 2 * cq;
 #pragma unroll
           for (int t = 0; t < NO; ++t) {
             const float a = o[t][2 * i] * inv, b = o[t][2 * i + 1] * inv;
             *reinterpret_cast<uint32_t*>(dst + 8 * t) = BF16 ? cvt_pack_bf16(a, b) : cvt_pack_f16(a, b);
           }
           if (cq == 0 && p.lse)
-            p.lse[static_cast<size_t>(w.s.q0 + tok[i]) * p.H + head[i]] =
+            p.lse[static_cast<size_t>(w.s.q0 + tok[i]) * p.H + head] =
                 l[i] > 0.f ? (m[i] + lg2_approx(l[i])) * 0.69314718055994531f : -INFINITY;
         } else {
           float* dst = p.part + (static_cast<size_t>(slot) * ROWS + r) * D + 2 * cq;
@@ -546,97 +553,106 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
 }
 
-// CTA (x, z): the pair whose first piece CTA x of few_kernel holds, every gridDim.y-th row. Four
-// warps take every fourth piece of a row.
-template <int D, bool BF16, int MT>
+// CTA (x, y): row y of the pair whose first piece CTA x of few_kernel holds. A warp's lanes hold
+// the pieces' maxima and sums, so the weights are known before the outputs are read; the four
+// warps take every fourth piece.
+template <int D, bool BF16>
 __global__ void __launch_bounds__(kCompute) few_merge_kernel(const FewParams p) {
-  constexpr int E = D / 32, ROWS = 16 * MT;
-  __shared__ float s_ml[4][2], s_acc[4][D];
-  const int x0 = blockIdx.x, nslots = 2 * gridDim.x;
+  constexpr int E = D / 32;
+  __shared__ float s_acc[4][D];
+  const int x0 = blockIdx.x, nslots = 2 * gridDim.x, r = blockIdx.y;
   const FewHead hd = p.heads[x0];
+  if (r >= hd.rows) return;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const float* ml = p.part + static_cast<size_t>(nslots) * ROWS * D;
-  for (int r = blockIdx.y; r < hd.rows; r += gridDim.y) {
-    float M = -INFINITY, L = 0.f, acc[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = 0.f;
-#pragma unroll 4
-    for (int x = x0 + warp; x <= hd.last; x += 4) {
-      const int slot = 2 * x + (x == x0 ? 1 : 0);
-      const float m = ml[slot * ROWS + r], l = ml[(nslots + slot) * ROWS + r];
-      const float* src = p.part + (static_cast<size_t>(slot) * ROWS + r) * D + lane * E;
-      float v[E];
-#pragma unroll
-      for (int e = 0; e < E; ++e) v[e] = src[e];
-      const float mn = fmaxf(M, m), mu = mn == -INFINITY ? 0.f : mn;
-      const float c = ex2_approx(M - mu), wt = ex2_approx(m - mu);
-      L = L * c + l * wt;
-#pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] = acc[e] * c + v[e] * wt;
-      M = mn;
+  auto slot_of = [&](int x) { return 2 * x + (x == x0 ? 1 : 0); };
+  // maximum and sum over the pieces, one per lane; loads before their uses throughout
+  float M = -INFINITY, L = 0.f;
+  for (int x1 = x0; x1 <= hd.last; x1 += 32) {
+    const int x = x1 + lane;
+    float m = -INFINITY, l = 0.f;
+    if (x <= hd.last) {
+      m = ml[slot_of(x) * ROWS + r];
+      l = ml[(nslots + slot_of(x)) * ROWS + r];
     }
-    if (lane == 0) {
-      s_ml[warp][0] = M;
-      s_ml[warp][1] = L;
-    }
+    float mx = fmaxf(M, m);
 #pragma unroll
-    for (int e = 0; e < E; ++e) s_acc[warp][lane * E + e] = acc[e];
-    __syncthreads();
-    float Ma = -INFINITY;
-    for (int i = 0; i < 4; ++i) Ma = fmaxf(Ma, s_ml[i][0]);
-    const float mu = Ma == -INFINITY ? 0.f : Ma;
-    float La = 0.f, wts[4];
-    for (int i = 0; i < 4; ++i) {
-      wts[i] = ex2_approx(s_ml[i][0] - mu);
-      La += s_ml[i][1] * wts[i];
-    }
-    const int tok = r / p.G, h = hd.kvh * p.G + r - tok * p.G;
-    const float inv = La > 0.f ? 1.f / La : 0.f;
-    uint16_t* out =
-        static_cast<uint16_t*>(p.o) + static_cast<int64_t>(hd.q0 + tok) * p.o_token + h * D;
-    for (int e = 2 * threadIdx.x; e < D; e += 2 * kCompute) {
-      float a = 0.f, c = 0.f;
-      for (int i = 0; i < 4; ++i) {
-        a += s_acc[i][e] * wts[i];
-        c += s_acc[i][e + 1] * wts[i];
-      }
-      *reinterpret_cast<uint32_t*>(out + e) =
-          BF16 ? cvt_pack_bf16(a * inv, c * inv) : cvt_pack_f16(a * inv, c * inv);
-    }
-    if (threadIdx.x == 0 && p.lse)
-      p.lse[static_cast<size_t>(hd.q0 + tok) * p.H + h] =
-          La > 0.f ? (Ma + lg2_approx(La)) * 0.69314718055994531f : -INFINITY;
-    __syncthreads();
+    for (int o = 16; o > 0; o /= 2) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    const float mu = mx == -INFINITY ? 0.f : mx;
+    l *= ex2_approx(m - mu);
+#pragma unroll
+    for (int o = 16; o > 0; o /= 2) l += __shfl_xor_sync(0xffffffffu, l, o);
+    L = L * ex2_approx(M - mu) + l;
+    M = mx;
   }
+  const float mu = M == -INFINITY ? 0.f : M;
+  float acc[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) acc[e] = 0.f;
+  constexpr int N = 6;  // pieces of this warp in flight
+  for (int x1 = x0 + warp; x1 <= hd.last; x1 += 4 * N) {
+    float m[N], v[N][E];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int x = x1 + 4 * i;
+      m[i] = -INFINITY;
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[i][e] = 0.f;
+      if (x <= hd.last) {
+        const int s = slot_of(x);
+        m[i] = ml[s * ROWS + r];
+        const float* src = p.part + (static_cast<size_t>(s) * ROWS + r) * D + lane * E;
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[i][e] = src[e];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float w = ex2_approx(m[i] - mu);
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] = fmaf(w, v[i][e], acc[e]);
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < E; ++e) s_acc[warp][lane * E + e] = acc[e];
+  __syncthreads();
+  const int tok = r / p.G, h = hd.kvh * p.G + r - tok * p.G;
+  const float inv = L > 0.f ? 1.f / L : 0.f;
+  uint16_t* out =
+      static_cast<uint16_t*>(p.o) + static_cast<int64_t>(hd.q0 + tok) * p.o_token + h * D;
+  for (int e = 2 * threadIdx.x; e < D; e += 2 * kCompute) {
+    float a = 0.f, c = 0.f;
+    for (int k = 0; k < 4; ++k) {
+      a += s_acc[k][e];
+      c += s_acc[k][e + 1];
+    }
+    *reinterpret_cast<uint32_t*>(out + e) =
+        BF16 ? cvt_pack_bf16(a * inv, c * inv) : cvt_pack_f16(a * inv, c * inv);
+  }
+  if (threadIdx.x == 0 && p.lse)
+    p.lse[static_cast<size_t>(hd.q0 + tok) * p.H + h] =
+        L > 0.f ? (M + lg2_approx(L)) * 0.69314718055994531f : -INFINITY;
 }
 
-template <int D, bool BF16, int MT>
-cudaError_t launch_mt(const FewLaunch& L, cudaStream_t stream) {
+template <int D, bool BF16>
+cudaError_t launch_t(const FewLaunch& L, cudaStream_t stream) {
   const int grid = 2 * L.sms < kFewMaxCtas ? 2 * L.sms : kFewMaxCtas;
-  auto* k = few_kernel<D, BF16, MT>;
+  auto* k = few_kernel<D, BF16>;
   constexpr int smem = Cfg<D>::SMEM;
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   k<<<grid, kThreads, smem, stream>>>(L.tmK, L.tmV, L.p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   const int rows = L.p.max_q * L.p.G;
-  const int y = rows < 1 ? 1 : (rows < 8 ? rows : 8);
-  few_merge_kernel<D, BF16, MT><<<dim3(grid, y), kCompute, 0, stream>>>(L.p);
+  few_merge_kernel<D, BF16><<<dim3(grid, rows < 1 ? 1 : rows), kCompute, 0, stream>>>(L.p);
   return cudaGetLastError();
-}
-
-template <int D, bool BF16>
-cudaError_t launch_t(const FewLaunch& L, int rows, cudaStream_t stream) {
-  if (rows <= 16) return launch_mt<D, BF16, 1>(L, stream);
-  if (rows <= 32) return launch_mt<D, BF16, 2>(L, stream);
-  return launch_mt<D, BF16, 4>(L, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_few(const FewLaunch& L, int D, bool bf16, int rows, cudaStream_t stream) {
-  if (D == 128) return bf16 ? launch_t<128, true>(L, rows, stream) : launch_t<128, false>(L, rows, stream);
-  return bf16 ? launch_t<64, true>(L, rows, stream) : launch_t<64, false>(L, rows, stream);
+cudaError_t launch_few(const FewLaunch& L, int D, bool bf16, cudaStream_t stream) {
+  if (D == 128) return bf16 ? launch_t<128, true>(L, stream) : launch_t<128, false>(L, stream);
+  return bf16 ? launch_t<64, true>(L, stream) : launch_t<64, false>(L, stream);
 }
 
 }  // namespace fa

@@ -132,14 +132,18 @@ __device__ __forceinline__ void mask_row(uint32_t* s, int n0, int pos, int sk,
 
 // ------------------------------------------------------------------ plan
 
-constexpr int kCandidates = 16;
+constexpr int kCandidates = 32;   // split sizes tried, one per warp of the plan kernel
+constexpr int kSplitBelow = 512;  // units (of one K/V head) above which nothing is split
+static_assert(kCandidates * 32 == kPlanThreads, "a warp per candidate");
 
 struct PlanSmem {
   SeqScan scan;
   int bins[kBins + 1];
   // units, largest and sum of their key blocks (used for few units alone), split choice
   int pairs, n_max, cost, slots, groups, split;
-  int units[kCandidates];
+  int blocks[kSplitBelow];  // key blocks of the units, while there are few
+  int split_of[kCandidates];
+  float cost_of[kCandidates];
 };
 
 // Calls f(unit) for every token block of every sequence (one unit of all its key blocks).
@@ -195,7 +199,6 @@ __global__ void __launch_bounds__(kPlanThreads) var_plan_kernel(const VarParams 
   __shared__ PlanSmem s;
   const int tid = threadIdx.x;
   for (int i = tid; i <= kBins; i += kPlanThreads) s.bins[i] = 0;
-  if (tid < kCandidates) s.units[tid] = 0;
   if (tid == 0) {
     s.pairs = s.n_max = s.cost = s.slots = s.groups = 0;
     s.split = INT_MAX;
@@ -206,7 +209,37 @@ __global__ void __launch_bounds__(kPlanThreads) var_plan_kernel(const VarParams 
 #pragma unroll 1
   for (int pass = kCount; pass < kPasses; ++pass) {
     const int split = s.split, n_max = s.n_max;
-    if (pass == kTry && !(p.part && s.pairs * p.Hkv < 2 * sms && n_max >= 8)) continue;
+    if (pass == kTry) {
+      if (!(p.part && s.pairs * p.Hkv < 2 * sms && s.pairs <= kSplitBelow && n_max >= 8)) continue;
+      // warp c: sizes from the largest unit (no split) down to a third of an SM's share
+      const int c = tid / 32, lane = tid % 32;
+      const float lo = fmaxf(4.f, static_cast<float>(s.cost) * p.Hkv / (3.f * sms));
+      const float f = static_cast<float>(kCandidates - 1 - c) / (kCandidates - 1);
+      const int S = c == 0 ? n_max
+                           : max(1, min(n_max, static_cast<int>(ceilf(lo * powf(n_max / lo, f)))));
+      int units = 0;
+      for (int i = lane; i < s.pairs; i += 32) units += max(1, (s.blocks[i] + S - 1) / S);
+#pragma unroll
+      for (int o = 16; o > 0; o /= 2) units += __shfl_xor_sync(0xffffffffu, units, o);
+      if (lane == 0) {
+        const int items = units * p.Hkv;
+        const bool fits = c == 0 || (items <= kVarMaxSplit && units <= p.max_units);
+        const float mean = static_cast<float>(s.cost) / units;
+        s.cost_of[c] = !fits ? INFINITY
+                             : fmaxf(S + 4.f, ((items + sms - 1) / sms) * (mean + 4.f)) +
+                                   (units > s.pairs ? 8.f : 0.f);
+        s.split_of[c] = units > s.pairs ? S : INT_MAX;
+      }
+      __syncthreads();
+      if (tid == 0) {
+        int best = 0;
+        for (int k = 1; k < kCandidates; ++k)
+          if (s.cost_of[k] < s.cost_of[best]) best = k;
+        s.split = s.split_of[best];
+      }
+      __syncthreads();
+      continue;
+    }
     if (pass == kRecount) {
       if (split == INT_MAX) continue;
       for (int i = tid; i <= kBins; i += kPlanThreads) s.bins[i] = 0;
@@ -222,24 +255,18 @@ __global__ void __launch_bounds__(kPlanThreads) var_plan_kernel(const VarParams 
     auto visit = [&](VarUnit u) {
       const int n = u.j1, ns = split == INT_MAX ? 1 : max(1, (n + split - 1) / split);
       if (pass == kCount && p.part) {
-        atomicAdd(&s.pairs, 1);
+        const int i = atomicAdd(&s.pairs, 1);
+        if (i < kSplitBelow) s.blocks[i] = n;
         atomicMax(&s.n_max, n);
         atomicAdd(&s.cost, n);
-      }
-      if (pass == kTry) {
-        for (int c = 0; c < kCandidates; ++c) {
-          const int S = (n_max + c) / (c + 1);
-          atomicAdd(&s.units[c], max(1, (n + S - 1) / S));
-        }
-        return;
       }
       if (pass == kWrite && ns > 1) {
         u.slot = atomicAdd(&s.slots, ns);
         p.groups[atomicAdd(&s.groups, 1)] = VarGroup{u.q0, u.nq, u.slot, ns};
       }
       for (int k = 0; k < ns; ++k) {
-        u.j0 = n * k / ns;
-        u.j1 = n * (k + 1) / ns;
+        u.j0 = static_cast<int>(static_cast<long long>(n) * k / ns);
+        u.j1 = static_cast<int>(static_cast<long long>(n) * (k + 1) / ns);
         const int bin = cost_bin(u.j1 - u.j0, p.cost_shift);
         const int at = atomicAdd(&s.bins[pass == kWrite ? bin : bin + 1], 1);
         if (pass == kWrite && at < p.max_units) p.units[at] = u;
@@ -247,7 +274,31 @@ __global__ void __launch_bounds__(kPlanThreads) var_plan_kernel(const VarParams 
       }
     };
     if (one_pass) {
-      if (has) visit(mine);
+      const bool many = has && split != INT_MAX && mine.j1 > split;
+      if (has && !many) visit(mine);
+      // split units by the whole warp, one unit after the other, a piece per lane
+      for (uint32_t rest = __ballot_sync(0xffffffffu, many); rest; rest &= rest - 1) {
+        const int src = __ffs(rest) - 1, lane = tid % 32;
+        auto from = [&](int x) { return __shfl_sync(0xffffffffu, x, src); };
+        VarUnit u;
+        u.q0 = from(mine.q0), u.nq = from(mine.nq), u.sk = from(mine.sk), u.k0 = from(mine.k0);
+        u.qpos = from(mine.qpos), u.seq = from(mine.seq);
+        const int n = from(mine.j1), ns = (n + split - 1) / split;
+        int slot = 0;
+        if (pass == kWrite && lane == 0) {
+          slot = atomicAdd(&s.slots, ns);
+          p.groups[atomicAdd(&s.groups, 1)] = VarGroup{u.q0, u.nq, slot, ns};
+        }
+        slot = __shfl_sync(0xffffffffu, slot, 0);
+        for (int k = lane; k < ns; k += 32) {
+          u.j0 = static_cast<int>(static_cast<long long>(n) * k / ns);
+          u.j1 = static_cast<int>(static_cast<long long>(n) * (k + 1) / ns);
+          u.slot = slot + k;
+          const int bin = cost_bin(u.j1 - u.j0, p.cost_shift);
+          const int at = atomicAdd(&s.bins[pass == kWrite ? bin : bin + 1], 1);
+          if (pass == kWrite && at < p.max_units) p.units[at] = u;
+        }
+      }
       __syncthreads();
     } else {
       for_each_block(p, s, pass == kCount, [&](const VarUnit& u) {
@@ -256,23 +307,6 @@ __global__ void __launch_bounds__(kPlanThreads) var_plan_kernel(const VarParams 
         visit(u);
       });
       one_pass = p.B <= kPlanThreads && s.scan.off[p.B] <= kPlanThreads;
-    }
-    if (pass == kTry) {
-      if (tid == 0) {
-        float best = 0.f;
-        for (int c = 0; c < kCandidates; ++c) {
-          const int S = (n_max + c) / (c + 1), items = s.units[c] * p.Hkv;
-          if (c > 0 && (S < 4 || items > kVarMaxSplit || s.units[c] > p.max_units)) break;
-          const float mean = static_cast<float>(s.cost) / s.units[c];
-          float est = fmaxf(S + 4.f, ((items + sms - 1) / sms) * (mean + 4.f));
-          if (c > 0) est += 8.f;
-          if (c == 0 || est < best) {
-            best = est;
-            s.split = c == 0 ? INT_MAX : S;
-          }
-        }
-      }
-      __syncthreads();
     }
   }
   if (tid == 0) p.hdr->groups = s.groups;
@@ -733,35 +767,70 @@ __global__ void __launch_bounds__(kThreads, 1)
 // ------------------------------------------------------------------ joining split items
 
 // One warp per row: M = max m_s, O = sum 2^(m_s - M) O_s / sum 2^(m_s - M) l_s over the
-// group's slots in order.
+// group's slots in order. Rows without a token are skipped.
 constexpr int kMergeThreads = 512;
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kMergeThreads) var_merge_kernel(const VarParams p) {
   constexpr int E = D / 32;  // elements per lane
   const int lane = threadIdx.x % 32;
   const int warps = gridDim.x * (kMergeThreads / 32), per = p.Hkv * kVarSplitRows;
-  const int total = p.hdr->groups * per;
   const size_t step = static_cast<size_t>(p.Hkv) * kVarSplitRows * (D + 2);
-  for (int w = blockIdx.x * (kMergeThreads / 32) + threadIdx.x / 32; w < total; w += warps) {
-    const VarGroup g = p.groups[w / per];
+  for (int w = blockIdx.x * (kMergeThreads / 32) + threadIdx.x / 32; w / per < kVarMaxSplit;
+       w += warps) {
+    const int4 gw = reinterpret_cast<const int4*>(p.groups)[w / per];  // beside the count
+    if (w / per >= p.hdr->groups) return;
+    const VarGroup g{gw.x, gw.y, gw.z, gw.w};
     const int kvh = (w % per) / kVarSplitRows, r = w % kVarSplitRows;
     const int tok = (r / kTile) * p.TPT + (r % kTile) / p.G;
     if ((r % kTile) / p.G >= p.TPT || tok >= g.nq) continue;
     const float* s0 = p.part + (static_cast<size_t>(g.slot) * p.Hkv + kvh) *
                                    (static_cast<size_t>(kVarSplitRows) * (D + 2));
-    float M = -INFINITY, L = 0.f, acc[E];
+    const float* row = s0 + static_cast<size_t>(r) * D + lane * E;
+    constexpr int N = 12;  // slots in flight
+    float o[N][E];
+    auto load = [&](int s1) {
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int e = 0; e < E; e += 2) {
+          const float2 x = s1 + i < g.n ? *reinterpret_cast<const float2*>(row + (s1 + i) * step + e)
+                                        : make_float2(0.f, 0.f);
+          o[i][e] = x.x;
+          o[i][e + 1] = x.y;
+        }
+    };
+    load(0);  // beside the maxima and sums, one slot per lane
+    float M = -INFINITY, L = 0.f;
+    for (int s1 = 0; s1 < g.n; s1 += 32) {
+      float m = -INFINITY, l = 0.f;
+      if (s1 + lane < g.n) {
+        m = s0[(s1 + lane) * step + kVarSplitRows * D + r];
+        l = s0[(s1 + lane) * step + kVarSplitRows * (D + 1) + r];
+      }
+      float mx = fmaxf(M, m);
+#pragma unroll
+      for (int i = 16; i > 0; i /= 2) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, i));
+      const float mu = mx == -INFINITY ? 0.f : mx;
+      l *= ex2_approx(m - mu);
+#pragma unroll
+      for (int i = 16; i > 0; i /= 2) l += __shfl_xor_sync(0xffffffffu, l, i);
+      L = L * ex2_approx(M - mu) + l;
+      M = mx;
+    }
+    const float mu = M == -INFINITY ? 0.f : M;
+    float acc[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = 0.f;
-    for (int s = 0; s < g.n; ++s) {
-      const float* sl = s0 + s * step;
-      const float m = sl[kVarSplitRows * D + r], l = sl[kVarSplitRows * (D + 1) + r];
-      if (!(l > 0.f)) continue;  // saw no key
-      const float mn = fmaxf(M, m), c = ex2_approx(M - mn), wt = ex2_approx(m - mn);
-      L = L * c + l * wt;
+    for (int s1 = 0;;) {
 #pragma unroll
-      for (int e = 0; e < E; ++e)
-        acc[e] = acc[e] * c + wt * sl[static_cast<size_t>(r) * D + lane * E + e];
-      M = mn;
+      for (int i = 0; i < N; ++i) {
+        const float m = s1 + i < g.n ? s0[(s1 + i) * step + kVarSplitRows * D + r] : -INFINITY;
+        const float wt = ex2_approx(m - mu);
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = fmaf(wt, o[i][e], acc[e]);
+      }
+      if ((s1 += N) >= g.n) break;
+      load(s1);
     }
     const float inv = L > 0.f ? 1.f / L : 0.f;
     const int h = kvh * p.G + (r % kTile) % p.G;

@@ -151,10 +151,10 @@ cudaError_t launch_bwd_varlen(const VarBwdLaunch& L, int D, bool bf16, cudaStrea
 
 // ------------------------------------------------ few rows over a paged cache (fa_few.cu)
 //
-// Chunks whose rows (tokens x heads of a group) are at most 64, a decode step above all: bound
+// Chunks whose rows (tokens x heads of a group) are at most 16, a decode step above all: bound
 // by reading the cache, so the key tiles of all sequences and K/V heads are laid end to end and
 // dealt to the CTAs in equal runs, whatever the lengths.
-constexpr int kFewRows = 64;
+constexpr int kFewRows = 16;
 constexpr int kFewMaxCtas = 320;
 // A pair (sequence, K/V head) whose first piece CTA x holds: its first row of q, rows, K/V head,
 // and the CTA of its last piece; rows = 0: none.
@@ -162,8 +162,8 @@ struct FewHead {
   int32_t q0, rows, kvh, last;
 };
 constexpr size_t kFewHeadBytes = kFewMaxCtas * sizeof(FewHead);
-inline size_t few_part_floats(int rows, int d) {  // a CTA leaves at most two partial results
-  return static_cast<size_t>(2) * kFewMaxCtas * rows * (d + 2);
+inline size_t few_part_floats(int d) {  // a CTA leaves at most two partial results
+  return static_cast<size_t>(2) * kFewMaxCtas * kFewRows * (d + 2);
 }
 
 struct FewParams {
@@ -178,7 +178,7 @@ struct FewParams {
   int B, H, Hkv, G, total_q, max_q;
   int page_size, max_pages, num_pages, box;  // box: rows of one TMA box (<= 64)
   FewHead* heads;  // [CTAs]
-  float* part;  // [2 CTAs][rows][D], then m [2 CTAs][rows], l [2 CTAs][rows]
+  float* part;  // [2 CTAs][16 rows][D], then m [2 CTAs][16], l [2 CTAs][16]
 };
 
 struct FewLaunch {
@@ -186,6 +186,6 @@ struct FewLaunch {
   FewParams p;
   int sms;
 };
-cudaError_t launch_few(const FewLaunch& L, int D, bool bf16, int rows, cudaStream_t stream);
+cudaError_t launch_few(const FewLaunch& L, int D, bool bf16, cudaStream_t stream);
 
 }  // namespace fa
