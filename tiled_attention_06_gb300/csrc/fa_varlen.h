@@ -106,11 +106,10 @@ cudaError_t launch_varlen(const VarLaunch& L, int D, bool bf16, cudaStream_t str
 //
 // The query side moves in halves of 64 rows: TPH = 64 / GS consecutive tokens of a sequence with
 // GS heads of one group (row r: token r / GS, head r % GS). A group's G heads are dealt to HS
-// subsets of GS = G / HS when there are too few key blocks for the SMs; each subset then has
-// its own partial dk and dv. A half's slot: sequence b's halves start at cu[b] / TPH + b, which
+// subsets of GS = G / HS when few key blocks would keep few SMs busy for long; each subset then
+// has its own partial dk and dv. A half's slot: sequence b's halves start at cu[b] / TPH + b, which
 // leaves room for every sequence's rounding without a scan.
 constexpr int kBwdHalf = 64;
-constexpr int kBwdMinItems = 304;  // key blocks x K/V heads x HS aimed at: 2 per SM
 
 struct VarBwdUnit {  // one block of 128 keys (48 bytes), written by the plan kernel
   int32_t k0, nk, j0;     // first row of k, keys in the block, first key's position
