@@ -479,8 +479,8 @@ fa_status fa_rope_append(const fa_rope_append_params* params, fa_stream_t stream
  * the last keys of their own sequence).
  *   q, o [total_q, H, d]; k, v [total_k, Hkv, d]; lse [total_q, H] float32 or NULL
  *   cu_seqlens_q, cu_seqlens_k [B + 1] (the same array for self-attention)
- *   d 64 or 128; dtype FA_F16 or FA_BF16; token steps a multiple of 8 elements; mask_mode every
- *   mask but FA_MASK_BLOCK_SPARSE, with window and n_global per sequence.
+ *   d 64 or 128; dtype FA_F16 or FA_BF16; token steps a multiple of 8 elements; scale positive;
+ *   mask_mode every mask but FA_MASK_BLOCK_SPARSE, with window and n_global per sequence.
  *   workspace  device scratch of fa_varlen_workspace_size(...) bytes, 16-byte aligned, owned by
  *              the caller; its contents on entry do not matter. Calls that may overlap on the
  *              GPU, two captured graphs among them, need workspaces of their own.

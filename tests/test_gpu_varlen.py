@@ -259,3 +259,115 @@ def test_paged_lengths_and_pages_out_of_range(new):
     assert fa.fa_get_device_status() == fa.FA_OK
     assert (o[:new - few] == 0).all() and lse[:new - few].isneginf().all()
     assert torch.isfinite(lse[new - few:new]).all()
+
+
+@pytest.mark.parametrize("new", [1, 40])
+def test_pages_beyond_32_bit_offsets(new):
+    """A pool of 2.3e9 elements whose last pages hold the sequence."""
+    H, Hkv, d, page, dt = 4, 2, 128, 64, torch.float16
+    pages = 140000
+    q, k, v, kp, vp, table, total, cu, cu_k = paged_case([new], [300], H, Hkv, d, page, dt, seed=2)
+    shift = pages - kp.shape[0]
+    assert pages * Hkv * page * d > 2 ** 31
+    big_k, big_v = (torch.empty(pages, Hkv, page, d, dtype=dt, device="cuda") for _ in range(2))
+    big_k[shift:], big_v[shift:] = kp.cuda(), vp.cuda()
+    far = torch.where(table >= 0, table + shift, table)
+    o = torch.full((new + 2, H, d), float("nan"), dtype=dt, device="cuda")
+    lse = torch.full((new + 2, H), float("nan"), device="cuda")
+    ws = torch.empty(fa.fa_paged_varlen_workspace_size(1, H, Hkv, new + 2, new, far.shape[1], page,
+                                                       d), dtype=torch.uint8, device="cuda")
+    fa.fa_fwd_paged_varlen(q.cuda(), big_k, big_v, far.cuda(), i32(total), i32(cu), new, o, lse,
+                           0.09, ws)
+    assert fa.fa_get_device_status() == fa.FA_OK
+    check_forward(o, lse, attention(q, k, v, cu, cu_k, 0.09, fa.FA_MASK_CAUSAL), dt, new)
+
+
+def test_two_streams_at_once():
+    """Calls of two shapes that overlap, each on its own stream with its own workspace."""
+    cases = []
+    for i, (lens, H, Hkv, d) in enumerate([([700, 33], 8, 2, 128), ([64] * 9, 6, 3, 64)]):
+        q, k, v, cu, _ = case(lens, lens, H, Hkv, d, torch.bfloat16, seed=i)
+        args = [x.cuda() for x in (q, k, v)]
+        want = forward(*args, cu, cu, 0.1)
+        T = sum(lens)
+        o = torch.zeros(T, H, d, dtype=torch.bfloat16, device="cuda")
+        lse = torch.zeros(T, H, device="cuda")
+        ws = torch.empty(fa.fa_varlen_workspace_size(len(lens), H, Hkv, T, T, d),
+                         dtype=torch.uint8, device="cuda")
+        cases.append((args, i32(cu), o, lse, ws, want, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for args, cu, o, lse, ws, _, stream in cases:
+            fa.fa_fwd_varlen(*args, o, lse, cu, cu, 0.1, ws, stream=stream)
+    torch.cuda.synchronize()
+    assert fa.fa_get_device_status() == fa.FA_OK
+    for _, _, o, lse, _, want, _ in cases:
+        assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+
+
+def test_many_calls_in_a_row_without_waiting():
+    """A few hundred calls queued at once over three sets of buffers, few rows and many."""
+    H, Hkv, d, page, dt = 8, 2, 128, 64, torch.bfloat16
+    for new, before in (([1] * 6, [0, 100, 3000, 64, 63, 700]), ([90, 3, 200], [800, 2000, 0])):
+        sets = []
+        for i in range(3):
+            q, k, v, kp, vp, table, total, cu, _ = paged_case(new, before, H, Hkv, d, page, dt,
+                                                              seed=i)
+            want = run_paged(q, kp, vp, table, total, cu, max(new), 0.09)
+            T = q.shape[0]
+            ws = torch.empty(fa.fa_paged_varlen_workspace_size(len(new), H, Hkv, T, max(new),
+                                                               table.shape[1], page, d),
+                             dtype=torch.uint8, device="cuda")
+            sets.append((q.cuda(), kp.cuda(), vp.cuda(), table.cuda(), i32(total), i32(cu),
+                         torch.zeros_like(want[0]), torch.zeros_like(want[1]), ws, want))
+        for i in range(300):
+            q, kp, vp, table, ctx, cu, o, lse, ws, _ = sets[i % 3]
+            fa.fa_fwd_paged_varlen(q, kp, vp, table, ctx, cu, max(new), o, lse, 0.09, ws)
+        assert fa.fa_get_device_status() == fa.FA_OK
+        n = sum(new)
+        for *_, o, lse, _, want in sets:
+            assert torch.equal(o[:n], want[0][:n]) and torch.equal(lse[:n], want[1][:n])
+
+
+def test_long_sequence_of_many_units():
+    """More token blocks than the plan kernel has threads, and more sequences too."""
+    lens = [1] * 1500 + [0] * 7 + [3] * 40
+    q, k, v, cu, _ = case(lens, lens, 2, 1, 64, torch.float16, seed=8)
+    o, lse = forward(q.cuda(), k.cuda(), v.cuda(), cu, cu, 0.125)
+    check_forward(o, lse, attention(q, k, v, cu, cu, 0.125, fa.FA_MASK_CAUSAL), torch.float16,
+                  sum(lens))
+    T = 40000  # 64 tokens a unit at 4 heads a group ... 32 at 8
+    g = torch.Generator().manual_seed(1)
+    q = torch.randn(T, 8, 64, generator=g).to(torch.float16)
+    k, v = (torch.randn(T, 1, 64, generator=g).to(torch.float16) for _ in range(2))
+    o, lse = forward(q.cuda(), k.cuda(), v.cuda(), [0, T], [0, T], 0.125,
+                     (fa.FA_MASK_CAUSAL_WINDOW, 100, 3))
+    for a in (0, 20001, T - 300):  # windows of queries with the keys that they can see
+        lo = max(0, a - 100)
+        keys = list(range(3)) + list(range(max(3, lo), a + 300)) if lo > 3 else range(a + 300)
+        i, j = torch.arange(a, a + 300)[:, None], torch.tensor(list(keys))[None]
+        vis = (j <= i) & ((i - j < 100) | (j < 3))
+        from _packed import head
+        _, want, wl = head(q[a:a + 300, 5], k[j[0], 0], v[j[0], 0], vis, 0.125)
+        big = (vis * v[j[0], 0].double().abs().amax(-1)[None]).amax(-1)
+        ref = (want[:, None], wl[:, None], big[:, None])
+        check_forward(o[a:a + 300, 5:6], lse[a:a + 300, 5:6], ref, torch.float16, 300, f"from {a}")
+
+
+def test_python_refusals():
+    H, Hkv, d, T = 4, 2, 64, 10
+    q, k, v, cu, _ = case([T], [T], H, Hkv, d, torch.float16, seed=1)
+    q, k, v, cu = q.cuda(), k.cuda(), v.cuda(), i32(cu)
+    o = torch.empty_like(q)
+    ws = torch.empty(fa.fa_varlen_workspace_size(1, H, Hkv, T, T, d), dtype=torch.uint8,
+                     device="cuda")
+    good = dict(q=q, k=k, v=v, o=o, lse=None, cu_seqlens_q=cu, cu_seqlens_k=cu, scale=0.125,
+                workspace=ws)
+    fa.fa_fwd_varlen(**good)
+    bad = [dict(cu_seqlens_q=cu.long()), dict(k=k.bfloat16()), dict(v=v[:-1]), dict(o=o[:, :2]),
+           dict(q=q.transpose(0, 1)), dict(k=k[:, :1].expand(T, Hkv, d)), dict(q=q.cpu()),
+           dict(workspace=ws[:16]), dict(lse=torch.empty(T, H + 1, device="cuda")),
+           dict(cu_seqlens_k=cu[:1]), dict(lse=torch.empty(T, H, device="cuda").half())]
+    for kw in bad:
+        with pytest.raises(fa.FaError):
+            fa.fa_fwd_varlen(**dict(good, **kw))

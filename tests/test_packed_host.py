@@ -114,7 +114,7 @@ VARLEN = dict(q=A, k=A, v=A, o=A, lse=A, q_token=256, k_token=128, v_token=128, 
 SHARED = [
     (dict(B=0), INVALID), (dict(H=3), INVALID), (dict(Hkv=0), INVALID), (dict(d=96), UNSUPPORTED),
     (dict(H=258, q_token=258 * 64, o_token=258 * 64), UNSUPPORTED), (dict(dtype=2), UNSUPPORTED),
-    (dict(scale=math.nan), INVALID), (dict(mask_mode=6), INVALID),
+    (dict(scale=math.nan), INVALID), (dict(scale=0.0), INVALID), (dict(scale=-0.1), INVALID), (dict(mask_mode=6), INVALID),
     (dict(mask_mode=5), UNSUPPORTED), (dict(mask_mode=2, window=0), INVALID),
     (dict(mask_mode=2, window=1, n_global=-1), INVALID), (dict(mask_mode=3, window=-1), INVALID),
     (dict(mask_mode=4, n_global=-1), INVALID), (dict(total_q=-1), INVALID),

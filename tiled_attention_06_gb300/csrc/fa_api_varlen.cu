@@ -65,7 +65,9 @@ fa_status check_common(const Common& c) {
   if (c.d != 64 && c.d != 128)
     return fail(FA_ERR_UNSUPPORTED, "head dim %d (supported: 64, 128)", c.d);
   if (c.dtype != FA_F16 && c.dtype != FA_BF16) return fail(FA_ERR_UNSUPPORTED, "dtype %d", c.dtype);
-  if (!std::isfinite(c.scale)) return fail(FA_ERR_INVALID_ARG, "scale must be finite");
+  // hidden scores are -inf before the scale is applied, and the maximum is taken unscaled
+  if (!(c.scale > 0) || !std::isfinite(c.scale))
+    return fail(FA_ERR_INVALID_ARG, "scale must be positive and finite");
   if (c.mask_mode < FA_MASK_NONE || c.mask_mode > FA_MASK_BLOCK_SPARSE)
     return fail(FA_ERR_INVALID_ARG, "mask_mode %d", c.mask_mode);
   if (c.mask_mode == FA_MASK_BLOCK_SPARSE)

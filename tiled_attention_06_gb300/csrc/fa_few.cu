@@ -305,6 +305,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int kw = warp, r0 = lane / 4;  // key group; this thread's rows are r0 and r0 + 8
   const int cq = lane % 4;
   uint32_t pos = 0;
+  bool ok = true;
   while (w.left > 0) {
     const int cnt = min(w.left, w.s.tiles - w.j);
     const int rows = w.s.n * p.G;
@@ -332,7 +333,10 @@ __global__ void __launch_bounds__(kThreads, 2)
     for (int j = w.j; j < w.j + cnt; ++j, ++pos) {
       const int n0 = tile_at(w.s.rg, j) * BK;
       const int st = pos % C::NST;
-      if (!mbar_wait(B(bars->full[st]), (pos / C::NST) & 1, wc)) return;
+      // a warp that gives up still meets the others at the joins (its results are void)
+      ok = ok && mbar_wait(B(bars->full[st]), (pos / C::NST) & 1, wc);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) continue;
       const uint32_t sK = base + 2 * st * C::TILE, sV = sK + C::TILE;
       const int live = w.s.sk - n0;
       float s[NT][4];
