@@ -442,7 +442,9 @@ fa_status fa_fwd_varlen(const fa_varlen_params* params, fa_stream_t stream) {
   L.sms = dev.sms;
   const bool bf16 = a.dtype == FA_BF16;
   if ((st = make_map3(&L.tmQ, a.q, bf16, a.d, a.H, a.d, a.total_q, a.q_token, L.p.G, L.p.TPT)) !=
-      FA_OK)
+          FA_OK ||
+      (st = make_map3(&L.tmO, a.o, bf16, a.d, a.H, a.d, a.total_q, a.o_token, L.p.G, L.p.TPT)) !=
+          FA_OK)
     return st;
   // without keys no block is loaded; the maps only need a valid address
   const bool any = a.total_k > 0;
@@ -551,7 +553,9 @@ fa_status fa_fwd_paged_varlen(const fa_paged_varlen_params* params, fa_stream_t 
   L.p.box = std::min(fa::kVarBN, pow2);
   L.sms = dev.sms;
   if ((st = make_map3(&L.tmQ, a.q, bf16, a.d, a.H, a.d, a.total_q, a.q_token, L.p.G, L.p.TPT)) !=
-      FA_OK)
+          FA_OK ||
+      (st = make_map3(&L.tmO, a.o, bf16, a.d, a.H, a.d, a.total_q, a.o_token, L.p.G, L.p.TPT)) !=
+          FA_OK)
     return st;
   if ((st = make_map3(&L.tmK, a.k_pages, bf16, a.d, a.page_size, a.d, planes, plane, L.p.box,
                       1)) != FA_OK)

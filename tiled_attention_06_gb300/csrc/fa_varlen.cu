@@ -46,6 +46,7 @@ constexpr uint32_t kSmemLimit = 232448;
 constexpr int kThreads = 384;
 constexpr int kTmaWarp = 8;
 constexpr int kMmaWarp = 9;
+constexpr int kStoreWarp = 10;  // and 11: outputs of tiles A and B
 // launched at 168 registers per thread: 128 x (200 + 200 + 104) = 384 x 168
 constexpr uint32_t kRegsSoftmax = 200;
 constexpr uint32_t kRegsProducer = 104;
@@ -56,6 +57,20 @@ __device__ __forceinline__ void mbar_wait_quiet(uint32_t bar, uint32_t parity, c
   WaitCtx w2 = wc;
   w2.abort = &zero;
   mbar_wait(bar, parity, w2);
+}
+
+// 3-D tiled bulk-tensor store shared -> global of this thread's bulk group; then the group is
+// closed and waited for until its reads of shared memory are done.
+__device__ __forceinline__ void tma_store_3d(const void* map, uint32_t src, int x, int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+          reinterpret_cast<uint64_t>(map)),
+      "r"(src), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+__device__ __forceinline__ void bulk_commit_and_wait_read() {
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
 }
 
 // ------------------------------------------------------------------ masks by key position
@@ -331,6 +346,7 @@ struct Bars {
   uint64_t full[8], empty[8];
   uint64_t q_full[2], q_empty[2];
   uint64_t s_full[2], p_full[2], pv_done[2], o_empty[2];
+  uint64_t o_staged[2];  // the tile's output is in shared memory
   uint64_t final_mma;
   uint32_t tmem_base;
   uint32_t abort;
@@ -342,6 +358,11 @@ struct Item {
   int kvh;
   Range rg;
   int tiles;
+  // The output of tile q leaves through shared memory: a whole tile of final results. (A TMA
+  // store writes whole boxes, and what is behind a sequence's last token is not its own.)
+  __device__ __forceinline__ bool staged(int q, int TPT) const {
+    return u.slot < 0 && u.j1 > u.j0 && u.nq >= (q + 1) * TPT;
+  }
 };
 
 // The items of this CTA one after the other, in snake order over a list sorted by cost: round r
@@ -449,7 +470,8 @@ __device__ __forceinline__ void softmax_row(uint32_t t_lane, uint32_t s_col, uin
 template <int D, bool BF16, bool PAGED>
 __global__ void __launch_bounds__(kThreads, 1)
     var_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                   const __grid_constant__ CUtensorMap tmV, const __grid_constant__ VarParams p) {
+                   const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
+                   const __grid_constant__ VarParams p) {
   using C = Cfg<D>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
@@ -472,6 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(B(bars->p_full[i]), 128);
       mbar_init(B(bars->pv_done[i]), 1);
       mbar_init(B(bars->o_empty[i]), 128);
+      mbar_init(B(bars->o_staged[i]), 128);
     }
     mbar_init(B(bars->final_mma), 1);
     bars->abort = 0;
@@ -485,6 +508,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&tmQ);
     tma_prefetch_desc(&tmK);
     tma_prefetch_desc(&tmV);
+    tma_prefetch_desc(&tmO);
   }
   tc_fence_before();
   __syncthreads();
@@ -584,6 +608,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (Items items(p, total); ok && items.next(p, it);) {
         const int n = it.u.j1 - it.u.j0, last = it.tiles - 1;
         if (n == 0) continue;
+        const bool keep[2] = {it.staged(0, p.TPT), it.staged(1, p.TPT)};
         {
           const int slot = pos % C::NSLOT;
           if (!(ok = mbar_wait(B(bars->full[slot]), (pos / C::NSLOT) & 1, wc))) break;
@@ -598,7 +623,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           if (!ok) break;
-          if (leader) umma_commit(B(bars->empty[slot]));
+          // the last K slot takes tile A's output and the last V slot tile B's, where they leave
+          // through shared memory; the store warps then release them
+          if (leader && !(n == 1 && keep[0])) umma_commit(B(bars->empty[slot]));
           ++pos;
         }
         for (int j = 0; j < n && ok; ++j) {
@@ -628,7 +655,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (leader) {
               issue_pv<D, BN, BF16>(tO[q], tS[q], sRing + vslot * C::TILE_BYTES, j > 0);
               if (j == n - 1) umma_commit(B(bars->pv_done[q]));
-              if (q == last) umma_commit(B(bars->empty[vslot]));
+              if (q == last && !(j == n - 1 && keep[1])) umma_commit(B(bars->empty[vslot]));
             }
             if (j + 1 < n) {  // S(j+1) overwrites P(j) only after PV(j) in the pipe
               if (q == 0) {
@@ -638,7 +665,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (leader) {
                 qk(q, kslot);
                 if (j + 2 == n) umma_commit(B(bars->q_empty[q]));
-                if (q == last) umma_commit(B(bars->empty[kslot]));
+                if (q == last && !(j + 2 == n && keep[0])) umma_commit(B(bars->empty[kslot]));
               }
             }
           }
@@ -649,6 +676,29 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (leader) umma_commit(B(bars->final_mma));  // all MMAs done before TMEM is released
       mbar_wait_quiet(B(bars->final_mma), 0, wc);
+      __syncwarp();
+    } else {
+      // -------------------------------------------------------------- output of tile q
+      const int q = warp - kStoreWarp;
+      const bool leader = elect_one();
+      uint32_t pos = 0, done = 0;
+      Item it;
+      for (Items items(p, total); items.next(p, it);) {
+        const int n = it.u.j1 - it.u.j0;
+        pos += 2 * n;
+        if (!it.staged(q, p.TPT)) continue;
+        if (!mbar_wait(B(bars->o_staged[q]), done & 1, wc)) break;
+        ++done;
+        const int slot = (pos - 2 + q) % C::NSLOT;
+        if (leader) {
+          for (int c = 0; c < C::KCH; ++c)
+            tma_store_3d(&tmO, sRing + slot * C::TILE_BYTES + c * (kTile * 128), c * 64,
+                         it.kvh * p.G, it.u.q0 + q * p.TPT);
+          bulk_commit_and_wait_read();
+          mbar_arrive(B(bars->empty[slot]));
+        }
+        __syncwarp();
+      }
       __syncwarp();
     }
     tc_fence_before();
@@ -662,12 +712,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t t_lane = tmem + (static_cast<uint32_t>((warp % 4) * 32) << 16);
   const uint32_t s_col = q * BN, o_col = 2 * BN + q * D;
   const int tok = row / p.G, head = row - (row / p.G) * p.G;  // of the tile, of the group
-  uint32_t ii = 0, tc = 0;
+  uint32_t ii = 0, tc = 0, pos = 0;
   bool ok = true;
   Item it;
   for (Items items(p, total); ok && items.next(p, it);) {
-    if (q >= it.tiles) continue;
     const int n = it.u.j1 - it.u.j0;
+    pos += 2 * n;  // ring position behind this item
+    if (q >= it.tiles) continue;
     const int left = it.u.nq - q * p.TPT;  // tokens of this tile and behind it
     const int toks = min(p.TPT, left);
     const bool valid = tok < toks;
@@ -704,7 +755,31 @@ __global__ void __launch_bounds__(kThreads, 1)
     ok = __all_sync(0xffffffffu, ok);
     if (!ok) break;
     tc_fence_after();
-    if (it.u.slot < 0) {
+    if (it.staged(q, p.TPT)) {
+      const float inv_l = l > 0.f ? 1.f / l : 0.f;
+      // row `row` of the tile in the 128-byte swizzle of its TMA box: conflict-free stores
+      const uint32_t dst = sRing + (pos - 2 + q) % C::NSLOT * C::TILE_BYTES + row * 128;
+#pragma unroll 1
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t ov[32];
+        tmem_ld32(t_lane + o_col + c * 32, ov);
+        tmem_ld_wait<32>(ov);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const float a = __uint_as_float(ov[2 * e]) * inv_l, b = __uint_as_float(ov[2 * e + 1]) * inv_l;
+          ov[e] = BF16 ? cvt_pack_bf16(a, b) : cvt_pack_f16(a, b);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          st_shared_v4(dst + (c / 2) * (kTile * 128) +
+                           ((static_cast<uint32_t>((c % 2) * 4 + e) ^ (row & 7)) << 4),
+                       ov[4 * e], ov[4 * e + 1], ov[4 * e + 2], ov[4 * e + 3]);
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(B(bars->o_staged[q]));
+      if (valid && p.lse)
+        p.lse[orow] = l > 0.f ? (m_ref + lg2_approx(l)) * 0.69314718055994531f : -INFINITY;
+    } else if (it.u.slot < 0) {
       const float inv_l = l > 0.f ? 1.f / l : 0.f;
       const bool wide = ((reinterpret_cast<uintptr_t>(p.o) | (p.o_token * 2)) & 31u) == 0;
 #pragma unroll 1
@@ -857,7 +932,7 @@ cudaError_t launch_t(const VarLaunch& L, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   const int64_t items = static_cast<int64_t>(L.p.max_units) * L.p.Hkv;
   const int grid = static_cast<int>(items < L.sms ? items : L.sms);
-  k<<<grid, kThreads, smem, stream>>>(L.tmQ, L.tmK, L.tmV, L.p);
+  k<<<grid, kThreads, smem, stream>>>(L.tmQ, L.tmK, L.tmV, L.tmO, L.p);
   if ((e = cudaGetLastError()) != cudaSuccess || !L.p.part) return e;
   var_merge_kernel<D, BF16><<<L.sms * 2, kMergeThreads, 0, stream>>>(L.p);
   return cudaGetLastError();

@@ -96,7 +96,7 @@ struct VarParams {
 };
 
 struct VarLaunch {
-  CUtensorMap tmQ, tmK, tmV;
+  CUtensorMap tmQ, tmK, tmV, tmO;
   VarParams p;
   int sms;
 };
