@@ -85,9 +85,9 @@ __device__ __forceinline__ Range blocks_seen(int lo, int hi, int sk, const Prefi
   return key_range(lo, hi, BN, sk, f, 0);
 }
 
-// The j-th visited block.
-__device__ __forceinline__ int block_at(const Range& r, int j) {
-  return j < r.a_end ? j : r.b_start + (j - r.a_end);
+// The j-th visited block of a unit.
+__device__ __forceinline__ int block_at(const VarUnit& u, int j) {
+  return j < u.a_end ? j : u.b_start + (j - u.a_end);
 }
 
 // Every query at positions [lo, hi] sees every key of the block at n0 (and all are in range).
@@ -195,7 +195,10 @@ __device__ __forceinline__ void for_each_block(const VarParams& p, PlanSmem& s, 
         u.qpos = i * tpi + q.sk - q.sq;
         u.seq = b;
         u.j0 = 0;
-        u.j1 = range_count(blocks_seen(u.qpos, u.qpos + u.nq, u.sk, p.m));
+        const Range rg = blocks_seen(u.qpos, u.qpos + u.nq, u.sk, p.m);
+        u.j1 = range_count(rg);
+        u.a_end = rg.a_end;
+        u.b_start = rg.b_start;
         u.slot = -1;
         f(u);
       });
@@ -298,6 +301,7 @@ __global__ void __launch_bounds__(kPlanThreads) var_plan_kernel(const VarParams 
         VarUnit u;
         u.q0 = from(mine.q0), u.nq = from(mine.nq), u.sk = from(mine.sk), u.k0 = from(mine.k0);
         u.qpos = from(mine.qpos), u.seq = from(mine.seq);
+        u.a_end = from(mine.a_end), u.b_start = from(mine.b_start);
         const int n = from(mine.j1), ns = (n + split - 1) / split;
         int slot = 0;
         if (pass == kWrite && lane == 0) {
@@ -352,11 +356,10 @@ struct Bars {
   uint32_t abort;
 };
 
-// A work item: its unit, K/V head, visited key blocks, and tiles (1 when the second has no token).
+// A work item: its unit, K/V head, and tiles (1 when the second has no token).
 struct Item {
   VarUnit u;
   int kvh;
-  Range rg;
   int tiles;
   // The output of tile q leaves through shared memory: a whole tile of final results. (A TMA
   // store writes whole boxes, and what is behind a sequence's last token is not its own.)
@@ -366,12 +369,13 @@ struct Item {
 };
 
 // The items of this CTA one after the other, in snake order over a list sorted by cost: round r
-// covers items r G .. r G + G - 1, backwards on odd rounds. The words of the item to come are
-// loaded while the present one is worked on.
+// covers items r G .. r G + G - 1, backwards on odd rounds. AHEAD: the words of the item to come
+// are loaded while the present one is worked on (the softmax warps have no registers for that,
+// and have to wait for the item's first scores anyway).
+template <bool AHEAD>
 struct Items {
-  int total, round, t;  // t: the item whose words are in a, b, slot; total when there is none
-  int4 a, b;
-  int slot;
+  int total, round, t;  // t: the item whose words are in a, b, c; total when there is none
+  int4 a, b, c;
   __device__ __forceinline__ void fetch(const VarParams& p) {
     const int G = gridDim.x;
     t = total;
@@ -386,21 +390,21 @@ struct Items {
       const int4* src = reinterpret_cast<const int4*>(p.units + t / p.Hkv);
       a = src[0];
       b = src[1];
-      slot = src[2].x;
+      c = src[2];
     }
   }
   __device__ __forceinline__ Items(const VarParams& p, int total) : total(total), round(0) {
-    fetch(p);
+    if (AHEAD) fetch(p);
   }
   __device__ __forceinline__ bool next(const VarParams& p, Item& it) {
+    if (!AHEAD) fetch(p);
     if (t >= total) return false;
     it.u.q0 = a.x, it.u.nq = a.y, it.u.sk = a.z, it.u.k0 = a.w;
     it.u.qpos = b.x, it.u.seq = b.y, it.u.j0 = b.z, it.u.j1 = b.w;
-    it.u.slot = slot;
-    it.kvh = t - (t / p.Hkv) * p.Hkv;
-    it.rg = blocks_seen(it.u.qpos, it.u.qpos + it.u.nq, it.u.sk, p.m);
+    it.u.slot = c.x, it.u.a_end = c.y, it.u.b_start = c.z;
+    it.kvh = t % p.Hkv;
     it.tiles = it.u.nq > p.TPT ? 2 : 1;
-    fetch(p);
+    if (AHEAD) fetch(p);
     return true;
   }
 };
@@ -528,7 +532,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       Item it;
       const uint32_t q_bytes = static_cast<uint32_t>(p.TPT * p.G) * D * 2;
-      for (Items items(p, total); ok && items.next(p, it);) {
+      for (Items<true> items(p, total); ok && items.next(p, it);) {
         if (it.u.j1 == it.u.j0) continue;
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
@@ -543,7 +547,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++iq[q];
         }
         for (int j = it.u.j0; j < it.u.j1 && ok; ++j) {
-          const int n0 = block_at(it.rg, j) * BN;
+          const int n0 = block_at(it.u, j) * BN;
           // paged: lane i loads box i of the block, rows of one page; boxes behind the last
           // key are left out
           int y = 0, z = 0, boxes = 1;
@@ -605,9 +609,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         issue_qk<D, BN, BF16>(tS[q], sQ + q * C::Q_BYTES, sRing + slot * C::TILE_BYTES);
         umma_commit(B(bars->s_full[q]));
       };
-      for (Items items(p, total); ok && items.next(p, it);) {
+      Items<true> items(p, total);
+      for (bool more = items.next(p, it); ok && more;) {
         const int n = it.u.j1 - it.u.j0, last = it.tiles - 1;
-        if (n == 0) continue;
+        if (n == 0) {
+          more = items.next(p, it);
+          continue;
+        }
         const bool keep[2] = {it.staged(0, p.TPT), it.staged(1, p.TPT)};
         {
           const int slot = pos % C::NSLOT;
@@ -628,10 +636,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (leader && !(n == 1 && keep[0])) umma_commit(B(bars->empty[slot]));
           ++pos;
         }
+        Item coming;  // while the first softmax runs
+        more = items.next(p, coming);
         for (int j = 0; j < n && ok; ++j) {
           const int vslot = pos % C::NSLOT, kslot = (pos + 1) % C::NSLOT;
           if (!(ok = mbar_wait(B(bars->full[vslot]), (pos / C::NSLOT) & 1, wc))) break;
-          const int live = it.u.sk - block_at(it.rg, it.u.j0 + j) * BN;  // rows below sk
+          const int live = it.u.sk - block_at(it.u, it.u.j0 + j) * BN;  // rows below sk
           if (live < BN) {  // zero the rows of V behind the last key
             uint8_t* v = smem + 2 * C::Q_BYTES + vslot * C::TILE_BYTES;
             for (int c = 0; c < C::KCH; ++c) {
@@ -673,6 +683,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         ++iq[0];
         if (it.tiles > 1) ++iq[1];
+        it = coming;
       }
       if (leader) umma_commit(B(bars->final_mma));  // all MMAs done before TMEM is released
       mbar_wait_quiet(B(bars->final_mma), 0, wc);
@@ -683,7 +694,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool leader = elect_one();
       uint32_t pos = 0, done = 0;
       Item it;
-      for (Items items(p, total); items.next(p, it);) {
+      for (Items<false> items(p, total); items.next(p, it);) {
         const int n = it.u.j1 - it.u.j0;
         pos += 2 * n;
         if (!it.staged(q, p.TPT)) continue;
@@ -715,7 +726,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t ii = 0, tc = 0, pos = 0;
   bool ok = true;
   Item it;
-  for (Items items(p, total); ok && items.next(p, it);) {
+  for (Items<false> items(p, total); ok && items.next(p, it);) {
     const int n = it.u.j1 - it.u.j0;
     pos += 2 * n;  // ring position behind this item
     if (q >= it.tiles) continue;
@@ -737,7 +748,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int p_lo = it.u.qpos + q * p.TPT, p_hi = p_lo + toks - 1, pos_q = p_lo + tok;
     float m_ref = -INFINITY, l = 0.f;
     for (int j = it.u.j0; j < it.u.j1; ++j) {
-      const int n0 = block_at(it.rg, j) * BN;
+      const int n0 = block_at(it.u, j) * BN;
       ok = mbar_wait(B(bars->s_full[q]), tc & 1, wc);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;

@@ -60,7 +60,8 @@ struct VarUnit {
   int32_t seq;
   int32_t j0, j1;  // which of the visited key blocks
   int32_t slot;    // -1: writes o and lse; else a partial result, slot * Hkv + kv head
-  int32_t pad[3];
+  int32_t a_end, b_start;  // visited blocks: 0 .. a_end - 1, then b_start on
+  int32_t pad;
 };
 // A token block whose key blocks were split: its partial results, slot .. slot + n - 1.
 struct VarGroup {
