@@ -14,6 +14,8 @@
 // to o, a piece to the workspace. A warp takes 16 keys of every tile and keeps its own running
 // maximum, sum and output in registers; the four are joined through shared memory at the end of
 // a segment.
+// 32 sequences of 110,000 keys in all, 32/8 heads of 128, fp16: 79 to 84 us, 6.1 TB/s (the join 4 more;
+// the cache's bytes alone take 72.6 us at the measured copy rate).
 // few_merge_kernel joins the pieces of each pair in the order of the keys; the CTA that holds a
 // pair's first piece leaves word of where the others are.
 #include <cuda_bf16.h>

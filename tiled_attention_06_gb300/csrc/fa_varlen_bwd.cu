@@ -21,6 +21,12 @@
 //                 warpgroups (two per half in flight, 32 columns each), TMA warp, MMA warp.
 //   bwd_dq        scales and rounds the accumulator into dq (HBM-bound).
 //   bwd_sum       HS > 1 alone: sums the head subsets' dk and dv, in order.
+// Bounds. 11343 tokens in 4 sequences, 32/8 heads of 128, bf16, causal: 797 us, 979 TFLOP/s over
+// the five products (51 % of 1923.5 measured); the main kernel 665 of them (1173 TFLOP/s, MMAs of
+// N = 64 issued by one thread and the elementwise warps in turn), prep 62 and dq 51, both at about
+// 5.5 TB/s of mostly accumulator traffic. 24 short sequences, 12/4 heads of 64: 44 us, four
+// launches and a CTA's fixed 9 us around 7 halves.
+//
 // Rows of K, Q and dO behind a sequence's end belong to others: they are zeroed in shared
 // memory (0 times an infinity or NaN is not 0), and masked probabilities and dS are set to 0.
 #include <cuda_bf16.h>
