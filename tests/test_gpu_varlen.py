@@ -371,3 +371,29 @@ def test_python_refusals():
     for kw in bad:
         with pytest.raises(fa.FaError):
             fa.fa_fwd_varlen(**dict(good, **kw))
+
+
+@pytest.mark.parametrize("new", [1, 3, 5, 40, 100])
+@pytest.mark.parametrize("dt", list(DT))
+def test_scores_that_climb(new, dt):
+    """Every later block lifts every row's maximum by more than the lazy-rescale threshold (12 in
+    log2 units a block of 128 keys, as in inputs.climbing_inputs), for few rows, items of one tile
+    and of two; and their falling mirror image."""
+    H, Hkv, d, page, ctx = 8, 1, 64, 64, 1500
+    for sign in (1.0, -1.0):
+        q, k, v, kp, vp, table, total, cu, cu_k = paged_case([new], [ctx], H, Hkv, d, page, DT[dt],
+                                                             seed=new)
+        T = total[0]
+        # q = N(0,1) + 1, k_j = N(0,1) + a_j: the mean score rises by scale d a_j = 8 a_j
+        q = (q.float() + 1).to(DT[dt])
+        a = sign * torch.arange(T).float() / 128 * (12 * math.log(2) / 8)
+        k = (k.float() + a[:, None, None]).to(DT[dt])
+        pos = torch.arange(T)
+        kp[table[0, pos // page].long(), :, pos % page] = k
+        o, lse = run_paged(q, kp, vp, table, total, cu, new, 0.125)
+        assert fa.fa_get_device_status() == fa.FA_OK
+        ref = attention(q, k, v, cu, cu_k, 0.125, fa.FA_MASK_CAUSAL)
+        # |scores| reach 130 here: the FP32 products' and sums' error grows with them (2^-24 of a
+        # sum of |q k| up to 300 in 64 terms: 2^-13), and the weights' by as much
+        check_forward(o, None, (ref[0], ref[1], ref[2] * (1 + 2.0 ** -4)), DT[dt], new)
+        assert float((lse[:new].double().cpu() - ref[1][:new]).abs().max()) <= 2.0 ** -10

@@ -17,8 +17,9 @@
 //   var_fwd_kernel    persistent, one CTA per SM, which takes the list's items in a snake
 //                     order. Warps 0-3 and 4-7 are the softmax of tiles A and B (TMEM lane =
 //                     row, a whole row per thread), warp 8 loads by TMA, warp 9 issues the
-//                     MMAs. Tensor-pipe order S_A S_B | PV_A S_A' | PV_B S_B' | ..., so that
-//                     one tile's softmax runs while the tensor core works for the other.
+//                     MMAs, warps 10 and 11 store outputs. Tensor-pipe order S_A S_B | PV_A S_A' |
+//                     PV_B S_B' | ..., so that one tile's softmax runs while the tensor core
+//                     works for the other; with one tile S(0) | S(1) PV(0) | S(2) PV(1) | ...
 //   var_merge_kernel  joins the partial results of split items.
 //
 // Bounds. In the middle of an item a key block takes about 3000 cycles for both tiles: 2 x 16384
@@ -359,7 +360,9 @@ struct Cfg {
 struct Bars {
   uint64_t full[8], empty[8];
   uint64_t q_full[2], q_empty[2];
-  uint64_t s_full[2], p_full[2], pv_done[2], o_empty[2];
+  uint64_t s_full[3], p_full[3];  // tiles A and B; odd blocks of an item with one tile
+  uint64_t pv_done[2], o_empty[2];
+  uint64_t pv_step;      // every P V of an item with one tile
   uint64_t o_staged[2];  // the tile's output is in shared memory
   uint64_t final_mma;
   uint32_t tmem_base;
@@ -423,10 +426,12 @@ struct Items {
 // when the maximum rose by more than kTau; decided per warp), P = 2^(S sl2 - m) rounded to 16
 // bits over S, l += the unrounded sum. P of at most 2^8 and l in FP32 keep the rounding of P
 // the only one on the way.
-template <int D, bool BF16>
-__device__ __forceinline__ void softmax_row(uint32_t t_lane, uint32_t s_col, uint32_t o_col,
+// `before_rescale` makes O safe to touch, false on abort.
+template <int D, bool BF16, typename PreRescale>
+__device__ __forceinline__ bool softmax_row(uint32_t t_lane, uint32_t s_col, uint32_t o_col,
                                             bool full, int n0, int pos, int sk,
-                                            const PrefillParams& m, float& m_ref, float& l) {
+                                            const PrefillParams& m, float& m_ref, float& l,
+                                            PreRescale before_rescale) {
   uint32_t s[BN];
   tmem_ld64(t_lane + s_col, s);
   tmem_ld64(t_lane + s_col + 64, s + 64);
@@ -445,6 +450,7 @@ __device__ __forceinline__ void softmax_row(uint32_t t_lane, uint32_t s_col, uin
   const bool need = m_ref != -INFINITY && m_new > m_ref + kTau;
   if (m_ref == -INFINITY) m_ref = m_new;
   if (__any_sync(0xffffffffu, need)) {
+    if (!before_rescale()) return false;
     const float alpha = need ? ex2_approx(m_ref - m_new) : 1.f;
     if (need) {
       l *= alpha;
@@ -479,6 +485,7 @@ __device__ __forceinline__ void softmax_row(uint32_t t_lane, uint32_t s_col, uin
   tmem_st32(t_lane + s_col, s);
   tmem_st32(t_lane + s_col + 32, s + 32);
   tmem_st_wait();
+  return true;
 }
 
 template <int D, bool BF16, bool PAGED>
@@ -504,12 +511,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(B(bars->q_full[i]), 1);
       mbar_init(B(bars->q_empty[i]), 1);
-      mbar_init(B(bars->s_full[i]), 1);
-      mbar_init(B(bars->p_full[i]), 128);
       mbar_init(B(bars->pv_done[i]), 1);
       mbar_init(B(bars->o_empty[i]), 128);
       mbar_init(B(bars->o_staged[i]), 128);
     }
+    for (int i = 0; i < 3; ++i) {
+      mbar_init(B(bars->s_full[i]), 1);
+      mbar_init(B(bars->p_full[i]), 128);
+    }
+    mbar_init(B(bars->pv_step), 1);
     mbar_init(B(bars->final_mma), 1);
     bars->abort = 0;
     mbar_fence_init();
@@ -612,12 +622,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool leader = elect_one();
       const uint32_t tS[2] = {tmem, tmem + BN};
       const uint32_t tO[2] = {tmem + 2 * BN, tmem + 2 * BN + D};
-      uint32_t pos = 0, iq[2] = {0, 0}, tc[2] = {0, 0};
+      uint32_t pos = 0, iq[2] = {0, 0}, tc[3] = {0, 0, 0};
       bool ok = true;
       Item it;
       auto qk = [&](int q, int slot) {
         issue_qk<D, BN, BF16>(tS[q], sQ + q * C::Q_BYTES, sRing + slot * C::TILE_BYTES);
         umma_commit(B(bars->s_full[q]));
+      };
+      // zero the rows of V behind the last key of the j-th visited block
+      auto clean = [&](const VarUnit& u, int j, int vslot) {
+        const int live = u.sk - block_at(u, u.j0 + j) * BN;  // rows below sk
+        if (live >= BN) return;
+        uint8_t* v = smem + 2 * C::Q_BYTES + vslot * C::TILE_BYTES;
+        for (int c = 0; c < C::KCH; ++c) {
+          uint4* r = reinterpret_cast<uint4*>(v + c * (BN * 128));
+          for (int i = live * 8 + lane; i < BN * 8; i += 32) r[i] = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
       };
       Items<true> items(p, total);
       for (bool more = items.next(p, it); ok && more;) {
@@ -648,19 +670,40 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         Item coming;  // while the first softmax runs
         more = items.next(p, coming);
-        for (int j = 0; j < n && ok; ++j) {
+        // One tile: its scores alternate between both S buffers, so S(j+1) is made while the
+        // softmax works on S(j); with P V in between, a block took the whole chain's latency.
+        for (int j = 0; j < n && ok && it.tiles == 1; ++j) {
+          const int vslot = pos % C::NSLOT, kslot = (pos + 1) % C::NSLOT;
+          const bool odd = j & 1;
+          if (j + 1 < n) {  // over P(j-1), whose P V is before it in the pipe
+            if (!(ok = mbar_wait(B(bars->full[kslot]), ((pos + 1) / C::NSLOT) & 1, wc))) break;
+            tc_fence_after();
+            if (leader) {
+              issue_qk<D, BN, BF16>(tS[odd ? 0 : 1], sQ, sRing + kslot * C::TILE_BYTES);
+              umma_commit(B(bars->s_full[odd ? 0 : 2]));
+              if (j + 2 == n) umma_commit(B(bars->q_empty[0]));
+              if (!(j + 2 == n && keep[0])) umma_commit(B(bars->empty[kslot]));
+            }
+          }
+          if (!(ok = mbar_wait(B(bars->full[vslot]), (pos / C::NSLOT) & 1, wc))) break;
+          clean(it.u, j, vslot);
+          if (!(ok = mbar_wait(B(bars->p_full[odd ? 2 : 0]), (odd ? tc[2] : tc[0]) & 1, wc))) break;
+          if (odd) ++tc[2]; else ++tc[0];
+          if (j == 0 && iq[0] > 0 && !(ok = mbar_wait(B(bars->o_empty[0]), (iq[0] - 1) & 1, wc)))
+            break;
+          tc_fence_after();
+          if (leader) {
+            issue_pv<D, BN, BF16>(tO[0], tS[odd ? 1 : 0], sRing + vslot * C::TILE_BYTES, j > 0);
+            umma_commit(B(bars->pv_step));
+            if (j == n - 1) umma_commit(B(bars->pv_done[0]));
+            umma_commit(B(bars->empty[vslot]));
+          }
+          pos += (j + 1 < n) ? 2 : 1;
+        }
+        for (int j = 0; j < n && ok && it.tiles == 2; ++j) {
           const int vslot = pos % C::NSLOT, kslot = (pos + 1) % C::NSLOT;
           if (!(ok = mbar_wait(B(bars->full[vslot]), (pos / C::NSLOT) & 1, wc))) break;
-          const int live = it.u.sk - block_at(it.u, it.u.j0 + j) * BN;  // rows below sk
-          if (live < BN) {  // zero the rows of V behind the last key
-            uint8_t* v = smem + 2 * C::Q_BYTES + vslot * C::TILE_BYTES;
-            for (int c = 0; c < C::KCH; ++c) {
-              uint4* r = reinterpret_cast<uint4*>(v + c * (BN * 128));
-              for (int i = live * 8 + lane; i < BN * 8; i += 32) r[i] = make_uint4(0, 0, 0, 0);
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-          }
+          clean(it.u, j, vslot);
           tc_fence_after();
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
@@ -731,9 +774,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int q = warp / 4;
   const int row = (warp % 4) * 32 + lane;
   const uint32_t t_lane = tmem + (static_cast<uint32_t>((warp % 4) * 32) << 16);
-  const uint32_t s_col = q * BN, o_col = 2 * BN + q * D;
+  const uint32_t o_col = 2 * BN + q * D;
   const int tok = row / p.G, head = row - (row / p.G) * p.G;  // of the tile, of the group
-  uint32_t ii = 0, tc = 0, pos = 0;
+  // phases behind: this tile's barriers, those of odd blocks of one-tile items, their P Vs
+  uint32_t ii = 0, tc = 0, tc_odd = 0, steps = 0, pos = 0;
   bool ok = true;
   Item it;
   for (Items<false> items(p, total); ok && items.next(p, it);) {
@@ -759,19 +803,30 @@ __global__ void __launch_bounds__(kThreads, 1)
     float m_ref = -INFINITY, l = 0.f;
     for (int j = it.u.j0; j < it.u.j1; ++j) {
       const int n0 = block_at(it.u, j) * BN;
-      ok = mbar_wait(B(bars->s_full[q]), tc & 1, wc);
+      const bool odd = it.tiles == 1 && ((j - it.u.j0) & 1);
+      const int bar = odd ? 2 : q;
+      ok = mbar_wait(B(bars->s_full[bar]), (odd ? tc_odd : tc) & 1, wc);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after();
-      // S(j) was issued after PV(j-1), so O needs no wait before a rescale
+      // With two tiles S(j) was issued after PV(j-1), so O needs no wait before a rescale; with
+      // one it was issued before.
       if (work)
-        softmax_row<D, BF16>(t_lane, s_col, o_col, block_full(p_lo, p_hi, n0, it.u.sk, p.m), n0,
-                             pos_q, it.u.sk, p.m, m_ref, l);
+        ok = softmax_row<D, BF16>(
+            t_lane, odd || q ? BN : 0, o_col, block_full(p_lo, p_hi, n0, it.u.sk, p.m), n0, pos_q,
+            it.u.sk, p.m, m_ref, l, [&] {
+              if (it.tiles == 2 || j == it.u.j0) return true;
+              const bool done = mbar_wait(B(bars->pv_step), (steps + (j - it.u.j0) - 1) & 1, wc);
+              tc_fence_after();
+              return __all_sync(0xffffffffu, done) != 0;
+            });
+      if (!ok) break;
       tc_fence_before();
-      mbar_arrive(B(bars->p_full[q]));
-      ++tc;
+      mbar_arrive(B(bars->p_full[bar]));
+      if (odd) ++tc_odd; else ++tc;
     }
     if (!ok) break;
+    if (it.tiles == 1) steps += n;
     ok = mbar_wait(B(bars->pv_done[q]), ii & 1, wc);
     ok = __all_sync(0xffffffffu, ok);
     if (!ok) break;
