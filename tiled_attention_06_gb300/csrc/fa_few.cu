@@ -14,8 +14,8 @@
 // to o, a piece to the workspace. A warp takes 16 keys of every tile and keeps its own running
 // maximum, sum and output in registers; the four are joined through shared memory at the end of
 // a segment.
-// 32 sequences of 110,000 keys in all, 32/8 heads of 128, fp16: 79 to 84 us, 6.1 TB/s (the join 4 more;
-// the cache's bytes alone take 72.6 us at the measured copy rate).
+// 32 sequences of 110,000 keys in all, 32/8 heads of 128, fp16: 79 to 84 us, 6.1 TB/s (the join
+// 4 more; the cache's bytes alone take 72.6 us at the measured copy rate).
 // few_merge_kernel joins the pieces of each pair in the order of the keys; the CTA that holds a
 // pair's first piece leaves word of where the others are.
 #include <cuda_bf16.h>
@@ -645,7 +645,7 @@ cudaError_t launch_t(const FewLaunch& L, cudaStream_t stream) {
   const int grid = 2 * L.sms < kFewMaxCtas ? 2 * L.sms : kFewMaxCtas;
   auto* k = few_kernel<D, BF16>;
   constexpr int smem = Cfg<D>::SMEM;
-  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  cudaError_t e = prepare_kernel<few_kernel<D, BF16>>(smem);
   if (e != cudaSuccess) return e;
   k<<<grid, kThreads, smem, stream>>>(L.tmK, L.tmV, L.p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;

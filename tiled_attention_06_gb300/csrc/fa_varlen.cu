@@ -1004,7 +1004,8 @@ cudaError_t launch_t(const VarLaunch& L, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   auto* k = L.p.block_table ? var_fwd_kernel<D, BF16, true> : var_fwd_kernel<D, BF16, false>;
   constexpr int smem = Cfg<D>::SMEM;
-  e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  e = L.p.block_table ? prepare_kernel<var_fwd_kernel<D, BF16, true>>(smem)
+                      : prepare_kernel<var_fwd_kernel<D, BF16, false>>(smem);
   if (e != cudaSuccess) return e;
   const int64_t items = static_cast<int64_t>(L.p.max_units) * L.p.Hkv;
   const int grid = static_cast<int>(items < L.sms ? items : L.sms);

@@ -6,6 +6,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 
@@ -13,6 +14,20 @@
 #include "fa_internal.h"
 
 namespace fa {
+
+// The dynamic shared memory of KERN, set once per device (a driver call otherwise paid per call).
+template <auto KERN>
+inline cudaError_t prepare_kernel(int smem) {
+  static std::atomic<uint64_t> ready{0};  // this kernel: one bit per device index below 64
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? uint64_t{1} << dev : 0;
+  if (bit && (ready.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+  e = cudaFuncSetAttribute(KERN, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess) ready.fetch_or(bit, std::memory_order_release);
+  return e;
+}
 
 // Rotary positions (fa_rope.cu). Token and head steps are in elements. fa_rope: x -> y, H
 // heads, pos[T]. fa_rope_append: x = q and y = q_out with heads d apart, k and v beside it,

@@ -816,7 +816,7 @@ cudaError_t launch_t(const VarBwdLaunch& L, cudaStream_t stream) {
   if (p.total_k > 0) {
     constexpr int smem = Cfg<D>::SMEM;
     auto* k = bwd_main_kernel<D, BF16>;
-    e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    e = prepare_kernel<bwd_main_kernel<D, BF16>>(smem);
     if (e != cudaSuccess) return e;
     k<<<static_cast<unsigned>(p.max_units) * per, kThreads, smem, stream>>>(L.tmQ, L.tmK, L.tmV,
                                                                             L.tmdO, p);

@@ -13,6 +13,7 @@ namespace {
 constexpr int kPlanThreads = 1024;
 constexpr int kBins = 1024;
 static_assert(kBins == kPlanThreads, "the scan takes one bin per thread");
+static_assert(kPlanThreads == 32 * 32, "the scan reads a sum of every one of 32 warps");
 
 // One sequence: first rows and lengths of its queries and keys, and its number of parts.
 struct Seq {
