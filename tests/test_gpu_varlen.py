@@ -79,6 +79,32 @@ def test_other_keys_than_queries(lens_q, lens_k, G, mask):
                   sum(lens_q), f"{lens_q} {lens_k} {mask}")
 
 
+@pytest.mark.parametrize("mask", [(fa.FA_MASK_CAUSAL_WINDOW, 2 ** 31 - 1, 0),
+                                  (fa.FA_MASK_CAUSAL_WINDOW, 2 ** 31 - 1, 2 ** 31 - 1),
+                                  (fa.FA_MASK_BAND, 2 ** 31 - 1, 0),
+                                  (fa.FA_MASK_PREFIX_LM, 0, 2 ** 31 - 1)], ids=str)
+@pytest.mark.parametrize("lens_q,lens_k", [([200, 3], [3, 200]), ([5], [2])], ids=str)
+def test_the_largest_windows_with_more_queries_than_keys(lens_q, lens_k, mask):
+    """Queries before the first key make positions negative: a window takes them out of 32 bits."""
+    H, Hkv, d = 4, 2, 64
+    q, k, v, cu_q, cu_k = case(lens_q, lens_k, H, Hkv, d, torch.float16, seed=7)
+    ref = attention(q, k, v, cu_q, cu_k, 0.125, *mask)
+    o, lse = forward(q.cuda(), k.cuda(), v.cuda(), cu_q, cu_k, 0.125, mask)
+    check_forward(o, lse, ref, torch.float16, sum(lens_q))
+    page = 16  # the same keys in a cache, for few rows and for many
+    width = -(-max(lens_k) // page)
+    kp = torch.zeros(len(lens_k) * width, Hkv, page, d, dtype=torch.float16)
+    vp = torch.zeros_like(kp)
+    for b, n in enumerate(lens_k):
+        for j in range(n):
+            kp[b * width + j // page, :, j % page] = k[cu_k[b] + j]
+            vp[b * width + j // page, :, j % page] = v[cu_k[b] + j]
+    table = torch.arange(len(lens_k) * width, dtype=torch.int32).reshape(-1, width)
+    o, lse = run_paged(q, kp, vp, table, lens_k, cu_q, max(lens_q), 0.125, mask)
+    assert fa.fa_get_device_status() == fa.FA_OK
+    check_forward(o, lse, ref, torch.float16, sum(lens_q))
+
+
 @pytest.mark.parametrize("G", [1, 2, 3, 8, 12, 33, 64, 100, 128])
 def test_group_sizes(G):
     lens = [70, 3, 150]

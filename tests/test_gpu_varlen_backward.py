@@ -86,6 +86,15 @@ def test_gradients_with_other_keys_than_queries(lens_q, lens_k, G, mask):
     check_gradients(got, ref, sum(lens_q), sum(lens_k), f"{lens_q} {lens_k} {mask}")
 
 
+@pytest.mark.parametrize("mask", [(fa.FA_MASK_CAUSAL_WINDOW, 2 ** 31 - 1, 0),
+                                  (fa.FA_MASK_BAND, 2 ** 31 - 1, 0)], ids=str)
+def test_gradients_of_the_largest_windows(mask):
+    q, k, v, dout, cu_q, cu_k = case([200, 3], [3, 200], 4, 2, 64, torch.float16, seed=8)
+    got = step(q.cuda(), k.cuda(), v.cuda(), dout.cuda(), cu_q, cu_k, 0.125, mask)
+    ref = gradients(q, k, v, dout, cu_q, cu_k, 0.125, torch.float16, *mask)
+    check_gradients(got, ref, 203, 203)
+
+
 @pytest.mark.parametrize("G", [2, 3, 8, 12, 33, 64, 100, 128])
 def test_gradients_for_group_sizes(G):
     lens = [70, 3, 150]
