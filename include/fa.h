@@ -484,8 +484,9 @@ fa_status fa_rope_append(const fa_rope_append_params* params, fa_stream_t stream
  *   workspace  device scratch of fa_varlen_workspace_size(...) bytes, 16-byte aligned, owned by
  *              the caller; its contents on entry do not matter. Calls that may overlap on the
  *              GPU, two captured graphs among them, need workspaces of their own.
- * Results do not depend on how the work is spread over the GPU, and are the same on every
- * run. An infinity or NaN in V reaches the queries of its own sequence only.
+ * Results are the same on every run of the same lengths on the same GPU. (Where few sequences
+ * would leave SMs idle, long ones are split, by sizes that depend on the whole batch; the last
+ * bits of a row can then differ from those it has among other neighbours.) An infinity or NaN in V reaches the queries of its own sequence only.
  */
 typedef struct fa_varlen_params {
   const void* q;

@@ -145,7 +145,11 @@ PAGED = dict(q=A, k_pages=A, v_pages=A, block_table=A, ctx_lens=A, cu_seqlens_q=
     (dict(max_pages_per_seq=0), INVALID), (dict(num_pages=0), INVALID),
     (dict(k_pages=None), INVALID), (dict(v_pages=A + 8), INVALID),
     (dict(block_table=None), INVALID), (dict(ctx_lens=A + 1), INVALID),
-    (dict(page_size=4096, max_pages_per_seq=1 << 20), INVALID)], ids=str)
+    (dict(page_size=4096, max_pages_per_seq=1 << 20), INVALID),
+    (dict(page_size=4096, max_pages_per_seq=1 << 18, H=128, Hkv=128, q_token=8192, o_token=8192,
+          max_q=1), INVALID),
+    (dict(page_size=4096, max_pages_per_seq=1 << 18, H=64, Hkv=64, q_token=4096, o_token=4096,
+          max_q=1, B=1 << 9), INVALID)], ids=str)
 def test_paged_varlen_refusals(L, kw, want):
     p = fill(fa.PagedVarlenParams, PAGED, kw)
     assert L.fa_fwd_paged_varlen(ctypes.byref(p), None) == want

@@ -487,6 +487,11 @@ fa_status fa_fwd_paged_varlen(const fa_paged_varlen_params* params, fa_stream_t 
   const long long cap = static_cast<long long>(a.page_size) * a.max_pages_per_seq;
   if (cap > (1LL << 30) || static_cast<long long>(a.num_pages) * a.Hkv > (1LL << 31) - 1)
     return fail(FA_ERR_INVALID_ARG, "problem too large");
+  // few rows number the 64-key tiles of a sequence's K/V heads in 32 bits, and a CTA's run too
+  const bool few = few_rows(a.max_q, a.H / a.Hkv);
+  const long long tiles = (cap + 63) / 64 * a.Hkv;
+  if (few && (tiles > (1LL << 31) - 1 || tiles * a.B > (1LL << 38)))
+    return fail(FA_ERR_INVALID_ARG, "problem too large");
   if (a.total_q == 0) return FA_OK;
   if ((st = check_rows("q", a.q, a.q_token, a.H, a.d)) != FA_OK) return st;
   if ((st = check_rows("o", a.o, a.o_token, a.H, a.d)) != FA_OK) return st;
@@ -508,7 +513,7 @@ fa_status fa_fwd_paged_varlen(const fa_paged_varlen_params* params, fa_stream_t 
   const long long planes = static_cast<long long>(a.num_pages) * a.Hkv;
   const long long plane = static_cast<long long>(a.page_size) * a.d;
   const int pow2 = a.page_size & -a.page_size;
-  if (few_rows(a.max_q, a.H / a.Hkv)) {
+  if (few) {
     fa::FewLaunch F;
     std::memset(&F, 0, sizeof F);
     fa::FewParams& p = F.p;

@@ -165,8 +165,8 @@ static_assert(kCandidates * 32 == kPlanThreads, "a warp per candidate");
 struct PlanSmem {
   SeqScan scan;
   int bins[kBins + 1];
-  // units, largest and sum of their key blocks (used for few units alone), split choice
-  int pairs, n_max, cost, slots, groups, split;
+  // units and the most key blocks of one (used for few units alone), split choice
+  int pairs, n_max, slots, groups, split;
   int blocks[kSplitBelow];  // key blocks of the units, while there are few
   int split_of[kCandidates];
   float cost_of[kCandidates];
@@ -229,7 +229,7 @@ __global__ void __launch_bounds__(kPlanThreads) var_plan_kernel(const VarParams 
   const int tid = threadIdx.x;
   for (int i = tid; i <= kBins; i += kPlanThreads) s.bins[i] = 0;
   if (tid == 0) {
-    s.pairs = s.n_max = s.cost = s.slots = s.groups = 0;
+    s.pairs = s.n_max = s.slots = s.groups = 0;
     s.split = INT_MAX;
   }
   __syncthreads();
@@ -242,7 +242,11 @@ __global__ void __launch_bounds__(kPlanThreads) var_plan_kernel(const VarParams 
       if (!(p.part && s.pairs * p.Hkv < 2 * sms && s.pairs <= kSplitBelow && n_max >= 8)) continue;
       // warp c: sizes from the largest unit (no split) down to a third of an SM's share
       const int c = tid / 32, lane = tid % 32;
-      const float lo = fmaxf(4.f, static_cast<float>(s.cost) * p.Hkv / (3.f * sms));
+      long long cost = 0;  // of all units: 512 of 2^23 key blocks leave 32 bits
+      for (int i = lane; i < s.pairs; i += 32) cost += s.blocks[i];
+#pragma unroll
+      for (int o = 16; o > 0; o /= 2) cost += __shfl_xor_sync(0xffffffffu, cost, o);
+      const float lo = fmaxf(4.f, static_cast<float>(cost) * p.Hkv / (3.f * sms));
       const float f = static_cast<float>(kCandidates - 1 - c) / (kCandidates - 1);
       const int S = c == 0 ? n_max
                            : max(1, min(n_max, static_cast<int>(ceilf(lo * powf(n_max / lo, f)))));
@@ -253,7 +257,7 @@ __global__ void __launch_bounds__(kPlanThreads) var_plan_kernel(const VarParams 
       if (lane == 0) {
         const int items = units * p.Hkv;
         const bool fits = c == 0 || (items <= kVarMaxSplit && units <= p.max_units);
-        const float mean = static_cast<float>(s.cost) / units;
+        const float mean = static_cast<float>(cost) / units;
         s.cost_of[c] = !fits ? INFINITY
                              : fmaxf(S + 4.f, ((items + sms - 1) / sms) * (mean + 4.f)) +
                                    (units > s.pairs ? 8.f : 0.f);
@@ -277,8 +281,8 @@ __global__ void __launch_bounds__(kPlanThreads) var_plan_kernel(const VarParams 
     if (pass == kWrite) {
       const int units = scan_bins(s.scan, s.bins);
       if (tid == 0) {  // more than fit only when starts overlap, which no packed rows have
-        p.hdr->units = min(units, p.max_units);
-        if (units > p.max_units) atomicOr(p.m.status, FA_DEV_BAD_PAGE);
+        p.hdr->units = max(0, min(units, p.max_units));
+        if (units < 0 || units > p.max_units) atomicOr(p.m.status, FA_DEV_BAD_PAGE);
       }
     }
     auto visit = [&](VarUnit u) {
@@ -287,7 +291,6 @@ __global__ void __launch_bounds__(kPlanThreads) var_plan_kernel(const VarParams 
         const int i = atomicAdd(&s.pairs, 1);
         if (i < kSplitBelow) s.blocks[i] = n;
         atomicMax(&s.n_max, n);
-        atomicAdd(&s.cost, n);
       }
       if (pass == kWrite && ns > 1) {
         u.slot = atomicAdd(&s.slots, ns);
@@ -298,7 +301,7 @@ __global__ void __launch_bounds__(kPlanThreads) var_plan_kernel(const VarParams 
         u.j1 = static_cast<int>(static_cast<long long>(n) * (k + 1) / ns);
         const int bin = cost_bin(u.j1 - u.j0, p.cost_shift);
         const int at = atomicAdd(&s.bins[pass == kWrite ? bin : bin + 1], 1);
-        if (pass == kWrite && at < p.max_units) p.units[at] = u;
+        if (pass == kWrite && at >= 0 && at < p.max_units) p.units[at] = u;
         if (ns > 1) ++u.slot;
       }
     };
@@ -326,7 +329,7 @@ __global__ void __launch_bounds__(kPlanThreads) var_plan_kernel(const VarParams 
           u.slot = slot + k;
           const int bin = cost_bin(u.j1 - u.j0, p.cost_shift);
           const int at = atomicAdd(&s.bins[pass == kWrite ? bin : bin + 1], 1);
-          if (pass == kWrite && at < p.max_units) p.units[at] = u;
+          if (pass == kWrite && at >= 0 && at < p.max_units) p.units[at] = u;
         }
       }
       __syncthreads();

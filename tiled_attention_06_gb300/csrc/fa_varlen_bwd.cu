@@ -163,14 +163,14 @@ __global__ void __launch_bounds__(kPlanThreads) bwd_plan_kernel(const VarBwdPara
     if (pass == 1) {
       const int units = scan_bins(s.scan, s.bins);
       if (threadIdx.x == 0) {  // more than fit only when starts overlap, which no packed rows have
-        p.n_units[0] = min(units, p.max_units);
-        if (units > p.max_units) atomicOr(p.m.status, FA_DEV_BAD_PAGE);
+        p.n_units[0] = max(0, min(units, p.max_units));
+        if (units < 0 || units > p.max_units) atomicOr(p.m.status, FA_DEV_BAD_PAGE);
       }
     }
     auto visit = [&](const VarBwdUnit& u) {
       const int bin = cost_bin(u.n, p.cost_shift);
       const int at = atomicAdd(&s.bins[pass ? bin : bin + 1], 1);
-      if (pass && at < p.max_units) p.units[at] = u;
+      if (pass && at >= 0 && at < p.max_units) p.units[at] = u;
     };
     if (one_pass) {
       if (has) visit(mine);
