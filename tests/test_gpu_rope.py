@@ -210,3 +210,42 @@ def test_append_reports_and_skips_bad_slots():
     assert torch.equal(vp[2, :, 15], qkv[2, H + 1:])  # position 31 is the last slot
     assert (vp[2, :, :15] == 0).all()
     assert (out != 0).any(-1).all()  # every q is rotated
+
+
+@pytest.mark.parametrize("style", [fa.FA_ROPE_HALF, fa.FA_ROPE_PAIRS])
+def test_append_of_many_sequences(style):
+    """More sequences than a CTA has threads, and CTAs whose tokens belong to several of them."""
+    H, Hkv, d, page, B, dtype = 2, 1, 64, 16, 901, torch.bfloat16
+    new, before = [(3 * b) % 8 for b in range(B)], [(5 * b) % 30 for b in range(B)]
+    T, cu = sum(new), starts(new)
+    assert T > 16 * 152  # several tokens per CTA
+    width, pages = 3, B * 3
+    qkv = draw((T, H + 2 * Hkv, d), dtype, seed=11)
+    table = torch.randperm(pages, generator=torch.Generator().manual_seed(2)).reshape(B, width)
+    kg, vg = (torch.full((pages, Hkv, page, d), float("nan"), dtype=dtype, device="cuda")
+              for _ in range(2))
+    freqs, amp = fa.fa_rope_freqs(d)
+    x = qkv.cuda()
+    out = torch.full((T, H, d), float("nan"), dtype=dtype, device="cuda")
+    args = (x[:, :H], x[:, H:H + Hkv], x[:, H + Hkv:], out, kg, vg, table.to(torch.int32).cuda(),
+            torch.tensor(before, dtype=torch.int32).cuda(),
+            torch.tensor(cu, dtype=torch.int32).cuda(), freqs.cuda(), style, amp)
+    graph = torch.cuda.CUDAGraph()  # once captured, once by itself: the same bits
+    with torch.cuda.graph(graph):
+        fa.fa_rope_append(*args)
+    graph.replay()
+    torch.cuda.synchronize()
+    first = [t.clone() for t in (out, kg, vg)]
+    fa.fa_rope_append(*args)
+    assert fa.fa_get_device_status() == fa.FA_OK
+    for a, b in zip(first, (out, kg, vg)):
+        assert torch.equal(a.view(torch.int16), b.view(torch.int16))
+    seq = torch.repeat_interleave(torch.arange(B), torch.tensor(new))
+    pos = torch.tensor(before)[seq] + torch.arange(T) - torch.tensor(cu)[seq]
+    at = (table[seq, pos // page], slice(None), pos % page)
+    half = style == fa.FA_ROPE_HALF
+    for src, have in ((qkv[:, :H], out.cpu()), (qkv[:, H:H + Hkv], kg.cpu()[at])):
+        err = (have.double() - rotate(src, pos, freqs, d, half, amp)).abs()
+        assert (err <= limit(src, d, half, amp, dtype)).all()
+    assert torch.equal(vg.cpu()[at], qkv[:, H + Hkv:])
+    assert int((~vg.isnan()).any(-1).sum()) == T * Hkv

@@ -422,3 +422,73 @@ def test_scores_that_climb(new, dt):
         # sum of |q k| up to 300 in 64 terms: 2^-13), and the weights' by as much
         check_forward(o, None, (ref[0], ref[1], ref[2] * (1 + 2.0 ** -4)), DT[dt], new)
         assert float((lse[:new].double().cpu() - ref[1][:new]).abs().max()) <= 2.0 ** -10
+
+
+@pytest.mark.parametrize("H,Hkv", [(4, 2), (32, 1)])
+def test_more_sequences_than_the_plan_has_threads(H, Hkv):
+    """1500 sequences of 0 to 3 tokens: by themselves and as chunks over a cache."""
+    d, dt = 64, torch.float16
+    lens = [(5 * b) % 4 for b in range(1500)]
+    q, k, v, cu, _ = case(lens, lens, H, Hkv, d, dt, seed=9, pad=1)
+    o, lse = forward(q.cuda(), k.cuda(), v.cuda(), cu, cu, 0.125)
+    check_forward(o, lse, attention(q, k, v, cu, cu, 0.125, fa.FA_MASK_CAUSAL), dt, sum(lens))
+    assert o[sum(lens):].isnan().all()
+    before = [(7 * b) % 40 for b in range(1500)]
+    q, k, v, kp, vp, table, total, cu, cu_k = paged_case(lens, before, H, Hkv, d, 16, dt, seed=9)
+    o, lse = run_paged(q, kp, vp, table, total, cu, 3, 0.125)
+    assert fa.fa_get_device_status() == fa.FA_OK
+    check_forward(o, lse, attention(q, k, v, cu, cu_k, 0.125, fa.FA_MASK_CAUSAL), dt, sum(lens))
+    assert o[sum(lens):].isnan().all() and lse[sum(lens):].isnan().all()
+
+
+@pytest.mark.parametrize("max_q", [3, 40])
+def test_captured_paged_call_follows_lengths_pages_and_chunks(max_q):
+    """One graph, replayed after the lengths, the table and the chunks have changed."""
+    H, Hkv, d, page, dt = 8, 2, 128, 16, torch.bfloat16
+    B, width, T = 3, 30, 3 * max_q
+    o = torch.zeros(T, H, d, dtype=dt, device="cuda")
+    lse = torch.zeros(T, H, device="cuda")
+    pool = torch.zeros(B * width + 4, Hkv, page, d, dtype=dt, device="cuda")
+    kp, vp, q = pool, pool.clone(), torch.zeros_like(o)
+    table = torch.zeros(B, width, dtype=torch.int32, device="cuda")
+    ctx, cu = i32([0] * B), i32([0] * (B + 1))
+    ws = torch.empty(fa.fa_paged_varlen_workspace_size(B, H, Hkv, T, max_q, width, page, d),
+                     dtype=torch.uint8, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        fa.fa_fwd_paged_varlen(q, kp, vp, table, ctx, cu, max_q, o, lse, 0.09, ws)
+    for new, before in (([1, 1, 1], [9, 0, 400]), ([3, 0, 2], [60, 17, 1]),
+                        ([max_q, 1, max_q], [200, 3, 5]), ([0, 0, 0], [4, 5, 6])):
+        qc, kc, vc, kpc, vpc, tc, total, cuc, cu_k = paged_case(new, before, H, Hkv, d, page, dt,
+                                                                seed=sum(before), pad=0)
+        q[:sum(new)] = qc.cuda()
+        kp[:kpc.shape[0]], vp[:vpc.shape[0]] = kpc.cuda(), vpc.cuda()
+        table.fill_(-1)
+        table[:, :tc.shape[1]] = tc.cuda()
+        ctx.copy_(i32(total))
+        cu.copy_(i32(cuc))
+        o.fill_(float("nan"))
+        lse.fill_(float("nan"))
+        graph.replay()
+        assert fa.fa_get_device_status() == fa.FA_OK
+        check_forward(o, lse, attention(qc, kc, vc, cuc, cu_k, 0.09, fa.FA_MASK_CAUSAL), dt,
+                      sum(new), f"{new} {before}")
+        assert o[sum(new):].isnan().all() and lse[sum(new):].isnan().all()
+
+
+@pytest.mark.parametrize("new", [2, 50])
+def test_masks_that_leave_rows_of_a_cached_chunk_empty(new):
+    """A band over fewer keys than queries: rows far before the first key see nothing."""
+    H, Hkv, d, page, dt = 4, 2, 64, 16, torch.float16
+    keys = max(1, new // 5)
+    q, k, v, cu_q, cu_k = case([new, new], [keys, keys], H, Hkv, d, dt, seed=new)
+    kp = torch.full((2, Hkv, page, d), float("nan"), dtype=dt)
+    vp = kp.clone()
+    for b in range(2):
+        kp[b, :, :keys] = k[b * keys:(b + 1) * keys].transpose(0, 1)
+        vp[b, :, :keys] = v[b * keys:(b + 1) * keys].transpose(0, 1)
+    table = torch.tensor([[0], [1]], dtype=torch.int32)
+    mask = (fa.FA_MASK_BAND, 0, 0)
+    o, lse = run_paged(q, kp, vp, table, [keys, keys], cu_q, new, 0.125, mask)
+    assert fa.fa_get_device_status() == fa.FA_OK
+    check_forward(o, lse, attention(q, k, v, cu_q, cu_k, 0.125, *mask), dt, 2 * new)

@@ -129,6 +129,16 @@ def test_infinities_of_one_sequence_stay_there():
                         10 ** 9)
 
 
+@pytest.mark.parametrize("H,Hkv", [(4, 2), (32, 1)])
+def test_gradients_of_more_sequences_than_the_plan_has_threads(H, Hkv):
+    lens = [(5 * b) % 4 for b in range(1500)]
+    q, k, v, dout, cu, _ = case(lens, lens, H, Hkv, 64, torch.float16, seed=9, pad=1)
+    got = step(q.cuda(), k.cuda(), v.cuda(), dout.cuda(), cu, cu, 0.125)
+    ref = gradients(q, k, v, dout, cu, cu, 0.125, torch.float16, fa.FA_MASK_CAUSAL)
+    check_gradients(got, ref, sum(lens), sum(lens))
+    assert all(x[sum(lens):].isnan().all() for x in got)
+
+
 def test_slices_of_a_fused_projection_as_inputs_and_outputs():
     H, Hkv, d, lens = 6, 2, 64, [40, 129]
     T, cu = sum(lens), starts(lens)
