@@ -163,7 +163,7 @@ constexpr int kSplitBelow = 512;  // units (of one K/V head) above which nothing
 static_assert(kCandidates * 32 == kPlanThreads, "a warp per candidate");
 
 struct PlanSmem {
-  SeqScan scan;
+  SeqScan<kPlanThreads> scan;
   int bins[kBins + 1];
   // units and the most key blocks of one (used for few units alone), split choice
   int pairs, n_max, slots, groups, split;

@@ -10,10 +10,9 @@
 // sequence or the block on the causal diagonal fills a half with few tokens of many heads.
 //
 // Kernels:
-//   bwd_plan      one CTA: key blocks of all sequences with the halves that see them, sorted so
-//                 that the longest start first.
 //   bwd_prep      per half: -LSE log2(e) and -D of its 64 rows, and zeros of its part of the
-//                 FP32 dQ accumulator (HBM-bound).
+//                 FP32 dQ accumulator (HBM-bound). Beside them one CTA plans: key blocks of all
+//                 sequences with the halves that see them, sorted so that the longest start first.
 //   bwd_main      per half: S^T = K Q^T and dP^T = V dO^T (tcgen05); P^T and dS^T by the
 //                 elementwise warps, P^T in 16 bits over its TMEM columns, dS^T into shared
 //                 memory; then dV += P^T dO, dK += dS^T Q, dQ^T = K^T dS^T, the last added into
@@ -21,10 +20,10 @@
 //                 warpgroups (two per half in flight, 32 columns each), TMA warp, MMA warp.
 //   bwd_dq        scales and rounds the accumulator into dq (HBM-bound).
 //   bwd_sum       HS > 1 alone: sums the head subsets' dk and dv, in order.
-// Bounds. 11343 tokens in 4 sequences, 32/8 heads of 128, bf16, causal: 797 us, 979 TFLOP/s over
+// Bounds. 11343 tokens in 4 sequences, 32/8 heads of 128, bf16, causal: 795 us, 981 TFLOP/s over
 // the five products (51 % of 1923.5 measured); the main kernel 665 of them (1173 TFLOP/s, MMAs of
 // N = 64 issued by one thread and the elementwise warps in turn), prep 62 and dq 51, both at about
-// 5.5 TB/s of mostly accumulator traffic. 24 short sequences, 12/4 heads of 64: 44 us, four
+// 5.5 TB/s of mostly accumulator traffic. 24 short sequences, 12/4 heads of 64: 39 us, three
 // launches and a CTA's fixed 9 us around 7 halves.
 //
 // Rows of K, Q and dO behind a sequence's end belong to others: they are zeroed in shared
@@ -117,8 +116,13 @@ __device__ __forceinline__ Span queries_of_block(int j0, int n, int sq, int delt
 
 // ------------------------------------------------------------------ plan
 
+// The plan is one CTA of bwd_prep: a launch of its own, 1024 threads, put its 4 to 5 us before
+// everything else (24 short sequences 43.6 us against 39.1 here, 11343 tokens in 4 sequences 806
+// against 795). Thousands of tiny sequences lose a little by the fewer threads (4096 of 1 to 8
+// tokens, 8 heads on one: 220 -> 229 us; on 12/4 heads they gain, 766 -> 744).
+constexpr int kPrepThreads = 256;
 struct BwdPlanSmem {
-  SeqScan scan;
+  SeqScan<kPrepThreads> scan;
   int bins[kBins + 1];
 };
 
@@ -150,9 +154,8 @@ __device__ __forceinline__ void for_each_key_block(const VarBwdParams& p, BwdPla
       });
 }
 
-__global__ void __launch_bounds__(kPlanThreads) bwd_plan_kernel(const VarBwdParams p) {
-  __shared__ BwdPlanSmem s;
-  for (int i = threadIdx.x; i <= kBins; i += kPlanThreads) s.bins[i] = 0;
+__device__ __noinline__ void bwd_plan(const VarBwdParams& p, BwdPlanSmem& s) {
+  for (int i = threadIdx.x; i <= kBins; i += kPrepThreads) s.bins[i] = 0;
   __syncthreads();
   // two passes, counting and writing, that share one copy of the code; units stay in registers
   // when there are no more of them than threads
@@ -180,7 +183,7 @@ __global__ void __launch_bounds__(kPlanThreads) bwd_plan_kernel(const VarBwdPara
         has = true;
         visit(u);
       });
-      one_pass = p.B <= kPlanThreads && s.scan.off[p.B] <= kPlanThreads;
+      one_pass = p.B <= kPrepThreads && s.scan.off[p.B] <= kPrepThreads;
     }
   }
 }
@@ -230,22 +233,28 @@ __device__ __forceinline__ float dot8(const uint4& a, const uint4& b) {
 }
 
 template <int D, bool BF16>
-__global__ void __launch_bounds__(256) bwd_prep_kernel(const VarBwdParams p) {
-  constexpr int LPR = D / 8;          // lanes per row, 16 bytes each
-  constexpr int RPP = 256 / LPR;      // rows per pass
+__global__ void __launch_bounds__(kPrepThreads, 6)
+    bwd_prep_kernel(const __grid_constant__ VarBwdParams p) {
+  constexpr int LPR = D / 8;               // lanes per row, 16 bytes each
+  constexpr int RPP = kPrepThreads / LPR;  // rows per pass
+  __shared__ BwdPlanSmem plan;
   __shared__ HalfRows sh;
-  const int hh = blockIdx.y;          // K/V head x head subset
+  if (blockIdx.x == 0) {  // the plan, beside the other CTAs' work
+    if (blockIdx.y == 0) bwd_plan(p, plan);
+    return;
+  }
+  const int hh = blockIdx.y;  // K/V head x head subset
   const int kvh = hh / p.HS, h0 = kvh * p.G + (hh % p.HS) * p.GS;
   if (threadIdx.x < 32) {
-    const HalfRows f = half_rows(p, blockIdx.x);
+    const HalfRows f = half_rows(p, blockIdx.x - 1);
     if (threadIdx.x == 0) sh = f;
   }
   __syncthreads();
   const HalfRows r = sh;
   if (r.n == 0) return;
-  const size_t slot = static_cast<size_t>(hh) * p.slots + blockIdx.x;
+  const size_t slot = static_cast<size_t>(hh) * p.slots + blockIdx.x - 1;
   float4* acc = reinterpret_cast<float4*>(p.dqacc + slot * kHalf * D);
-  for (int i = threadIdx.x; i < kHalf * D / 4; i += 256) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i = threadIdx.x; i < kHalf * D / 4; i += kPrepThreads) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
   float* st = p.stats + slot * 2 * kHalf;
   const int c = threadIdx.x % LPR;
 #pragma unroll
@@ -806,13 +815,10 @@ cudaError_t launch_t(const VarBwdLaunch& L, cudaStream_t stream) {
   const VarBwdParams& p = L.p;
   const int per = p.Hkv * p.HS;
   cudaError_t e;
-  bwd_plan_kernel<<<1, kPlanThreads, 0, stream>>>(p);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
   const dim3 slots(p.slots, per);
-  if (p.total_q > 0) {
-    bwd_prep_kernel<D, BF16><<<slots, 256, 0, stream>>>(p);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  }
+  const dim3 prep = p.total_q > 0 ? dim3(p.slots + 1, per) : dim3(1, 1);  // CTA (0, 0) plans
+  bwd_prep_kernel<D, BF16><<<prep, kPrepThreads, 0, stream>>>(p);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
   if (p.total_k > 0) {
     constexpr int smem = Cfg<D>::SMEM;
     auto* k = bwd_main_kernel<D, BF16>;
