@@ -139,9 +139,10 @@ BwdLayout bwd_layout(int B, int H, int Hkv, int total_q, int total_k, int d) {
   // d = 64) for each; under a causal mask a block sees half the queries on average and the first
   // block all of them. Subsets cost a summing pass (5 us, and their partials at 4 TB/s).
   // One sequence of 4096, 8 heads on one: HS = 8 takes 137 us, 4 takes 210; 24 short ones of
-  // d = 64, 12 heads on 4: HS = 1 takes 44 us, 3 takes 61.
+  // d = 64, 12 heads on 4: HS = 1 takes 44 us, 3 takes 61 (a planning launch of 5 us in all four).
   const double units = (total_k / 128 + (B + 1) / 2) * static_cast<double>(Hkv);
-  const double all = static_cast<double>(total_q) / B * G / fa::kBwdHalf, each = d == 128 ? 1.1 : 0.6;
+  const double all = static_cast<double>(total_q) / B * G / fa::kBwdHalf;
+  const double each = d == 128 ? 1.1 : 0.6;
   double best = 0;
   L.HS = 0;
   for (int hs = 1; hs <= G; ++hs) {
