@@ -389,9 +389,10 @@ fa_status fa_decode_paged_noalloc(const void* q, const void* k_pages, const void
  * to nobody and no output row of theirs is written. H query heads share Hkv K/V heads, H a
  * multiple of Hkv: query head h reads K/V head h / (H / Hkv). H / Hkv is at most 128.
  * Everything about lengths is read on the device, so a captured graph may be replayed after
- * they change. A start outside [0, total], a decreasing one, or a length beyond a cache's
- * capacity is reported as FA_ERR_BAD_PAGE by fa_get_device_status; such a sequence counts as
- * empty (starts) or is cut to the capacity (lengths).
+ * they change. A sequence whose starts make no sense (cu[b] < 0, cu[b+1] < cu[b] or cu[b+1]
+ * above the number of rows) counts as empty, a length beyond a cache's capacity is cut to it;
+ * either is reported as FA_ERR_BAD_PAGE by fa_get_device_status. Other sequences keep their
+ * results (but for rows that several of them claim, as can be after a decreasing start).
  */
 
 /* Layout of the rotated pairs: (i, i + R/2), or (2i, 2i + 1). */

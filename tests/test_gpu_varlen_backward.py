@@ -296,3 +296,75 @@ def test_serving_chunks_then_single_tokens():
         check_forward(o, lse, attention(q_rot.cpu(), k, v, cu, cu_k, scale, fa.FA_MASK_CAUSAL), dt,
                       T, f"{new}")
     assert have == total
+
+
+def bad_starts(B, seed):
+    """Starts of B sequences of 0 to 7 tokens with bad ones: three below zero, one beyond the
+    rows, and a decreasing one that is followed by another beyond the rows."""
+    g = torch.Generator().manual_seed(seed)
+    cu = starts(torch.randint(0, 8, (B,), generator=g).tolist())
+    T = cu[-1]
+    for b in (0, B // 3, B - 40):
+        cu[b] = -7 - b
+    cu[B // 2] = T + 50
+    cu[B // 4], cu[B // 4 + 1] = 3, T + 9
+    return cu, T
+
+
+BAD = {"end": [0, 40, 65], "falls": [0, 40, 20], "first": [-1, 20, 64], "below": [0, 10, 20, -5, 30],
+       "far below": [0, 10, 20, -2 ** 31, 30], "far above": [0, 10, 20, 2 ** 31 - 1, 30],
+       "no rows": [0, 64, 70], "disorder": [32, 64, 0, 32]}
+
+
+@pytest.mark.parametrize("name", list(BAD) + ["many"])
+@pytest.mark.parametrize("H,Hkv,d,dt", [(2, 1, 64, "f16"), (8, 1, 128, "bf16"), (3, 3, 64, "bf16")])
+def test_bad_starts_leave_the_gradients_of_other_sequences(name, H, Hkv, d, dt):
+    """Valid sequences get their gradients, rows that no valid sequence owns are left alone,
+    whatever the workspace held."""
+    cu, T = bad_starts(700, 3) if name == "many" else (BAD[name], 64)
+    B, dtype = len(cu) - 1, DT[dt]
+    q, k, v, dout, _, _ = case([T], [T], H, Hkv, d, dtype, seed=T + H)
+    gq, gk, gv, gd = (x.cuda() for x in (q, k, v, dout))
+    o, dq = (torch.full((T, H, d), float("nan"), dtype=dtype, device="cuda") for _ in range(2))
+    dk, dv = (torch.full((T, Hkv, d), float("nan"), dtype=dtype, device="cuda") for _ in range(2))
+    lse = torch.full((T, H), float("nan"), device="cuda")
+    size = max(fa.fa_varlen_workspace_size(B, H, Hkv, T, T, d),
+               fa.fa_bwd_varlen_workspace_size(B, H, Hkv, T, T, d))
+    ws = torch.full((size,), 255, dtype=torch.uint8, device="cuda")
+    c, scale = i32(cu), 1 / math.sqrt(d)
+    fa.fa_fwd_varlen(gq, gk, gv, o, lse, c, c, scale, ws)
+    assert fa.fa_get_device_status() == fa.FA_ERR_BAD_PAGE
+    ws.fill_(255)
+    fa.fa_bwd_varlen(gq, gk, gv, o, gd, lse, dq, dk, dv, c, c, scale, ws)
+    assert fa.fa_get_device_status() == fa.FA_ERR_BAD_PAGE
+    rows = torch.ones(T, dtype=torch.bool)
+    for a, b in [(a, b) for a, b in zip(cu, cu[1:]) if 0 <= a <= b <= T]:
+        rows[a:b] = False
+        ref = gradients(q[a:b], k[a:b], v[a:b], dout[a:b], [0, b - a], [0, b - a], scale, dtype,
+                        fa.FA_MASK_CAUSAL)
+        check_gradients((dq[a:b], dk[a:b], dv[a:b]), ref, b - a, b - a, f"{name} [{a}, {b})")
+    for x in (dq, dk, dv):
+        assert x[rows.cuda()].isnan().all()
+
+
+def test_bad_starts_of_one_side_leave_the_gradients_of_other_sequences():
+    H, Hkv, d, T, dtype = 4, 2, 64, 64, torch.float16
+    q, k, v, dout, _, _ = case([T], [T], H, Hkv, d, dtype, seed=5)
+    gq, gk, gv, gd = (x.cuda() for x in (q, k, v, dout))
+    for cu_q, cu_k in (([0, 10, 20, -5, 30], [0, 12, 30, 40, 64]),
+                       ([0, 12, 30, 40, 64], [0, 10, 20, -5, 30])):
+        o, dq = (torch.full((T, H, d), float("nan"), dtype=dtype, device="cuda") for _ in range(2))
+        dk, dv = (torch.full((T, Hkv, d), float("nan"), dtype=dtype, device="cuda")
+                  for _ in range(2))
+        lse = torch.full((T, H), float("nan"), device="cuda")
+        size = max(fa.fa_varlen_workspace_size(4, H, Hkv, T, T, d),
+                   fa.fa_bwd_varlen_workspace_size(4, H, Hkv, T, T, d))
+        ws = torch.full((size,), 255, dtype=torch.uint8, device="cuda")
+        fa.fa_fwd_varlen(gq, gk, gv, o, lse, i32(cu_q), i32(cu_k), 0.125, ws)
+        ws.fill_(255)
+        fa.fa_bwd_varlen(gq, gk, gv, o, gd, lse, dq, dk, dv, i32(cu_q), i32(cu_k), 0.125, ws)
+        assert fa.fa_get_device_status() == fa.FA_ERR_BAD_PAGE
+        ref = gradients(q[:cu_q[2]], k[:cu_k[2]], v[:cu_k[2]], dout[:cu_q[2]], cu_q[:3], cu_k[:3],
+                        0.125, dtype, fa.FA_MASK_CAUSAL)
+        check_gradients((dq, dk, dv), ref, cu_q[2], cu_k[2], f"{cu_q} {cu_k}")
+        assert dk[cu_k[2]:].isnan().all() and dv[cu_k[2]:].isnan().all()

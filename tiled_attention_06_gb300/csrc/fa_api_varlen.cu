@@ -129,7 +129,7 @@ VarLayout var_layout(int B, int H, int Hkv, int total_q, int d) {
 // How the backward deals a group's heads and lays its workspace out (fa_varlen.h).
 struct BwdLayout {
   int HS, GS, TPH, slots, max_units;
-  size_t units, stats, dqacc, part, total;
+  size_t units, seq_slot, stats, dqacc, part, total;
 };
 BwdLayout bwd_layout(int B, int H, int Hkv, int total_q, int total_k, int d) {
   BwdLayout L;
@@ -162,8 +162,9 @@ BwdLayout bwd_layout(int B, int H, int Hkv, int total_q, int total_k, int d) {
       std::min<long long>(static_cast<long long>(total_k) / 128 + B, std::max(total_k, 1)));
   const size_t planes = static_cast<size_t>(Hkv) * L.HS * L.slots;
   L.units = 64;
-  L.stats = L.units + round16(sizeof(fa::VarBwdUnit) * static_cast<size_t>(L.max_units));
-  L.dqacc = L.stats + planes * 2 * fa::kBwdHalf * sizeof(float);
+  L.seq_slot = L.units + round16(sizeof(fa::VarBwdUnit) * static_cast<size_t>(L.max_units));
+  L.stats = L.seq_slot + round16(sizeof(int32_t) * static_cast<size_t>(B));
+  L.dqacc = L.stats + round16(2 * static_cast<size_t>(total_q) * H * sizeof(float));
   L.part = L.dqacc + planes * fa::kBwdHalf * d * sizeof(float);
   L.total = L.part + (L.HS > 1 ? static_cast<size_t>(L.HS) * 2 * total_k * Hkv * d * sizeof(float)
                                : 0);
@@ -641,6 +642,7 @@ fa_status fa_bwd_varlen(const fa_varlen_params* params, const fa_varlen_grads* g
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
   p.n_units = reinterpret_cast<int32_t*>(ws);
   p.units = reinterpret_cast<fa::VarBwdUnit*>(ws + B.units);
+  p.seq_slot = reinterpret_cast<int32_t*>(ws + B.seq_slot);
   p.stats = reinterpret_cast<float*>(ws + B.stats);
   p.dqacc = reinterpret_cast<float*>(ws + B.dqacc);
   p.part = reinterpret_cast<float*>(ws + B.part);

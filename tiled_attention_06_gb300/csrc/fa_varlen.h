@@ -123,8 +123,9 @@ cudaError_t launch_varlen(const VarLaunch& L, int D, bool bf16, cudaStream_t str
 // The query side moves in halves of 64 rows: TPH = 64 / GS consecutive tokens of a sequence with
 // GS heads of one group (row r: token r / GS, head r % GS). A group's G heads are dealt to HS
 // subsets of GS = G / HS when few key blocks would keep few SMs busy for long; each subset then
-// has its own partial dk and dv. A half's slot: sequence b's halves start at cu[b] / TPH + b, which
-// leaves room for every sequence's rounding without a scan.
+// has its own partial dk and dv. A half's slot in the dq accumulator: sequence b's halves start at
+// cu[b] / TPH + b, which leaves room for every sequence's rounding without a scan (where a start is
+// bad, the plan deals slots out instead).
 constexpr int kBwdHalf = 64;
 
 struct VarBwdUnit {  // one block of 128 keys (48 bytes), written by the plan kernel
@@ -151,9 +152,10 @@ struct VarBwdParams {
   int max_units;  // entries of `units`
   int cost_shift;
   // workspace
-  int32_t* n_units;   // [16]
+  int32_t* n_units;   // [16]: units; whether the slots were dealt out
   VarBwdUnit* units;
-  float* stats;       // [Hkv HS][slots][2][64]: -lse log2(e), -D
+  int32_t* seq_slot;  // [B]: first slot of the sequence or -1, where slots were dealt out
+  float* stats;       // [2][Hkv HS][total_q][GS]: -lse log2(e), -D
   float* dqacc;       // [Hkv HS][slots][16 groups of 4 rows][D][4]
   float* part;        // HS > 1: [HS][2 (dk, dv)][total_k][Hkv][D]
 };

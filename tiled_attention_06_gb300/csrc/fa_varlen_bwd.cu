@@ -10,8 +10,8 @@
 // sequence or the block on the causal diagonal fills a half with few tokens of many heads.
 //
 // Kernels:
-//   bwd_prep      per half: -LSE log2(e) and -D of its 64 rows, and zeros of its part of the
-//                 FP32 dQ accumulator (HBM-bound). Beside them one CTA plans: key blocks of all
+//   bwd_prep      -LSE log2(e) and -D of every row, whichever sequence it belongs to, and zeros of
+//                 the FP32 dQ accumulator (HBM-bound). Beside them one CTA plans: key blocks of all
 //                 sequences with the halves that see them, sorted so that the longest start first.
 //   bwd_main      per half: S^T = K Q^T and dP^T = V dO^T (tcgen05); P^T and dS^T by the
 //                 elementwise warps, P^T in 16 bits over its TMEM columns, dS^T into shared
@@ -124,16 +124,32 @@ constexpr int kPrepThreads = 256;
 struct BwdPlanSmem {
   SeqScan<kPrepThreads> scan;
   int bins[kBins + 1];
+  int bad, next;  // cu_q has a bad start; first free slot of such a call
 };
+
+// Slots of a call's halves. The halves of sequence b start at slot cu[b] / TPH + b, which needs no
+// scan but non-decreasing starts. In a call with a bad start, sequences that are valid by themselves
+// may lie in any order and share slots that way; there the plan deals the slots out, and leaves
+// each sequence's first one (or -1) in seq_slot.
+enum { kCount, kDeal, kWrite };
 
 template <typename F>
 __device__ __forceinline__ void for_each_key_block(const VarBwdParams& p, BwdPlanSmem& s,
-                                                   bool report, F f) {
+                                                   int pass, bool dealt, F f) {
   for_each_part(
       s.scan, p.B,
       [&](int b) {
         const SeqRows q = rows_of(p.cu_q, b, p.total_q), k = rows_of(p.cu_k, b, p.total_k);
-        if ((q.bad || k.bad) && report) atomicOr(p.m.status, FA_DEV_BAD_PAGE);
+        if (pass == kCount) {
+          if (q.bad || k.bad) atomicOr(p.m.status, FA_DEV_BAD_PAGE);
+          if (q.bad) s.bad = 1;
+        }
+        if (pass == kDeal) {
+          const int n = (q.n + p.TPH - 1) / p.TPH;
+          int at = n > 0 ? atomicAdd(&s.next, n) : -1;
+          if (at < 0 || at > p.slots - n) at = -1;  // only where sequences overlap
+          p.seq_slot[b] = at;
+        }
         // a sequence whose starts make no sense counts as empty on both sides
         const int sq = k.bad ? 0 : q.n, sk = q.bad ? 0 : k.n;
         return Seq{q.first, sq, k.first, sk, (sk + kBT - 1) / kBT};
@@ -149,41 +165,51 @@ __device__ __forceinline__ void for_each_key_block(const VarBwdParams& p, BwdPla
         const Span see = queries_of_block(u.j0, u.nk, u.sq, u.delta, p.m);
         u.h0 = see.lo <= see.hi ? see.lo / p.TPH : 0;
         u.n = see.lo <= see.hi ? see.hi / p.TPH - u.h0 + 1 : 0;
-        u.slot0 = q.q0 / p.TPH + b;
+        u.slot0 = dealt ? p.seq_slot[b] : q.q0 / p.TPH + b;
+        if (u.slot0 < 0) u.h0 = u.n = u.slot0 = 0;
         f(u);
       });
 }
 
 __device__ __noinline__ void bwd_plan(const VarBwdParams& p, BwdPlanSmem& s) {
   for (int i = threadIdx.x; i <= kBins; i += kPrepThreads) s.bins[i] = 0;
+  if (threadIdx.x == 0) s.bad = s.next = 0;
   __syncthreads();
-  // two passes, counting and writing, that share one copy of the code; units stay in registers
-  // when there are no more of them than threads
+  // passes that share one copy of the code: counting, counting again while dealing slots (after a
+  // bad start), writing; units stay in registers when there are no more of them than threads
   VarBwdUnit mine;
-  bool has = false, one_pass = false;
+  bool has = false, one_pass = false, dealt = false;
 #pragma unroll 1
-  for (int pass = 0; pass < 2; ++pass) {
-    if (pass == 1) {
+  for (int pass = kCount; pass <= kWrite; ++pass) {
+    if (pass == kDeal) {
+      if (!s.bad) continue;
+      dealt = true;
+      one_pass = false;
+      for (int i = threadIdx.x; i <= kBins; i += kPrepThreads) s.bins[i] = 0;
+      __syncthreads();
+    }
+    if (pass == kWrite) {
       const int units = scan_bins(s.scan, s.bins);
       if (threadIdx.x == 0) {  // more than fit only when starts overlap, which no packed rows have
         p.n_units[0] = max(0, min(units, p.max_units));
+        p.n_units[1] = dealt;
         if (units < 0 || units > p.max_units) atomicOr(p.m.status, FA_DEV_BAD_PAGE);
       }
     }
     auto visit = [&](const VarBwdUnit& u) {
       const int bin = cost_bin(u.n, p.cost_shift);
-      const int at = atomicAdd(&s.bins[pass ? bin : bin + 1], 1);
-      if (pass && at >= 0 && at < p.max_units) p.units[at] = u;
+      const int at = atomicAdd(&s.bins[pass == kWrite ? bin : bin + 1], 1);
+      if (pass == kWrite && at >= 0 && at < p.max_units) p.units[at] = u;
     };
     if (one_pass) {
       if (has) visit(mine);
     } else {
-      for_each_key_block(p, s, pass == 0, [&](const VarBwdUnit& u) {
+      for_each_key_block(p, s, pass, dealt, [&](const VarBwdUnit& u) {
         mine = u;
         has = true;
         visit(u);
       });
-      one_pass = p.B <= kPrepThreads && s.scan.off[p.B] <= kPrepThreads;
+      one_pass = !dealt && p.B <= kPrepThreads && s.scan.off[p.B] <= kPrepThreads;
     }
   }
 }
@@ -194,8 +220,9 @@ __device__ __noinline__ void bwd_plan(const VarBwdParams& p, BwdPlanSmem& s) {
 struct HalfRows {
   int t0, n;
 };
-// Found by one warp: 32 sequences probed at a time narrow the range 32-fold per load.
-__device__ __forceinline__ HalfRows half_rows(const VarBwdParams& p, int s) {
+// Found by one warp where no start is bad: 32 sequences probed at a time narrow the range 32-fold
+// per load.
+__device__ __forceinline__ HalfRows half_rows_sorted(const VarBwdParams& p, int s) {
   const int lane = threadIdx.x % 32;
   int lo = 0, n = p.B;  // the last sequence whose slots start at or before s is in [lo, lo + n)
   while (n > 1) {
@@ -210,6 +237,27 @@ __device__ __forceinline__ HalfRows half_rows(const VarBwdParams& p, int s) {
   const int at = (s - (r.first / p.TPH + lo)) * p.TPH;
   if (r.bad || at < 0 || at >= r.n) return HalfRows{0, 0};
   return HalfRows{r.first + at, min(p.TPH, r.n - at)};
+}
+// The same after the plan has run: where slots were dealt out, every sequence is asked.
+__device__ __forceinline__ HalfRows half_rows(const VarBwdParams& p, int s) {
+  if (!p.n_units[1]) return half_rows_sorted(p, s);
+  for (int b0 = 0; b0 < p.B; b0 += 32) {
+    const int b = b0 + static_cast<int>(threadIdx.x % 32);
+    SeqRows r{0, 0, true};
+    int i = -1;  // which half of the sequence
+    if (b < p.B) {
+      r = rows_of(p.cu_q, b, p.total_q);
+      if (p.seq_slot[b] >= 0) i = s - p.seq_slot[b];
+    }
+    const bool hit = i >= 0 && i < (r.n + p.TPH - 1) / p.TPH;
+    const uint32_t who = __ballot_sync(0xffffffffu, hit);
+    if (who) {
+      const int src = __ffs(who) - 1, at = i * p.TPH;
+      return HalfRows{__shfl_sync(0xffffffffu, r.first + at, src),
+                      __shfl_sync(0xffffffffu, min(p.TPH, r.n - at), src)};
+    }
+  }
+  return HalfRows{0, 0};
 }
 
 template <bool BF16>
@@ -232,38 +280,25 @@ __device__ __forceinline__ float dot8(const uint4& a, const uint4& b) {
   return acc;
 }
 
+// Statistics of rows 64 s .. 64 s + 63 of head subset hh (row: token, head), tokens [t0, t1) alone.
 template <int D, bool BF16>
-__global__ void __launch_bounds__(kPrepThreads, 6)
-    bwd_prep_kernel(const __grid_constant__ VarBwdParams p) {
+__device__ __forceinline__ void prep_rows(const VarBwdParams& p, int hh, int s, int t0, int t1) {
   constexpr int LPR = D / 8;               // lanes per row, 16 bytes each
   constexpr int RPP = kPrepThreads / LPR;  // rows per pass
-  __shared__ BwdPlanSmem plan;
-  __shared__ HalfRows sh;
-  if (blockIdx.x == 0) {  // the plan, beside the other CTAs' work
-    if (blockIdx.y == 0) bwd_plan(p, plan);
-    return;
-  }
-  const int hh = blockIdx.y;  // K/V head x head subset
-  const int kvh = hh / p.HS, h0 = kvh * p.G + (hh % p.HS) * p.GS;
-  if (threadIdx.x < 32) {
-    const HalfRows f = half_rows(p, blockIdx.x - 1);
-    if (threadIdx.x == 0) sh = f;
-  }
-  __syncthreads();
-  const HalfRows r = sh;
-  if (r.n == 0) return;
-  const size_t slot = static_cast<size_t>(hh) * p.slots + blockIdx.x - 1;
-  float4* acc = reinterpret_cast<float4*>(p.dqacc + slot * kHalf * D);
-  for (int i = threadIdx.x; i < kHalf * D / 4; i += kPrepThreads) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-  float* st = p.stats + slot * 2 * kHalf;
+  const int64_t row0 = static_cast<int64_t>(s) * kHalf;
+  if (row0 >= static_cast<int64_t>(t1) * p.GS) return;
+  float* nl = p.stats + static_cast<size_t>(hh) * p.total_q * p.GS;
+  float* nd = nl + static_cast<size_t>(p.total_q) * p.H;
   const int c = threadIdx.x % LPR;
 #pragma unroll
   for (int r0 = 0; r0 < kHalf; r0 += RPP) {
-    const int row = r0 + threadIdx.x / LPR, tok = row / p.GS;
-    const bool live = tok < r.n;
+    // total_q H fits 32 bits, and so does what is at most 63 rows behind it, without a sign
+    const uint32_t row = static_cast<uint32_t>(row0) + r0 + threadIdx.x / LPR;
+    const uint32_t tok = row / static_cast<uint32_t>(p.GS);
+    const bool live = tok >= static_cast<uint32_t>(t0) && tok < static_cast<uint32_t>(t1);
+    const int64_t t = tok;
+    const int h = hh * p.GS + static_cast<int>(row - tok * p.GS);
     float d = 0.f;
-    const int64_t t = r.t0 + tok;
-    const int h = h0 + row - tok * p.GS;
     if (live)
       d = dot8<BF16>(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.o) +
                                                     t * p.o_token + h * D)[c],
@@ -271,11 +306,56 @@ __global__ void __launch_bounds__(kPrepThreads, 6)
                                                     t * p.dout_token + h * D)[c]);
 #pragma unroll
     for (int off = LPR / 2; off > 0; off /= 2) d += __shfl_xor_sync(0xffffffffu, d, off);
-    if (c == 0) {
-      st[row] = live ? -p.lse[t * p.H + h] * 1.4426950408889634f : 0.f;
-      st[kHalf + row] = live ? -d : 0.f;
+    if (c == 0 && live) {
+      nl[row] = -p.lse[t * p.H + h] * 1.4426950408889634f;
+      nd[row] = -d;
     }
   }
+}
+
+template <int D>
+__device__ __forceinline__ void zero_slot(const VarBwdParams& p, int hh, int s) {
+  float4* acc = reinterpret_cast<float4*>(
+      p.dqacc + (static_cast<size_t>(hh) * p.slots + s) * (kHalf * D));
+  for (int i = threadIdx.x; i < kHalf * D / 4; i += kPrepThreads)
+    acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+}
+
+// What the other CTAs may have left out after a bad start, by the plan's CTA: rows from token
+// t_end on, and slots that they did not take for a half.
+template <int D, bool BF16>
+__device__ __noinline__ void prep_rest(const VarBwdParams& p, int t_end) {
+  for (int s = 0; s < p.slots; ++s)
+    for (int hh = 0; hh < p.Hkv * p.HS; ++hh) {
+      if (s >= static_cast<int64_t>(t_end) * p.GS / kHalf)
+        prep_rows<D, BF16>(p, hh, s, t_end, p.total_q);
+      zero_slot<D>(p, hh, s);
+    }
+}
+
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kPrepThreads, 6)
+    bwd_prep_kernel(const __grid_constant__ VarBwdParams p) {
+  __shared__ BwdPlanSmem plan;
+  __shared__ bool used;
+  // rows behind the last start are nobody's, unless a start is bad
+  const int t_end = max(0, min(p.cu_q[p.B], p.total_q));
+  if (blockIdx.x == 0) {  // the plan, beside the other CTAs' work
+    if (blockIdx.y == 0) {
+      bwd_plan(p, plan);
+      if (plan.bad && p.total_q > 0) prep_rest<D, BF16>(p, t_end);
+    }
+    return;
+  }
+  const int s = blockIdx.x - 1;
+  if (s > t_end / p.TPH + p.B) return;  // and so are slots behind the last one
+  if (threadIdx.x < 32) {
+    const HalfRows f = half_rows_sorted(p, s);
+    if (threadIdx.x == 0) used = f.n > 0;
+  }
+  prep_rows<D, BF16>(p, blockIdx.y, s, 0, t_end);
+  __syncthreads();
+  if (used) zero_slot<D>(p, blockIdx.y, s);
 }
 
 // dq of one half: the accumulator's [16 groups][D][4] transposed through shared memory.
@@ -546,6 +626,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = bars->tmem_base;
   const WaitCtx wc{&bars->abort, p.m.status, p.m.timeout_ns};
   const size_t slot0 = static_cast<size_t>(hh) * p.slots + u.slot0 + u.h0;  // of half 0
+  // statistics of this head subset: -LSE log2(e) of every (token, head), then -D
+  const float* nl = p.stats + static_cast<size_t>(hh) * p.total_q * p.GS;
+  const float* nd = nl + static_cast<size_t>(p.total_q) * p.H;
 
   if (warp == kTmaWarp) {
     // ------------------------------------------------------------ TMA
@@ -567,14 +650,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < u.n && ok; ++i) {
       const int h = stage_of(i);
       // the half's statistics, loaded before the wait for the stage
-      const float4 st = reinterpret_cast<const float4*>(p.stats + (slot0 + i) * 2 * kHalf)[lane];
+      const int tok0 = (u.h0 + i) * p.TPH, live = min(p.TPH, u.sq - tok0) * p.GS;
+      const size_t row = static_cast<size_t>(u.q0 + tok0) * p.GS + lane;
+      const bool a = lane < live, b = lane + 32 < live;
+      const float l0 = a ? nl[row] : 0.f, l1 = b ? nl[row + 32] : 0.f;
+      const float d0 = a ? nd[row] : 0.f, d1 = b ? nd[row + 32] : 0.f;
       if (i >= kStages && !(ok = mbar_wait(B(bars->st_empty[h]), stage_parity(i - kStages), wc)))
         break;
-      reinterpret_cast<float4*>(stats + h * 2 * kHalf)[lane] = st;
+      float* st = stats + h * 2 * kHalf + lane;
+      st[0] = l0, st[32] = l1, st[kHalf] = d0, st[kHalf + 32] = d1;
       __syncwarp();  // the leader's arrive below releases every lane's writes
       if (leader) {
         mbar_arrive_expect_tx(B(bars->st_full[h]), bytes);
-        const int t = u.q0 + (u.h0 + i) * p.TPH;
+        const int t = u.q0 + tok0;
 #pragma unroll
         for (int c = 0; c < D / 64; ++c) {
           tma_load_3d(sQ(h) + c * (kHalf * 128), &tmQ, B(bars->st_full[h]), c * 64, head0, t);
