@@ -451,8 +451,8 @@ fa_status fa_rope(const void* x, void* y, const int32_t* positions, const double
  *   FA_BF16, 16-byte aligned, steps a multiple of 8 elements; q_out may be q. d 64 or 128;
  *   page_size a multiple of 16 in [16, 4096].
  * A token whose table entry is outside [0, num_pages), or whose position is beyond
- * page_size * max_pages_per_seq, is not cached (its q is rotated) and reported as
- * FA_ERR_BAD_PAGE.
+ * page_size * max_pages_per_seq or below 0, is not cached (its q is rotated) and reported as
+ * FA_ERR_BAD_PAGE. Tokens that no sequence owns are neither rotated nor cached.
  */
 typedef struct fa_rope_append_params {
   const void* q;

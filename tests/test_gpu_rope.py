@@ -249,3 +249,65 @@ def test_append_of_many_sequences(style):
         assert (err <= limit(src, d, half, amp, dtype)).all()
     assert torch.equal(vg.cpu()[at], qkv[:, H + Hkv:])
     assert int((~vg.isnan()).any(-1).sum()) == T * Hkv
+
+
+BAD = {"end": lambda T: [0, 40, T + 1], "falls": lambda T: [0, 40, 20],
+       "first": lambda T: [-1, 20, T], "below": lambda T: [0, 10, 20, -5, T],
+       "far below": lambda T: [0, 10, 20, -2 ** 31, T],
+       "far above": lambda T: [0, 10, 20, 2 ** 31 - 1, T], "no rows": lambda T: [0, T, T + 6],
+       "disorder": lambda T: [40, T, 0, 40]}
+
+
+@pytest.mark.parametrize("name", list(BAD) + ["many"])
+@pytest.mark.parametrize("long", [False, True])
+def test_append_reports_bad_starts_and_keeps_other_sequences(name, long):
+    """Valid sequences are rotated and cached, no other token writes anything; for one token
+    per CTA and for several."""
+    H, Hkv, d, page, dtype = 2, 1, 64, 16, torch.float16
+    T = 16 * torch.cuda.get_device_properties(0).multi_processor_count + 3 if long else 64
+    if name == "many":
+        g = torch.Generator().manual_seed(4)
+        cu = starts(torch.randint(0, 8 if long else 2, (700,), generator=g).tolist())
+        T = max(cu[-1], T)
+        cu[0] = cu[233] = cu[660] = -9
+        cu[350] = T + 50
+        cu[175], cu[176] = 3, T + 9
+    else:
+        cu = BAD[name](T)
+    B = len(cu) - 1
+    good = [(b, cu[b], cu[b + 1]) for b in range(B) if 0 <= cu[b] <= cu[b + 1] <= T]
+    before = [(7 * b) % 20 for b in range(B)]
+    width = (20 + T) // page + 1
+    # pages of a sequence's own, and one for all that it must not reach
+    need = {b: -(-(before[b] + e - a) // page) for b, a, e in good}
+    table = torch.zeros(B, width, dtype=torch.int32)
+    at = 1
+    for b, n in need.items():
+        table[b, :n] = torch.arange(at, at + n)
+        at += n
+    qkv = draw((T, H + 2 * Hkv, d), dtype, seed=21)
+    freqs, amp = fa.fa_rope_freqs(d)
+    kg, vg = (torch.full((at, Hkv, page, d), float("nan"), dtype=dtype, device="cuda")
+              for _ in range(2))
+    out = torch.full((T, H, d), float("nan"), dtype=dtype, device="cuda")
+    x = qkv.cuda()
+    fa.fa_rope_append(x[:, :H], x[:, H:H + Hkv], x[:, H + Hkv:], out, kg, vg, table.cuda(),
+                      torch.tensor(before, dtype=torch.int32).cuda(),
+                      torch.tensor(cu, dtype=torch.int32).cuda(), freqs.cuda())
+    assert fa.fa_get_device_status() == fa.FA_ERR_BAD_PAGE
+    assert fa.fa_get_device_status() == fa.FA_OK
+    got, kc, vc = out.cpu(), kg.cpu(), vg.cpu()
+    rows = torch.ones(T, dtype=torch.bool)
+    written = torch.zeros(at, page, dtype=torch.bool)
+    for b, a, e in good:
+        rows[a:e] = False
+        pos = before[b] + torch.arange(e - a)
+        slot = (table[b, pos // page].long(), slice(None), pos % page)
+        written[slot[0], slot[2]] = True
+        for src, have in ((qkv[a:e, :H], got[a:e]), (qkv[a:e, H:H + Hkv], kc[slot])):
+            err = (have.double() - rotate(src, pos, freqs, d, True, amp)).abs()
+            assert (err <= limit(src, d, True, amp, dtype)).all(), (b, a, e)
+        assert torch.equal(vc[slot], qkv[a:e, H + Hkv:])
+    assert got[rows].isnan().all()
+    for pool in (kc, vc):
+        assert pool.transpose(1, 2)[~written].isnan().all()

@@ -19,9 +19,11 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <climits>
 #include <cstdint>
 
 #include "fa_varlen.h"
+#include "fa_varlen_plan.cuh"
 
 namespace fa {
 namespace {
@@ -82,15 +84,20 @@ __device__ __forceinline__ uint64_t turns_q64(double radians) {
   return bits >> 63 ? 0 - t : t;
 }
 
-// The sequence of token t: the number of sequences that end at or before it (cu holds B + 1
-// non-decreasing starts), counted by the whole CTA.
-__device__ __forceinline__ int sequence_of(const int32_t* cu, int B, int64_t t) {
-  int n = 0;
-  for (int i0 = 0; i0 < B; i0 += kRopeThreads) {
-    const int i = i0 + threadIdx.x;
-    n += __syncthreads_count(i < B && cu[i + 1] <= t);
+// The sequences of tokens t0 .. t0 + nt - 1, found by the whole CTA: every sequence is asked, so
+// that a bad start takes no token from another one. kNobody: no valid sequence owns the token.
+constexpr int kNobody = INT_MAX;
+__device__ __forceinline__ void sequences_of(const RopeParams& p, int64_t t0, int nt, int* s_seq) {
+  if (threadIdx.x < nt) s_seq[threadIdx.x] = kNobody;
+  __syncthreads();
+  for (int b = threadIdx.x; b < p.B; b += kRopeThreads) {
+    const SeqRows r = rows_of(p.cu, b, static_cast<int>(p.T));
+    if (r.bad && blockIdx.x == 0) atomicOr(p.status, FA_DEV_BAD_PAGE);
+    const int64_t end = static_cast<int64_t>(r.first) + r.n;
+    for (int64_t t = max(t0, static_cast<int64_t>(r.first)); t < min(t0 + nt, end); ++t)
+      atomicMin(s_seq + (t - t0), b);
   }
-  return n;
+  __syncthreads();
 }
 
 // One CTA per `tok` tokens. A row (head) is cut into units of two chunks (of 16 bytes, or one
@@ -105,7 +112,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p, 
   using T = typename E::T;
   using C = Chunk<T, VEC>;
   extern __shared__ float2 s_cs[];         // [tok][R/2] (cos, sin), amplitude included
-  __shared__ int64_t s_dst[8];             // APPEND: first element of the token's slot, or -1
+  __shared__ int64_t s_dst[8];             // APPEND: first element of the token's slot, or below 0
   const int half = p.rot / 2;
   uint64_t* s_freq = reinterpret_cast<uint64_t*>(s_cs + static_cast<size_t>(tok) * half);
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * tok;
@@ -113,18 +120,19 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p, 
   for (int i = threadIdx.x; i < half; i += kRopeThreads) s_freq[i] = turns_q64(p.freqs[i]);
   __shared__ int s_pos[8];
   if constexpr (APPEND) {
-    const int b0 = sequence_of(p.cu, p.B, t0);
-    if (threadIdx.x < nt) {  // a later token of the CTA may belong to a later sequence
+    __shared__ int s_seq[8];
+    sequences_of(p, t0, nt, s_seq);
+    if (threadIdx.x < nt) {
       const int64_t t = t0 + threadIdx.x;
-      int b = b0;
-      while (b < p.B && p.cu[b + 1] <= t) ++b;
-      int64_t dst = -1;
+      const int b = s_seq[threadIdx.x];
+      int64_t dst = -2;
       int pos = 0;
-      if (b < p.B && p.cu[b] <= t) {
+      if (b != kNobody) {
         const int64_t at = static_cast<int64_t>(p.ctx[b]) + (t - p.cu[b]);
         const int64_t lp = at / p.page_size;
         const bool in = p.ctx[b] >= 0 && lp < p.max_pages;
         const int phys = in ? p.block_table[static_cast<size_t>(b) * p.max_pages + lp] : -1;
+        dst = -1;
         if (phys < 0 || phys >= p.num_pages)
           atomicOr(p.status, FA_DEV_BAD_PAGE);
         else
@@ -132,8 +140,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p, 
         pos = static_cast<int>(at);
       }
       s_pos[threadIdx.x] = pos;
-      // -2: behind the last sequence, nothing is written; -1: no slot, q alone is
-      s_dst[threadIdx.x] = (b < p.B && p.cu[b] <= t) ? dst : -2;
+      s_dst[threadIdx.x] = dst;  // -2: nobody's token, nothing is written; -1: no slot, q alone is
     }
   } else if (threadIdx.x < nt) {
     s_pos[threadIdx.x] = p.pos[t0 + threadIdx.x];
