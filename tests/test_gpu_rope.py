@@ -311,3 +311,24 @@ def test_append_reports_bad_starts_and_keeps_other_sequences(name, long):
     assert got[rows].isnan().all()
     for pool in (kc, vc):
         assert pool.transpose(1, 2)[~written].isnan().all()
+
+
+def test_append_beyond_32_bit_positions():
+    """A chunk whose positions pass 2^31: nothing of it is cached, its q is rotated."""
+    H, d, page = 2, 64, 16
+    qkv = draw((3, H + 2, d), torch.float16, seed=2).cuda()
+    kp = torch.zeros(2, 1, page, d, dtype=torch.float16, device="cuda")
+    vp = kp.clone()
+    freqs, _ = fa.fa_rope_freqs(d)
+    out = torch.full((3, H, d), float("nan"), dtype=torch.float16, device="cuda")
+    ints = [torch.tensor(x, dtype=torch.int32, device="cuda")
+            for x in ([[0, 1]], [2 ** 31 - 2], [0, 3])]
+    fa.fa_rope_append(qkv[:, :H], qkv[:, H:H + 1], qkv[:, H + 1:], out, kp, vp, *ints, freqs.cuda())
+    assert fa.fa_get_device_status() == fa.FA_ERR_BAD_PAGE
+    pos = 2 ** 31 - 2 + torch.arange(3)
+    x = qkv[:, :H].cpu()
+    err = (out.double().cpu() - rotate(x, pos, freqs, d, True)).abs()
+    # the reference's own 64-bit product and the frequencies' fixed point: 2^-21 rad
+    lim = limit(x, d, True, 1.0, torch.float16) * (1 + 2.0 ** -9)
+    assert (err <= lim).all(), float((err - lim).max())
+    assert (kp == 0).all() and (vp == 0).all()

@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p, 
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * tok;
   const int nt = static_cast<int>(min(static_cast<int64_t>(tok), p.T - t0));
   for (int i = threadIdx.x; i < half; i += kRopeThreads) s_freq[i] = turns_q64(p.freqs[i]);
-  __shared__ int s_pos[8];
+  __shared__ int64_t s_pos[8];  // a length near 2^31 and the chunk's tokens leave 32 bits
   if constexpr (APPEND) {
     __shared__ int s_seq[8];
     sequences_of(p, t0, nt, s_seq);
@@ -126,7 +126,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p, 
       const int64_t t = t0 + threadIdx.x;
       const int b = s_seq[threadIdx.x];
       int64_t dst = -2;
-      int pos = 0;
+      int64_t pos = 0;
       if (b != kNobody) {
         const int64_t at = static_cast<int64_t>(p.ctx[b]) + (t - p.cu[b]);
         const int64_t lp = at / p.page_size;
@@ -137,7 +137,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p, 
           atomicOr(p.status, FA_DEV_BAD_PAGE);
         else
           dst = (static_cast<int64_t>(phys) * p.Hkv * p.page_size + (at - lp * p.page_size)) * p.d;
-        pos = static_cast<int>(at);
+        pos = at;
       }
       s_pos[threadIdx.x] = pos;
       s_dst[threadIdx.x] = dst;  // -2: nobody's token, nothing is written; -1: no slot, q alone is
@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p, 
   __syncthreads();
   for (int i = threadIdx.x; i < nt * half; i += kRopeThreads) {
     const int tk = i / half, f = i - tk * half;
-    const int64_t at = p.inverse ? -static_cast<int64_t>(s_pos[tk]) : s_pos[tk];
+    const int64_t at = p.inverse ? -s_pos[tk] : s_pos[tk];
     const uint64_t phase = static_cast<uint64_t>(at) * s_freq[f];
     float s, c;  // the phase as a signed fraction of a turn: half turns in [-1, 1]
     sincospif(static_cast<float>(static_cast<int64_t>(phase)) * 1.08420217248550443e-19f, &s, &c);
