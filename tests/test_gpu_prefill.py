@@ -306,3 +306,15 @@ def test_output_only_16_byte_aligned(dt):
         else:
             compare(o, lse, ref_o, ref_l, f"16-byte aligned O, mode {mode}")
         assert torch.isnan(buf[:step].float()).all() and torch.isnan(buf[step + q.numel():].float()).all()
+
+
+@pytest.mark.parametrize("Sq,Sk", [(200, 3), (300, 130), (5, 2)])
+@pytest.mark.parametrize("bm", [64, 128, 256])
+def test_largest_window_with_more_queries_than_keys(Sq, Sk, bm):
+    """A window beyond every distance sees what the causal mask sees."""
+    q = inputs.prefill_inputs(1, 2, Sq, Sq, 64, torch.float16, seed=8)[0]
+    _, k, v = inputs.prefill_inputs(1, 2, Sk, Sk, 64, torch.float16, seed=9)
+    ref_o, ref_l = oracle.attention(q, k, v, 0.125, oracle.MASK_CAUSAL)
+    for window in (2 ** 31 - 1, 2 ** 31 - 100):
+        o, lse = run_fwd(q, k, v, 0.125, fa.FA_MASK_CAUSAL_WINDOW, window, 0, block_m=bm)
+        compare(o, lse, ref_o, ref_l, f"window {window}")

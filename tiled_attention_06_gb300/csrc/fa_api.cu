@@ -407,7 +407,7 @@ fa_status run_fwd(const fa_fwd_params& a, const PagedKV* pg, fa_stream_t stream,
   p.mask_mode = a.mask_mode;
   const bool uses_window = a.mask_mode == FA_MASK_CAUSAL_WINDOW || a.mask_mode == FA_MASK_BAND;
   const bool uses_global = a.mask_mode == FA_MASK_CAUSAL_WINDOW || a.mask_mode == FA_MASK_PREFIX_LM;
-  p.window = uses_window ? a.window : 0;
+  p.window = uses_window ? std::min(a.window, fa::kMaxWindow) : 0;
   p.n_global = uses_global ? a.n_global : 0;
   p.sl2 = a.scale * 1.4426950408889634f;
   // Heads scheduled together so that their K/V stays resident in L2 (~48 MiB budget).
@@ -823,7 +823,9 @@ static fa_status bwd(const void* q, const void* k, const void* v, const void* o,
   p.Sq = Sq;
   p.Sk = Sk;
   p.mask_mode = mask_mode;
-  p.window = (mask_mode == FA_MASK_CAUSAL_WINDOW || mask_mode == FA_MASK_BAND) ? window : 0;
+  p.window = (mask_mode == FA_MASK_CAUSAL_WINDOW || mask_mode == FA_MASK_BAND)
+                 ? std::min(window, fa::kMaxWindow)
+                 : 0;
   p.n_global = (mask_mode == FA_MASK_CAUSAL_WINDOW || mask_mode == FA_MASK_PREFIX_LM) ? n_global : 0;
   p.sl2 = scale * 1.4426950408889634f;
   p.status = dev.status;

@@ -187,12 +187,9 @@ fa_status check_workspace(const void* ws, size_t bytes, size_t need) {
 void fill_mask(fa::PrefillParams* m, const Common& c, uint32_t timeout_us, uint32_t* status) {
   const bool w = c.mask_mode == FA_MASK_CAUSAL_WINDOW || c.mask_mode == FA_MASK_BAND;
   const bool g = c.mask_mode == FA_MASK_CAUSAL_WINDOW || c.mask_mode == FA_MASK_PREFIX_LM;
-  // Positions lie within 2^30 of zero on both sides, keys and queries less than 2^30 apart: wider
-  // windows see the same, and the clamped ones leave room for position - window in 32 bits.
-  constexpr int kFar = 1 << 30;
   m->mask_mode = c.mask_mode;
-  m->window = w ? std::min(c.window, kFar) : 0;
-  m->n_global = g ? std::min(c.n_global, kFar) : 0;
+  m->window = w ? std::min(c.window, fa::kMaxWindow) : 0;
+  m->n_global = g ? std::min(c.n_global, 1 << 30) : 0;  // no sequence has more keys
   m->sl2 = c.scale * 1.4426950408889634f;
   m->status = status;
   m->timeout_ns = static_cast<uint64_t>(timeout_us ? timeout_us : 1000000u) * 1000u;

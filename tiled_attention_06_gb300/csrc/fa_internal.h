@@ -16,12 +16,16 @@ namespace fa {
 // boundary for its layout and did nothing.
 enum : uint32_t { FA_DEV_TIMEOUT = 1u, FA_DEV_BAD_PAGE = 2u, FA_DEV_SMEM_BASE = 4u };
 
+// Positions lie within 2^30 of zero on both sides, keys and queries less than 2^30 apart: wider
+// windows see the same, and clamped ones leave room for position - window in 32 bits.
+constexpr int kMaxWindow = 1 << 30;
+
 struct PrefillParams {
   void* o;            // [B,H,Sq,D] 16-bit (FP32 for FP32 inputs)
   float* lse;         // [B,H,Sq] or nullptr
   int BH, Sq, Sk;
   int nmb, nnb;       // query blocks (BM rows per work item), key blocks (BN keys)
-  int mask_mode, window, n_global;
+  int mask_mode, window, n_global;  // window at most kMaxWindow
   float sl2;          // scale * log2(e)
   int group_heads;    // (batch, head) pairs per scheduling group
   int total_items;    // BH * nmb
