@@ -492,3 +492,52 @@ def test_masks_that_leave_rows_of_a_cached_chunk_empty(new):
     o, lse = run_paged(q, kp, vp, table, [keys, keys], cu_q, new, 0.125, mask)
     assert fa.fa_get_device_status() == fa.FA_OK
     check_forward(o, lse, attention(q, k, v, cu_q, cu_k, 0.125, *mask), dt, 2 * new)
+
+
+def test_python_refusals_of_shapes_and_numbers():
+    """Wrong dimensions and numbers that a field does not hold raise FaError in every call."""
+    H, Hkv, d, T, page = 4, 2, 64, 10, 16
+    q, k, v, cu, _ = case([T], [T], H, Hkv, d, torch.float16, seed=1)
+    q, k, v, cu = q.cuda(), k.cuda(), v.cuda(), i32(cu)
+    o, lse = torch.empty_like(q), torch.empty(T, H, device="cuda")
+    kp = torch.zeros(2, Hkv, page, d, dtype=torch.float16, device="cuda")
+    table, ctx = i32([[0, 1]]), i32([0])
+    freqs, _ = fa.fa_rope_freqs(d, device="cuda")
+    ws = torch.empty(max(fa.fa_varlen_workspace_size(1, H, Hkv, T, T, d),
+                         fa.fa_bwd_varlen_workspace_size(1, H, Hkv, T, T, d),
+                         fa.fa_paged_varlen_workspace_size(1, H, Hkv, T, T, 2, page, d)),
+                     dtype=torch.uint8, device="cuda")
+    mask = [dict(window=2 ** 40), dict(n_global=2 ** 31), dict(mask_mode=-2 ** 31 - 1),
+            dict(scale=1e300), dict(q=q[0]), dict(q=q[None]), dict(o=o[:, 0]), dict(o=o[:-1]),
+            dict(lse=lse[0])]
+    kv = [dict(k=k[0]), dict(k=k[None]), dict(v=v[:, 0]), dict(v=v[:-1]),
+          dict(cu_seqlens_k=cu[:1]), dict(cu_seqlens_k=cu[None]), dict(cu_seqlens_q=cu[0])]
+    pools = [dict(k_pages=kp[0]), dict(v_pages=kp[0]), dict(k_pages=kp[None]),
+             dict(block_table=table[0]), dict(ctx_lens=ctx[None])]
+    packed = dict(q=q, k=k, v=v, o=o, lse=lse, cu_seqlens_q=cu, cu_seqlens_k=cu, scale=0.125,
+                  workspace=ws)
+    grads = dict(dout=torch.zeros_like(q), dq=torch.empty_like(q), dk=torch.empty_like(k),
+                 dv=torch.empty_like(v))
+    x = torch.empty(T, H, d, dtype=torch.float16, device="cuda")
+    for call, good, bad in (
+            (fa.fa_fwd_varlen, packed, mask + kv),
+            (fa.fa_bwd_varlen, dict(packed, **grads), mask + kv + [
+                {n: t[0]} for n, t in grads.items()] + [{n: t[:-1]} for n, t in grads.items()]),
+            (fa.fa_fwd_paged_varlen,
+             dict(q=q, k_pages=kp, v_pages=kp, block_table=table, ctx_lens=i32([T]),
+                  cu_seqlens_q=cu, max_q=T, o=o, lse=lse, scale=0.125, workspace=ws),
+             mask + pools + [dict(max_q=2 ** 31), dict(max_q=2.0), dict(cu_seqlens_q=cu[0])]),
+            (fa.fa_rope_append,
+             dict(q=q, k=k, v=v, q_out=x, k_pages=kp, v_pages=kp.clone(), block_table=table,
+                  ctx_lens=ctx, cu_seqlens=cu, freqs=freqs),
+             pools + [dict(q=q[0]), dict(k=k[:-1]), dict(v=v[0]), dict(q_out=x[:-1]),
+                      dict(style=2 ** 32), dict(amplitude=1e300), dict(freqs=freqs[0]),
+                      dict(cu_seqlens=cu[0])]),
+            (fa.fa_rope, dict(x=q, y=x, positions=i32(list(range(T))), freqs=freqs),
+             [dict(style=2 ** 32), dict(x=q[0]), dict(y=x[0]), dict(positions=cu),
+              dict(freqs=freqs[0]), dict(freqs=freqs[None]), dict(amplitude=1e300)])):
+        call(**good)
+        for kw in bad:
+            with pytest.raises(fa.FaError):
+                call(**dict(good, **kw))
+    assert fa.fa_get_device_status() == fa.FA_OK

@@ -211,3 +211,47 @@ def test_cpu_tensors_are_refused():
     with pytest.raises(fa.FaError) as e:
         fa.fa_rope(x, x, torch.zeros(2, dtype=torch.int32), torch.zeros(32, dtype=torch.float64))
     assert e.value.status == INVALID
+
+
+# ------------------------------------------------------------------ the binding's own refusals
+
+@pytest.mark.parametrize("cls,pack", [(fa.RopeAppendParams, "append"), (fa.VarlenParams, "varlen"),
+                                      (fa.VarlenGrads, "grads"), (fa.PagedVarlenParams, "paged")])
+def test_values_that_do_not_fit_their_field_are_refused(cls, pack):
+    pack = getattr(fa, "_pack_" + pack)
+    good = [1.0 if t is ctypes.c_float else 1 for _, t in cls._fields_]
+    assert bytes(pack(*good)) == bytes(cls(*good))[:len(pack(*good))]
+    for i, (name, t) in enumerate(cls._fields_):
+        # (a float out of range becomes an infinity, which the library refuses)
+        for bad in (2 ** 64, -2 ** 64, None) if t is not ctypes.c_float else (None,):
+            with pytest.raises(fa.FaError, match=name) as e:
+                pack(*(good[:i] + [bad] + good[i + 1:]))
+            assert e.value.status == INVALID
+        if t is ctypes.c_int:
+            for bad in (2 ** 31, -2 ** 31 - 1, 2 ** 32 + 1, 0.5):
+                with pytest.raises(fa.FaError, match=name):
+                    pack(*(good[:i] + [bad] + good[i + 1:]))
+
+
+@pytest.mark.parametrize("name,n", [("fa_varlen_workspace_size", 6),
+                                    ("fa_bwd_varlen_workspace_size", 6),
+                                    ("fa_paged_varlen_workspace_size", 8)])
+def test_workspace_sizes_refuse_what_an_int_does_not_hold(L, name, n):
+    size = getattr(fa, name)
+    good = dict([("B", 1), ("H", 4), ("Hkv", 2), ("total_q", 8)] +
+                ([("total_k", 8)] if n == 6 else [("max_q", 8), ("max_pages_per_seq", 2),
+                                                  ("page_size", 16)]) + [("d", 64)])
+    assert size(**good) > 0
+    for key in good:
+        for bad in (2 ** 32 + good[key], 2 ** 31, -2 ** 31 - 1, 1.5, None):
+            with pytest.raises(fa.FaError, match=key):
+                size(**dict(good, **{key: bad}))
+
+
+def test_frequencies_refuse_what_an_int_does_not_hold(L):
+    for kw in (dict(rot_dim=2 ** 32 + 64), dict(rot_dim=2 ** 31 - 2), dict(rot_dim=64.0),
+               dict(rot_dim=64, scaling=2 ** 32),
+               dict(rot_dim=64, scaling=3, factor=2.0, trained_len=2 ** 32 + 4096)):
+        with pytest.raises(fa.FaError) as e:
+            fa.fa_rope_freqs(**kw)
+        assert e.value.status == INVALID

@@ -7,6 +7,7 @@ computation runs in the library's CUDA kernels: there is no fallback, and a
 missing library raises ``FaError``.
 """
 import ctypes
+import operator
 import os
 import struct
 
@@ -462,11 +463,34 @@ def _refuse(msg):
     raise FaError(FA_ERR_INVALID_ARG, msg)
 
 
+def _int32(**values):
+    """Refuse what a C int does not hold: ctypes would cut it to its low 32 bits."""
+    for name, x in values.items():
+        try:
+            ok = -2 ** 31 <= operator.index(x) < 2 ** 31
+        except TypeError:
+            ok = False
+        if not ok:
+            _refuse(f"{name} = {x!r} is not a 32-bit integer")
+
+
 def _packer(cls):
     """The bytes of a parameter struct from its values in order: a Structure's constructor costs
     several times as much (1.2 us against 0.2)."""
     code = {_vp: "P", _i64: "q", _i: "i", _f: "f", _sz: "N", _u32: "I"}
-    return struct.Struct("@" + "".join(code[t] for _, t in cls._fields_)).pack
+    pack = struct.Struct("@" + "".join(code[t] for _, t in cls._fields_)).pack
+
+    def checked(*values):
+        try:
+            return pack(*values)
+        except (struct.error, OverflowError):  # which value was it?
+            for (name, t), x in zip(cls._fields_, values):
+                try:
+                    struct.pack(code[t], x)
+                except (struct.error, OverflowError) as e:
+                    _refuse(f"{name} = {x!r}: {e}")
+            raise
+    return checked
 
 
 _pack_append = _packer(RopeAppendParams)
@@ -475,30 +499,34 @@ _pack_grads = _packer(VarlenGrads)
 _pack_paged = _packer(PagedVarlenParams)
 
 
-def _rows(name, t, heads, d, dtype, device):
-    """Elements between the tokens of packed rows [tokens, heads, d] (a view of a wider row
-    is fine: the last two dimensions have to be dense)."""
-    if t.dtype is dtype and t.device == device:
-        n, *rest = t.shape
-        if rest == [heads, d] and n > 1:
-            st = t.stride()
-            if st[2] == 1 and st[1] == d:
-                return st[0]
-    return _rows_checked(name, t, heads, d, dtype, device)
+def _rows(name, t, n, heads, d, dtype, device):
+    """Elements between the tokens of packed rows [n, heads, d] (a view of a wider row is fine:
+    the last two dimensions have to be dense)."""
+    if t.dtype is dtype and t.device == device and n > 1 and t.shape == (n, heads, d):
+        st = t.stride()
+        if st[2] == 1 and st[1] == d:
+            return st[0]
+    return _rows_checked(name, t, n, heads, d, dtype, device)
 
 
-def _rows_checked(name, t, heads, d, dtype, device):
-    if t.dim() != 3 or t.dtype != dtype or t.device != device:
-        _refuse(f"{name} must be [tokens, heads, d] of {dtype} on {device}")
-    n, h, e = t.shape
-    if h != heads or e != d:
-        _refuse(f"{name} has {h} heads of {e}, not {heads} of {d}")
+def _rows_checked(name, t, n, heads, d, dtype, device):
+    if t.shape != (n, heads, d) or t.dtype != dtype or t.device != device:
+        _refuse(f"{name} must be [{n}, {heads}, {d}] of {dtype} on {device}, not "
+                f"{list(t.shape)} of {t.dtype} on {t.device}")
     st = t.stride()
     if n == 0:
         return heads * d
     if (d > 1 and st[2] != 1) or (heads > 1 and st[1] != d):
         _refuse(f"{name}: the heads of a token must lie next to each other")
     return st[0] if n > 1 else heads * d
+
+
+def _dims(name, t, n):
+    """The shape of t, which must have n dimensions."""
+    shape = t.shape
+    if len(shape) != n:
+        _refuse(f"{name} must have {n} dimensions, not {len(shape)}")
+    return shape
 
 
 def _ints(name, t, shape, device):
@@ -537,7 +565,8 @@ def fa_rope_freqs(rot_dim, base=10000.0, scaling=FA_ROPE_PLAIN, factor=1.0, trai
                   fast=32.0, slow=1.0, device=None):
     """(frequencies float64 [rot_dim/2] in radians per position, amplitude) of a rotary
     embedding; the rules are those of fa_rope_freqs in fa.h. On `device` (CPU when None)."""
-    host = torch.empty(max(rot_dim // 2, 1), dtype=torch.float64)
+    _int32(rot_dim=rot_dim, scaling=scaling, trained_len=trained_len)
+    host = torch.empty(min(max(rot_dim // 2, 1), 256), dtype=torch.float64)  # 512 is the largest
     amp = _f()
     _check(lib().fa_rope_freqs(ctypes.cast(host.data_ptr(), ctypes.POINTER(ctypes.c_double)),
                                ctypes.byref(amp), rot_dim, float(base), scaling, float(factor),
@@ -566,9 +595,13 @@ def fa_rope(x, y, positions, freqs, style=FA_ROPE_HALF, amplitude=1.0, inverse=F
     xs, ys = x.stride(), y.stride()
     if d > 1 and (xs[2] != 1 or ys[2] != 1):
         _refuse("the elements of a head must be contiguous")
-    dense = H * d
+    dense, rot = H * d, 2 * freqs.numel()
+    if H >= 2 ** 31 or d >= 2 ** 31 or rot >= 2 ** 31:
+        _int32(heads=H, head_dim=d, rot_dim=rot)
+    if style != FA_ROPE_HALF and style != FA_ROPE_PAIRS:
+        _refuse(f"style {style}")
     _check(lib().fa_rope(x.data_ptr(), y.data_ptr(), _ints("positions", positions, (T,), device),
-                         _freqs_ptr(freqs, device), T, H, d, 2 * freqs.numel(),
+                         _freqs_ptr(freqs, device), T, H, d, rot,
                          xs[0] if T > 1 else dense, xs[1] if H > 1 else d,
                          ys[0] if T > 1 else dense, ys[1] if H > 1 else d,
                          style, float(amplitude), 1 if inverse else 0, _dtype_code(x),
@@ -581,19 +614,18 @@ def fa_rope_append(q, k, v, q_out, k_pages, v_pages, block_table, ctx_lens, cu_s
     positions ctx_lens[b] + t - cu_seqlens[b] (ctx_lens: tokens cached before the chunk), write
     q to q_out and k and v into the pools [num_pages, Hkv, page_size, d]."""
     device = _packed_device(q)
-    T, H, d = q.shape
-    P, Hkv, page, _ = k_pages.shape
-    B, width = block_table.shape
-    if k.shape[0] != T or v.shape[0] != T or q_out.shape[0] != T:
-        _refuse("q, k, v and q_out must have the same tokens")
+    T, H, d = _dims("q", q, 3)
+    P, Hkv, page, _ = _dims("k_pages", k_pages, 4)
+    B, width = _dims("block_table", block_table, 2)
     _pools(k_pages, v_pages, d, q.dtype, device)
     p = _pack_append(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(), k_pages.data_ptr(),
         v_pages.data_ptr(), _ints("block_table", block_table, (B, width), device),
         _ints("ctx_lens", ctx_lens, (B,), device),
         _ints("cu_seqlens", cu_seqlens, (B + 1,), device), _freqs_ptr(freqs, device),
-        _rows("q", q, H, d, q.dtype, device), _rows("k", k, Hkv, d, q.dtype, device),
-        _rows("v", v, Hkv, d, q.dtype, device), _rows("q_out", q_out, H, d, q.dtype, device),
+        _rows("q", q, T, H, d, q.dtype, device), _rows("k", k, T, Hkv, d, q.dtype, device),
+        _rows("v", v, T, Hkv, d, q.dtype, device),
+        _rows("q_out", q_out, T, H, d, q.dtype, device),
         T, B, H, Hkv, d, 2 * freqs.numel(), page, width, P, style, float(amplitude),
         _dtype_code(q))
     _check(lib().fa_rope_append(p, _stream(stream)))
@@ -608,14 +640,18 @@ def _pools(k_pages, v_pages, d, dtype, device):
 
 
 def fa_varlen_workspace_size(B, H, Hkv, total_q, total_k, d):
+    _int32(B=B, H=H, Hkv=Hkv, total_q=total_q, total_k=total_k, d=d)
     return lib().fa_varlen_workspace_size(B, H, Hkv, total_q, total_k, d)
 
 
 def fa_bwd_varlen_workspace_size(B, H, Hkv, total_q, total_k, d):
+    _int32(B=B, H=H, Hkv=Hkv, total_q=total_q, total_k=total_k, d=d)
     return lib().fa_bwd_varlen_workspace_size(B, H, Hkv, total_q, total_k, d)
 
 
 def fa_paged_varlen_workspace_size(B, H, Hkv, total_q, max_q, max_pages_per_seq, page_size, d):
+    _int32(B=B, H=H, Hkv=Hkv, total_q=total_q, max_q=max_q, max_pages_per_seq=max_pages_per_seq,
+           page_size=page_size, d=d)
     return lib().fa_paged_varlen_workspace_size(B, H, Hkv, total_q, max_q, max_pages_per_seq,
                                                 page_size, d)
 
@@ -623,16 +659,14 @@ def fa_paged_varlen_workspace_size(B, H, Hkv, total_q, max_q, max_pages_per_seq,
 def _varlen(q, k, v, o, lse, cu_seqlens_q, cu_seqlens_k, scale, workspace, mask_mode, window,
             n_global):
     device = _packed_device(q)
-    Tq, H, d = q.shape
-    Tk, Hkv, _ = k.shape
+    Tq, H, d = _dims("q", q, 3)
+    Tk, Hkv, _ = _dims("k", k, 3)
     B = cu_seqlens_q.numel() - 1
-    if o.shape[0] != Tq or v.shape[0] != Tk:
-        _refuse("o must have q's tokens, v k's")
     ws, ws_bytes = _bytes_of(workspace, device)
     return _pack_varlen(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), _lse_ptr(lse, Tq, H, device),
-        _rows("q", q, H, d, q.dtype, device), _rows("k", k, Hkv, d, q.dtype, device),
-        _rows("v", v, Hkv, d, q.dtype, device), _rows("o", o, H, d, q.dtype, device),
+        _rows("q", q, Tq, H, d, q.dtype, device), _rows("k", k, Tk, Hkv, d, q.dtype, device),
+        _rows("v", v, Tk, Hkv, d, q.dtype, device), _rows("o", o, Tq, H, d, q.dtype, device),
         _ints("cu_seqlens_q", cu_seqlens_q, (B + 1,), device),
         _ints("cu_seqlens_k", cu_seqlens_k, (B + 1,), device), B, H, Hkv, d, Tq, Tk,
         float(scale), mask_mode, window, n_global, _dtype_code(q), ws, ws_bytes, 0)
@@ -659,13 +693,11 @@ def fa_bwd_varlen(q, k, v, o, dout, lse, dq, dk, dv, cu_seqlens_q, cu_seqlens_k,
                 n_global)
     Tq, H, d = q.shape
     Tk, Hkv, _ = k.shape
-    if dout.shape[0] != Tq or dq.shape[0] != Tq or dk.shape[0] != Tk or dv.shape[0] != Tk:
-        _refuse("dout and dq must have q's tokens, dk and dv k's")
     g = _pack_grads(dout.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
-                    _rows("dout", dout, H, d, q.dtype, q.device),
-                    _rows("dq", dq, H, d, q.dtype, q.device),
-                    _rows("dk", dk, Hkv, d, q.dtype, q.device),
-                    _rows("dv", dv, Hkv, d, q.dtype, q.device))
+                    _rows("dout", dout, Tq, H, d, q.dtype, q.device),
+                    _rows("dq", dq, Tq, H, d, q.dtype, q.device),
+                    _rows("dk", dk, Tk, Hkv, d, q.dtype, q.device),
+                    _rows("dv", dv, Tk, Hkv, d, q.dtype, q.device))
     _check(lib().fa_bwd_varlen(p, g, _stream(stream)))
 
 
@@ -677,11 +709,9 @@ def fa_fwd_paged_varlen(q, k_pages, v_pages, block_table, ctx_lens, cu_seqlens_q
     [B, max_pages]; ctx_lens int32 [B] (cached keys, the chunk's included); max_q at least the
     longest chunk. workspace: a CUDA byte tensor of fa_paged_varlen_workspace_size(...)."""
     device = _packed_device(q)
-    Tq, H, d = q.shape
-    P, Hkv, page, _ = k_pages.shape
-    B, width = block_table.shape
-    if o.shape[0] != Tq:
-        _refuse("o must have q's tokens")
+    Tq, H, d = _dims("q", q, 3)
+    P, Hkv, page, _ = _dims("k_pages", k_pages, 4)
+    B, width = _dims("block_table", block_table, 2)
     _pools(k_pages, v_pages, d, q.dtype, device)
     ws, ws_bytes = _bytes_of(workspace, device)
     p = _pack_paged(
@@ -689,7 +719,7 @@ def fa_fwd_paged_varlen(q, k_pages, v_pages, block_table, ctx_lens, cu_seqlens_q
         _ints("block_table", block_table, (B, width), device),
         _ints("ctx_lens", ctx_lens, (B,), device),
         _ints("cu_seqlens_q", cu_seqlens_q, (B + 1,), device), o.data_ptr(),
-        _lse_ptr(lse, Tq, H, device), _rows("q", q, H, d, q.dtype, device),
-        _rows("o", o, H, d, q.dtype, device), B, H, Hkv, d, Tq, max_q, page, width, P,
+        _lse_ptr(lse, Tq, H, device), _rows("q", q, Tq, H, d, q.dtype, device),
+        _rows("o", o, Tq, H, d, q.dtype, device), B, H, Hkv, d, Tq, max_q, page, width, P,
         float(scale), mask_mode, window, n_global, _dtype_code(q), ws, ws_bytes, 0)
     _check(lib().fa_fwd_paged_varlen(p, _stream(stream)))
