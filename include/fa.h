@@ -482,6 +482,7 @@ fa_status fa_rope_append(const fa_rope_append_params* params, fa_stream_t stream
  *   cu_seqlens_q, cu_seqlens_k [B + 1] (the same array for self-attention)
  *   d 64 or 128; dtype FA_F16 or FA_BF16; token steps a multiple of 8 elements; scale positive;
  *   mask_mode every mask but FA_MASK_BLOCK_SPARSE, with window and n_global per sequence.
+ *   A query that sees no key gets o = 0 and lse = -inf, one with a NaN among its scores NaN in both.
  *   workspace  device scratch of fa_varlen_workspace_size(...) bytes, 16-byte aligned, owned by
  *              the caller; its contents on entry do not matter. Calls that may overlap on the
  *              GPU, two captured graphs among them, need workspaces of their own.

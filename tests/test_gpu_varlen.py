@@ -541,3 +541,40 @@ def test_python_refusals_of_shapes_and_numbers():
             with pytest.raises(fa.FaError):
                 call(**dict(good, **kw))
     assert fa.fa_get_device_status() == fa.FA_OK
+
+
+def check_nan_rows(o, lse, hit, T):
+    """Rows (token, head) of `hit` are NaN in o and lse, every other of the T tokens is finite."""
+    want = torch.zeros(T, o.shape[1], dtype=torch.bool)
+    for t, h in hit:
+        want[t, h] = True
+    assert torch.equal(o[:T].isnan().all(-1).cpu(), want)
+    assert torch.equal(o[:T].isfinite().all(-1).cpu(), ~want)
+    assert torch.equal(lse[:T].isnan().cpu(), want)
+    assert torch.equal(lse[:T].isfinite().cpu(), ~want)
+
+
+@pytest.mark.parametrize("lens", [[300, 40, 3], [4000]], ids=str)
+@pytest.mark.parametrize("d,dt", [(64, "f16"), (128, "bf16")])
+def test_a_row_of_nan_scores_has_a_nan_lse(lens, d, dt):
+    """An -inf there would say that the row sees no key. Whole tiles, partial ones, split items."""
+    H, Hkv, T = 4, 2, sum(lens)
+    q, k, v, cu, _ = case(lens, lens, H, Hkv, d, DT[dt], seed=1)
+    hit = [(0, 1), (257, 3), (T - 1, 0)]
+    for t, h in hit:
+        q[t, h, t % d] = float("nan")
+    o, lse = forward(q.cuda(), k.cuda(), v.cuda(), cu, cu, 1 / math.sqrt(d))
+    check_nan_rows(o, lse, hit, T)
+
+
+@pytest.mark.parametrize("new,before", [([1, 2], [300, 5000]), ([40, 3], [30, 5000])], ids=str)
+def test_a_row_of_nan_scores_over_a_cache_has_a_nan_lse(new, before):
+    """Few rows (whole pairs and joined pieces) and the 128-row tiles."""
+    q, _, _, kp, vp, table, total, cu, _ = paged_case(new, before, 4, 2, 64, 16, torch.float16, 3)
+    T = sum(new)
+    hit = [(0, 1), (T - 1, 2)]
+    for t, h in hit:
+        q[t, h, 5] = float("nan")
+    o, lse = run_paged(q, kp, vp, table, total, cu, max(new), 0.125)
+    assert fa.fa_get_device_status() == fa.FA_OK
+    check_nan_rows(o, lse, hit, T)

@@ -531,7 +531,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         if (r >= rows) continue;
         const int head = w.kvh * p.G + r - tok[i] * p.G;
         if (whole) {
-          const float inv = l[i] > 0.f ? 1.f / l[i] : 0.f;
+          const float inv = l[i] != 0.f ? 1.f / l[i] : 0.f;
           uint16_t* dst = static_cast<uint16_t*>(p.o) +
                           static_cast<int64_t>(w.s.q0 + tok[i]) * p.o_token + head * D + 2 * cq;
 #pragma unroll
@@ -540,8 +540,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             *reinterpret_cast<uint32_t*>(dst + 8 * t) = BF16 ? cvt_pack_bf16(a, b) : cvt_pack_f16(a, b);
           }
           if (cq == 0 && p.lse)
-            p.lse[static_cast<size_t>(w.s.q0 + tok[i]) * p.H + head] =
-                l[i] > 0.f ? (m[i] + lg2_approx(l[i])) * 0.69314718055994531f : -INFINITY;
+            p.lse[static_cast<size_t>(w.s.q0 + tok[i]) * p.H + head] = lse_of(m[i], l[i]);
         } else {
           float* dst = p.part + (static_cast<size_t>(slot) * ROWS + r) * D + 2 * cq;
 #pragma unroll
@@ -623,7 +622,7 @@ __global__ void __launch_bounds__(kCompute) few_merge_kernel(const FewParams p) 
   for (int e = 0; e < E; ++e) s_acc[warp][lane * E + e] = acc[e];
   __syncthreads();
   const int tok = r / p.G, h = hd.kvh * p.G + r - tok * p.G;
-  const float inv = L > 0.f ? 1.f / L : 0.f;
+  const float inv = L != 0.f ? 1.f / L : 0.f;
   uint16_t* out =
       static_cast<uint16_t*>(p.o) + static_cast<int64_t>(hd.q0 + tok) * p.o_token + h * D;
   for (int e = 2 * threadIdx.x; e < D; e += 2 * kCompute) {
@@ -636,8 +635,7 @@ __global__ void __launch_bounds__(kCompute) few_merge_kernel(const FewParams p) 
         BF16 ? cvt_pack_bf16(a * inv, c * inv) : cvt_pack_f16(a * inv, c * inv);
   }
   if (threadIdx.x == 0 && p.lse)
-    p.lse[static_cast<size_t>(hd.q0 + tok) * p.H + h] =
-        L > 0.f ? (M + lg2_approx(L)) * 0.69314718055994531f : -INFINITY;
+    p.lse[static_cast<size_t>(hd.q0 + tok) * p.H + h] = lse_of(M, L);
 }
 
 template <int D, bool BF16>

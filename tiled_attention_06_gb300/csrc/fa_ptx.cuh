@@ -416,4 +416,10 @@ __device__ __forceinline__ float lg2_approx(float x) {
   return y;
 }
 
+// LSE of a row from its maximum (log2 units) and sum: -inf says that it sees no key (l = 0), NaN
+// scores leave a NaN.
+__device__ __forceinline__ float lse_of(float m, float l) {
+  return l != 0.f ? (m + lg2_approx(l)) * 0.69314718055994531f : -INFINITY;
+}
+
 }  // namespace fa

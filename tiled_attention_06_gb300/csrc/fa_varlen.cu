@@ -835,7 +835,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!ok) break;
     tc_fence_after();
     if (it.staged(q, p.TPT)) {
-      const float inv_l = l > 0.f ? 1.f / l : 0.f;
+      const float inv_l = l != 0.f ? 1.f / l : 0.f;
       // row `row` of the tile in the 128-byte swizzle of its TMA box: conflict-free stores
       const uint32_t dst = sRing + (pos - 2 + q) % C::NSLOT * C::TILE_BYTES + row * 128;
 #pragma unroll 1
@@ -857,9 +857,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       fence_proxy_async_smem();
       mbar_arrive(B(bars->o_staged[q]));
       if (valid && p.lse)
-        p.lse[orow] = l > 0.f ? (m_ref + lg2_approx(l)) * 0.69314718055994531f : -INFINITY;
+        p.lse[orow] = lse_of(m_ref, l);
     } else if (it.u.slot < 0) {
-      const float inv_l = l > 0.f ? 1.f / l : 0.f;
+      const float inv_l = l != 0.f ? 1.f / l : 0.f;
       const bool wide = ((reinterpret_cast<uintptr_t>(p.o) | (p.o_token * 2)) & 31u) == 0;
 #pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
@@ -884,7 +884,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (valid && p.lse)
-        p.lse[orow] = l > 0.f ? (m_ref + lg2_approx(l)) * 0.69314718055994531f : -INFINITY;
+        p.lse[orow] = lse_of(m_ref, l);
     } else {  // partial result: O unnormalised, m in log2 units, l
       float* slot = p.part + (static_cast<size_t>(it.u.slot) * p.Hkv + it.kvh) *
                                  (static_cast<size_t>(kVarSplitRows) * (D + 2));
@@ -986,7 +986,7 @@ __global__ void __launch_bounds__(kMergeThreads) var_merge_kernel(const VarParam
       if ((s1 += N) >= g.n) break;
       load(s1);
     }
-    const float inv = L > 0.f ? 1.f / L : 0.f;
+    const float inv = L != 0.f ? 1.f / L : 0.f;
     const int h = kvh * p.G + (r % kTile) % p.G;
     uint32_t* out = reinterpret_cast<uint32_t*>(
         static_cast<uint16_t*>(p.o) + static_cast<int64_t>(g.q0 + tok) * p.o_token + h * D);
@@ -995,8 +995,7 @@ __global__ void __launch_bounds__(kMergeThreads) var_merge_kernel(const VarParam
       out[(lane * E + e) / 2] = BF16 ? cvt_pack_bf16(acc[e] * inv, acc[e + 1] * inv)
                                      : cvt_pack_f16(acc[e] * inv, acc[e + 1] * inv);
     if (lane == 0 && p.lse)
-      p.lse[static_cast<size_t>(g.q0 + tok) * p.H + h] =
-          L > 0.f ? (M + lg2_approx(L)) * 0.69314718055994531f : -INFINITY;
+      p.lse[static_cast<size_t>(g.q0 + tok) * p.H + h] = lse_of(M, L);
   }
 }
 
