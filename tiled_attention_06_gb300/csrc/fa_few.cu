@@ -185,6 +185,8 @@ __global__ void __launch_bounds__(kThreads, 2)
       reinterpret_cast<Bars*>(smem + C::NST * 2 * C::TILE + C::COMB + C::STATES);
   auto B = [&](uint64_t& x) { return smem_u32(&x); };
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  // whatever ends this CTA early, the joining kernel finds no piece of it
+  if (threadIdx.x == 0) p.heads[blockIdx.x] = FewHead{0, 0, 0, 0};
   if (base & 1023u) {  // the swizzle needs the stages on 1024-byte boundaries
     if (threadIdx.x == 0) atomicOr(p.m.status, FA_DEV_SMEM_BASE);
     return;
@@ -225,7 +227,6 @@ __global__ void __launch_bounds__(kThreads, 2)
       at += n;
     }
   }
-  if (threadIdx.x == 0) p.heads[blockIdx.x] = FewHead{0, 0, 0, 0};
   if (blockIdx.x == 0 && threadIdx.x < kCompute) {  // chunks that see no key at all
     for (int b = tot.b0; b < tot.b1; ++b) {
       const FewSeq s = few_seq(p, b, false);
