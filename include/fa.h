@@ -518,6 +518,9 @@ size_t fa_varlen_workspace_size(int B, int H, int Hkv, int total_q, int total_k,
  * A key no query sees gets dk = dv = 0, a query that sees no key dq = 0. dq adds the key blocks'
  * contributions with FP32 atomics, so its last bit can differ between runs; dk and dv are the
  * same on every run.
+ * Where sequences claim the same rows (after a decreasing start), gradients of others may be
+ * missing too. FA_F16 rounds dS = P (dP - D) to 16 bits before the scale is applied, so above 65504
+ * it is infinite even where dq and dk would not be (a loss scale can lead there).
  */
 typedef struct fa_varlen_grads {
   const void* dout;

@@ -368,3 +368,34 @@ def test_bad_starts_of_one_side_leave_the_gradients_of_other_sequences():
                         0.125, dtype, fa.FA_MASK_CAUSAL)
         check_gradients((dq, dk, dv), ref, cu_q[2], cu_k[2], f"{cu_q} {cu_k}")
         assert dk[cu_k[2]:].isnan().all() and dv[cu_k[2]:].isnan().all()
+
+
+@pytest.mark.parametrize("H,Hkv,d", [(2, 1, 64), (8, 1, 128), (64, 1, 64)])
+@pytest.mark.parametrize("cu", [[0, 64, 0, 64], [0, 64, 0, 64, 0, 64, 0, 64], [10, 64, 3, 60, 0, 5]],
+                         ids=str)
+def test_sequences_that_claim_the_same_rows_stay_in_them(H, Hkv, d, cu):
+    """Reported, dk and dv of the claimed rows are finite, every other row is left alone."""
+    T, B, dtype = 72, len(cu) - 1, torch.float16
+    q, k, v, dout, _, _ = case([T], [T], H, Hkv, d, dtype, seed=H)
+    gq, gk, gv, gd = (x.cuda() for x in (q, k, v, dout))
+    o, dq = (torch.full((T, H, d), float("nan"), dtype=dtype, device="cuda") for _ in range(2))
+    dk, dv = (torch.full((T, Hkv, d), float("nan"), dtype=dtype, device="cuda") for _ in range(2))
+    lse = torch.full((T, H), float("nan"), device="cuda")
+    size = max(fa.fa_varlen_workspace_size(B, H, Hkv, T, T, d),
+               fa.fa_bwd_varlen_workspace_size(B, H, Hkv, T, T, d))
+    guard = 1 << 16
+    ws = torch.full((size + guard,), 255, dtype=torch.uint8, device="cuda")
+    fa.fa_fwd_varlen(gq, gk, gv, o, lse, i32(cu), i32(cu), 0.125, ws[:size])
+    assert fa.fa_get_device_status() == fa.FA_ERR_BAD_PAGE
+    o.nan_to_num_(0.0), lse.nan_to_num_(0.0)
+    ws[:size].fill_(255)
+    fa.fa_bwd_varlen(gq, gk, gv, o, gd, lse, dq, dk, dv, i32(cu), i32(cu), 0.125, ws[:size])
+    assert fa.fa_get_device_status() == fa.FA_ERR_BAD_PAGE
+    rows = torch.zeros(T, dtype=torch.bool)
+    for a, b in zip(cu, cu[1:]):
+        rows[a:max(a, b)] = True
+    for x in (dk, dv):
+        assert x[rows.cuda()].isfinite().all()
+    for x in (dq, dk, dv):
+        assert x[~rows.cuda()].isnan().all()
+    assert (ws[size:] == 255).all()
