@@ -26,6 +26,7 @@ constexpr double kTwoPi = 6.283185307179586476925286766559;
 
 bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
 size_t round16(size_t n) { return (n + 15) / 16 * 16; }
+size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 int ceil_div(long long a, long long b) { return static_cast<int>((a + b - 1) / b); }
 
 // A 16-bit tensor of three dimensions (the first of `d` contiguous elements) as a TMA map with
@@ -163,8 +164,11 @@ BwdLayout bwd_layout(int B, int H, int Hkv, int total_q, int total_k, int d) {
   const size_t planes = static_cast<size_t>(Hkv) * L.HS * L.slots;
   L.units = 64;
   L.seq_slot = L.units + round16(sizeof(fa::VarBwdUnit) * static_cast<size_t>(L.max_units));
-  L.stats = L.seq_slot + round16(sizeof(int32_t) * static_cast<size_t>(B));
-  L.dqacc = L.stats + round16(2 * static_cast<size_t>(total_q) * H * sizeof(float));
+  // from here on whole cache lines: with the accumulator 16 bytes off one, 11343 tokens in 4
+  // sequences took 806 us instead of 784
+  L.stats = round256(L.seq_slot + sizeof(int32_t) * static_cast<size_t>(B));
+  L.dqacc = round256(L.stats +
+                     (2 * static_cast<size_t>(total_q) * H + fa::kBwdHalf) * sizeof(float));
   L.part = L.dqacc + planes * fa::kBwdHalf * d * sizeof(float);
   L.total = L.part + (L.HS > 1 ? static_cast<size_t>(L.HS) * 2 * total_k * Hkv * d * sizeof(float)
                                : 0);

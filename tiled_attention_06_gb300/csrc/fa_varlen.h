@@ -155,7 +155,7 @@ struct VarBwdParams {
   int32_t* n_units;   // [16]: units; whether the slots were dealt out
   VarBwdUnit* units;
   int32_t* seq_slot;  // [B]: first slot of the sequence or -1, where slots were dealt out
-  float* stats;       // [2][Hkv HS][total_q][GS]: -lse log2(e), -D
+  float* stats;       // [2][Hkv HS][total_q][GS]: -lse log2(e), -D; a half behind them is read
   float* dqacc;       // [Hkv HS][slots][16 groups of 4 rows][D][4]
   float* part;        // HS > 1: [HS][2 (dk, dv)][total_k][Hkv][D]
 };

@@ -240,7 +240,9 @@ __device__ __forceinline__ HalfRows half_rows_sorted(const VarBwdParams& p, int 
 }
 // The same after the plan has run: where slots were dealt out, every sequence is asked.
 __device__ __forceinline__ HalfRows half_rows(const VarBwdParams& p, int s) {
-  if (!p.n_units[1]) return half_rows_sorted(p, s);
+  const int dealt = p.n_units[1];  // on its way during the search
+  const HalfRows sorted = half_rows_sorted(p, s);
+  if (!dealt) return sorted;
   for (int b0 = 0; b0 < p.B; b0 += 32) {
     const int b = b0 + static_cast<int>(threadIdx.x % 32);
     SeqRows r{0, 0, true};
@@ -626,9 +628,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = bars->tmem_base;
   const WaitCtx wc{&bars->abort, p.m.status, p.m.timeout_ns};
   const size_t slot0 = static_cast<size_t>(hh) * p.slots + u.slot0 + u.h0;  // of half 0
-  // statistics of this head subset: -LSE log2(e) of every (token, head), then -D
-  const float* nl = p.stats + static_cast<size_t>(hh) * p.total_q * p.GS;
-  const float* nd = nl + static_cast<size_t>(p.total_q) * p.H;
 
   if (warp == kTmaWarp) {
     // ------------------------------------------------------------ TMA
@@ -636,6 +635,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     uint32_t fills[kStages] = {0, 0, 0, 0};
     const uint32_t bytes = 2 * static_cast<uint32_t>(used) * D * 2;
+    // statistics of the first half: -LSE log2(e) of its rows by lanes 0-15, -D by lanes 16-31; rows
+    // that the half does not have hold others' or anything, and are hidden
+    const float* src = p.stats + static_cast<size_t>(hh) * p.total_q * p.GS +
+                       static_cast<size_t>(u.q0 + u.h0 * p.TPH) * p.GS + (lane % 16) * 4 +
+                       (lane < 16 ? 0 : static_cast<size_t>(p.total_q) * p.H);
+    const bool wide = p.GS % 4 == 0;
     if (leader && u.n > 0) {
       mbar_arrive_expect_tx(B(bars->res_full), 2 * C::TILE);
 #pragma unroll
@@ -650,19 +655,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < u.n && ok; ++i) {
       const int h = stage_of(i);
       // the half's statistics, loaded before the wait for the stage
-      const int tok0 = (u.h0 + i) * p.TPH, live = min(p.TPH, u.sq - tok0) * p.GS;
-      const size_t row = static_cast<size_t>(u.q0 + tok0) * p.GS + lane;
-      const bool a = lane < live, b = lane + 32 < live;
-      const float l0 = a ? nl[row] : 0.f, l1 = b ? nl[row + 32] : 0.f;
-      const float d0 = a ? nd[row] : 0.f, d1 = b ? nd[row + 32] : 0.f;
+      const float4 st = wide ? *reinterpret_cast<const float4*>(src)
+                             : make_float4(src[0], src[1], src[2], src[3]);
+      src += used;
       if (i >= kStages && !(ok = mbar_wait(B(bars->st_empty[h]), stage_parity(i - kStages), wc)))
         break;
-      float* st = stats + h * 2 * kHalf + lane;
-      st[0] = l0, st[32] = l1, st[kHalf] = d0, st[kHalf + 32] = d1;
+      reinterpret_cast<float4*>(stats + h * 2 * kHalf)[lane] = st;
       __syncwarp();  // the leader's arrive below releases every lane's writes
       if (leader) {
         mbar_arrive_expect_tx(B(bars->st_full[h]), bytes);
-        const int t = u.q0 + tok0;
+        const int t = u.q0 + (u.h0 + i) * p.TPH;
 #pragma unroll
         for (int c = 0; c < D / 64; ++c) {
           tma_load_3d(sQ(h) + c * (kHalf * 128), &tmQ, B(bars->st_full[h]), c * 64, head0, t);
