@@ -139,8 +139,10 @@ BwdLayout bwd_layout(int B, int H, int Hkv, int total_q, int total_k, int d) {
   // block on average. A CTA takes about 9 us around its halves of 64 rows and 1.1 us (0.6 at
   // d = 64) for each; under a causal mask a block sees half the queries on average and the first
   // block all of them. Subsets cost a summing pass (5 us, and their partials at 4 TB/s).
-  // One sequence of 4096, 8 heads on one: HS = 8 takes 137 us, 4 takes 210; 24 short ones of
-  // d = 64, 12 heads on 4: HS = 1 takes 44 us, 3 takes 61 (a planning launch of 5 us in all four).
+  // One sequence of 4096, 8 heads on one: HS = 8 took 137 us, 4 took 210; 24 short ones of
+  // d = 64, 12 heads on 4: HS = 1 took 44 us, 3 took 61 (measured when the plan was a launch of
+  // 5 us before all four). 152 is the number of SMs of a GB300, a constant so that the workspace
+  // has one size wherever it is asked for; another count would change the time alone.
   const double units = (total_k / 128 + (B + 1) / 2) * static_cast<double>(Hkv);
   const double all = static_cast<double>(total_q) / B * G / fa::kBwdHalf;
   const double each = d == 128 ? 1.1 : 0.6;

@@ -22,12 +22,13 @@
 //                     works for the other; with one tile S(0) | S(1) PV(0) | S(2) PV(1) | ...
 //   var_merge_kernel  joins the partial results of split items.
 //
-// Bounds. In the middle of an item a key block takes about 3000 cycles for both tiles: 2 x 16384
-// exponentials (2048 cycles of the SM's special-function units) with their maxima, scaling and
-// rounding, against 2600 cycles of MMAs. Around it an item takes about 3000 more: the last P V,
-// the output, the next item's first scores. 14266 tokens in 8 sequences, 32/8 heads of 128,
-// bf16, causal: 199 us, 1273 TFLOP/s (66 % of 1923.5 measured); 4 x 4096 tokens: 1467. Whole
-// tiles leave through ring slots held back for them and a TMA store, because 32 rows per warp
+// Bounds. In the middle of an item a key block takes about 3000 cycles for both tiles, the issue
+// and the latencies of the softmax's instructions (2 x 16384 exponentials with their maxima,
+// scaling and rounding), against 2600 cycles of MMAs; the special-function units alone are not the
+// limit (a third busy in the same softmax of fa_prefill.cu). Around it an item takes about 3000
+// more: the last P V, the output, the next item's first scores. 14266 tokens in 8 sequences, 32/8
+// heads of 128, bf16, causal: 198 to 209 us from one GPU to another, 1214 to 1280 TFLOP/s (63 to
+// 66 % of 1923.5 measured); 4 x 4096 tokens: 1467. Whole tiles leave through ring slots held back for them and a TMA store, because 32 rows per warp
 // instruction kept the load/store unit, and with it every other warp's loads, busy for 2000
 // cycles (211 -> 203 us). Branches inside the softmax that skip hidden columns cost more than
 // they save (199 -> 212 us).

@@ -20,11 +20,11 @@
 //                 warpgroups (two per half in flight, 32 columns each), TMA warp, MMA warp.
 //   bwd_dq        scales and rounds the accumulator into dq (HBM-bound).
 //   bwd_sum       HS > 1 alone: sums the head subsets' dk and dv, in order.
-// Bounds. 11343 tokens in 4 sequences, 32/8 heads of 128, bf16, causal: 795 us, 981 TFLOP/s over
-// the five products (51 % of 1923.5 measured); the main kernel 665 of them (1173 TFLOP/s, MMAs of
-// N = 64 issued by one thread and the elementwise warps in turn), prep 62 and dq 51, both at about
-// 5.5 TB/s of mostly accumulator traffic. 24 short sequences, 12/4 heads of 64: 39 us, three
-// launches and a CTA's fixed 9 us around 7 halves.
+// Bounds. 11343 tokens in 4 sequences, 32/8 heads of 128, bf16, causal: 784 to 817 us from one GPU
+// to another, 955 to 995 TFLOP/s over the five products (50 to 52 % of 1923.5 measured); the main
+// kernel 657 of them (1187 TFLOP/s, MMAs of N = 64 issued by one thread and the elementwise warps in
+// turn), prep 62 and dq 50, both at about 5.5 TB/s of mostly accumulator traffic. 24 short
+// sequences, 12/4 heads of 64: 37.5 us, three launches and a CTA's fixed 9 us around 7 halves.
 //
 // Rows of K, Q and dO behind a sequence's end belong to others: they are zeroed in shared
 // memory (0 times an infinity or NaN is not 0), and masked probabilities and dS are set to 0.
@@ -117,8 +117,8 @@ __device__ __forceinline__ Span queries_of_block(int j0, int n, int sq, int delt
 // ------------------------------------------------------------------ plan
 
 // The plan is one CTA of bwd_prep: a launch of its own, 1024 threads, put its 4 to 5 us before
-// everything else (24 short sequences 43.6 us against 39.1 here, 11343 tokens in 4 sequences 806
-// against 795). Thousands of tiny sequences lose a little by the fewer threads (4096 of 1 to 8
+// everything else (when it was moved here 24 short sequences went from 43.6 us to 39.1, 11343
+// tokens in 4 sequences from 806 to 795). Thousands of tiny sequences lose a little by the fewer threads (4096 of 1 to 8
 // tokens, 8 heads on one: 220 -> 229 us; on 12/4 heads they gain, 766 -> 744).
 constexpr int kPrepThreads = 256;
 struct BwdPlanSmem {
