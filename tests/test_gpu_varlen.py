@@ -578,3 +578,27 @@ def test_a_row_of_nan_scores_over_a_cache_has_a_nan_lse(new, before):
     o, lse = run_paged(q, kp, vp, table, total, cu, max(new), 0.125)
     assert fa.fa_get_device_status() == fa.FA_OK
     check_nan_rows(o, lse, hit, T)
+
+
+@pytest.mark.parametrize("cu", [[0, 5, 13], [0, 6, 4], [-1, 6, 12], [0, 3, 6, -5, 12],
+                                [0, 3, 6, 2 ** 31 - 1, 12], [6, 12, 0, 6]], ids=str)
+@pytest.mark.parametrize("max_q", [6, 60])
+def test_bad_starts_over_a_cache_are_reported_and_leave_others(cu, max_q):
+    """For few rows and for the 128-row tiles."""
+    H, Hkv, d, page, T, B = 4, 2, 64, 16, 12, len(cu) - 1
+    good = [0 <= a <= b <= T for a, b in zip(cu, cu[1:])]
+    new = [b - a if ok else 0 for a, b, ok in zip(cu, cu[1:], good)]
+    q, k, v, kp, vp, table, total, _, cu_k = paged_case(new, [40 + 70 * b for b in range(B)], H, Hkv,
+                                                       d, page, torch.float16, seed=2)
+    q = torch.randn(T, H, d, generator=torch.Generator().manual_seed(3)).half()
+    o, lse = run_paged(q, kp, vp, table, total, cu, max_q, 0.125)
+    assert fa.fa_get_device_status() == fa.FA_ERR_BAD_PAGE
+    rows = torch.ones(T, dtype=torch.bool)
+    for b in range(B):
+        if good[b]:
+            a, e, keys = cu[b], cu[b + 1], slice(cu_k[b], cu_k[b + 1])
+            rows[a:e] = False
+            ref = attention(q[a:e], k[keys], v[keys], [0, e - a], [0, total[b]], 0.125,
+                            fa.FA_MASK_CAUSAL)
+            check_forward(o[a:e], lse[a:e], ref, torch.float16, e - a, f"{cu} {b}")
+    assert o[rows.cuda()].isnan().all() and lse[rows.cuda()].isnan().all()
