@@ -80,7 +80,8 @@ enum {
   FA_MASK_CAUSAL_WINDOW = 2,
   FA_MASK_BAND = 3,
   FA_MASK_PREFIX_LM = 4,
-  FA_MASK_BLOCK_SPARSE = 5
+  FA_MASK_BLOCK_SPARSE = 5,
+  FA_MASK_TREE = 6 /* fa_fwd_paged_varlen_ex only */
 };
 
 /* Block size of a block-sparse layout (query rows x keys). */
@@ -571,6 +572,188 @@ typedef struct fa_paged_varlen_params {
 fa_status fa_fwd_paged_varlen(const fa_paged_varlen_params* params, fa_stream_t stream);
 size_t fa_paged_varlen_workspace_size(int B, int H, int Hkv, int total_q, int max_q,
                                       int max_pages_per_seq, int page_size, int d);
+
+/*
+ * ---------------------------------------------------------------------------------------
+ * Norms of query and key heads, positions of several axes, an 8-bit cache, drafted trees.
+ */
+
+/* Norm of fa_norm_rope and its kin: none, or by the root of the mean square. */
+enum { FA_NORM_NONE = 0, FA_NORM_RMS = 1 };
+/* Most axes of a position. */
+#define FA_MAX_AXES 4
+
+/*
+ * fa_rope_axes - which axis turns which rotated pair, on the HOST: pair_axis[i], i < rot_dim / 2.
+ * sections[a] pairs belong to axis a (they add up to rot_dim / 2): in blocks, axis after axis, or,
+ * interleaved, dealt out in turns to the axes that have pairs left.
+ */
+fa_status fa_rope_axes(int32_t* pair_axis, int rot_dim, const int32_t* sections, int axes,
+                       int interleaved);
+
+/*
+ * fa_norm_rope - the step between a projection and attention: norm every head of q and k on its
+ * own, then rotate it, in one pass. With FA_NORM_RMS
+ *     n = x / sqrt(mean(x^2) + eps) * weight     (over the d elements of a head; FP32),
+ * with FA_NORM_NONE n = x; then y is n rotated as fa_rope does, pair i by the angle
+ * positions[pair_axis[i]][token] * freqs[i]. One rounding, at the store.
+ *   q, q_out   element e of head h of token t at t * q_token + h * q_head + e (and so on);
+ *   k, k_out   the same for Hkv heads; Hkv = 0: none (k, k_out and k_weight are ignored).
+ *              q_out may be q with the same steps (in place), and k_out k; otherwise outputs
+ *              overlap neither inputs nor each other.
+ *   positions  int32 [axes][T], device; any values
+ *   pair_axis  int32 [rot_dim / 2], device, in [0, axes); NULL: axis 0. A value out of range is
+ *              read as 0 and reported as FA_ERR_BAD_PAGE.
+ *   freqs      float64 [rot_dim / 2], device
+ *   q_weight, k_weight  [d] of weight_dtype (FA_F32 or dtype); NULL: ones. Ignored without a norm.
+ *   T >= 0, H >= 1, Hkv >= 0, d even in [2, 512], rot_dim even in [2, d], axes in
+ *   [1, FA_MAX_AXES], eps >= 0; dtype FA_F16, FA_BF16 or FA_F32. Alignment as for fa_rope: with
+ *   16-byte aligned pointers, steps of a multiple of 16 bytes and rot_dim and d a multiple of 32
+ *   bytes, heads move in 16-byte accesses, else element by element.
+ */
+typedef struct fa_norm_rope_params {
+  const void* q;
+  const void* k;
+  void* q_out;
+  void* k_out;
+  const int32_t* positions;
+  const int32_t* pair_axis;
+  const double* freqs;
+  const void* q_weight;
+  const void* k_weight;
+  int64_t T;
+  int64_t q_token, q_head, k_token, k_head, q_out_token, q_out_head, k_out_token, k_out_head;
+  int H, Hkv, d, rot_dim, axes, style;
+  float amplitude;
+  int norm;
+  float eps;
+  int weight_dtype, dtype;
+} fa_norm_rope_params;
+
+fa_status fa_norm_rope(const fa_norm_rope_params* params, fa_stream_t stream);
+
+/*
+ * fa_norm_rope_bwd - gradients of fa_norm_rope: params holds the forward call's arguments (q_out
+ * and k_out are not read), grads the upstream gradients dq_out and dk_out and the outputs
+ *     g = R^T dy,   dx = r w g - x r^3 mean(w g x),   dweight = sum over tokens and heads of g x r
+ * with r = 1 / sqrt(mean(x^2) + eps) and R the rotation. dq may be dq_out with the same steps (in
+ * place), and dk dk_out.
+ *   dq_weight, dk_weight  float32 [d], written (not added to); NULL: not wanted
+ *   workspace  device scratch of fa_norm_rope_bwd_workspace_size(...) bytes, 16-byte aligned, for
+ *              calls that want a weight's gradient (else it may be NULL); calls that may overlap
+ *              need workspaces of their own.
+ * The same bits on every run on the same GPU. With T = 0 the weights' gradients are zeroed.
+ */
+typedef struct fa_norm_rope_grads {
+  const void* dq_out;
+  const void* dk_out;
+  void* dq;
+  void* dk;
+  float* dq_weight;
+  float* dk_weight;
+  int64_t dq_out_token, dq_out_head, dk_out_token, dk_out_head;
+  int64_t dq_token, dq_head, dk_token, dk_head;
+  void* workspace;
+  size_t workspace_bytes;
+} fa_norm_rope_grads;
+
+fa_status fa_norm_rope_bwd(const fa_norm_rope_params* params, const fa_norm_rope_grads* grads,
+                           fa_stream_t stream);
+size_t fa_norm_rope_bwd_workspace_size(int H, int Hkv, int d);
+
+/*
+ * The 8-bit cache. Pools k_pages, v_pages [num_pages, Hkv, page_size, d] of one byte per element,
+ * and exponent bytes k_scales, v_scales [num_pages, Hkv, page_size], one per row (token and head).
+ * An element is a float of 4 exponent and 3 mantissa bits (e4m3, largest finite 448); its value is
+ * that times 2^(byte - 127), byte the smallest in [0, 254] that brings the row's largest magnitude
+ * within 448; to nearest, ties to even, from the FP32 value (no rounding to 16 bits before). A row
+ * with an infinity or a NaN gets byte 255 (and zero elements) and every element of it is NaN when
+ * read. Times a power of two the elements are exact in 16 bits (in FA_F16 down to 2^-24), so
+ * fa_fwd_paged_varlen_ex computes with exactly these values. Element bytes 0x7f and 0xff, which
+ * fa_norm_rope_append does not write, are NaN to fa_kv_read; to fa_fwd_paged_varlen_ex they
+ * are NaN or +-480.
+ *
+ * fa_norm_rope_append - fa_rope_append with a norm of q and k (as fa_norm_rope), with positions of
+ * several axes, and into either cache: 8 bits where k_scales is given, else pools of dtype.
+ *   positions  int32 [axes][T], device: the angles' positions (a drafted tree's depths, an image's
+ *              rows and columns); NULL (axes = 1): the tokens' places. Where a token is stored is
+ *              its place, ctx_lens[b] + t - cu_seqlens[b], either way.
+ * Everything else as for fa_rope_append and fa_norm_rope; H, Hkv >= 1.
+ */
+typedef struct fa_norm_rope_append_params {
+  const void* q;
+  const void* k;
+  const void* v;
+  void* q_out;
+  void* k_pages;
+  void* v_pages;
+  uint8_t* k_scales;
+  uint8_t* v_scales;
+  const int32_t* block_table; /* [B, max_pages_per_seq] */
+  const int32_t* ctx_lens;    /* [B] */
+  const int32_t* cu_seqlens;  /* [B + 1] */
+  const int32_t* positions;
+  const int32_t* pair_axis;
+  const double* freqs;
+  const void* q_weight;
+  const void* k_weight;
+  int64_t q_token, k_token, v_token, q_out_token;
+  int T, B, H, Hkv, d, rot_dim, axes, page_size, max_pages_per_seq, num_pages;
+  int style;
+  float amplitude;
+  int norm;
+  float eps;
+  int weight_dtype, dtype;
+} fa_norm_rope_append_params;
+
+fa_status fa_norm_rope_append(const fa_norm_rope_append_params* params, fa_stream_t stream);
+
+/*
+ * fa_kv_read - rows of an 8-bit cache back in 16 bits: token t of sequence b, cu_seqlens[b] <= t <
+ * cu_seqlens[b+1], is the cached position starts[b] + t - cu_seqlens[b] of its sequence.
+ *   k, v  [T, Hkv, d] dtype FA_F16 or FA_BF16, written; steps a multiple of 8 elements
+ *   starts int32 [B]; d 64 or 128; page_size a multiple of 16 in [16, 4096]
+ * A position whose table entry is outside [0, num_pages), or that is beyond page_size *
+ * max_pages_per_seq or below 0, gives zeros and is reported as FA_ERR_BAD_PAGE. Rows that no
+ * sequence owns are left as they were. What is beyond dtype's range becomes an infinity.
+ */
+typedef struct fa_kv_read_params {
+  const void* k_pages;
+  const void* v_pages;
+  const uint8_t* k_scales;
+  const uint8_t* v_scales;
+  const int32_t* block_table; /* [B, max_pages_per_seq] */
+  const int32_t* starts;      /* [B] */
+  const int32_t* cu_seqlens;  /* [B + 1] */
+  void* k;
+  void* v;
+  int64_t k_token, v_token;
+  int T, B, Hkv, d, page_size, max_pages_per_seq, num_pages, dtype;
+} fa_kv_read_params;
+
+fa_status fa_kv_read(const fa_kv_read_params* params, fa_stream_t stream);
+
+/*
+ * fa_fwd_paged_varlen_ex - fa_fwd_paged_varlen over either cache and with one more mask.
+ *   k_scales, v_scales  given: params' pools are an 8-bit cache (both or neither)
+ *   tree                given (with mask_mode FA_MASK_TREE, and only then): uint32 [total_q]
+ *                       [tree_words], device; bit j % 32 of word j / 32 of a query's row says
+ *                       whether it sees token j of its own chunk (its ancestors and itself, in a
+ *                       tree of drafted tokens). Keys before the chunk are seen by every query.
+ *                       32 * tree_words >= max_q; bits from the chunk's length on are ignored.
+ * A query without any key gets o = 0 and lse = -inf. A NaN in a row of V reaches every query of
+ * its sequence, seen or not (as in fa_fwd_paged_varlen). The workspace, of
+ * fa_paged_varlen_workspace_size(...) bytes, and everything else as for fa_fwd_paged_varlen.
+ */
+typedef struct fa_paged_varlen_extra {
+  const uint8_t* k_scales;
+  const uint8_t* v_scales;
+  const uint32_t* tree;
+  int tree_words;
+} fa_paged_varlen_extra;
+
+fa_status fa_fwd_paged_varlen_ex(const fa_paged_varlen_params* params,
+                                 const fa_paged_varlen_extra* extra, fa_stream_t stream);
 
 /*
  * fa_get_device_status - synchronise `stream`, then read and clear the device

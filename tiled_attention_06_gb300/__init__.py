@@ -29,14 +29,20 @@ __all__ = [
     "FA_ERR_BAD_PAGE", "FA_F16", "FA_BF16", "FA_F32", "FA_MASK_NONE", "FA_MASK_CAUSAL",
     "FA_MASK_CAUSAL_WINDOW", "FA_MASK_BAND", "FA_MASK_PREFIX_LM", "FA_MASK_BLOCK_SPARSE",
     "FA_LAYOUT_BLOCK",
+    "fa_rope_axes", "fa_norm_rope", "fa_norm_rope_bwd", "fa_norm_rope_bwd_workspace_size",
+    "fa_norm_rope_append", "fa_kv_read", "fa_fwd_paged_varlen_ex", "FA_NORM_NONE", "FA_NORM_RMS",
+    "FA_MASK_TREE", "FA_MAX_AXES",
 ]
 
 FA_OK, FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED, FA_ERR_CUDA, FA_ERR_TIMEOUT, FA_ERR_BAD_PAGE = range(6)
 FA_F16, FA_BF16, FA_F32 = 0, 1, 2
 FA_MASK_NONE, FA_MASK_CAUSAL, FA_MASK_CAUSAL_WINDOW, FA_MASK_BAND, FA_MASK_PREFIX_LM = 0, 1, 2, 3, 4
 FA_MASK_BLOCK_SPARSE = 5
+FA_MASK_TREE = 6
 FA_LAYOUT_BLOCK = 128
 FA_ROPE_HALF, FA_ROPE_PAIRS = 0, 1
+FA_NORM_NONE, FA_NORM_RMS = 0, 1
+FA_MAX_AXES = 4
 FA_ROPE_PLAIN, FA_ROPE_LINEAR, FA_ROPE_BASE, FA_ROPE_BY_PARTS = 0, 1, 2, 3
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libfa.so")
@@ -106,6 +112,46 @@ class PagedVarlenParams(ctypes.Structure):
                 ("workspace_bytes", _sz), ("timeout_us", _u32)]
 
 
+class NormRopeParams(ctypes.Structure):
+    _fields_ = [("q", _vp), ("k", _vp), ("q_out", _vp), ("k_out", _vp), ("positions", _vp),
+                ("pair_axis", _vp), ("freqs", _vp), ("q_weight", _vp), ("k_weight", _vp),
+                ("T", _i64), ("q_token", _i64), ("q_head", _i64), ("k_token", _i64),
+                ("k_head", _i64), ("q_out_token", _i64), ("q_out_head", _i64),
+                ("k_out_token", _i64), ("k_out_head", _i64), ("H", _i), ("Hkv", _i), ("d", _i),
+                ("rot_dim", _i), ("axes", _i), ("style", _i), ("amplitude", _f), ("norm", _i),
+                ("eps", _f), ("weight_dtype", _i), ("dtype", _i)]
+
+
+class NormRopeGrads(ctypes.Structure):
+    _fields_ = [("dq_out", _vp), ("dk_out", _vp), ("dq", _vp), ("dk", _vp), ("dq_weight", _vp),
+                ("dk_weight", _vp), ("dq_out_token", _i64), ("dq_out_head", _i64),
+                ("dk_out_token", _i64), ("dk_out_head", _i64), ("dq_token", _i64),
+                ("dq_head", _i64), ("dk_token", _i64), ("dk_head", _i64), ("workspace", _vp),
+                ("workspace_bytes", _sz)]
+
+
+class NormRopeAppendParams(ctypes.Structure):
+    _fields_ = [("q", _vp), ("k", _vp), ("v", _vp), ("q_out", _vp), ("k_pages", _vp),
+                ("v_pages", _vp), ("k_scales", _vp), ("v_scales", _vp), ("block_table", _vp),
+                ("ctx_lens", _vp), ("cu_seqlens", _vp), ("positions", _vp), ("pair_axis", _vp),
+                ("freqs", _vp), ("q_weight", _vp), ("k_weight", _vp), ("q_token", _i64),
+                ("k_token", _i64), ("v_token", _i64), ("q_out_token", _i64), ("T", _i), ("B", _i),
+                ("H", _i), ("Hkv", _i), ("d", _i), ("rot_dim", _i), ("axes", _i),
+                ("page_size", _i), ("max_pages_per_seq", _i), ("num_pages", _i), ("style", _i),
+                ("amplitude", _f), ("norm", _i), ("eps", _f), ("weight_dtype", _i), ("dtype", _i)]
+
+
+class KvReadParams(ctypes.Structure):
+    _fields_ = [("k_pages", _vp), ("v_pages", _vp), ("k_scales", _vp), ("v_scales", _vp),
+                ("block_table", _vp), ("starts", _vp), ("cu_seqlens", _vp), ("k", _vp), ("v", _vp),
+                ("k_token", _i64), ("v_token", _i64), ("T", _i), ("B", _i), ("Hkv", _i), ("d", _i),
+                ("page_size", _i), ("max_pages_per_seq", _i), ("num_pages", _i), ("dtype", _i)]
+
+
+class PagedVarlenExtra(ctypes.Structure):
+    _fields_ = [("k_scales", _vp), ("v_scales", _vp), ("tree", _vp), ("tree_words", _i)]
+
+
 _lib = None
 
 
@@ -169,12 +215,17 @@ def lib():
                                     ctypes.c_double]
         L.fa_rope.restype = _i
         L.fa_rope.argtypes = [_vp] * 4 + [_i64, _i, _i, _i] + [_i64] * 4 + [_i, _f, _i, _i, _vp]
+        L.fa_rope_axes.restype = _i
+        L.fa_rope_axes.argtypes = [_vp, _i, _vp, _i, _i]
         for name, n in (("fa_rope_append", 1), ("fa_fwd_varlen", 1), ("fa_bwd_varlen", 2),
-                        ("fa_fwd_paged_varlen", 1)):  # pointers to their parameter structs
+                        ("fa_fwd_paged_varlen", 1), ("fa_norm_rope", 1), ("fa_norm_rope_bwd", 2),
+                        ("fa_norm_rope_append", 1), ("fa_kv_read", 1),
+                        ("fa_fwd_paged_varlen_ex", 2)):  # pointers to their parameter structs
             getattr(L, name).restype = _i
             getattr(L, name).argtypes = [_vp] * n + [_vp]
         for name, n in (("fa_varlen_workspace_size", 6), ("fa_bwd_varlen_workspace_size", 6),
-                        ("fa_paged_varlen_workspace_size", 8)):
+                        ("fa_paged_varlen_workspace_size", 8),
+                        ("fa_norm_rope_bwd_workspace_size", 3)):
             getattr(L, name).restype = _sz
             getattr(L, name).argtypes = [_i] * n
         _lib = L
@@ -497,6 +548,11 @@ _pack_append = _packer(RopeAppendParams)
 _pack_varlen = _packer(VarlenParams)
 _pack_grads = _packer(VarlenGrads)
 _pack_paged = _packer(PagedVarlenParams)
+_pack_norm_rope = _packer(NormRopeParams)
+_pack_norm_grads = _packer(NormRopeGrads)
+_pack_norm_append = _packer(NormRopeAppendParams)
+_pack_kv_read = _packer(KvReadParams)
+_pack_extra = _packer(PagedVarlenExtra)
 
 
 def _rows(name, t, n, heads, d, dtype, device):
@@ -723,3 +779,226 @@ def fa_fwd_paged_varlen(q, k_pages, v_pages, block_table, ctx_lens, cu_seqlens_q
         _rows("o", o, Tq, H, d, q.dtype, device), B, H, Hkv, d, Tq, max_q, page, width, P,
         float(scale), mask_mode, window, n_global, _dtype_code(q), ws, ws_bytes, 0)
     _check(lib().fa_fwd_paged_varlen(p, _stream(stream)))
+
+
+# ------------------------------------- norms, positions of several axes, 8-bit cache, trees
+
+def fa_rope_axes(sections, interleaved=False, device=None):
+    """int32 [sum(sections)]: which axis turns which rotated pair, sections[a] pairs for axis a, in
+    blocks or (interleaved) dealt out in turns. On `device` (CPU when None)."""
+    n = len(sections)
+    _int32(axes=n, **{f"sections_{i}": x for i, x in enumerate(sections)})
+    pairs = sum(sections)
+    host = torch.empty(min(max(pairs, 1), 256), dtype=torch.int32)
+    _check(lib().fa_rope_axes(host.data_ptr(), min(2 * pairs, 2 ** 30), (_i * max(n, 1))(*sections),
+                              n, 1 if interleaved else 0))
+    return host if device is None else host.to(device)
+
+
+def _heads(name, t, T, heads, d, dtype, device):
+    """(pointer, elements between tokens, between heads) of rows of heads [T, heads, d]."""
+    if t.shape != (T, heads, d) or t.dtype != dtype or t.device != device:
+        _refuse(f"{name} must be [{T}, {heads}, {d}] of {dtype} on {device}, not "
+                f"{list(t.shape)} of {t.dtype} on {t.device}")
+    st = t.stride()
+    if d > 1 and st[2] != 1:
+        _refuse(f"{name}: the elements of a head must be contiguous")
+    head = st[1] if heads > 1 else d
+    return t.data_ptr(), st[0] if T > 1 else (heads - 1) * head + d, head
+
+
+def _weight(name, w, d, dtype, device):
+    if w is None:
+        return 0
+    if w.shape != (d,) or w.device != device or not w.is_contiguous() \
+            or (w.dtype != dtype and w.dtype != torch.float32):
+        _refuse(f"{name} must be a contiguous [{d}] tensor of {dtype} or float32 on {device}")
+    return w.data_ptr()
+
+
+def _weights(q_weight, k_weight, d, dtype, device):
+    """(pointers, their common dtype's code)"""
+    if q_weight is not None and k_weight is not None and q_weight.dtype != k_weight.dtype:
+        _refuse("q_weight and k_weight must have the same dtype")
+    one = q_weight if q_weight is not None else k_weight
+    code = FA_F32 if one is None or one.dtype == torch.float32 else _dtype_code(one)
+    return (_weight("q_weight", q_weight, d, dtype, device),
+            _weight("k_weight", k_weight, d, dtype, device), code)
+
+
+def _axes(positions, pair_axis, freqs, T, device):
+    """(positions' pointer, pair_axis' pointer, number of axes)"""
+    axes = 1 if positions is None or positions.dim() == 1 else positions.shape[0]
+    at = 0
+    if positions is not None:
+        shape = (T,) if positions.dim() == 1 else (axes, T)
+        at = _ints("positions", positions, shape, device)
+    if pair_axis is None:
+        return at, 0, axes
+    return at, _ints("pair_axis", pair_axis, (freqs.numel(),), device), axes
+
+
+def _norm_rope(q, k, q_out, k_out, positions, freqs, q_weight, k_weight, norm, eps, pair_axis,
+               style, amplitude):
+    device = _packed_device(q)
+    T, H, d = _dims("q", q, 3)
+    Hkv = 0 if k is None else _dims("k", k, 3)[1]
+    if (k is None) != (k_out is None):
+        _refuse("k and its counterpart: both or neither")
+    none = (0, 0, 0)
+    a = _heads("q", q, T, H, d, q.dtype, device)
+    b = _heads("q_out", q_out, T, H, d, q.dtype, device)
+    c = _heads("k", k, T, Hkv, d, q.dtype, device) if Hkv else none
+    e = _heads("k_out", k_out, T, Hkv, d, q.dtype, device) if Hkv else none
+    at, pairs, axes = _axes(positions, pair_axis, freqs, T, device)
+    wq, wk, code = _weights(q_weight, k_weight, d, q.dtype, device)
+    return _pack_norm_rope(
+        a[0], c[0], b[0], e[0], at, pairs, _freqs_ptr(freqs, device), wq, wk, T, a[1], a[2], c[1],
+        c[2], b[1], b[2], e[1], e[2], H, Hkv, d, 2 * freqs.numel(), axes, style, float(amplitude),
+        norm, float(eps), code, _dtype_code(q))
+
+
+def fa_norm_rope(q, k, q_out, k_out, positions, freqs, q_weight=None, k_weight=None,
+                 norm=FA_NORM_NONE, eps=1e-6, pair_axis=None, style=FA_ROPE_HALF, amplitude=1.0,
+                 stream=None):
+    """Norm (FA_NORM_RMS: x / sqrt(mean(x^2) + eps) * weight, per head) and rotate q [T, H, d] and
+    k [T, Hkv, d] (or None) into q_out and k_out (which may be q and k). positions int32 [axes, T]
+    or [T]; pair_axis int32 [len(freqs)] says which axis turns which pair (fa_rope_axes); weights
+    [d] of q's dtype or float32, None: ones. float16, bfloat16 or float32; any token and head
+    steps."""
+    p = _norm_rope(q, k, q_out, k_out, positions, freqs, q_weight, k_weight, norm, eps, pair_axis,
+                   style, amplitude)
+    _check(lib().fa_norm_rope(p, _stream(stream)))
+
+
+def fa_norm_rope_bwd_workspace_size(H, Hkv, d):
+    _int32(H=H, Hkv=Hkv, d=d)
+    return lib().fa_norm_rope_bwd_workspace_size(H, Hkv, d)
+
+
+def fa_norm_rope_bwd(q, k, dq_out, dk_out, dq, dk, positions, freqs, q_weight=None, k_weight=None,
+                     dq_weight=None, dk_weight=None, workspace=None, norm=FA_NORM_NONE, eps=1e-6,
+                     pair_axis=None, style=FA_ROPE_HALF, amplitude=1.0, stream=None):
+    """Gradients of fa_norm_rope: dq, dk (which may be dq_out and dk_out) and, where given, the
+    float32 [d] gradients of the weights, from the upstream dq_out and dk_out. workspace: a CUDA
+    byte tensor of fa_norm_rope_bwd_workspace_size(...), needed for the weights' gradients."""
+    p = _norm_rope(q, k, q, k, positions, freqs, q_weight, k_weight, norm, eps, pair_axis, style,
+                   amplitude)
+    device, (T, H, d) = q.device, q.shape
+    Hkv = 0 if k is None else k.shape[1]
+    if (k is None) != (dk_out is None) or (k is None) != (dk is None):
+        _refuse("k, dk_out and dk: all or none")
+    none = (0, 0, 0)
+    a = _heads("dq_out", dq_out, T, H, d, q.dtype, device)
+    b = _heads("dk_out", dk_out, T, Hkv, d, q.dtype, device) if Hkv else none
+    c = _heads("dq", dq, T, H, d, q.dtype, device)
+    e = _heads("dk", dk, T, Hkv, d, q.dtype, device) if Hkv else none
+    for name, w in (("dq_weight", dq_weight), ("dk_weight", dk_weight)):
+        if w is not None and w.dtype != torch.float32:
+            _refuse(f"{name} must be a contiguous [{d}] tensor of float32 on {device}")
+    ws, ws_bytes = (0, 0) if workspace is None else _bytes_of(workspace, device)
+    g = _pack_norm_grads(
+        a[0], b[0], c[0], e[0], _weight("dq_weight", dq_weight, d, q.dtype, device),
+        _weight("dk_weight", dk_weight, d, q.dtype, device), a[1], a[2], b[1], b[2], c[1], c[2],
+        e[1], e[2], ws, ws_bytes)
+    _check(lib().fa_norm_rope_bwd(p, g, _stream(stream)))
+
+
+def _bytes8(name, t, shape, dtype, device):
+    """An 8-bit tensor: the named float type or uint8."""
+    if t.shape != shape or (t.dtype != dtype and t.dtype != torch.uint8) or t.device != device \
+            or not t.is_contiguous():
+        _refuse(f"{name} must be contiguous {list(shape)} of {dtype} or uint8 on {device}")
+    return t.data_ptr()
+
+
+def _pools8(k_pages, v_pages, k_scales, v_scales, d, device):
+    """(pointers of the exponent bytes) of an 8-bit cache."""
+    if k_scales is None or v_scales is None:
+        _refuse("k_scales and v_scales: both or neither")
+    shape = k_pages.shape
+    for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
+        _bytes8(name, t, shape[:3] + (d,), torch.float8_e4m3fn, device)
+    return tuple(_bytes8(name, t, shape[:3], torch.float8_e8m0fnu, device)
+                 for name, t in (("k_scales", k_scales), ("v_scales", v_scales)))
+
+
+def fa_norm_rope_append(q, k, v, q_out, k_pages, v_pages, block_table, ctx_lens, cu_seqlens, freqs,
+                        k_scales=None, v_scales=None, positions=None, q_weight=None, k_weight=None,
+                        norm=FA_NORM_NONE, eps=1e-6, pair_axis=None, style=FA_ROPE_HALF,
+                        amplitude=1.0, stream=None):
+    """fa_rope_append with a norm of q and k (as fa_norm_rope), positions int32 [axes, T] for the
+    angles (None: the tokens' places) and, where k_scales and v_scales [num_pages, Hkv, page_size]
+    (float8_e8m0fnu or uint8) are given, into an 8-bit cache (pools of float8_e4m3fn or uint8)."""
+    device = _packed_device(q)
+    T, H, d = _dims("q", q, 3)
+    P, Hkv, page, _ = _dims("k_pages", k_pages, 4)
+    B, width = _dims("block_table", block_table, 2)
+    ks = vs = 0
+    if k_scales is None and v_scales is None:
+        _pools(k_pages, v_pages, d, q.dtype, device)
+    else:
+        ks, vs = _pools8(k_pages, v_pages, k_scales, v_scales, d, device)
+    at, pairs, axes = _axes(positions, pair_axis, freqs, T, device)
+    wq, wk, code = _weights(q_weight, k_weight, d, q.dtype, device)
+    p = _pack_norm_append(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(), k_pages.data_ptr(),
+        v_pages.data_ptr(), ks, vs, _ints("block_table", block_table, (B, width), device),
+        _ints("ctx_lens", ctx_lens, (B,), device),
+        _ints("cu_seqlens", cu_seqlens, (B + 1,), device), at, pairs, _freqs_ptr(freqs, device),
+        wq, wk, _rows("q", q, T, H, d, q.dtype, device), _rows("k", k, T, Hkv, d, q.dtype, device),
+        _rows("v", v, T, Hkv, d, q.dtype, device),
+        _rows("q_out", q_out, T, H, d, q.dtype, device), T, B, H, Hkv, d, 2 * freqs.numel(), axes,
+        page, width, P, style, float(amplitude), norm, float(eps), code, _dtype_code(q))
+    _check(lib().fa_norm_rope_append(p, _stream(stream)))
+
+
+def fa_kv_read(k_pages, v_pages, k_scales, v_scales, block_table, starts, cu_seqlens, k, v,
+               stream=None):
+    """Rows of an 8-bit cache back in 16 bits: k, v [T, Hkv, d] float16 or bfloat16, whose rows
+    cu_seqlens[b] .. cu_seqlens[b+1]-1 are sequence b's positions from starts[b] (int32 [B]) on."""
+    device = _packed_device(k)
+    T, Hkv, d = _dims("k", k, 3)
+    P, heads, page, _ = _dims("k_pages", k_pages, 4)
+    B, width = _dims("block_table", block_table, 2)
+    if heads != Hkv:
+        _refuse(f"k has {Hkv} heads, the pools {heads}")
+    ks, vs = _pools8(k_pages, v_pages, k_scales, v_scales, d, device)
+    p = _pack_kv_read(
+        k_pages.data_ptr(), v_pages.data_ptr(), ks, vs,
+        _ints("block_table", block_table, (B, width), device), _ints("starts", starts, (B,), device),
+        _ints("cu_seqlens", cu_seqlens, (B + 1,), device), k.data_ptr(), v.data_ptr(),
+        _rows("k", k, T, Hkv, d, k.dtype, device), _rows("v", v, T, Hkv, d, k.dtype, device), T, B,
+        Hkv, d, page, width, P, _dtype_code(k))
+    _check(lib().fa_kv_read(p, _stream(stream)))
+
+
+def fa_fwd_paged_varlen_ex(q, k_pages, v_pages, block_table, ctx_lens, cu_seqlens_q, max_q, o, lse,
+                           scale, workspace, k_scales=None, v_scales=None, tree=None,
+                           mask_mode=FA_MASK_CAUSAL, window=0, n_global=0, stream=None):
+    """fa_fwd_paged_varlen over an 8-bit cache (k_scales and v_scales given) and for trees of
+    drafted tokens: tree int32 [Tq, words], bit j % 32 of word j // 32 of a query's row set where it
+    sees token j of its own chunk (mask_mode is then FA_MASK_TREE whatever is passed)."""
+    device = _packed_device(q)
+    Tq, H, d = _dims("q", q, 3)
+    P, Hkv, page, _ = _dims("k_pages", k_pages, 4)
+    B, width = _dims("block_table", block_table, 2)
+    ks = vs = bits = words = 0
+    if k_scales is None and v_scales is None:
+        _pools(k_pages, v_pages, d, q.dtype, device)
+    else:
+        ks, vs = _pools8(k_pages, v_pages, k_scales, v_scales, d, device)
+    if tree is not None:
+        words = _dims("tree", tree, 2)[1]
+        bits = _ints("tree", tree, (Tq, words), device)
+        mask_mode, window, n_global = FA_MASK_TREE, 0, 0
+    ws, ws_bytes = _bytes_of(workspace, device)
+    p = _pack_paged(
+        q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
+        _ints("block_table", block_table, (B, width), device),
+        _ints("ctx_lens", ctx_lens, (B,), device),
+        _ints("cu_seqlens_q", cu_seqlens_q, (B + 1,), device), o.data_ptr(),
+        _lse_ptr(lse, Tq, H, device), _rows("q", q, Tq, H, d, q.dtype, device),
+        _rows("o", o, Tq, H, d, q.dtype, device), B, H, Hkv, d, Tq, max_q, page, width, P,
+        float(scale), mask_mode, window, n_global, _dtype_code(q), ws, ws_bytes, 0)
+    _check(lib().fa_fwd_paged_varlen_ex(p, _pack_extra(ks, vs, bits, words), _stream(stream)))

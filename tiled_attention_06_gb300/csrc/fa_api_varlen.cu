@@ -49,6 +49,27 @@ fa_status make_map3(CUtensorMap* m, const void* ptr, bool bf16, int d, long long
   return FA_OK;
 }
 
+// Rows of d bytes of an 8-bit cache, (d, page_size, planes): boxes of whole rows, swizzled over
+// them.
+fa_status make_map8(CUtensorMap* m, const void* ptr, int d, int page_size, long long planes,
+                    int box) {
+  auto enc = encode_fn();
+  if (!enc) return fail(FA_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(page_size),
+                              static_cast<cuuint64_t>(planes)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(d),
+                                 static_cast<cuuint64_t>(d) * page_size};
+  const cuuint32_t boxes[3] = {static_cast<cuuint32_t>(d), static_cast<cuuint32_t>(box), 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r =
+      enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(ptr), dims, strides, boxes, estr,
+          CU_TENSOR_MAP_INTERLEAVE_NONE,
+          d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(FA_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+  return FA_OK;
+}
+
 // What every attention call here has in common.
 struct Common {
   int B, H, Hkv, d, total_q;
@@ -478,13 +499,24 @@ size_t fa_paged_varlen_workspace_size(int B, int H, int Hkv, int total_q, int ma
                                   : var_layout(B, H, Hkv, total_q, d).total;
 }
 
-fa_status fa_fwd_paged_varlen(const fa_paged_varlen_params* params, fa_stream_t stream) {
-  if (!params) return fail(FA_ERR_INVALID_ARG, "params is null");
-  const fa_paged_varlen_params& a = *params;
+// Both paged calls; x: all zeros for the plain one.
+static fa_status paged_varlen(const fa_paged_varlen_params& a, const fa_paged_varlen_extra& x,
+                              fa_stream_t stream) {
   const Common c{a.B,         a.H,      a.Hkv,      a.d,    a.total_q, a.scale,
                  a.mask_mode, a.window, a.n_global, a.dtype};
-  fa_status st = check_common(c);
+  Common checked = c;
+  const bool tree = c.mask_mode == FA_MASK_TREE, q8 = x.k_scales != nullptr;
+  if (tree) checked.mask_mode = FA_MASK_NONE;
+  if (tree != (x.tree != nullptr))
+    return fail(FA_ERR_INVALID_ARG, "mask_mode %d: a tree goes with FA_MASK_TREE", c.mask_mode);
+  fa_status st = check_common(checked);
   if (st != FA_OK) return st;
+  if (tree && (x.tree_words < 1 || x.tree_words > (1 << 26) || 32LL * x.tree_words < a.max_q ||
+               !aligned4(x.tree)))
+    return fail(FA_ERR_INVALID_ARG,
+                "tree: 4-byte aligned, with 32 * tree_words at least max_q = %d", a.max_q);
+  if (q8 != (x.v_scales != nullptr) || !aligned16(x.k_scales) || !aligned16(x.v_scales))
+    return fail(FA_ERR_INVALID_ARG, "k_scales and v_scales: both or neither, 16-byte aligned");
   if (a.max_pages_per_seq < 1 || a.num_pages < 1 || a.max_q < 0)
     return fail(FA_ERR_INVALID_ARG, "need max_pages_per_seq, num_pages >= 1 and max_q >= 0");
   if (a.page_size < 16 || a.page_size > 4096 || a.page_size % 16 != 0)
@@ -543,13 +575,21 @@ fa_status fa_fwd_paged_varlen(const fa_paged_varlen_params* params, fa_stream_t 
     p.box = std::min(64, pow2);
     p.heads = static_cast<fa::FewHead*>(a.workspace);
     p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + fa::kFewHeadBytes);
+    p.k_scales = x.k_scales;
+    p.v_scales = x.v_scales;
+    p.tree = x.tree;
+    p.tree_words = x.tree_words;
     F.sms = dev.sms;
-    if ((st = make_map3(&F.tmK, a.k_pages, bf16, a.d, a.page_size, a.d, planes, plane, p.box,
-                        1)) != FA_OK)
+    if (q8) {
+      if ((st = make_map8(&F.tmK, a.k_pages, a.d, a.page_size, planes, p.box)) != FA_OK ||
+          (st = make_map8(&F.tmV, a.v_pages, a.d, a.page_size, planes, p.box)) != FA_OK)
+        return st;
+    } else if ((st = make_map3(&F.tmK, a.k_pages, bf16, a.d, a.page_size, a.d, planes, plane,
+                               p.box, 1)) != FA_OK ||
+               (st = make_map3(&F.tmV, a.v_pages, bf16, a.d, a.page_size, a.d, planes, plane,
+                               p.box, 1)) != FA_OK) {
       return st;
-    if ((st = make_map3(&F.tmV, a.v_pages, bf16, a.d, a.page_size, a.d, planes, plane, p.box,
-                        1)) != FA_OK)
-      return st;
+    }
     const cudaError_t e = fa::launch_few(F, a.d, bf16, cs);
     if (e != cudaSuccess) return cuda_fail(e, "paged packed attention launch");
     return FA_OK;
@@ -564,21 +604,38 @@ fa_status fa_fwd_paged_varlen(const fa_paged_varlen_params* params, fa_stream_t 
   L.p.max_pages = a.max_pages_per_seq;
   L.p.num_pages = a.num_pages;
   L.p.box = std::min(fa::kVarBN, pow2);
+  L.p.k_pages = a.k_pages;
+  L.p.v_pages = a.v_pages;
+  L.p.k_scales = x.k_scales;
+  L.p.v_scales = x.v_scales;
+  L.p.tree = x.tree;
+  L.p.tree_words = x.tree_words;
   L.sms = dev.sms;
   if ((st = make_map3(&L.tmQ, a.q, bf16, a.d, a.H, a.d, a.total_q, a.q_token, L.p.G, L.p.TPT)) !=
           FA_OK ||
       (st = make_map3(&L.tmO, a.o, bf16, a.d, a.H, a.d, a.total_q, a.o_token, L.p.G, L.p.TPT)) !=
           FA_OK)
     return st;
-  if ((st = make_map3(&L.tmK, a.k_pages, bf16, a.d, a.page_size, a.d, planes, plane, L.p.box,
-                      1)) != FA_OK)
-    return st;
-  if ((st = make_map3(&L.tmV, a.v_pages, bf16, a.d, a.page_size, a.d, planes, plane, L.p.box,
-                      1)) != FA_OK)
+  // (the tiles of an 8-bit cache are loaded as they lie there, without a map)
+  if (!q8 && ((st = make_map3(&L.tmK, a.k_pages, bf16, a.d, a.page_size, a.d, planes, plane,
+                              L.p.box, 1)) != FA_OK ||
+              (st = make_map3(&L.tmV, a.v_pages, bf16, a.d, a.page_size, a.d, planes, plane,
+                              L.p.box, 1)) != FA_OK))
     return st;
   const cudaError_t e = fa::launch_varlen(L, a.d, bf16, cs);
   if (e != cudaSuccess) return cuda_fail(e, "paged packed attention launch");
   return FA_OK;
+}
+
+fa_status fa_fwd_paged_varlen(const fa_paged_varlen_params* params, fa_stream_t stream) {
+  if (!params) return fail(FA_ERR_INVALID_ARG, "params is null");
+  return paged_varlen(*params, fa_paged_varlen_extra{nullptr, nullptr, nullptr, 0}, stream);
+}
+
+fa_status fa_fwd_paged_varlen_ex(const fa_paged_varlen_params* params,
+                                 const fa_paged_varlen_extra* extra, fa_stream_t stream) {
+  if (!params || !extra) return fail(FA_ERR_INVALID_ARG, "params or extra is null");
+  return paged_varlen(*params, *extra, stream);
 }
 
 size_t fa_bwd_varlen_workspace_size(int B, int H, int Hkv, int total_q, int total_k, int d) {

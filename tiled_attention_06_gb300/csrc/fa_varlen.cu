@@ -59,9 +59,17 @@ constexpr int kThreads = 384;
 constexpr int kTmaWarp = 8;
 constexpr int kMmaWarp = 9;
 constexpr int kStoreWarp = 10;  // and 11: outputs of tiles A and B
+constexpr int kConvertWarp = 12;  // and 13 to 15, with an 8-bit cache alone
 // launched at 168 registers per thread: 128 x (200 + 200 + 104) = 384 x 168
 constexpr uint32_t kRegsSoftmax = 200;
 constexpr uint32_t kRegsProducer = 104;
+// with four warps more at 128: 128 x (184 + 184 + 72 + 72) = 512 x 128
+constexpr uint32_t kRegsSoftmax8 = 184;
+constexpr uint32_t kRegsProducer8 = 72;
+
+// Forms of the forward kernel. Trees take their masks from the caller (FA_MASK_TREE), which the
+// other two forms tell apart at run time; the plain one carries nothing of them.
+enum : int { kPlain = 0, kTree = 1, kCache8 = 2 };
 
 // Wait that ignores the abort flag (used while winding down).
 __device__ __forceinline__ void mbar_wait_quiet(uint32_t bar, uint32_t parity, const WaitCtx& wc) {
@@ -90,7 +98,7 @@ __device__ __forceinline__ void bulk_commit_and_wait_read() {
 // Key blocks seen by queries at key positions [lo, hi) of a sequence with sk keys.
 __device__ __forceinline__ Range blocks_seen(int lo, int hi, int sk, const PrefillParams& m) {
   PrefillParams f;
-  f.mask_mode = m.mask_mode;
+  f.mask_mode = m.mask_mode == FA_MASK_TREE ? FA_MASK_NONE : m.mask_mode;
   f.window = m.window;
   f.n_global = m.n_global;
   f.Sq = sk;  // positions instead of query indices
@@ -103,10 +111,13 @@ __device__ __forceinline__ int block_at(const VarUnit& u, int j) {
 }
 
 // Every query at positions [lo, hi] sees every key of the block at n0 (and all are in range).
-__device__ __forceinline__ bool block_full(int lo, int hi, int n0, int sk,
+// `start`: position of the chunk's first token (FA_MASK_TREE).
+template <int FORM>
+__device__ __forceinline__ bool block_full(int lo, int hi, int n0, int sk, int start,
                                            const PrefillParams& m) {
   const int n1 = n0 + BN;
   if (n1 > sk) return false;
+  if (FORM != kPlain && m.mask_mode == FA_MASK_TREE) return n1 <= start;
   switch (m.mask_mode) {
     case FA_MASK_NONE:
       return true;
@@ -151,6 +162,27 @@ __device__ __forceinline__ void mask_row(uint32_t* s, int n0, int pos, int sk,
     const uint32_t from = a <= 0 ? 0xffffffffu : (a >= 32 ? 0u : ~((1u << a) - 1u));
     const uint32_t below = g <= 0 ? 0u : (g >= 32 ? 0xffffffffu : (1u << g) - 1u);
     const uint32_t mk = upto & (from | below);
+#pragma unroll
+    for (int c = 0; c < 32; ++c)
+      if (!((mk >> c) & 1u)) s[32 * k + c] = __float_as_uint(-INFINITY);
+  }
+}
+
+// A query's row of a tree's bits: bit j of `words` words, token j of its chunk, which starts at
+// position `start`.
+struct TreeRow {
+  const uint32_t* row;
+  int words, start;
+};
+// The same for a tree.
+__device__ __forceinline__ void mask_tree_row(uint32_t* s, int n0, int sk, const TreeRow& t) {
+#pragma unroll
+  for (int k = 0; k < BN / 32; ++k) {
+    const int idx = n0 + 32 * k - t.start, w = idx >> 5, left = sk - n0 - 32 * k;
+    const uint32_t a = w < 0 ? ~0u : w < t.words ? t.row[w] : 0u;
+    const uint32_t b = w < -1 ? ~0u : w + 1 < t.words ? t.row[w + 1] : 0u;
+    uint32_t mk = __funnelshift_r(a, b, idx & 31);
+    mk &= left <= 0 ? 0u : left >= 32 ? ~0u : (1u << left) - 1u;
 #pragma unroll
     for (int c = 0; c < 32; ++c)
       if (!((mk >> c) & 1u)) s[32 * k + c] = __float_as_uint(-INFINITY);
@@ -212,6 +244,7 @@ __device__ __forceinline__ void for_each_block(const VarParams& p, PlanSmem& s, 
         u.a_end = rg.a_end;
         u.b_start = rg.b_start;
         u.slot = -1;
+        u.start = q.sk - q.sq;
         f(u);
       });
 }
@@ -316,7 +349,7 @@ __global__ void __launch_bounds__(kPlanThreads) var_plan_kernel(const VarParams 
         VarUnit u;
         u.q0 = from(mine.q0), u.nq = from(mine.nq), u.sk = from(mine.sk), u.k0 = from(mine.k0);
         u.qpos = from(mine.qpos), u.seq = from(mine.seq);
-        u.a_end = from(mine.a_end), u.b_start = from(mine.b_start);
+        u.a_end = from(mine.a_end), u.b_start = from(mine.b_start), u.start = from(mine.start);
         const int n = from(mine.j1), ns = (n + split - 1) / split;
         int slot = 0;
         if (pass == kWrite && lane == 0) {
@@ -348,15 +381,24 @@ __global__ void __launch_bounds__(kPlanThreads) var_plan_kernel(const VarParams 
 
 // ------------------------------------------------------------------ forward
 
-template <int D>
+template <int D, int FORM>
 struct Cfg {
+  static constexpr bool Q8 = FORM == kCache8;
+  static constexpr int THREADS = Q8 ? 512 : kThreads;
   static constexpr int KCH = D / 64;
   static constexpr int Q_BYTES = kTile * D * 2;  // one tile
   static constexpr int TILE_BYTES = BN * D * 2;
   static constexpr int BAR_BYTES = 1024;
-  static constexpr int FIT = (int)((kSmemLimit - 1024 - BAR_BYTES - 2 * Q_BYTES) / TILE_BYTES);
+  // an 8-bit cache: tiles as they lie there, rows of D bytes and 128 exponent bytes behind them
+  static constexpr int RAW_BYTES = BN * D + BN;
+  static constexpr int NRAW = Q8 ? 4 : 0;
+  static constexpr int FIT = (int)((kSmemLimit - 1024 - BAR_BYTES - 2 * Q_BYTES - NRAW * RAW_BYTES) /
+                                   TILE_BYTES);
   static constexpr int NSLOT = FIT > 8 ? 8 : FIT;
-  static constexpr int SMEM = 1024 + 2 * Q_BYTES + NSLOT * TILE_BYTES + BAR_BYTES;
+  static constexpr int RAW_AT = 2 * Q_BYTES + NSLOT * TILE_BYTES;
+  static constexpr int BARS_AT = RAW_AT + NRAW * RAW_BYTES;
+  static constexpr int SMEM = 1024 + BARS_AT + BAR_BYTES;
+  static_assert(NSLOT >= 3, "too few tiles");
   static constexpr int TMEM_COLS = 512;  // S_A S_B [0, 256), O_A O_B [256, 256 + 2 D)
   static_assert(2 * BN + 2 * D <= 512, "TMEM over budget");
 };
@@ -369,9 +411,11 @@ struct Bars {
   uint64_t pv_step;      // every P V of an item with one tile
   uint64_t o_staged[2];  // the tile's output is in shared memory
   uint64_t final_mma;
+  uint64_t raw_full[4], raw_empty[4];  // tiles of an 8-bit cache
   uint32_t tmem_base;
   uint32_t abort;
 };
+static_assert(sizeof(Bars) <= 1024, "barrier block over its reserve");
 
 // A work item: its unit, K/V head, and tiles (1 when the second has no token).
 struct Item {
@@ -418,7 +462,7 @@ struct Items {
     if (t >= total) return false;
     it.u.q0 = a.x, it.u.nq = a.y, it.u.sk = a.z, it.u.k0 = a.w;
     it.u.qpos = b.x, it.u.seq = b.y, it.u.j0 = b.z, it.u.j1 = b.w;
-    it.u.slot = c.x, it.u.a_end = c.y, it.u.b_start = c.z;
+    it.u.slot = c.x, it.u.a_end = c.y, it.u.b_start = c.z, it.u.start = c.w;
     it.kvh = t % p.Hkv;
     it.tiles = it.u.nq > p.TPT ? 2 : 1;
     if (AHEAD) fetch(p);
@@ -431,16 +475,21 @@ struct Items {
 // bits over S, l += the unrounded sum. P of at most 2^8 and l in FP32 keep the rounding of P
 // the only one on the way.
 // `before_rescale` makes O safe to touch, false on abort.
-template <int D, bool BF16, typename PreRescale>
+template <int D, bool BF16, int FORM, typename PreRescale>
 __device__ __forceinline__ bool softmax_row(uint32_t t_lane, uint32_t s_col, uint32_t o_col,
                                             bool full, int n0, int pos, int sk,
-                                            const PrefillParams& m, float& m_ref, float& l,
-                                            PreRescale before_rescale) {
+                                            const PrefillParams& m, const TreeRow& tree,
+                                            float& m_ref, float& l, PreRescale before_rescale) {
   uint32_t s[BN];
   tmem_ld64(t_lane + s_col, s);
   tmem_ld64(t_lane + s_col + 64, s + 64);
   tmem_ld_wait<BN>(s);
-  if (!full) mask_row(s, n0, pos, sk, m);
+  if (!full) {
+    if (FORM != kPlain && m.mask_mode == FA_MASK_TREE)
+      mask_tree_row(s, n0, sk, tree);
+    else
+      mask_row(s, n0, pos, sk, m);
+  }
   float mx[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
@@ -492,25 +541,88 @@ __device__ __forceinline__ bool softmax_row(uint32_t t_lane, uint32_t s_col, uin
   return true;
 }
 
-template <int D, bool BF16, bool PAGED>
-__global__ void __launch_bounds__(kThreads, 1)
+// ------------------------------------------------------------------ tiles of an 8-bit cache
+
+// Two elements of a row, times its power of two, in the call's type. The FP32 products are exact;
+// so is the rounding, but for what FP16 does not hold (16-bit products of FP16 pairs round alike, and
+// serve where the power itself is an FP16 number).
+template <bool BF16>
+__device__ __forceinline__ uint32_t widen8(uint32_t x, float power, uint32_t power2, bool half) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(x)));
+  if (!BF16 && half) {
+    asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(h) : "r"(power2));
+    return h;
+  }
+  const float2 f = __half22float2(*reinterpret_cast<__half2*>(&h));
+  return BF16 ? cvt_pack_bf16(f.x * power, f.y * power) : cvt_pack_f16(f.x * power, f.y * power);
+}
+// One tile by 128 threads: raw rows of D bytes and exponent bytes to the 128-byte swizzle of a
+// 16-bit tile; rows from `live` on become zeros. 16 elements to a thread at a time; the lanes of
+// the second region store their halves in the other order, or they met the first's banks.
+template <int D, bool BF16>
+__device__ __forceinline__ void convert_tile(const uint8_t* raw, uint32_t dst, int live, int t) {
+  constexpr int CPR = D / 16;  // 16-byte chunks of a raw row
+  const int c = t % CPR, flip = c / 4;
+#pragma unroll 4
+  for (int row = t / CPR; row < BN; row += 128 / CPR) {
+    uint4 x = *reinterpret_cast<const uint4*>(raw + row * D + 16 * c);
+    const uint32_t b = raw[BN * D + row];
+    // 2^(b - 127): NaN for 255, 0 for 0 (2^-127); as FP16 where that is one, 2^-14 to 2^15
+    float power = __uint_as_float(b == 255 ? 0x7fffffffu : b << 23);
+    const bool half = b >= 113 && b <= 142;
+    uint32_t power2 = (b - 112) * 0x04000400u;
+    if (row >= live) x = make_uint4(0, 0, 0, 0), power = 0.f;
+    const uint32_t in[4] = {x.x, x.y, x.z, x.w};
+    uint32_t out[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      out[i] = widen8<BF16>(in[i / 2] >> (16 * (i % 2)), power, power2, half);
+    const uint32_t at = dst + flip * (BN * 128) + row * 128;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const bool second = (h ^ flip) & 1;
+      const uint32_t chunk = static_cast<uint32_t>(((2 * c) % 8 + (second ? 1 : 0)) ^ (row & 7));
+      st_shared_v4(at + (chunk << 4), second ? out[4] : out[0], second ? out[5] : out[1],
+                   second ? out[6] : out[2], second ? out[7] : out[3]);
+    }
+  }
+}
+// `bytes` (a multiple of 16) from global to shared memory, counted on `bar`.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
+                                          uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
+          "r"(dst),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
+
+template <int D, bool BF16, bool PAGED, int FORM>
+__global__ void __launch_bounds__(Cfg<D, FORM>::THREADS, 1)
     var_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                    const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
                    const __grid_constant__ VarParams p) {
-  using C = Cfg<D>;
+  using C = Cfg<D, FORM>;
+  constexpr bool Q8 = C::Q8;
+  static_assert(PAGED || FORM == kPlain, "the other forms are paged");
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* smem = smem_raw + (base - raw);
   const uint32_t sQ = base, sRing = base + 2 * C::Q_BYTES;
-  Bars* bars = reinterpret_cast<Bars*>(smem + 2 * C::Q_BYTES + C::NSLOT * C::TILE_BYTES);
+  Bars* bars = reinterpret_cast<Bars*>(smem + C::BARS_AT);
   auto B = [&](uint64_t& b) { return smem_u32(&b); };
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::NSLOT; ++i) {
-      mbar_init(B(bars->full[i]), 1);
+      mbar_init(B(bars->full[i]), Q8 ? 4 : 1);
       mbar_init(B(bars->empty[i]), 1);
+    }
+    for (int i = 0; i < C::NRAW; ++i) {
+      mbar_init(B(bars->raw_full[i]), 1);
+      mbar_init(B(bars->raw_empty[i]), 4);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(B(bars->q_full[i]), 1);
@@ -534,8 +646,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (warp == kTmaWarp && lane == 0) {
     tma_prefetch_desc(&tmQ);
-    tma_prefetch_desc(&tmK);
-    tma_prefetch_desc(&tmV);
+    if (!Q8) {
+      tma_prefetch_desc(&tmK);
+      tma_prefetch_desc(&tmV);
+    }
     tma_prefetch_desc(&tmO);
   }
   tc_fence_before();
@@ -547,8 +661,35 @@ __global__ void __launch_bounds__(kThreads, 1)
   // The role branches never rejoin: each ends with the CTA-wide teardown barrier, so no code
   // runs under two register budgets.
   if (warp >= 8) {
-    regs_decrease<kRegsProducer>();
-    if (warp == kTmaWarp) {
+    regs_decrease<Q8 ? kRegsProducer8 : kRegsProducer>();
+    if (Q8 && warp >= kConvertWarp) {
+      // -------------------------------------------------------------- 8 to 16 bits
+      uint32_t pos = 0;
+      bool ok = true;
+      Item it;
+      for (Items<false> items(p, total); ok && items.next(p, it);) {
+        for (int j = it.u.j0; j < it.u.j1 && ok; ++j) {
+          const int live = it.u.sk - block_at(it.u, j) * BN;
+          for (int kv = 0; kv < 2; ++kv, ++pos) {
+            const int raw = pos % 4, slot = pos % C::NSLOT;
+            ok = mbar_wait(B(bars->raw_full[raw]), (pos / 4) & 1, wc) &&
+                 mbar_wait(B(bars->empty[slot]), ((pos / C::NSLOT) & 1) ^ 1, wc);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            convert_tile<D, BF16>(smem + C::RAW_AT + raw * C::RAW_BYTES,
+                                  sRing + slot * C::TILE_BYTES, live,
+                                  threadIdx.x - kConvertWarp * 32);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(B(bars->full[slot]));
+              mbar_arrive(B(bars->raw_empty[raw]));
+            }
+          }
+        }
+      }
+      __syncwarp();
+    } else if (warp == kTmaWarp) {
       // -------------------------------------------------------------- TMA producer
       const bool leader = elect_one();
       uint32_t pos = 0, iq[2] = {0, 0};
@@ -589,9 +730,30 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           for (int kv = 0; kv < 2; ++kv) {  // K, then V
-            const int slot = pos % C::NSLOT;
-            const uint32_t use = pos / C::NSLOT;
-            if (!(ok = mbar_wait(B(bars->empty[slot]), (use & 1) ^ 1, wc))) break;
+            constexpr int NS = Q8 ? C::NRAW : C::NSLOT;
+            const int slot = pos % NS;
+            const uint32_t use = pos / NS;
+            if (!(ok = mbar_wait(B(Q8 ? bars->raw_empty[slot % 4] : bars->empty[slot]),
+                                 (use & 1) ^ 1, wc)))
+              break;
+            if constexpr (Q8) {  // a box's rows are neighbours in the pool
+              const uint32_t raw = base + C::RAW_AT + slot * C::RAW_BYTES;
+              const uint32_t bar = B(bars->raw_full[slot % 4]);
+              if (leader) mbar_arrive_expect_tx(bar, boxes * p.box * (D + 1));
+              __syncwarp();
+              if (lane < boxes) {
+                const int64_t row = static_cast<int64_t>(z) * p.page_size + y;
+                bulk_load(raw + lane * p.box * D,
+                          static_cast<const uint8_t*>(kv ? p.v_pages : p.k_pages) + row * D,
+                          p.box * D, bar);
+                bulk_load(raw + BN * D + lane * p.box, (kv ? p.v_scales : p.k_scales) + row, p.box,
+                          bar);
+              }
+              __syncwarp();
+              fills[slot] = use + 1;
+              ++pos;
+              continue;
+            }
             const uint32_t dst = sRing + slot * C::TILE_BYTES;
             const void* map = kv ? (const void*)&tmV : (const void*)&tmK;
             if constexpr (PAGED) {
@@ -615,8 +777,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (!ok) {  // wind down: every load issued lands before the CTA exits
-        for (int s = 0; s < C::NSLOT; ++s)
-          if (fills[s] > 0) mbar_wait_quiet(B(bars->full[s]), (fills[s] - 1) & 1, wc);
+        for (int s = 0; s < (Q8 ? C::NRAW : C::NSLOT); ++s)
+          if (fills[s] > 0)
+            mbar_wait_quiet(B(Q8 ? bars->raw_full[s % 4] : bars->full[s]), (fills[s] - 1) & 1, wc);
         for (int q = 0; q < 2; ++q)
           if (iq[q] > 0) mbar_wait_quiet(B(bars->q_full[q]), (iq[q] - 1) & 1, wc);
       }
@@ -636,7 +799,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // zero the rows of V behind the last key of the j-th visited block
       auto clean = [&](const VarUnit& u, int j, int vslot) {
         const int live = u.sk - block_at(u, u.j0 + j) * BN;  // rows below sk
-        if (live >= BN) return;
+        if (Q8 || live >= BN) return;  // (the conversion has written zeros)
         uint8_t* v = smem + 2 * C::Q_BYTES + vslot * C::TILE_BYTES;
         for (int c = 0; c < C::KCH; ++c) {
           uint4* r = reinterpret_cast<uint4*>(v + c * (BN * 128));
@@ -773,7 +936,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();  // teardown: every role is done with TMEM and shared memory
     return;
   }
-  regs_increase<kRegsSoftmax>();
+  regs_increase<Q8 ? kRegsSoftmax8 : kRegsSoftmax>();
   // ---------------------------------------------------------------- softmax, tiles A / B
   const int q = warp / 4;
   const int row = (warp % 4) * 32 + lane;
@@ -804,6 +967,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       continue;
     }
     const int p_lo = it.u.qpos + q * p.TPT, p_hi = p_lo + toks - 1, pos_q = p_lo + tok;
+    TreeRow tree{nullptr, 0, 0};
+    if (FORM != kPlain)  // a row without a token reads the last token's bits
+      tree = TreeRow{p.tree + static_cast<size_t>(it.u.q0 + q * p.TPT + min(tok, toks - 1)) * p.tree_words,
+                     p.tree_words, it.u.start};
     float m_ref = -INFINITY, l = 0.f;
     for (int j = it.u.j0; j < it.u.j1; ++j) {
       const int n0 = block_at(it.u, j) * BN;
@@ -816,9 +983,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       // With two tiles S(j) was issued after PV(j-1), so O needs no wait before a rescale; with
       // one it was issued before.
       if (work)
-        ok = softmax_row<D, BF16>(
-            t_lane, odd || q ? BN : 0, o_col, block_full(p_lo, p_hi, n0, it.u.sk, p.m), n0, pos_q,
-            it.u.sk, p.m, m_ref, l, [&] {
+        ok = softmax_row<D, BF16, FORM>(
+            t_lane, odd || q ? BN : 0, o_col,
+            block_full<FORM>(p_lo, p_hi, n0, it.u.sk, it.u.start, p.m), n0, pos_q, it.u.sk, p.m, tree,
+            m_ref, l, [&] {
               if (it.tiles == 2 || j == it.u.j0) return true;
               const bool done = mbar_wait(B(bars->pv_step), (steps + (j - it.u.j0) - 1) & 1, wc);
               tc_fence_after();
@@ -1000,20 +1168,28 @@ __global__ void __launch_bounds__(kMergeThreads) var_merge_kernel(const VarParam
   }
 }
 
+template <int D, bool BF16, bool PAGED, int FORM>
+cudaError_t launch_fwd(const VarLaunch& L, int grid, cudaStream_t stream) {
+  using C = Cfg<D, FORM>;
+  const cudaError_t e = prepare_kernel<var_fwd_kernel<D, BF16, PAGED, FORM>>(C::SMEM);
+  if (e != cudaSuccess) return e;
+  var_fwd_kernel<D, BF16, PAGED, FORM>
+      <<<grid, C::THREADS, C::SMEM, stream>>>(L.tmQ, L.tmK, L.tmV, L.tmO, L.p);
+  return cudaGetLastError();
+}
+
 template <int D, bool BF16>
 cudaError_t launch_t(const VarLaunch& L, cudaStream_t stream) {
   var_plan_kernel<<<1, kPlanThreads, 0, stream>>>(L.p, L.sms);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  auto* k = L.p.block_table ? var_fwd_kernel<D, BF16, true> : var_fwd_kernel<D, BF16, false>;
-  constexpr int smem = Cfg<D>::SMEM;
-  e = L.p.block_table ? prepare_kernel<var_fwd_kernel<D, BF16, true>>(smem)
-                      : prepare_kernel<var_fwd_kernel<D, BF16, false>>(smem);
-  if (e != cudaSuccess) return e;
   const int64_t items = static_cast<int64_t>(L.p.max_units) * L.p.Hkv;
   const int grid = static_cast<int>(items < L.sms ? items : L.sms);
-  k<<<grid, kThreads, smem, stream>>>(L.tmQ, L.tmK, L.tmV, L.tmO, L.p);
-  if ((e = cudaGetLastError()) != cudaSuccess || !L.p.part) return e;
+  e = !L.p.block_table                       ? launch_fwd<D, BF16, false, kPlain>(L, grid, stream)
+      : L.p.k_scales                         ? launch_fwd<D, BF16, true, kCache8>(L, grid, stream)
+      : L.p.m.mask_mode == FA_MASK_TREE      ? launch_fwd<D, BF16, true, kTree>(L, grid, stream)
+                                             : launch_fwd<D, BF16, true, kPlain>(L, grid, stream);
+  if (e != cudaSuccess || !L.p.part) return e;
   var_merge_kernel<D, BF16><<<L.sms * 2, kMergeThreads, 0, stream>>>(L.p);
   return cudaGetLastError();
 }

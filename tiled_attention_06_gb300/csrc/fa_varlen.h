@@ -57,6 +57,66 @@ cudaError_t launch_rope(const RopeParams& p, int dtype, bool half_style, bool ve
 cudaError_t launch_rope_append(const RopeParams& p, int dtype, bool half_style, bool vec, int sms,
                                cudaStream_t stream);
 
+// Norms of query and key heads with rotary positions (fa_norm_rope.cu). Token and head steps are
+// in elements. Rows of a token: H of q, Hkv of k and, when appending, Hkv of v.
+struct NormRopeParams {
+  const void* q;
+  const void* k;
+  const void* v;  // appending
+  void* q_out;    // the gradient writes dq and dk here
+  void* k_out;
+  int64_t q_token, q_head, k_token, k_head, v_token;
+  int64_t q_out_token, q_out_head, k_out_token, k_out_head;
+  const double* freqs;       // [rot/2] radians per position
+  const int32_t* pos;        // [axes][T]; appending: nullptr for the tokens' places
+  const int32_t* pair_axis;  // [rot/2], or nullptr: axis 0
+  const void* q_weight;      // [d] of the dtype, or of FP32 where w_f32; nullptr: ones
+  const void* k_weight;
+  int64_t T;
+  int H, Hkv, d, rot, axes, norm, inverse, w_f32;
+  float amplitude, eps;
+  // appending
+  void* k_pages;
+  void* v_pages;
+  uint8_t* k_scales;  // exponent bytes [num_pages, Hkv, page_size]; nullptr: 16-bit pools
+  uint8_t* v_scales;
+  const int32_t* cu;           // [B+1]
+  const int32_t* ctx;          // [B] tokens cached before the chunk
+  const int32_t* block_table;  // [B, max_pages]
+  int B, page_size, max_pages, num_pages;
+  // gradient
+  const void* dyq;
+  const void* dyk;
+  int64_t dyq_token, dyq_head, dyk_token, dyk_head;
+  float* part;  // [CTAs][2][d] sums of the weights' gradients, or nullptr
+  float* dq_weight;
+  float* dk_weight;
+  uint32_t* status;
+};
+constexpr int kNormCtas = 320;  // CTAs of the gradient at most
+cudaError_t launch_norm_rope(const NormRopeParams& p, int dtype, bool half_style, bool vec,
+                             int sms, cudaStream_t stream);
+cudaError_t launch_norm_rope_bwd(const NormRopeParams& p, int dtype, bool half_style, bool vec,
+                                 int sms, cudaStream_t stream);
+cudaError_t launch_norm_rope_append(const NormRopeParams& p, int dtype, bool half_style, bool vec,
+                                    int sms, cudaStream_t stream);
+
+// Rows of an 8-bit cache back in 16 bits: tokens [cu[b], cu[b+1]) from position starts[b] on.
+struct KvReadParams {
+  const void* k_pages;  // [num_pages, Hkv, page_size, d]
+  const void* v_pages;
+  const uint8_t* k_scales;
+  const uint8_t* v_scales;
+  const int32_t* block_table;
+  const int32_t* starts;
+  const int32_t* cu;
+  void* k;  // [T, Hkv, d]
+  void* v;
+  int64_t k_token, v_token, T;
+  int B, Hkv, d, page_size, max_pages, num_pages;
+  uint32_t* status;
+};
+cudaError_t launch_kv_read(const KvReadParams& p, bool bf16, int sms, cudaStream_t stream);
 
 // ------------------------------------------------ packed grouped-head attention (fa_varlen.cu)
 //
@@ -76,7 +136,7 @@ struct VarUnit {
   int32_t j0, j1;  // which of the visited key blocks
   int32_t slot;    // -1: writes o and lse; else a partial result, slot * Hkv + kv head
   int32_t a_end, b_start;  // visited blocks: 0 .. a_end - 1, then b_start on
-  int32_t pad;
+  int32_t start;   // key position of the sequence's first token
 };
 // A token block whose key blocks were split: its partial results, slot .. slot + n - 1.
 struct VarGroup {
@@ -102,6 +162,13 @@ struct VarParams {
   const int32_t* ctx;
   const int32_t* block_table;
   int page_size, max_pages, num_pages, box;
+  // an 8-bit cache: pools and exponent bytes; null otherwise
+  const void* k_pages;
+  const void* v_pages;
+  const uint8_t* k_scales;
+  const uint8_t* v_scales;
+  const uint32_t* tree;  // FA_MASK_TREE: [total_q][tree_words]
+  int tree_words;
   // workspace
   VarHeader* hdr;
   VarUnit* units;
@@ -194,6 +261,10 @@ struct FewParams {
   const int32_t* block_table;
   int B, H, Hkv, G, total_q, max_q;
   int page_size, max_pages, num_pages, box;  // box: rows of one TMA box (<= 64)
+  const uint8_t* k_scales;  // exponent bytes of an 8-bit cache [num_pages, Hkv, page_size], or null
+  const uint8_t* v_scales;
+  const uint32_t* tree;  // FA_MASK_TREE: [total_q][tree_words]
+  int tree_words;
   FewHead* heads;  // [CTAs]
   float* part;  // [2 CTAs][16 rows][D], then m [2 CTAs][16], l [2 CTAs][16]
 };
