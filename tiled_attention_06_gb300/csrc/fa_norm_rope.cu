@@ -19,6 +19,7 @@
 // elements to a lane, whose sums meet in log2(LN) shuffles; a group of lanes keeps to one token
 // and takes its heads one after the other, so the sines, cosines and the weight stay in registers,
 // and the next head's load is under way while one is worked on.
+#include <algorithm>
 #include <cstdint>
 
 #include "fa_ptx.cuh"
@@ -27,7 +28,7 @@
 namespace fa {
 namespace {
 
-constexpr int kTokMax = 4;  // tokens of a CTA
+constexpr int kTokMax = 32;  // tokens of a CTA at most
 constexpr uint32_t kAll = 0xffffffffu;
 
 // The exponent byte of a row from the bits of its largest magnitude: bits of an infinity or NaN
@@ -68,31 +69,108 @@ __device__ __forceinline__ void unit_at(int u, int ru, int half, int& oa, int& o
   ob = split ? half + oa : oa + VEC;
 }
 
-// Sines and cosines of the CTA's tokens, [token][e][unit] for pair unit * VEC + e, so that
-// neighbouring lanes read neighbouring words. pos(axis, token) in 64 bits.
-template <int VEC, typename Pos>
-__device__ __forceinline__ void fill_angles(const NormRopeParams& p, int nt, uint64_t* s_freq,
-                                            uint8_t* s_axis, float2* s_cs, bool inverse, Pos pos) {
-  const int half = p.rot / 2, ru = half / VEC;
-  for (int i = threadIdx.x; i < nt * half; i += kRopeThreads) {
-    const int tk = i / half, f = i - tk * half;
-    const int64_t at = pos(s_axis[f], tk);
-    const uint64_t phase = static_cast<uint64_t>(inverse ? -at : at) * s_freq[f];
-    float s, c;  // the phase as a signed fraction of a turn: half turns in [-1, 1]
-    sincospif(static_cast<float>(static_cast<int64_t>(phase)) * 1.08420217248550443e-19f, &s, &c);
-    s_cs[tk * half + (f % VEC) * ru + f / VEC] = make_float2(c * p.amplitude, s * p.amplitude);
+// A CTA's shared memory: sines and cosines of its tokens, the frequencies, the weights of q and k,
+// the pairs' axes. Neighbouring units lie next to each other, 16 bytes of a unit at a time where it
+// has that many, so that neighbouring lanes read neighbouring 16 bytes.
+struct Shared {
+  float2* cs;
+  uint64_t* freq;
+  float* w;
+  uint8_t* axis;
+  __device__ __forceinline__ Shared(float4* base, int tok, int half, int d) {
+    cs = reinterpret_cast<float2*>(base);
+    w = reinterpret_cast<float*>(cs + static_cast<size_t>((tok * half + 1) & ~1));
+    freq = reinterpret_cast<uint64_t*>(w + static_cast<size_t>((2 * d + 3) & ~3));
+    axis = reinterpret_cast<uint8_t*>(freq + half);
   }
+};
+size_t shared_bytes(int tok, int half, int d) {
+  return static_cast<size_t>((tok * half + 1) & ~1) * 8 + static_cast<size_t>((2 * d + 3) & ~3) * 4 +
+         static_cast<size_t>(half) * 9;
 }
-__device__ __forceinline__ void fill_freqs(const NormRopeParams& p, uint64_t* s_freq,
-                                           uint8_t* s_axis) {
-  for (int i = threadIdx.x; i < p.rot / 2; i += kRopeThreads) {
-    s_freq[i] = turns_q64(p.freqs[i]);
+
+__device__ __forceinline__ float weight_at(const void* w, int f32, int dt, int i) {
+  if (!w) return 1.f;
+  if (f32) return static_cast<const float*>(w)[i];
+  const uint16_t x = static_cast<const uint16_t*>(w)[i];
+  return dt == FA_BF16 ? Elem<FA_BF16>::get(x) : Elem<FA_F16>::get(x);
+}
+
+// Frequencies, axes and weights: the part that does not depend on the tokens.
+template <int DT, int VEC, bool HALF>
+__device__ __forceinline__ void fill_fixed(const NormRopeParams& p, const Shared& sh) {
+  const int half = p.rot / 2, ru = half / VEC, U = p.d / (2 * VEC);
+  for (int i = threadIdx.x; i < half; i += kRopeThreads) {
+    sh.freq[i] = turns_q64(p.freqs[i]);
     int a = p.pair_axis ? p.pair_axis[i] : 0;
     if (a < 0 || a >= p.axes) {
       if (blockIdx.x == 0) atomicOr(p.status, FA_DEV_BAD_PAGE);
       a = 0;
     }
-    s_axis[i] = static_cast<uint8_t>(a);
+    sh.axis[i] = static_cast<uint8_t>(a);
+  }
+  if (!p.norm) return;
+  constexpr int W = VEC == 1 ? 2 : 4;  // floats of a unit next to each other
+  for (int i = threadIdx.x; i < 2 * p.d; i += kRopeThreads) {
+    const int kind = i / p.d, j = i - kind * p.d, u = j / (2 * VEC), e = j % (2 * VEC);
+    int oa, ob;
+    unit_at<VEC, HALF>(u, ru, half, oa, ob);
+    const int c = e < VEC ? oa + e : ob + e - VEC;
+    sh.w[kind * p.d + ((e / W) * U + u) * W + e % W] =
+        weight_at(kind ? p.k_weight : p.q_weight, p.w_f32, DT, c);
+  }
+}
+// Sines and cosines of nt tokens; pos(axis, token) in 64 bits.
+template <int VEC, typename Pos>
+__device__ __forceinline__ void fill_angles(const NormRopeParams& p, int nt, const Shared& sh,
+                                            bool inverse, Pos pos) {
+  const int half = p.rot / 2, ru = half / VEC;
+  constexpr int W = VEC == 1 ? 1 : 2;  // pairs of a unit next to each other
+  for (int i = threadIdx.x; i < nt * half; i += kRopeThreads) {
+    const int tk = i / half, f = i - tk * half, u = f / VEC, e = f % VEC;
+    const int64_t at = pos(sh.axis[f], tk);
+    const uint64_t phase = static_cast<uint64_t>(inverse ? -at : at) * sh.freq[f];
+    float s, c;  // the phase as a signed fraction of a turn: half turns in [-1, 1]
+    sincospif(static_cast<float>(static_cast<int64_t>(phase)) * 1.08420217248550443e-19f, &s, &c);
+    sh.cs[tk * half + ((e / W) * ru + u) * W + e % W] =
+        make_float2(c * p.amplitude, s * p.amplitude);
+  }
+}
+
+// The rotation of one unit's pairs.
+template <int VEC, bool HALF>
+__device__ __forceinline__ void turn(float* v, const float2* cs, int ru, int u) {
+  auto pair = [&](int e, float c, float s) {
+    constexpr bool kSplit = HALF || VEC == 1;  // pair e: e of both chunks, or 2e and 2e + 1
+    float& xa = v[kSplit ? e : 2 * e];
+    float& xb = v[kSplit ? VEC + e : 2 * e + 1];
+    const float a = xa, b = xb;
+    xa = a * c - b * s;
+    xb = b * c + a * s;
+  };
+  if constexpr (VEC == 1) {
+    pair(0, cs[u].x, cs[u].y);
+  } else {
+#pragma unroll
+    for (int e = 0; e < VEC; e += 2) {
+      const float4 k = *reinterpret_cast<const float4*>(cs + ((e / 2) * ru + u) * 2);
+      pair(e, k.x, k.y);
+      pair(e + 1, k.z, k.w);
+    }
+  }
+}
+// The weights of one unit.
+template <int VEC>
+__device__ __forceinline__ void unit_weights(const float* w, int U, int u, float* out) {
+  if constexpr (VEC == 1) {
+    out[0] = w[2 * u];
+    out[1] = w[2 * u + 1];
+  } else {
+#pragma unroll
+    for (int e = 0; e < 2 * VEC; e += 4) {
+      const float4 k = *reinterpret_cast<const float4*>(w + ((e / 4) * U + u) * 4);
+      out[e] = k.x, out[e + 1] = k.y, out[e + 2] = k.z, out[e + 3] = k.w;
+    }
   }
 }
 
@@ -102,52 +180,68 @@ struct Part {
   using T = typename Elem<DT>::T;
   using C = Chunk<T, VEC>;
   C a[KU], b[KU];
-};
-// x of the lane's units; elements 0 .. VEC-1 of unit k at v[k][0 ..], its others behind them.
-template <int DT, int VEC, int KU>
-__device__ __forceinline__ void widen(const Part<DT, VEC, KU>& x, float (*v)[2 * VEC]) {
+  __device__ __forceinline__ void clear() {
 #pragma unroll
-  for (int k = 0; k < KU; ++k)
+    for (int k = 0; k < KU; ++k)
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      v[k][e] = Elem<DT>::get(x.a[k].e[e]);
-      v[k][VEC + e] = Elem<DT>::get(x.b[k].e[e]);
-    }
-}
-// The rotation of one unit's pairs by (cos, sin) of cs.
-template <int VEC, bool HALF>
-__device__ __forceinline__ void turn(float* v, const float2* cs) {
-#pragma unroll
-  for (int e = 0; e < VEC; ++e) {
-    constexpr bool kSplit = HALF || VEC == 1;  // pair e: e of both chunks, or 2e and 2e + 1
-    float& xa = v[kSplit ? e : 2 * e];
-    float& xb = v[kSplit ? VEC + e : 2 * e + 1];
-    const float a = xa, b = xb;
-    xa = a * cs[e].x - b * cs[e].y;
-    xb = b * cs[e].x + a * cs[e].y;
+      for (int e = 0; e < VEC; ++e) a[k].e[e] = b[k].e[e] = T(0);
   }
-}
+  __device__ __forceinline__ void load(const void* row, const int* oa, const int* ob, int have) {
+    const T* src = static_cast<const T*>(row);
+#pragma unroll
+    for (int k = 0; k < KU; ++k)
+      if (k < have) {
+        a[k] = *reinterpret_cast<const C*>(src + oa[k]);
+        b[k] = *reinterpret_cast<const C*>(src + ob[k]);
+      }
+  }
+  // elements 0 .. VEC-1 of unit k at v[k][0 ..], its others behind them
+  __device__ __forceinline__ void widen(float (*v)[2 * VEC]) const {
+#pragma unroll
+    for (int k = 0; k < KU; ++k)
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        v[k][e] = Elem<DT>::get(a[k].e[e]);
+        v[k][VEC + e] = Elem<DT>::get(b[k].e[e]);
+      }
+  }
+  static __device__ __forceinline__ void store(void* row, const int* oa, const int* ob, int have,
+                                               const float (*v)[2 * VEC]) {
+    T* dst = static_cast<T*>(row);
+#pragma unroll
+    for (int k = 0; k < KU; ++k) {
+      if (k >= have) continue;
+      C a, b;
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        a.e[e] = Elem<DT>::put(v[k][e]);
+        b.e[e] = Elem<DT>::put(v[k][VEC + e]);
+      }
+      *reinterpret_cast<C*>(dst + oa[k]) = a;
+      *reinterpret_cast<C*>(dst + ob[k]) = b;
+    }
+  }
+};
 __device__ __forceinline__ float sum_lanes(float x, int ln) {
   for (int o = ln / 2; o > 0; o /= 2) x += __shfl_xor_sync(kAll, x, o);
   return x;
 }
-__device__ __forceinline__ float weight_at(const void* w, int f32, int dt, int i) {
-  if (!w) return 1.f;
-  if (f32) return static_cast<const float*>(w)[i];
-  const uint16_t x = static_cast<const uint16_t*>(w)[i];
-  return dt == FA_BF16 ? Elem<FA_BF16>::get(x) : Elem<FA_F16>::get(x);
-}
-template <int DT, int VEC, int KU>
-__device__ __forceinline__ void load_weight(const void* w, int f32, const int* oa, const int* ob,
-                                            int have, float (*v)[2 * VEC]) {
-#pragma unroll
-  for (int k = 0; k < KU; ++k)
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      v[k][e] = k < have ? weight_at(w, f32, DT, oa[k] + e) : 0.f;
-      v[k][VEC + e] = k < have ? weight_at(w, f32, DT, ob[k] + e) : 0.f;
+
+// The walk of a group of lanes over the rows of the CTA's tokens, (token, head) with the heads
+// first: rows g, g + groups, ...
+struct RowWalk {
+  int tk, r, dt, dr, rows;
+  __device__ __forceinline__ RowWalk(int g, int groups, int rows)
+      : tk(g / rows), r(g % rows), dt(groups / rows), dr(groups % rows), rows(rows) {}
+  __device__ __forceinline__ void next() {
+    tk += dt;
+    r += dr;
+    if (r >= rows) {
+      r -= rows;
+      ++tk;
     }
-}
+  }
+};
 
 // Rows r of a token: H of q, Hkv of k and, when appending, Hkv of v. MODE 0: y to q_out and k_out;
 // 1 and 2: q to q_out, k and v to the cache's slot of the token, in 16 and in 8 bits.
@@ -155,50 +249,34 @@ template <int DT, int VEC, int KU, bool HALF, int MODE>
 __global__ void __launch_bounds__(kRopeThreads)
     norm_rope_kernel(const __grid_constant__ NormRopeParams p, int tok, int ln) {
   using T = typename Elem<DT>::T;
-  using C = Chunk<T, VEC>;
-  extern __shared__ float2 s_cs[];
-  __shared__ int64_t s_dst[kTokMax], s_pos[4][kTokMax];
+  extern __shared__ float4 s_dyn[];
+  __shared__ int64_t s_dst[kTokMax], s_pos[FA_MAX_AXES][kTokMax];
   __shared__ int s_seq[kTokMax];
   const int half = p.rot / 2, ru = half / VEC, U = p.d / (2 * VEC);
-  uint64_t* s_freq = reinterpret_cast<uint64_t*>(s_cs + static_cast<size_t>(tok) * half);
-  uint8_t* s_axis = reinterpret_cast<uint8_t*>(s_freq + half);
+  const Shared sh(s_dyn, tok, half, p.d);
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * tok;
   const int nt = static_cast<int>(min(static_cast<int64_t>(tok), p.T - t0));
-  const int groups = kRopeThreads / ln, step = groups / tok;
-  const int g = threadIdx.x / ln, gl = threadIdx.x % ln, tk = g / step;
+  const int groups = kRopeThreads / ln, gl = threadIdx.x % ln;
   const int rows = MODE ? p.H + 2 * p.Hkv : p.H + p.Hkv;
-  const int64_t t = t0 + tk;
   int oa[KU], ob[KU], have = 0;
 #pragma unroll
   for (int k = 0; k < KU; ++k) {
     unit_at<VEC, HALF>(gl + k * ln, ru, half, oa[k], ob[k]);
     if (gl + k * ln < U) have = k + 1;
   }
-  auto load = [&](int r, Part<DT, VEC, KU>& x) {
-    const T* src;
-    if (r < p.H)
-      src = static_cast<const T*>(p.q) + t * p.q_token + r * p.q_head;
-    else if (r < p.H + p.Hkv)
-      src = static_cast<const T*>(p.k) + t * p.k_token + (r - p.H) * p.k_head;
-    else
-      src = static_cast<const T*>(p.v) + t * p.v_token +
-            static_cast<int64_t>(r - p.H - p.Hkv) * p.d;
-#pragma unroll
-    for (int k = 0; k < KU; ++k)
-      if (k < have) {
-        x.a[k] = *reinterpret_cast<const C*>(src + oa[k]);
-        x.b[k] = *reinterpret_cast<const C*>(src + ob[k]);
-      }
+  RowWalk w(threadIdx.x / ln, groups, rows);
+  auto row_at = [&]() -> const void* {
+    const int64_t t = t0 + w.tk;
+    if (w.r < p.H) return static_cast<const T*>(p.q) + t * p.q_token + w.r * p.q_head;
+    if (w.r < p.H + p.Hkv)
+      return static_cast<const T*>(p.k) + t * p.k_token + (w.r - p.H) * p.k_head;
+    return static_cast<const T*>(p.v) + t * p.v_token +
+           static_cast<int64_t>(w.r - p.H - p.Hkv) * p.d;
   };
-  Part<DT, VEC, KU> cur, next;
-#pragma unroll
-  for (int k = 0; k < KU; ++k)
-#pragma unroll
-    for (int e = 0; e < VEC; ++e)
-      cur.a[k].e[e] = cur.b[k].e[e] = next.a[k].e[e] = next.b[k].e[e] = T(0);
-  int r = g % step;
-  if (tk < nt && r < rows) load(r, cur);  // under way while the angles are made
-  fill_freqs(p, s_freq, s_axis);
+  Part<DT, VEC, KU> x;
+  x.clear();
+  if (w.tk < nt) x.load(row_at(), oa, ob, have);  // under way while the angles are made
+  fill_fixed<DT, VEC, HALF>(p, sh);
   if constexpr (MODE) {
     sequences_of(p.cu, p.B, static_cast<int>(p.T), p.status, t0, nt, s_seq);
     if (threadIdx.x < nt) {
@@ -226,29 +304,16 @@ __global__ void __launch_bounds__(kRopeThreads)
     s_pos[a][i] = p.pos[a * p.T + t0 + i];
   }
   __syncthreads();
-  fill_angles<VEC>(p, nt, s_freq, s_axis, s_cs, p.inverse != 0,
-                   [&](int a, int i) { return s_pos[a][i]; });
+  fill_angles<VEC>(p, nt, sh, p.inverse != 0, [&](int a, int i) { return s_pos[a][i]; });
   __syncthreads();
 
-  float2 cs[KU][VEC];
-#pragma unroll
-  for (int k = 0; k < KU; ++k)
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      const int u = gl + k * ln;
-      cs[k][e] = tk < nt && u < ru ? s_cs[tk * half + e * ru + u] : make_float2(1.f, 0.f);
-    }
-  float w[KU][2 * VEC];
-  int kind = -1;  // whose weight w holds
   const float inv_d = 1.f / p.d;
-  const int64_t slot = MODE && tk < nt ? s_dst[tk] : 0;
-  for (int r1 = 0; r1 < rows; r1 += step, r += step) {  // every lane of a warp goes round alike
-    const bool live = tk < nt && r < rows;
-    if (tk < nt && r + step < rows) load(r + step, next);
+  for (int left = nt * rows; left > 0; left -= groups) {  // every lane goes round alike
+    const bool live = w.tk < nt, is_v = MODE && w.r >= p.H + p.Hkv;
+    const int r = w.r;
+    const int64_t t = t0 + w.tk;
     float v[KU][2 * VEC];
-    widen<DT, VEC, KU>(cur, v);
-    cur = next;
-    const bool is_v = r >= p.H + p.Hkv;
+    x.widen(v);
     if (p.norm) {
       float ss = 0.f;
 #pragma unroll
@@ -257,22 +322,23 @@ __global__ void __launch_bounds__(kRopeThreads)
         for (int e = 0; e < 2 * VEC; ++e) ss = k < have ? fmaf(v[k][e], v[k][e], ss) : ss;
       ss = sum_lanes(ss, ln);
       if (!is_v) {
-        if (kind != (r >= p.H)) {
-          kind = r >= p.H;
-          load_weight<DT, VEC, KU>(kind ? p.k_weight : p.q_weight, p.w_f32, oa, ob, have, w);
-        }
         const float rr = rsqrtf(fmaf(ss, inv_d, p.eps));
 #pragma unroll
-        for (int k = 0; k < KU; ++k)
+        for (int k = 0; k < KU; ++k) {
+          if (k >= have) continue;
+          float wt[2 * VEC];
+          unit_weights<VEC>(sh.w + (r < p.H ? 0 : p.d), U, gl + k * ln, wt);
 #pragma unroll
-          for (int e = 0; e < 2 * VEC; ++e) v[k][e] *= rr * w[k][e];
+          for (int e = 0; e < 2 * VEC; ++e) v[k][e] *= rr * wt[e];
+        }
       }
     }
-    if (!is_v) {
+    if (!is_v && live) {
 #pragma unroll
       for (int k = 0; k < KU; ++k)
-        if (gl + k * ln < ru) turn<VEC, HALF>(v[k], cs[k]);
+        if (gl + k * ln < ru) turn<VEC, HALF>(v[k], sh.cs + w.tk * half, ru, gl + k * ln);
     }
+    const int64_t slot = MODE && live ? s_dst[w.tk] : 0;
     if (MODE == 2) {  // every group of the warp takes part in the shuffles
       uint32_t big = 0;
 #pragma unroll
@@ -294,23 +360,24 @@ __global__ void __launch_bounds__(kRopeThreads)
 #pragma unroll
           for (int e = 0; e < VEC; e += 2) {
             const int e1 = e + 1 < VEC ? e + 1 : e;
-            uint32_t x = cvt_e4m3x2(v[k][e] * up, v[k][e1] * up);
-            uint32_t y = cvt_e4m3x2(v[k][VEC + e] * up, v[k][VEC + e1] * up);
-            if (byte == 255) x = y = 0;
-            a.e[e] = static_cast<uint8_t>(x);
-            b.e[e] = static_cast<uint8_t>(y);
+            uint32_t lo = cvt_e4m3x2(v[k][e] * up, v[k][e1] * up);
+            uint32_t hi = cvt_e4m3x2(v[k][VEC + e] * up, v[k][VEC + e1] * up);
+            if (byte == 255) lo = hi = 0;
+            a.e[e] = static_cast<uint8_t>(lo);
+            b.e[e] = static_cast<uint8_t>(hi);
             if (VEC > 1) {
-              a.e[e1] = static_cast<uint8_t>(x >> 8);
-              b.e[e1] = static_cast<uint8_t>(y >> 8);
+              a.e[e1] = static_cast<uint8_t>(lo >> 8);
+              b.e[e1] = static_cast<uint8_t>(hi >> 8);
             }
           }
           *reinterpret_cast<Chunk<uint8_t, VEC>*>(dst + oa[k]) = a;
           *reinterpret_cast<Chunk<uint8_t, VEC>*>(dst + ob[k]) = b;
         }
       }
-      if (r >= p.H) continue;
     }
-    if (!live || (MODE && (r < p.H ? slot == -2 : slot < 0))) continue;
+    w.next();
+    if (w.tk < nt) x.load(row_at(), oa, ob, have);  // of the row to come
+    if (!live || (MODE && (r < p.H ? slot == -2 : MODE == 2 || slot < 0))) continue;
     T* dst;
     if (r < p.H)
       dst = static_cast<T*>(p.q_out) + t * p.q_out_token + r * p.q_out_head;
@@ -319,198 +386,150 @@ __global__ void __launch_bounds__(kRopeThreads)
     else
       dst = static_cast<T*>(is_v ? p.v_pages : p.k_pages) +
             (slot + static_cast<int64_t>(r - p.H - (is_v ? p.Hkv : 0)) * p.page_size) * p.d;
-#pragma unroll
-    for (int k = 0; k < KU; ++k) {
-      if (k >= have) continue;
-      C a, b;
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        a.e[e] = Elem<DT>::put(v[k][e]);
-        b.e[e] = Elem<DT>::put(v[k][VEC + e]);
-      }
-      *reinterpret_cast<C*>(dst + oa[k]) = a;
-      *reinterpret_cast<C*>(dst + ob[k]) = b;
-    }
+    Part<DT, VEC, KU>::store(dst, oa, ob, have, v);
   }
 }
 
-// The gradient. Persistent: CTA x takes the token batches x, x + gridDim.x, ..., a thread the same
-// elements of every row, so the weights' gradients add up in its registers; they meet once at the
-// end, per CTA, in a fixed order, and norm_rope_sum_kernel adds the CTAs in theirs: the same bits
-// on every run of the same sizes.
+// The gradient. Persistent, CTAs 0 .. ctas_q - 1 for the heads of q, the others for those of k, each
+// over every ctas'th batch of tokens. A thread has the same elements of every row, so the weight's
+// gradient adds up in its registers; they meet once at the end, per CTA, in a fixed order, and
+// norm_rope_sum_kernel adds the CTAs in theirs: the same bits on every run of the same sizes.
 template <int DT, int VEC, int KU, bool HALF>
-__global__ void __launch_bounds__(kRopeThreads)
-    norm_rope_bwd_kernel(const __grid_constant__ NormRopeParams p, int tok, int ln) {
+__global__ void __launch_bounds__(kRopeThreads, VEC == 8 ? 2 : 1)
+    norm_rope_bwd_kernel(const __grid_constant__ NormRopeParams p, int tok, int ln, int ctas_q) {
   using T = typename Elem<DT>::T;
-  using C = Chunk<T, VEC>;
-  extern __shared__ float2 s_cs[];
-  __shared__ int64_t s_pos[4][kTokMax];
+  extern __shared__ float4 s_dyn[];
+  __shared__ int64_t s_pos[FA_MAX_AXES][kTokMax];
   const int half = p.rot / 2, ru = half / VEC, U = p.d / (2 * VEC);
-  uint64_t* s_freq = reinterpret_cast<uint64_t*>(s_cs + static_cast<size_t>(tok) * half);
-  uint8_t* s_axis = reinterpret_cast<uint8_t*>(s_freq + half);
-  const int groups = kRopeThreads / ln, step = groups / tok;
-  const int g = threadIdx.x / ln, gl = threadIdx.x % ln, tk = g / step;
-  const int rows = p.H + p.Hkv;
+  const Shared sh(s_dyn, tok, half, p.d);
+  const int groups = kRopeThreads / ln, gl = threadIdx.x % ln;
+  const bool is_k = static_cast<int>(blockIdx.x) >= ctas_q;
+  const int rows = is_k ? p.Hkv : p.H, ctas = is_k ? gridDim.x - ctas_q : ctas_q;
+  const T* const px = static_cast<const T*>(is_k ? p.k : p.q);
+  const T* const py = static_cast<const T*>(is_k ? p.dyk : p.dyq);
+  T* const pd = static_cast<T*>(is_k ? p.k_out : p.q_out);
+  const int64_t x_token = is_k ? p.k_token : p.q_token, x_head = is_k ? p.k_head : p.q_head;
+  const int64_t y_token = is_k ? p.dyk_token : p.dyq_token, y_head = is_k ? p.dyk_head : p.dyq_head;
+  const int64_t d_token = is_k ? p.k_out_token : p.q_out_token;
+  const int64_t d_head = is_k ? p.k_out_head : p.q_out_head;
   int oa[KU], ob[KU], have = 0;
 #pragma unroll
   for (int k = 0; k < KU; ++k) {
     unit_at<VEC, HALF>(gl + k * ln, ru, half, oa[k], ob[k]);
     if (gl + k * ln < U) have = k + 1;
   }
-  float dw[2][KU][2 * VEC];
+  float dw[KU][2 * VEC];
 #pragma unroll
   for (int k = 0; k < KU; ++k)
 #pragma unroll
-    for (int e = 0; e < 2 * VEC; ++e) dw[0][k][e] = dw[1][k][e] = 0.f;
+    for (int e = 0; e < 2 * VEC; ++e) dw[k][e] = 0.f;
   const float inv_d = 1.f / p.d;
-  fill_freqs(p, s_freq, s_axis);
-  for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * tok; t0 < p.T;
-       t0 += static_cast<int64_t>(gridDim.x) * tok) {
+  const float* const wt = sh.w + (is_k ? p.d : 0);
+  fill_fixed<DT, VEC, HALF>(p, sh);
+  for (int64_t t0 = static_cast<int64_t>(blockIdx.x - (is_k ? ctas_q : 0)) * tok; t0 < p.T;
+       t0 += static_cast<int64_t>(ctas) * tok) {
     const int nt = static_cast<int>(min(static_cast<int64_t>(tok), p.T - t0));
-    const int64_t t = t0 + tk;
-    auto load = [&](int r, Part<DT, VEC, KU>& x, Part<DT, VEC, KU>& dy) {
-      const T *src, *up;
-      if (r < p.H) {
-        src = static_cast<const T*>(p.q) + t * p.q_token + r * p.q_head;
-        up = static_cast<const T*>(p.dyq) + t * p.dyq_token + r * p.dyq_head;
-      } else {
-        src = static_cast<const T*>(p.k) + t * p.k_token + (r - p.H) * p.k_head;
-        up = static_cast<const T*>(p.dyk) + t * p.dyk_token + (r - p.H) * p.dyk_head;
-      }
-#pragma unroll
-      for (int k = 0; k < KU; ++k)
-        if (k < have) {
-          x.a[k] = *reinterpret_cast<const C*>(src + oa[k]);
-          x.b[k] = *reinterpret_cast<const C*>(src + ob[k]);
-          dy.a[k] = *reinterpret_cast<const C*>(up + oa[k]);
-          dy.b[k] = *reinterpret_cast<const C*>(up + ob[k]);
-        }
+    RowWalk w(threadIdx.x / ln, groups, rows);
+    Part<DT, VEC, KU> x, dy;
+    x.clear();
+    dy.clear();
+    auto load = [&] {
+      const int64_t t = t0 + w.tk;
+      x.load(px + t * x_token + w.r * x_head, oa, ob, have);
+      dy.load(py + t * y_token + w.r * y_head, oa, ob, have);
     };
-    Part<DT, VEC, KU> x, dy, nx, ndy;
-#pragma unroll
-    for (int k = 0; k < KU; ++k)
-#pragma unroll
-      for (int e = 0; e < VEC; ++e)
-        x.a[k].e[e] = x.b[k].e[e] = dy.a[k].e[e] = dy.b[k].e[e] = nx.a[k].e[e] = nx.b[k].e[e] =
-            ndy.a[k].e[e] = ndy.b[k].e[e] = T(0);
-    int r = g % step;
-    if (tk < nt && r < rows) load(r, x, dy);
+    if (w.tk < nt) load();
     if (threadIdx.x < nt * p.axes) {
       const int a = threadIdx.x / nt, i = threadIdx.x - a * nt;
       s_pos[a][i] = p.pos[a * p.T + t0 + i];
     }
     __syncthreads();  // also: the last batch's sines have been read
-    fill_angles<VEC>(p, nt, s_freq, s_axis, s_cs, true,
-                     [&](int a, int i) { return s_pos[a][i]; });
+    fill_angles<VEC>(p, nt, sh, true, [&](int a, int i) { return s_pos[a][i]; });
     __syncthreads();
-    float2 cs[KU][VEC];
-#pragma unroll
-    for (int k = 0; k < KU; ++k)
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        const int u = gl + k * ln;
-        cs[k][e] = tk < nt && u < ru ? s_cs[tk * half + e * ru + u] : make_float2(1.f, 0.f);
-      }
-    float w[KU][2 * VEC];
-    int kind = -1;
-    for (int r1 = 0; r1 < rows; r1 += step, r += step) {
-      const bool live = tk < nt && r < rows;
-      if (tk < nt && r + step < rows) load(r + step, nx, ndy);
-      float v[KU][2 * VEC], d[KU][2 * VEC];
-      widen<DT, VEC, KU>(x, v);
-      widen<DT, VEC, KU>(dy, d);
-      x = nx;
-      dy = ndy;
-      if (kind != (r >= p.H)) {
-        kind = r >= p.H;
-        load_weight<DT, VEC, KU>(kind ? p.k_weight : p.q_weight, p.w_f32, oa, ob, have, w);
-      }
-#pragma unroll
-      for (int k = 0; k < KU; ++k)
-        if (gl + k * ln < ru) turn<VEC, HALF>(d[k], cs[k]);
+    for (int left = nt * rows; left > 0; left -= groups) {
+      const bool live = w.tk < nt;
+      T* const dst = pd + (t0 + w.tk) * d_token + w.r * d_head;
+      float v[KU][2 * VEC], g[KU][2 * VEC];
+      x.widen(v);
+      dy.widen(g);
       float ss = 0.f, sg = 0.f;
+      if (live) {
 #pragma unroll
-      for (int k = 0; k < KU; ++k)
+        for (int k = 0; k < KU; ++k)
+          if (gl + k * ln < ru) turn<VEC, HALF>(g[k], sh.cs + w.tk * half, ru, gl + k * ln);
+      }
+      w.next();
+      if (w.tk < nt) load();  // of the row to come
 #pragma unroll
-        for (int e = 0; e < 2 * VEC; ++e)
-          if (k < have) {
-            ss = fmaf(v[k][e], v[k][e], ss);
-            sg = fmaf(w[k][e] * d[k][e], v[k][e], sg);
-          }
+      for (int k = 0; k < KU; ++k) {
+        if (k >= have) continue;
+        float wk[2 * VEC];
+        unit_weights<VEC>(wt, U, gl + k * ln, wk);
+#pragma unroll
+        for (int e = 0; e < 2 * VEC; ++e) {
+          ss = fmaf(v[k][e], v[k][e], ss);
+          sg = fmaf(wk[e] * g[k][e], v[k][e], sg);
+        }
+      }
       ss = sum_lanes(ss, ln);
       sg = sum_lanes(sg, ln);
       if (!live) continue;
       const float rr = rsqrtf(fmaf(ss, inv_d, p.eps)), c = rr * rr * rr * (sg * inv_d);
-      if (r < p.H) {
-#pragma unroll
-        for (int k = 0; k < KU; ++k)
-#pragma unroll
-          for (int e = 0; e < 2 * VEC; ++e) dw[0][k][e] = fmaf(d[k][e] * v[k][e], rr, dw[0][k][e]);
-      } else {
-#pragma unroll
-        for (int k = 0; k < KU; ++k)
-#pragma unroll
-          for (int e = 0; e < 2 * VEC; ++e) dw[1][k][e] = fmaf(d[k][e] * v[k][e], rr, dw[1][k][e]);
-      }
-      T* dst = r < p.H ? static_cast<T*>(p.q_out) + t * p.q_out_token + r * p.q_out_head
-                       : static_cast<T*>(p.k_out) + t * p.k_out_token + (r - p.H) * p.k_out_head;
 #pragma unroll
       for (int k = 0; k < KU; ++k) {
         if (k >= have) continue;
-        C a, b;
+        float wk[2 * VEC];
+        unit_weights<VEC>(wt, U, gl + k * ln, wk);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          a.e[e] = Elem<DT>::put(fmaf(-v[k][e], c, rr * (w[k][e] * d[k][e])));
-          b.e[e] = Elem<DT>::put(fmaf(-v[k][VEC + e], c, rr * (w[k][VEC + e] * d[k][VEC + e])));
+        for (int e = 0; e < 2 * VEC; ++e) {
+          dw[k][e] = fmaf(g[k][e] * v[k][e], rr, dw[k][e]);
+          v[k][e] = fmaf(-v[k][e], c, rr * (wk[e] * g[k][e]));
         }
-        *reinterpret_cast<C*>(dst + oa[k]) = a;
-        *reinterpret_cast<C*>(dst + ob[k]) = b;
       }
+      Part<DT, VEC, KU>::store(dst, oa, ob, have, v);
     }
   }
   if (!p.part) return;
-  // the groups of a warp, then the warps, per kind of row
+  // the groups of a warp, then the warps
   __shared__ float s_dw[kRopeThreads / 32][512];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
 #pragma unroll
-  for (int kd = 0; kd < 2; ++kd) {
-    __syncthreads();
+  for (int k = 0; k < KU; ++k)
 #pragma unroll
-    for (int k = 0; k < KU; ++k)
-#pragma unroll
-      for (int e = 0; e < 2 * VEC; ++e) {
-        float s = dw[kd][k][e];
-        for (int o = ln; o < 32; o *= 2) s += __shfl_xor_sync(kAll, s, o);
-        if (lane < ln && k < have) s_dw[warp][(e < VEC ? oa[k] : ob[k] - VEC) + e] = s;
-      }
-    __syncthreads();
-    for (int i = threadIdx.x; i < p.d; i += kRopeThreads) {
-      float s = 0.f;
-#pragma unroll
-      for (int x = 0; x < kRopeThreads / 32; ++x) s += s_dw[x][i];
-      p.part[(static_cast<size_t>(blockIdx.x) * 2 + kd) * p.d + i] = s;
+    for (int e = 0; e < 2 * VEC; ++e) {
+      float s = dw[k][e];
+      for (int o = ln; o < 32; o *= 2) s += __shfl_xor_sync(kAll, s, o);
+      if (lane < ln && k < have) s_dw[warp][(e < VEC ? oa[k] : ob[k] - VEC) + e] = s;
     }
+  __syncthreads();
+  for (int i = threadIdx.x; i < p.d; i += kRopeThreads) {
+    float s = 0.f;
+#pragma unroll
+    for (int x = 0; x < kRopeThreads / 32; ++x) s += s_dw[x][i];
+    p.part[static_cast<size_t>(blockIdx.x) * p.d + i] = s;
   }
 }
 
-// Column c of the CTAs' partial sums [ctas][2 d]: 32 columns and 32 shares of the CTAs per CTA.
+// Column c of the CTAs' partial sums [ctas][d], the first ctas_q rows of q's weight, the others of
+// k's: 32 columns and 32 shares of the rows per CTA; blockIdx.y picks the weight.
 __global__ void __launch_bounds__(1024)
-    norm_rope_sum_kernel(const float* part, int ctas, int d, float* dq_weight, float* dk_weight) {
+    norm_rope_sum_kernel(const float* part, int ctas, int ctas_q, int d, float* dq_weight,
+                         float* dk_weight) {
   __shared__ float s[32][33];
+  float* const out = blockIdx.y ? dk_weight : dq_weight;
+  if (!out) return;
   const int lane = threadIdx.x % 32, share = threadIdx.x / 32, c = blockIdx.x * 32 + lane;
+  const int from = blockIdx.y ? ctas_q : 0, to = blockIdx.y ? ctas : ctas_q;
   float x = 0.f;
-  if (c < 2 * d)
-    for (int i = share; i < ctas; i += 32) x += part[static_cast<size_t>(i) * 2 * d + c];
+  if (c < d)
+    for (int i = from + share; i < to; i += 32) x += part[static_cast<size_t>(i) * d + c];
   s[share][lane] = x;
   __syncthreads();
   x = s[lane][share];  // lane: share; share: column
 #pragma unroll
   for (int o = 16; o > 0; o /= 2) x += __shfl_xor_sync(kAll, x, o);
   const int col = blockIdx.x * 32 + share;
-  if (lane == 0 && col < 2 * d) {
-    float* out = col < d ? dq_weight : dk_weight;
-    if (out) out[col < d ? col : col - d] = x;
-  }
+  if (lane == 0 && col < d) out[col] = x;
 }
 
 // Cached rows back as packed 16-bit ones: a CTA takes `tok` tokens, eight or four lanes a row of K
@@ -578,12 +597,21 @@ int lanes_of(int units, int ku) {
   return ln;
 }
 
+// Tokens of a CTA: as many as give every group of lanes `each` rows, where that leaves every SM a few
+// CTAs and their sines fit (the angles' cost is shared by more heads than by more tokens).
+int tokens_of(const NormRopeParams& p, int ln, int rows, int each, int64_t ctas) {
+  const int groups = kRopeThreads / ln;
+  int64_t tok = std::max(1, each * groups / rows);
+  tok = std::min<int64_t>({tok, kTokMax, std::max<int64_t>(1, p.T / ctas)});
+  while (tok > 1 && shared_bytes(static_cast<int>(tok), p.rot / 2, p.d) > 16384) --tok;
+  return static_cast<int>(tok);
+}
+
 template <int DT, int VEC, int KU, int MODE>
 cudaError_t launch_v(const NormRopeParams& p, bool half_style, int sms, cudaStream_t stream) {
-  // Tokens per CTA: one while that leaves SMs without work (a decode step), four for a prompt.
-  const int tok = p.T >= 16LL * sms ? 4 : 1;
-  const int ln = lanes_of(p.d / (2 * VEC), KU);
-  const size_t smem = static_cast<size_t>(p.rot / 2) * (tok * sizeof(float2) + sizeof(uint64_t) + 1);
+  const int ln = lanes_of(p.d / (2 * VEC), KU), rows = p.H + (MODE ? 2 : 1) * p.Hkv;
+  const int tok = tokens_of(p, ln, rows, 4, 8LL * sms);
+  const size_t smem = shared_bytes(tok, p.rot / 2, p.d);
   const int64_t grid = (p.T + tok - 1) / tok;
   if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
   auto* k = half_style ? norm_rope_kernel<DT, VEC, KU, true, MODE>
@@ -593,19 +621,25 @@ cudaError_t launch_v(const NormRopeParams& p, bool half_style, int sms, cudaStre
 }
 template <int DT, int VEC, int KU>
 cudaError_t launch_bwd_v(const NormRopeParams& p, bool half_style, int sms, cudaStream_t stream) {
-  const int tok = p.T >= 16LL * sms ? 4 : 1;
   const int ln = lanes_of(p.d / (2 * VEC), KU);
-  const size_t smem = static_cast<size_t>(p.rot / 2) * (tok * sizeof(float2) + sizeof(uint64_t) + 1);
+  const int tok = tokens_of(p, ln, std::max(1, std::min(p.H, p.Hkv ? p.Hkv : p.H)), 4, 4LL * sms);
+  const size_t smem = shared_bytes(tok, p.rot / 2, p.d);
   const int64_t batches = (p.T + tok - 1) / tok;
-  const int64_t most = 2 * sms < kNormCtas ? 2 * sms : kNormCtas;
-  const int grid = static_cast<int>(batches < most ? batches : most);
+  const int64_t most = std::min<int64_t>(2 * sms, kNormCtas);
+  // CTAs of q and k by their heads, at least one each
+  const int all = static_cast<int>(std::min<int64_t>(most, p.Hkv ? 2 * batches : batches));
+  int ctas_k = p.Hkv ? static_cast<int>(static_cast<int64_t>(all) * p.Hkv / (p.H + p.Hkv)) : 0;
+  if (p.Hkv) ctas_k = std::max(1, ctas_k);
+  int ctas_q = std::max(1, all - ctas_k);
+  ctas_q = static_cast<int>(std::min<int64_t>(ctas_q, batches));
+  ctas_k = static_cast<int>(std::min<int64_t>(ctas_k, batches));
   auto* k = half_style ? norm_rope_bwd_kernel<DT, VEC, KU, true>
                        : norm_rope_bwd_kernel<DT, VEC, KU, false>;
-  k<<<grid, kRopeThreads, smem, stream>>>(p, tok, ln);
+  k<<<ctas_q + ctas_k, kRopeThreads, smem, stream>>>(p, tok, ln, ctas_q);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || !p.part) return e;
-  norm_rope_sum_kernel<<<(2 * p.d + 31) / 32, 1024, 0, stream>>>(p.part, grid, p.d, p.dq_weight,
-                                                                 p.dk_weight);
+  norm_rope_sum_kernel<<<dim3((p.d + 31) / 32, 2), 1024, 0, stream>>>(
+      p.part, ctas_q + ctas_k, ctas_q, p.d, p.dq_weight, p.dk_weight);
   return cudaGetLastError();
 }
 

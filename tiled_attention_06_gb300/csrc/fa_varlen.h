@@ -88,7 +88,7 @@ struct NormRopeParams {
   const void* dyq;
   const void* dyk;
   int64_t dyq_token, dyq_head, dyk_token, dyk_head;
-  float* part;  // [CTAs][2][d] sums of the weights' gradients, or nullptr
+  float* part;  // [CTAs][d] sums of the weights' gradients, or nullptr
   float* dq_weight;
   float* dk_weight;
   uint32_t* status;
