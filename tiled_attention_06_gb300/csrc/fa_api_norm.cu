@@ -235,8 +235,8 @@ fa_status fa_norm_rope(const fa_norm_rope_params* params, fa_stream_t stream) {
 }
 
 size_t fa_norm_rope_bwd_workspace_size(int H, int Hkv, int d) {
-  if (H < 1 || Hkv < 0 || d < 2 || d > 512) return 0;
-  return static_cast<size_t>(fa::kNormCtas) * d * sizeof(float);
+  if (H < 1 || Hkv < 0 || H > (1 << 16) || Hkv > (1 << 16) || d < 2 || d > 512) return 0;
+  return static_cast<size_t>(fa::norm_parts(H + Hkv)) * 2 * d * sizeof(float);
 }
 
 fa_status fa_norm_rope_bwd(const fa_norm_rope_params* params, const fa_norm_rope_grads* grads,

@@ -15,10 +15,13 @@
 // a NaN gets byte 255 and is NaN when read.
 //
 // What bounds it: each element is read once and written once (the gradient reads x and dy), so
-// HBM does in bulk and latency in a decode step. A row is spread over LN neighbouring lanes, 16
-// elements to a lane, whose sums meet in log2(LN) shuffles; a group of lanes keeps to one token
-// and takes its heads one after the other, so the sines, cosines and the weight stay in registers,
-// and the next head's load is under way while one is worked on.
+// HBM does in bulk and latency in a decode step; on the way there, instructions. A row is spread over
+// LN neighbouring lanes, 16 elements to a lane, whose sums meet in log2(LN) shuffles. A group of lanes
+// keeps to one head and walks over the tokens of its CTA, so that its pointers advance by a constant, its
+// weight stays in registers and the weight's gradient adds up there; arithmetic is in packed FP32, and
+// rows come three rounds ahead by cp.async. With rows dealt to groups in order, whatever their token and
+// head, a row cost 3x the instructions and 16384 tokens x 40 heads of 128 in bf16 took 68 us and their
+// gradient 117; so they take NORM_US and GRAD_US.
 #include <algorithm>
 #include <cstdint>
 
@@ -28,7 +31,8 @@
 namespace fa {
 namespace {
 
-constexpr int kTokMax = 32;  // tokens of a CTA at most
+constexpr int kTokMax = 32;  // tokens of a batch at most
+constexpr int kMostThreads = 320;
 constexpr uint32_t kAll = 0xffffffffu;
 
 // The exponent byte of a row from the bits of its largest magnitude: bits of an infinity or NaN
@@ -74,34 +78,24 @@ __device__ __forceinline__ void unit_at(int u, int ru, int half, int& oa, int& o
 // pairs at a time, (A_e, A_{e+1}) and (B_e, B_{e+1}), in packed FP32: of one unit, or where units are
 // pairs (VEC = 1) of two of the lane's units.
 //
-// A CTA's shared memory: sines and cosines of its tokens, the frequencies, the weights of q and k,
-// the pairs' axes. For VEC > 1 the cosines and sines (the weights of A and B) of two pairs are 16
-// bytes, neighbouring units next to each other, so that neighbouring lanes read neighbouring 16 bytes.
+// A CTA's shared memory: rows on their way, sines and cosines of a batch of its tokens, the frequencies
+// and the pairs' axes. For VEC > 1 the cosines and sines of two pairs are 16 bytes, neighbouring units
+// next to each other, so that neighbouring lanes read neighbouring 16 bytes.
 struct Shared {
   float2* cs;
   uint64_t* freq;
-  float* w;
   uint8_t* axis;
-  __device__ __forceinline__ Shared(float4* base, int tok, int half, int d) {
+  __device__ __forceinline__ Shared(float4* base, int tok, int half) {
     cs = reinterpret_cast<float2*>(base);
-    w = reinterpret_cast<float*>(cs + static_cast<size_t>((tok * half + 1) & ~1));
-    freq = reinterpret_cast<uint64_t*>(w + static_cast<size_t>((2 * d + 3) & ~3));
+    freq = reinterpret_cast<uint64_t*>(cs + static_cast<size_t>(tok) * half);
     axis = reinterpret_cast<uint8_t*>(freq + half);
   }
 };
-size_t shared_bytes(int tok, int half, int d) {
-  return static_cast<size_t>((tok * half + 1) & ~1) * 8 + static_cast<size_t>((2 * d + 3) & ~3) * 4 +
-         static_cast<size_t>(half) * 9;
-}
+int shared_bytes(int tok, int half) { return tok * half * 8 + half * 9; }
 // Rows on their way: every thread copies its own 16-byte chunks of the rows to come to shared memory
-// (cp.async, three rounds ahead and on into the next batch) and reads them back itself, so nothing waits
-// for anyone else. In registers a row ahead is what there is room for: 32 KB per SM on their way,
-// 73 us where this takes 5x, 152 us for the gradient's 9x.
-constexpr int kStages = 4;
-template <int VEC>
-__host__ __device__ constexpr int ring_bytes(int chunks) {  // chunks of 16 bytes, per thread and round
-  return VEC == 1 ? 0 : kStages * chunks * kRopeThreads * 16;
-}
+// (cp.async) and reads them back itself, so nothing waits for anyone else. In registers a row ahead is
+// what there is room for, 32 KB per SM on their way.
+constexpr int kStages = 4, kGradStages = 3;  // the gradient's rounds are twice as large
 __device__ __forceinline__ void copy_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
@@ -120,18 +114,16 @@ __device__ __forceinline__ float weight_at(const void* w, int f32, int dt, int i
   return dt == FA_BF16 ? Elem<FA_BF16>::get(x) : Elem<FA_F16>::get(x);
 }
 
-// Where the first of pair e of unit u's two numbers lies (the second is two behind it for VEC > 1,
-// one for VEC = 1), `units` of them in all: [e / 2][u][A_e A_{e+1} B_e B_{e+1}], or [u][A B].
+// Where the cosine of pair e of unit u lies (its sine is two behind it for VEC > 1, one for VEC = 1),
+// `units` rotated units in all: [e / 2][u][c_e c_{e+1} s_e s_{e+1}], or [u][c s].
 template <int VEC>
 __device__ __forceinline__ int pair_at(int u, int e, int units) {
   return VEC == 1 ? 2 * u : ((e / 2) * units + u) * 4 + e % 2;
 }
 
-// Frequencies, axes and weights: the part that does not depend on the tokens.
-template <int DT, int VEC, bool HALF>
+// Frequencies and axes: the part that does not depend on the tokens.
 __device__ __forceinline__ void fill_fixed(const NormRopeParams& p, const Shared& sh) {
-  const int half = p.rot / 2, ru = half / VEC, U = p.d / (2 * VEC);
-  for (int i = threadIdx.x; i < half; i += kRopeThreads) {
+  for (int i = threadIdx.x; i < p.rot / 2; i += blockDim.x) {
     sh.freq[i] = turns_q64(p.freqs[i]);
     int a = p.pair_axis ? p.pair_axis[i] : 0;
     if (a < 0 || a >= p.axes) {
@@ -140,23 +132,13 @@ __device__ __forceinline__ void fill_fixed(const NormRopeParams& p, const Shared
     }
     sh.axis[i] = static_cast<uint8_t>(a);
   }
-  if (!p.norm) return;
-  for (int i = threadIdx.x; i < 2 * U * VEC; i += kRopeThreads) {
-    const int e = i % VEC, q = i / VEC, kind = q >= U ? 1 : 0, u = q - kind * U;
-    const void* const w = kind ? p.k_weight : p.q_weight;
-    int oa, ob;
-    unit_at<VEC, HALF>(u, ru, half, oa, ob);
-    float* const at = sh.w + kind * p.d + pair_at<VEC>(u, e, U);
-    at[0] = weight_at(w, p.w_f32, DT, HALF || VEC == 1 ? oa + e : oa + 2 * e);
-    at[VEC == 1 ? 1 : 2] = weight_at(w, p.w_f32, DT, HALF || VEC == 1 ? ob + e : oa + 2 * e + 1);
-  }
 }
 // Sines and cosines of nt tokens; pos(axis, token) in 64 bits.
 template <int VEC, typename Pos>
 __device__ __forceinline__ void fill_angles(const NormRopeParams& p, int nt, const Shared& sh,
                                             bool inverse, Pos pos) {
   const int half = p.rot / 2, ru = half / VEC;
-  const int dt = kRopeThreads / half, df = kRopeThreads % half;
+  const int dt = blockDim.x / half, df = blockDim.x % half;
   int tk = threadIdx.x / half, f = threadIdx.x % half;
   while (tk < nt) {
     const int64_t at = pos(sh.axis[f], tk);
@@ -180,11 +162,25 @@ __device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
-__device__ __forceinline__ uint64_t f2_neg(uint64_t a) { return a ^ 0x8000000080000000ull; }
 __device__ __forceinline__ float f2_sum(uint64_t a) {
   float x, y;
   f2_split(a, x, y);
   return x + y;
+}
+
+template <typename C>
+__device__ __forceinline__ C load_shared16(uint32_t at) {
+  static_assert(sizeof(C) == 16 || sizeof(C) < 16, "one access");
+  C c;
+  if constexpr (sizeof(C) == 16) {
+    uint32_t r[4];
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(at)
+                 : "memory");
+    __builtin_memcpy(&c, r, 16);
+  }
+  return c;
 }
 
 // A lane's part of a row: KU units of VEC + VEC elements; N pairs, worked on two at a time.
@@ -208,24 +204,27 @@ struct Part {
         b[k] = *reinterpret_cast<const C*>(src + ob[k]);
       }
   }
-  // the same by way of shared memory: chunk c of the thread at c * kRopeThreads * 16
-  static __device__ __forceinline__ void fetch(uint32_t at, const T* src, const int* oa,
-                                               const int* ob, int have) {
+  // the same by way of shared memory: chunk c of the thread at c * step
+  static __device__ __forceinline__ void fetch(uint32_t at, uint32_t step, const T* src,
+                                               const int* oa, const int* ob, int have) {
 #pragma unroll
     for (int k = 0; k < KU; ++k)
       if (k < have) {
-        copy_async16(at + (2 * k) * (kRopeThreads * 16), src + oa[k]);
-        copy_async16(at + (2 * k + 1) * (kRopeThreads * 16), src + ob[k]);
+        copy_async16(at + (2 * k) * step, src + oa[k]);
+        copy_async16(at + (2 * k + 1) * step, src + ob[k]);
       }
   }
-  __device__ __forceinline__ void take(const uint8_t* at, int have) {
-    clear();
+  // (a chunk that the row does not have is whatever lies there; its elements are zeroed)
+  __device__ __forceinline__ void take(uint32_t at, uint32_t step, int have) {
 #pragma unroll
-    for (int k = 0; k < KU; ++k)
-      if (k < have) {
-        a[k] = *reinterpret_cast<const C*>(at + (2 * k) * (kRopeThreads * 16));
-        b[k] = *reinterpret_cast<const C*>(at + (2 * k + 1) * (kRopeThreads * 16));
+    for (int k = 0; k < KU; ++k) {
+      a[k] = load_shared16<C>(at + (2 * k) * step);
+      b[k] = load_shared16<C>(at + (2 * k + 1) * step);
+      if (k >= have) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) a[k].e[e] = b[k].e[e] = T(0);
       }
+    }
   }
   __device__ __forceinline__ T& first(int i) {
     const int k = i / VEC, e = i % VEC;
@@ -266,32 +265,33 @@ struct Part {
   }
 };
 
-// The two numbers of two pairs, (A_e, A_{e+1}) and (B_e, B_{e+1}), for the lane's packed pair i; its
-// units are u0, u0 + ln, ... A unit that the row does not have reads the last one's.
+// Cosines and sines of the lane's packed pair i, (c_e, c_{e+1}) and (s_e, s_{e+1}); its units are u0,
+// u0 + ln, .... A unit behind the rotated part reads the last one's.
 template <int VEC>
-__device__ __forceinline__ void pairs_of(const float* at, int i, int u0, int ln, int units,
-                                         uint64_t& A, uint64_t& B) {
+__device__ __forceinline__ void angles_of(const float* at, int i, int u0, int ln, int units,
+                                          uint64_t& c, uint64_t& s) {
   if constexpr (VEC == 1) {
     const float2 x = *reinterpret_cast<const float2*>(at + 2 * min(u0 + 2 * i * ln, units - 1));
     const float2 y = *reinterpret_cast<const float2*>(at + 2 * min(u0 + (2 * i + 1) * ln, units - 1));
-    A = f2(x.x, y.x);
-    B = f2(x.y, y.y);
+    c = f2(x.x, y.x);
+    s = f2(x.y, y.y);
   } else {
     const int u = min(u0 + (2 * i / VEC) * ln, units - 1);
     const ulonglong2 x =
         *reinterpret_cast<const ulonglong2*>(at + pair_at<VEC>(u, 2 * i % VEC, units));
-    A = x.x;
-    B = x.y;
+    c = x.x;
+    s = x.y;
   }
 }
-// The rotation of a lane's pairs; those behind the rotated part stay.
+// The rotation of a lane's pairs, (A, B) to (A c - B s, B c + A s), with nB = -B; those behind the
+// rotated part stay.
 template <int VEC, int N2>
-__device__ __forceinline__ void turn(uint64_t* A, uint64_t* B, const float2* cs, int u0, int ln,
-                                     int ru) {
+__device__ __forceinline__ void turn(uint64_t* A, uint64_t* B, const uint64_t* nB, const float2* cs,
+                                     int u0, int ln, int ru) {
 #pragma unroll
   for (int i = 0; i < N2; ++i) {
     uint64_t c, s;
-    pairs_of<VEC>(reinterpret_cast<const float*>(cs), i, u0, ln, ru, c, s);
+    angles_of<VEC>(reinterpret_cast<const float*>(cs), i, u0, ln, ru, c, s);
     if (VEC == 1) {  // two units, of which the rotated part may end with the first
       const bool in0 = u0 + 2 * i * ln < ru, in1 = u0 + (2 * i + 1) * ln < ru;
       const uint64_t lo = 0xffffffffull, one = 0x3f800000ull;
@@ -300,9 +300,24 @@ __device__ __forceinline__ void turn(uint64_t* A, uint64_t* B, const float2* cs,
     } else if (u0 + (2 * i / VEC) * ln >= ru) {
       continue;
     }
-    const uint64_t a = A[i], b = B[i];
-    A[i] = f2_fma(a, c, f2_mul(b, f2_neg(s)));
-    B[i] = f2_fma(b, c, f2_mul(a, s));
+    const uint64_t a = A[i];
+    A[i] = f2_fma(a, c, f2_mul(nB[i], s));
+    B[i] = f2_fma(B[i], c, f2_mul(a, s));
+  }
+}
+// The weights of a lane's elements, as its pairs lie.
+template <int DT, int VEC, int KU, bool HALF>
+__device__ __forceinline__ void weights_of(const NormRopeParams& p, const void* w, const int* oa,
+                                           const int* ob, int have, uint64_t* A, uint64_t* B) {
+  auto get = [&](int n, int second) {
+    const int k = n / VEC, e = n % VEC;
+    const int at = HALF || VEC == 1 ? (second ? ob[k] : oa[k]) + e : oa[k] + 2 * e + second;
+    return k < have ? weight_at(w, p.w_f32, DT, at) : 0.f;
+  };
+#pragma unroll
+  for (int i = 0; i < KU * VEC / 2; ++i) {
+    A[i] = f2(get(2 * i, 0), get(2 * i + 1, 0));
+    B[i] = f2(get(2 * i, 1), get(2 * i + 1, 1));
   }
 }
 __device__ __forceinline__ float sum_lanes(float x, int ln) {
@@ -310,146 +325,122 @@ __device__ __forceinline__ float sum_lanes(float x, int ln) {
   return x;
 }
 
-// The walk of a group of lanes over the rows of the CTA's batches of tokens, (token, head) with the
-// heads first: rows g, g + groups, ... of a batch, and so on in the next one. Every group goes the same
-// number of rounds in a batch, in the last of which it may have no row.
-struct RowWalk {
-  int64_t t0;  // first token of the batch
-  int tk, r, left;  // token of the batch, row of it, rows of the batch from this round on
-  __device__ __forceinline__ int tokens(const NormRopeParams& p, int tok) const {
-    return static_cast<int>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(tok), p.T - t0)));
-  }
+// How the rows are dealt. A CTA has a run of tokens and `heads` heads from blockIdx.y * heads on; group
+// g of its lanes has head g % heads of tokens g / heads, g / heads + per_round, ... of the run. Angles are
+// made for `tok` tokens (a multiple of per_round) at a time.
+struct Deal {
+  int ln, heads, per_round, tok;
 };
-struct RowSteps {
-  int g, groups, rows, tok, dt, dr;
-  int64_t step;  // tokens between the CTA's batches
-  __device__ __forceinline__ RowSteps(int ln, int rows, int tok, int64_t step)
-      : g(threadIdx.x / ln),
-        groups(kRopeThreads / ln),
-        rows(rows),
-        tok(tok),
-        dt(groups / rows),
-        dr(groups % rows),
-        step(step) {}
-  __device__ __forceinline__ void start(RowWalk& w, const NormRopeParams& p, int64_t t0) const {
-    w.t0 = t0;
-    w.tk = g / rows;
-    w.r = g - w.tk * rows;
-    w.left = w.tokens(p, tok) * rows;
-  }
-  // to the next round of the batch; false at its end
-  __device__ __forceinline__ bool next(RowWalk& w) const {
-    w.tk += dt;
-    w.r += dr;
-    if (w.r >= rows) {
-      w.r -= rows;
-      ++w.tk;
-    }
-    w.left -= groups;
-    return w.left > 0;
+struct Mine {
+  int tr, r;           // first token of the run, head
+  bool on;             // this group has a head
+  int64_t begin, end;  // the CTA's tokens
+  __device__ __forceinline__ Mine(const NormRopeParams& p, const Deal& d, int rows) {
+    const int g = threadIdx.x / d.ln;
+    tr = g / d.heads;
+    r = blockIdx.y * d.heads + g - tr * d.heads;
+    on = tr < d.per_round && r < rows;
+    begin = p.T * blockIdx.x / gridDim.x;
+    end = p.T * (blockIdx.x + 1) / gridDim.x;
   }
 };
 
 // Rows r of a token: H of q, Hkv of k and, when appending, Hkv of v. MODE 0: y to q_out and k_out;
-// 1 and 2: q to q_out, k and v to the cache's slot of the token, in 16 and in 8 bits. Persistent, every
-// grid'th batch of tokens: what comes before the first row (a dozen integer divisions, frequencies,
-// weights) was 45 % of all instructions with a CTA per batch of three tokens (91 us, now 6x).
+// 1 and 2: q to q_out, k and v to the cache's slot of the token, in 16 and in 8 bits.
 template <int DT, int VEC, int KU, bool HALF, int MODE>
-__global__ void __launch_bounds__(kRopeThreads, 4)
-    norm_rope_kernel(const __grid_constant__ NormRopeParams p, int tok, int ln) {
+__global__ void __launch_bounds__(kMostThreads, DT != FA_F32 && VEC > 1 ? 3 : 2)
+    norm_rope_kernel(const __grid_constant__ NormRopeParams p, const Deal deal) {
   using T = typename Elem<DT>::T;
   using X = Part<DT, VEC, KU, HALF>;
   constexpr int N2 = X::N2;
   extern __shared__ float4 s_dyn[];
   __shared__ int64_t s_dst[kTokMax], s_pos[FA_MAX_AXES][kTokMax];
   __shared__ int s_seq[kTokMax];
-  const int half = p.rot / 2, ru = half / VEC, U = p.d / (2 * VEC);
-  constexpr int kRing = ring_bytes<VEC>(2 * KU);
-  uint8_t* const ring = reinterpret_cast<uint8_t*>(s_dyn) + threadIdx.x * 16;
-  const Shared sh(s_dyn + kRing / 16, tok, half, p.d);
-  const int gl = threadIdx.x % ln;
-  const int rows = MODE ? p.H + 2 * p.Hkv : p.H + p.Hkv;
+  const int half = p.rot / 2, ru = half / VEC, U = p.d / (2 * VEC), ln = deal.ln;
+  // chunk c of round i of the thread at ((i % kStages) * 2 KU + c) * step
+  const uint32_t step = blockDim.x * 16, stage = 2 * KU * step;
+  const uint32_t ring = smem_u32(s_dyn) + threadIdx.x * 16;
+  const Shared sh(s_dyn + (VEC == 1 ? 0 : kStages * 2 * KU * blockDim.x), deal.tok, half);
+  const int gl = threadIdx.x % ln, rows = MODE ? p.H + 2 * p.Hkv : p.H + p.Hkv;
+  const Mine me(p, deal, rows);
+  const bool is_q = me.r < p.H, is_v = MODE && me.r >= p.H + p.Hkv;
+  const int h = is_q ? me.r : me.r - p.H - (is_v ? p.Hkv : 0);  // head of q, k or v
   int oa[KU], ob[KU], have = 0;
 #pragma unroll
   for (int k = 0; k < KU; ++k) {
     unit_at<VEC, HALF>(gl + k * ln, ru, half, oa[k], ob[k]);
-    if (gl + k * ln < U) have = k + 1;
+    if (me.on && gl + k * ln < U) have = k + 1;
   }
-  const RowSteps steps(ln, rows, tok, static_cast<int64_t>(gridDim.x) * tok);
-  const float inv_d = 1.f / p.d;
-  auto row_at = [&](const RowWalk& w) -> const T* {
-    const int64_t t = w.t0 + w.tk;
-    if (w.r < p.H) return static_cast<const T*>(p.q) + t * p.q_token + w.r * p.q_head;
-    if (w.r < p.H + p.Hkv)
-      return static_cast<const T*>(p.k) + t * p.k_token + (w.r - p.H) * p.k_head;
-    return static_cast<const T*>(p.v) + t * p.v_token +
-           static_cast<int64_t>(w.r - p.H - p.Hkv) * p.d;
-  };
-  RowWalk w, ahead;
-  steps.start(ahead, p, static_cast<int64_t>(blockIdx.x) * tok);
-  uint32_t in = 0, out = 0;  // rounds fetched and taken
+  const int64_t in_token = is_q ? p.q_token : is_v ? p.v_token : p.k_token;
+  const int64_t in_step = in_token * deal.per_round;
+  const int64_t out_token = is_q ? p.q_out_token : p.k_out_token;
+  int64_t t = me.begin + me.tr, ahead = t;  // tokens of the round, and of the fetch
+  const T* src = static_cast<const T*>(is_q ? p.q : is_v ? p.v : p.k) + t * in_token +
+                 h * (is_q ? p.q_head : is_v ? static_cast<int64_t>(p.d) : p.k_head);
+  T* dst = MODE && !is_q ? nullptr
+                         : static_cast<T*>(is_q ? p.q_out : p.k_out) + t * out_token +
+                               h * (is_q ? p.q_out_head : p.k_out_head);
+  uint32_t in = 0, out = 0;  // stages of the ring
   auto fetch = [&] {
-    if (ahead.t0 < p.T) {
-      if (ahead.tk < ahead.tokens(p, tok))
-        X::fetch(smem_u32(ring) + in % kStages * (kRing / kStages), row_at(ahead), oa, ob, have);
-      if (!steps.next(ahead)) steps.start(ahead, p, ahead.t0 + steps.step);
-    }
+    if (ahead < me.end) X::fetch(ring + in, step, src, oa, ob, have);
     copy_commit();
-    ++in;
+    ahead += deal.per_round;
+    src += in_step;
+    in = in == (kStages - 1) * stage ? 0 : in + stage;
   };
-  if constexpr (VEC > 1) {
-#pragma unroll 1
+  if constexpr (VEC > 1) {  // under way while the angles are made
+#pragma unroll
     for (int i = 0; i < kStages - 1; ++i) fetch();
   }
-  bool first = true;
-  for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * tok; t0 < p.T; t0 += steps.step) {
-    steps.start(w, p, t0);
-    const int nt = w.tokens(p, tok);
-    if (first) fill_fixed<DT, VEC, HALF>(p, sh);
-    first = false;
+  uint64_t wA[N2], wB[N2];
+  if (p.norm && !is_v)
+    weights_of<DT, VEC, KU, HALF>(p, is_q ? p.q_weight : p.k_weight, oa, ob, have, wA, wB);
+  const float inv_d = 1.f / p.d;
+  fill_fixed(p, sh);
+  for (int64_t t0 = me.begin; t0 < me.end; t0 += deal.tok) {
+    const int nt = static_cast<int>(min(static_cast<int64_t>(deal.tok), me.end - t0));
     if constexpr (MODE) {
       sequences_of(p.cu, p.B, static_cast<int>(p.T), p.status, t0, nt, s_seq);
       if (threadIdx.x < nt) {
         const int64_t tt = t0 + threadIdx.x;
         const int b = s_seq[threadIdx.x];
-        int64_t dst = -2, pos = 0;
+        int64_t slot = -2, pos = 0;
         if (b != kNobody) {
           const int64_t at = static_cast<int64_t>(p.ctx[b]) + (tt - p.cu[b]);
           const int64_t lp = at / p.page_size;
-          const bool in = p.ctx[b] >= 0 && lp < p.max_pages;
-          const int phys = in ? p.block_table[static_cast<size_t>(b) * p.max_pages + lp] : -1;
-          dst = -1;
+          const bool in_table = p.ctx[b] >= 0 && lp < p.max_pages;
+          const int phys =
+              in_table ? p.block_table[static_cast<size_t>(b) * p.max_pages + lp] : -1;
+          slot = -1;
           if (phys < 0 || phys >= p.num_pages)
             atomicOr(p.status, FA_DEV_BAD_PAGE);
           else
-            dst = static_cast<int64_t>(phys) * p.Hkv * p.page_size + (at - lp * p.page_size);
+            slot = static_cast<int64_t>(phys) * p.Hkv * p.page_size + (at - lp * p.page_size);
           pos = at;
         }
-        s_dst[threadIdx.x] = dst;  // -2: nobody's token, nothing is written; -1: no slot, q alone is
+        s_dst[threadIdx.x] = slot;  // -2: nobody's token, nothing is written; -1: no slot, q alone is
         if (!p.pos) s_pos[0][threadIdx.x] = pos;
       }
     }
-    if (p.pos && threadIdx.x < nt * p.axes) {
-      const int a = threadIdx.x / nt, i = threadIdx.x - a * nt;
-      s_pos[a][i] = p.pos[a * p.T + t0 + i];
-    }
+    if (p.pos)
+      for (int i = threadIdx.x; i < nt * p.axes; i += blockDim.x)
+        s_pos[i / nt][i % nt] = p.pos[(i / nt) * p.T + t0 + i % nt];
     __syncthreads();  // also: the last batch's sines have been read
     fill_angles<VEC>(p, nt, sh, p.inverse != 0, [&](int a, int i) { return s_pos[a][i]; });
     __syncthreads();
-
-    bool more = true;
-    while (more) {  // every lane goes round alike
-      const bool live = w.tk < nt, is_v = MODE && w.r >= p.H + p.Hkv;
-      const int r = w.r;
-      const int64_t t = t0 + w.tk;
+    // every lane goes round alike; the last round may have no token for it
+    for (int tk = me.tr; tk - me.tr < nt; tk += deal.per_round) {
+      const bool live = me.on && tk < nt;
       X x;
       if constexpr (VEC > 1) {
         copy_wait<kStages - 2>();
-        x.take(ring + out++ % kStages * (kRing / kStages), live ? have : 0);
+        x.take(ring + out, step, have);
+        out = out == (kStages - 1) * stage ? 0 : out + stage;
         fetch();
       } else {
         x.clear();
-        if (live) x.load(row_at(w), oa, ob, have);
+        if (live) x.load(src, oa, ob, have);
+        src += in_step;
       }
       uint64_t A[N2], B[N2];
       x.widen(A, B);
@@ -464,19 +455,21 @@ __global__ void __launch_bounds__(kRopeThreads, 4)
         if (!is_v) {
           const float rr = rsqrtf(fmaf(ss, inv_d, p.eps));
           const uint64_t rr2 = f2(rr, rr);
-          const float* const wt = sh.w + (r < p.H ? 0 : p.d);
 #pragma unroll
           for (int i = 0; i < N2; ++i) {
-            uint64_t wa, wb;
-            pairs_of<VEC>(wt, i, gl, ln, U, wa, wb);
-            A[i] = f2_mul(f2_mul(A[i], rr2), wa);
-            B[i] = f2_mul(f2_mul(B[i], rr2), wb);
+            A[i] = f2_mul(f2_mul(A[i], wA[i]), rr2);
+            B[i] = f2_mul(f2_mul(B[i], wB[i]), rr2);
           }
         }
       }
-      if (!is_v && live) turn<VEC, N2>(A, B, sh.cs + w.tk * half, gl, ln, ru);
-      const int64_t slot = MODE && live ? s_dst[w.tk] : 0;
-      more = steps.next(w);
+      if (!is_v && live) {
+        const uint64_t minus = f2(-1.f, -1.f);
+        uint64_t nB[N2];
+#pragma unroll
+        for (int i = 0; i < N2; ++i) nB[i] = f2_mul(B[i], minus);
+        turn<VEC, N2>(A, B, nB, sh.cs + tk * half, gl, ln, ru);
+      }
+      const int64_t slot = MODE && live ? s_dst[tk] : 0;
       if (MODE == 2) {  // every group of the warp takes part in the shuffles
         // the largest magnitude, which passes over NaNs, and zero times everything, which does not
         float big = 0.f;
@@ -492,11 +485,11 @@ __global__ void __launch_bounds__(kRopeThreads, 4)
         }
         uint32_t bits = f2_sum(nan) == 0.f ? __float_as_uint(big) : 0x7f800000u;
         for (int o = ln / 2; o > 0; o /= 2) bits = max(bits, __shfl_xor_sync(kAll, bits, o));
-        if (live && r >= p.H && slot >= 0) {
-          const int h = r - p.H - (is_v ? p.Hkv : 0), byte = power_byte(bits);
+        if (live && !is_q && slot >= 0) {
+          const int byte = power_byte(bits);
           const float up = byte == 255 ? 0.f : up_of(byte);
           const int64_t row = slot + static_cast<int64_t>(h) * p.page_size;
-          uint8_t* dst = static_cast<uint8_t*>(is_v ? p.v_pages : p.k_pages) + row * p.d;
+          uint8_t* const to = static_cast<uint8_t*>(is_v ? p.v_pages : p.k_pages) + row * p.d;
           if (gl == 0) (is_v ? p.v_scales : p.k_scales)[row] = static_cast<uint8_t>(byte);
           Chunk<uint8_t, VEC> oc[2 * KU];
 #pragma unroll
@@ -530,148 +523,146 @@ __global__ void __launch_bounds__(kRopeThreads, 4)
 #pragma unroll
           for (int k = 0; k < KU; ++k)
             if (k < have) {
-              *reinterpret_cast<Chunk<uint8_t, VEC>*>(dst + oa[k]) = oc[2 * k];
-              *reinterpret_cast<Chunk<uint8_t, VEC>*>(dst + ob[k]) = oc[2 * k + 1];
+              *reinterpret_cast<Chunk<uint8_t, VEC>*>(to + oa[k]) = oc[2 * k];
+              *reinterpret_cast<Chunk<uint8_t, VEC>*>(to + ob[k]) = oc[2 * k + 1];
             }
         }
       }
-      if (!live || (MODE && (r < p.H ? slot == -2 : MODE == 2 || slot < 0))) continue;
-      T* dst;
-      if (r < p.H)
-        dst = static_cast<T*>(p.q_out) + t * p.q_out_token + r * p.q_out_head;
-      else if (MODE == 0)
-        dst = static_cast<T*>(p.k_out) + t * p.k_out_token + (r - p.H) * p.k_out_head;
-      else
-        dst = static_cast<T*>(is_v ? p.v_pages : p.k_pages) +
-              (slot + static_cast<int64_t>(r - p.H - (is_v ? p.Hkv : 0)) * p.page_size) * p.d;
-      X::store(dst, oa, ob, have, A, B);
+      T* const to = dst;
+      dst += out_token * deal.per_round;
+      if (!live) continue;
+      if (MODE == 0 || is_q) {
+        if (MODE == 0 || slot != -2) X::store(to, oa, ob, have, A, B);
+      } else if (MODE == 1 && slot >= 0) {
+        X::store(static_cast<T*>(is_v ? p.v_pages : p.k_pages) +
+                     (slot + static_cast<int64_t>(h) * p.page_size) * p.d,
+                 oa, ob, have, A, B);
+      }
     }
   }
 }
 
-// The gradient. Persistent, CTAs 0 .. ctas_q - 1 for the heads of q, the others for those of k, each
-// over every ctas'th batch of tokens. A thread has the same elements of every row, so the weight's
-// gradient adds up in its registers; they meet once at the end, per CTA, in a fixed order, and
+// The gradient. A thread has the same elements of one head of every token, so the weight's gradient
+// adds up in its registers; they meet once at the end, per CTA, in a fixed order, and
 // norm_rope_sum_kernel adds the CTAs in theirs: the same bits on every run of the same sizes.
 template <int DT, int VEC, int KU, bool HALF>
-__global__ void __launch_bounds__(kRopeThreads, VEC == 1 ? 1 : 2)
-    norm_rope_bwd_kernel(const __grid_constant__ NormRopeParams p, int tok, int ln, int ctas_q) {
+__global__ void __launch_bounds__(kMostThreads, VEC == 1 ? 1 : 2)
+    norm_rope_bwd_kernel(const __grid_constant__ NormRopeParams p, const Deal deal) {
   using T = typename Elem<DT>::T;
   using X = Part<DT, VEC, KU, HALF>;
   constexpr int N2 = X::N2;
   extern __shared__ float4 s_dyn[];
   __shared__ int64_t s_pos[FA_MAX_AXES][kTokMax];
-  const int half = p.rot / 2, ru = half / VEC, U = p.d / (2 * VEC);
-  constexpr int kRing = ring_bytes<VEC>(4 * KU);
-  uint8_t* const ring = reinterpret_cast<uint8_t*>(s_dyn) + threadIdx.x * 16;
-  const Shared sh(s_dyn + kRing / 16, tok, half, p.d);
+  const int half = p.rot / 2, ru = half / VEC, U = p.d / (2 * VEC), ln = deal.ln;
+  const uint32_t step = blockDim.x * 16, stage = 4 * KU * step;
+  const uint32_t ring = smem_u32(s_dyn) + threadIdx.x * 16;
+  const Shared sh(s_dyn + (VEC == 1 ? 0 : kGradStages * 4 * KU * blockDim.x), deal.tok, half);
   const int gl = threadIdx.x % ln;
-  const bool is_k = static_cast<int>(blockIdx.x) >= ctas_q;
-  const int rows = is_k ? p.Hkv : p.H, ctas = is_k ? gridDim.x - ctas_q : ctas_q;
-  const T* const px = static_cast<const T*>(is_k ? p.k : p.q);
-  const T* const py = static_cast<const T*>(is_k ? p.dyk : p.dyq);
-  T* const pd = static_cast<T*>(is_k ? p.k_out : p.q_out);
-  const int64_t x_token = is_k ? p.k_token : p.q_token, x_head = is_k ? p.k_head : p.q_head;
-  const int64_t y_token = is_k ? p.dyk_token : p.dyq_token, y_head = is_k ? p.dyk_head : p.dyq_head;
-  const int64_t d_token = is_k ? p.k_out_token : p.q_out_token;
-  const int64_t d_head = is_k ? p.k_out_head : p.q_out_head;
+  const Mine me(p, deal, p.H + p.Hkv);
+  const bool is_k = me.r >= p.H;
+  const int h = is_k ? me.r - p.H : me.r;
   int oa[KU], ob[KU], have = 0;
 #pragma unroll
   for (int k = 0; k < KU; ++k) {
     unit_at<VEC, HALF>(gl + k * ln, ru, half, oa[k], ob[k]);
-    if (gl + k * ln < U) have = k + 1;
+    if (me.on && gl + k * ln < U) have = k + 1;
   }
-  uint64_t da[N2], db[N2];  // the weight's gradient
+  const int64_t x_token = is_k ? p.k_token : p.q_token, y_token = is_k ? p.dyk_token : p.dyq_token;
+  const int64_t d_token = is_k ? p.k_out_token : p.q_out_token;
+  int64_t ahead = me.begin + me.tr;
+  const T* px = static_cast<const T*>(is_k ? p.k : p.q) + ahead * x_token +
+                h * (is_k ? p.k_head : p.q_head);
+  const T* py = static_cast<const T*>(is_k ? p.dyk : p.dyq) + ahead * y_token +
+                h * (is_k ? p.dyk_head : p.dyq_head);
+  T* dst = static_cast<T*>(is_k ? p.k_out : p.q_out) + ahead * d_token +
+           h * (is_k ? p.k_out_head : p.q_out_head);
+  uint32_t in = 0, out = 0;  // stages of the ring
+  auto fetch = [&] {
+    if (ahead < me.end) {
+      X::fetch(ring + in, step, px, oa, ob, have);
+      X::fetch(ring + in + 2 * KU * step, step, py, oa, ob, have);
+    }
+    copy_commit();
+    ahead += deal.per_round;
+    px += x_token * deal.per_round;
+    py += y_token * deal.per_round;
+    in = in == (kGradStages - 1) * stage ? 0 : in + stage;
+  };
+  if constexpr (VEC > 1) {
+#pragma unroll
+    for (int i = 0; i < kGradStages - 1; ++i) fetch();
+  }
+  uint64_t wA[N2], wB[N2], da[N2], db[N2];  // the weight and its gradient
+  weights_of<DT, VEC, KU, HALF>(p, is_k ? p.k_weight : p.q_weight, oa, ob, have, wA, wB);
 #pragma unroll
   for (int i = 0; i < N2; ++i) da[i] = db[i] = 0;
   const float inv_d = 1.f / p.d;
-  const float* const wt = sh.w + (is_k ? p.d : 0);
-  fill_fixed<DT, VEC, HALF>(p, sh);
-  const RowSteps steps(ln, rows, tok, static_cast<int64_t>(ctas) * tok);
-  const int64_t begin = static_cast<int64_t>(blockIdx.x - (is_k ? ctas_q : 0)) * tok;
-  RowWalk w, ahead;
-  steps.start(ahead, p, begin);
-  uint32_t in = 0, out = 0;  // rounds fetched and taken
-  auto fetch = [&] {
-    if (ahead.t0 < p.T) {
-      if (ahead.tk < ahead.tokens(p, tok)) {
-        const int64_t t = ahead.t0 + ahead.tk;
-        const uint32_t at = smem_u32(ring) + in % kStages * (kRing / kStages);
-        X::fetch(at, px + t * x_token + ahead.r * x_head, oa, ob, have);
-        X::fetch(at + 2 * KU * (kRopeThreads * 16), py + t * y_token + ahead.r * y_head, oa, ob, have);
-      }
-      if (!steps.next(ahead)) steps.start(ahead, p, ahead.t0 + steps.step);
-    }
-    copy_commit();
-    ++in;
-  };
-  if constexpr (VEC > 1) {
-#pragma unroll 1
-    for (int i = 0; i < kStages - 1; ++i) fetch();
-  }
-  for (int64_t t0 = begin; t0 < p.T; t0 += steps.step) {
-    steps.start(w, p, t0);
-    const int nt = w.tokens(p, tok);
-    if (threadIdx.x < nt * p.axes) {
-      const int a = threadIdx.x / nt, i = threadIdx.x - a * nt;
-      s_pos[a][i] = p.pos[a * p.T + t0 + i];
-    }
+  fill_fixed(p, sh);
+  for (int64_t t0 = me.begin; t0 < me.end; t0 += deal.tok) {
+    const int nt = static_cast<int>(min(static_cast<int64_t>(deal.tok), me.end - t0));
+    for (int i = threadIdx.x; i < nt * p.axes; i += blockDim.x)
+      s_pos[i / nt][i % nt] = p.pos[(i / nt) * p.T + t0 + i % nt];
     __syncthreads();  // also: the last batch's sines have been read
     fill_angles<VEC>(p, nt, sh, true, [&](int a, int i) { return s_pos[a][i]; });
     __syncthreads();
-    bool more = true;
-    while (more) {
-      const bool live = w.tk < nt;
-      T* const dst = pd + (t0 + w.tk) * d_token + w.r * d_head;
+    for (int tk = me.tr; tk - me.tr < nt; tk += deal.per_round) {
+      const bool live = me.on && tk < nt;
       X x, dy;
       if constexpr (VEC > 1) {
-        copy_wait<kStages - 2>();
-        const uint8_t* const at = ring + out++ % kStages * (kRing / kStages);
-        x.take(at, live ? have : 0);
-        dy.take(at + 2 * KU * (kRopeThreads * 16), live ? have : 0);
+        copy_wait<kGradStages - 2>();
+        x.take(ring + out, step, have);
+        dy.take(ring + out + 2 * KU * step, step, have);
+        out = out == (kGradStages - 1) * stage ? 0 : out + stage;
         fetch();
       } else {
         x.clear();
         dy.clear();
         if (live) {
-          x.load(px + (t0 + w.tk) * x_token + w.r * x_head, oa, ob, have);
-          dy.load(py + (t0 + w.tk) * y_token + w.r * y_head, oa, ob, have);
+          x.load(px, oa, ob, have);
+          dy.load(py, oa, ob, have);
         }
+        px += x_token * deal.per_round;
+        py += y_token * deal.per_round;
       }
       uint64_t A[N2], B[N2], gA[N2], gB[N2];
-      x.widen(A, B);
       dy.widen(gA, gB);
-      if (live) turn<VEC, N2>(gA, gB, sh.cs + w.tk * half, gl, ln, ru);
-      more = steps.next(w);
+      if (live) {
+        const uint64_t minus = f2(-1.f, -1.f);
+        uint64_t nB[N2];
+#pragma unroll
+        for (int i = 0; i < N2; ++i) nB[i] = f2_mul(gB[i], minus);
+        turn<VEC, N2>(gA, gB, nB, sh.cs + tk * half, gl, ln, ru);
+      }
+      x.widen(A, B);
       uint64_t ss2 = 0, sg2 = 0;
 #pragma unroll
       for (int i = 0; i < N2; ++i) {
-        uint64_t wa, wb;
-        pairs_of<VEC>(wt, i, gl, ln, U, wa, wb);
         ss2 = f2_fma(A[i], A[i], f2_fma(B[i], B[i], ss2));
-        sg2 = f2_fma(f2_mul(gA[i], A[i]), wa, f2_fma(f2_mul(gB[i], B[i]), wb, sg2));
+        sg2 = f2_fma(f2_mul(gA[i], wA[i]), A[i], f2_fma(f2_mul(gB[i], wB[i]), B[i], sg2));
       }
       const float ss = sum_lanes(f2_sum(ss2), ln), sg = sum_lanes(f2_sum(sg2), ln);
+      T* const to = dst;
+      dst += d_token * deal.per_round;
       if (!live) continue;
       const float rr = rsqrtf(fmaf(ss, inv_d, p.eps)), c = -rr * rr * rr * (sg * inv_d);
       const uint64_t rr2 = f2(rr, rr), c2 = f2(c, c);
 #pragma unroll
       for (int i = 0; i < N2; ++i) {
-        uint64_t wa, wb;
-        pairs_of<VEC>(wt, i, gl, ln, U, wa, wb);
         const uint64_t ga = f2_mul(gA[i], rr2), gb = f2_mul(gB[i], rr2);
         da[i] = f2_fma(ga, A[i], da[i]);
         db[i] = f2_fma(gb, B[i], db[i]);
-        A[i] = f2_fma(A[i], c2, f2_mul(ga, wa));
-        B[i] = f2_fma(B[i], c2, f2_mul(gb, wb));
+        A[i] = f2_fma(A[i], c2, f2_mul(ga, wA[i]));
+        B[i] = f2_fma(B[i], c2, f2_mul(gb, wB[i]));
       }
-      X::store(dst, oa, ob, have, A, B);
+      X::store(to, oa, ob, have, A, B);
     }
   }
   if (!p.part) return;
-  // the groups of a warp, then the warps
-  __shared__ float s_dw[kRopeThreads / 32][512];
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  // the CTA's groups, first those of q's heads and then those of k's, one after the other
+  copy_wait<0>();
+  __syncthreads();  // the ring becomes [groups][d]
+  float* const s_dw = reinterpret_cast<float*>(s_dyn);
+  const int g = threadIdx.x / ln;
 #pragma unroll
   for (int i = 0; i < N2; ++i) {
     float v[4];  // A, A of the next pair, B, B
@@ -679,41 +670,48 @@ __global__ void __launch_bounds__(kRopeThreads, VEC == 1 ? 1 : 2)
     f2_split(db[i], v[2], v[3]);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      for (int o = ln; o < 32; o *= 2) v[j] += __shfl_xor_sync(kAll, v[j], o);
       const int n = 2 * i + j % 2, k = n / VEC, e = n % VEC;
       const int at = HALF || VEC == 1 ? (j < 2 ? oa[k] : ob[k]) + e : oa[k] + 2 * e + j / 2;
-      if (lane < ln && k < have) s_dw[warp][at] = v[j];
+      if (k < have) s_dw[g * p.d + at] = v[j];
     }
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < p.d; i += kRopeThreads) {
+  const size_t cta = static_cast<size_t>(blockIdx.y) * gridDim.x + blockIdx.x;
+  for (int i = threadIdx.x; i < 2 * p.d; i += blockDim.x) {
+    const int kd = i >= p.d ? 1 : 0, c = i - kd * p.d;
+    const int first = blockIdx.y * deal.heads;
+    const int from = kd ? max(0, p.H - first) : 0;
+    const int to = kd ? min(deal.heads, p.H + p.Hkv - first) : min(deal.heads, p.H - first);
     float s = 0.f;
-#pragma unroll
-    for (int x = 0; x < kRopeThreads / 32; ++x) s += s_dw[x][i];
-    p.part[static_cast<size_t>(blockIdx.x) * p.d + i] = s;
+    for (int t = 0; t < deal.per_round; ++t)
+      for (int r = from; r < to; ++r) s += s_dw[(t * deal.heads + r) * p.d + c];
+    p.part[(cta * 2 + kd) * p.d + c] = s;
   }
 }
 
-// Column c of the CTAs' partial sums [ctas][d], the first ctas_q rows of q's weight, the others of
-// k's: 32 columns and 32 shares of the rows per CTA; blockIdx.y picks the weight.
+// Column c of the CTAs' partial sums [ctas][2][d]: 32 columns and 32 shares of the CTAs per CTA;
+// blockIdx.y picks the weight.
 __global__ void __launch_bounds__(1024)
-    norm_rope_sum_kernel(const float* part, int ctas, int ctas_q, int d, float* dq_weight,
-                         float* dk_weight) {
+    norm_rope_sum_kernel(const float* part, int ctas, int d, float* dq_weight, float* dk_weight) {
   __shared__ float s[32][33];
   float* const out = blockIdx.y ? dk_weight : dq_weight;
   if (!out) return;
   const int lane = threadIdx.x % 32, share = threadIdx.x / 32, c = blockIdx.x * 32 + lane;
-  const int from = blockIdx.y ? ctas_q : 0, to = blockIdx.y ? ctas : ctas_q;
-  float x = 0.f;
+  const float* const mine = part + static_cast<size_t>(blockIdx.y) * d + c;
+  float x[4] = {0.f, 0.f, 0.f, 0.f};
   if (c < d)
-    for (int i = from + share; i < to; i += 32) x += part[static_cast<size_t>(i) * d + c];
-  s[share][lane] = x;
-  __syncthreads();
-  x = s[lane][share];  // lane: share; share: column
+    for (int i = share; i < ctas; i += 128) {
 #pragma unroll
-  for (int o = 16; o > 0; o /= 2) x += __shfl_xor_sync(kAll, x, o);
+      for (int j = 0; j < 4; ++j)
+        if (i + 32 * j < ctas) x[j] += mine[static_cast<size_t>(i + 32 * j) * 2 * d];
+    }
+  s[share][lane] = (x[0] + x[1]) + (x[2] + x[3]);
+  __syncthreads();
+  float y = s[lane][share];  // lane: share; share: column
+#pragma unroll
+  for (int o = 16; o > 0; o /= 2) y += __shfl_xor_sync(kAll, y, o);
   const int col = blockIdx.x * 32 + share;
-  if (lane == 0 && col < d) out[col] = x;
+  if (lane == 0 && col < d) out[col] = y;
 }
 
 // Cached rows back as packed 16-bit ones: a CTA takes `tok` tokens, eight or four lanes a row of K
@@ -781,69 +779,66 @@ int lanes_of(int units, int ku) {
   return ln;
 }
 
-// Tokens of a batch: the least time, in rounds of a CTA's groups of lanes over rows. A CTA has a whole
-// number of batches, and a batch takes as many rounds as its rows need and about two for its angles
-// and barriers.
-constexpr int kMostShared = 81920;  // of the forward; the gradient's is at most twice that
-struct Share {  // rows of a token, and the CTAs that share the tokens
-  int rows, ctas;
+// The deal of `rows` heads of T tokens over at most `ctas` CTAs (per_sm of them per SM), with `ring`
+// bytes of rows on their way per thread.
+struct Launch {
+  Deal deal;
+  dim3 grid;
+  int threads, smem;
 };
-int tokens_of(const NormRopeParams& p, int ln, Share a, Share b) {
-  const int groups = kRopeThreads / ln;
-  int best = 1;
-  int64_t least = INT64_MAX;
-  for (int tok = 1; tok <= kTokMax; ++tok) {
-    if (tok > 1 && shared_bytes(tok, p.rot / 2, p.d) > 16384) break;
-    const int64_t batches = (p.T + tok - 1) / tok;
-    int64_t cost = 0;
-    for (const Share& s : {a, b})
-      if (s.rows)
-        cost = std::max(cost, (batches + s.ctas - 1) / s.ctas *
-                                  ((static_cast<int64_t>(s.rows) * tok + groups - 1) / groups + 2));
-    if (cost < least) {
-      least = cost;
-      best = tok;
-    }
-  }
-  return best;
+Launch deal_rows(const NormRopeParams& p, int ln, int rows, int ctas, int ring) {
+  Launch L;
+  Deal& d = L.deal;
+  d.ln = ln;
+  // all heads of a token side by side, or several equal shares of them; several tokens of few heads
+  const int chunks = (rows * ln + kMostThreads - 1) / kMostThreads;
+  d.heads = (rows + chunks - 1) / chunks;
+  d.per_round = std::max(1, 256 / (d.heads * ln));
+  d.per_round = static_cast<int>(std::min<int64_t>({d.per_round, p.T, kTokMax}));
+  L.threads = (d.per_round * d.heads * ln + 31) / 32 * 32;
+  const int64_t runs = (p.T + d.per_round - 1) / d.per_round;  // rounds of all tokens
+  L.grid = dim3(static_cast<unsigned>(std::min<int64_t>(runs, std::max(1, ctas / chunks))), chunks);
+  // the sines of a batch within 12 KB; no more than the CTA's own tokens
+  const int64_t own = (p.T + L.grid.x - 1) / L.grid.x;
+  int64_t tok = std::min<int64_t>({kTokMax, 12288 / (p.rot / 2 * 8),
+                                   (own + d.per_round - 1) / d.per_round * d.per_round});
+  d.tok = static_cast<int>(std::max<int64_t>(1, tok / d.per_round)) * d.per_round;
+  L.smem = shared_bytes(d.tok, p.rot / 2) + ring * L.threads;
+  return L;
 }
+constexpr int kMostShared = 16384 + kTokMax * 256 * 8;  // beside the ring
 
 template <int DT, int VEC, int KU, int MODE>
 cudaError_t launch_v(const NormRopeParams& p, bool half_style, int sms, cudaStream_t stream) {
-  const int ln = lanes_of(p.d / (2 * VEC), KU), rows = p.H + (MODE ? 2 : 1) * p.Hkv;
-  const int tok = tokens_of(p, ln, Share{rows, 4 * sms}, Share{0, 1});
-  const int smem = static_cast<int>(shared_bytes(tok, p.rot / 2, p.d)) + ring_bytes<VEC>(2 * KU);
-  const int64_t grid = std::min<int64_t>((p.T + tok - 1) / tok, 4 * sms);
+  constexpr int ring = VEC == 1 ? 0 : kStages * 2 * KU * 16;
+  constexpr int most = kMostShared + ring * kMostThreads;
+  const Launch L = deal_rows(p, lanes_of(p.d / (2 * VEC), KU), p.H + (MODE ? 2 : 1) * p.Hkv,
+                             (DT != FA_F32 && VEC > 1 ? 3 : 2) * sms, ring);
   auto* k = half_style ? norm_rope_kernel<DT, VEC, KU, true, MODE>
                        : norm_rope_kernel<DT, VEC, KU, false, MODE>;
-  const cudaError_t e = half_style ? prepare_kernel<norm_rope_kernel<DT, VEC, KU, true, MODE>>(kMostShared)
-                                   : prepare_kernel<norm_rope_kernel<DT, VEC, KU, false, MODE>>(kMostShared);
+  const cudaError_t e = half_style ? prepare_kernel<norm_rope_kernel<DT, VEC, KU, true, MODE>>(most)
+                                   : prepare_kernel<norm_rope_kernel<DT, VEC, KU, false, MODE>>(most);
   if (e != cudaSuccess) return e;
-  k<<<static_cast<unsigned>(grid), kRopeThreads, smem, stream>>>(p, tok, ln);
+  k<<<L.grid, L.threads, L.smem, stream>>>(p, L.deal);
   return cudaGetLastError();
 }
 template <int DT, int VEC, int KU>
 cudaError_t launch_bwd_v(const NormRopeParams& p, bool half_style, int sms, cudaStream_t stream) {
-  const int ln = lanes_of(p.d / (2 * VEC), KU);
-  // CTAs of q and k by their heads, at least one each
-  const int most = std::min(2 * sms, kNormCtas);
-  int ctas_k = p.Hkv ? std::max<int>(1, static_cast<int64_t>(most) * p.Hkv / (p.H + p.Hkv)) : 0;
-  int ctas_q = most - ctas_k;
-  const int tok = tokens_of(p, ln, Share{p.H, ctas_q}, Share{p.Hkv, ctas_k});
-  const int smem = static_cast<int>(shared_bytes(tok, p.rot / 2, p.d)) + ring_bytes<VEC>(4 * KU);
-  const int64_t batches = (p.T + tok - 1) / tok;
-  ctas_q = static_cast<int>(std::min<int64_t>(ctas_q, batches));
-  ctas_k = static_cast<int>(std::min<int64_t>(ctas_k, batches));
+  constexpr int ring = VEC == 1 ? 0 : kGradStages * 4 * KU * 16;
+  constexpr int most = kMostShared + ring * kMostThreads;
+  Launch L = deal_rows(p, lanes_of(p.d / (2 * VEC), KU), p.H + p.Hkv, std::min(2 * sms, kNormCtas), ring);
+  // the weights' gradients of its groups meet in the ring's place
+  L.smem = std::max(L.smem, L.deal.per_round * L.deal.heads * p.d * 4);
   auto* k = half_style ? norm_rope_bwd_kernel<DT, VEC, KU, true>
                        : norm_rope_bwd_kernel<DT, VEC, KU, false>;
-  cudaError_t e = half_style ? prepare_kernel<norm_rope_bwd_kernel<DT, VEC, KU, true>>(2 * kMostShared)
-                             : prepare_kernel<norm_rope_bwd_kernel<DT, VEC, KU, false>>(2 * kMostShared);
+  cudaError_t e = half_style ? prepare_kernel<norm_rope_bwd_kernel<DT, VEC, KU, true>>(most)
+                             : prepare_kernel<norm_rope_bwd_kernel<DT, VEC, KU, false>>(most);
   if (e != cudaSuccess) return e;
-  k<<<ctas_q + ctas_k, kRopeThreads, smem, stream>>>(p, tok, ln, ctas_q);
+  k<<<L.grid, L.threads, L.smem, stream>>>(p, L.deal);
   e = cudaGetLastError();
   if (e != cudaSuccess || !p.part) return e;
   norm_rope_sum_kernel<<<dim3((p.d + 31) / 32, 2), 1024, 0, stream>>>(
-      p.part, ctas_q + ctas_k, ctas_q, p.d, p.dq_weight, p.dk_weight);
+      p.part, static_cast<int>(L.grid.x * L.grid.y), p.d, p.dq_weight, p.dk_weight);
   return cudaGetLastError();
 }
 

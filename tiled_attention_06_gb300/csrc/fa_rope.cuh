@@ -77,7 +77,7 @@ __device__ __forceinline__ void sequences_of(const int32_t* cu, int B, int T, ui
                                              int64_t t0, int nt, int* s_seq) {
   if (threadIdx.x < nt) s_seq[threadIdx.x] = kNobody;
   __syncthreads();
-  for (int b = threadIdx.x; b < B; b += kRopeThreads) {
+  for (int b = threadIdx.x; b < B; b += blockDim.x) {
     const SeqRows r = rows_of(cu, b, T);
     if (r.bad && blockIdx.x == 0) atomicOr(status, FA_DEV_BAD_PAGE);
     const int64_t end = static_cast<int64_t>(r.first) + r.n;

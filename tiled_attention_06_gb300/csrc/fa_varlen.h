@@ -88,12 +88,13 @@ struct NormRopeParams {
   const void* dyq;
   const void* dyk;
   int64_t dyq_token, dyq_head, dyk_token, dyk_head;
-  float* part;  // [CTAs][d] sums of the weights' gradients, or nullptr
+  float* part;  // [CTAs][2][d] sums of the weights' gradients, or nullptr
   float* dq_weight;
   float* dk_weight;
   uint32_t* status;
 };
-constexpr int kNormCtas = 320;  // CTAs of the gradient at most
+constexpr int kNormCtas = 320;  // CTAs of the gradient at most, unless a token's heads need more
+inline int norm_parts(int rows) { return rows / 8 > kNormCtas ? rows / 8 : kNormCtas; }
 cudaError_t launch_norm_rope(const NormRopeParams& p, int dtype, bool half_style, bool vec,
                              int sms, cudaStream_t stream);
 cudaError_t launch_norm_rope_bwd(const NormRopeParams& p, int dtype, bool half_style, bool vec,
