@@ -16,7 +16,8 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libfa.so")
 SOURCES = ["fa_api.cu", "fa_prefill.cu", "fa_prefill_split.cu", "fa_decode.cu", "fa_merge.cu",
            "fa_cache.cu", "fa_backward.cu", "fa_api_varlen.cu", "fa_rope.cu", "fa_varlen.cu",
-           "fa_varlen_bwd.cu", "fa_few.cu", "fa_norm_rope.cu", "fa_api_norm.cu"]
+           "fa_varlen_bwd.cu", "fa_few.cu", "fa_few8.cu",
+           "fa_norm_rope.cu", "fa_api_norm.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -572,9 +572,11 @@ static fa_status paged_varlen(const fa_paged_varlen_params& a, const fa_paged_va
     p.page_size = a.page_size;
     p.max_pages = a.max_pages_per_seq;
     p.num_pages = a.num_pages;
-    p.box = std::min(64, pow2);
+    p.box = std::min(q8 ? fa::kFew8Tile : 64, pow2);
     p.heads = static_cast<fa::FewHead*>(a.workspace);
-    p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + fa::kFewHeadBytes);
+    const bool more = q8 && a.max_q * p.G <= 8;  // CTAs
+    p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) +
+                                      (more ? fa::kFew8HeadBytes : fa::kFewHeadBytes));
     p.k_scales = x.k_scales;
     p.v_scales = x.v_scales;
     p.tree = x.tree;
@@ -590,7 +592,7 @@ static fa_status paged_varlen(const fa_paged_varlen_params& a, const fa_paged_va
                                p.box, 1)) != FA_OK) {
       return st;
     }
-    const cudaError_t e = fa::launch_few(F, a.d, bf16, cs);
+    const cudaError_t e = q8 ? fa::launch_few8(F, a.d, bf16, cs) : fa::launch_few(F, a.d, bf16, cs);
     if (e != cudaSuccess) return cuda_fail(e, "paged packed attention launch");
     return FA_OK;
   }

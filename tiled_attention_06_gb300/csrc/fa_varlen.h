@@ -267,7 +267,7 @@ struct FewParams {
   const uint32_t* tree;  // FA_MASK_TREE: [total_q][tree_words]
   int tree_words;
   FewHead* heads;  // [CTAs]
-  float* part;  // [2 CTAs][16 rows][D], then m [2 CTAs][16], l [2 CTAs][16]
+  float* part;  // [2 CTAs][16 rows][D], then m [2 CTAs][16], l [2 CTAs][16] (or 8 rows: fa_few8.cu)
 };
 
 struct FewLaunch {
@@ -276,5 +276,17 @@ struct FewLaunch {
   int sms;
 };
 cudaError_t launch_few(const FewLaunch& L, int D, bool bf16, cudaStream_t stream);
+// The same over an 8-bit cache (fa_few8.cu). With at most 8 rows it has more CTAs, whose pieces have 8
+// rows each and fit in the same workspace.
+constexpr int kFew8MaxCtas = 480;
+constexpr int kFew8Blocks = 1;                // blocks of 16 keys of a warp
+constexpr int kFew8Tile = 64 * kFew8Blocks;   // keys of a tile
+constexpr size_t kFew8HeadBytes = kFew8MaxCtas * sizeof(FewHead);
+static_assert(kFew8HeadBytes + 2 * kFew8MaxCtas * 8 * (64 + 2) * 4 <=
+                  kFewHeadBytes + 2 * kFewMaxCtas * kFewRows * (64 + 2) * 4 &&
+              kFew8HeadBytes + 2 * kFew8MaxCtas * 8 * (128 + 2) * 4 <=
+                  kFewHeadBytes + 2 * kFewMaxCtas * kFewRows * (128 + 2) * 4,
+              "over the workspace");
+cudaError_t launch_few8(const FewLaunch& L, int D, bool bf16, cudaStream_t stream);
 
 }  // namespace fa
