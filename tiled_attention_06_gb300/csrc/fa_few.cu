@@ -82,7 +82,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     tma_prefetch_desc(&tmK);
     tma_prefetch_desc(&tmV);
   }
-  const Totals tot = tile_totals<BK, TREE>(p, bars->sum);
+  const Totals tot = tile_totals<BK, TREE, 0>(p, bars->sum);
   const int64_t all = tot.all * p.Hkv;
   const int used = ctas_used(all, gridDim.x);
   const bool idle = static_cast<int>(blockIdx.x) >= used || all == 0;
@@ -457,7 +457,7 @@ cudaError_t launch_t(const FewLaunch& L, cudaStream_t stream) {
   k<<<grid, kThreads, smem, stream>>>(L.tmK, L.tmV, L.p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   const int rows = L.p.max_q * L.p.G;
-  few_merge_kernel<D, BF16, ROWS>
+  few_merge_kernel<D, BF16, ROWS, false>
       <<<dim3(grid, rows < 1 ? 1 : rows), kCompute, 0, stream>>>(L.p);
   return cudaGetLastError();
 }

@@ -92,12 +92,13 @@ __device__ __forceinline__ int tile_at(const Range& r, int j) {
   return j < r.a_end ? j : r.b_start + (j - r.a_end);
 }
 
-// Sums over the CTA's first 128 threads of each thread's contiguous share of the sequences.
+// Sums over the CTA's first 128 threads of each thread's contiguous share of the sequences, of units:
+// a sequence's tiles and, where it has any, EXTRA more.
 struct Totals {
-  int64_t before, mine, all;  // tiles before this thread's share, in it, of every sequence
+  int64_t before, mine, all;  // units before this thread's share, in it, of every sequence
   int b0, b1;                 // the share
 };
-template <int BK, bool TREE>
+template <int BK, bool TREE, int EXTRA>
 __device__ __forceinline__ Totals tile_totals(const FewParams& p, int64_t* scratch) {
   Totals t{0, 0, 0, 0, 0};
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
@@ -106,7 +107,10 @@ __device__ __forceinline__ Totals tile_totals(const FewParams& p, int64_t* scrat
     const int per = (p.B + kCompute - 1) / kCompute;
     t.b0 = min(p.B, tid * per);
     t.b1 = min(p.B, t.b0 + per);
-    for (int b = t.b0; b < t.b1; ++b) x += few_seq<BK, TREE>(p, b, blockIdx.x == 0).tiles;
+    for (int b = t.b0; b < t.b1; ++b) {
+      const int tiles = few_seq<BK, TREE>(p, b, blockIdx.x == 0).tiles;
+      x += EXTRA && tiles ? tiles + EXTRA : tiles;
+    }
     t.mine = x;
     for (int o = 1; o < 32; o *= 2) {
       const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
@@ -147,8 +151,10 @@ __device__ __forceinline__ uint32_t tree_bits(const uint32_t* row, int words, in
 // CTA (x, y): row y of the pair whose first piece CTA x of few_kernel holds. A warp's lanes hold
 // the pieces' maxima and sums, so the weights are known before the outputs are read; the four
 // warps take every fourth piece.
-template <int D, bool BF16, int ROWS>
+// EARLY: launched while the kernel before it runs (programmatic stream serialization), it waits here.
+template <int D, bool BF16, int ROWS, bool EARLY>
 __global__ void __launch_bounds__(kCompute) few_merge_kernel(const FewParams p) {
+  if constexpr (EARLY) asm volatile("griddepcontrol.wait;" ::: "memory");
   constexpr int E = D / 32;
   __shared__ float s_acc[4][D];
   const int x0 = blockIdx.x, nslots = 2 * gridDim.x, r = blockIdx.y;

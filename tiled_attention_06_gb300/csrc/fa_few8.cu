@@ -26,6 +26,12 @@
 namespace fa {
 namespace {
 
+// What a segment costs beside its tiles (q, the join of the warps, the output), in tiles: CTAs get equal
+// runs of units, and the first kSegment of a (sequence, K/V head) pair's have no tile. Dealt by tiles
+// alone, CTAs with many short sequences kept the others waiting (SMs were busy 68 % of the time:
+// SEGFIG).
+constexpr int kSegment = 2;
+
 // NB: blocks of 8 rows. BK: keys of a tile, of which a warp takes a quarter.
 template <int D, int NB>
 struct Cfg {
@@ -38,11 +44,12 @@ struct Cfg {
   static constexpr int OROW = D + 4;              // floats of an output row in shared memory
   static constexpr int COMB = 2 * ROWS * OROW * 4;  // two warps' outputs
   static constexpr int STATES = 2 * ROWS * 2 * 4;   // their (m, l)
+  static constexpr int MULS = 2 * BK;               // V's multipliers, FP16
   static constexpr int BARS = 256;
   static constexpr int BUDGET = 233472 / CTAS - 1024;  // 1 KB taken per CTA
-  static constexpr int FIT = (BUDGET - COMB - STATES - BARS) / (2 * TILE + SCALES);
+  static constexpr int FIT = (BUDGET - COMB - STATES - MULS - BARS) / (2 * TILE + SCALES);
   static constexpr int NST = FIT > 8 ? 8 : FIT;
-  static constexpr int SMEM = NST * (2 * TILE + SCALES) + COMB + STATES + BARS;
+  static constexpr int SMEM = NST * (2 * TILE + SCALES) + COMB + STATES + MULS + BARS;
   static_assert(NST >= 2, "too few stages");
 };
 
@@ -64,26 +71,24 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(x));
   return d;
 }
-// 2^(b - 127) of an exponent byte, NaN for 255 (0 for 0: 2^-127 of a row that small)
-__device__ __forceinline__ float power8(uint32_t b) {
-  return __uint_as_float(b == 255 ? 0x7fffffffu : b << 23);
-}
-// Multiplier of V's elements of a key: its power over the running one, 0 when the key is dead.
-__device__ __forceinline__ float relative8(int b, int ref, bool live) {
-  const int e = b - ref + 127;
-  return !live ? 0.f
-               : __uint_as_float(b == 255 ? 0x7fffffffu
-                                          : e <= 0 ? 0u : static_cast<uint32_t>(e) << 23);
+// 2^(b - 127) of an exponent byte: an infinity for 255, 0 for 0 (2^-127, of a row that small).
+__device__ __forceinline__ float power8(uint32_t b) { return __uint_as_float(b << 23); }
+// 2^(b - ref), 0 below 2^-126
+__device__ __forceinline__ float relative8(int b, int ref) {
+  return __uint_as_float(static_cast<uint32_t>(max(b - ref + 127, 0)) << 23);
 }
 __device__ __forceinline__ uint32_t load_u8(uint32_t addr) {
   uint32_t x;
   asm volatile("ld.shared.u8 %0, [%1];" : "=r"(x) : "r"(addr) : "memory");
   return x;
 }
-__device__ __forceinline__ uint32_t load_u16(uint32_t addr) {
-  uint16_t x;
-  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(addr) : "memory");
+__device__ __forceinline__ uint32_t load_u32(uint32_t addr) {
+  uint32_t x;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(x) : "r"(addr) : "memory");
   return x;
+}
+__device__ __forceinline__ void store_u16(uint32_t addr, uint32_t x) {
+  asm volatile("st.shared.u16 [%0], %1;" ::"r"(addr), "h"(static_cast<uint16_t>(x)) : "memory");
 }
 // `bytes` (a multiple of 16) from global to shared memory, counted on `bar`.
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
@@ -107,9 +112,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::CTAS)
   const uint32_t sScales = base + C::NST * 2 * C::TILE;  // K's, then V's of a stage
   float* comb = reinterpret_cast<float*>(smem + kBehind);
   float* states = reinterpret_cast<float*>(smem + kBehind + C::COMB);
-  Bars* bars = reinterpret_cast<Bars*>(smem + kBehind + C::COMB + C::STATES);
+  const uint32_t sMuls = base + kBehind + C::COMB + C::STATES;
+  Bars* bars = reinterpret_cast<Bars*>(smem + kBehind + C::COMB + C::STATES + C::MULS);
   auto B = [&](uint64_t& x) { return smem_u32(&x); };
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the joining kernel may come up
   // whatever ends this CTA early, the joining kernel finds no piece of it
   if (threadIdx.x == 0) p.heads[blockIdx.x] = FewHead{0, 0, 0, 0};
   if (base & 1023u) {  // the swizzle needs the stages on 1024-byte boundaries
@@ -128,7 +135,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::CTAS)
     tma_prefetch_desc(&tmK);
     tma_prefetch_desc(&tmV);
   }
-  const Totals tot = tile_totals<BK, true>(p, bars->sum);
+  const Totals tot = tile_totals<BK, true, kSegment>(p, bars->sum);
   const int64_t all = tot.all * p.Hkv;
   const int used = ctas_used(all, gridDim.x);
   const bool idle = static_cast<int>(blockIdx.x) >= used || all == 0;
@@ -143,7 +150,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::CTAS)
       begin < (tot.before + tot.mine) * p.Hkv) {
     int64_t at = tot.before * p.Hkv;
     for (int b = tot.b0; b < tot.b1; ++b) {
-      const int64_t n = static_cast<int64_t>(few_seq<BK, true>(p, b, false).tiles) * p.Hkv;
+      const int tiles = few_seq<BK, true>(p, b, false).tiles;
+      const int64_t n = tiles ? static_cast<int64_t>(tiles + kSegment) * p.Hkv : 0;
       if (begin < at + n) {
         bars->first[0] = b;
         bars->first[1] = static_cast<int>(begin - at);
@@ -168,18 +176,24 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::CTAS)
   Walk w;
   w.b = bars->first[0];
   w.s = few_seq<BK, true>(p, w.b, false);
-  w.kvh = bars->first[1] / w.s.tiles;
-  w.j = bars->first[1] - w.kvh * w.s.tiles;
-  w.left = static_cast<int>(end - begin);
-  // step to the segment after one of `done` tiles
-  auto advance = [&](int done) {
-    w.left -= done;
+  w.kvh = bars->first[1] / (w.s.tiles + kSegment);
+  w.j = bars->first[1] - w.kvh * (w.s.tiles + kSegment);  // first unit of the pair
+  w.left = static_cast<int>(end - begin);                 // units
+  // the tiles [j0, j0 + cnt) of the run in the present pair
+  int j0, cnt, take;
+  auto segment = [&] {
+    take = min(w.left, w.s.tiles + kSegment - w.j);
+    j0 = max(w.j - kSegment, 0);
+    cnt = max(w.j + take - kSegment, 0) - j0;
+  };
+  auto advance = [&] {  // to the next pair
+    w.left -= take;
     w.j = 0;
     if (++w.kvh < p.Hkv || w.left <= 0) return;
     w.kvh = 0;
     do {
       w.s = few_seq<BK, true>(p, ++w.b, false);
-    } while (w.s.tiles == 0);  // ends: `left` tiles lie ahead
+    } while (w.s.tiles == 0);  // ends: `left` units lie ahead
   };
   const WaitCtx wc{&bars->abort, p.m.status, p.m.timeout_ns};
 
@@ -192,8 +206,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::CTAS)
     uint32_t pos = 0, fills[8] = {0, 0, 0, 0, 0, 0, 0, 0};
     bool ok = true;
     while (w.left > 0 && ok) {
-      const int cnt = min(w.left, w.s.tiles - w.j);
-      for (int j = w.j; j < w.j + cnt && ok; ++j, ++pos) {
+      segment();
+      for (int j = j0; j < j0 + cnt && ok; ++j, ++pos) {
         const int n0 = tile_at(w.s.rg, j) * BK;
         const int boxes = (min(BK, w.s.sk - n0) + p.box - 1) / p.box;
         int y = 0, z = 0;
@@ -222,7 +236,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::CTAS)
         __syncwarp();
         fills[st] = use + 1;
       }
-      advance(cnt);
+      advance();
     }
     if (!ok) {  // every load issued lands before the CTA exits
       volatile uint32_t zero = 0;
@@ -239,7 +253,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::CTAS)
   uint32_t pos = 0;
   bool ok = true;
   while (w.left > 0) {
-    const int cnt = min(w.left, w.s.tiles - w.j);
+    segment();
+    if (cnt == 0) {
+      advance();
+      continue;
+    }
     const int rows = w.s.n * p.G;
     // Q fragments straight from global memory (rows past the chunk are zero): row gq of a block,
     // channels 4 cq .. 4 cq + 3 of every 16
@@ -288,6 +306,28 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::CTAS)
         tok[b][e] = (8 * b + 2 * cq + e) / p.G;
       }
     }
+    // tiles that every row sees whole start at most at full_to, and at least at full_from or at
+    // most at full_global
+    int full_to = w.s.sk - BK, full_from = 0, full_global = INT_MIN;
+    {
+      const int first = w.s.qpos, last = w.s.qpos + w.s.n - 1;
+      if (p.m.mask_mode == FA_MASK_CAUSAL || p.m.mask_mode == FA_MASK_CAUSAL_WINDOW)
+        full_to = min(full_to, first - BK + 1);
+      if (p.m.mask_mode == FA_MASK_CAUSAL_WINDOW) {
+        full_from = last - p.m.window + 1;
+        // behind the global keys; or the global keys reach the window
+        if (full_from <= p.m.n_global) full_from = 0;
+        full_global = p.m.n_global - BK;
+      }
+      if (p.m.mask_mode == FA_MASK_BAND) {
+        const long long to = static_cast<long long>(first) + p.m.window - BK + 1;
+        full_to = static_cast<int>(min(static_cast<long long>(full_to), to));
+        full_from = last - p.m.window;
+      }
+      if (p.m.mask_mode == FA_MASK_PREFIX_LM)
+        full_to = min(full_to, max(first - BK + 1, p.m.n_global - BK));
+      if (p.m.mask_mode == FA_MASK_TREE) full_to = min(full_to, first - BK);
+    }
     int ref = 0;  // exponent byte of the running power of V
     float m[NB][2], l[NB][2], o[NB][CH][4];
 #pragma unroll
@@ -302,7 +342,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::CTAS)
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[b][c][e] = 0.f;
     }
-    for (int j = w.j; j < w.j + cnt; ++j, ++pos) {
+    for (int j = j0; j < j0 + cnt; ++j, ++pos) {
       const int n0 = tile_at(w.s.rg, j) * BK;
       const int st = pos % C::NST;
       // a warp that gives up still meets the others at the joins (its results are void)
@@ -334,33 +374,25 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::CTAS)
               mma<false>(half[b][h], a, qf[b][c + h][0], qf[b][c + h][1]);
           }
         }
+        // an infinite power (of 255) makes the score NaN: f - f is
         const float f0 = power8(load_u8(sc + 16 * mb + gq)), f1 = power8(load_u8(sc + 16 * mb + gq + 8));
+        const float z0 = f0 - f0, z1 = f1 - f1;
 #pragma unroll
         for (int b = 0; b < NB; ++b)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float f = e < 2 ? f0 : f1;
-            s[b][mb][e] = (half[b][0][e] + half[b][1][e]) * (BF16 ? f * qs[b][e % 2] : f);
+            const float x = half[b][0][e] + half[b][1][e];
+            s[b][mb][e] = fmaf(BF16 ? x * qs[b][e % 2] : x, e < 2 ? f0 : f1, e < 2 ? z0 : z1);
           }
       }
-      // V's powers: the running one covers the warp's keys (lanes 0-3 of a quad hold them all)
-      uint32_t vb[MB][2], mv[MB][2];
-      int big = 0;
-#pragma unroll
-      for (int mb = 0; mb < MB; ++mb)
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          vb[mb][t] = load_u16(sc + BK + 16 * mb + 8 * t + 2 * cq);
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int x = (vb[mb][t] >> (8 * e)) & 255;
-            if (x != 255 && kw * KPW + 16 * mb + 8 * t + 2 * cq + e < live) big = max(big, x);
-          }
-        }
-      big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
-      big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
+      // V's powers, a key to a lane: the running one covers the warp's keys, and the multipliers go
+      // round by way of shared memory
+      const int mine = lane % KPW, vb = static_cast<int>(load_u8(sc + BK + mine));
+      const bool dead = kw * KPW + mine >= live;
+      const int big = static_cast<int>(
+          __reduce_max_sync(0xffffffffu, dead || vb == 255 ? 0u : static_cast<uint32_t>(vb)));
       if (big > ref + 7) {  // the same for the whole warp
-        const float a = ref ? relative8(ref, big, true) : 0.f;
+        const float a = ref ? relative8(ref, big) : 0.f;
         ref = big;
 #pragma unroll
         for (int b = 0; b < NB; ++b)
@@ -369,30 +401,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::CTAS)
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[b][c][e] *= a;
       }
-#pragma unroll
-      for (int mb = 0; mb < MB; ++mb)
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          const int key = kw * KPW + 16 * mb + 8 * t + 2 * cq;
-          mv[mb][t] = cvt_pack_f16(relative8(vb[mb][t] & 255, ref, key < live),
-                                   relative8(vb[mb][t] >> 8, ref, key + 1 < live));
-        }
-      // hidden keys to -inf where some row does not see the whole tile
-      const int lo_pos = w.s.qpos, hi_pos = w.s.qpos + w.s.n - 1;
-      bool full = n0 + BK <= w.s.sk;
-      if (p.m.mask_mode != FA_MASK_NONE) {
-        if (p.m.mask_mode == FA_MASK_CAUSAL || p.m.mask_mode == FA_MASK_CAUSAL_WINDOW)
-          full = full && n0 + BK - 1 <= lo_pos;
-        if (p.m.mask_mode == FA_MASK_CAUSAL_WINDOW)
-          full = full && (n0 + BK <= p.m.n_global || hi_pos - max(n0, p.m.n_global) < p.m.window);
-        if (p.m.mask_mode == FA_MASK_BAND)
-          full = full && static_cast<long long>(hi_pos) - n0 <= p.m.window &&
-                 static_cast<long long>(n0 + BK - 1) - lo_pos <= p.m.window;
-        if (p.m.mask_mode == FA_MASK_PREFIX_LM)
-          full = full && (n0 + BK <= p.m.n_global || n0 + BK - 1 <= lo_pos);
-        if (p.m.mask_mode == FA_MASK_TREE) full = full && n0 + BK <= lo_pos;
+      {
+        const uint32_t x = cvt_pack_f16(relative8(vb, ref), 0.f);
+        store_u16(sMuls + 2 * (kw * KPW + mine), dead ? 0u : vb == 255 ? 0x7fffu : x);
+        __syncwarp();
       }
-      if (!full) {
+      // hidden keys to -inf where some row does not see the whole tile
+      if (n0 > full_to || (n0 < full_from && n0 > full_global)) {
 #pragma unroll 1
         for (int b = 0; b < NB; ++b)
 #pragma unroll
@@ -428,8 +443,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::CTAS)
             for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
               for (int t = 0; t < 2; ++t) {
-                const int mine = 16 * mb + 8 * t + gq, key = kw * KPW + mine;
-                const bool sees = key <= lim && (key >= lo || key < gl) && ((seen >> mine) & 1);
+                const int own = 16 * mb + 8 * t + gq, key = kw * KPW + own;
+                const bool sees = key <= lim && (key >= lo || key < gl) && ((seen >> own) & 1);
 #pragma unroll
                 for (int bb = 0; bb < NB; ++bb)
                   if (bb == b && !sees) s[bb][mb][2 * t + i] = -INFINITY;
@@ -497,6 +512,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::CTAS)
 #pragma unroll
       for (int mb = 0; mb < MB; ++mb) {
         const int key = kw * KPW + 16 * mb + ((lane / 8) % 2) * 8 + lane % 8;
+        const uint32_t mv[2] = {load_u32(sMuls + 2 * (kw * KPW + 16 * mb + 2 * cq)),
+                                load_u32(sMuls + 2 * (kw * KPW + 16 * mb + 8 + 2 * cq))};
 #pragma unroll
         for (int c = 0; c < CH; c += 2) {
           const int ch = c + lane / 16;
@@ -506,8 +523,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::CTAS)
           for (int i = 0; i < 4; ++i) {  // (key, channel) pairs side by side to keys side by side
             uint32_t lo, hi;
             cvt8(__byte_perm(vf[i], 0, 0x3120), lo, hi);
-            a[i / 2][2 * (i % 2)] = hmul2(lo, mv[mb][i % 2]);
-            a[i / 2][2 * (i % 2) + 1] = hmul2(hi, mv[mb][i % 2]);
+            a[i / 2][2 * (i % 2)] = hmul2(lo, mv[i % 2]);
+            a[i / 2][2 * (i % 2) + 1] = hmul2(hi, mv[i % 2]);
           }
 #pragma unroll
           for (int h = 0; h < 2; ++h)
@@ -578,14 +595,14 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::CTAS)
       compute_sync();
     }
     if (kw == 0) {
-      const bool whole = w.j == 0 && cnt == w.s.tiles;
+      const bool whole = j0 == 0 && cnt == w.s.tiles;
       // a piece that starts its pair goes to slot 2x + 1, one that continues it to slot 2x
-      const int slot = 2 * blockIdx.x + (w.j == 0 ? 1 : 0);
+      const int slot = 2 * blockIdx.x + (j0 == 0 ? 1 : 0);
       const int nslots = 2 * gridDim.x;
-      if (!whole && w.j == 0 && threadIdx.x == 0) {
-        // the piece that starts a pair says where the rest is: CTAs on to that of its last tile
+      if (!whole && j0 == 0 && threadIdx.x == 0) {
+        // the piece that starts a pair says where the rest is: CTAs on to that of its last unit
         const int64_t n = bars->all, own_end = n * (blockIdx.x + 1) / bars->used;
-        const int64_t last = own_end - w.left + w.s.tiles - 1;
+        const int64_t last = own_end - w.left + (w.s.tiles + kSegment - w.j) - 1;
         int x = blockIdx.x + 1;
         while (n * (x + 1) / bars->used <= last) ++x;
         p.heads[blockIdx.x] = FewHead{w.s.q0, rows, w.kvh, x};
@@ -622,7 +639,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::CTAS)
           }
         }
     }
-    advance(cnt);
+    advance();
   }
 }
 
@@ -636,9 +653,16 @@ cudaError_t launch_t(const FewLaunch& L, cudaStream_t stream) {
   few8_kernel<D, BF16, NB><<<grid, kThreads, C::SMEM, stream>>>(L.tmK, L.tmV, L.p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   const int rows = L.p.max_q * L.p.G;
-  few_merge_kernel<D, BF16, C::ROWS>
-      <<<dim3(grid, rows < 1 ? 1 : rows), kCompute, 0, stream>>>(L.p);
-  return cudaGetLastError();
+  cudaLaunchAttribute early;
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid, rows < 1 ? 1 : rows);
+  cfg.blockDim = dim3(kCompute);
+  cfg.stream = stream;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, few_merge_kernel<D, BF16, C::ROWS, true>, L.p);
 }
 template <int D, bool BF16>
 cudaError_t launch_rows(const FewLaunch& L, cudaStream_t stream) {

@@ -279,7 +279,7 @@ cudaError_t launch_few(const FewLaunch& L, int D, bool bf16, cudaStream_t stream
 // The same over an 8-bit cache (fa_few8.cu). With at most 8 rows it has more CTAs, whose pieces have 8
 // rows each and fit in the same workspace.
 constexpr int kFew8MaxCtas = 480;
-constexpr int kFew8Blocks = 1;                // blocks of 16 keys of a warp
+constexpr int kFew8Blocks = 2;                // blocks of 16 keys of a warp
 constexpr int kFew8Tile = 64 * kFew8Blocks;   // keys of a tile
 constexpr size_t kFew8HeadBytes = kFew8MaxCtas * sizeof(FewHead);
 static_assert(kFew8HeadBytes + 2 * kFew8MaxCtas * 8 * (64 + 2) * 4 <=
