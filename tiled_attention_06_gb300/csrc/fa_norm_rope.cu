@@ -157,11 +157,6 @@ __device__ __forceinline__ void fill_angles(const NormRopeParams& p, int nt, con
   }
 }
 
-__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
 __device__ __forceinline__ float f2_sum(uint64_t a) {
   float x, y;
   f2_split(a, x, y);

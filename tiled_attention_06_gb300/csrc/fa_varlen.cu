@@ -41,6 +41,7 @@
 
 #include <climits>
 #include <cstdint>
+#include <type_traits>
 
 #include "fa_mma.cuh"
 #include "fa_plan.h"
@@ -389,16 +390,15 @@ struct Cfg {
   static constexpr int Q_BYTES = kTile * D * 2;  // one tile
   static constexpr int TILE_BYTES = BN * D * 2;
   static constexpr int BAR_BYTES = 1024;
-  // an 8-bit cache: tiles as they lie there, rows of D bytes and 128 exponent bytes behind them
-  static constexpr int RAW_BYTES = BN * D + BN;
-  static constexpr int NRAW = Q8 ? 4 : 0;
-  static constexpr int FIT = (int)((kSmemLimit - 1024 - BAR_BYTES - 2 * Q_BYTES - NRAW * RAW_BYTES) /
-                                   TILE_BYTES);
+  // an 8-bit cache: a slot's second half takes its tile as it lies there, rows of D bytes, which are
+  // then converted in place; the exponent bytes of every slot lie behind the ring
+  static constexpr int SCALES = Q8 ? BN : 0;
+  static constexpr int FIT =
+      (int)((kSmemLimit - 1024 - BAR_BYTES - 2 * Q_BYTES) / (TILE_BYTES + SCALES));
   static constexpr int NSLOT = FIT > 8 ? 8 : FIT;
-  static constexpr int RAW_AT = 2 * Q_BYTES + NSLOT * TILE_BYTES;
-  static constexpr int BARS_AT = RAW_AT + NRAW * RAW_BYTES;
+  static constexpr int SCALES_AT = 2 * Q_BYTES + NSLOT * TILE_BYTES;
+  static constexpr int BARS_AT = SCALES_AT + NSLOT * SCALES;
   static constexpr int SMEM = 1024 + BARS_AT + BAR_BYTES;
-  static_assert(NSLOT >= 3, "too few tiles");
   static constexpr int TMEM_COLS = 512;  // S_A S_B [0, 256), O_A O_B [256, 256 + 2 D)
   static_assert(2 * BN + 2 * D <= 512, "TMEM over budget");
 };
@@ -411,7 +411,7 @@ struct Bars {
   uint64_t pv_step;      // every P V of an item with one tile
   uint64_t o_staged[2];  // the tile's output is in shared memory
   uint64_t final_mma;
-  uint64_t raw_full[4], raw_empty[4];  // tiles of an 8-bit cache
+  uint64_t raw_full[8];  // tiles of an 8-bit cache, before their conversion
   uint32_t tmem_base;
   uint32_t abort;
 };
@@ -543,50 +543,97 @@ __device__ __forceinline__ bool softmax_row(uint32_t t_lane, uint32_t s_col, uin
 
 // ------------------------------------------------------------------ tiles of an 8-bit cache
 
-// Two elements of a row, times its power of two, in the call's type. The FP32 products are exact;
-// so is the rounding, but for what FP16 does not hold (16-bit products of FP16 pairs round alike, and
-// serve where the power itself is an FP16 number).
-template <bool BF16>
-__device__ __forceinline__ uint32_t widen8(uint32_t x, float power, uint32_t power2, bool half) {
-  uint32_t h;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(x)));
-  if (!BF16 && half) {
-    asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(h) : "r"(power2));
-    return h;
+// Four elements of a row (one byte each), times its power of two, as two pairs of the call's type, by
+// way of FP16, to which an instruction converts. WIDE: the product is FP32, exact, and rounded once
+// (exactly, in BF16). Otherwise it is FP16 with a power that is an FP16 number, which rounds alike.
+// (BF16 in integers, sign, exponent and fraction moved into place, took as long.)
+template <bool BF16, bool WIDE>
+__device__ __forceinline__ void widen8(uint32_t x, uint64_t power, uint32_t& lo, uint32_t& hi) {
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(lo) : "h"(static_cast<uint16_t>(x)));
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(hi) : "h"(static_cast<uint16_t>(x >> 16)));
+  if constexpr (!WIDE) {
+    asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(lo) : "r"(static_cast<uint32_t>(power)));
+    asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(hi) : "r"(static_cast<uint32_t>(power)));
+  } else {
+    const float2 a = __half22float2(*reinterpret_cast<__half2*>(&lo));
+    const float2 b = __half22float2(*reinterpret_cast<__half2*>(&hi));
+    float u, v;
+    f2_split(f2_mul(f2(a.x, a.y), power), u, v);
+    lo = BF16 ? cvt_pack_bf16(u, v) : cvt_pack_f16(u, v);
+    f2_split(f2_mul(f2(b.x, b.y), power), u, v);
+    hi = BF16 ? cvt_pack_bf16(u, v) : cvt_pack_f16(u, v);
   }
-  const float2 f = __half22float2(*reinterpret_cast<__half2*>(&h));
-  return BF16 ? cvt_pack_bf16(f.x * power, f.y * power) : cvt_pack_f16(f.x * power, f.y * power);
 }
-// One tile by 128 threads: raw rows of D bytes and exponent bytes to the 128-byte swizzle of a
-// 16-bit tile; rows from `live` on become zeros. 16 elements to a thread at a time; the lanes of
-// the second region store their halves in the other order, or they met the first's banks.
+// One slot by the 128 threads of the converting warps: rows of D bytes in its second half and their
+// exponent bytes to the 128-byte swizzle of a 16-bit tile over the whole slot; rows from `live` on
+// become zeros. A thread takes 16 elements of N neighbouring rows, whose exponents are one access, and
+// holds them before any thread writes. Lanes that would meet in a bank store their halves in the other
+// order. False when some thread came with !ok; nothing is written then.
 template <int D, bool BF16>
-__device__ __forceinline__ void convert_tile(const uint8_t* raw, uint32_t dst, int live, int t) {
+__device__ __forceinline__ bool convert_slot(const uint8_t* slot, const uint8_t* scales, int live,
+                                             int t, bool ok) {
   constexpr int CPR = D / 16;  // 16-byte chunks of a raw row
-  const int c = t % CPR, flip = c / 4;
-#pragma unroll 4
-  for (int row = t / CPR; row < BN; row += 128 / CPR) {
-    uint4 x = *reinterpret_cast<const uint4*>(raw + row * D + 16 * c);
-    const uint32_t b = raw[BN * D + row];
-    // 2^(b - 127): NaN for 255, 0 for 0 (2^-127); as FP16 where that is one, 2^-14 to 2^15
-    float power = __uint_as_float(b == 255 ? 0x7fffffffu : b << 23);
-    const bool half = b >= 113 && b <= 142;
-    uint32_t power2 = (b - 112) * 0x04000400u;
-    if (row >= live) x = make_uint4(0, 0, 0, 0), power = 0.f;
-    const uint32_t in[4] = {x.x, x.y, x.z, x.w};
-    uint32_t out[8];
+  constexpr int N = CPR;       // 128 threads, 128 rows
+  const int c = t % CPR, g = t / CPR;
+  uint4 x[N];
+  uint32_t b[2] = {0x7f7f7f7fu, 0x7f7f7f7fu};
+  bool wide = false;
+  if (ok) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      out[i] = widen8<BF16>(in[i / 2] >> (16 * (i % 2)), power, power2, half);
-    const uint32_t at = dst + flip * (BN * 128) + row * 128;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const bool second = (h ^ flip) & 1;
-      const uint32_t chunk = static_cast<uint32_t>(((2 * c) % 8 + (second ? 1 : 0)) ^ (row & 7));
-      st_shared_v4(at + (chunk << 4), second ? out[4] : out[0], second ? out[5] : out[1],
-                   second ? out[6] : out[2], second ? out[7] : out[3]);
+    for (int i = 0; i < N; ++i)
+      x[i] = *reinterpret_cast<const uint4*>(slot + BN * D + (N * g + i) * D + 16 * c);
+    if (N == 8) {
+      const uint2 y = *reinterpret_cast<const uint2*>(scales + 8 * g);
+      b[0] = y.x, b[1] = y.y;
+    } else {
+      b[0] = *reinterpret_cast<const uint32_t*>(scales + 4 * g);
     }
+    if (live < BN) {
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (N * g + i >= live) {
+          x[i] = make_uint4(0, 0, 0, 0);
+          b[i / 4] = (b[i / 4] & ~(255u << (8 * (i % 4)))) | 127u << (8 * (i % 4));
+        }
+    }
+    // powers that are no FP16 number (below 2^-14 or above 2^15), four at a time
+    wide = BF16 || (__vcmpgtu4(b[0], 0x8e8e8e8eu) | __vcmpltu4(b[0], 0x71717171u)) ||
+                      (__vcmpgtu4(b[1], 0x8e8e8e8eu) | __vcmpltu4(b[1], 0x71717171u));
   }
+  uint32_t all;  // a barrier and a vote in one: no warp is left waiting for one that gave up
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\t"
+      "barrier.cta.red.and.pred.aligned q, 2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(all)
+      : "r"(static_cast<uint32_t>(ok))
+      : "memory");
+  if (!all) return false;
+  // chunks 2c and 2c + 1 of the row's 16-byte chunks, eight to a region of 64 elements
+  const int flip = D == 128 ? c / 4 : g % 2;
+  const uint32_t dst = smem_u32(slot) + (c / 4) * (BN * 128) + N * g * 128;
+  const uint32_t one = ((2 * c) % 8 + flip) ^ (D == 128 ? 0 : 4 * (g % 2)), two = one ^ 1u;
+  auto convert = [&](auto as) {
+    constexpr bool WIDE = decltype(as)::value;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const uint32_t e = __byte_perm(b[i / 4], 0, 0x4440 + i % 4);
+      // 2^(e - 127): NaN for 255, 0 for 0 (2^-127)
+      const float f = __uint_as_float(e == 255 ? 0x7fffffffu : e << 23);
+      const uint64_t power = WIDE ? f2(f, f) : e * 0x04000400u - 112u * 0x04000400u;
+      const uint32_t in[4] = {flip ? x[i].z : x[i].x, flip ? x[i].w : x[i].y,
+                              flip ? x[i].x : x[i].z, flip ? x[i].y : x[i].w};
+      uint32_t out[8];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) widen8<BF16, WIDE>(in[k], power, out[2 * k], out[2 * k + 1]);
+      st_shared_v4(dst + i * 128 + ((one ^ i) << 4), out[0], out[1], out[2], out[3]);
+      st_shared_v4(dst + i * 128 + ((two ^ i) << 4), out[4], out[5], out[6], out[7]);
+    }
+  };
+  if (BF16 || __any_sync(0xffffffffu, wide))
+    convert(std::true_type{});
+  else
+    convert(std::false_type{});
+  return true;
 }
 // `bytes` (a multiple of 16) from global to shared memory, counted on `bar`.
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
@@ -620,10 +667,7 @@ __global__ void __launch_bounds__(Cfg<D, FORM>::THREADS, 1)
       mbar_init(B(bars->full[i]), Q8 ? 4 : 1);
       mbar_init(B(bars->empty[i]), 1);
     }
-    for (int i = 0; i < C::NRAW; ++i) {
-      mbar_init(B(bars->raw_full[i]), 1);
-      mbar_init(B(bars->raw_empty[i]), 4);
-    }
+    for (int i = 0; i < C::NSLOT && Q8; ++i) mbar_init(B(bars->raw_full[i]), 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(B(bars->q_full[i]), 1);
       mbar_init(B(bars->q_empty[i]), 1);
@@ -671,20 +715,16 @@ __global__ void __launch_bounds__(Cfg<D, FORM>::THREADS, 1)
         for (int j = it.u.j0; j < it.u.j1 && ok; ++j) {
           const int live = it.u.sk - block_at(it.u, j) * BN;
           for (int kv = 0; kv < 2; ++kv, ++pos) {
-            const int raw = pos % 4, slot = pos % C::NSLOT;
-            ok = mbar_wait(B(bars->raw_full[raw]), (pos / 4) & 1, wc) &&
-                 mbar_wait(B(bars->empty[slot]), ((pos / C::NSLOT) & 1) ^ 1, wc);
+            const int slot = pos % C::NSLOT;
+            ok = mbar_wait(B(bars->raw_full[slot]), (pos / C::NSLOT) & 1, wc);
             ok = __all_sync(0xffffffffu, ok);
+            ok = convert_slot<D, BF16>(smem + 2 * C::Q_BYTES + slot * C::TILE_BYTES,
+                                       smem + C::SCALES_AT + slot * C::SCALES, live,
+                                       threadIdx.x - kConvertWarp * 32, ok);
             if (!ok) break;
-            convert_tile<D, BF16>(smem + C::RAW_AT + raw * C::RAW_BYTES,
-                                  sRing + slot * C::TILE_BYTES, live,
-                                  threadIdx.x - kConvertWarp * 32);
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) {
-              mbar_arrive(B(bars->full[slot]));
-              mbar_arrive(B(bars->raw_empty[raw]));
-            }
+            if (lane == 0) mbar_arrive(B(bars->full[slot]));
           }
         }
       }
@@ -730,15 +770,12 @@ __global__ void __launch_bounds__(Cfg<D, FORM>::THREADS, 1)
             }
           }
           for (int kv = 0; kv < 2; ++kv) {  // K, then V
-            constexpr int NS = Q8 ? C::NRAW : C::NSLOT;
-            const int slot = pos % NS;
-            const uint32_t use = pos / NS;
-            if (!(ok = mbar_wait(B(Q8 ? bars->raw_empty[slot % 4] : bars->empty[slot]),
-                                 (use & 1) ^ 1, wc)))
-              break;
+            const int slot = pos % C::NSLOT;
+            const uint32_t use = pos / C::NSLOT;
+            if (!(ok = mbar_wait(B(bars->empty[slot]), (use & 1) ^ 1, wc))) break;
             if constexpr (Q8) {  // a box's rows are neighbours in the pool
-              const uint32_t raw = base + C::RAW_AT + slot * C::RAW_BYTES;
-              const uint32_t bar = B(bars->raw_full[slot % 4]);
+              const uint32_t raw = sRing + slot * C::TILE_BYTES + BN * D;
+              const uint32_t bar = B(bars->raw_full[slot]);
               if (leader) mbar_arrive_expect_tx(bar, boxes * p.box * (D + 1));
               __syncwarp();
               if (lane < boxes) {
@@ -746,8 +783,8 @@ __global__ void __launch_bounds__(Cfg<D, FORM>::THREADS, 1)
                 bulk_load(raw + lane * p.box * D,
                           static_cast<const uint8_t*>(kv ? p.v_pages : p.k_pages) + row * D,
                           p.box * D, bar);
-                bulk_load(raw + BN * D + lane * p.box, (kv ? p.v_scales : p.k_scales) + row, p.box,
-                          bar);
+                bulk_load(base + C::SCALES_AT + slot * C::SCALES + lane * p.box,
+                          (kv ? p.v_scales : p.k_scales) + row, p.box, bar);
               }
               __syncwarp();
               fills[slot] = use + 1;
@@ -777,9 +814,9 @@ __global__ void __launch_bounds__(Cfg<D, FORM>::THREADS, 1)
         }
       }
       if (!ok) {  // wind down: every load issued lands before the CTA exits
-        for (int s = 0; s < (Q8 ? C::NRAW : C::NSLOT); ++s)
+        for (int s = 0; s < C::NSLOT; ++s)
           if (fills[s] > 0)
-            mbar_wait_quiet(B(Q8 ? bars->raw_full[s % 4] : bars->full[s]), (fills[s] - 1) & 1, wc);
+            mbar_wait_quiet(B(Q8 ? bars->raw_full[s] : bars->full[s]), (fills[s] - 1) & 1, wc);
         for (int q = 0; q < 2; ++q)
           if (iq[q] > 0) mbar_wait_quiet(B(bars->q_full[q]), (iq[q] - 1) & 1, wc);
       }
