@@ -390,15 +390,16 @@ struct Cfg {
   static constexpr int Q_BYTES = kTile * D * 2;  // one tile
   static constexpr int TILE_BYTES = BN * D * 2;
   static constexpr int BAR_BYTES = 1024;
-  // an 8-bit cache: a slot's second half takes its tile as it lies there, rows of D bytes, which are
-  // then converted in place; the exponent bytes of every slot lie behind the ring
-  static constexpr int SCALES = Q8 ? BN : 0;
-  static constexpr int FIT =
-      (int)((kSmemLimit - 1024 - BAR_BYTES - 2 * Q_BYTES) / (TILE_BYTES + SCALES));
+  // an 8-bit cache: tiles as they lie there, rows of D bytes and 128 exponent bytes behind them
+  static constexpr int RAW_BYTES = BN * D + BN;
+  static constexpr int NRAW = Q8 ? 4 : 0;
+  static constexpr int FIT = (int)((kSmemLimit - 1024 - BAR_BYTES - 2 * Q_BYTES - NRAW * RAW_BYTES) /
+                                   TILE_BYTES);
   static constexpr int NSLOT = FIT > 8 ? 8 : FIT;
-  static constexpr int SCALES_AT = 2 * Q_BYTES + NSLOT * TILE_BYTES;
-  static constexpr int BARS_AT = SCALES_AT + NSLOT * SCALES;
+  static constexpr int RAW_AT = 2 * Q_BYTES + NSLOT * TILE_BYTES;
+  static constexpr int BARS_AT = RAW_AT + NRAW * RAW_BYTES;
   static constexpr int SMEM = 1024 + BARS_AT + BAR_BYTES;
+  static_assert(NSLOT >= 3, "too few tiles");
   static constexpr int TMEM_COLS = 512;  // S_A S_B [0, 256), O_A O_B [256, 256 + 2 D)
   static_assert(2 * BN + 2 * D <= 512, "TMEM over budget");
 };
@@ -411,7 +412,7 @@ struct Bars {
   uint64_t pv_step;      // every P V of an item with one tile
   uint64_t o_staged[2];  // the tile's output is in shared memory
   uint64_t final_mma;
-  uint64_t raw_full[8];  // tiles of an 8-bit cache, before their conversion
+  uint64_t raw_full[4], raw_empty[4];  // tiles of an 8-bit cache
   uint32_t tmem_base;
   uint32_t abort;
 };
@@ -570,18 +571,18 @@ __device__ __forceinline__ void widen8(uint32_t x, uint64_t power, uint32_t& lo,
 // holds them before any thread writes. Lanes that would meet in a bank store their halves in the other
 // order. False when some thread came with !ok; nothing is written then.
 template <int D, bool BF16>
-__device__ __forceinline__ bool convert_slot(const uint8_t* slot, const uint8_t* scales, int live,
-                                             int t, bool ok) {
+__device__ __forceinline__ void convert_tile(const uint8_t* raw, uint32_t slot, int live, int t) {
+  const uint8_t* scales = raw + BN * D;
   constexpr int CPR = D / 16;  // 16-byte chunks of a raw row
   constexpr int N = CPR;       // 128 threads, 128 rows
   const int c = t % CPR, g = t / CPR;
   uint4 x[N];
   uint32_t b[2] = {0x7f7f7f7fu, 0x7f7f7f7fu};
   bool wide = false;
-  if (ok) {
+  {
 #pragma unroll
     for (int i = 0; i < N; ++i)
-      x[i] = *reinterpret_cast<const uint4*>(slot + BN * D + (N * g + i) * D + 16 * c);
+      x[i] = *reinterpret_cast<const uint4*>(raw + (N * g + i) * D + 16 * c);
     if (N == 8) {
       const uint2 y = *reinterpret_cast<const uint2*>(scales + 8 * g);
       b[0] = y.x, b[1] = y.y;
@@ -600,17 +601,9 @@ __device__ __forceinline__ bool convert_slot(const uint8_t* slot, const uint8_t*
     wide = BF16 || (__vcmpgtu4(b[0], 0x8e8e8e8eu) | __vcmpltu4(b[0], 0x71717171u)) ||
                       (__vcmpgtu4(b[1], 0x8e8e8e8eu) | __vcmpltu4(b[1], 0x71717171u));
   }
-  uint32_t all;  // a barrier and a vote in one: no warp is left waiting for one that gave up
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\t"
-      "barrier.cta.red.and.pred.aligned q, 2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(all)
-      : "r"(static_cast<uint32_t>(ok))
-      : "memory");
-  if (!all) return false;
   // chunks 2c and 2c + 1 of the row's 16-byte chunks, eight to a region of 64 elements
   const int flip = D == 128 ? c / 4 : g % 2;
-  const uint32_t dst = smem_u32(slot) + (c / 4) * (BN * 128) + N * g * 128;
+  const uint32_t dst = slot + (c / 4) * (BN * 128) + N * g * 128;
   const uint32_t one = ((2 * c) % 8 + flip) ^ (D == 128 ? 0 : 4 * (g % 2)), two = one ^ 1u;
   auto convert = [&](auto as) {
     constexpr bool WIDE = decltype(as)::value;
@@ -633,7 +626,6 @@ __device__ __forceinline__ bool convert_slot(const uint8_t* slot, const uint8_t*
     convert(std::true_type{});
   else
     convert(std::false_type{});
-  return true;
 }
 // `bytes` (a multiple of 16) from global to shared memory, counted on `bar`.
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
@@ -667,7 +659,10 @@ __global__ void __launch_bounds__(Cfg<D, FORM>::THREADS, 1)
       mbar_init(B(bars->full[i]), Q8 ? 4 : 1);
       mbar_init(B(bars->empty[i]), 1);
     }
-    for (int i = 0; i < C::NSLOT && Q8; ++i) mbar_init(B(bars->raw_full[i]), 1);
+    for (int i = 0; i < C::NRAW; ++i) {
+      mbar_init(B(bars->raw_full[i]), 1);
+      mbar_init(B(bars->raw_empty[i]), 4);
+    }
     for (int i = 0; i < 2; ++i) {
       mbar_init(B(bars->q_full[i]), 1);
       mbar_init(B(bars->q_empty[i]), 1);
@@ -715,16 +710,20 @@ __global__ void __launch_bounds__(Cfg<D, FORM>::THREADS, 1)
         for (int j = it.u.j0; j < it.u.j1 && ok; ++j) {
           const int live = it.u.sk - block_at(it.u, j) * BN;
           for (int kv = 0; kv < 2; ++kv, ++pos) {
-            const int slot = pos % C::NSLOT;
-            ok = mbar_wait(B(bars->raw_full[slot]), (pos / C::NSLOT) & 1, wc);
+            const int raw = pos % 4, slot = pos % C::NSLOT;
+            ok = mbar_wait(B(bars->raw_full[raw]), (pos / 4) & 1, wc) &&
+                 mbar_wait(B(bars->empty[slot]), ((pos / C::NSLOT) & 1) ^ 1, wc);
             ok = __all_sync(0xffffffffu, ok);
-            ok = convert_slot<D, BF16>(smem + 2 * C::Q_BYTES + slot * C::TILE_BYTES,
-                                       smem + C::SCALES_AT + slot * C::SCALES, live,
-                                       threadIdx.x - kConvertWarp * 32, ok);
             if (!ok) break;
+            convert_tile<D, BF16>(smem + C::RAW_AT + raw * C::RAW_BYTES,
+                                  sRing + slot * C::TILE_BYTES, live,
+                                  threadIdx.x - kConvertWarp * 32);
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(B(bars->full[slot]));
+            if (lane == 0) {
+              mbar_arrive(B(bars->full[slot]));
+              mbar_arrive(B(bars->raw_empty[raw]));
+            }
           }
         }
       }
@@ -770,12 +769,15 @@ __global__ void __launch_bounds__(Cfg<D, FORM>::THREADS, 1)
             }
           }
           for (int kv = 0; kv < 2; ++kv) {  // K, then V
-            const int slot = pos % C::NSLOT;
-            const uint32_t use = pos / C::NSLOT;
-            if (!(ok = mbar_wait(B(bars->empty[slot]), (use & 1) ^ 1, wc))) break;
+            constexpr int NS = Q8 ? C::NRAW : C::NSLOT;
+            const int slot = pos % NS;
+            const uint32_t use = pos / NS;
+            if (!(ok = mbar_wait(B(Q8 ? bars->raw_empty[slot % 4] : bars->empty[slot]),
+                                 (use & 1) ^ 1, wc)))
+              break;
             if constexpr (Q8) {  // a box's rows are neighbours in the pool
-              const uint32_t raw = sRing + slot * C::TILE_BYTES + BN * D;
-              const uint32_t bar = B(bars->raw_full[slot]);
+              const uint32_t raw = base + C::RAW_AT + slot * C::RAW_BYTES;
+              const uint32_t bar = B(bars->raw_full[slot % 4]);
               if (leader) mbar_arrive_expect_tx(bar, boxes * p.box * (D + 1));
               __syncwarp();
               if (lane < boxes) {
@@ -783,8 +785,8 @@ __global__ void __launch_bounds__(Cfg<D, FORM>::THREADS, 1)
                 bulk_load(raw + lane * p.box * D,
                           static_cast<const uint8_t*>(kv ? p.v_pages : p.k_pages) + row * D,
                           p.box * D, bar);
-                bulk_load(base + C::SCALES_AT + slot * C::SCALES + lane * p.box,
-                          (kv ? p.v_scales : p.k_scales) + row, p.box, bar);
+                bulk_load(raw + BN * D + lane * p.box, (kv ? p.v_scales : p.k_scales) + row, p.box,
+                          bar);
               }
               __syncwarp();
               fills[slot] = use + 1;
@@ -814,9 +816,9 @@ __global__ void __launch_bounds__(Cfg<D, FORM>::THREADS, 1)
         }
       }
       if (!ok) {  // wind down: every load issued lands before the CTA exits
-        for (int s = 0; s < C::NSLOT; ++s)
+        for (int s = 0; s < (Q8 ? C::NRAW : C::NSLOT); ++s)
           if (fills[s] > 0)
-            mbar_wait_quiet(B(Q8 ? bars->raw_full[s] : bars->full[s]), (fills[s] - 1) & 1, wc);
+            mbar_wait_quiet(B(Q8 ? bars->raw_full[s % 4] : bars->full[s]), (fills[s] - 1) & 1, wc);
         for (int q = 0; q < 2; ++q)
           if (iq[q] > 0) mbar_wait_quiet(B(bars->q_full[q]), (iq[q] - 1) & 1, wc);
       }
