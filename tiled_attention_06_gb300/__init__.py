@@ -795,67 +795,100 @@ def fa_rope_axes(sections, interleaved=False, device=None):
     return host if device is None else host.to(device)
 
 
-def _heads(name, t, T, heads, d, dtype, device):
-    """(pointer, elements between tokens, between heads) of rows of heads [T, heads, d]."""
-    if t.shape != (T, heads, d) or t.dtype != dtype or t.device != device:
-        _refuse(f"{name} must be [{T}, {heads}, {d}] of {dtype} on {device}, not "
-                f"{list(t.shape)} of {t.dtype} on {t.device}")
+# What a call of a few microseconds on the GPU pays here is mostly the reading of its tensors'
+# attributes (0.1 to 0.25 us each), so these calls read each once and leave the wording of a refusal to
+# _refuse_tensor.
+
+_get_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_CODES = {torch.float16: FA_F16, torch.bfloat16: FA_BF16, torch.float32: FA_F32}
+
+
+def _device_of(t):
+    """The index of t's device, which must be the current CUDA device."""
+    dev = t.get_device()
+    if dev < 0 or dev != _get_device():
+        _packed_device(t)
+    return dev
+
+
+def _code(t, dtype):
+    code = _CODES.get(dtype)
+    return _dtype_code(t) if code is None else code
+
+
+def _refuse_tensor(name, t, shape, dtypes, dev, what=""):
+    _refuse(f"{name} must be {what}{list(shape)} of {dtypes} on cuda:{dev}, not {list(t.shape)} of "
+            f"{t.dtype} on {t.device}, steps {t.stride()}")
+
+
+def _heads(name, t, shape, dtype, dev):
+    """(elements between tokens, between heads) of rows of heads, `shape` [T, heads, d]."""
     st = t.stride()
-    if d > 1 and st[2] != 1:
-        _refuse(f"{name}: the elements of a head must be contiguous")
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != dev or (
+            st[2] != 1 and shape[2] > 1):
+        _refuse_tensor(name, t, shape, dtype, dev, "rows with contiguous heads, ")
+    T, heads, d = shape
     head = st[1] if heads > 1 else d
-    return t.data_ptr(), st[0] if T > 1 else (heads - 1) * head + d, head
+    return (st[0] if T > 1 else (heads - 1) * head + d), head
 
 
-def _weight(name, w, d, dtype, device):
-    if w is None:
-        return 0
-    if w.shape != (d,) or w.device != device or not w.is_contiguous() \
-            or (w.dtype != dtype and w.dtype != torch.float32):
-        _refuse(f"{name} must be a contiguous [{d}] tensor of {dtype} or float32 on {device}")
-    return w.data_ptr()
+def _dense(name, t, n, dtype, dev):
+    """The pointer of a contiguous tensor of n elements."""
+    if t.numel() != n or t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+        _refuse_tensor(name, t, [n], dtype, dev, "contiguous ")
+    return t.data_ptr()
 
 
-def _weights(q_weight, k_weight, d, dtype, device):
+def _weights(q_weight, k_weight, d, dtype, dev):
     """(pointers, their common dtype's code)"""
-    if q_weight is not None and k_weight is not None and q_weight.dtype != k_weight.dtype:
-        _refuse("q_weight and k_weight must have the same dtype")
-    one = q_weight if q_weight is not None else k_weight
-    code = FA_F32 if one is None or one.dtype == torch.float32 else _dtype_code(one)
-    return (_weight("q_weight", q_weight, d, dtype, device),
-            _weight("k_weight", k_weight, d, dtype, device), code)
+    if q_weight is None and k_weight is None:
+        return 0, 0, FA_F32
+    one = (q_weight if q_weight is not None else k_weight).dtype
+    if one is not dtype and one is not torch.float32:
+        _refuse(f"weights must be of {dtype} or float32, not {one}")
+    return (0 if q_weight is None else _dense("q_weight", q_weight, d, one, dev),
+            0 if k_weight is None else _dense("k_weight", k_weight, d, one, dev), _CODES[one])
 
 
-def _axes(positions, pair_axis, freqs, T, device):
+def _axes(positions, pair_axis, pairs, T, dev):
     """(positions' pointer, pair_axis' pointer, number of axes)"""
-    axes = 1 if positions is None or positions.dim() == 1 else positions.shape[0]
-    at = 0
+    axes, at = 1, 0
     if positions is not None:
-        shape = (T,) if positions.dim() == 1 else (axes, T)
-        at = _ints("positions", positions, shape, device)
+        shape = positions.shape
+        if len(shape) == 2:
+            axes = shape[0]
+        if len(shape) not in (1, 2) or shape[-1] != T or positions.dtype is not torch.int32 \
+                or positions.get_device() != dev or not positions.is_contiguous():
+            _refuse_tensor("positions", positions, ["axes", T], "int32", dev, "contiguous ")
+        at = positions.data_ptr()
     if pair_axis is None:
         return at, 0, axes
-    return at, _ints("pair_axis", pair_axis, (freqs.numel(),), device), axes
+    return at, _dense("pair_axis", pair_axis, pairs, torch.int32, dev), axes
 
 
-def _norm_rope(q, k, q_out, k_out, positions, freqs, q_weight, k_weight, norm, eps, pair_axis,
+def _norm_rope(dev, q, k, q_out, k_out, positions, freqs, q_weight, k_weight, norm, eps, pair_axis,
                style, amplitude):
-    device = _packed_device(q)
-    T, H, d = _dims("q", q, 3)
-    Hkv = 0 if k is None else _dims("k", k, 3)[1]
+    dtype, shape = q.dtype, q.shape
+    T, H, d = _dims("q", q, 3) if len(shape) != 3 else shape
+    pairs = freqs.numel()
+    a = _heads("q", q, shape, dtype, dev)
+    b = _heads("q_out", q_out, shape, dtype, dev)
+    Hkv, kp, kop, c, e = 0, 0, 0, (0, 0), (0, 0)
+    if k is not None:
+        Hkv = _dims("k", k, 3)[1]
     if (k is None) != (k_out is None):
         _refuse("k and its counterpart: both or neither")
-    none = (0, 0, 0)
-    a = _heads("q", q, T, H, d, q.dtype, device)
-    b = _heads("q_out", q_out, T, H, d, q.dtype, device)
-    c = _heads("k", k, T, Hkv, d, q.dtype, device) if Hkv else none
-    e = _heads("k_out", k_out, T, Hkv, d, q.dtype, device) if Hkv else none
-    at, pairs, axes = _axes(positions, pair_axis, freqs, T, device)
-    wq, wk, code = _weights(q_weight, k_weight, d, q.dtype, device)
+    if Hkv:
+        rows = (T, Hkv, d)
+        c, kp = _heads("k", k, rows, dtype, dev), k.data_ptr()
+        e, kop = _heads("k_out", k_out, rows, dtype, dev), k_out.data_ptr()
+    at, axis, axes = _axes(positions, pair_axis, pairs, T, dev)
+    wq, wk, code = _weights(q_weight, k_weight, d, dtype, dev)
     return _pack_norm_rope(
-        a[0], c[0], b[0], e[0], at, pairs, _freqs_ptr(freqs, device), wq, wk, T, a[1], a[2], c[1],
-        c[2], b[1], b[2], e[1], e[2], H, Hkv, d, 2 * freqs.numel(), axes, style, float(amplitude),
-        norm, float(eps), code, _dtype_code(q))
+        q.data_ptr(), kp, q_out.data_ptr(), kop, at, axis,
+        _dense("freqs", freqs, pairs, torch.float64, dev), wq, wk, T, a[0], a[1], c[0], c[1], b[0],
+        b[1], e[0], e[1], H, Hkv, d, 2 * pairs, axes, style, amplitude, norm, eps, code,
+        _code(q, dtype))
 
 
 def fa_norm_rope(q, k, q_out, k_out, positions, freqs, q_weight=None, k_weight=None,
@@ -866,9 +899,14 @@ def fa_norm_rope(q, k, q_out, k_out, positions, freqs, q_weight=None, k_weight=N
     or [T]; pair_axis int32 [len(freqs)] says which axis turns which pair (fa_rope_axes); weights
     [d] of q's dtype or float32, None: ones. float16, bfloat16 or float32; any token and head
     steps."""
-    p = _norm_rope(q, k, q_out, k_out, positions, freqs, q_weight, k_weight, norm, eps, pair_axis,
-                   style, amplitude)
-    _check(lib().fa_norm_rope(p, _stream(stream)))
+    dev = _device_of(q)
+    p = _norm_rope(dev, q, k, q_out, k_out, positions, freqs, q_weight, k_weight, norm, eps,
+                   pair_axis, style, amplitude)
+    _check(lib().fa_norm_rope(p, _stream_on(dev, stream)))
+
+
+def _stream_on(dev, stream):
+    return _raw_stream(dev) if stream is None and _raw_stream is not None else _stream(stream)
 
 
 def fa_norm_rope_bwd_workspace_size(H, Hkv, d):
@@ -882,45 +920,74 @@ def fa_norm_rope_bwd(q, k, dq_out, dk_out, dq, dk, positions, freqs, q_weight=No
     """Gradients of fa_norm_rope: dq, dk (which may be dq_out and dk_out) and, where given, the
     float32 [d] gradients of the weights, from the upstream dq_out and dk_out. workspace: a CUDA
     byte tensor of fa_norm_rope_bwd_workspace_size(...), needed for the weights' gradients."""
-    p = _norm_rope(q, k, q, k, positions, freqs, q_weight, k_weight, norm, eps, pair_axis, style,
-                   amplitude)
-    device, (T, H, d) = q.device, q.shape
-    Hkv = 0 if k is None else k.shape[1]
+    dev = _device_of(q)
+    p = _norm_rope(dev, q, k, q, k, positions, freqs, q_weight, k_weight, norm, eps, pair_axis,
+                   style, amplitude)
+    dtype, shape = q.dtype, q.shape
+    T, H, d = shape
     if (k is None) != (dk_out is None) or (k is None) != (dk is None):
         _refuse("k, dk_out and dk: all or none")
-    none = (0, 0, 0)
-    a = _heads("dq_out", dq_out, T, H, d, q.dtype, device)
-    b = _heads("dk_out", dk_out, T, Hkv, d, q.dtype, device) if Hkv else none
-    c = _heads("dq", dq, T, H, d, q.dtype, device)
-    e = _heads("dk", dk, T, Hkv, d, q.dtype, device) if Hkv else none
-    for name, w in (("dq_weight", dq_weight), ("dk_weight", dk_weight)):
-        if w is not None and w.dtype != torch.float32:
-            _refuse(f"{name} must be a contiguous [{d}] tensor of float32 on {device}")
-    ws, ws_bytes = (0, 0) if workspace is None else _bytes_of(workspace, device)
+    a = _heads("dq_out", dq_out, shape, dtype, dev)
+    c = _heads("dq", dq, shape, dtype, dev)
+    b = e = (0, 0)
+    bp = ep = 0
+    if k is not None and k.shape[1]:
+        rows = (T, k.shape[1], d)
+        b, bp = _heads("dk_out", dk_out, rows, dtype, dev), dk_out.data_ptr()
+        e, ep = _heads("dk", dk, rows, dtype, dev), dk.data_ptr()
+    ws, ws_bytes = (0, 0) if workspace is None else _bytes_of(workspace, q.device)
     g = _pack_norm_grads(
-        a[0], b[0], c[0], e[0], _weight("dq_weight", dq_weight, d, q.dtype, device),
-        _weight("dk_weight", dk_weight, d, q.dtype, device), a[1], a[2], b[1], b[2], c[1], c[2],
-        e[1], e[2], ws, ws_bytes)
-    _check(lib().fa_norm_rope_bwd(p, g, _stream(stream)))
+        dq_out.data_ptr(), bp, dq.data_ptr(), ep,
+        0 if dq_weight is None else _dense("dq_weight", dq_weight, d, torch.float32, dev),
+        0 if dk_weight is None else _dense("dk_weight", dk_weight, d, torch.float32, dev), a[0],
+        a[1], b[0], b[1], c[0], c[1], e[0], e[1], ws, ws_bytes)
+    _check(lib().fa_norm_rope_bwd(p, g, _stream_on(dev, stream)))
 
 
-def _bytes8(name, t, shape, dtype, device):
-    """An 8-bit tensor: the named float type or uint8."""
-    if t.shape != shape or (t.dtype != dtype and t.dtype != torch.uint8) or t.device != device \
-            or not t.is_contiguous():
-        _refuse(f"{name} must be contiguous {list(shape)} of {dtype} or uint8 on {device}")
+_E4M3, _E8M0 = torch.float8_e4m3fn, torch.float8_e8m0fnu
+
+
+def _bytes8(name, t, shape, dtype, dev):
+    """The pointer of a contiguous 8-bit tensor: the named float type or uint8."""
+    have = t.dtype
+    if (have is not dtype and have is not torch.uint8) or t.shape != shape \
+            or t.get_device() != dev or not t.is_contiguous():
+        _refuse_tensor(name, t, shape, f"{dtype} or uint8", dev, "contiguous ")
     return t.data_ptr()
 
 
-def _pools8(k_pages, v_pages, k_scales, v_scales, d, device):
-    """(pointers of the exponent bytes) of an 8-bit cache."""
+def _cache(k_pages, v_pages, k_scales, v_scales, shape, dtype, dev):
+    """Pointers of the pools of `shape` and of their exponent bytes (0: a cache of dtype)."""
+    if k_scales is None and v_scales is None:
+        for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
+            if t.dtype is not dtype or t.shape != shape or t.get_device() != dev \
+                    or not t.is_contiguous():
+                _refuse_tensor(name, t, shape, dtype, dev, "contiguous ")
+        return k_pages.data_ptr(), v_pages.data_ptr(), 0, 0
     if k_scales is None or v_scales is None:
         _refuse("k_scales and v_scales: both or neither")
-    shape = k_pages.shape
-    for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
-        _bytes8(name, t, shape[:3] + (d,), torch.float8_e4m3fn, device)
-    return tuple(_bytes8(name, t, shape[:3], torch.float8_e8m0fnu, device)
-                 for name, t in (("k_scales", k_scales), ("v_scales", v_scales)))
+    rows = shape[:3]
+    return (_bytes8("k_pages", k_pages, shape, _E4M3, dev),
+            _bytes8("v_pages", v_pages, shape, _E4M3, dev),
+            _bytes8("k_scales", k_scales, rows, _E8M0, dev),
+            _bytes8("v_scales", v_scales, rows, _E8M0, dev))
+
+
+def _packed(name, t, shape, dtype, dev):
+    """Elements between the tokens of packed rows, `shape` [T, heads, d], heads d apart."""
+    st = t.stride()
+    T, heads, d = shape
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != dev or (
+            T and ((st[2] != 1 and d > 1) or (st[1] != d and heads > 1))):
+        _refuse_tensor(name, t, shape, dtype, dev, "rows of neighbouring heads, ")
+    return st[0] if T > 1 else heads * d
+
+
+def _paging(k_pages, block_table, dev):
+    """(shape of the pools, B, pages of a sequence, the table's pointer)"""
+    shape, table = _dims("k_pages", k_pages, 4), _dims("block_table", block_table, 2)
+    return shape, table[0], table[1], _dense("block_table", block_table, table[0] * table[1],
+                                             torch.int32, dev)
 
 
 def fa_norm_rope_append(q, k, v, q_out, k_pages, v_pages, block_table, ctx_lens, cu_seqlens, freqs,
@@ -930,47 +997,44 @@ def fa_norm_rope_append(q, k, v, q_out, k_pages, v_pages, block_table, ctx_lens,
     """fa_rope_append with a norm of q and k (as fa_norm_rope), positions int32 [axes, T] for the
     angles (None: the tokens' places) and, where k_scales and v_scales [num_pages, Hkv, page_size]
     (float8_e8m0fnu or uint8) are given, into an 8-bit cache (pools of float8_e4m3fn or uint8)."""
-    device = _packed_device(q)
-    T, H, d = _dims("q", q, 3)
-    P, Hkv, page, _ = _dims("k_pages", k_pages, 4)
-    B, width = _dims("block_table", block_table, 2)
-    ks = vs = 0
-    if k_scales is None and v_scales is None:
-        _pools(k_pages, v_pages, d, q.dtype, device)
-    else:
-        ks, vs = _pools8(k_pages, v_pages, k_scales, v_scales, d, device)
-    at, pairs, axes = _axes(positions, pair_axis, freqs, T, device)
-    wq, wk, code = _weights(q_weight, k_weight, d, q.dtype, device)
+    dev = _device_of(q)
+    dtype, qs = q.dtype, q.shape
+    T, H, d = _dims("q", q, 3) if len(qs) != 3 else qs
+    (P, Hkv, page, _), B, width, table = _paging(k_pages, block_table, dev)
+    kp, vp, ks, vs = _cache(k_pages, v_pages, k_scales, v_scales, (P, Hkv, page, d), dtype, dev)
+    pairs, rows = freqs.numel(), (T, Hkv, d)
+    at, axis, axes = _axes(positions, pair_axis, pairs, T, dev)
+    wq, wk, code = _weights(q_weight, k_weight, d, dtype, dev)
     p = _pack_norm_append(
-        q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(), k_pages.data_ptr(),
-        v_pages.data_ptr(), ks, vs, _ints("block_table", block_table, (B, width), device),
-        _ints("ctx_lens", ctx_lens, (B,), device),
-        _ints("cu_seqlens", cu_seqlens, (B + 1,), device), at, pairs, _freqs_ptr(freqs, device),
-        wq, wk, _rows("q", q, T, H, d, q.dtype, device), _rows("k", k, T, Hkv, d, q.dtype, device),
-        _rows("v", v, T, Hkv, d, q.dtype, device),
-        _rows("q_out", q_out, T, H, d, q.dtype, device), T, B, H, Hkv, d, 2 * freqs.numel(), axes,
-        page, width, P, style, float(amplitude), norm, float(eps), code, _dtype_code(q))
-    _check(lib().fa_norm_rope_append(p, _stream(stream)))
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(), kp, vp, ks, vs, table,
+        _dense("ctx_lens", ctx_lens, B, torch.int32, dev),
+        _dense("cu_seqlens", cu_seqlens, B + 1, torch.int32, dev), at, axis,
+        _dense("freqs", freqs, pairs, torch.float64, dev), wq, wk, _packed("q", q, qs, dtype, dev),
+        _packed("k", k, rows, dtype, dev), _packed("v", v, rows, dtype, dev),
+        _packed("q_out", q_out, qs, dtype, dev), T, B, H, Hkv, d, 2 * pairs, axes, page, width, P,
+        style, amplitude, norm, eps, code, _code(q, dtype))
+    _check(lib().fa_norm_rope_append(p, _stream_on(dev, stream)))
 
 
 def fa_kv_read(k_pages, v_pages, k_scales, v_scales, block_table, starts, cu_seqlens, k, v,
                stream=None):
     """Rows of an 8-bit cache back in 16 bits: k, v [T, Hkv, d] float16 or bfloat16, whose rows
     cu_seqlens[b] .. cu_seqlens[b+1]-1 are sequence b's positions from starts[b] (int32 [B]) on."""
-    device = _packed_device(k)
-    T, Hkv, d = _dims("k", k, 3)
-    P, heads, page, _ = _dims("k_pages", k_pages, 4)
-    B, width = _dims("block_table", block_table, 2)
+    dev = _device_of(k)
+    dtype, rows = k.dtype, k.shape
+    T, Hkv, d = _dims("k", k, 3) if len(rows) != 3 else rows
+    (P, heads, page, _), B, width, table = _paging(k_pages, block_table, dev)
     if heads != Hkv:
         _refuse(f"k has {Hkv} heads, the pools {heads}")
-    ks, vs = _pools8(k_pages, v_pages, k_scales, v_scales, d, device)
+    if k_scales is None or v_scales is None:
+        _refuse("k_scales and v_scales are needed")
+    kp, vp, ks, vs = _cache(k_pages, v_pages, k_scales, v_scales, (P, Hkv, page, d), dtype, dev)
     p = _pack_kv_read(
-        k_pages.data_ptr(), v_pages.data_ptr(), ks, vs,
-        _ints("block_table", block_table, (B, width), device), _ints("starts", starts, (B,), device),
-        _ints("cu_seqlens", cu_seqlens, (B + 1,), device), k.data_ptr(), v.data_ptr(),
-        _rows("k", k, T, Hkv, d, k.dtype, device), _rows("v", v, T, Hkv, d, k.dtype, device), T, B,
-        Hkv, d, page, width, P, _dtype_code(k))
-    _check(lib().fa_kv_read(p, _stream(stream)))
+        kp, vp, ks, vs, table, _dense("starts", starts, B, torch.int32, dev),
+        _dense("cu_seqlens", cu_seqlens, B + 1, torch.int32, dev), k.data_ptr(), v.data_ptr(),
+        _packed("k", k, rows, dtype, dev), _packed("v", v, rows, dtype, dev), T, B, Hkv, d, page,
+        width, P, _code(k, dtype))
+    _check(lib().fa_kv_read(p, _stream_on(dev, stream)))
 
 
 def fa_fwd_paged_varlen_ex(q, k_pages, v_pages, block_table, ctx_lens, cu_seqlens_q, max_q, o, lse,
@@ -979,26 +1043,24 @@ def fa_fwd_paged_varlen_ex(q, k_pages, v_pages, block_table, ctx_lens, cu_seqlen
     """fa_fwd_paged_varlen over an 8-bit cache (k_scales and v_scales given) and for trees of
     drafted tokens: tree int32 [Tq, words], bit j % 32 of word j // 32 of a query's row set where it
     sees token j of its own chunk (mask_mode is then FA_MASK_TREE whatever is passed)."""
-    device = _packed_device(q)
-    Tq, H, d = _dims("q", q, 3)
-    P, Hkv, page, _ = _dims("k_pages", k_pages, 4)
-    B, width = _dims("block_table", block_table, 2)
-    ks = vs = bits = words = 0
-    if k_scales is None and v_scales is None:
-        _pools(k_pages, v_pages, d, q.dtype, device)
-    else:
-        ks, vs = _pools8(k_pages, v_pages, k_scales, v_scales, d, device)
+    dev = _device_of(q)
+    dtype, qs = q.dtype, q.shape
+    Tq, H, d = _dims("q", q, 3) if len(qs) != 3 else qs
+    (P, Hkv, page, _), B, width, table = _paging(k_pages, block_table, dev)
+    kp, vp, ks, vs = _cache(k_pages, v_pages, k_scales, v_scales, (P, Hkv, page, d), dtype, dev)
+    bits = words = 0
     if tree is not None:
         words = _dims("tree", tree, 2)[1]
-        bits = _ints("tree", tree, (Tq, words), device)
+        bits = _dense("tree", tree, Tq * words, torch.int32, dev)
         mask_mode, window, n_global = FA_MASK_TREE, 0, 0
-    ws, ws_bytes = _bytes_of(workspace, device)
+    if lse is not None and lse.shape != (Tq, H):
+        _refuse_tensor("lse", lse, (Tq, H), "float32", dev, "contiguous ")
+    ws, ws_bytes = _bytes_of(workspace, q.device)
     p = _pack_paged(
-        q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
-        _ints("block_table", block_table, (B, width), device),
-        _ints("ctx_lens", ctx_lens, (B,), device),
-        _ints("cu_seqlens_q", cu_seqlens_q, (B + 1,), device), o.data_ptr(),
-        _lse_ptr(lse, Tq, H, device), _rows("q", q, Tq, H, d, q.dtype, device),
-        _rows("o", o, Tq, H, d, q.dtype, device), B, H, Hkv, d, Tq, max_q, page, width, P,
-        float(scale), mask_mode, window, n_global, _dtype_code(q), ws, ws_bytes, 0)
-    _check(lib().fa_fwd_paged_varlen_ex(p, _pack_extra(ks, vs, bits, words), _stream(stream)))
+        q.data_ptr(), kp, vp, table, _dense("ctx_lens", ctx_lens, B, torch.int32, dev),
+        _dense("cu_seqlens_q", cu_seqlens_q, B + 1, torch.int32, dev), o.data_ptr(),
+        0 if lse is None else _dense("lse", lse, Tq * H, torch.float32, dev),
+        _packed("q", q, qs, dtype, dev), _packed("o", o, qs, dtype, dev), B, H, Hkv, d, Tq, max_q,
+        page, width, P, scale, mask_mode, window, n_global, _code(q, dtype), ws, ws_bytes, 0)
+    _check(lib().fa_fwd_paged_varlen_ex(p, _pack_extra(ks, vs, bits, words),
+                                       _stream_on(dev, stream)))
