@@ -23,6 +23,7 @@
 // head, a row cost 3x the instructions and 16384 tokens x 40 heads of 128 in bf16 took 68 us and their
 // gradient 117; so they take NORM_US and GRAD_US.
 #include <algorithm>
+#include <climits>
 #include <cstdint>
 
 #include "fa_ptx.cuh"
@@ -107,13 +108,6 @@ __device__ __forceinline__ void copy_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-__device__ __forceinline__ float weight_at(const void* w, int f32, int dt, int i) {
-  if (!w) return 1.f;
-  if (f32) return static_cast<const float*>(w)[i];
-  const uint16_t x = static_cast<const uint16_t*>(w)[i];
-  return dt == FA_BF16 ? Elem<FA_BF16>::get(x) : Elem<FA_F16>::get(x);
-}
-
 // Where the cosine of pair e of unit u lies (its sine is two behind it for VEC > 1, one for VEC = 1),
 // `units` rotated units in all: [e / 2][u][c_e c_{e+1} s_e s_{e+1}], or [u][c s].
 template <int VEC>
@@ -121,17 +115,41 @@ __device__ __forceinline__ int pair_at(int u, int e, int units) {
   return VEC == 1 ? 2 * u : ((e / 2) * units + u) * 4 + e % 2;
 }
 
+// What a CTA reads before its first row: the frequencies and axes, and the first batch's positions, a
+// thread's first of each in registers, so that these loads and the weights' wait for memory once.
+struct Ahead {
+  double freq = 0;
+  int axis = 0, pos = 0;
+  __device__ __forceinline__ void load(const NormRopeParams& p, int64_t t0, int nt) {
+    const int i = threadIdx.x;
+    if (i < p.rot / 2) {
+      freq = p.freqs[i];
+      if (p.pair_axis) axis = p.pair_axis[i];
+    }
+    if (p.pos && i < nt * p.axes) pos = p.pos[(i / nt) * p.T + t0 + i % nt];
+  }
+};
 // Frequencies and axes: the part that does not depend on the tokens.
-__device__ __forceinline__ void fill_fixed(const NormRopeParams& p, const Shared& sh) {
+__device__ __forceinline__ void fill_fixed(const NormRopeParams& p, const Shared& sh,
+                                           const Ahead& first) {
   for (int i = threadIdx.x; i < p.rot / 2; i += blockDim.x) {
-    sh.freq[i] = turns_q64(p.freqs[i]);
-    int a = p.pair_axis ? p.pair_axis[i] : 0;
+    const bool mine = i == static_cast<int>(threadIdx.x);
+    sh.freq[i] = turns_q64(mine ? first.freq : p.freqs[i]);
+    int a = mine ? first.axis : p.pair_axis ? p.pair_axis[i] : 0;
     if (a < 0 || a >= p.axes) {
       if (blockIdx.x == 0) atomicOr(p.status, FA_DEV_BAD_PAGE);
       a = 0;
     }
     sh.axis[i] = static_cast<uint8_t>(a);
   }
+}
+// The positions of the nt tokens from t0 on.
+__device__ __forceinline__ void fill_positions(const NormRopeParams& p, int64_t (*s_pos)[kTokMax],
+                                               int64_t t0, int nt, bool first, const Ahead& ahead) {
+  for (int i = threadIdx.x; i < nt * p.axes; i += blockDim.x)
+    s_pos[i / nt][i % nt] = first && i == static_cast<int>(threadIdx.x)
+                                ? ahead.pos
+                                : p.pos[(i / nt) * p.T + t0 + i % nt];
 }
 // Sines and cosines of nt tokens; pos(axis, token) in 64 bits.
 template <int VEC, typename Pos>
@@ -300,19 +318,50 @@ __device__ __forceinline__ void turn(uint64_t* A, uint64_t* B, const uint64_t* n
     B[i] = f2_fma(B[i], c, f2_mul(a, s));
   }
 }
-// The weights of a lane's elements, as its pairs lie.
+// The weights of a lane's elements, as its pairs lie; 0 where the row has no element. All loads of a
+// kind of weight stand before their uses (one by one, each behind the question of which kind it is, they
+// took 3.5 us of every CTA).
 template <int DT, int VEC, int KU, bool HALF>
 __device__ __forceinline__ void weights_of(const NormRopeParams& p, const void* w, const int* oa,
                                            const int* ob, int have, uint64_t* A, uint64_t* B) {
-  auto get = [&](int n, int second) {
-    const int k = n / VEC, e = n % VEC;
-    const int at = HALF || VEC == 1 ? (second ? ob[k] : oa[k]) + e : oa[k] + 2 * e + second;
-    return k < have ? weight_at(w, p.w_f32, DT, at) : 0.f;
-  };
+  constexpr int N = KU * VEC;
+  int at[2][N];
 #pragma unroll
-  for (int i = 0; i < KU * VEC / 2; ++i) {
-    A[i] = f2(get(2 * i, 0), get(2 * i + 1, 0));
-    B[i] = f2(get(2 * i, 1), get(2 * i + 1, 1));
+  for (int n = 0; n < N; ++n) {
+    const int k = n / VEC, e = n % VEC;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      at[h][n] = k >= have                 ? -1
+                 : HALF || VEC == 1 ? (h ? ob[k] : oa[k]) + e
+                                    : oa[k] + 2 * e + h;
+  }
+  float v[2][N];
+  if (!w) {
+#pragma unroll
+    for (int n = 0; n < 2 * N; ++n) v[n / N][n % N] = at[n / N][n % N] < 0 ? 0.f : 1.f;
+  } else if (DT == FA_F32 || p.w_f32) {
+#pragma unroll
+    for (int n = 0; n < 2 * N; ++n) {
+      const int i = at[n / N][n % N];
+      const float x = static_cast<const float*>(w)[max(i, 0)];
+      v[n / N][n % N] = i < 0 ? 0.f : x;
+    }
+  } else {
+    uint16_t x[2][N];
+#pragma unroll
+    for (int n = 0; n < 2 * N; ++n)
+      x[n / N][n % N] = static_cast<const uint16_t*>(w)[max(at[n / N][n % N], 0)];
+#pragma unroll
+    for (int n = 0; n < 2 * N; ++n) {
+      const float f = DT == FA_BF16 ? Elem<FA_BF16>::get(x[n / N][n % N])
+                                    : Elem<FA_F16>::get(x[n / N][n % N]);
+      v[n / N][n % N] = at[n / N][n % N] < 0 ? 0.f : f;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) {
+    A[i] = f2(v[0][2 * i], v[0][2 * i + 1]);
+    B[i] = f2(v[1][2 * i], v[1][2 * i + 1]);
   }
 }
 __device__ __forceinline__ float sum_lanes(float x, int ln) {
@@ -387,11 +436,13 @@ __global__ void __launch_bounds__(kMostThreads, DT != FA_F32 && VEC > 1 ? 3 : 2)
 #pragma unroll
     for (int i = 0; i < kStages - 1; ++i) fetch();
   }
+  Ahead first;
+  first.load(p, me.begin, static_cast<int>(min(static_cast<int64_t>(deal.tok), me.end - me.begin)));
   uint64_t wA[N2], wB[N2];
   if (p.norm && !is_v)
     weights_of<DT, VEC, KU, HALF>(p, is_q ? p.q_weight : p.k_weight, oa, ob, have, wA, wB);
   const float inv_d = 1.f / p.d;
-  fill_fixed(p, sh);
+  fill_fixed(p, sh, first);
   for (int64_t t0 = me.begin; t0 < me.end; t0 += deal.tok) {
     const int nt = static_cast<int>(min(static_cast<int64_t>(deal.tok), me.end - t0));
     if constexpr (MODE) {
@@ -417,9 +468,7 @@ __global__ void __launch_bounds__(kMostThreads, DT != FA_F32 && VEC > 1 ? 3 : 2)
         if (!p.pos) s_pos[0][threadIdx.x] = pos;
       }
     }
-    if (p.pos)
-      for (int i = threadIdx.x; i < nt * p.axes; i += blockDim.x)
-        s_pos[i / nt][i % nt] = p.pos[(i / nt) * p.T + t0 + i % nt];
+    if (p.pos) fill_positions(p, s_pos, t0, nt, t0 == me.begin, first);
     __syncthreads();  // also: the last batch's sines have been read
     fill_angles<VEC>(p, nt, sh, p.inverse != 0, [&](int a, int i) { return s_pos[a][i]; });
     __syncthreads();
@@ -553,6 +602,7 @@ __global__ void __launch_bounds__(kMostThreads, VEC == 1 ? 1 : 2)
   const uint32_t ring = smem_u32(s_dyn) + threadIdx.x * 16;
   const Shared sh(s_dyn + (VEC == 1 ? 0 : kGradStages * 4 * KU * blockDim.x), deal.tok, half);
   const int gl = threadIdx.x % ln;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the summing kernel may come up
   const Mine me(p, deal, p.H + p.Hkv);
   const bool is_k = me.r >= p.H;
   const int h = is_k ? me.r - p.H : me.r;
@@ -587,16 +637,17 @@ __global__ void __launch_bounds__(kMostThreads, VEC == 1 ? 1 : 2)
 #pragma unroll
     for (int i = 0; i < kGradStages - 1; ++i) fetch();
   }
+  Ahead first;
+  first.load(p, me.begin, static_cast<int>(min(static_cast<int64_t>(deal.tok), me.end - me.begin)));
   uint64_t wA[N2], wB[N2], da[N2], db[N2];  // the weight and its gradient
   weights_of<DT, VEC, KU, HALF>(p, is_k ? p.k_weight : p.q_weight, oa, ob, have, wA, wB);
 #pragma unroll
   for (int i = 0; i < N2; ++i) da[i] = db[i] = 0;
   const float inv_d = 1.f / p.d;
-  fill_fixed(p, sh);
+  fill_fixed(p, sh, first);
   for (int64_t t0 = me.begin; t0 < me.end; t0 += deal.tok) {
     const int nt = static_cast<int>(min(static_cast<int64_t>(deal.tok), me.end - t0));
-    for (int i = threadIdx.x; i < nt * p.axes; i += blockDim.x)
-      s_pos[i / nt][i % nt] = p.pos[(i / nt) * p.T + t0 + i % nt];
+    fill_positions(p, s_pos, t0, nt, t0 == me.begin, first);
     __syncthreads();  // also: the last batch's sines have been read
     fill_angles<VEC>(p, nt, sh, true, [&](int a, int i) { return s_pos[a][i]; });
     __syncthreads();
@@ -678,8 +729,11 @@ __global__ void __launch_bounds__(kMostThreads, VEC == 1 ? 1 : 2)
     const int from = kd ? max(0, p.H - first) : 0;
     const int to = kd ? min(deal.heads, p.H + p.Hkv - first) : min(deal.heads, p.H - first);
     float s = 0.f;
-    for (int t = 0; t < deal.per_round; ++t)
-      for (int r = from; r < to; ++r) s += s_dw[(t * deal.heads + r) * p.d + c];
+    for (int t = 0; t < deal.per_round; ++t) {
+      const float* const x = s_dw + t * deal.heads * p.d + c;
+#pragma unroll 8
+      for (int r = from; r < to; ++r) s += x[r * p.d];
+    }
     p.part[(cta * 2 + kd) * p.d + c] = s;
   }
 }
@@ -689,6 +743,7 @@ __global__ void __launch_bounds__(kMostThreads, VEC == 1 ? 1 : 2)
 __global__ void __launch_bounds__(1024)
     norm_rope_sum_kernel(const float* part, int ctas, int d, float* dq_weight, float* dk_weight) {
   __shared__ float s[32][33];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   float* const out = blockIdx.y ? dk_weight : dq_weight;
   if (!out) return;
   const int lane = threadIdx.x % 32, share = threadIdx.x / 32, c = blockIdx.x * 32 + lane;
@@ -774,14 +829,14 @@ int lanes_of(int units, int ku) {
   return ln;
 }
 
-// The deal of `rows` heads of T tokens over at most `ctas` CTAs (per_sm of them per SM), with `ring`
-// bytes of rows on their way per thread.
+// The deal of `rows` heads of T tokens over as many CTAs as give an SM at most `per_sm` threads, and at
+// most `most`, with `ring` bytes of rows on their way per thread.
 struct Launch {
   Deal deal;
   dim3 grid;
   int threads, smem;
 };
-Launch deal_rows(const NormRopeParams& p, int ln, int rows, int ctas, int ring) {
+Launch deal_rows(const NormRopeParams& p, int ln, int rows, int sms, int per_sm, int most, int ring) {
   Launch L;
   Deal& d = L.deal;
   d.ln = ln;
@@ -792,6 +847,7 @@ Launch deal_rows(const NormRopeParams& p, int ln, int rows, int ctas, int ring) 
   d.per_round = static_cast<int>(std::min<int64_t>({d.per_round, p.T, kTokMax}));
   L.threads = (d.per_round * d.heads * ln + 31) / 32 * 32;
   const int64_t runs = (p.T + d.per_round - 1) / d.per_round;  // rounds of all tokens
+  const int ctas = std::min(most, sms * (per_sm / L.threads));
   L.grid = dim3(static_cast<unsigned>(std::min<int64_t>(runs, std::max(1, ctas / chunks))), chunks);
   // the sines of a batch within 12 KB; no more than the CTA's own tokens
   const int64_t own = (p.T + L.grid.x - 1) / L.grid.x;
@@ -808,7 +864,7 @@ cudaError_t launch_v(const NormRopeParams& p, bool half_style, int sms, cudaStre
   constexpr int ring = VEC == 1 ? 0 : kStages * 2 * KU * 16;
   constexpr int most = kMostShared + ring * kMostThreads;
   const Launch L = deal_rows(p, lanes_of(p.d / (2 * VEC), KU), p.H + (MODE ? 2 : 1) * p.Hkv,
-                             (DT != FA_F32 && VEC > 1 ? 3 : 2) * sms, ring);
+                             sms, (DT != FA_F32 && VEC > 1 ? 3 : 2) * kMostThreads, INT_MAX, ring);
   auto* k = half_style ? norm_rope_kernel<DT, VEC, KU, true, MODE>
                        : norm_rope_kernel<DT, VEC, KU, false, MODE>;
   const cudaError_t e = half_style ? prepare_kernel<norm_rope_kernel<DT, VEC, KU, true, MODE>>(most)
@@ -821,7 +877,8 @@ template <int DT, int VEC, int KU>
 cudaError_t launch_bwd_v(const NormRopeParams& p, bool half_style, int sms, cudaStream_t stream) {
   constexpr int ring = VEC == 1 ? 0 : kGradStages * 4 * KU * 16;
   constexpr int most = kMostShared + ring * kMostThreads;
-  Launch L = deal_rows(p, lanes_of(p.d / (2 * VEC), KU), p.H + p.Hkv, std::min(2 * sms, kNormCtas), ring);
+  Launch L = deal_rows(p, lanes_of(p.d / (2 * VEC), KU), p.H + p.Hkv, sms,
+                       (VEC == 1 ? 1 : 2) * kMostThreads, kNormCtas, ring);
   // the weights' gradients of its groups meet in the ring's place
   L.smem = std::max(L.smem, L.deal.per_round * L.deal.heads * p.d * 4);
   auto* k = half_style ? norm_rope_bwd_kernel<DT, VEC, KU, true>
@@ -832,9 +889,17 @@ cudaError_t launch_bwd_v(const NormRopeParams& p, bool half_style, int sms, cuda
   k<<<L.grid, L.threads, L.smem, stream>>>(p, L.deal);
   e = cudaGetLastError();
   if (e != cudaSuccess || !p.part) return e;
-  norm_rope_sum_kernel<<<dim3((p.d + 31) / 32, 2), 1024, 0, stream>>>(
-      p.part, static_cast<int>(L.grid.x * L.grid.y), p.d, p.dq_weight, p.dk_weight);
-  return cudaGetLastError();
+  cudaLaunchAttribute early;  // it may come up while the gradient runs, which it then waits for
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((p.d + 31) / 32, 2);
+  cfg.blockDim = dim3(1024);
+  cfg.stream = stream;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, norm_rope_sum_kernel, static_cast<const float*>(p.part),
+                            static_cast<int>(L.grid.x * L.grid.y), p.d, p.dq_weight, p.dk_weight);
 }
 
 template <int DT, int MODE>

@@ -200,7 +200,7 @@ struct PlanSmem {
   SeqScan<kPlanThreads> scan;
   int bins[kBins + 1];
   // units and the most key blocks of one (used for few units alone), split choice
-  int pairs, n_max, slots, groups, split;
+  int pairs, n_max, slots, groups, split, run;
   int blocks[kSplitBelow];  // key blocks of the units, while there are few
   int split_of[kCandidates];
   float cost_of[kCandidates];
@@ -254,6 +254,10 @@ __device__ __forceinline__ void for_each_block(const VarParams& p, PlanSmem& s, 
 // first loads, last P V, epilogue); with splits of at most S blocks the launch takes about
 // max(S + 4, ceil(items / SMs) (mean + 4)), and 8 more to join them (a 512-token chunk over
 // 8192 cached tokens with 8 K/V heads has 64 items for 152 SMs). The least of a few S wins.
+// Or (p.runs, the calls over an 8-bit cache or with a tree) the blocks of all items, end to end,
+// are cut into equal runs, one per SM: an SM has a run's one or two pieces (the list's snake order
+// puts a large piece and a small one together), L + 8 in all, and there are fewer pieces to join (eight
+// trees of 32 tokens over 65,000 keys, 8 K/V heads: 456 pieces and 72.5 us, 208 and RUN_US).
 //
 // One CTA for a few microseconds, most of them spent fetching its instructions: the passes over
 // the units share one copy of the code, and units stay in registers when there are no more of
@@ -266,15 +270,44 @@ __global__ void __launch_bounds__(kPlanThreads) var_plan_kernel(const VarParams 
   if (tid == 0) {
     s.pairs = s.n_max = s.slots = s.groups = 0;
     s.split = INT_MAX;
+    s.run = 0;
   }
   __syncthreads();
   VarUnit mine;       // the last unit this thread has seen
   bool has = false, one_pass = false;
+  int before = 0;     // p.runs: key blocks of the units before mine
 #pragma unroll 1
   for (int pass = kCount; pass < kPasses; ++pass) {
-    const int split = s.split, n_max = s.n_max;
+    const int split = s.split, n_max = s.n_max, run = s.run;
+    // pieces of a unit of n blocks, and where piece k starts
+    auto pieces = [&](int n, int at) {
+      if (run) return n > 0 ? (at + n - 1) / run - at / run + 1 : 1;
+      return split == INT_MAX ? 1 : max(1, (n + split - 1) / split);
+    };
+    auto piece_at = [&](int n, int ns, int at, int k) {
+      if (run) return max(0, min(n, (at / run + k) * run - at));
+      return static_cast<int>(static_cast<long long>(n) * k / ns);
+    };
     if (pass == kTry) {
       if (!(p.part && s.pairs * p.Hkv < 2 * sms && s.pairs <= kSplitBelow && n_max >= 8)) continue;
+      if (p.runs && one_pass && static_cast<long long>(n_max) * s.pairs < (1 << 30) &&
+          (sms / p.Hkv + s.pairs) * p.Hkv <= kVarMaxSplit &&
+          sms / p.Hkv + s.pairs <= p.max_units) {
+        // runs: as many as there are SMs for a K/V head, and at most a piece more per unit
+        const int n = has ? mine.j1 : 0;
+        before = scan_cta<kPlanThreads>(n, s.scan.warp_sum) - n;
+        if (tid == 0) {
+          const int all = s.scan.warp_sum[kPlanThreads / 32 - 1], runs = sms / p.Hkv;
+          const int items = s.pairs * p.Hkv;
+          const float whole =
+              fmaxf(n_max + 4.f, ((items + sms - 1) / sms) * (static_cast<float>(all) / s.pairs + 4.f));
+          const int len = (all + runs - 1) / max(runs, 1);
+          // (an SM's run of pieces, and joining them)
+          if (runs > 1 && len + 16.f < whole) s.run = len;
+        }
+        __syncthreads();
+        continue;
+      }
       // warp c: sizes from the largest unit (no split) down to a third of an SM's share
       const int c = tid / 32, lane = tid % 32;
       long long cost = 0;  // of all units: 512 of 2^23 key blocks leave 32 bits
@@ -309,7 +342,7 @@ __global__ void __launch_bounds__(kPlanThreads) var_plan_kernel(const VarParams 
       continue;
     }
     if (pass == kRecount) {
-      if (split == INT_MAX) continue;
+      if (split == INT_MAX && !run) continue;
       for (int i = tid; i <= kBins; i += kPlanThreads) s.bins[i] = 0;
       __syncthreads();
     }
@@ -321,7 +354,7 @@ __global__ void __launch_bounds__(kPlanThreads) var_plan_kernel(const VarParams 
       }
     }
     auto visit = [&](VarUnit u) {
-      const int n = u.j1, ns = split == INT_MAX ? 1 : max(1, (n + split - 1) / split);
+      const int n = u.j1, ns = pieces(n, before);
       if (pass == kCount && p.part) {
         const int i = atomicAdd(&s.pairs, 1);
         if (i < kSplitBelow) s.blocks[i] = n;
@@ -332,8 +365,8 @@ __global__ void __launch_bounds__(kPlanThreads) var_plan_kernel(const VarParams 
         p.groups[atomicAdd(&s.groups, 1)] = VarGroup{u.q0, u.nq, u.slot, ns};
       }
       for (int k = 0; k < ns; ++k) {
-        u.j0 = static_cast<int>(static_cast<long long>(n) * k / ns);
-        u.j1 = static_cast<int>(static_cast<long long>(n) * (k + 1) / ns);
+        u.j0 = piece_at(n, ns, before, k);
+        u.j1 = piece_at(n, ns, before, k + 1);
         const int bin = cost_bin(u.j1 - u.j0, p.cost_shift);
         const int at = atomicAdd(&s.bins[pass == kWrite ? bin : bin + 1], 1);
         if (pass == kWrite && at >= 0 && at < p.max_units) p.units[at] = u;
@@ -341,7 +374,7 @@ __global__ void __launch_bounds__(kPlanThreads) var_plan_kernel(const VarParams 
       }
     };
     if (one_pass) {
-      const bool many = has && split != INT_MAX && mine.j1 > split;
+      const bool many = has && pieces(mine.j1, before) > 1;
       if (has && !many) visit(mine);
       // split units by the whole warp, one unit after the other, a piece per lane
       for (uint32_t rest = __ballot_sync(0xffffffffu, many); rest; rest &= rest - 1) {
@@ -351,7 +384,7 @@ __global__ void __launch_bounds__(kPlanThreads) var_plan_kernel(const VarParams 
         u.q0 = from(mine.q0), u.nq = from(mine.nq), u.sk = from(mine.sk), u.k0 = from(mine.k0);
         u.qpos = from(mine.qpos), u.seq = from(mine.seq);
         u.a_end = from(mine.a_end), u.b_start = from(mine.b_start), u.start = from(mine.start);
-        const int n = from(mine.j1), ns = (n + split - 1) / split;
+        const int n = from(mine.j1), at0 = from(before), ns = pieces(n, at0);
         int slot = 0;
         if (pass == kWrite && lane == 0) {
           slot = atomicAdd(&s.slots, ns);
@@ -359,8 +392,8 @@ __global__ void __launch_bounds__(kPlanThreads) var_plan_kernel(const VarParams 
         }
         slot = __shfl_sync(0xffffffffu, slot, 0);
         for (int k = lane; k < ns; k += 32) {
-          u.j0 = static_cast<int>(static_cast<long long>(n) * k / ns);
-          u.j1 = static_cast<int>(static_cast<long long>(n) * (k + 1) / ns);
+          u.j0 = piece_at(n, ns, at0, k);
+          u.j1 = piece_at(n, ns, at0, k + 1);
           u.slot = slot + k;
           const int bin = cost_bin(u.j1 - u.j0, p.cost_shift);
           const int at = atomicAdd(&s.bins[pass == kWrite ? bin : bin + 1], 1);

@@ -177,6 +177,7 @@ struct VarParams {
   float* part;    // slots, or nullptr: no splitting
   int max_units;  // entries of `units`
   int cost_shift; // key blocks >> cost_shift is a sort key below 1024
+  int runs;       // the plan may cut the items into equal runs (fa_varlen.cu)
 };
 
 struct VarLaunch {
