@@ -96,7 +96,7 @@ int shared_bytes(int tok, int half) { return tok * half * 8 + half * 9; }
 // Rows on their way: every thread copies its own 16-byte chunks of the rows to come to shared memory
 // (cp.async) and reads them back itself, so nothing waits for anyone else. In registers a row ahead is
 // what there is room for, 32 KB per SM on their way.
-constexpr int kStages = 4, kGradStages = 3;  // the gradient's rounds are twice as large
+constexpr int kStages = 4, kGradStages = 3;  // (the gradient's rounds are twice as large)
 __device__ __forceinline__ void copy_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }

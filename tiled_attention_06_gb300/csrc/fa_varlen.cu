@@ -374,7 +374,8 @@ __global__ void __launch_bounds__(kPlanThreads) var_plan_kernel(const VarParams 
       }
     };
     if (one_pass) {
-      const bool many = has && pieces(mine.j1, before) > 1;
+      // (runs leave a unit few pieces, which its thread writes itself)
+      const bool many = has && !run && pieces(mine.j1, before) > 1;
       if (has && !many) visit(mine);
       // split units by the whole warp, one unit after the other, a piece per lane
       for (uint32_t rest = __ballot_sync(0xffffffffu, many); rest; rest &= rest - 1) {
@@ -1165,7 +1166,7 @@ __global__ void __launch_bounds__(Cfg<D, FORM>::THREADS, 1)
 // group's slots in order. Rows without a token are skipped.
 constexpr int kMergeThreads = 512;
 template <int D, bool BF16>
-__global__ void __launch_bounds__(kMergeThreads) var_merge_kernel(const VarParams p) {
+__global__ void __launch_bounds__(kMergeThreads, 2) var_merge_kernel(const VarParams p) {
   constexpr int E = D / 32;  // elements per lane
   const int lane = threadIdx.x % 32;
   const int warps = gridDim.x * (kMergeThreads / 32), per = p.Hkv * kVarSplitRows;
@@ -1181,27 +1182,29 @@ __global__ void __launch_bounds__(kMergeThreads) var_merge_kernel(const VarParam
     const float* s0 = p.part + (static_cast<size_t>(g.slot) * p.Hkv + kvh) *
                                    (static_cast<size_t>(kVarSplitRows) * (D + 2));
     const float* row = s0 + static_cast<size_t>(r) * D + lane * E;
-    constexpr int N = 12;  // slots in flight
+    constexpr int N = 8;  // slots in flight
     float o[N][E];
     auto load = [&](int s1) {
 #pragma unroll
       for (int i = 0; i < N; ++i)
+        if (s1 + i < g.n) {
 #pragma unroll
-        for (int e = 0; e < E; e += 2) {
-          const float2 x = s1 + i < g.n ? *reinterpret_cast<const float2*>(row + (s1 + i) * step + e)
-                                        : make_float2(0.f, 0.f);
-          o[i][e] = x.x;
-          o[i][e + 1] = x.y;
+          for (int e = 0; e < E; e += 2) {
+            const float2 x = *reinterpret_cast<const float2*>(row + (s1 + i) * step + e);
+            o[i][e] = x.x;
+            o[i][e + 1] = x.y;
+          }
         }
     };
     load(0);  // beside the maxima and sums, one slot per lane
-    float M = -INFINITY, L = 0.f;
+    float M = -INFINITY, L = 0.f, m_own = -INFINITY;
     for (int s1 = 0; s1 < g.n; s1 += 32) {
       float m = -INFINITY, l = 0.f;
       if (s1 + lane < g.n) {
         m = s0[(s1 + lane) * step + kVarSplitRows * D + r];
         l = s0[(s1 + lane) * step + kVarSplitRows * (D + 1) + r];
       }
+      if (s1 == 0) m_own = m;
       float mx = fmaxf(M, m);
 #pragma unroll
       for (int i = 16; i > 0; i /= 2) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, i));
@@ -1216,16 +1219,20 @@ __global__ void __launch_bounds__(kMergeThreads) var_merge_kernel(const VarParam
     float acc[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = 0.f;
-    for (int s1 = 0;;) {
+    for (int s32 = 0; s32 < g.n; s32 += 32) {  // weights of 32 slots, one per lane
+      if (s32)
+        m_own = s32 + lane < g.n ? s0[(s32 + lane) * step + kVarSplitRows * D + r] : -INFINITY;
+      const float weight = ex2_approx(m_own - mu);
+      for (int s1 = s32; s1 < min(g.n, s32 + 32); s1 += N) {
+        if (s1) load(s1);
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const float m = s1 + i < g.n ? s0[(s1 + i) * step + kVarSplitRows * D + r] : -INFINITY;
-        const float wt = ex2_approx(m - mu);
+        for (int i = 0; i < N; ++i) {
+          const float wt = __shfl_sync(0xffffffffu, weight, (s1 - s32 + i) % 32);
+          if (s1 + i >= g.n) continue;
 #pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = fmaf(wt, o[i][e], acc[e]);
+          for (int e = 0; e < E; ++e) acc[e] = fmaf(wt, o[i][e], acc[e]);
+        }
       }
-      if ((s1 += N) >= g.n) break;
-      load(s1);
     }
     const float inv = L != 0.f ? 1.f / L : 0.f;
     const int h = kvh * p.G + (r % kTile) % p.G;
