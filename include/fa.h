@@ -596,7 +596,9 @@ fa_status fa_rope_axes(int32_t* pair_axis, int rot_dim, const int32_t* sections,
  * own, then rotate it, in one pass. With FA_NORM_RMS
  *     n = x / sqrt(mean(x^2) + eps) * weight     (over the d elements of a head; FP32),
  * with FA_NORM_NONE n = x; then y is n rotated as fa_rope does, pair i by the angle
- * positions[pair_axis[i]][token] * freqs[i]. One rounding, at the store.
+ * positions[pair_axis[i]][token] * freqs[i]. One rounding, at the store. The sum of squares is FP32:
+ * a row of elements beyond 1e18 or so is infinitely long and becomes zeros. With eps = 0 a row of
+ * zeros becomes NaN. Infinities and NaN stay within their row (and a weight's gradient).
  *   q, q_out   element e of head h of token t at t * q_token + h * q_head + e (and so on);
  *   k, k_out   the same for Hkv heads; Hkv = 0: none (k, k_out and k_weight are ignored).
  *              q_out may be q with the same steps (in place), and k_out k; otherwise outputs

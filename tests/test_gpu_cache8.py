@@ -157,7 +157,7 @@ def test_rows_of_very_different_sizes(lens, ctx, dtype, low, high):
 
 
 @pytest.mark.parametrize("lens,ctx", [([1, 2], [400, 130]), ([50], [500])])
-@pytest.mark.parametrize("size", [1e-30, 1e-3, 1e4, 1e30])
+@pytest.mark.parametrize("size", [1e-34, 1e-30, 1e-3, 1e4, 1e30, 1e37])
 def test_queries_of_any_size(lens, ctx, size):
     """bf16 queries far outside FP16's range, keys that bring the scores back."""
     T = sum(lens)

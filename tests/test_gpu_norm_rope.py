@@ -154,6 +154,31 @@ def test_gradient_against_differences():
         assert abs((a - b) / (2 * h) - got) <= 2.0 ** -8 * (1 + abs(got)), (got, (a - b) / (2 * h))
 
 
+@pytest.mark.parametrize("size", [1e-15, 1e-18, 1e15])
+def test_rows_far_from_one(size):
+    """Lengths whose cube leaves 32 bits, without an eps to hold them: the same directions."""
+    T, H, d = 5, 2, 64
+    x = (randn(T, H, d, seed=1) * size).to(BF)
+    dy = randn(T, H, d, dtype=BF, seed=2)
+    w = (1 + 0.2 * randn(d, seed=3)).to(BF)
+    pos, freqs = torch.arange(T, dtype=torch.int32), fa.fa_rope_freqs(d)[0]
+    args = (pos[None], torch.zeros(d // 2), freqs, d, True)
+    y, dx = (torch.empty(T, H, d, dtype=BF, device="cuda") for _ in range(2))
+    dw = torch.empty(d, device="cuda")
+    ws = torch.empty(fa.fa_norm_rope_bwd_workspace_size(H, 0, d), dtype=torch.uint8, device="cuda")
+    kw = dict(q_weight=w.cuda(), norm=fa.FA_NORM_RMS, eps=0.0)
+    fa.fa_norm_rope(x.cuda(), None, y, None, pos.cuda(), freqs.cuda(), **kw)
+    fa.fa_norm_rope_bwd(x.cuda(), None, dy.cuda(), None, dx, None, pos.cuda(), freqs.cuda(),
+                        dq_weight=dw, workspace=ws, **kw)
+    status_ok()
+    want, bound = c8.norm_rope(x, w, 0.0, *args)
+    c8.check(y, want, bound, BF, "y")
+    (gx, bx), (gw, bw) = c8.norm_rope_grad(x, w, 0.0, dy, *args)
+    scale = 2.0 ** round(math.log2(float(gx.abs().max())))  # exact in both
+    c8.check(dx.double() / scale, gx / scale, bx / scale, BF, "dx")
+    c8.check(dw, gw, bw, FP, "dw")
+
+
 def test_in_place_and_head_major_layouts():
     T, H, d = 37, 4, 64
     x = randn(H, T, d, dtype=BF, seed=3)  # [heads, tokens, d]

@@ -71,8 +71,8 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(x));
   return d;
 }
-// 2^(b - 127) of an exponent byte: an infinity for 255, 0 for 0 (2^-127, of a row that small).
-__device__ __forceinline__ float power8(uint32_t b) { return __uint_as_float(b << 23); }
+// 2^(b - 127) of an exponent byte: an infinity for 255, a subnormal for 0.
+__device__ __forceinline__ float power8(uint32_t b) { return __uint_as_float(max(b << 23, 0x400000u)); }
 // 2^(b - ref), 0 below 2^-126
 __device__ __forceinline__ float relative8(int b, int ref) {
   return __uint_as_float(static_cast<uint32_t>(max(b - ref + 127, 0)) << 23);
@@ -382,7 +382,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::CTAS)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const float x = half[b][0][e] + half[b][1][e];
-            s[b][mb][e] = fmaf(BF16 ? x * qs[b][e % 2] : x, e < 2 ? f0 : f1, e < 2 ? z0 : z1);
+            // (the powers together first: x times q's alone may leave FP32 where the score does not)
+            const float f = e < 2 ? f0 : f1;
+            s[b][mb][e] = fmaf(x, BF16 ? f * qs[b][e % 2] : f, e < 2 ? z0 : z1);
           }
       }
       // V's powers, a key to a lane: the running one covers the warp's keys, and the multipliers go

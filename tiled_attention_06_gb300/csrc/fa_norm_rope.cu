@@ -690,7 +690,8 @@ __global__ void __launch_bounds__(kMostThreads, VEC == 1 ? 1 : 2)
       T* const to = dst;
       dst += d_token * deal.per_round;
       if (!live) continue;
-      const float rr = rsqrtf(fmaf(ss, inv_d, p.eps)), c = -rr * rr * rr * (sg * inv_d);
+      // r x (sum) first: r^3 alone leaves FP32 for rows below 1e-13
+      const float rr = rsqrtf(fmaf(ss, inv_d, p.eps)), c = -(rr * (sg * inv_d)) * rr * rr;
       const uint64_t rr2 = f2(rr, rr), c2 = f2(c, c);
 #pragma unroll
       for (int i = 0; i < N2; ++i) {

@@ -644,8 +644,8 @@ __device__ __forceinline__ void convert_tile(const uint8_t* raw, uint32_t slot, 
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const uint32_t e = __byte_perm(b[i / 4], 0, 0x4440 + i % 4);
-      // 2^(e - 127): NaN for 255, 0 for 0 (2^-127)
-      const float f = __uint_as_float(e == 255 ? 0x7fffffffu : e << 23);
+      // 2^(e - 127): NaN for 255, a subnormal for 0
+      const float f = __uint_as_float(e == 255 ? 0x7fffffffu : max(e << 23, 0x400000u));
       const uint64_t power = WIDE ? f2(f, f) : e * 0x04000400u - 112u * 0x04000400u;
       const uint32_t in[4] = {flip ? x[i].z : x[i].x, flip ? x[i].w : x[i].y,
                               flip ? x[i].x : x[i].z, flip ? x[i].y : x[i].w};
