@@ -55,6 +55,10 @@ class Call:
         fa.fa_fwd_paged_varlen_ex(self.qd, self.k, self.v, self.table, self.ctx_d, self.cu, self.max_q,
                                   self.o, self.lse, self.scale, self.ws, stream=stream, **self.kw)
 
+    def run_and_check(self):
+        self.run()
+        self.check()
+
     def check(self, what=""):
         torch.cuda.synchronize()
         assert fa.fa_get_device_status() == fa.FA_OK
@@ -95,6 +99,33 @@ def test_trees(shape, bits):
     c = Call(*shape, bits=bits, mask=TREE, seed=3)
     c.run()
     c.check()
+
+
+LONG = [  # items cut into pieces for the SMs, among them sequences without keys or tokens
+    ([64], [6000], 8, 2, 128, 64, BF),
+    ([40, 0, 3, 64, 20], [5000, 4000, 0, 9000, 20], 4, 4, 64, 128, HF),
+    ([33, 200], [3000, 7000], 2, 1, 128, 16, HF),
+]
+
+
+@pytest.mark.parametrize("shape", LONG, ids=str)
+@pytest.mark.parametrize("mask", MASKS + [(WINDOW, 2500, 300), (BAND, 1500, 0)], ids=str)
+def test_pieces_over_8_bits(shape, mask):
+    test_positional_masks_over_8_bits(shape, mask)
+
+
+@pytest.mark.parametrize("bits", [8, 16])
+@pytest.mark.parametrize("shape", LONG, ids=str)
+def test_pieces_with_trees(shape, bits):
+    test_trees(shape, bits)
+
+
+@pytest.mark.parametrize("mask,bits", [(CAUSAL, 8), (WINDOW, 8), (TREE, 8), (TREE, 16)])
+@pytest.mark.parametrize("lens", [[1, 2, 0], [1, 17, 0]])
+def test_many_short_sequences(lens, mask, bits):
+    """More sequences than threads, few rows and tiles."""
+    Call(lens * 400, [3, 40, 0] * 400, 2, 1, 64, 16, BF, bits=bits, mask=mask,
+         window=2 if mask == WINDOW else 0, n_global=1 if mask == WINDOW else 0).run_and_check()
 
 
 @pytest.mark.parametrize("bits", [8, 16])

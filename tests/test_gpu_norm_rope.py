@@ -130,6 +130,49 @@ def test_norm_rope_gradient(case):
     assert all(torch.equal(a, b) for a, b in zip(again, (dx, *dw)))  # the same bits
 
 
+SPREAD = [  # heads over several CTAs, long runs of tokens per CTA, the last of them ragged
+    (7, 80, 8, 128, 128, 3, True, BF, BF, 1e-6),
+    (5, 33, 7, 256, 256, 2, False, HF, FP, 1e-6),
+    (3, 23, 9, 512, 512, 1, True, BF, BF, 1e-6),
+    (2, 700, 5, 64, 32, 1, False, BF, BF, 1e-6),
+    (2, 50, 1, 198, 66, 2, True, FP, FP, 1e-6),     # element by element
+    (20011, 2, 1, 64, 64, 2, True, BF, BF, 1e-6),
+    (15013, 1, 1, 34, 30, 1, False, HF, HF, 1e-6),
+    (9001, 1, 0, 16, 16, 4, True, FP, FP, 1e-6),
+]
+
+
+@pytest.mark.parametrize("case", SPREAD, ids=str)
+def test_many_heads_and_many_tokens(case):
+    test_norm_rope(case)
+    test_norm_rope_gradient(case)
+
+
+def test_gradients_on_two_streams_and_of_one_weight():
+    """Own workspaces, and either weight's gradient alone: the same as one after the other."""
+    T, H, Hkv, d = 600, 6, 2, 128
+    freqs, pos = fa.fa_rope_freqs(d)[0].cuda(), torch.arange(T, dtype=torch.int32).cuda()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    runs = []
+    for i, s in enumerate([None] * 3 + streams):
+        i %= 3
+        x = [randn(T, n, d, dtype=BF, seed=i + n).cuda() for n in (H, Hkv)]
+        dy = [randn(T, n, d, dtype=BF, seed=10 + i + n).cuda() for n in (H, Hkv)]
+        w = [(1 + 0.1 * randn(d, seed=i + n)).cuda() for n in range(2)]
+        dx, dw = [torch.empty_like(t) for t in x], [torch.full((d,), 7.0, device="cuda") for _ in w]
+        ws = torch.empty(fa.fa_norm_rope_bwd_workspace_size(H, Hkv, d), dtype=torch.uint8, device="cuda")
+        runs.append((x, dy, dx, w, dw, ws, s, i))
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for x, dy, dx, w, dw, ws, s, i in runs:
+            fa.fa_norm_rope_bwd(*x, *dy, *dx, pos, freqs, *w, dw[0] if i != 1 else None,
+                                dw[1] if i != 2 else None, ws, norm=fa.FA_NORM_RMS, stream=s)
+    status_ok()
+    for a, b in zip(runs[:3], runs[3:]):
+        assert all(torch.equal(u, v) for u, v in zip(a[2] + a[4], b[2] + b[4]))
+    assert (runs[1][4][0] == 7).all() and (runs[2][4][1] == 7).all()
+
+
 def test_gradient_against_differences():
     """A step of 2^-9 in 32 bits along a random direction: the difference quotient's own error is
     its third derivative (below 2^-12 here) and FP32 noise over the step (2^-22 * 2^9)."""
@@ -418,11 +461,19 @@ def test_append_with_bad_pages_and_starts():
     assert torch.isfinite(q_out[:2].float()).all() and (q_out[a.T:] == 7).all()
 
 
+@pytest.mark.parametrize("bits", [8, 16])
+def test_append_for_many_sequences_and_heads(bits):
+    """More sequences than a CTA has threads; heads over several CTAs; several batches of tokens."""
+    test_append(([1, 0, 2] * 300, [3, 40, 17] * 300, 2, 1, 64, 64, 16, 0, True, BF, bits, True))
+    test_append(([5, 30], [9, 2], 70, 10, 128, 128, 64, 3, True, HF, bits, True))
+    test_append(([6000, 1, 5000], [3, 200, 0], 1, 1, 64, 64, 256, 2, False, BF, bits, True))
+
+
 # ------------------------------------------------------------------------------ read back
 
 @pytest.mark.parametrize("lens,starts,Hkv,d,page,dtype", [
     ([1, 0, 5], [0, 3, 15], 1, 64, 16, BF), ([300, 17], [1, 250], 2, 128, 64, HF),
-    ([64], [64], 3, 128, 48, BF), ([3000, 8000, 1], [5, 0, 77], 1, 64, 256, HF)], ids=str)
+    ([64], [64], 3, 128, 48, BF), ([1, 0, 3] * 400, [7, 0, 20] * 400, 2, 64, 16, BF), ([3000, 8000, 1], [5, 0, 77], 1, 64, 256, HF)], ids=str)
 def test_read(lens, starts, Hkv, d, page, dtype):
     ctx = [n + s for n, s in zip(lens, starts)]
     cache = c8.Cache(ctx, Hkv, d, page, seed=3)

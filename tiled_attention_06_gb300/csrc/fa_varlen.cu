@@ -33,6 +33,17 @@
 // cycles (211 -> 203 us). Branches inside the softmax that skip hidden columns cost more than
 // they save (199 -> 212 us).
 //
+// Over an 8-bit cache (Q8) four more warps make 16-bit tiles of it: raw tiles, one byte per element and
+// one power of two per row, come into a ring of their own and leave it for the slots that the MMAs read;
+// the values are exact in BF16, and in FP16 wherever the power lets them be. A tile costs those
+// warps 1400 (FP16) to 1800 (BF16) cycles, and its 48 KB in and out of shared memory compete with the
+// operands of the MMAs. Eight chunks of up to 512 tokens over 30,000 keys, 32/8 heads of 128, bf16: 212 us,
+// 170 with the same cache in 16 bits; the bytes alone are 15 us, so the 8-bit cache saves room here,
+// not time. Tiles converted in place in five slots: 234; eight converting warps: no faster.
+//
+// With a tree a query's row of bits stands for the causal bound among the call's own tokens; the keys
+// before them are seen by all, so only key blocks that reach the own tokens read bits.
+//
 // Rows of V behind a sequence's last key belong to the next sequence, or are a page's unused
 // slots: their probability is 0, but 0 times an infinity or NaN is not. The MMA warp zeroes
 // them in shared memory before the block's P V; the scores of such keys are replaced by -inf.
@@ -256,8 +267,11 @@ __device__ __forceinline__ void for_each_block(const VarParams& p, PlanSmem& s, 
 // 8192 cached tokens with 8 K/V heads has 64 items for 152 SMs). The least of a few S wins.
 // Or (p.runs, the calls over an 8-bit cache or with a tree) the blocks of all items, end to end,
 // are cut into equal runs, one per SM: an SM has a run's one or two pieces (the list's snake order
-// puts a large piece and a small one together), L + 8 in all, and there are fewer pieces to join (eight
-// trees of 32 tokens over 65,000 keys, 8 K/V heads: 456 pieces and 72.5 us, 208 and RUN_US).
+// puts a large piece and a small one together), and there are fewer pieces to join. Over the best S:
+// eight trees of 32 tokens over 53,000 keys, 32/8 heads: 73.5 -> 68.0 us; over an 8-bit cache four chunks
+// of up to 300 tokens 134 -> 121, one of 512 175 -> 154; it loses where S happens to fit (two trees of
+// 64 tokens 64.0 -> 67.1, one of 64 over 8192 keys 41.0 -> 43.4). Calls over a 16-bit cache without a tree
+// keep the S they had, and their results with it.
 //
 // One CTA for a few microseconds, most of them spent fetching its instructions: the passes over
 // the units share one copy of the code, and units stay in registers when there are no more of
