@@ -612,7 +612,7 @@ static fa_status paged_varlen(const fa_paged_varlen_params& a, const fa_paged_va
   L.p.v_scales = x.v_scales;
   L.p.tree = x.tree;
   L.p.tree_words = x.tree_words;
-  L.p.runs = q8 || tree;
+  L.runs = q8 || tree;
   L.sms = dev.sms;
   if ((st = make_map3(&L.tmQ, a.q, bf16, a.d, a.H, a.d, a.total_q, a.q_token, L.p.G, L.p.TPT)) !=
           FA_OK ||

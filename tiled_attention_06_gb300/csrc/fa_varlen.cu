@@ -265,7 +265,7 @@ __device__ __forceinline__ void for_each_block(const VarParams& p, PlanSmem& s, 
 // first loads, last P V, epilogue); with splits of at most S blocks the launch takes about
 // max(S + 4, ceil(items / SMs) (mean + 4)), and 8 more to join them (a 512-token chunk over
 // 8192 cached tokens with 8 K/V heads has 64 items for 152 SMs). The least of a few S wins.
-// Or (p.runs, the calls over an 8-bit cache or with a tree) the blocks of all items, end to end,
+// Or (RUNS, the calls over an 8-bit cache or with a tree) the blocks of all items, end to end,
 // are cut into equal runs, one per SM: an SM has a run's one or two pieces (the list's snake order
 // puts a large piece and a small one together), and there are fewer pieces to join. Over the best S:
 // eight trees of 32 tokens over 53,000 keys, 32/8 heads: 73.5 -> 68.0 us; over an 8-bit cache four chunks
@@ -275,8 +275,9 @@ __device__ __forceinline__ void for_each_block(const VarParams& p, PlanSmem& s, 
 //
 // One CTA for a few microseconds, most of them spent fetching its instructions: the passes over
 // the units share one copy of the code, and units stay in registers when there are no more of
-// them than threads.
+// them than threads. RUNS is a kernel of its own because its code would cost the others 2 us.
 enum { kCount, kTry, kRecount, kWrite, kPasses };
+template <bool RUNS>
 __global__ void __launch_bounds__(kPlanThreads) var_plan_kernel(const VarParams p, int sms) {
   __shared__ PlanSmem s;
   const int tid = threadIdx.x;
@@ -289,10 +290,10 @@ __global__ void __launch_bounds__(kPlanThreads) var_plan_kernel(const VarParams 
   __syncthreads();
   VarUnit mine;       // the last unit this thread has seen
   bool has = false, one_pass = false;
-  int before = 0;     // p.runs: key blocks of the units before mine
+  int before = 0;     // RUNS: key blocks of the units before mine
 #pragma unroll 1
   for (int pass = kCount; pass < kPasses; ++pass) {
-    const int split = s.split, n_max = s.n_max, run = s.run;
+    const int split = s.split, n_max = s.n_max, run = RUNS ? s.run : 0;
     // pieces of a unit of n blocks, and where piece k starts
     auto pieces = [&](int n, int at) {
       if (run) return n > 0 ? (at + n - 1) / run - at / run + 1 : 1;
@@ -304,7 +305,7 @@ __global__ void __launch_bounds__(kPlanThreads) var_plan_kernel(const VarParams 
     };
     if (pass == kTry) {
       if (!(p.part && s.pairs * p.Hkv < 2 * sms && s.pairs <= kSplitBelow && n_max >= 8)) continue;
-      if (p.runs && one_pass && static_cast<long long>(n_max) * s.pairs < (1 << 30) &&
+      if (RUNS && one_pass && static_cast<long long>(n_max) * s.pairs < (1 << 30) &&
           (sms / p.Hkv + s.pairs) * p.Hkv <= kVarMaxSplit &&
           sms / p.Hkv + s.pairs <= p.max_units) {
         // runs: as many as there are SMs for a K/V head, and at most a piece more per unit
@@ -613,11 +614,10 @@ __device__ __forceinline__ void widen8(uint32_t x, uint64_t power, uint32_t& lo,
     hi = BF16 ? cvt_pack_bf16(u, v) : cvt_pack_f16(u, v);
   }
 }
-// One slot by the 128 threads of the converting warps: rows of D bytes in its second half and their
-// exponent bytes to the 128-byte swizzle of a 16-bit tile over the whole slot; rows from `live` on
-// become zeros. A thread takes 16 elements of N neighbouring rows, whose exponents are one access, and
-// holds them before any thread writes. Lanes that would meet in a bank store their halves in the other
-// order. False when some thread came with !ok; nothing is written then.
+// One tile by the 128 threads of the converting warps: raw rows of D bytes and their exponent bytes to
+// the 128-byte swizzle of a 16-bit tile; rows from `live` on become zeros. A thread takes 16 elements of
+// N neighbouring rows, whose exponents are one access. Lanes that would meet in a bank store their halves
+// in the other order.
 template <int D, bool BF16>
 __device__ __forceinline__ void convert_tile(const uint8_t* raw, uint32_t slot, int live, int t) {
   const uint8_t* scales = raw + BN * D;
@@ -1273,7 +1273,10 @@ cudaError_t launch_fwd(const VarLaunch& L, int grid, cudaStream_t stream) {
 
 template <int D, bool BF16>
 cudaError_t launch_t(const VarLaunch& L, cudaStream_t stream) {
-  var_plan_kernel<<<1, kPlanThreads, 0, stream>>>(L.p, L.sms);
+  if (L.runs)
+    var_plan_kernel<true><<<1, kPlanThreads, 0, stream>>>(L.p, L.sms);
+  else
+    var_plan_kernel<false><<<1, kPlanThreads, 0, stream>>>(L.p, L.sms);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const int64_t items = static_cast<int64_t>(L.p.max_units) * L.p.Hkv;

@@ -177,13 +177,13 @@ struct VarParams {
   float* part;    // slots, or nullptr: no splitting
   int max_units;  // entries of `units`
   int cost_shift; // key blocks >> cost_shift is a sort key below 1024
-  int runs;       // the plan may cut the items into equal runs (fa_varlen.cu)
 };
 
 struct VarLaunch {
   CUtensorMap tmQ, tmK, tmV, tmO;
   VarParams p;
   int sms;
+  bool runs;  // the plan may cut the items into equal runs (fa_varlen.cu)
 };
 cudaError_t launch_varlen(const VarLaunch& L, int D, bool bf16, cudaStream_t stream);
 
