@@ -609,9 +609,10 @@ fa_status fa_rope_axes(int32_t* pair_axis, int rot_dim, const int32_t* sections,
  *   freqs      float64 [rot_dim / 2], device
  *   q_weight, k_weight  [d] of weight_dtype (FA_F32 or dtype); NULL: ones. Ignored without a norm.
  *   T >= 0, H >= 1, Hkv >= 0, d even in [2, 512], rot_dim even in [2, d], axes in
- *   [1, FA_MAX_AXES], eps >= 0; dtype FA_F16, FA_BF16 or FA_F32. Alignment as for fa_rope: with
- *   16-byte aligned pointers, steps of a multiple of 16 bytes and rot_dim and d a multiple of 32
- *   bytes, heads move in 16-byte accesses, else element by element.
+ *   [1, FA_MAX_AXES], eps >= 0; dtype FA_F16, FA_BF16 or FA_F32. With 16-byte aligned pointers,
+ *   steps of a multiple of 16 bytes and d a multiple of 32 bytes, heads move in 16-byte accesses
+ *   (FA_ROPE_HALF: in the largest part of them that divides rot_dim / 2 elements), else element by
+ *   element.
  */
 typedef struct fa_norm_rope_params {
   const void* q;

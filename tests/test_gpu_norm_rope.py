@@ -148,6 +148,45 @@ def test_many_heads_and_many_tokens(case):
     test_norm_rope_gradient(case)
 
 
+CHUNKS = [  # rotated parts that end inside 16 bytes, rows of three, five and six lanes
+    (45, 6, 2, 128, 66, 1, False, BF, BF, 1e-6),
+    (45, 6, 2, 128, 66, 1, True, BF, BF, 1e-6),
+    (31, 3, 1, 64, 40, 2, True, HF, HF, 1e-6),
+    (31, 3, 1, 64, 36, 2, True, BF, FP, 1e-6),
+    (31, 3, 1, 64, 38, 3, False, HF, HF, 1e-6),
+    (26, 4, 2, 64, 20, 1, True, FP, FP, 1e-6),
+    (26, 4, 2, 64, 22, 1, False, FP, FP, 1e-6),
+    (26, 4, 2, 64, 22, 1, True, FP, FP, 1e-6),
+    (300, 8, 2, 80, 80, 3, True, BF, BF, 1e-6),
+    (301, 7, 3, 96, 96, 1, False, HF, HF, 1e-6),
+    (77, 7, 3, 96, 2, 1, True, BF, BF, 1e-6),
+    (1203, 5, 1, 48, 48, 1, True, BF, BF, 1e-6),
+    (50, 2, 1, 256, 250, 1, False, BF, BF, 1e-6),
+    (50, 2, 1, 80, 76, 4, True, FP, FP, 1e-6),
+    (9, 41, 7, 80, 18, 2, False, BF, BF, 1e-6),
+]
+
+
+@pytest.mark.parametrize("case", CHUNKS, ids=str)
+def test_chunks_and_groups(case):
+    test_norm_rope(case)
+    test_norm_rope_gradient(case)
+
+
+def test_elements_behind_the_rotated_part_are_copied():
+    T, H, d, rot = 6, 2, 64, 38
+    x = randn(T, H, d, dtype=BF, seed=1)
+    x[:, :, rot:] = torch.tensor([float("inf"), -0.0, float("-inf"), 1.0])[torch.arange(d - rot) % 4].to(BF)
+    freqs = fa.fa_rope_freqs(rot)[0].cuda()
+    for style in (fa.FA_ROPE_HALF, fa.FA_ROPE_PAIRS):
+        y = torch.empty_like(x).cuda()
+        fa.fa_norm_rope(x.cuda(), None, y, None, torch.arange(T, dtype=torch.int32).cuda(), freqs,
+                        style=style)
+        status_ok()
+        assert torch.equal(y[:, :, rot:].cpu().view(torch.int16), x[:, :, rot:].view(torch.int16))
+        assert torch.isfinite(y[:, :, :rot]).all()
+
+
 def test_gradients_on_two_streams_and_of_one_weight():
     """Own workspaces, and either weight's gradient alone: the same as one after the other."""
     T, H, Hkv, d = 600, 6, 2, 128
@@ -459,6 +498,12 @@ def test_append_with_bad_pages_and_starts():
     torch.cuda.synchronize()
     assert fa.fa_get_device_status() == fa.FA_ERR_BAD_PAGE
     assert torch.isfinite(q_out[:2].float()).all() and (q_out[a.T:] == 7).all()
+
+
+@pytest.mark.parametrize("rot,half", [(66, True), (66, False), (40, True), (36, True), (72, False)])
+@pytest.mark.parametrize("bits", [8, 16])
+def test_append_of_rotated_parts_that_end_inside_16_bytes(rot, half, bits):
+    test_append(([3, 0, 70, 1], [5, 9, 60, 0], 6, 3, 128, rot, 64, 3, half, HF, bits, True))
 
 
 @pytest.mark.parametrize("bits", [8, 16])

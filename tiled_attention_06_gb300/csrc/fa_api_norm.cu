@@ -113,12 +113,6 @@ void fill_turn(fa::NormRopeParams* p, const Turn& t) {
   p->q_weight = t.norm == FA_NORM_RMS ? t.q_weight : nullptr;
   p->k_weight = t.norm == FA_NORM_RMS ? t.k_weight : nullptr;
 }
-// 16-byte accesses, two to a unit
-bool wide_heads(const Turn& t) {
-  const int unit = static_cast<int>(32 / elem_size(t.dtype));
-  return t.d % unit == 0 && t.rot_dim % unit == 0;
-}
-
 Turn turn_of(const fa_norm_rope_params& a) {
   return Turn{a.d,   a.rot_dim,   a.axes,      a.style, a.norm,     a.weight_dtype, a.dtype, a.amplitude,
               a.eps, a.positions, a.pair_axis, a.freqs, a.q_weight, a.k_weight};
@@ -201,7 +195,7 @@ fa_status fa_norm_rope(const fa_norm_rope_params* params, fa_stream_t stream) {
                         {"q_out", a.q_out, a.q_out_token, a.q_out_head, true},
                         {"k", a.k, a.k_token, a.k_head, false},
                         {"k_out", a.k_out, a.k_out_token, a.k_out_head, true}};
-  bool vec = wide_heads(t);
+  bool vec = true;
   for (int i = 0; i < (a.Hkv ? 4 : 2); ++i) {
     if ((st = check_rows(rows[i], a.T, i < 2 ? a.H : a.Hkv, a.d, es)) != FA_OK) return st;
     if (i % 2 && (st = check_in_place(rows[i - 1], rows[i])) != FA_OK) return st;
@@ -271,7 +265,7 @@ fa_status fa_norm_rope_bwd(const fa_norm_rope_params* params, const fa_norm_rope
                         {"dk_out", g.dk_out, g.dk_out_token, g.dk_out_head, false},
                         {"dk", g.dk, g.dk_token, g.dk_head, true},
                         {"k", a.k, a.k_token, a.k_head, false}};
-  bool vec = wide_heads(t);
+  bool vec = true;
   for (int i = 0; i < (a.Hkv ? 6 : 3); ++i) {
     if (i % 3 == 2 && !norm) continue;  // the input is not read
     if ((st = check_rows(rows[i], a.T, i < 3 ? a.H : a.Hkv, a.d, es)) != FA_OK) return st;
@@ -392,7 +386,7 @@ fa_status fa_norm_rope_append(const fa_norm_rope_append_params* params, fa_strea
   p.num_pages = a.num_pages;
   p.status = dev.status;
   const cudaError_t e =
-      fa::launch_norm_rope_append(p, a.dtype, a.style == FA_ROPE_HALF, wide_heads(t), dev.sms,
+      fa::launch_norm_rope_append(p, a.dtype, a.style == FA_ROPE_HALF, true, dev.sms,
                                   reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "norm rope append launch");
   return FA_OK;

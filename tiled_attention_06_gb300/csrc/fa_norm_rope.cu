@@ -22,10 +22,12 @@
 // rows come three rounds ahead by cp.async. With rows dealt to groups in order, whatever their token and
 // head, addresses and weights cost a row more instructions than its arithmetic and 16384 tokens x 40
 // heads of 128 in bf16 took 68 us and their gradient 117; so they take 62.5 (5370 GB/s, 80 % of the
-// measured copy rate) and 97 (5190 GB/s).
+// measured copy rate) and 95 (5290 GB/s). Halves of the rotated part that are no multiple of 16 bytes move in
+// chunks of 8 or 4 (8192 tokens, 72 or 68 of 128 elements rotated: 57 us element by element, 33 and 39).
 #include <algorithm>
 #include <climits>
 #include <cstdint>
+#include <type_traits>
 
 #include "fa_ptx.cuh"
 #include "fa_rope.cuh"
@@ -87,19 +89,24 @@ struct Shared {
   float2* cs;
   uint64_t* freq;
   uint8_t* axis;
-  __device__ __forceinline__ Shared(float4* base, int tok, int half) {
+  __device__ __forceinline__ Shared(float4* base, int pairs, int half) {
     cs = reinterpret_cast<float2*>(base);
-    freq = reinterpret_cast<uint64_t*>(cs + static_cast<size_t>(tok) * half);
+    freq = reinterpret_cast<uint64_t*>(cs + pairs);
     axis = reinterpret_cast<uint8_t*>(freq + half);
   }
 };
-int shared_bytes(int tok, int half) { return tok * half * 8 + half * 9; }
-// Rows on their way: every thread copies its own 16-byte chunks of the rows to come to shared memory
+int shared_bytes(int pairs, int half) { return pairs * 8 + half * 9; }
+// Rows on their way: every thread copies its own chunks of the rows to come to shared memory
 // (cp.async) and reads them back itself, so nothing waits for anyone else. In registers a row ahead is
 // what there is room for, 32 KB per SM on their way.
-constexpr int kStages = 4, kGradStages = 3;  // (the gradient's rounds are twice as large)
-__device__ __forceinline__ void copy_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+constexpr int kStages = 4;
+constexpr int grad_stages(int chunks) { return chunks == 1 ? 3 : 2; }  // rounds of x and dy, FP32's of twice that
+template <int N>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {
+  if constexpr (N == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(N) : "memory");
 }
 __device__ __forceinline__ void copy_commit() {
   asm volatile("cp.async.commit_group;" ::: "memory");
@@ -130,9 +137,18 @@ struct Ahead {
     if (p.pos && i < nt * p.axes) pos = p.pos[(i / nt) * p.T + t0 + i % nt];
   }
 };
-// Frequencies and axes: the part that does not depend on the tokens.
+// Frequencies and axes, and the pairs behind the last rotated one that share its unit (neighbours):
+// the part that does not depend on the tokens.
+template <int VEC>
 __device__ __forceinline__ void fill_fixed(const NormRopeParams& p, const Shared& sh,
-                                           const Ahead& first) {
+                                           const Ahead& first, int tok, int slots) {
+  const int rest = slots - p.rot / 2;
+  for (int i = threadIdx.x; i < tok * rest; i += blockDim.x) {
+    const int tk = i / rest, f = p.rot / 2 + i - tk * rest;
+    float* const to = reinterpret_cast<float*>(sh.cs + tk * slots) + pair_at<VEC>(f / VEC, f % VEC, slots / VEC);
+    to[0] = 1.f;
+    to[VEC == 1 ? 1 : 2] = 0.f;
+  }
   for (int i = threadIdx.x; i < p.rot / 2; i += blockDim.x) {
     const bool mine = i == static_cast<int>(threadIdx.x);
     sh.freq[i] = turns_q64(mine ? first.freq : p.freqs[i]);
@@ -154,9 +170,9 @@ __device__ __forceinline__ void fill_positions(const NormRopeParams& p, int64_t 
 }
 // Sines and cosines of nt tokens; pos(axis, token) in 64 bits.
 template <int VEC, typename Pos>
-__device__ __forceinline__ void fill_angles(const NormRopeParams& p, int nt, const Shared& sh,
+__device__ __forceinline__ void fill_angles(const NormRopeParams& p, int nt, const Shared& sh, int slots,
                                             bool inverse, Pos pos) {
-  const int half = p.rot / 2, ru = half / VEC;
+  const int half = p.rot / 2, ru = slots / VEC;
   const int dt = blockDim.x / half, df = blockDim.x % half;
   int tk = threadIdx.x / half, f = threadIdx.x % half;
   while (tk < nt) {
@@ -164,7 +180,7 @@ __device__ __forceinline__ void fill_angles(const NormRopeParams& p, int nt, con
     const uint64_t phase = static_cast<uint64_t>(inverse ? -at : at) * sh.freq[f];
     float s, c;  // the phase as a signed fraction of a turn: half turns in [-1, 1]
     sincospif(static_cast<float>(static_cast<int64_t>(phase)) * 1.08420217248550443e-19f, &s, &c);
-    float* const to = reinterpret_cast<float*>(sh.cs + tk * half) + pair_at<VEC>(f / VEC, f % VEC, ru);
+    float* const to = reinterpret_cast<float*>(sh.cs + tk * slots) + pair_at<VEC>(f / VEC, f % VEC, ru);
     to[0] = c * p.amplitude;
     to[VEC == 1 ? 1 : 2] = s * p.amplitude;
     tk += dt;
@@ -183,8 +199,7 @@ __device__ __forceinline__ float f2_sum(uint64_t a) {
 }
 
 template <typename C>
-__device__ __forceinline__ C load_shared16(uint32_t at) {
-  static_assert(sizeof(C) == 16 || sizeof(C) < 16, "one access");
+__device__ __forceinline__ C load_chunk(uint32_t at) {
   C c;
   if constexpr (sizeof(C) == 16) {
     uint32_t r[4];
@@ -193,6 +208,14 @@ __device__ __forceinline__ C load_shared16(uint32_t at) {
                  : "r"(at)
                  : "memory");
     __builtin_memcpy(&c, r, 16);
+  } else if constexpr (sizeof(C) == 8) {
+    uint32_t r[2];
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(at) : "memory");
+    __builtin_memcpy(&c, r, 8);
+  } else if constexpr (sizeof(C) == 4) {
+    uint32_t r;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(r) : "r"(at) : "memory");
+    __builtin_memcpy(&c, &r, 4);
   }
   return c;
 }
@@ -224,16 +247,16 @@ struct Part {
 #pragma unroll
     for (int k = 0; k < KU; ++k)
       if (k < have) {
-        copy_async16(at + (2 * k) * step, src + oa[k]);
-        copy_async16(at + (2 * k + 1) * step, src + ob[k]);
+        copy_async<sizeof(C)>(at + (2 * k) * step, src + oa[k]);
+        copy_async<sizeof(C)>(at + (2 * k + 1) * step, src + ob[k]);
       }
   }
   // (a chunk that the row does not have is whatever lies there; its elements are zeroed)
   __device__ __forceinline__ void take(uint32_t at, uint32_t step, int have) {
 #pragma unroll
     for (int k = 0; k < KU; ++k) {
-      a[k] = load_shared16<C>(at + (2 * k) * step);
-      b[k] = load_shared16<C>(at + (2 * k + 1) * step);
+      a[k] = load_chunk<C>(at + (2 * k) * step);
+      b[k] = load_chunk<C>(at + (2 * k + 1) * step);
       if (k >= have) {
 #pragma unroll
         for (int e = 0; e < VEC; ++e) a[k].e[e] = b[k].e[e] = T(0);
@@ -299,24 +322,26 @@ __device__ __forceinline__ void angles_of(const float* at, int i, int u0, int ln
 }
 // The rotation of a lane's pairs, (A, B) to (A c - B s, B c + A s), with nB = -B; those behind the
 // rotated part stay.
-template <int VEC, int N2>
+template <int VEC, int N2, bool RAGGED>
 __device__ __forceinline__ void turn(uint64_t* A, uint64_t* B, const uint64_t* nB, const float2* cs,
-                                     int u0, int ln, int ru) {
+                                     int u0, int ln, int ru, int half) {
 #pragma unroll
   for (int i = 0; i < N2; ++i) {
     uint64_t c, s;
     angles_of<VEC>(reinterpret_cast<const float*>(cs), i, u0, ln, ru, c, s);
-    if (VEC == 1) {  // two units, of which the rotated part may end with the first
-      const bool in0 = u0 + 2 * i * ln < ru, in1 = u0 + (2 * i + 1) * ln < ru;
-      const uint64_t lo = 0xffffffffull, one = 0x3f800000ull;
-      if (!in0) c = (c & ~lo) | one, s &= ~lo;
-      if (!in1) c = (c & lo) | one << 32, s &= lo;
-    } else if (u0 + (2 * i / VEC) * ln >= ru) {
-      continue;
-    }
-    const uint64_t a = A[i];
+    if (VEC > 1 && u0 + (2 * i / VEC) * ln >= ru) continue;
+    const uint64_t a = A[i], b = B[i];
     A[i] = f2_fma(a, c, f2_mul(nB[i], s));
-    B[i] = f2_fma(B[i], c, f2_mul(a, s));
+    B[i] = f2_fma(b, c, f2_mul(a, s));
+    // pairs behind the last rotated one stay as they are, infinities too: the second of two units, or
+    // neighbours that share its unit
+    if (VEC == 1 || RAGGED) {
+      const int in = VEC == 1 ? (u0 + 2 * i * ln < ru) + (u0 + (2 * i + 1) * ln < ru)
+                              : half - (u0 + (2 * i / VEC) * ln) * VEC - 2 * i % VEC;
+      const uint64_t keep = in < 1 ? ~0ull : in < 2 ? ~0ull << 32 : 0ull;
+      A[i] = (A[i] & ~keep) | (a & keep);
+      B[i] = (B[i] & ~keep) | (b & keep);
+    }
   }
 }
 // The weights of a lane's elements, as its pairs lie; 0 where the row has no element. All loads of a
@@ -390,10 +415,16 @@ struct Mine {
   }
 };
 
+// Three of 64 registers a thread where those do; with the cache's addresses and bytes they spill (chunks
+// of 8 sequences of up to 512 tokens, 8 bits: 14.9 us, 13.6 with two).
+constexpr int ctas_per_sm(int dt, int vec, int mode) {
+  return dt != FA_F32 && vec == 8 && mode == 0 ? 3 : 2;
+}
+
 // Rows r of a token: H of q, Hkv of k and, when appending, Hkv of v. MODE 0: y to q_out and k_out;
 // 1 and 2: q to q_out, k and v to the cache's slot of the token, in 16 and in 8 bits.
-template <int DT, int VEC, int KU, bool HALF, int MODE>
-__global__ void __launch_bounds__(kMostThreads, DT != FA_F32 && VEC > 1 ? 3 : 2)
+template <int DT, int VEC, int KU, bool HALF, bool RAGGED, int MODE>
+__global__ void __launch_bounds__(kMostThreads, ctas_per_sm(DT, VEC, MODE))
     norm_rope_kernel(const __grid_constant__ NormRopeParams p, const Deal deal) {
   using T = typename Elem<DT>::T;
   using X = Part<DT, VEC, KU, HALF>;
@@ -401,13 +432,16 @@ __global__ void __launch_bounds__(kMostThreads, DT != FA_F32 && VEC > 1 ? 3 : 2)
   extern __shared__ float4 s_dyn[];
   __shared__ int64_t s_dst[kTokMax], s_pos[FA_MAX_AXES][kTokMax];
   __shared__ int s_seq[kTokMax];
-  const int half = p.rot / 2, ru = half / VEC, U = p.d / (2 * VEC), ln = deal.ln;
+  const int half = p.rot / 2, ru = (half + VEC - 1) / VEC, slots = ru * VEC;
+  const int U = p.d / (2 * VEC), ln = deal.ln;
   // chunk c of round i of the thread at ((i % kStages) * 2 KU + c) * step
-  const uint32_t step = blockDim.x * 16, stage = 2 * KU * step;
-  const uint32_t ring = smem_u32(s_dyn) + threadIdx.x * 16;
-  const Shared sh(s_dyn + (VEC == 1 ? 0 : kStages * 2 * KU * blockDim.x), deal.tok, half);
-  const int gl = threadIdx.x % ln, rows = MODE ? p.H + 2 * p.Hkv : p.H + p.Hkv;
+  constexpr int CB = sizeof(typename X::C);  // bytes of a chunk
+  const uint32_t step = blockDim.x * CB, stage = 2 * KU * step;
+  const uint32_t ring = smem_u32(s_dyn) + threadIdx.x * CB;
+  const Shared sh(s_dyn + (VEC == 1 ? 0 : kStages * 2 * KU * CB / 16 * blockDim.x), deal.tok * slots, half);
+  const int rows = MODE ? p.H + 2 * p.Hkv : p.H + p.Hkv;
   const Mine me(p, deal, rows);
+  const int gl = threadIdx.x % ln;
   const bool is_q = me.r < p.H, is_v = MODE && me.r >= p.H + p.Hkv;
   const int h = is_q ? me.r : me.r - p.H - (is_v ? p.Hkv : 0);  // head of q, k or v
   int oa[KU], ob[KU], have = 0;
@@ -442,8 +476,11 @@ __global__ void __launch_bounds__(kMostThreads, DT != FA_F32 && VEC > 1 ? 3 : 2)
   uint64_t wA[N2], wB[N2];
   if (p.norm && !is_v)
     weights_of<DT, VEC, KU, HALF>(p, is_q ? p.q_weight : p.k_weight, oa, ob, have, wA, wB);
+  // warps whose groups are all v's form no norm, those with none of k or v no bytes
+  const bool normed = p.norm && __any_sync(kAll, !is_v);
+  const bool cached = MODE == 2 && __any_sync(kAll, me.on && !is_q);
   const float inv_d = 1.f / p.d;
-  fill_fixed(p, sh, first);
+  fill_fixed<VEC>(p, sh, first, deal.tok, slots);
   for (int64_t t0 = me.begin; t0 < me.end; t0 += deal.tok) {
     const int nt = static_cast<int>(min(static_cast<int64_t>(deal.tok), me.end - t0));
     if constexpr (MODE) {
@@ -471,7 +508,7 @@ __global__ void __launch_bounds__(kMostThreads, DT != FA_F32 && VEC > 1 ? 3 : 2)
     }
     if (p.pos) fill_positions(p, s_pos, t0, nt, t0 == me.begin, first);
     __syncthreads();  // also: the last batch's sines have been read
-    fill_angles<VEC>(p, nt, sh, p.inverse != 0, [&](int a, int i) { return s_pos[a][i]; });
+    fill_angles<VEC>(p, nt, sh, slots, p.inverse != 0, [&](int a, int i) { return s_pos[a][i]; });
     __syncthreads();
     // every lane goes round alike; the last round may have no token for it
     for (int tk = me.tr; tk - me.tr < nt; tk += deal.per_round) {
@@ -489,7 +526,7 @@ __global__ void __launch_bounds__(kMostThreads, DT != FA_F32 && VEC > 1 ? 3 : 2)
       }
       uint64_t A[N2], B[N2];
       x.widen(A, B);
-      if (p.norm) {  // (elements that the row does not have are zeros)
+      if (normed) {  // (elements that the row does not have are zeros)
         uint64_t sa = 0, sb = 0;
 #pragma unroll
         for (int i = 0; i < N2; ++i) {
@@ -512,23 +549,20 @@ __global__ void __launch_bounds__(kMostThreads, DT != FA_F32 && VEC > 1 ? 3 : 2)
         uint64_t nB[N2];
 #pragma unroll
         for (int i = 0; i < N2; ++i) nB[i] = f2_mul(B[i], minus);
-        turn<VEC, N2>(A, B, nB, sh.cs + tk * half, gl, ln, ru);
+        turn<VEC, N2, RAGGED>(A, B, nB, sh.cs + tk * slots, gl, ln, ru, half);
       }
       const int64_t slot = MODE && live ? s_dst[tk] : 0;
-      if (MODE == 2) {  // every group of the warp takes part in the shuffles
-        // the largest magnitude, which passes over NaNs, and zero times everything, which does not
+      if (MODE == 2 && cached) {  // every group of the warp takes part in the shuffles
         float big = 0.f;
-        uint64_t nan = 0;
 #pragma unroll
         for (int i = 0; i < N2; ++i) {
           float u, v;
           f2_split(A[i], u, v);
-          big = max3f(big, fabsf(u), fabsf(v));
+          big = max3_abs_nan(big, u, v);
           f2_split(B[i], u, v);
-          big = max3f(big, fabsf(u), fabsf(v));
-          nan = f2_fma(A[i], 0, f2_fma(B[i], 0, nan));
+          big = max3_abs_nan(big, u, v);
         }
-        uint32_t bits = f2_sum(nan) == 0.f ? __float_as_uint(big) : 0x7f800000u;
+        uint32_t bits = __float_as_uint(big);  // (a NaN's are above an infinity's)
         for (int o = ln / 2; o > 0; o /= 2) bits = max(bits, __shfl_xor_sync(kAll, bits, o));
         if (live && !is_q && slot >= 0) {
           const int byte = power_byte(bits);
@@ -590,21 +624,23 @@ __global__ void __launch_bounds__(kMostThreads, DT != FA_F32 && VEC > 1 ? 3 : 2)
 // The gradient. A thread has the same elements of one head of every token, so the weight's gradient
 // adds up in its registers; they meet once at the end, per CTA, in a fixed order, and
 // norm_rope_sum_kernel adds the CTAs in theirs: the same bits on every run of the same sizes.
-template <int DT, int VEC, int KU, bool HALF>
+template <int DT, int VEC, int KU, bool HALF, bool RAGGED>
 __global__ void __launch_bounds__(kMostThreads, VEC == 1 ? 1 : 2)
     norm_rope_bwd_kernel(const __grid_constant__ NormRopeParams p, const Deal deal) {
   using T = typename Elem<DT>::T;
   using X = Part<DT, VEC, KU, HALF>;
-  constexpr int N2 = X::N2;
+  constexpr int N2 = X::N2, kGradStages = grad_stages(KU * VEC * sizeof(T) / 16);
   extern __shared__ float4 s_dyn[];
   __shared__ int64_t s_pos[FA_MAX_AXES][kTokMax];
-  const int half = p.rot / 2, ru = half / VEC, U = p.d / (2 * VEC), ln = deal.ln;
-  const uint32_t step = blockDim.x * 16, stage = 4 * KU * step;
-  const uint32_t ring = smem_u32(s_dyn) + threadIdx.x * 16;
-  const Shared sh(s_dyn + (VEC == 1 ? 0 : kGradStages * 4 * KU * blockDim.x), deal.tok, half);
-  const int gl = threadIdx.x % ln;
+  const int half = p.rot / 2, ru = (half + VEC - 1) / VEC, slots = ru * VEC;
+  const int U = p.d / (2 * VEC), ln = deal.ln;
+  constexpr int CB = sizeof(typename X::C);
+  const uint32_t step = blockDim.x * CB, stage = 4 * KU * step;
+  const uint32_t ring = smem_u32(s_dyn) + threadIdx.x * CB;
+  const Shared sh(s_dyn + (VEC == 1 ? 0 : kGradStages * 4 * KU * CB / 16 * blockDim.x), deal.tok * slots, half);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the summing kernel may come up
   const Mine me(p, deal, p.H + p.Hkv);
+  const int gl = threadIdx.x % ln;
   const bool is_k = me.r >= p.H;
   const int h = is_k ? me.r - p.H : me.r;
   int oa[KU], ob[KU], have = 0;
@@ -645,12 +681,12 @@ __global__ void __launch_bounds__(kMostThreads, VEC == 1 ? 1 : 2)
 #pragma unroll
   for (int i = 0; i < N2; ++i) da[i] = db[i] = 0;
   const float inv_d = 1.f / p.d;
-  fill_fixed(p, sh, first);
+  fill_fixed<VEC>(p, sh, first, deal.tok, slots);
   for (int64_t t0 = me.begin; t0 < me.end; t0 += deal.tok) {
     const int nt = static_cast<int>(min(static_cast<int64_t>(deal.tok), me.end - t0));
     fill_positions(p, s_pos, t0, nt, t0 == me.begin, first);
     __syncthreads();  // also: the last batch's sines have been read
-    fill_angles<VEC>(p, nt, sh, true, [&](int a, int i) { return s_pos[a][i]; });
+    fill_angles<VEC>(p, nt, sh, slots, true, [&](int a, int i) { return s_pos[a][i]; });
     __syncthreads();
     for (int tk = me.tr; tk - me.tr < nt; tk += deal.per_round) {
       const bool live = me.on && tk < nt;
@@ -678,7 +714,7 @@ __global__ void __launch_bounds__(kMostThreads, VEC == 1 ? 1 : 2)
         uint64_t nB[N2];
 #pragma unroll
         for (int i = 0; i < N2; ++i) nB[i] = f2_mul(gB[i], minus);
-        turn<VEC, N2>(gA, gB, nB, sh.cs + tk * half, gl, ln, ru);
+        turn<VEC, N2, RAGGED>(gA, gB, nB, sh.cs + tk * slots, gl, ln, ru, half);
       }
       x.widen(A, B);
       uint64_t ss2 = 0, sg2 = 0;
@@ -710,7 +746,6 @@ __global__ void __launch_bounds__(kMostThreads, VEC == 1 ? 1 : 2)
   copy_wait<0>();
   __syncthreads();  // the ring becomes [groups][d]
   float* const s_dw = reinterpret_cast<float*>(s_dyn);
-  const int g = threadIdx.x / ln;
 #pragma unroll
   for (int i = 0; i < N2; ++i) {
     float v[4];  // A, A of the next pair, B, B
@@ -720,7 +755,7 @@ __global__ void __launch_bounds__(kMostThreads, VEC == 1 ? 1 : 2)
     for (int j = 0; j < 4; ++j) {
       const int n = 2 * i + j % 2, k = n / VEC, e = n % VEC;
       const int at = HALF || VEC == 1 ? (j < 2 ? oa[k] : ob[k]) + e : oa[k] + 2 * e + j / 2;
-      if (k < have) s_dw[g * p.d + at] = v[j];
+      if (k < have) s_dw[threadIdx.x / ln * p.d + at] = v[j];
     }
   }
   __syncthreads();
@@ -838,7 +873,8 @@ struct Launch {
   dim3 grid;
   int threads, smem;
 };
-Launch deal_rows(const NormRopeParams& p, int ln, int rows, int sms, int per_sm, int most, int ring) {
+Launch deal_rows(const NormRopeParams& p, int ln, int vec, int rows, int sms, int per_sm, int most,
+                 int ring) {
   Launch L;
   Deal& d = L.deal;
   d.ln = ln;
@@ -853,40 +889,67 @@ Launch deal_rows(const NormRopeParams& p, int ln, int rows, int sms, int per_sm,
   L.grid = dim3(static_cast<unsigned>(std::min<int64_t>(runs, std::max(1, ctas / chunks))), chunks);
   // the sines of a batch within 12 KB; no more than the CTA's own tokens
   const int64_t own = (p.T + L.grid.x - 1) / L.grid.x;
-  int64_t tok = std::min<int64_t>({kTokMax, 12288 / (p.rot / 2 * 8),
+  const int slots = (p.rot / 2 + vec - 1) / vec * vec;
+  int64_t tok = std::min<int64_t>({kTokMax, 12288 / (slots * 8),
                                    (own + d.per_round - 1) / d.per_round * d.per_round});
   d.tok = static_cast<int>(std::max<int64_t>(1, tok / d.per_round)) * d.per_round;
-  L.smem = shared_bytes(d.tok, p.rot / 2) + ring * L.threads;
+  L.smem = shared_bytes(d.tok * slots, p.rot / 2) + ring * L.threads;
   return L;
 }
 constexpr int kMostShared = 16384 + kTokMax * 256 * 8;  // beside the ring
 
+// bytes of rows on their way per thread: `parts` halves of a lane's part
+template <int DT, int VEC, int KU>
+constexpr int ring_bytes(int parts) {
+  return VEC == 1 ? 0 : parts * KU * VEC * static_cast<int>(sizeof(typename Elem<DT>::T));
+}
+// f(half layout, neighbours whose last unit is rotated in part): chunks below 16 bytes are for halves alone,
+// and a kernel of its own keeps the rest free of the registers that such units take (the gradient of
+// 8191 tokens x 20 heads of 64, half of them rotated: 26.2 us with one kernel, 24.8 so).
+template <int DT, int VEC, typename F>
+void pick_kernel(const NormRopeParams& p, bool half_style, F f) {
+  constexpr bool kWide = VEC * sizeof(typename Elem<DT>::T) == 16;
+  if constexpr (VEC == 1 || kWide) {
+    if (!half_style) {
+      if constexpr (kWide)
+        if (p.rot / 2 % VEC) return f(std::false_type{}, std::true_type{});
+      return f(std::false_type{}, std::false_type{});
+    }
+  }
+  f(std::true_type{}, std::false_type{});
+}
 template <int DT, int VEC, int KU, int MODE>
 cudaError_t launch_v(const NormRopeParams& p, bool half_style, int sms, cudaStream_t stream) {
-  constexpr int ring = VEC == 1 ? 0 : kStages * 2 * KU * 16;
+  constexpr int ring = ring_bytes<DT, VEC, KU>(kStages * 2);
   constexpr int most = kMostShared + ring * kMostThreads;
-  const Launch L = deal_rows(p, lanes_of(p.d / (2 * VEC), KU), p.H + (MODE ? 2 : 1) * p.Hkv,
-                             sms, (DT != FA_F32 && VEC > 1 ? 3 : 2) * kMostThreads, INT_MAX, ring);
-  auto* k = half_style ? norm_rope_kernel<DT, VEC, KU, true, MODE>
-                       : norm_rope_kernel<DT, VEC, KU, false, MODE>;
-  const cudaError_t e = half_style ? prepare_kernel<norm_rope_kernel<DT, VEC, KU, true, MODE>>(most)
-                                   : prepare_kernel<norm_rope_kernel<DT, VEC, KU, false, MODE>>(most);
+  const Launch L = deal_rows(p, lanes_of(p.d / (2 * VEC), KU), VEC, p.H + (MODE ? 2 : 1) * p.Hkv,
+                             sms, ctas_per_sm(DT, VEC, MODE) * kMostThreads, INT_MAX, ring);
+  void (*k)(NormRopeParams, Deal);
+  cudaError_t e;
+  pick_kernel<DT, VEC>(p, half_style, [&](auto half, auto ragged) {
+    constexpr bool H = decltype(half)::value, R = decltype(ragged)::value;
+    k = norm_rope_kernel<DT, VEC, KU, H, R, MODE>;
+    e = prepare_kernel<norm_rope_kernel<DT, VEC, KU, H, R, MODE>>(most);
+  });
   if (e != cudaSuccess) return e;
   k<<<L.grid, L.threads, L.smem, stream>>>(p, L.deal);
   return cudaGetLastError();
 }
 template <int DT, int VEC, int KU>
 cudaError_t launch_bwd_v(const NormRopeParams& p, bool half_style, int sms, cudaStream_t stream) {
-  constexpr int ring = VEC == 1 ? 0 : kGradStages * 4 * KU * 16;
+  constexpr int ring = ring_bytes<DT, VEC, KU>(grad_stages(KU * VEC * (DT == FA_F32 ? 2 : 1) / 8) * 4);
   constexpr int most = kMostShared + ring * kMostThreads;
-  Launch L = deal_rows(p, lanes_of(p.d / (2 * VEC), KU), p.H + p.Hkv, sms,
+  Launch L = deal_rows(p, lanes_of(p.d / (2 * VEC), KU), VEC, p.H + p.Hkv, sms,
                        (VEC == 1 ? 1 : 2) * kMostThreads, kNormCtas, ring);
   // the weights' gradients of its groups meet in the ring's place
   L.smem = std::max(L.smem, L.deal.per_round * L.deal.heads * p.d * 4);
-  auto* k = half_style ? norm_rope_bwd_kernel<DT, VEC, KU, true>
-                       : norm_rope_bwd_kernel<DT, VEC, KU, false>;
-  cudaError_t e = half_style ? prepare_kernel<norm_rope_bwd_kernel<DT, VEC, KU, true>>(most)
-                             : prepare_kernel<norm_rope_bwd_kernel<DT, VEC, KU, false>>(most);
+  void (*k)(NormRopeParams, Deal);
+  cudaError_t e;
+  pick_kernel<DT, VEC>(p, half_style, [&](auto half, auto ragged) {
+    constexpr bool H = decltype(half)::value, R = decltype(ragged)::value;
+    k = norm_rope_bwd_kernel<DT, VEC, KU, H, R>;
+    e = prepare_kernel<norm_rope_bwd_kernel<DT, VEC, KU, H, R>>(most);
+  });
   if (e != cudaSuccess) return e;
   k<<<L.grid, L.threads, L.smem, stream>>>(p, L.deal);
   e = cudaGetLastError();
@@ -904,23 +967,34 @@ cudaError_t launch_bwd_v(const NormRopeParams& p, bool half_style, int sms, cuda
                             static_cast<int>(L.grid.x * L.grid.y), p.d, p.dq_weight, p.dk_weight);
 }
 
+// Elements of a chunk, at most 16 bytes: what the rotated halves divide into (neighbours need no such
+// thing). Steps and pointers are multiples of 16 bytes; without that, 1.
+int chunk_of(const NormRopeParams& p, bool half_style, bool vec, int most) {
+  int v = vec && p.d % (2 * most) == 0 ? most : 1;
+  while (half_style && v > 1 && (p.rot / 2) % v) v /= 2;
+  return v;
+}
 template <int DT, int MODE>
 cudaError_t launch_m(const NormRopeParams& p, bool half_style, bool vec, int sms,
                      cudaStream_t stream) {
-  if (!vec) return launch_v<DT, 1, 8, MODE>(p, half_style, sms, stream);
-  if constexpr (DT == FA_F32)
-    return launch_v<DT, 4, 2, MODE>(p, half_style, sms, stream);
-  else
-    return launch_v<DT, 8, 1, MODE>(p, half_style, sms, stream);
+  constexpr int most = DT == FA_F32 ? 4 : 8;
+  switch (chunk_of(p, half_style, vec, most)) {
+    case most: return launch_v<DT, most, 8 / most, MODE>(p, half_style, sms, stream);
+    case most / 2: return launch_v<DT, most / 2, 16 / most, MODE>(p, half_style, sms, stream);
+    case most / 4: if (most > 4) return launch_v<DT, 2, 4, MODE>(p, half_style, sms, stream);
+  }
+  return launch_v<DT, 1, 8, MODE>(p, half_style, sms, stream);
 }
 template <int DT>
 cudaError_t launch_bwd_t(const NormRopeParams& p, bool half_style, bool vec, int sms,
                          cudaStream_t stream) {
-  if (!vec) return launch_bwd_v<DT, 1, 8>(p, half_style, sms, stream);
-  if constexpr (DT == FA_F32)
-    return launch_bwd_v<DT, 4, 2>(p, half_style, sms, stream);
-  else
-    return launch_bwd_v<DT, 8, 1>(p, half_style, sms, stream);
+  constexpr int most = DT == FA_F32 ? 4 : 8;
+  switch (chunk_of(p, half_style, vec, most)) {
+    case most: return launch_bwd_v<DT, most, 8 / most>(p, half_style, sms, stream);
+    case most / 2: return launch_bwd_v<DT, most / 2, 16 / most>(p, half_style, sms, stream);
+    case most / 4: if (most > 4) return launch_bwd_v<DT, 2, 4>(p, half_style, sms, stream);
+  }
+  return launch_bwd_v<DT, 1, 8>(p, half_style, sms, stream);
 }
 
 }  // namespace

@@ -372,6 +372,12 @@ __device__ __forceinline__ float max3f(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
+// Largest magnitude of three, NaN if one of them is.
+__device__ __forceinline__ float max3_abs_nan(float a, float b, float c) {
+  float d;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
 // Round two floats to a packed pair of 16-bit floats, `lo` in the low half.
 __device__ __forceinline__ uint32_t cvt_pack_bf16(float lo, float hi) {
   uint32_t d;
