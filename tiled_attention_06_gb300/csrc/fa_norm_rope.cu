@@ -100,7 +100,9 @@ int shared_bytes(int pairs, int half) { return pairs * 8 + half * 9; }
 // (cp.async) and reads them back itself, so nothing waits for anyone else. In registers a row ahead is
 // what there is room for, 32 KB per SM on their way.
 constexpr int kStages = 4;
-constexpr int grad_stages(int chunks) { return chunks == 1 ? 3 : 2; }  // rounds of x and dy, FP32's of twice that
+// Rounds of x and dy; FP32's are twice as large, and with three of them one CTA is all that fits an SM
+// (8192 tokens x 40 heads of 64: 70 us, 60 with two).
+constexpr int grad_stages(int chunks) { return chunks == 1 ? 3 : 2; }
 template <int N>
 __device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {
   if constexpr (N == 16)
@@ -145,7 +147,8 @@ __device__ __forceinline__ void fill_fixed(const NormRopeParams& p, const Shared
   const int rest = slots - p.rot / 2;
   for (int i = threadIdx.x; i < tok * rest; i += blockDim.x) {
     const int tk = i / rest, f = p.rot / 2 + i - tk * rest;
-    float* const to = reinterpret_cast<float*>(sh.cs + tk * slots) + pair_at<VEC>(f / VEC, f % VEC, slots / VEC);
+    float* const to =
+        reinterpret_cast<float*>(sh.cs + tk * slots) + pair_at<VEC>(f / VEC, f % VEC, slots / VEC);
     to[0] = 1.f;
     to[VEC == 1 ? 1 : 2] = 0.f;
   }
@@ -637,7 +640,8 @@ __global__ void __launch_bounds__(kMostThreads, VEC == 1 ? 1 : 2)
   constexpr int CB = sizeof(typename X::C);
   const uint32_t step = blockDim.x * CB, stage = 4 * KU * step;
   const uint32_t ring = smem_u32(s_dyn) + threadIdx.x * CB;
-  const Shared sh(s_dyn + (VEC == 1 ? 0 : kGradStages * 4 * KU * CB / 16 * blockDim.x), deal.tok * slots, half);
+  const Shared sh(s_dyn + (VEC == 1 ? 0 : kGradStages * 4 * KU * CB / 16 * blockDim.x),
+                  deal.tok * slots, half);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the summing kernel may come up
   const Mine me(p, deal, p.H + p.Hkv);
   const int gl = threadIdx.x % ln;
