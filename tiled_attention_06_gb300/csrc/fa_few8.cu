@@ -10,9 +10,10 @@
 // Every product is formed in FP16, whatever the call's type: an element of the cache is exact there,
 // and so is a row of q over the power of two that brings its largest magnitude to [2^14, 2^15)
 // (elements 2^-29 of it and above; what smaller ones lose is 2^-40 of it). K's powers of two multiply
-// the FP32 scores. V's go with its elements, relative to a running power of the warp's keys (at most
-// 2^7 above it, else the output so far is rescaled), which the output gets back at the end: powers
-// within 2^-15 of the running one lose nothing, and below it the loss is 2^-33 of the largest row.
+// the FP32 scores. V's, 2^e_j, go with the probabilities, P'_j = 2^(s_j + e_j - R) (s in log2 units),
+// where every row of queries has its own running R, an integer near the largest s_j + e_j of the keys
+// that it sees: keys that it does not see move nothing, and what FP16 loses below 2^-24 is 2^-23 of the
+// row's largest term. The row sum takes 2^(s_j - m) as ever, and the output its 2^(R - m) at the end.
 //
 // ldmatrix moves pairs of bytes: a lane gets four neighbouring channels of a key of K, and two keys
 // times two channels of V (transposed). The products take d in that order, and q and the output
@@ -48,12 +49,11 @@ struct Cfg {
   static constexpr int OROW = D + 4;              // floats of an output row in shared memory
   static constexpr int COMB = 2 * ROWS * OROW * 4;  // two warps' outputs
   static constexpr int STATES = 2 * ROWS * 2 * 4;   // their (m, l)
-  static constexpr int MULS = 2 * BK;               // V's multipliers, FP16
   static constexpr int BARS = 256;
   static constexpr int BUDGET = 233472 / CTAS - 1024;  // 1 KB taken per CTA
-  static constexpr int FIT = (BUDGET - COMB - STATES - MULS - BARS) / (2 * TILE + SCALES);
+  static constexpr int FIT = (BUDGET - COMB - STATES - BARS) / (2 * TILE + SCALES);
   static constexpr int NST = FIT > 8 ? 8 : FIT;
-  static constexpr int SMEM = NST * (2 * TILE + SCALES) + COMB + STATES + MULS + BARS;
+  static constexpr int SMEM = NST * (2 * TILE + SCALES) + COMB + STATES + BARS;
   static_assert(NST >= 2, "too few stages");
 };
 
@@ -64,11 +64,6 @@ __device__ __forceinline__ void cvt8(uint32_t x, uint32_t& lo, uint32_t& hi) {
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(lo) : "h"(static_cast<uint16_t>(x)));
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(hi) : "h"(static_cast<uint16_t>(x >> 16)));
 }
-__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
 // An 8 x 8 matrix of 16-bit elements, transposed.
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   uint32_t d;
@@ -77,22 +72,14 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
 }
 // 2^(b - 127) of an exponent byte: an infinity for 255, a subnormal for 0.
 __device__ __forceinline__ float power8(uint32_t b) { return __uint_as_float(max(b << 23, 0x400000u)); }
-// 2^(b - ref), 0 below 2^-126
-__device__ __forceinline__ float relative8(int b, int ref) {
-  return __uint_as_float(static_cast<uint32_t>(max(b - ref + 127, 0)) << 23);
+// The exponent e of a byte's 2^e, a NaN for 255.
+__device__ __forceinline__ float exponent8(uint32_t b) {
+  return b == 255 ? __uint_as_float(0x7fffffffu) : static_cast<float>(static_cast<int>(b) - 127);
 }
 __device__ __forceinline__ uint32_t load_u8(uint32_t addr) {
   uint32_t x;
   asm volatile("ld.shared.u8 %0, [%1];" : "=r"(x) : "r"(addr) : "memory");
   return x;
-}
-__device__ __forceinline__ uint32_t load_u32(uint32_t addr) {
-  uint32_t x;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(x) : "r"(addr) : "memory");
-  return x;
-}
-__device__ __forceinline__ void store_u16(uint32_t addr, uint32_t x) {
-  asm volatile("st.shared.u16 [%0], %1;" ::"r"(addr), "h"(static_cast<uint16_t>(x)) : "memory");
 }
 // `bytes` (a multiple of 16) from global to shared memory, counted on `bar`.
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
@@ -116,8 +103,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::CTAS)
   const uint32_t sScales = base + C::NST * 2 * C::TILE;  // K's, then V's of a stage
   float* comb = reinterpret_cast<float*>(smem + kBehind);
   float* states = reinterpret_cast<float*>(smem + kBehind + C::COMB);
-  const uint32_t sMuls = base + kBehind + C::COMB + C::STATES;
-  Bars* bars = reinterpret_cast<Bars*>(smem + kBehind + C::COMB + C::STATES + C::MULS);
+  Bars* bars = reinterpret_cast<Bars*>(smem + kBehind + C::COMB + C::STATES);
   auto B = [&](uint64_t& x) { return smem_u32(&x); };
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the joining kernel may come up
@@ -332,13 +318,12 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::CTAS)
         full_to = min(full_to, max(first - BK + 1, p.m.n_global - BK));
       if (p.m.mask_mode == FA_MASK_TREE) full_to = min(full_to, first - BK);
     }
-    int ref = 0;  // exponent byte of the running power of V
-    float m[NB][2], l[NB][2], o[NB][CH][4];
+    float m[NB][2], l[NB][2], R[NB][2], o[NB][CH][4];
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        m[b][e] = -INFINITY;
+        m[b][e] = R[b][e] = -INFINITY;
         l[b][e] = 0.f;
       }
 #pragma unroll
@@ -391,27 +376,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::CTAS)
             s[b][mb][e] = fmaf(x, BF16 ? f * qs[b][e % 2] : f, e < 2 ? z0 : z1);
           }
       }
-      // V's powers, a key to a lane: the running one covers the warp's keys, and the multipliers go
-      // round by way of shared memory
-      const int mine = lane % KPW, vb = static_cast<int>(load_u8(sc + BK + mine));
-      const bool dead = kw * KPW + mine >= live;
-      const int big = static_cast<int>(
-          __reduce_max_sync(0xffffffffu, dead || vb == 255 ? 0u : static_cast<uint32_t>(vb)));
-      if (big > ref + 7) {  // the same for the whole warp
-        const float a = relative8(ref, big);
-        ref = big;
-#pragma unroll
-        for (int b = 0; b < NB; ++b)
-#pragma unroll
-          for (int c = 0; c < CH; ++c)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[b][c][e] *= a;
-      }
-      {
-        const uint32_t x = cvt_pack_f16(relative8(vb, ref), 0.f);
-        store_u16(sMuls + 2 * (kw * KPW + mine), dead ? 0u : vb == 255 ? 0x7fffu : x);
-        __syncwarp();
-      }
       // hidden keys to -inf where some row does not see the whole tile
       if (n0 > full_to || (n0 < full_from && n0 > full_global)) {
 #pragma unroll 1
@@ -457,32 +421,53 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::CTAS)
               }
           }
       }
-      // running maximum (a row's keys are spread over eight lanes), lazy rescale, P
+      // V's exponents (of any key behind the last: its probability is 0)
+      float ve[MB][2];
+#pragma unroll
+      for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const int own = 16 * mb + 8 * t + gq;
+          const float e = exponent8(load_u8(sc + BK + own));
+          ve[mb][t] = kw * KPW + own < live ? e : 0.f;
+        }
+      // the largest score and the largest term of a row (its keys are spread over eight lanes), m and R,
+      // move when some lane finds one 2^kTau above
+      float mx[NB][2], tx[NB][2];
       bool need = false;
-      float mn[NB][2];
 #pragma unroll
       for (int b = 0; b < NB; ++b)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          float mx = -INFINITY;
+          mx[b][i] = tx[b][i] = -INFINITY;
 #pragma unroll
-          for (int mb = 0; mb < MB; ++mb) mx = max3f(mx, s[b][mb][i], s[b][mb][2 + i]);
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-          mn[b][i] = fmaxf(m[b][i], mx * p.m.sl2);
-          need = need || (m[b][i] != -INFINITY && mn[b][i] > m[b][i] + kTau);
-          if (m[b][i] == -INFINITY) m[b][i] = mn[b][i];
+          for (int mb = 0; mb < MB; ++mb) {
+            const float x = s[b][mb][i], y = s[b][mb][2 + i];
+            mx[b][i] = max3f(mx[b][i], x, y);
+            tx[b][i] = max3f(tx[b][i], fmaf(x, p.m.sl2, ve[mb][0]), fmaf(y, p.m.sl2, ve[mb][1]));
+          }
+          mx[b][i] *= p.m.sl2;
+          need = need || mx[b][i] > m[b][i] + kTau || tx[b][i] > R[b][i] + kTau;
         }
       if (__any_sync(0xffffffffu, need)) {
 #pragma unroll
         for (int b = 0; b < NB; ++b)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const bool move = mn[b][i] > m[b][i] + kTau;
-            const float a = move ? ex2_approx(m[b][i] - mn[b][i]) : 1.f;
-            if (move) m[b][i] = mn[b][i];
-            l[b][i] *= a;
+            float x = mx[b][i], y = tx[b][i];
+#pragma unroll
+            for (int lanes = 4; lanes < 32; lanes *= 2) {
+              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, lanes));
+              y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, lanes));
+            }
+            if (x > m[b][i] + kTau) {
+              l[b][i] *= ex2_approx(m[b][i] - x);
+              m[b][i] = x;
+            }
+            const bool move = y > R[b][i] + kTau;
+            y = ceilf(y);
+            const float a = move ? ex2_approx(R[b][i] - y) : 1.f;
+            if (move) R[b][i] = y;
 #pragma unroll
             for (int c = 0; c < CH; ++c) {
               o[b][c][i] *= a;
@@ -490,20 +475,24 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::CTAS)
             }
           }
       }
-      uint32_t pf[NB][MB][2];  // P^T: keys 2 cq, 2 cq + 1 (and 8 on) of row gq
+      uint32_t pf[NB][MB][2];  // P'^T: keys 2 cq, 2 cq + 1 (and 8 on) of row gq
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
-        const float mu0 = m[b][0] == -INFINITY ? 0.f : m[b][0];
-        const float mu1 = m[b][1] == -INFINITY ? 0.f : m[b][1];
+        float mu[2], ru[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          mu[i] = m[b][i] == -INFINITY ? 0.f : m[b][i];
+          ru[i] = R[b][i] == -INFINITY ? 0.f : R[b][i];
+        }
 #pragma unroll
         for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
-            const float x = ex2_approx(fmaf(s[b][mb][2 * t], p.m.sl2, -mu0));
-            const float y = ex2_approx(fmaf(s[b][mb][2 * t + 1], p.m.sl2, -mu1));
-            l[b][0] += x;
-            l[b][1] += y;
-            pf[b][mb][t] = transpose8(cvt_pack_f16(x, y));
+            const float x = s[b][mb][2 * t], y = s[b][mb][2 * t + 1];
+            l[b][0] += ex2_approx(fmaf(x, p.m.sl2, -mu[0]));
+            l[b][1] += ex2_approx(fmaf(y, p.m.sl2, -mu[1]));
+            pf[b][mb][t] = transpose8(cvt_pack_f16(ex2_approx(fmaf(x, p.m.sl2, ve[mb][t] - ru[0])),
+                                                   ex2_approx(fmaf(y, p.m.sl2, ve[mb][t] - ru[1]))));
           }
       }
       if (live < BK) {  // rows of V behind the last key: 0 times what they hold may not be 0
@@ -518,20 +507,14 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::CTAS)
 #pragma unroll
       for (int mb = 0; mb < MB; ++mb) {
         const int key = kw * KPW + 16 * mb + ((lane / 8) % 2) * 8 + lane % 8;
-        const uint32_t mv[2] = {load_u32(sMuls + 2 * (kw * KPW + 16 * mb + 2 * cq)),
-                                load_u32(sMuls + 2 * (kw * KPW + 16 * mb + 8 + 2 * cq))};
 #pragma unroll
         for (int c = 0; c < CH; c += 2) {
           const int ch = c + lane / 16;
           uint32_t vf[4], a[2][4];
           ldsm4_t(sV + key * D + ((ch ^ (D == 128 ? key & 7 : (key >> 1) & 3)) << 4), vf);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {  // (key, channel) pairs side by side to keys side by side
-            uint32_t lo, hi;
-            cvt8(__byte_perm(vf[i], 0, 0x3120), lo, hi);
-            a[i / 2][2 * (i % 2)] = hmul2(lo, mv[i % 2]);
-            a[i / 2][2 * (i % 2) + 1] = hmul2(hi, mv[i % 2]);
-          }
+          for (int i = 0; i < 4; ++i)  // (key, channel) pairs side by side to keys side by side
+            cvt8(__byte_perm(vf[i], 0, 0x3120), a[i / 2][2 * (i % 2)], a[i / 2][2 * (i % 2) + 1]);
 #pragma unroll
           for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -541,16 +524,19 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::CTAS)
       __syncwarp();
       if (lane == 0) mbar_arrive(B(bars->empty[st]));
     }
-    // the output's own units, the sums over the lanes of a row
-    const float unit = power8(ref);
+    // the output over 2^m, as the row sum (by two factors: 2^(R - m) may be below FP32's normal range
+    // where the output is not), the sums over the lanes of a row
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
 #pragma unroll
-      for (int c = 0; c < CH; ++c)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[b][c][e] *= unit;
-#pragma unroll
       for (int i = 0; i < 2; ++i) {
+        const float r = R[b][i] == -INFINITY ? 0.f : R[b][i] - m[b][i], h = floorf(0.5f * r);
+        const float u = ex2_approx(h), v = ex2_approx(r - h);
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+          o[b][c][i] = o[b][c][i] * u * v;
+          o[b][c][2 + i] = o[b][c][2 + i] * u * v;
+        }
         l[b][i] += __shfl_xor_sync(0xffffffffu, l[b][i], 4);
         l[b][i] += __shfl_xor_sync(0xffffffffu, l[b][i], 8);
         l[b][i] += __shfl_xor_sync(0xffffffffu, l[b][i], 16);
