@@ -597,8 +597,10 @@ fa_status fa_rope_axes(int32_t* pair_axis, int rot_dim, const int32_t* sections,
  *     n = x / sqrt(mean(x^2) + eps) * weight     (over the d elements of a head; FP32),
  * with FA_NORM_NONE n = x; then y is n rotated as fa_rope does, pair i by the angle
  * positions[pair_axis[i]][token] * freqs[i]. One rounding, at the store. The sum of squares is FP32:
- * a row of elements beyond 1e18 or so is infinitely long and becomes zeros. With eps = 0 a row of
- * zeros becomes NaN. Infinities and NaN stay within their row (and a weight's gradient).
+ * a row of elements beyond 1e18 or so is infinitely long and becomes zeros, its gradients too. With
+ * eps = 0 a row whose squares leave FP32 below (elements under 1e-23 or so, zeros among them) is not
+ * finite, and one near there (1e-19) loses bits. Infinities and NaN stay within their row (and a
+ * weight's gradient).
  *   q, q_out   element e of head h of token t at t * q_token + h * q_head + e (and so on);
  *   k, k_out   the same for Hkv heads; Hkv = 0: none (k, k_out and k_weight are ignored).
  *              q_out may be q with the same steps (in place), and k_out k; otherwise outputs
@@ -639,8 +641,9 @@ fa_status fa_norm_rope(const fa_norm_rope_params* params, fa_stream_t stream);
  * fa_norm_rope_bwd - gradients of fa_norm_rope: params holds the forward call's arguments (q_out
  * and k_out are not read), grads the upstream gradients dq_out and dk_out and the outputs
  *     g = R^T dy,   dx = r w g - x r^3 mean(w g x),   dweight = sum over tokens and heads of g x r
- * with r = 1 / sqrt(mean(x^2) + eps) and R the rotation. dq may be dq_out with the same steps (in
- * place), and dk dk_out.
+ * with r = 1 / sqrt(mean(x^2) + eps) and R the rotation. The mean is an FP32 sum: products w g x that
+ * leave FP32 in a row of finite length make its dx infinite or NaN. dq may be dq_out with the same
+ * steps (in place), and dk dk_out.
  *   dq_weight, dk_weight  float32 [d], written (not added to); NULL: not wanted
  *   workspace  device scratch of fa_norm_rope_bwd_workspace_size(...) bytes, 16-byte aligned, for
  *              calls that want a weight's gradient (else it may be NULL); calls that may overlap

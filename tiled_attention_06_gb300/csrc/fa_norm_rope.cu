@@ -540,10 +540,11 @@ __global__ void __launch_bounds__(kMostThreads, ctas_per_sm(DT, VEC, MODE))
         if (!is_v) {
           const float rr = rsqrtf(fmaf(ss, inv_d, p.eps));
           const uint64_t rr2 = f2(rr, rr);
+          // x r first: w x alone may leave FP32, and an infinitely long row (r = 0) is to become zeros
 #pragma unroll
           for (int i = 0; i < N2; ++i) {
-            A[i] = f2_mul(f2_mul(A[i], wA[i]), rr2);
-            B[i] = f2_mul(f2_mul(B[i], wB[i]), rr2);
+            A[i] = f2_mul(f2_mul(A[i], rr2), wA[i]);
+            B[i] = f2_mul(f2_mul(B[i], rr2), wB[i]);
           }
         }
       }
@@ -731,8 +732,10 @@ __global__ void __launch_bounds__(kMostThreads, VEC == 1 ? 1 : 2)
       T* const to = dst;
       dst += d_token * deal.per_round;
       if (!live) continue;
-      // r x (sum) first: r^3 alone leaves FP32 for rows below 1e-13
-      const float rr = rsqrtf(fmaf(ss, inv_d, p.eps)), c = -(rr * (sg * inv_d)) * rr * rr;
+      // r x (sum) first: r^3 alone leaves FP32 for rows below 1e-13. An infinitely long row (r = 0) has no
+      // gradient, though its sum may be infinite.
+      const float rr = rsqrtf(fmaf(ss, inv_d, p.eps));
+      const float c = rr == 0.f ? 0.f : -(rr * (sg * inv_d)) * rr * rr;
       const uint64_t rr2 = f2(rr, rr), c2 = f2(c, c);
 #pragma unroll
       for (int i = 0; i < N2; ++i) {
