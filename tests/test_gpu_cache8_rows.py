@@ -94,3 +94,20 @@ def test_every_row_of_v_counts_by_its_probability(rows, by, dtype):
     lim += 2.0 ** -25 if dtype is HF else 0.0  # half a step of the smallest FP16 numbers
     err = (c.o[0].double().cpu() - o).abs().amax()
     assert err <= lim, (float(err), float(lim))
+
+
+@pytest.mark.parametrize("kw", [dict(mask_mode=WINDOW, window=8), dict(mask_mode=BAND, window=8),
+                                dict(mask_mode=PREFIX, n_global=4), dict(mask_mode=fa.FA_MASK_NONE),
+                                dict(window=8), dict(n_global=4), dict(mask_mode=TREE, window=8),
+                                dict(mask_mode=9)], ids=str)
+def test_a_tree_takes_no_other_mask(kw):
+    c = Call([2], [40], 2, 1, 64, 16, BF, mask=TREE)
+    c.kw.update(kw)
+    with pytest.raises(fa.FaError) as e:
+        c.run()
+    assert e.value.status == fa.FA_ERR_INVALID_ARG
+    torch.cuda.synchronize()
+    assert (c.o == 7).all()
+    for mask in (TREE, CAUSAL):  # the tree itself, and the default
+        c.kw.update(mask_mode=mask, window=0, n_global=0)
+        c.run_and_check()

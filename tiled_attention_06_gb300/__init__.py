@@ -1042,7 +1042,8 @@ def fa_fwd_paged_varlen_ex(q, k_pages, v_pages, block_table, ctx_lens, cu_seqlen
                            mask_mode=FA_MASK_CAUSAL, window=0, n_global=0, stream=None):
     """fa_fwd_paged_varlen over an 8-bit cache (k_scales and v_scales given) and for trees of
     drafted tokens: tree int32 [Tq, words], bit j % 32 of word j // 32 of a query's row set where it
-    sees token j of its own chunk (mask_mode is then FA_MASK_TREE whatever is passed)."""
+    sees token j of its own chunk. A tree is the call's mask (FA_MASK_TREE; the default gives way to it):
+    with another mode, a window or global keys the call is refused."""
     dev = _device_of(q)
     dtype, qs = q.dtype, q.shape
     Tq, H, d = _dims("q", q, 3) if len(qs) != 3 else qs
@@ -1052,7 +1053,10 @@ def fa_fwd_paged_varlen_ex(q, k_pages, v_pages, block_table, ctx_lens, cu_seqlen
     if tree is not None:
         words = _dims("tree", tree, 2)[1]
         bits = _dense("tree", tree, Tq * words, torch.int32, dev)
-        mask_mode, window, n_global = FA_MASK_TREE, 0, 0
+        if mask_mode not in (FA_MASK_CAUSAL, FA_MASK_TREE) or window or n_global:
+            _refuse(f"a tree takes no other mask (mask_mode {mask_mode}, window {window}, n_global "
+                    f"{n_global})")
+        mask_mode = FA_MASK_TREE
     if lse is not None and lse.shape != (Tq, H):
         _refuse_tensor("lse", lse, (Tq, H), "float32", dev, "contiguous ")
     ws, ws_bytes = _bytes_of(workspace, q.device)
