@@ -113,9 +113,10 @@ void fill_turn(fa::NormRopeParams* p, const Turn& t) {
   p->q_weight = t.norm == FA_NORM_RMS ? t.q_weight : nullptr;
   p->k_weight = t.norm == FA_NORM_RMS ? t.k_weight : nullptr;
 }
+// (without key heads k_weight is ignored; lanes without a head would read its first element)
 Turn turn_of(const fa_norm_rope_params& a) {
-  return Turn{a.d,   a.rot_dim,   a.axes,      a.style, a.norm,     a.weight_dtype, a.dtype, a.amplitude,
-              a.eps, a.positions, a.pair_axis, a.freqs, a.q_weight, a.k_weight};
+  return Turn{a.d,       a.rot_dim,   a.axes,  a.style,    a.norm, a.weight_dtype, a.dtype, a.amplitude, a.eps,
+              a.positions, a.pair_axis, a.freqs, a.q_weight, a.Hkv ? a.k_weight : nullptr};
 }
 
 fa_status check_sizes(const fa_norm_rope_params& a) {
