@@ -111,3 +111,22 @@ def test_a_tree_takes_no_other_mask(kw):
     for mask in (TREE, CAUSAL):  # the tree itself, and the default
         c.kw.update(mask_mode=mask, window=0, n_global=0)
         c.run_and_check()
+
+
+# ------------------------------------------------------------------------------ far pages, FP16's range
+
+@pytest.mark.parametrize("lens", [[1, 0], [1, 40]], ids=["few rows", "tiles"])
+def test_rows_beyond_2_to_the_31_bytes(lens):
+    """Either kernel over pages in the last 2.5 GB of the pools; rows that no sequence owns stay."""
+    d, page, H, P = 128, 4096, 8, 600
+    c = Call(lens, [100, 300], H, H, d, page, BF, seed=2)
+    n = c.k.shape[0]
+    far = []
+    for small in (c.k, c.v, c.kw["k_scales"], c.kw["v_scales"]):
+        big = torch.zeros(P, *small.shape[1:], dtype=torch.uint8, device="cuda")
+        big[P - n:].copy_(small.view(torch.uint8))
+        far.append(big)
+    c.k, c.v, c.kw["k_scales"], c.kw["v_scales"] = far
+    c.table.add_(torch.where(c.table >= 0, P - n, 0).to(torch.int32))
+    c.run()
+    c.check()
