@@ -674,10 +674,13 @@ size_t fa_norm_rope_bwd_workspace_size(int H, int Hkv, int d);
  * that times 2^(byte - 127), byte the smallest in [0, 254] that brings the row's largest magnitude
  * within 448; to nearest, ties to even, from the FP32 value (no rounding to 16 bits before). A row
  * with an infinity or a NaN gets byte 255 (and zero elements) and every element of it is NaN when
- * read. Times a power of two the elements are exact in 16 bits (in FA_F16 down to 2^-24), so
- * fa_fwd_paged_varlen_ex computes with exactly these values. Element bytes 0x7f and 0xff, which
- * fa_norm_rope_append does not write, are NaN to fa_kv_read; to fa_fwd_paged_varlen_ex they
- * are NaN or +-480.
+ * read. Times a power of two the elements are exact in FA_BF16 and, from 2^-24 to 65504, in FA_F16,
+ * so fa_fwd_paged_varlen_ex computes with exactly these values. What FA_F16 does not hold (a row's
+ * largest elements from 63488 on may round up to 65536 in 8 bits) is an infinity to fa_kv_read, and in
+ * attention where max_q * H / Hkv is above 16: one in K gives infinite or NaN scores to the queries
+ * that see it, one in V reaches every query of its sequence as a NaN does. With fewer rows such values
+ * count as they are. Element bytes 0x7f and 0xff, which fa_norm_rope_append does not write, are NaN to
+ * fa_kv_read; to fa_fwd_paged_varlen_ex they are NaN or +-480.
  *
  * fa_norm_rope_append - fa_rope_append with a norm of q and k (as fa_norm_rope), with positions of
  * several axes, and into either cache: 8 bits where k_scales is given, else pools of dtype.

@@ -130,3 +130,33 @@ def test_rows_beyond_2_to_the_31_bytes(lens):
     c.table.add_(torch.where(c.table >= 0, P - n, 0).to(torch.int32))
     c.run()
     c.check()
+
+
+@pytest.mark.parametrize("lens", [[1, 2], [50, 3]], ids=["few rows", "tiles"])
+@pytest.mark.parametrize("which", ["k", "v"])
+@pytest.mark.parametrize("by,outside", [(8, False), (24, True)])
+def test_values_beyond_fp16(lens, which, by, outside):
+    """FP16 calls over rows that FP16 does not hold: few rows take them as they are, tiles as
+    infinities, which the queries of that sequence show; other sequences keep theirs."""
+    ctx, d = [400, 130], 64
+    q = torch.randn(sum(lens) + 2, 3, d, generator=torch.Generator().manual_seed(1))
+    q *= 2.0 ** -by if which == "k" else 1.0
+    c = Call(lens, ctx, 2, 1, d, 16, HF, q=q, seed=3)
+    i = "kv".index(which)
+    page = c.cache.table[0, 1].item()
+    c.cache.scales[i][page] += by
+    c.kw[which + "_scales"].view(torch.uint8)[page] += by
+    c.run()
+    torch.cuda.synchronize()
+    assert fa.fa_get_device_status() == fa.FA_OK
+    want = c8.attention(c.q[:c.T], c.cache, ctx, lens, c.scale, CAUSAL)
+    got = c.o[:c.T].double().cpu()
+    ok = (got - want[0]).abs().amax(-1) <= 2 * 2.0 ** -11 * want[2] + 2.0 ** -18 * (1 + want[2])
+    first = slice(0, lens[0])
+    assert ok[lens[0]:].all()
+    if not outside or (lens[0] < 9 and which == "k"):
+        assert ok[first].all()
+    elif lens[0] < 9:  # the output itself leaves FP16
+        assert got[first][want[0][first].abs() > 2.0 ** 17].isinf().all()
+    else:
+        assert not torch.isfinite(got[first]).all(-1).any()
