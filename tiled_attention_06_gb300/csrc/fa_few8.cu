@@ -10,10 +10,11 @@
 // Every product is formed in FP16, whatever the call's type: an element of the cache is exact there,
 // and so is a row of q over the power of two that brings its largest magnitude to [2^14, 2^15)
 // (elements 2^-29 of it and above; what smaller ones lose is 2^-40 of it). K's powers of two multiply
-// the FP32 scores. V's, 2^e_j, go with the probabilities, P'_j = 2^(s_j + e_j - R) (s in log2 units),
-// where every row of queries has its own running R, an integer near the largest s_j + e_j of the keys
-// that it sees: keys that it does not see move nothing, and what FP16 loses below 2^-24 is 2^-23 of the
-// row's largest term. The row sum takes 2^(s_j - m) as ever, and the output its 2^(R - m) at the end.
+// the FP32 scores. V's, 2^e_j, go with the probabilities, P'_j = 2^(x_j + e_j - r) of x_j = s_j - m (s in
+// log2 units, m the row's running maximum), where every row of queries has its own running integer r, 7 to
+// 15 below the largest x_j + e_j of the keys that it sees. So keys that it does not see move nothing, terms
+// down to 2^-20 of the row's largest keep FP16's eleven bits (the likeliest key's, a power of two, is exact),
+// and below them 2^-31 of the largest is lost. The output gets its 2^r back at the end.
 //
 // ldmatrix moves pairs of bytes: a lane gets four neighbouring channels of a key of K, and two keys
 // times two channels of V (transposed). The products take d in that order, and q and the output
@@ -36,6 +37,7 @@ namespace {
 // alone, CTAs with many short sequences kept the others waiting (SMs were busy 68 % of the time:
 // 60.9 us in the case above, 50.5 so).
 constexpr int kSegment = 2;
+constexpr float kTop = 7.0f;  // log2 of the largest P' when r moves; with kTau it stays within FP16
 
 // NB: blocks of 8 rows. BK: keys of a tile, of which a warp takes a quarter.
 template <int D, int NB>
@@ -75,6 +77,12 @@ __device__ __forceinline__ float power8(uint32_t b) { return __uint_as_float(max
 // The exponent e of a byte's 2^e, a NaN for 255.
 __device__ __forceinline__ float exponent8(uint32_t b) {
   return b == 255 ? __uint_as_float(0x7fffffffu) : static_cast<float>(static_cast<int>(b) - 127);
+}
+// The largest of the eight lanes of a row (those of the same lane % 4).
+__device__ __forceinline__ float max8(float x) {
+#pragma unroll
+  for (int o = 4; o < 32; o *= 2) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+  return x;
 }
 __device__ __forceinline__ uint32_t load_u8(uint32_t addr) {
   uint32_t x;
@@ -318,12 +326,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::CTAS)
         full_to = min(full_to, max(first - BK + 1, p.m.n_global - BK));
       if (p.m.mask_mode == FA_MASK_TREE) full_to = min(full_to, first - BK);
     }
-    float m[NB][2], l[NB][2], R[NB][2], o[NB][CH][4];
+    float m[NB][2], l[NB][2], r[NB][2], o[NB][CH][4];
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        m[b][e] = R[b][e] = -INFINITY;
+        m[b][e] = -INFINITY;
+        r[b][e] = -1e6f;  // below any term
         l[b][e] = 0.f;
       }
 #pragma unroll
@@ -431,43 +440,68 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::CTAS)
           const float e = exponent8(load_u8(sc + BK + own));
           ve[mb][t] = kw * KPW + own < live ? e : 0.f;
         }
-      // the largest score and the largest term of a row (its keys are spread over eight lanes), m and R,
-      // move when some lane finds one 2^kTau above
-      float mx[NB][2], tx[NB][2];
+      // m moves when some lane finds a score 2^kTau above it (a row's keys are spread over eight lanes); r
+      // goes down by the whole part, so that the output's own unit, 2^(m + r), goes up by the rest alone
+      float mx[NB][2];
       bool need = false;
 #pragma unroll
       for (int b = 0; b < NB; ++b)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          mx[b][i] = tx[b][i] = -INFINITY;
+          mx[b][i] = -INFINITY;
 #pragma unroll
-          for (int mb = 0; mb < MB; ++mb) {
-            const float x = s[b][mb][i], y = s[b][mb][2 + i];
-            mx[b][i] = max3f(mx[b][i], x, y);
-            tx[b][i] = max3f(tx[b][i], fmaf(x, p.m.sl2, ve[mb][0]), fmaf(y, p.m.sl2, ve[mb][1]));
-          }
+          for (int mb = 0; mb < MB; ++mb) mx[b][i] = max3f(mx[b][i], s[b][mb][i], s[b][mb][2 + i]);
           mx[b][i] *= p.m.sl2;
-          need = need || mx[b][i] > m[b][i] + kTau || tx[b][i] > R[b][i] + kTau;
+          need = need || mx[b][i] > m[b][i] + kTau;
         }
       if (__any_sync(0xffffffffu, need)) {
 #pragma unroll
         for (int b = 0; b < NB; ++b)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            float x = mx[b][i], y = tx[b][i];
-#pragma unroll
-            for (int lanes = 4; lanes < 32; lanes *= 2) {
-              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, lanes));
-              y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, lanes));
-            }
+            const float x = max8(mx[b][i]);
+            float a = 1.f;
             if (x > m[b][i] + kTau) {
-              l[b][i] *= ex2_approx(m[b][i] - x);
+              const float up = x - m[b][i], whole = m[b][i] == -INFINITY ? 0.f : floorf(up);
+              a = ex2_approx(whole - up);
+              l[b][i] *= ex2_approx(-up);
+              r[b][i] -= whole;
               m[b][i] = x;
             }
-            const bool move = y > R[b][i] + kTau;
-            y = ceilf(y);
-            const float a = move ? ex2_approx(R[b][i] - y) : 1.f;
-            if (move) R[b][i] = y;
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
+              o[b][c][i] *= a;
+              o[b][c][2 + i] *= a;
+            }
+          }
+      }
+      // the row's sum, and its terms' exponents x + e in the scores' place; r moves as m does
+      need = false;
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float mu = m[b][i] == -INFINITY ? 0.f : m[b][i];
+          mx[b][i] = -INFINITY;
+#pragma unroll
+          for (int mb = 0; mb < MB; ++mb) {
+            const float x = fmaf(s[b][mb][i], p.m.sl2, -mu), y = fmaf(s[b][mb][2 + i], p.m.sl2, -mu);
+            l[b][i] += ex2_approx(x) + ex2_approx(y);
+            s[b][mb][i] = x + ve[mb][0];
+            s[b][mb][2 + i] = y + ve[mb][1];
+            mx[b][i] = max3f(mx[b][i], s[b][mb][i], s[b][mb][2 + i]);
+          }
+          need = need || mx[b][i] > r[b][i] + kTop + kTau;
+        }
+      if (__any_sync(0xffffffffu, need)) {
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float y = max8(mx[b][i]), to = ceilf(y) - kTop;
+            const bool move = y > r[b][i] + kTop + kTau;
+            const float a = move ? ex2_approx(r[b][i] - to) : 1.f;
+            if (move) r[b][i] = to;
 #pragma unroll
             for (int c = 0; c < CH; ++c) {
               o[b][c][i] *= a;
@@ -477,24 +511,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::CTAS)
       }
       uint32_t pf[NB][MB][2];  // P'^T: keys 2 cq, 2 cq + 1 (and 8 on) of row gq
 #pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        float mu[2], ru[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          mu[i] = m[b][i] == -INFINITY ? 0.f : m[b][i];
-          ru[i] = R[b][i] == -INFINITY ? 0.f : R[b][i];
-        }
+      for (int b = 0; b < NB; ++b)
 #pragma unroll
         for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            const float x = s[b][mb][2 * t], y = s[b][mb][2 * t + 1];
-            l[b][0] += ex2_approx(fmaf(x, p.m.sl2, -mu[0]));
-            l[b][1] += ex2_approx(fmaf(y, p.m.sl2, -mu[1]));
-            pf[b][mb][t] = transpose8(cvt_pack_f16(ex2_approx(fmaf(x, p.m.sl2, ve[mb][t] - ru[0])),
-                                                   ex2_approx(fmaf(y, p.m.sl2, ve[mb][t] - ru[1]))));
-          }
-      }
+          for (int t = 0; t < 2; ++t)
+            pf[b][mb][t] = transpose8(cvt_pack_f16(ex2_approx(s[b][mb][2 * t] - r[b][0]),
+                                                   ex2_approx(s[b][mb][2 * t + 1] - r[b][1])));
       if (live < BK) {  // rows of V behind the last key: 0 times what they hold may not be 0
         constexpr int CPR = D / 16;  // 16-byte chunks of a row
         for (int i = lane; i < KPW * CPR; i += 32) {
@@ -524,14 +547,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::CTAS)
       __syncwarp();
       if (lane == 0) mbar_arrive(B(bars->empty[st]));
     }
-    // the output over 2^m, as the row sum (by two factors: 2^(R - m) may be below FP32's normal range
-    // where the output is not), the sums over the lanes of a row
+    // the output in its own size (by two factors: 2^r may be below FP32's normal range where the output is
+    // not), the sums over the lanes of a row
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const float r = R[b][i] == -INFINITY ? 0.f : R[b][i] - m[b][i], h = floorf(0.5f * r);
-        const float u = ex2_approx(h), v = ex2_approx(r - h);
+        const float h = floorf(0.5f * r[b][i]), u = ex2_approx(h), v = ex2_approx(r[b][i] - h);
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
           o[b][c][i] = o[b][c][i] * u * v;
