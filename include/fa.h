@@ -687,7 +687,8 @@ size_t fa_norm_rope_bwd_workspace_size(int H, int Hkv, int d);
  *   positions  int32 [axes][T], device: the angles' positions (a drafted tree's depths, an image's
  *              rows and columns); NULL (axes = 1): the tokens' places. Where a token is stored is
  *              its place, ctx_lens[b] + t - cu_seqlens[b], either way.
- * Everything else as for fa_rope_append and fa_norm_rope; H, Hkv >= 1.
+ * Everything else as for fa_rope_append and fa_norm_rope; H, Hkv >= 1. New tokens of several sequences
+ * that share a slot (a page in two tables) write over each other: give each page one writer.
  */
 typedef struct fa_norm_rope_append_params {
   const void* q;

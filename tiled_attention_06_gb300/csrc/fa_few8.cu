@@ -21,7 +21,7 @@
 // follow it.
 //
 // Bound by reading K and V once, 2 (d + 1) bytes per key and K/V head: 32 sequences of 128,000 keys
-// in all, 32/8 heads of 128, bf16: 50.5 us, 5.2 TB/s, of which the join is 5 and the first tiles' wait
+// in all, 32/8 heads of 128, bf16: 51.2 us, 5.15 TB/s, of which the join is 5 and the first tiles' wait
 // about 2 (39.5 us at the measured copy rate); 89 to 93 with the same cache in 16 bits. Up to 16 rows;
 // with 17 to 32 the products and their scaling, not the bytes, set the pace (20 rows: 121 us, where
 // fa_varlen.cu takes 70), so those go there.

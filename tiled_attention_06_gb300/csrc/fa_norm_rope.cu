@@ -21,8 +21,9 @@
 // weight stays in registers and the weight's gradient adds up there; arithmetic is in packed FP32, and
 // rows come three rounds ahead by cp.async. With rows dealt to groups in order, whatever their token and
 // head, addresses and weights cost a row more instructions than its arithmetic and 16384 tokens x 40
-// heads of 128 in bf16 took 68 us and their gradient 117; so they take 62.5 (5370 GB/s, 80 % of the
-// measured copy rate) and 95 (5290 GB/s). Halves of the rotated part that are no multiple of 16 bytes move in
+// heads of 128 in bf16 took 68 us and their gradient 117; so they take 62.8 (5340 GB/s, 80 % of the
+// measured copy rate) and 95.8 (5250 GB/s). FP32, 8192 tokens x 40 heads of 64: 29.9 and 59.7 (floors 25.1
+// and 37.7). Halves of the rotated part that are no multiple of 16 bytes move in
 // chunks of 8 or 4 (8192 tokens, 72 or 68 of 128 elements rotated: 57 us element by element, 33 and 39).
 #include <algorithm>
 #include <climits>
@@ -418,7 +419,7 @@ struct Mine {
   }
 };
 
-// Three of 64 registers a thread where those do; with the cache's addresses and bytes they spill (chunks
+// Three of 64 registers a thread (8 to 12 bytes of them spilled) where those do; with the cache's addresses and bytes they spill (chunks
 // of 8 sequences of up to 512 tokens, 8 bits: 14.9 us, 13.6 with two).
 constexpr int ctas_per_sm(int dt, int vec, int mode) {
   return dt != FA_F32 && vec == 8 && mode == 0 ? 3 : 2;

@@ -269,8 +269,8 @@ __device__ __forceinline__ void for_each_block(const VarParams& p, PlanSmem& s, 
 // are cut into equal runs, one per SM: an SM has a run's one or two pieces (the list's snake order
 // puts a large piece and a small one together), and there are fewer pieces to join. Over the best S:
 // eight trees of 32 tokens over 53,000 keys, 32/8 heads: 73.5 -> 68.0 us; over an 8-bit cache four chunks
-// of up to 300 tokens 134 -> 121, one of 512 175 -> 154; it loses where S happens to fit (two trees of
-// 64 tokens 64.0 -> 67.1, one of 64 over 8192 keys 41.0 -> 43.4). Calls over a 16-bit cache without a tree
+// of up to 300 tokens 134 -> 121, one of 512 175 -> 154; the rule compares runs with whole items alone, so
+// it loses where S happens to fit (two trees of 64 tokens 64.0 -> 67.1, one of 64 over 8192 keys 41.0 -> 43.4). Calls over a 16-bit cache without a tree
 // keep the S they had, and their results with it.
 //
 // One CTA for a few microseconds, most of them spent fetching its instructions: the passes over

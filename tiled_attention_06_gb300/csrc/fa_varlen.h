@@ -262,7 +262,7 @@ struct FewParams {
   const int32_t* ctx;
   const int32_t* block_table;
   int B, H, Hkv, G, total_q, max_q;
-  int page_size, max_pages, num_pages, box;  // box: rows of one TMA box (<= 64)
+  int page_size, max_pages, num_pages, box;  // box: rows of one TMA box (<= 64, 8 bits 128)
   const uint8_t* k_scales;  // exponent bytes of an 8-bit cache [num_pages, Hkv, page_size], or null
   const uint8_t* v_scales;
   const uint32_t* tree;  // FA_MASK_TREE: [total_q][tree_words]
