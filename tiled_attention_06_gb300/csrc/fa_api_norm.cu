@@ -15,6 +15,7 @@ namespace {
 
 using fa::host::aligned16;
 using fa::host::aligned4;
+using fa::host::check_packed;
 using fa::host::cuda_fail;
 using fa::host::device_info;
 using fa::host::DeviceInfo;
@@ -137,17 +138,6 @@ fa_status check_paging(int B, int Hkv, int d, int page_size, int max_pages, int 
   if (Hkv > (1 << 16) || B > (1 << 24) ||
       static_cast<long long>(page_size) * max_pages > (1LL << 30))
     return fail(FA_ERR_INVALID_ARG, "problem too large");
-  return FA_OK;
-}
-
-// Packed rows with heads d apart, as the other calls over a paged cache take them.
-fa_status check_packed(const char* name, const void* ptr, long long token, int heads, int d) {
-  if (!ptr) return fail(FA_ERR_INVALID_ARG, "%s must be non-null", name);
-  if (!aligned16(ptr)) return fail(FA_ERR_INVALID_ARG, "%s must be 16-byte aligned", name);
-  if (token % 8 != 0 || token < static_cast<long long>(heads) * d || token > (1LL << 38))
-    return fail(FA_ERR_INVALID_ARG,
-                "%s: %lld elements between tokens (a multiple of 8, at least heads * d = %d)", name,
-                token, heads * d);
   return FA_OK;
 }
 

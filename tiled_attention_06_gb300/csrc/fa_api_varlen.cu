@@ -16,6 +16,7 @@ namespace {
 
 using fa::host::aligned16;
 using fa::host::aligned4;
+using fa::host::check_packed;
 using fa::host::cuda_fail;
 using fa::host::device_info;
 using fa::host::DeviceInfo;
@@ -103,17 +104,6 @@ fa_status check_common(const Common& c) {
   if (c.B > (1 << 24) || c.H > (1 << 16) || c.total_q > (1 << 30) ||
       static_cast<long long>(c.total_q) * c.H > (1LL << 31) - 1)
     return fail(FA_ERR_INVALID_ARG, "problem too large");
-  return FA_OK;
-}
-
-// Rows [.., heads, d] with `token` elements between tokens.
-fa_status check_rows(const char* name, const void* ptr, long long token, int heads, int d) {
-  if (!ptr) return fail(FA_ERR_INVALID_ARG, "%s must be non-null", name);
-  if (!aligned16(ptr)) return fail(FA_ERR_INVALID_ARG, "%s must be 16-byte aligned", name);
-  if (token % 8 != 0 || token < static_cast<long long>(heads) * d || token > (1LL << 38))
-    return fail(FA_ERR_INVALID_ARG,
-                "%s: %lld elements between tokens (a multiple of 8, at least heads * d = %d)", name,
-                token, heads * d);
   return FA_OK;
 }
 
@@ -368,10 +358,10 @@ fa_status fa_rope_append(const fa_rope_append_params* params, fa_stream_t stream
     return fail(FA_ERR_INVALID_ARG, "problem too large");
   if (a.T == 0) return FA_OK;
   fa_status st;
-  if ((st = check_rows("q", a.q, a.q_token, a.H, a.d)) != FA_OK) return st;
-  if ((st = check_rows("q_out", a.q_out, a.q_out_token, a.H, a.d)) != FA_OK) return st;
-  if ((st = check_rows("k", a.k, a.k_token, a.Hkv, a.d)) != FA_OK) return st;
-  if ((st = check_rows("v", a.v, a.v_token, a.Hkv, a.d)) != FA_OK) return st;
+  if ((st = check_packed("q", a.q, a.q_token, a.H, a.d)) != FA_OK) return st;
+  if ((st = check_packed("q_out", a.q_out, a.q_out_token, a.H, a.d)) != FA_OK) return st;
+  if ((st = check_packed("k", a.k, a.k_token, a.Hkv, a.d)) != FA_OK) return st;
+  if ((st = check_packed("v", a.v, a.v_token, a.Hkv, a.d)) != FA_OK) return st;
   if (a.q == a.q_out && a.q_token != a.q_out_token)
     return fail(FA_ERR_INVALID_ARG, "in place, q and q_out have the same step");
   if (!a.k_pages || !a.v_pages || !a.block_table || !a.ctx_lens || !a.cu_seqlens || !a.freqs)
@@ -441,12 +431,12 @@ static fa_status check_varlen(const fa_varlen_params& a) {
   if (!a.cu_seqlens_q || !a.cu_seqlens_k || !aligned4(a.cu_seqlens_q) || !aligned4(a.cu_seqlens_k))
     return fail(FA_ERR_INVALID_ARG, "cu_seqlens_q and cu_seqlens_k: non-null, 4-byte aligned");
   if (a.total_q > 0) {
-    if ((st = check_rows("q", a.q, a.q_token, a.H, a.d)) != FA_OK) return st;
-    if ((st = check_rows("o", a.o, a.o_token, a.H, a.d)) != FA_OK) return st;
+    if ((st = check_packed("q", a.q, a.q_token, a.H, a.d)) != FA_OK) return st;
+    if ((st = check_packed("o", a.o, a.o_token, a.H, a.d)) != FA_OK) return st;
   }
   if (a.total_k > 0) {
-    if ((st = check_rows("k", a.k, a.k_token, a.Hkv, a.d)) != FA_OK) return st;
-    if ((st = check_rows("v", a.v, a.v_token, a.Hkv, a.d)) != FA_OK) return st;
+    if ((st = check_packed("k", a.k, a.k_token, a.Hkv, a.d)) != FA_OK) return st;
+    if ((st = check_packed("v", a.v, a.v_token, a.Hkv, a.d)) != FA_OK) return st;
   }
   if (!aligned4(a.lse)) return fail(FA_ERR_INVALID_ARG, "lse must be 4-byte aligned");
   return FA_OK;
@@ -530,8 +520,8 @@ static fa_status paged_varlen(const fa_paged_varlen_params& a, const fa_paged_va
   if (few && (tiles > (1LL << 31) - 1 || tiles * a.B > (1LL << 38)))
     return fail(FA_ERR_INVALID_ARG, "problem too large");
   if (a.total_q == 0) return FA_OK;
-  if ((st = check_rows("q", a.q, a.q_token, a.H, a.d)) != FA_OK) return st;
-  if ((st = check_rows("o", a.o, a.o_token, a.H, a.d)) != FA_OK) return st;
+  if ((st = check_packed("q", a.q, a.q_token, a.H, a.d)) != FA_OK) return st;
+  if ((st = check_packed("o", a.o, a.o_token, a.H, a.d)) != FA_OK) return st;
   if (!a.k_pages || !a.v_pages || !aligned16(a.k_pages) || !aligned16(a.v_pages))
     return fail(FA_ERR_INVALID_ARG, "pools: non-null, 16-byte aligned");
   if (!a.block_table || !a.ctx_lens || !a.cu_seqlens_q || !aligned4(a.block_table) ||
@@ -657,12 +647,12 @@ fa_status fa_bwd_varlen(const fa_varlen_params* params, const fa_varlen_grads* g
   if (st != FA_OK) return st;
   if (a.total_q > 0) {
     if (!a.lse) return fail(FA_ERR_INVALID_ARG, "lse must be non-null");
-    if ((st = check_rows("dout", g.dout, g.dout_token, a.H, a.d)) != FA_OK) return st;
-    if ((st = check_rows("dq", g.dq, g.dq_token, a.H, a.d)) != FA_OK) return st;
+    if ((st = check_packed("dout", g.dout, g.dout_token, a.H, a.d)) != FA_OK) return st;
+    if ((st = check_packed("dq", g.dq, g.dq_token, a.H, a.d)) != FA_OK) return st;
   }
   if (a.total_k > 0) {
-    if ((st = check_rows("dk", g.dk, g.dk_token, a.Hkv, a.d)) != FA_OK) return st;
-    if ((st = check_rows("dv", g.dv, g.dv_token, a.Hkv, a.d)) != FA_OK) return st;
+    if ((st = check_packed("dk", g.dk, g.dk_token, a.Hkv, a.d)) != FA_OK) return st;
+    if ((st = check_packed("dv", g.dv, g.dv_token, a.Hkv, a.d)) != FA_OK) return st;
   }
   if (a.total_q == 0 && a.total_k == 0) return FA_OK;
   const BwdLayout B = bwd_layout(a.B, a.H, a.Hkv, a.total_q, a.total_k, a.d);

@@ -140,14 +140,6 @@ struct Walk {
   FewSeq s;
 };
 
-// The row of a tree's bits for keys idx .. idx + 31 of the chunk (keys before it are seen).
-__device__ __forceinline__ uint32_t tree_bits(const uint32_t* row, int words, int idx) {
-  const int w = idx >> 5;  // rounds down
-  const uint32_t a = w < 0 ? ~0u : w < words ? row[w] : 0u;
-  const uint32_t b = w < -1 ? ~0u : w + 1 < words ? row[w + 1] : 0u;
-  return __funnelshift_r(a, b, idx & 31);
-}
-
 // CTA (x, y): row y of the pair whose first piece CTA x of few_kernel holds. A warp's lanes hold
 // the pieces' maxima and sums, so the weights are known before the outputs are read; the four
 // warps take every fourth piece.

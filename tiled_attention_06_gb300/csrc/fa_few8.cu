@@ -89,15 +89,6 @@ __device__ __forceinline__ uint32_t load_u8(uint32_t addr) {
   asm volatile("ld.shared.u8 %0, [%1];" : "=r"(x) : "r"(addr) : "memory");
   return x;
 }
-// `bytes` (a multiple of 16) from global to shared memory, counted on `bar`.
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
-                                          uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
-          "r"(dst),
-      "l"(src), "r"(bytes), "r"(bar)
-      : "memory");
-}
 
 template <int D, bool BF16, int NB>
 __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::CTAS)

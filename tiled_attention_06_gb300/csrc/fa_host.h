@@ -19,6 +19,18 @@ fa_status cuda_fail(cudaError_t e, const char* what);
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
+// Rows [.., heads, d] with heads d apart and `token` elements between tokens.
+inline fa_status check_packed(const char* name, const void* ptr, long long token, int heads,
+                              int d) {
+  if (!ptr) return fail(FA_ERR_INVALID_ARG, "%s must be non-null", name);
+  if (!aligned16(ptr)) return fail(FA_ERR_INVALID_ARG, "%s must be 16-byte aligned", name);
+  if (token % 8 != 0 || token < static_cast<long long>(heads) * d || token > (1LL << 38))
+    return fail(FA_ERR_INVALID_ARG,
+                "%s: %lld elements between tokens (a multiple of 8, at least heads * d = %d)", name,
+                token, heads * d);
+  return FA_OK;
+}
+
 struct DeviceInfo {
   bool ready = false;
   int sms = 0;

@@ -86,6 +86,14 @@ FA_HD bool range_has(const Range& r, int nb) {
 }
 
 #if defined(__CUDACC__)
+// The row of a tree's bits for keys idx .. idx + 31 of the chunk (keys before it are seen).
+__device__ __forceinline__ uint32_t tree_bits(const uint32_t* row, int words, int idx) {
+  const int w = idx >> 5;  // rounds down
+  const uint32_t a = w < 0 ? ~0u : w < words ? row[w] : 0u;
+  const uint32_t b = w < -1 ? ~0u : w + 1 < words ? row[w + 1] : 0u;
+  return __funnelshift_r(a, b, idx & 31);
+}
+
 // Block-sparse ranges: the layout rows of the query blocks of [m0, m1) (at most two).
 __device__ __forceinline__ SparseRange key_range_sparse(int m0, int m1, int BN, int sk,
                                                         const PrefillParams& p, int bh) {

@@ -190,10 +190,8 @@ struct TreeRow {
 __device__ __forceinline__ void mask_tree_row(uint32_t* s, int n0, int sk, const TreeRow& t) {
 #pragma unroll
   for (int k = 0; k < BN / 32; ++k) {
-    const int idx = n0 + 32 * k - t.start, w = idx >> 5, left = sk - n0 - 32 * k;
-    const uint32_t a = w < 0 ? ~0u : w < t.words ? t.row[w] : 0u;
-    const uint32_t b = w < -1 ? ~0u : w + 1 < t.words ? t.row[w + 1] : 0u;
-    uint32_t mk = __funnelshift_r(a, b, idx & 31);
+    const int left = sk - n0 - 32 * k;
+    uint32_t mk = tree_bits(t.row, t.words, n0 + 32 * k - t.start);
     mk &= left <= 0 ? 0u : left >= 32 ? ~0u : (1u << left) - 1u;
 #pragma unroll
     for (int c = 0; c < 32; ++c)
@@ -674,15 +672,6 @@ __device__ __forceinline__ void convert_tile(const uint8_t* raw, uint32_t slot, 
     convert(std::true_type{});
   else
     convert(std::false_type{});
-}
-// `bytes` (a multiple of 16) from global to shared memory, counted on `bar`.
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
-                                          uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
-          "r"(dst),
-      "l"(src), "r"(bytes), "r"(bar)
-      : "memory");
 }
 
 template <int D, bool BF16, bool PAGED, int FORM>
